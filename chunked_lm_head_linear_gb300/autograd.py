@@ -19,10 +19,18 @@ dtype, so a bf16 W receives bf16 gradients. Callers that keep fp32 weight
 gradients (gradient accumulation over micro-batches, fp32 reduction across
 ranks) call ``lce.lce_fwd_bwd`` with their fp32 buffer as ``dW`` and
 ``accumulate_dW=True`` instead.
+
+FusedLinearLogProbs and FusedLinearDistillation wrap the token operators
+(lce_logprobs, lce_distill_fwd_bwd) the same way: log-probabilities and
+entropies of given tokens, whose upstream gradients are known only in the
+backward, save lse and entropy and recompute the logits there; the distillation
+loss computes its gradients in the forward and scales them in the backward.
+Gradients nobody needs (a frozen W) are not computed.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import lce
 
@@ -70,3 +78,75 @@ class FusedLinearCrossEntropy(torch.nn.Module):
     def forward(self, H, W, y):
         fn = _RecomputeLCE if self.recompute else _FusedLCE
         return fn.apply(H, W, y, self.opts)
+
+
+class _LogProbs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, H, W, y, temperature, opts):
+        logp, lse, entropy, _, _ = lce.lce_logprobs(H, W, y, temperature=temperature, **opts)
+        ctx.save_for_backward(H, W, y, lse, entropy)
+        ctx.temperature, ctx.opts = temperature, opts
+        ctx.set_materialize_grads(False)   # an output nobody used comes back as None
+        return logp, entropy
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g_logp, g_entropy):
+        H, W, y, lse, entropy = ctx.saved_tensors
+        g_logp = torch.zeros_like(lse) if g_logp is None else g_logp.contiguous()
+        g_entropy = None if g_entropy is None else g_entropy.contiguous()
+        dH, dW = lce.lce_logprobs_backward(H, W, y, lse, entropy, g_logp, g_entropy, temperature=ctx.temperature,
+                                           need_dH=ctx.needs_input_grad[0], need_dW=ctx.needs_input_grad[1],
+                                           **ctx.opts)
+        return dH, dW, None, None, None
+
+
+class FusedLinearLogProbs(torch.nn.Module):
+    """logp [N] of the tokens y and entropy [N] of softmax(H W^T / temperature),
+    both differentiable in H and W (fp32; logp is 0 where y is ignore_index)."""
+
+    def __init__(self, temperature: float = 1.0, ignore_index: int = -100, chunk_tokens=0):
+        super().__init__()
+        self.temperature = temperature
+        self.opts = dict(ignore_index=ignore_index, chunk_tokens=chunk_tokens)
+
+    def forward(self, H, W, y):
+        return _LogProbs.apply(H, W, y, self.temperature, self.opts)
+
+
+class _Distillation(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, H, W, idx, t, kw):
+        need_dH, need_dW = ctx.needs_input_grad[:2]
+        if not (need_dH or need_dW):
+            loss, _ = lce.lce_distill_forward(H, W, idx, t, **kw)
+            return loss.reshape(())
+        loss, _, dH, dW = lce.lce_distill_fwd_bwd(H, W, idx, t, need_dH=need_dH, need_dW=need_dW, **kw)
+        ctx.grads = dH, dW
+        return loss.reshape(())
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        if ctx.grads is None:
+            raise RuntimeError("FusedLinearDistillation: the gradients were handed out by an earlier backward pass "
+                               "of this graph; run the forward again")
+        dH, dW = ctx.grads
+        ctx.grads = None
+        lce.lce_scale_grads(dH, dW, g.reshape(1).to(torch.float32).contiguous())
+        return dH, dW, None, None, None
+
+
+class FusedLinearDistillation(torch.nn.Module):
+    """KL divergence of softmax(H W^T / temperature) from a teacher's top tokens
+    idx [N, K] with values t [N, K], times temperature^2, mean over the rows that
+    keep an entry (lce.lce_distill_fwd_bwd)."""
+
+    def __init__(self, temperature: float = 1.0, renormalize: bool = True, ignore_index: int = -100,
+                 reduction: str = "mean", chunk_tokens=0):
+        super().__init__()
+        self.kw = dict(temperature=temperature, renormalize=renormalize, ignore_index=ignore_index,
+                       reduction=reduction, chunk_tokens=chunk_tokens)
+
+    def forward(self, H, W, idx, t):
+        return _Distillation.apply(H, W, idx, t, self.kw)

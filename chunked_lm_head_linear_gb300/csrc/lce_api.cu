@@ -391,14 +391,19 @@ int dh_dw(const Call& c, int64_t c0, int64_t rows, const float* rowscale, const 
   CUtensorMap mG, mW, mdH, mGt, mB, mdW;
   LCE_TRY(make_map(&mG, P, rows, c.V, c.L.ldp, lce::kBoxRowsK));      // dH: A, K-major
   LCE_TRY(make_map(&mW, c.W, c.V, c.d, c.d, lce::kBoxRowsMN));        // dH: B, N-major
-  if (dH_f32)                                                           // dH store
+  if (!dH)                                                              // not wanted: no tile stores through it
+    mdH = mW;
+  else if (dH_f32)                                                      // dH store
     LCE_TRY(make_map_t(&mdH, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, static_cast<float*>(dH) + c0 * c.d, rows, c.d, c.d,
                        32u, kStoreRows));
   else
     LCE_TRY(make_map(&mdH, static_cast<uint16_t*>(dH) + c0 * c.d, rows, c.d, c.d, kStoreRows));
   LCE_TRY(make_map(&mGt, P, rows, c.V, c.L.ldp, lce::kBoxRowsMN));    // dW: A, M-major
   LCE_TRY(make_map(&mB, B, rows, c.d, c.d, lce::kBoxRowsMN));          // dW: B, N-major
-  LCE_TRY(make_map_t(&mdW, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, dW, c.V, c.d, c.d, 32u, kStoreRows));
+  if (!dW)
+    mdW = mW;
+  else
+    LCE_TRY(make_map_t(&mdW, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, dW, c.V, c.d, c.d, 32u, kStoreRows));
   lce::DhParams dp;
   dp.rows = static_cast<int>(rows);
   dp.N = static_cast<int>(c.d);
@@ -967,6 +972,304 @@ int lce_norm_fwd_bwd(const void* x, const float* w_norm, float eps, const void* 
   if (flags & lce::kFlagTimeout) return LCE_ERR_TIMEOUT;
   if (flags & lce::kFlagLabelRange) return LCE_ERR_LABEL_RANGE;
   return LCE_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Token operators
+// ---------------------------------------------------------------------------
+namespace {
+
+// Workspace of one token operator: the chunk's triples, its fp32 logits (with_z), its gradient
+// tile and the dH parts (with_grad).
+struct TokLayout {
+  Layout base;         // status, ztgt, partials, P and the dH parts of the call record
+  int64_t ldz = 0;     // row stride of the logits buffer
+  size_t Z = 0;
+  size_t total = 0;
+};
+
+TokLayout tok_layout(int64_t N, int64_t d, int64_t V, bool with_z, bool with_grad, const lce_opts* o) {
+  TokLayout T;
+  Layout& L = T.base;
+  L.C = chunk_of(N, o);
+  L.T = ceil_div(V, kVocabTile);
+  L.ldp = L.T * kVocabTile;
+  L.chunks = N > 0 ? ceil_div(N, L.C) : 0;
+  T.ldz = L.ldp;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align256(bytes);
+    return at;
+  };
+  const size_t C = static_cast<size_t>(L.C);
+  L.status = take(sizeof(DevStatus));
+  L.ztgt = take(sizeof(float) * C);
+  L.partials = take(sizeof(float4) * C * static_cast<size_t>(2 * L.T));
+  if (with_z) T.Z = take(sizeof(float) * C * static_cast<size_t>(T.ldz));
+  if (with_grad) {
+    L.P = take(2 * C * static_cast<size_t>(L.ldp));
+    take_dh_parts(L, d, V, take);
+  }
+  L.total = T.total = off;
+  return T;
+}
+
+int check_temperature(float t) { return t > 0.f && t <= 3.0e38f ? LCE_OK : LCE_ERR_INVALID_ARG; }
+
+// Fills the call record of a token operator (after its own argument checks).
+int tok_begin(Call* c, const TokLayout& T, const void* H, const void* W, const int64_t* y, int64_t N, int64_t d,
+              int64_t V, const lce_opts& o, void* ws, size_t ws_bytes, void* stream) {
+  if (ws_bytes < T.total) return LCE_ERR_WORKSPACE;
+  c->o = o;
+  c->L = T.base;
+  c->H = static_cast<const uint16_t*>(H);
+  c->W = static_cast<const uint16_t*>(W);
+  c->y = y;
+  c->N = N;
+  c->d = d;
+  c->V = V;
+  c->V_total = V;
+  c->y_offset = 0;
+  c->ws = static_cast<uint8_t*>(ws);
+  c->st = reinterpret_cast<DevStatus*>(c->ws + c->L.status);
+  c->s = static_cast<cudaStream_t>(stream);
+  return device_check(&c->dev);
+}
+
+lce::TokParams tok_params(const Call& c, int64_t c0, int64_t rows, float temperature) {
+  lce::TokParams p;
+  std::memset(&p, 0, sizeof p);
+  p.rows = static_cast<int>(rows);
+  p.V = static_cast<int>(c.V);
+  p.nparts = static_cast<int>(2 * c.L.T);
+  p.inv_t = 1.f / temperature;
+  p.ignore_index = c.o.ignore_index;
+  p.y = c.y ? c.y + c0 : nullptr;
+  p.partials = reinterpret_cast<float4*>(c.ws + c.L.partials);
+  p.ztgt = reinterpret_cast<float*>(c.ws + c.L.ztgt);
+  p.flags = &c.st->flags;
+  return p;
+}
+
+// Logits of chunk rows [c0, c0 + rows) with a token epilogue. out: the chunk's logits buffer (fp32,
+// TOK_STATS_Z) or gradient tile (bf16, TOK_GRAD) with row stride ldo.
+int tok_logits(const Call& c, int64_t c0, int64_t rows, int mode, void* out, int64_t ldo, const lce::TokParams& p) {
+  CUtensorMap mA, mB, mC;
+  LCE_TRY(make_map(&mA, c.H + c0 * c.d, rows, c.d, c.d, lce::kBoxRowsK));
+  LCE_TRY(make_map(&mB, c.W, c.V, c.d, c.d, lce::kBoxRowsK));
+  if (mode == lce::TOK_STATS_Z)
+    LCE_TRY(make_map_t(&mC, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, out, rows, c.V, ldo, 32u, kStoreRows));
+  else if (mode == lce::TOK_GRAD)
+    LCE_TRY(make_map(&mC, out, rows, c.V, ldo, kStoreRows));
+  else
+    mC = mB;  // this epilogue stores nothing
+  const double flops = 2.0 * static_cast<double>(rows) * static_cast<double>(c.V) * static_cast<double>(c.d);
+  return timed(c.s, mode == lce::TOK_GRAD ? K_LOGITS_GRAD : K_LOGITS_STATS, flops, [&] {
+    return cuda_rc(lce::launch_tok_logits(mode, mA, mB, mC, rows, c.V, c.d, p, c.dev.num_sms, c.s));
+  });
+}
+
+// dW of a call without tokens: zero unless it is added to.
+int zero_dW(const Call& c, float* dW) {
+  if (!dW || c.o.accumulate_dW) return LCE_OK;
+  const size_t bytes = sizeof(float) * static_cast<size_t>(c.V) * static_cast<size_t>(c.d);
+  return timed(c.s, K_MEMSET, static_cast<double>(bytes), [&] { return cuda_rc(cudaMemsetAsync(dW, 0, bytes, c.s)); });
+}
+
+// The backward GEMMs of a chunk on its exact gradient tile, for the gradients that are wanted.
+int tok_grads(const Call& c, int64_t c0, int64_t rows, void* dH, float* dW) {
+  BwdPart part;
+  part.with_dh = dH != nullptr;
+  part.v_end = dW ? c.V : 0;
+  return dh_dw(c, c0, rows, nullptr, c.H + c0 * c.d, dH, dW, c.o.accumulate_dW || c0 > 0, false, part);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lce_logprobs_workspace_size(int64_t N, int64_t d, int64_t V, int32_t top_k, const lce_opts* opts) {
+  lce_opts o;
+  lce_opts_init(&o);
+  if (opts) o = *opts;
+  if (check_sizes(N, d, V, &o) != LCE_OK || top_k < 0 || top_k > LCE_MAX_TOP || top_k > V) return 0;
+  return tok_layout(N, d, V, top_k > 0, false, &o).total;
+}
+
+int lce_logprobs(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V, float temperature,
+                 int32_t top_k, float* logp, float* lse, float* entropy, float* top_logp, int64_t* top_idx,
+                 const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
+  lce_opts o;
+  lce_opts_init(&o);
+  if (opts) o = *opts;
+  LCE_TRY(check_sizes(N, d, V, &o));
+  LCE_TRY(check_temperature(temperature));
+  if (o.reserved != 0 || top_k < 0 || top_k > LCE_MAX_TOP || top_k > V) return LCE_ERR_INVALID_ARG;
+  if (!W || !ws || (N > 0 && (!H || !y || !logp || !lse || (top_k > 0 && (!top_logp || !top_idx)))))
+    return LCE_ERR_INVALID_ARG;
+  if (!aligned(W, 16) || !aligned(H, 16) || !aligned(y, 8) || !aligned(ws, 256) || !aligned(logp, 4) ||
+      !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(top_logp, 4) || !aligned(top_idx, 8))
+    return LCE_ERR_ALIGNMENT;
+  const TokLayout T = tok_layout(N, d, V, top_k > 0, false, &o);
+  Call c;
+  LCE_TRY(tok_begin(&c, T, H, W, y, N, d, V, o, ws, ws_bytes, stream));
+  LCE_TRY(prepare(c, nullptr));
+  float* Z = top_k > 0 ? reinterpret_cast<float*>(c.ws + T.Z) : nullptr;
+  for (int64_t c0 = 0; c0 < N; c0 += c.L.C) {
+    const int64_t rows = (N - c0) < c.L.C ? (N - c0) : c.L.C;
+    const lce::TokParams p = tok_params(c, c0, rows, temperature);
+    LCE_TRY(tok_logits(c, c0, rows, Z ? lce::TOK_STATS_Z : lce::TOK_STATS, Z, T.ldz, p));
+    lce::TokScoreArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.rows = p.rows;
+    a.V = p.V;
+    a.nparts = p.nparts;
+    a.K = top_k;
+    a.ldz = T.ldz;
+    a.inv_t = p.inv_t;
+    a.ignore_index = p.ignore_index;
+    a.y = p.y;
+    a.partials = p.partials;
+    a.ztgt = p.ztgt;
+    a.Z = Z;
+    a.logp = logp + c0;
+    a.lse = lse + c0;
+    a.entropy = entropy ? entropy + c0 : nullptr;
+    a.top_logp = top_k > 0 ? top_logp + c0 * top_k : nullptr;
+    a.top_idx = top_k > 0 ? top_idx + c0 * top_k : nullptr;
+    a.flags = p.flags;
+    const double bytes = static_cast<double>(rows) * (32.0 * static_cast<double>(c.L.T) + 20.0 + 524.0 * top_k);
+    LCE_TRY(timed(c.s, K_COMBINE, bytes, [&] { return cuda_rc(lce::launch_score(a, c.s)); }));
+  }
+  return finish(c);
+}
+
+int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
+                          float temperature, const float* lse, const float* entropy, const float* g_logp,
+                          const float* g_entropy, void* dH, float* dW, const lce_opts* opts, void* ws,
+                          size_t ws_bytes, void* stream) {
+  Call c;
+  LCE_TRY(begin(&c, LCE_OP_BACKWARD, H, W, y, N, d, V, opts, ws, ws_bytes, stream));
+  LCE_TRY(check_temperature(temperature));
+  if (c.o.reserved != 0 || (!dH && !dW) || (N > 0 && (!lse || !g_logp || (g_entropy && !entropy))))
+    return LCE_ERR_INVALID_ARG;
+  if (!aligned(dW, 16) || !aligned(dH, 16) || !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(g_logp, 4) ||
+      !aligned(g_entropy, 4))
+    return LCE_ERR_ALIGNMENT;
+  c.o.reduction = LCE_SUM;  // the upstream gradients carry every factor
+  LCE_TRY(device_check(&c.dev));
+  LCE_TRY(prepare(c, nullptr));
+  if (N == 0) LCE_TRY(zero_dW(c, dW));
+  uint16_t* G = reinterpret_cast<uint16_t*>(c.ws + c.L.P);
+  for (int64_t c0 = 0; c0 < N; c0 += c.L.C) {
+    const int64_t rows = (N - c0) < c.L.C ? (N - c0) : c.L.C;
+    lce::TokParams p = tok_params(c, c0, rows, temperature);
+    p.lse = lse + c0;
+    p.entropy = entropy ? entropy + c0 : nullptr;
+    p.g_logp = g_logp + c0;
+    p.g_entropy = g_entropy ? g_entropy + c0 : nullptr;
+    LCE_TRY(tok_logits(c, c0, rows, lce::TOK_GRAD, G, c.L.ldp, p));
+    LCE_TRY(tok_grads(c, c0, rows, dH, dW));
+  }
+  return finish(c);
+}
+
+}  // extern "C"
+
+namespace {
+
+int distill(const void* H, const void* W, const int64_t* idx, const void* t, int64_t N, int64_t d, int64_t V,
+            int32_t K, int32_t teacher, float temperature, const float* grad_loss, float* loss, float* row_loss,
+            void* dH, float* dW, bool with_grad, const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
+  lce_opts o;
+  lce_opts_init(&o);
+  if (opts) o = *opts;
+  LCE_TRY(check_sizes(N, d, V, &o));
+  LCE_TRY(check_temperature(temperature));
+  if (o.reserved != 0 || K < 1 || K > LCE_MAX_TOP ||
+      (teacher & ~(LCE_TEACHER_BF16 | LCE_TEACHER_LOGPROBS)) != 0 ||
+      ((teacher & LCE_TEACHER_LOGPROBS) && temperature != 1.f))
+    return LCE_ERR_INVALID_ARG;
+  if (!W || !ws || !loss || (with_grad && !dH && !dW) || (N > 0 && (!H || !idx || !t || !row_loss)))
+    return LCE_ERR_INVALID_ARG;
+  const int t_bf16 = (teacher & LCE_TEACHER_BF16) ? 1 : 0;
+  if (!aligned(W, 16) || !aligned(H, 16) || !aligned(idx, 8) || !aligned(t, t_bf16 ? 2 : 4) || !aligned(ws, 256) ||
+      !aligned(loss, 4) || !aligned(row_loss, 4) || !aligned(grad_loss, 4) || !aligned(dH, 16) || !aligned(dW, 16))
+    return LCE_ERR_ALIGNMENT;
+  const TokLayout T = tok_layout(N, d, V, true, with_grad, &o);
+  Call c;
+  LCE_TRY(tok_begin(&c, T, H, W, nullptr, N, d, V, o, ws, ws_bytes, stream));
+  int* cnt = with_grad ? reinterpret_cast<int*>(c.ws + c.L.dh_cnt) : nullptr;
+  LCE_TRY(timed(c.s, K_PREPARE, static_cast<double>(N) * K * (t_bf16 ? 10.0 : 12.0), [&] {
+    return cuda_rc(lce::launch_distill_count(idx, t, t_bf16, N, K, static_cast<int>(V), o.ignore_index, c.st, cnt,
+                                             with_grad ? c.L.dh_ncnt : 0, c.dev.num_sms, c.s));
+  }));
+  if (N == 0 && with_grad) LCE_TRY(zero_dW(c, dW));
+  float* Z = reinterpret_cast<float*>(c.ws + T.Z);
+  for (int64_t c0 = 0; c0 < N; c0 += c.L.C) {
+    const int64_t rows = (N - c0) < c.L.C ? (N - c0) : c.L.C;
+    const lce::TokParams p = tok_params(c, c0, rows, temperature);
+    LCE_TRY(tok_logits(c, c0, rows, lce::TOK_STATS_Z, Z, T.ldz, p));
+    lce::DistillArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.V = p.V;
+    a.K = K;
+    a.nparts = p.nparts;
+    a.renormalize = (teacher & LCE_TEACHER_LOGPROBS) ? 0 : 1;
+    a.mean = o.reduction == LCE_MEAN ? 1 : 0;
+    a.t_bf16 = t_bf16;
+    a.ldz = T.ldz;
+    a.ldg = c.L.ldp;
+    a.inv_t = p.inv_t;
+    a.ignore_index = o.ignore_index;
+    a.n_override = o.n_valid_override;
+    a.idx = idx + c0 * K;
+    a.t = static_cast<const uint8_t*>(t) + static_cast<size_t>(c0) * static_cast<size_t>(K) * (t_bf16 ? 2 : 4);
+    a.partials = p.partials;
+    a.Z = Z;
+    a.G = with_grad ? reinterpret_cast<__nv_bfloat16*>(c.ws + c.L.P) : nullptr;
+    a.row_loss = row_loss + c0;
+    a.grad_loss = grad_loss;
+    a.st = c.st;
+    const double bytes = static_cast<double>(rows) * (32.0 * static_cast<double>(c.L.T) + 12.0 * K +
+                                                      (with_grad ? 6.0 * static_cast<double>(V) : 32.0 * K));
+    LCE_TRY(timed(c.s, K_COMBINE, bytes,
+                  [&] { return cuda_rc(lce::launch_distill_row(a, static_cast<int>(rows), c.s)); }));
+    if (with_grad) LCE_TRY(tok_grads(c, c0, rows, dH, dW));
+  }
+  LCE_TRY(finalize(c, row_loss, loss));
+  return finish(c);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lce_distill_workspace_size(int64_t N, int64_t d, int64_t V, int32_t K, int32_t with_grad,
+                                  const lce_opts* opts) {
+  lce_opts o;
+  lce_opts_init(&o);
+  if (opts) o = *opts;
+  if (check_sizes(N, d, V, &o) != LCE_OK || K < 1 || K > LCE_MAX_TOP) return 0;
+  return tok_layout(N, d, V, true, with_grad != 0, &o).total;
+}
+
+int lce_distill_forward(const void* H, const void* W, const int64_t* idx, const void* t, int64_t N, int64_t d,
+                        int64_t V, int32_t K, int32_t teacher, float temperature, float* loss, float* row_loss,
+                        const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
+  return distill(H, W, idx, t, N, d, V, K, teacher, temperature, nullptr, loss, row_loss, nullptr, nullptr, false,
+                 opts, ws, ws_bytes, stream);
+}
+
+int lce_distill_fwd_bwd(const void* H, const void* W, const int64_t* idx, const void* t, int64_t N, int64_t d,
+                        int64_t V, int32_t K, int32_t teacher, float temperature, const float* grad_loss, float* loss,
+                        float* row_loss, void* dH, float* dW, const lce_opts* opts, void* ws, size_t ws_bytes,
+                        void* stream) {
+  return distill(H, W, idx, t, N, d, V, K, teacher, temperature, grad_loss, loss, row_loss, dH, dW, true, opts, ws,
+                 ws_bytes, stream);
 }
 
 int lce_scale_grads(void* dH, float* dW, int64_t N, int64_t d, int64_t V, const float* grad_loss, void* stream) {

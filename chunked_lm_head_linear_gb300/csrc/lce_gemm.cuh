@@ -135,6 +135,16 @@ __device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr, int k) {
   return smem_desc_sw128(addr + k * 2048, MN_SLAB_BYTES, 1024);
 }
 
+// This CTA's half of a k-block: 128 rows of a K-major operand (one box), or
+// 128 columns of an MN-major operand (two 64-wide boxes).
+__device__ __forceinline__ void load_k_major(uint8_t* dst, const CUtensorMap* m, uint32_t bar, int row0, int k0) {
+  tma_load_2d_pair(dst, m, bar, k0, row0);
+}
+__device__ __forceinline__ void load_mn_major(uint8_t* dst, const CUtensorMap* m, uint32_t bar, int mn0, int k0) {
+  tma_load_2d_pair(dst, m, bar, mn0, k0);
+  tma_load_2d_pair(dst + MN_SLAB_BYTES, m, bar, mn0 + 64, k0);
+}
+
 __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, int lane) {
   int ok = 0;
   if (lane == 0) ok = mbar_wait_cluster(bar, parity, abort) ? 1 : 0;

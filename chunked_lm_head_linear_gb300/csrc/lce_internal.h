@@ -216,6 +216,77 @@ cudaError_t launch_scale(void* bf16, long long n_bf16, float* f32, long long n_f
                          cudaStream_t s);
 cudaError_t launch_finalize(const float* loss_i, long long N, const DevStatus* st, float* loss, cudaStream_t s);
 
+// ----------------------------------------------------------------------------
+// Token operators (lce_tokens.cu)
+// ----------------------------------------------------------------------------
+enum TokMode : int {
+  TOK_STATS = 0,    // triples of each (row, half tile) and the label's logit
+  TOK_STATS_Z = 1,  // the triples and the fp32 logits
+  TOK_GRAD = 2,     // gradient tile of log-probability and entropy
+};
+
+constexpr int kMaxTop = 128;  // most alternatives of a row, most teacher entries of a row
+
+struct TokParams {
+  int rows;              // rows of this chunk
+  int V;
+  int nparts;            // triples per row: two per 256-column vocabulary tile
+  float inv_t;           // 1 / temperature
+  long long ignore_index;
+  const int64_t* y;      // labels of this chunk (TOK_STATS, TOK_GRAD)
+  float4* partials;      // [rows, nparts] (m, s, t, unused)
+  float* ztgt;           // [rows] logit of the label (TOK_STATS)
+  const float* lse;      // [rows] (TOK_GRAD; the next three too)
+  const float* entropy;  // [rows]
+  const float* g_logp;   // [rows] upstream gradients
+  const float* g_entropy;  // [rows] or null
+  int* flags;
+};
+
+struct TokScoreArgs {
+  int rows, V, nparts, K;
+  long long ldz;
+  float inv_t;
+  long long ignore_index;
+  const int64_t* y;
+  const float4* partials;
+  const float* ztgt;     // K == 0
+  const float* Z;        // [rows, ldz] fp32 logits, K > 0
+  float* logp;           // [rows]
+  float* lse;            // [rows]
+  float* entropy;        // [rows] or null
+  float* top_logp;       // [rows, K]
+  int64_t* top_idx;      // [rows, K]
+  int* flags;
+};
+
+struct DistillArgs {
+  int V, K, nparts;
+  int renormalize, mean, t_bf16;
+  long long ldz, ldg;
+  float inv_t;
+  long long ignore_index, n_override;
+  const int64_t* idx;    // [rows, K] teacher entries of this chunk
+  const void* t;         // [rows, K] their values, fp32 or bf16
+  const float4* partials;
+  const float* Z;        // [rows, ldz]
+  __nv_bfloat16* G;      // [rows, ldg] gradient tile, or null (loss only)
+  float* row_loss;       // [rows]
+  const float* grad_loss;
+  DevStatus* st;
+};
+
+// Logits GEMM z [M, N] = A [M, K] B [N, K]^T with a token epilogue; c: store
+// map of the logits (TOK_STATS_Z) or the gradient tile (TOK_GRAD).
+cudaError_t launch_tok_logits(int mode, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, long long M,
+                              long long N, long long K, const TokParams& ep, int num_sms, cudaStream_t s);
+cudaError_t launch_score(const TokScoreArgs& p, cudaStream_t s);
+// Clears the status block and cnt[0, ncnt), then counts the rows of idx [N, K] that keep an entry.
+cudaError_t launch_distill_count(const int64_t* idx, const void* t, int t_bf16, long long N, int K, int V,
+                                 long long ignore_index, DevStatus* st, int* cnt, int ncnt, int num_sms,
+                                 cudaStream_t s);
+cudaError_t launch_distill_row(const DistillArgs& p, int rows, cudaStream_t s);
+
 // GEMM tile geometry (must match the kernels): each CTA of a pair loads 128
 // rows of a K-major operand per box and 64 rows of an MN-major one.
 constexpr int kBoxRowsK = 128;

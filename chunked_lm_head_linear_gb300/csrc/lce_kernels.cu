@@ -760,16 +760,6 @@ __global__ void __launch_bounds__(1024) k_finalize(const float* __restrict__ los
 // ----------------------------------------------------------------------------
 enum : int { KIND_LOGITS = 0, KIND_DH = 1, KIND_DW = 2 };
 
-// This CTA's half of a k-block: 128 rows of a K-major operand (one box), or
-// 128 columns of an MN-major operand (two 64-wide boxes).
-__device__ __forceinline__ void load_k_major(uint8_t* dst, const CUtensorMap* m, uint32_t bar, int row0, int k0) {
-  tma_load_2d_pair(dst, m, bar, k0, row0);
-}
-__device__ __forceinline__ void load_mn_major(uint8_t* dst, const CUtensorMap* m, uint32_t bar, int mn0, int k0) {
-  tma_load_2d_pair(dst, m, bar, mn0, k0);
-  tma_load_2d_pair(dst + MN_SLAB_BYTES, m, bar, mn0 + 64, k0);
-}
-
 // Logits of a chunk: z = H_c W^T (both operands K-major) with the FwdEpi
 // epilogue. Tiles walk M first, so the pairs running at once share W tiles.
 struct LogitsProb {

@@ -1,0 +1,625 @@
+// Token operators of the LM head beside its cross-entropy: log-probabilities
+// of given tokens with entropy and top alternatives, their gradient, and the
+// distillation loss against a teacher's top logits. They share the pair GEMM
+// of lce_gemm.cuh (z = H W^T, never a whole [N, V] in memory) and the backward
+// GEMMs of lce_kernels.cu; what differs is the tile epilogue and the per-row
+// kernels behind it.
+//
+// Per row i, with z' = z / T:
+//   lse = log sum_v exp z'_v, logp = z'_y - lse, entropy = lse - sum_v p_v z'_v
+// The GEMM's epilogue keeps, per (row, 128 vocabulary columns), the triple
+//   m = max z,  s = sum exp((z - m)/T),  t = sum exp((z - m)/T) (z - m)/T
+// from which entropy = log S - T/S of the merged triple: no difference of two
+// large numbers, and one exponential per logit for both quantities.
+#include <math.h>
+
+#include "lce_gemm.cuh"
+#include "lce_internal.h"
+
+namespace lce {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kFloor = -1.0e30f;  // stands in for -inf where it is multiplied by a zero probability
+
+// ----------------------------------------------------------------------------
+// Tile epilogue: an epilogue warp owns 32 rows x 128 columns, one thread a row.
+//   TOK_STATS    the triple of each (row, half tile) and the label's logit
+//   TOK_STATS_Z  the triple, and the fp32 logits themselves into the chunk's
+//                buffer (top alternatives and distillation read them again:
+//                4 bytes a logit, written behind a main loop of d/16 MMAs)
+//   TOK_GRAD     the gradient tile of (logp, entropy) in bf16, from the saved
+//                lse and entropy:
+//                  G_v = ([v = y] a - p_v (a + e (z'_v - lse + entropy))) / T
+//                rounded to bf16 once (the operand type of the two GEMMs that
+//                follow), everything before it in fp32.
+// ----------------------------------------------------------------------------
+template <int MODE>
+struct TokEpi {
+  using Params = TokParams;
+  struct State {};
+
+  static __device__ __forceinline__ void stats_tile(const Params& p, const EpiCtx& ctx, int m0, int col0,
+                                                    uint32_t taddr) {
+    const int r = m0 + ctx.row0 + ctx.lane;
+    const bool live = r < p.rows;
+    const int vlim = p.V - col0;  // columns >= vlim are past the vocabulary (warp-uniform)
+    const int part = col0 / EPI_COLS;
+    float m = -INFINITY, s = 0.f, t = 0.f, zt = 0.f;
+    bool have_t = false;
+    int ycol = -1;
+    if (MODE == TOK_STATS && live) {
+      const long long yc = static_cast<long long>(p.y[r]) - col0;
+      if (yc >= 0 && yc < EPI_COLS && p.y[r] != p.ignore_index) ycol = static_cast<int>(yc);
+    }
+    const bool rows_in = m0 + ctx.row0 < p.rows;  // a store box never starts past the rows
+    const float k = p.inv_t * kLog2e;
+#pragma unroll 1
+    for (int c0 = 0; c0 < EPI_COLS; c0 += 32) {
+      if (c0 >= vlim) break;
+      float v[32];
+      tmem_ld_32x32b_x32(taddr + c0, v);
+      if (MODE == TOK_STATS_Z && rows_in) {
+        stage_acquire(ctx);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          *reinterpret_cast<float4*>(ctx.stage + stage_off(ctx.lane, q)) =
+              make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        stage_release(ctx, col0 + c0, m0 + ctx.row0, false);
+      }
+      if (vlim < c0 + 32) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (c0 + c >= vlim) v[c] = -INFINITY;
+      }
+      if (MODE == TOK_STATS) {
+        const int yo = ycol - c0;
+        if (yo >= 0 && yo < 32) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (c == yo) {
+              zt = v[c];
+              have_t = true;
+            }
+        }
+      }
+      float cm = v[0];
+#pragma unroll
+      for (int c = 1; c < 32; ++c) cm = fmaxf(cm, v[c]);
+      if (cm > m) {
+        if (s > 0.f) {
+          const float f = ex2_approx((m - cm) * k);
+          t = f * (t + s * fmaxf((m - cm) * p.inv_t, kFloor));
+          s *= f;
+        }
+        m = cm;
+      }
+      const float mb = m == -INFINITY ? 0.f : m;  // a group of -inf only: every term is zero
+      float s2 = 0.f, t2 = 0.f;
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const float dz = v[c] - mb;
+        const float e = ex2_approx(dz * k);
+        s2 += e;
+        t2 = fmaf(e, fmaxf(dz, kFloor), t2);
+      }
+      s += s2;
+      t = fmaf(t2, p.inv_t, t);
+    }
+    if (!live || !in_bounds(part, p.nparts, p.flags)) return;
+    p.partials[static_cast<long long>(r) * p.nparts + part] = make_float4(m, s, t, 0.f);
+    if (MODE == TOK_STATS && have_t) p.ztgt[r] = zt;
+  }
+
+  static __device__ __forceinline__ void grad_tile(const Params& p, const EpiCtx& ctx, int m0, int col0,
+                                                   uint32_t taddr) {
+    const int r = m0 + ctx.row0 + ctx.lane;
+    const int vlim = p.V - col0;
+    if (m0 + ctx.row0 >= p.rows || vlim <= 0) return;  // nothing of this half tile is stored
+    float lse = 0.f, a = 0.f, c1 = 0.f, c0g = 0.f;
+    int ycol = -1;
+    if (r < p.rows) {
+      const long long y = p.y[r];
+      const bool given = y != p.ignore_index && y >= 0 && y < p.V;
+      lse = p.lse[r];
+      a = given ? p.g_logp[r] * p.inv_t : 0.f;
+      const float e = p.g_entropy != nullptr ? p.g_entropy[r] * p.inv_t : 0.f;
+      c1 = -e;
+      c0g = -a;
+      if (p.g_entropy != nullptr) c0g -= e * p.entropy[r];
+      const long long yc = y - col0;
+      if (given && yc >= 0 && yc < EPI_COLS) ycol = static_cast<int>(yc);
+    }
+#pragma unroll 1
+    for (int u = 0; u < EPI_COLS / 64; ++u) {
+      if (u * 64 >= vlim) break;
+      stage_acquire(ctx);
+#pragma unroll 1
+      for (int hh = 0; hh < 2; ++hh) {
+        const int c0 = u * 64 + hh * 32;
+        float v[32];
+        tmem_ld_32x32b_x32(taddr + c0, v);
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          float g[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float dz = fmaf(v[c + h], p.inv_t, -lse);
+            g[h] = ex2_approx(dz * kLog2e) * fmaf(c1, fmaxf(dz, kFloor), c0g);
+            if (c0 + c + h == ycol) g[h] += a;
+          }
+          pk[c / 2] = pack_bf16x2(g[0], g[1]);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4*>(ctx.stage + stage_off(ctx.lane, hh * 4 + q)) =
+              make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+      }
+      stage_release(ctx, col0 + u * 64, m0 + ctx.row0, false);
+    }
+  }
+};
+
+// The logits of a chunk with one of these epilogues; tiles walk M first, so
+// the pairs running at once share W tiles.
+template <int MODE>
+struct TokProb {
+  struct Params {
+    CUtensorMap a, b, c;
+    int m_tiles, n_tiles, k_blocks;
+    TokParams ep;
+  };
+  struct State {};
+  static __device__ __forceinline__ bool skip(const Params&) { return false; }
+  static __device__ __forceinline__ bool no_loads(const Params&) { return false; }
+  static __device__ __forceinline__ int* flags(const Params& p) { return p.ep.flags; }
+  static __device__ __forceinline__ int num_jobs(const Params& p, int c, int P) {
+    const int tiles = p.m_tiles * p.n_tiles;
+    return c < tiles ? (tiles - 1 - c) / P + 1 : 0;
+  }
+  static __device__ __forceinline__ TileJob job(const Params& p, int c, int P, int j) {
+    const int t = c + j * P;
+    return TileJob{0, t % p.m_tiles, t / p.m_tiles, p.k_blocks, 0, 0};
+  }
+  static __device__ __forceinline__ bool job_ok(const Params& p, const TileJob& tj) {
+    return tj.mb >= 0 && tj.mb < p.m_tiles && tj.nb >= 0 && tj.nb < p.n_tiles && tj.k_blocks > 0;
+  }
+  static __device__ __forceinline__ void load(const Params& p, int, uint8_t* a, uint8_t* b, uint32_t bar, int m0,
+                                              int n0, int k0) {
+    load_k_major(a, &p.a, bar, m0, k0);
+    load_k_major(b, &p.b, bar, n0, k0);
+  }
+  static __device__ __forceinline__ uint64_t a_desc(int, uint32_t addr, int k) { return desc_k_major(addr, k); }
+  static __device__ __forceinline__ uint64_t b_desc(int, uint32_t addr, int k) { return desc_k_major(addr, k); }
+  static __device__ __forceinline__ uint32_t idesc(int) { return idesc_bf16_f32(P_TILE_M, BN, false, false); }
+  static __device__ __forceinline__ void init(const Params&, State&) {}
+  static __device__ __forceinline__ void epilogue(const Params& p, State&, const TileJob&, EpiCtx ctx, int m0,
+                                                  int col0, uint32_t taddr) {
+    ctx.out = &p.c;
+    if constexpr (MODE == TOK_GRAD)
+      TokEpi<MODE>::grad_tile(p.ep, ctx, m0, col0, taddr);
+    else
+      TokEpi<MODE>::stats_tile(p.ep, ctx, m0, col0, taddr);
+  }
+};
+
+template <int MODE>
+cudaError_t launch_tok_mode(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, long long M, long long N,
+                            long long K, const TokParams& ep, int num_sms, cudaStream_t s) {
+  using Prob = TokProb<MODE>;
+  typename Prob::Params p;
+  p.a = a;
+  p.b = b;
+  p.c = c;
+  p.m_tiles = static_cast<int>((M + P_TILE_M - 1) / P_TILE_M);
+  p.n_tiles = static_cast<int>((N + BN - 1) / BN);
+  p.k_blocks = static_cast<int>((K + BK - 1) / BK);
+  p.ep = ep;
+  const long long tiles = static_cast<long long>(p.m_tiles) * p.n_tiles;
+  const int clusters = static_cast<int>(tiles < num_sms / 2 ? tiles : num_sms / 2);
+  if (clusters <= 0) return cudaSuccess;
+  auto kern = gemm_pair_kernel<Prob>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PairSmemLayout::kDynamicBytes);
+  if (e != cudaSuccess) return e;
+  return launch_k(kern, 2 * clusters, NUM_THREADS, PairSmemLayout::kDynamicBytes, s, p);
+}
+
+// ----------------------------------------------------------------------------
+// Merging the triples
+// ----------------------------------------------------------------------------
+struct Mst {
+  float m, s, t;
+};
+
+// (m, s, t) of the union: both sides rescaled to the larger maximum M,
+// t' = f (t + s (m - M)/T). An empty side (s = 0) leaves the other as it is.
+__device__ __forceinline__ void merge_mst(Mst& a, const Mst& b, float inv_t) {
+  const float M = fmaxf(a.m, b.m);
+  const float k = inv_t * kLog2e;
+  const float da = a.m == M ? 0.f : a.m - M, db = b.m == M ? 0.f : b.m - M;
+  const float fa = exp2f(da * k), fb = exp2f(db * k);
+  a.t = fa * (a.t + a.s * fmaxf(da * inv_t, kFloor)) + fb * (b.t + b.s * fmaxf(db * inv_t, kFloor));
+  a.s = a.s * fa + b.s * fb;
+  a.m = M;
+}
+
+__device__ __forceinline__ Mst warp_merge_mst(Mst a, float inv_t) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    Mst b;
+    b.m = __shfl_xor_sync(0xffffffffu, a.m, off);
+    b.s = __shfl_xor_sync(0xffffffffu, a.s, off);
+    b.t = __shfl_xor_sync(0xffffffffu, a.t, off);
+    merge_mst(a, b, inv_t);
+  }
+  return a;
+}
+
+// ----------------------------------------------------------------------------
+// Top-K list of a warp: 32 KPL keys in descending order, slot 32 j + lane. A
+// key orders by (logit descending, index ascending): the logit's bits mapped
+// to an ordered unsigned number above the complement of the index. 0 is empty.
+// ----------------------------------------------------------------------------
+using Key = unsigned long long;
+
+__device__ __forceinline__ Key make_key(float z, uint32_t idx) {
+  uint32_t u = __float_as_uint(z + 0.f);  // -0 counts as 0
+  u = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return (static_cast<Key>(u) << 32) | static_cast<uint32_t>(~idx);
+}
+__device__ __forceinline__ float key_value(Key k) {
+  const uint32_t u = static_cast<uint32_t>(k >> 32);
+  return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
+}
+__device__ __forceinline__ uint32_t key_index(Key k) { return ~static_cast<uint32_t>(k); }
+
+template <int KPL>
+struct TopList {
+  Key slot[KPL];
+  Key kth;  // key of slot K - 1: candidates must exceed it
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < KPL; ++j) slot[j] = 0;
+    kth = 0;
+  }
+  __device__ __forceinline__ Key at(int i) const {  // slot i (warp-uniform), in every lane
+    Key k = 0;
+#pragma unroll
+    for (int j = 0; j < KPL; ++j) {
+      const Key v = __shfl_sync(0xffffffffu, slot[j], i & 31);
+      if (j == (i >> 5)) k = v;
+    }
+    return k;
+  }
+  __device__ __forceinline__ void insert(Key key, int lane) {
+    int pos = 0;
+#pragma unroll
+    for (int j = 0; j < KPL; ++j) pos += __popc(__ballot_sync(0xffffffffu, slot[j] > key));
+    Key carry = 0;
+#pragma unroll
+    for (int j = 0; j < KPL; ++j) {
+      const Key up = __shfl_up_sync(0xffffffffu, slot[j], 1);
+      const Key last = __shfl_sync(0xffffffffu, slot[j], 31);
+      const int me = 32 * j + lane;
+      const Key moved = lane == 0 ? carry : up;
+      slot[j] = me < pos ? slot[j] : (me == pos ? key : moved);
+      carry = last;
+    }
+  }
+  // One candidate per lane (0: none), inserted while they exceed the K-th key.
+  __device__ __forceinline__ void offer(Key cand, int K, int lane) {
+    uint32_t mask = __ballot_sync(0xffffffffu, cand > kth);
+    while (mask) {
+      const int src = __ffs(mask) - 1;
+      insert(__shfl_sync(0xffffffffu, cand, src), lane);
+      kth = at(K - 1);
+      if (lane == src) cand = 0;
+      mask = __ballot_sync(0xffffffffu, cand > kth);
+    }
+  }
+};
+
+// One warp per row: the row's triples merged in a fixed order into lse, logp
+// and entropy, and the top K alternatives. The K largest logits (ties to the
+// lower index) lie in the K half tiles with the largest maxima (ties to the
+// lower tile): before a half tile outside them come K others, each with an
+// element before all of its own. So only K x 128 of the row's logits are read
+// again.
+template <int KPL>
+__global__ void __launch_bounds__(256) k_score(const TokScoreArgs p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int r = static_cast<int>((blockIdx.x * static_cast<unsigned>(blockDim.x) + threadIdx.x) >> 5);
+  const int lane = threadIdx.x & 31;
+  if (r >= p.rows) return;
+  const float4* pr = p.partials + static_cast<long long>(r) * p.nparts;
+  const int tiles = (p.V + EPI_COLS - 1) / EPI_COLS;  // half tiles that hold vocabulary columns
+  const float* z = p.Z + static_cast<long long>(r) * p.ldz;
+  Mst acc{-INFINITY, 0.f, 0.f};
+  TopList<KPL> top;
+  top.clear();
+  for (int t0 = 0; t0 < tiles; t0 += 32) {
+    const int t = t0 + lane;
+    Mst q{-INFINITY, 0.f, 0.f};
+    if (t < tiles) {
+      const float4 v = pr[t];
+      q.m = v.x;
+      q.s = v.y;
+      q.t = v.z;
+    }
+    merge_mst(acc, q, p.inv_t);
+    if (p.K > 0) top.offer(t < tiles ? make_key(q.m, static_cast<uint32_t>(t)) : 0, p.K, lane);
+  }
+  acc = warp_merge_mst(acc, p.inv_t);
+  const float logs = logf(acc.s);
+  if (lane == 0) {
+    p.lse[r] = fmaf(acc.m, p.inv_t, logs);
+    if (p.entropy != nullptr) p.entropy[r] = logs - acc.t / acc.s;
+    const long long y = p.y[r];
+    const bool given = y != p.ignore_index && y >= 0 && y < p.V;
+    float lp = 0.f;
+    if (given) lp = ((p.K > 0 ? z[y] : p.ztgt[r]) - acc.m) * p.inv_t - logs;
+    p.logp[r] = lp;
+  }
+  if (p.K == 0) return;
+  TopList<KPL> best;
+  best.clear();
+  const int ntop = tiles < p.K ? tiles : p.K;
+  for (int i = 0; i < ntop; ++i) {
+    const int tile = static_cast<int>(key_index(top.at(i)));
+    const int c = tile * EPI_COLS + lane * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < p.V && in_bounds(c + 3, p.ldz, p.flags)) v = *reinterpret_cast<const float4*>(z + c);
+    best.offer(c < p.V ? make_key(v.x, c) : 0, p.K, lane);
+    best.offer(c + 1 < p.V ? make_key(v.y, c + 1) : 0, p.K, lane);
+    best.offer(c + 2 < p.V ? make_key(v.z, c + 2) : 0, p.K, lane);
+    best.offer(c + 3 < p.V ? make_key(v.w, c + 3) : 0, p.K, lane);
+  }
+#pragma unroll
+  for (int j = 0; j < KPL; ++j) {
+    const int i = 32 * j + lane;
+    if (i < p.K) {
+      const long long at = static_cast<long long>(r) * p.K + i;
+      p.top_logp[at] = (key_value(best.slot[j]) - acc.m) * p.inv_t - logs;
+      p.top_idx[at] = static_cast<int64_t>(key_index(best.slot[j]));
+    }
+  }
+}
+
+// ----------------------------------------------------------------------------
+// Distillation
+// ----------------------------------------------------------------------------
+__device__ __forceinline__ float teacher_value(const void* t, int bf16, long long i) {
+  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(t)[i]) : static_cast<const float*>(t)[i];
+}
+
+// Clears the status block and the dH part counters; the row count of
+// k_distill_count adds into it.
+__global__ void __launch_bounds__(1024) k_distill_init(DevStatus* st, int* cnt, int ncnt) {
+  grid_dep_wait();
+  grid_dep_launch();
+  for (int i = threadIdx.x; i < ncnt; i += blockDim.x) cnt[i] = 0;
+  if (threadIdx.x == 0) {
+    st->flags = 0;
+    st->n_valid = 0;
+    st->n_counted = 0;
+    st->gscale = 0.f;
+    st->lscale = 0.0;
+  }
+}
+
+// Rows with at least one kept entry (an index in [0, V) whose teacher value is
+// above -inf), and the range bit for an index that is neither kept nor
+// ignore_index. One warp per row; the count is a sum of whole numbers, so the
+// order of the atomics does not change it.
+__global__ void __launch_bounds__(256) k_distill_count(const int64_t* __restrict__ idx, const void* __restrict__ tv,
+                                                       int t_bf16, long long N, int K, int V, long long ignore_index,
+                                                       DevStatus* st) {
+  grid_dep_wait();
+  grid_dep_launch();
+  __shared__ int s_cnt, s_bad;
+  if (threadIdx.x == 0) s_cnt = s_bad = 0;
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  const long long nwarps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
+  for (long long r = (blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x) >> 5; r < N; r += nwarps) {
+    bool kept = false, bad = false;
+    for (int k = lane; k < K; k += 32) {
+      const long long v = idx[r * K + k];
+      if (v == ignore_index) continue;
+      if (v < 0 || v >= V)
+        bad = true;
+      else if (!(teacher_value(tv, t_bf16, r * K + k) == -INFINITY))
+        kept = true;
+    }
+    const bool any = __any_sync(0xffffffffu, kept), anybad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) {
+      if (any) atomicAdd(&s_cnt, 1);
+      if (anybad) atomicOr(&s_bad, 1);
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    if (s_cnt) atomicAdd(reinterpret_cast<unsigned long long*>(&st->n_counted), static_cast<unsigned long long>(s_cnt));
+    if (s_bad) atomicOr(&st->flags, kFlagLabelRange);
+  }
+}
+
+constexpr int kRowThreads = 256;
+
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float s = 0.f;
+  for (int i = 0; i < kRowThreads / 32; ++i) s += red[i];
+  return s;
+}
+__device__ __forceinline__ float block_max(float v, float* red) {
+  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float s = red[0];
+  for (int i = 1; i < kRowThreads / 32; ++i) s = fmaxf(s, red[i]);
+  return s;
+}
+
+// One block per row of the chunk. The row's triples give lse; the K entries
+// give the teacher's probabilities q and the row's loss
+//   T^2 sum_k q_k (log q_k - z'_k + lse);
+// with GRAD the row of the gradient tile is written in one pass over the
+// stored logits,
+//   G_v = m p_v - sum_k q_k [v = idx_k],   m = sum_k q_k,
+// in fp32 with one rounding to bf16 (the operand type of the GEMMs behind
+// it). The kept entries are written last, by one thread each: of entries with
+// the same index the first writes, with the sum of their q.
+template <bool GRAD>
+__global__ void __launch_bounds__(kRowThreads) k_distill_row(const DistillArgs p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  __shared__ float red[kRowThreads / 32];
+  __shared__ Mst s_mst[kRowThreads / 32];
+  __shared__ int s_idx[kMaxTop];
+  __shared__ float s_q[kMaxTop];
+  const int r = blockIdx.x, tid = threadIdx.x;
+  const float* z = p.Z + static_cast<long long>(r) * p.ldz;
+  __nv_bfloat16* g = GRAD ? p.G + static_cast<long long>(r) * p.ldg : nullptr;
+
+  // the chunk's first row sets the scales: n is known since the count ran
+  if (r == 0 && tid == 0) {
+    const long long n = p.n_override >= 0 ? p.n_override : p.st->n_counted;
+    const double w = p.mean ? (n > 0 ? 1.0 / static_cast<double>(n) : 0.0) : 1.0;
+    const float up = p.grad_loss != nullptr ? *p.grad_loss : 1.f;
+    p.st->n_valid = n;
+    p.st->lscale = w;
+    p.st->gscale = static_cast<float>(static_cast<double>(up) * w / static_cast<double>(p.inv_t));
+  }
+
+  // the teacher's entry of this thread
+  const long long at = static_cast<long long>(r) * p.K + tid;
+  int vi = -1;
+  float tv = -INFINITY;
+  if (tid < p.K) {
+    const long long v = p.idx[at];
+    if (v != p.ignore_index && v >= 0 && v < p.V) {
+      tv = teacher_value(p.t, p.t_bf16, at);
+      if (!(tv == -INFINITY)) vi = static_cast<int>(v);
+    }
+  }
+  const bool kept = __syncthreads_or(vi >= 0) != 0;
+  if (!kept) {  // nothing of the teacher in this row: no loss, a zero gradient
+    if (tid == 0) p.row_loss[r] = 0.f;
+    if (GRAD)
+      for (int c = tid * 8; c < p.V; c += kRowThreads * 8) *reinterpret_cast<uint4*>(g + c) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  float q = 0.f, logq = 0.f;
+  if (p.renormalize) {
+    const float top = block_max(vi >= 0 ? tv : -INFINITY, red);
+    const float e = vi >= 0 ? exp2f((tv - top) * p.inv_t * kLog2e) : 0.f;
+    const float sum = block_sum(e, red);
+    if (vi >= 0) {
+      q = e / sum;
+      logq = (tv - top) * p.inv_t - logf(sum);
+    }
+  } else if (vi >= 0) {
+    q = expf(tv);
+    logq = tv;
+  }
+  const float mass = block_sum(q, red);
+
+  Mst acc{-INFINITY, 0.f, 0.f};
+  const float4* pr = p.partials + static_cast<long long>(r) * p.nparts;
+  const int tiles = (p.V + EPI_COLS - 1) / EPI_COLS;
+  for (int t = tid; t < tiles; t += kRowThreads) {
+    const float4 v = pr[t];
+    merge_mst(acc, Mst{v.x, v.y, v.z}, p.inv_t);
+  }
+  acc = warp_merge_mst(acc, p.inv_t);
+  if ((tid & 31) == 0) s_mst[tid >> 5] = acc;
+  if (tid < kMaxTop) {
+    s_idx[tid] = vi;
+    s_q[tid] = q;
+  }
+  __syncthreads();
+  acc = s_mst[0];
+  for (int i = 1; i < kRowThreads / 32; ++i) merge_mst(acc, s_mst[i], p.inv_t);
+  const float logs = logf(acc.s);
+
+  float zk = 0.f, term = 0.f;
+  if (vi >= 0) {
+    zk = z[vi];
+    if (q > 0.f || q != q) term = q * (logq - (zk - acc.m) * p.inv_t + logs);
+  }
+  const float loss = block_sum(term, red);
+  if (tid == 0) p.row_loss[r] = loss / (p.inv_t * p.inv_t);
+  if (!GRAD) return;
+
+  const float k = p.inv_t * kLog2e, w = mass / acc.s;
+  for (int c = tid * 8; c < p.V; c += kRowThreads * 8) {
+    // columns past V (up to 7) lie inside the row's padding: never read by the GEMMs
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(z + c));
+    const float4 b = __ldcs(reinterpret_cast<const float4*>(z + c + 4));
+    uint4 o;
+    o.x = pack_bf16x2(w * ex2_approx((a.x - acc.m) * k), w * ex2_approx((a.y - acc.m) * k));
+    o.y = pack_bf16x2(w * ex2_approx((a.z - acc.m) * k), w * ex2_approx((a.w - acc.m) * k));
+    o.z = pack_bf16x2(w * ex2_approx((b.x - acc.m) * k), w * ex2_approx((b.y - acc.m) * k));
+    o.w = pack_bf16x2(w * ex2_approx((b.z - acc.m) * k), w * ex2_approx((b.w - acc.m) * k));
+    *reinterpret_cast<uint4*>(g + c) = o;
+  }
+  __syncthreads();
+  if (vi >= 0) {
+    float sum = 0.f;
+    bool first = true;
+    for (int j = 0; j < p.K; ++j) {
+      if (s_idx[j] != vi) continue;
+      if (j < tid) first = false;
+      sum += s_q[j];
+    }
+    if (first) g[vi] = __float2bfloat16_rn(w * ex2_approx((zk - acc.m) * k) - sum);
+  }
+}
+
+}  // namespace
+
+// ----------------------------------------------------------------------------
+// Launch wrappers
+// ----------------------------------------------------------------------------
+cudaError_t launch_tok_logits(int mode, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, long long M,
+                              long long N, long long K, const TokParams& ep, int num_sms, cudaStream_t s) {
+  switch (mode) {
+    case TOK_STATS: return launch_tok_mode<TOK_STATS>(a, b, c, M, N, K, ep, num_sms, s);
+    case TOK_STATS_Z: return launch_tok_mode<TOK_STATS_Z>(a, b, c, M, N, K, ep, num_sms, s);
+    default: return launch_tok_mode<TOK_GRAD>(a, b, c, M, N, K, ep, num_sms, s);
+  }
+}
+
+cudaError_t launch_score(const TokScoreArgs& p, cudaStream_t s) {
+  if (p.rows <= 0) return cudaSuccess;
+  const int grid = (p.rows + 7) / 8;
+  if (p.K <= 32) return launch_k(k_score<1>, grid, 256, 0, s, p);
+  return launch_k(k_score<kMaxTop / 32>, grid, 256, 0, s, p);
+}
+
+cudaError_t launch_distill_count(const int64_t* idx, const void* t, int t_bf16, long long N, int K, int V,
+                                 long long ignore_index, DevStatus* st, int* cnt, int ncnt, int num_sms,
+                                 cudaStream_t s) {
+  const cudaError_t e = launch_k(k_distill_init, 1, 1024, 0, s, st, cnt, ncnt);
+  if (e != cudaSuccess || N <= 0) return e;
+  const long long want = (N + 7) / 8;
+  const int grid = static_cast<int>(want < 4ll * num_sms ? want : 4ll * num_sms);
+  return launch_k(k_distill_count, grid, 256, 0, s, idx, t, t_bf16, N, K, V, ignore_index, st);
+}
+
+cudaError_t launch_distill_row(const DistillArgs& p, int rows, cudaStream_t s) {
+  if (rows <= 0) return cudaSuccess;
+  return p.G != nullptr ? launch_k(k_distill_row<true>, rows, kRowThreads, 0, s, p)
+                        : launch_k(k_distill_row<false>, rows, kRowThreads, 0, s, p);
+}
+
+}  // namespace lce

@@ -14,6 +14,10 @@ Entry points (same names as the C ABI):
   lce_vshard_forward_stats / lce_vshard_combine / lce_vshard_backward   W split by vocabulary rows
   lce_vshard_chunk_stats / lce_vshard_chunk_backward   the same per chunk, the exp tile kept between them
   lce_rmsnorm_forward / lce_rmsnorm_backward / lce_norm_fwd_bwd         the final RMSNorm, alone or fused
+  lce_logprobs(H, W, y, top_k=..)        -> logp, lse, entropy, top_logp, top_idx
+  lce_logprobs_backward(H, W, y, lse, entropy, g_logp, g_entropy) -> dH, dW
+  lce_distill_forward(H, W, idx, t)      -> loss, row_loss against a teacher's top logits
+  lce_distill_fwd_bwd(H, W, idx, t, g)   -> loss, row_loss, dH, dW
   lce_scale_grads, auto_chunk (lce_auto_chunk), workspace_size, read_device_status, profile_begin/end
 """
 from __future__ import annotations
@@ -40,6 +44,8 @@ LCE_OP_FORWARD, LCE_OP_BACKWARD, LCE_OP_FWD_BWD, LCE_OP_VSHARD_COMBINE, LCE_OP_N
 LCE_OP_VSHARD_CHUNK = 5
 LCE_DEVICE_LABEL_RANGE, LCE_DEVICE_TIMEOUT, LCE_DEVICE_BOUNDS = 1, 2, 4
 LCE_TEST_FORCE_TIMEOUT = 0x7E57
+LCE_MAX_TOP = 128
+LCE_TEACHER_BF16, LCE_TEACHER_LOGPROBS = 1, 2
 
 # Every symbol include/lce.h declares.
 EXPORTED = ("lce_opts_init", "lce_workspace_size", "lce_forward", "lce_backward", "lce_fwd_bwd",
@@ -47,7 +53,9 @@ EXPORTED = ("lce_opts_init", "lce_workspace_size", "lce_forward", "lce_backward"
             "lce_profile_end", "lce_kernel_name", "lce_forward_noalloc", "lce_auto_chunk",
             "lce_vshard_forward_stats", "lce_vshard_combine", "lce_vshard_backward",
             "lce_rmsnorm_workspace_size", "lce_rmsnorm_forward", "lce_rmsnorm_backward", "lce_norm_fwd_bwd",
-            "lce_scale_grads", "lce_fwd_bwd_sliced", "lce_vshard_chunk_stats", "lce_vshard_chunk_backward")
+            "lce_scale_grads", "lce_fwd_bwd_sliced", "lce_vshard_chunk_stats", "lce_vshard_chunk_backward",
+            "lce_logprobs_workspace_size", "lce_logprobs", "lce_logprobs_backward", "lce_distill_workspace_size",
+            "lce_distill_forward", "lce_distill_fwd_bwd")
 LCE_KERNEL_KINDS = 11
 # Kernel kinds whose profiled work is flops (tensor-core GEMMs); the others count bytes.
 GEMM_KINDS = ("logits_stats", "logits_grad", "gemm_dH_dW", "logits_ref")
@@ -140,6 +148,19 @@ def load(path: str | None = None):
         lib.lce_auto_chunk.restype = I64
         lib.lce_forward_noalloc.argtypes = [P, P, P, I64, I64, I64, P, P, OPT, P]
         lib.lce_forward_noalloc.restype = I32
+        SZ = ctypes.c_size_t
+        lib.lce_logprobs_workspace_size.argtypes = [I64, I64, I64, I32, OPT]
+        lib.lce_logprobs_workspace_size.restype = SZ
+        lib.lce_logprobs.argtypes = [P, P, P, I64, I64, I64, F32, I32, P, P, P, P, P, OPT, P, SZ, P]
+        lib.lce_logprobs.restype = I32
+        lib.lce_logprobs_backward.argtypes = [P, P, P, I64, I64, I64, F32, P, P, P, P, P, P, OPT, P, SZ, P]
+        lib.lce_logprobs_backward.restype = I32
+        lib.lce_distill_workspace_size.argtypes = [I64, I64, I64, I32, I32, OPT]
+        lib.lce_distill_workspace_size.restype = SZ
+        lib.lce_distill_forward.argtypes = [P, P, P, P, I64, I64, I64, I32, I32, F32, P, P, OPT, P, SZ, P]
+        lib.lce_distill_forward.restype = I32
+        lib.lce_distill_fwd_bwd.argtypes = [P, P, P, P, I64, I64, I64, I32, I32, F32, P, P, P, P, P, OPT, P, SZ, P]
+        lib.lce_distill_fwd_bwd.restype = I32
         lib.lce_kernel_name.argtypes = [I32]
         lib.lce_kernel_name.restype = ctypes.c_char_p
         _lib = lib
@@ -674,6 +695,187 @@ def lce_norm_fwd_bwd(x, w_norm, W, y, grad_loss=None, eps=1e-6, *, dW=None, work
     _raise(rc, "lce_norm_fwd_bwd")
     _keep(stream, ws, loss, lse, dx, dw_norm, dW, grad_loss)
     return loss, lse, dx, dw_norm, dW
+
+
+# ---------------------------------------------------------------------------
+# Token operators (see include/lce.h)
+# ---------------------------------------------------------------------------
+def lce_logprobs_workspace_size(N: int, d: int, V: int, top_k: int = 0, opts: LceOpts | None = None) -> int:
+    return int(load().lce_logprobs_workspace_size(int(N), int(d), int(V), int(top_k),
+                                                  ctypes.byref(opts) if opts is not None else None))
+
+
+def lce_distill_workspace_size(N: int, d: int, V: int, K: int, with_grad: bool = True,
+                               opts: LceOpts | None = None) -> int:
+    return int(load().lce_distill_workspace_size(int(N), int(d), int(V), int(K), int(bool(with_grad)),
+                                                 ctypes.byref(opts) if opts is not None else None))
+
+
+def _token_opts(opt_kw, N, device, size):
+    """Options of a token call; chunk_tokens="auto" takes the largest multiple
+    of 256 (at most 4096) whose workspace, size(opts), fits in half of the
+    device's free memory."""
+    if opt_kw.get("chunk_tokens", 0) != "auto":
+        return make_opts(**opt_kw)
+    import torch
+    free, _ = torch.cuda.mem_get_info(device)
+    for chunk in range(min(4096, max(256, (N + 255) // 256 * 256)), 0, -256):
+        opts = make_opts(**{**opt_kw, "chunk_tokens": chunk})
+        if size(opts) <= free // 2:
+            return opts
+    raise LCEError(LCE_ERR_WORKSPACE, "chunk_tokens: not even a 256-token chunk fits in half the free memory")
+
+
+def _token_workspace(need, what, device, workspace):
+    """As _workspace, for the calls whose size depends on more than N, d and V."""
+    import torch
+    if need == 0:
+        raise LCEError(LCE_ERR_INVALID_ARG, what)
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    _check_dev(workspace, "workspace", torch.uint8, device=device)
+    if workspace.numel() < need:
+        raise LCEError(LCE_ERR_WORKSPACE, f"workspace of {workspace.numel()} bytes, the call needs {need}")
+    return workspace
+
+
+def _token_grads(H, V, d, opts, dW, need_dH, need_dW):
+    """The gradient outputs of a token call: dH and dW, or None where not wanted."""
+    import torch
+    if not (need_dH or need_dW):
+        raise ValueError("neither dH nor dW is wanted")
+    if not need_dW:
+        if dW is not None:
+            raise ValueError("a dW tensor was passed, but need_dW is False")
+        _no_accumulate_without_dW(opts)
+    elif dW is None:
+        _no_accumulate_without_dW(opts)
+        dW = torch.empty((V, d), dtype=torch.float32, device=H.device)
+    return (torch.empty_like(H) if need_dH else None), dW
+
+
+def lce_logprobs(H, W, y, *, top_k: int = 0, temperature: float = 1.0, entropy: bool = True, workspace=None,
+                 stream=None, **opt_kw):
+    """Log-probabilities of the tokens y [N] under softmax(H W^T / temperature):
+    returns logp, lse, entropy (fp32 [N]; entropy None if not wanted) and the
+    top_k most likely tokens of each position, top_logp (fp32) and top_idx
+    (int64) [N, top_k] (None if top_k is 0). logp is 0 where y is ignore_index."""
+    import torch
+    N, d, V = _check_inputs(H, W, y)
+    K = int(top_k)
+    opts = _token_opts(opt_kw, N, H.device, lambda o: lce_logprobs_workspace_size(N, d, V, K, o))
+    ws = _token_workspace(lce_logprobs_workspace_size(N, d, V, K, opts), "lce_logprobs_workspace_size", H.device,
+                          workspace)
+    row = lambda: torch.empty(max(N, 1), dtype=torch.float32, device=H.device)[:N]  # noqa: E731
+    logp, lse, ent = row(), row(), row() if entropy else None
+    top_logp = top_idx = None
+    if K > 0:
+        top_logp = torch.empty((max(N, 1), K), dtype=torch.float32, device=H.device)[:N]
+        top_idx = torch.empty((max(N, 1), K), dtype=torch.int64, device=H.device)[:N]
+    rc = load().lce_logprobs(_ptr(H), _ptr(W), _ptr(y), N, d, V, float(temperature), K, _ptr(logp), _ptr(lse),
+                             _ptr(ent), _ptr(top_logp), _ptr(top_idx), ctypes.byref(opts), _ptr(ws), ws.numel(),
+                             _stream(stream))
+    _raise(rc, "lce_logprobs")
+    _keep(stream, H, W, y, ws, logp, lse, ent, top_logp, top_idx)
+    return logp, lse, ent, top_logp, top_idx
+
+
+def lce_logprobs_backward(H, W, y, lse, entropy, g_logp, g_entropy=None, *, temperature: float = 1.0, dW=None,
+                          need_dH: bool = True, need_dW: bool = True, workspace=None, stream=None, **opt_kw):
+    """dH (bf16 [N, d]) and dW (fp32 [V, d]) of lce_logprobs' logp and entropy for
+    upstream gradients g_logp and g_entropy (fp32 [N]; g_entropy may be None),
+    from its lse and entropy. A gradient that is not wanted is None."""
+    import torch
+    N, d, V = _check_inputs(H, W, y)
+    for name, t in (("lse", lse), ("g_logp", g_logp)):
+        if t is None:
+            raise ValueError(f"{name} is required")
+    if g_entropy is not None and entropy is None:
+        raise ValueError("g_entropy needs the entropy of lce_logprobs")
+    for name, t in (("lse", lse), ("entropy", entropy), ("g_logp", g_logp), ("g_entropy", g_entropy)):
+        _check_dev(t, name, torch.float32, shape=(N,), device=H.device)
+    _check_dev(dW, "dW", torch.float32, shape=(V, d), device=H.device)
+    opts = _token_opts(opt_kw, N, H.device, lambda o: workspace_size(LCE_OP_BACKWARD, N, d, V, o))
+    ws = _workspace(LCE_OP_BACKWARD, N, d, V, opts, H.device, workspace)
+    dH, dW = _token_grads(H, V, d, opts, dW, need_dH, need_dW)
+    rc = load().lce_logprobs_backward(_ptr(H), _ptr(W), _ptr(y), N, d, V, float(temperature), _ptr(lse),
+                                      _ptr(entropy), _ptr(g_logp), _ptr(g_entropy), _ptr(dH), _ptr(dW),
+                                      ctypes.byref(opts), _ptr(ws), ws.numel(), _stream(stream))
+    _raise(rc, "lce_logprobs_backward")
+    _keep(stream, H, W, y, ws, lse, entropy, g_logp, g_entropy, dH, dW)
+    return dH, dW
+
+
+def _check_teacher(H, W, idx, t):
+    import torch
+    if not (H.is_cuda and W.is_cuda and idx.is_cuda and t.is_cuda):
+        raise ValueError("H, W, idx and t must be CUDA tensors (there is no CPU path)")
+    if H.dtype != torch.bfloat16 or W.dtype != torch.bfloat16 or idx.dtype != torch.int64:
+        raise ValueError("H and W must be bfloat16, idx int64")
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"t must be float32 or bfloat16, got {t.dtype}")
+    if H.dim() != 2 or W.dim() != 2 or idx.dim() != 2 or H.shape[1] != W.shape[1] or idx.shape[0] != H.shape[0] \
+            or idx.shape != t.shape:
+        raise ValueError("shapes must be H [N, d], W [V, d], idx [N, K], t [N, K]")
+    if not 1 <= idx.shape[1] <= LCE_MAX_TOP:
+        raise ValueError(f"idx must have 1 to {LCE_MAX_TOP} entries a row, has {idx.shape[1]}")
+    if not (H.is_contiguous() and W.is_contiguous() and idx.is_contiguous() and t.is_contiguous()):
+        raise ValueError("H, W, idx and t must be contiguous")
+    if not (H.device == W.device == idx.device == t.device):
+        raise ValueError("H, W, idx and t must be on the same device")
+    if H.device.index != torch.cuda.current_device():
+        raise ValueError(f"the inputs are on {H.device}; make it the current device (torch.cuda.set_device)")
+    return H.shape[0], H.shape[1], W.shape[0], idx.shape[1], LCE_TEACHER_BF16 if t.dtype == torch.bfloat16 else 0
+
+
+def _distill_mode(teacher, renormalize, temperature):
+    if not renormalize and temperature != 1.0:
+        raise ValueError("renormalize=False takes the teacher's log-probabilities as they are: temperature must be 1")
+    return teacher | (0 if renormalize else LCE_TEACHER_LOGPROBS)
+
+
+def lce_distill_forward(H, W, idx, t, *, temperature: float = 1.0, renormalize: bool = True, workspace=None,
+                        stream=None, **opt_kw):
+    """loss (fp32 [1]) and row_loss (fp32 [N]) of KL(teacher || softmax(H W^T / temperature)),
+    the teacher given by its top tokens idx (int64 [N, K], ignore_index: not
+    kept) with values t (fp32 or bf16): logits, softmaxed over the kept entries,
+    or with renormalize=False log-probabilities taken as they are."""
+    import torch
+    N, d, V, K, teacher = _check_teacher(H, W, idx, t)
+    teacher = _distill_mode(teacher, renormalize, temperature)
+    opts = _token_opts(opt_kw, N, H.device, lambda o: lce_distill_workspace_size(N, d, V, K, False, o))
+    ws = _token_workspace(lce_distill_workspace_size(N, d, V, K, False, opts), "lce_distill_workspace_size", H.device,
+                          workspace)
+    loss = torch.empty(1, dtype=torch.float32, device=H.device)
+    row_loss = torch.empty(max(N, 1), dtype=torch.float32, device=H.device)[:N]
+    rc = load().lce_distill_forward(_ptr(H), _ptr(W), _ptr(idx), _ptr(t), N, d, V, K, teacher, float(temperature),
+                                    _ptr(loss), _ptr(row_loss), ctypes.byref(opts), _ptr(ws), ws.numel(),
+                                    _stream(stream))
+    _raise(rc, "lce_distill_forward")
+    _keep(stream, H, W, idx, t, ws, loss, row_loss)
+    return loss, row_loss
+
+
+def lce_distill_fwd_bwd(H, W, idx, t, grad_loss=None, *, temperature: float = 1.0, renormalize: bool = True, dW=None,
+                        need_dH: bool = True, need_dW: bool = True, workspace=None, stream=None, **opt_kw):
+    """lce_distill_forward and its gradients in one call: loss, row_loss, dH
+    (bf16 [N, d]), dW (fp32 [V, d]); a gradient that is not wanted is None."""
+    import torch
+    N, d, V, K, teacher = _check_teacher(H, W, idx, t)
+    teacher = _distill_mode(teacher, renormalize, temperature)
+    _check_grads(H, N, d, V, grad_loss=grad_loss, dW=dW)
+    opts = _token_opts(opt_kw, N, H.device, lambda o: lce_distill_workspace_size(N, d, V, K, True, o))
+    ws = _token_workspace(lce_distill_workspace_size(N, d, V, K, True, opts), "lce_distill_workspace_size", H.device,
+                          workspace)
+    loss = torch.empty(1, dtype=torch.float32, device=H.device)
+    row_loss = torch.empty(max(N, 1), dtype=torch.float32, device=H.device)[:N]
+    dH, dW = _token_grads(H, V, d, opts, dW, need_dH, need_dW)
+    rc = load().lce_distill_fwd_bwd(_ptr(H), _ptr(W), _ptr(idx), _ptr(t), N, d, V, K, teacher, float(temperature),
+                                    _ptr(grad_loss), _ptr(loss), _ptr(row_loss), _ptr(dH), _ptr(dW),
+                                    ctypes.byref(opts), _ptr(ws), ws.numel(), _stream(stream))
+    _raise(rc, "lce_distill_fwd_bwd")
+    _keep(stream, H, W, idx, t, ws, loss, row_loss, dH, dW, grad_loss)
+    return loss, row_loss, dH, dW
 
 
 def lce_scale_grads(dH, dW, grad_loss, *, stream=None):

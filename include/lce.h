@@ -298,6 +298,76 @@ int lce_norm_fwd_bwd(const void* x, const float* w_norm, float eps, const void* 
  * gradient only in its backward. No host synchronisation. */
 int lce_scale_grads(void* dH, float* dW, int64_t N, int64_t d, int64_t V, const float* grad_loss, void* stream);
 
+/*
+ * Token operators of the head: what a model needs of its logits besides the
+ * cross-entropy. z = H W^T as above, z' = z / temperature (> 0, finite), p =
+ * softmax(z'). H, W, y, dH, dW, opts, ws and stream are those of the calls
+ * above; the logits of one chunk at a time are held in the workspace, never
+ * [N, V]. opts->reserved must be 0.
+ *
+ * lce_logprobs, per row i (device outputs):
+ *   lse [N]      log sum_v exp(z'_iv)
+ *   logp [N]     z'_{i,y_i} - lse_i; 0 where y_i is ignore_index (or out of
+ *                range: the status bit of lce_forward)
+ *   entropy [N]  -sum_v p_iv log p_iv, every row; may be NULL
+ *   top_idx, top_logp [N, top_k]  (int64, fp32) the top_k most likely tokens of
+ *                every row in falling order of z, the lower index first among
+ *                equals, and their log-probabilities; 0 <= top_k <=
+ *                LCE_MAX_TOP, top_k <= V; NULL when top_k is 0
+ * A row with a NaN or +inf logit has NaN statistics, and its alternatives are
+ * some tokens of the vocabulary. Workspace: lce_logprobs_workspace_size.
+ *
+ * lce_logprobs_backward: gradients from upstream g_logp [N] and g_entropy [N]
+ * (fp32; g_entropy may be NULL: zero), with lse and entropy of lce_logprobs on
+ * the same inputs (entropy may be NULL if g_entropy is). With a_i = g_logp_i (0
+ * where y_i is ignored) and e_i = g_entropy_i
+ *   G_iv = ([v = y_i] a_i - p_iv (a_i + e_i (log p_iv + entropy_i))) / temperature
+ *   dH = G W (bf16), dW = G^T H (fp32; added to with opts->accumulate_dW).
+ * G is rounded to bf16 once. Either of dH, dW may be NULL: not wanted, not
+ * computed. Workspace: lce_workspace_size(LCE_OP_BACKWARD, ...).
+ */
+#define LCE_MAX_TOP 128
+size_t lce_logprobs_workspace_size(int64_t N, int64_t d, int64_t V, int32_t top_k, const lce_opts* opts);
+int lce_logprobs(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V, float temperature,
+                 int32_t top_k, float* logp, float* lse, float* entropy, float* top_logp, int64_t* top_idx,
+                 const lce_opts* opts, void* ws, size_t ws_bytes, void* stream);
+int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
+                          float temperature, const float* lse, const float* entropy, const float* g_logp,
+                          const float* g_entropy, void* dH, float* dW, const lce_opts* opts, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/*
+ * Distillation from a teacher's top logits: per row, K tokens idx [N, K]
+ * (int64) with their teacher values t [N, K] (fp32, or bf16 with
+ * LCE_TEACHER_BF16). An entry is kept unless its index is opts->ignore_index
+ * (a shorter list, padded) or its value -inf; an index that is neither
+ * ignore_index nor in [0, V) is not kept either and sets the status bit
+ * LCE_DEVICE_LABEL_RANGE. An index may occur twice: its shares add up.
+ *   q_ik = softmax over the row's kept entries of t_ik / temperature, or, with
+ *          LCE_TEACHER_LOGPROBS, exp(t_ik): log-probabilities taken as they
+ *          are (temperature must be 1), the rest of the teacher's mass left out
+ *   row_loss_i = temperature^2 sum_k q_ik (log q_ik - log p_{i,idx_ik})
+ *   loss = sum_i row_loss_i / n (LCE_MEAN) or without / n (LCE_SUM), n = rows
+ *          with a kept entry, or opts->n_valid_override
+ *   G_iv = (grad_loss temperature / n) (p_iv sum_k q_ik - sum_k q_ik [v = idx_ik])
+ *   dH = G W (bf16), dW = G^T H (fp32; opts->accumulate_dW)
+ * Rows without a kept entry have row_loss 0 and a zero gradient. The tile of G
+ * without its leading factor is rounded to bf16 once. 1 <= K <= LCE_MAX_TOP.
+ * loss [1], row_loss [N] fp32; grad_loss: device fp32 [1] or NULL (1.0); either
+ * of dH, dW may be NULL: not wanted, not computed. Workspace:
+ * lce_distill_workspace_size (with_grad: 0 for the forward, 1 for both).
+ */
+#define LCE_TEACHER_BF16 1
+#define LCE_TEACHER_LOGPROBS 2
+size_t lce_distill_workspace_size(int64_t N, int64_t d, int64_t V, int32_t K, int32_t with_grad, const lce_opts* opts);
+int lce_distill_forward(const void* H, const void* W, const int64_t* idx, const void* t, int64_t N, int64_t d,
+                        int64_t V, int32_t K, int32_t teacher, float temperature, float* loss, float* row_loss,
+                        const lce_opts* opts, void* ws, size_t ws_bytes, void* stream);
+int lce_distill_fwd_bwd(const void* H, const void* W, const int64_t* idx, const void* t, int64_t N, int64_t d,
+                        int64_t V, int32_t K, int32_t teacher, float temperature, const float* grad_loss, float* loss,
+                        float* row_loss, void* dH, float* dW, const lce_opts* opts, void* ws, size_t ws_bytes,
+                        void* stream);
+
 /* Synchronise the stream and copy the workspace's device status bits
  * (LCE_DEVICE_*) of the last call that used ws into *flags. */
 int lce_read_device_status(const void* ws, void* stream, int* flags);

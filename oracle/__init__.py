@@ -23,6 +23,9 @@ from .lce_oracle import (  # noqa: F401
     lce_f64, norm_lce_bf16, rmsnorm_backward_f64, rmsnorm_f64, round_bf16_bits,
     vshard_backward_f64, vshard_merge_f64, vshard_stats_f64,
 )
+from .tokens_oracle import (  # noqa: F401
+    distill_f64, logprobs_backward_f64, logprobs_f64, teacher_f64,
+)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _SRC = os.path.join(_HERE, "lce_oracle.c")

@@ -1,0 +1,510 @@
+"""The head's token operators on the GPU against the fp64 oracle.
+
+Inputs lie on a grid (H on 1/16 and W on 1/64, at most 7 bits and a sign), so
+every logit is a whole multiple of 2^-10 below 2^24 of them and exact in fp32
+in any order of its sum: the alternatives, ties included, are the oracle's.
+
+Tolerances, with z' = z / T, D the largest |z'| spread, eps = 2^-24 (fp32) and
+u = 2^-8 (bf16):
+  lse, logp    each exponential errs by 2^-22 (ex2.approx) and by the rounding
+               of its argument, 3 eps |z' - m| (weighted by p it averages below
+               3 eps (entropy + 1) <= 3 eps 13); a sum in fp32 over 32 terms, 4
+               groups and the merges of up to 1200 half tiles adds at most
+               (32 + 4 + 40 + 12) eps; the final sum rounds eps |lse|, z / T
+               eps |z'|: together below 2^-16 + 2^-21 (|lse| + |z'|)
+  entropy      log S - T/S: the same relative errors on S and on T, T/S up to
+               ln V <= 12: 13 times the bound above
+  gradients    each entry of G is rounded to bf16 once (u), its factors err by
+               less than 2^-10 relative (lse and entropy as above, up to 13
+               nats): every element of dW lies within (u + 2^-10) bulk, bulk the
+               sum of the absolute terms it is made of, of dH within that plus
+               its own rounding u |dH|; whole tensors within 5e-3 (rounding
+               errors average: 2 u / sqrt(3)).
+"""
+import numpy as np
+import pytest
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -8
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def grid(x, steps):
+    return np.clip(np.round(x * steps), -127, 127) / steps
+
+
+def dev(x, dtype=None):
+    torch = _torch()
+    t = torch.from_numpy(np.ascontiguousarray(x)).cuda()
+    return t if dtype is None else t.to(dtype)
+
+
+def make(N, d, V, seed=0, scale=2.0, peak=8.0):
+    """H, W (fp64, on the grid), labels with some ignored; rows lean towards their label."""
+    rng = np.random.default_rng(seed)
+    sigma = scale / np.sqrt(d)
+    W = grid(rng.standard_normal((V, d)) * min(1.0, sigma), 64)
+    y = rng.integers(0, V, N)
+    H = rng.standard_normal((N, d)) + W[y] * (peak * rng.random((N, 1)) / (sigma * sigma * d))
+    H = grid(H, 16)
+    y[rng.random(N) < 0.15] = oracle.IGNORE_INDEX
+    return rng, H, W, y.astype(np.int64)
+
+
+def heads(H, W):
+    torch = _torch()
+    return dev(H, torch.bfloat16), dev(W, torch.bfloat16)
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def close(got, ref, tol, what):
+    err = np.abs(np64(got) - ref)
+    assert np.all(err <= tol), f"{what}: off by {np.nanmax(err):.3e}, {np.nanmax(err / tol):.2f} of the bound"
+
+
+def tol_lse(H, W, lse, T):
+    zmax = np.abs(H @ W.T).max(axis=1) / T
+    return 2.0 ** -16 + 2.0 ** -21 * (np.abs(lse) + zmax)
+
+
+def check_scores(out, H, W, y, T, K):
+    logp, lse, ent, tl, ti = out
+    ref = oracle.logprobs_f64(H, W, y, temperature=T, top_k=K)
+    tol = tol_lse(H, W, ref["lse"], T)
+    close(lse, ref["lse"], tol, "lse")
+    close(logp, ref["logp"], 2 * tol, "logp")
+    if ent is not None:
+        close(ent, ref["entropy"], 13 * tol, "entropy")
+    if K:
+        assert (ti.cpu().numpy() == ref["top_idx"]).all(), "alternatives"
+        close(tl, ref["top_logp"], 2 * tol[:, None], "top_logp")
+    return ref
+
+
+def check_grads(dH, dW, ref):
+    for got, name in ((dH, "dH"), (dW, "dW")):
+        if got is None:
+            continue
+        out = U * np.abs(ref[name]) if name == "dH" else 0.0
+        close(got, ref[name], (U + 2.0 ** -10) * ref[name + "_bulk"] + out + 1e-30, name)
+        norm = np.linalg.norm(ref[name])
+        assert np.linalg.norm(np64(got) - ref[name]) <= 5e-3 * norm, name
+
+
+# N, d, V, K, T, chunk
+SCORE_CASES = [
+    (1, 8, 1, 1, 1.0, 0),            # one token, one word
+    (1, 64, 37, 5, 1.0, 0),          # one decoded token
+    (3, 72, 2, 2, 0.7, 0),           # K tail, two words, both returned
+    (5, 64, 128, 128, 2.0, 0),       # every word of one half tile returned
+    (16, 128, 129, 33, 1.0, 0),      # one column in the second half tile
+    (33, 64, 5003, 64, 0.5, 0),
+    (64, 256, 4096, 8, 1.0, 0),
+    (65, 256, 4096, 1, 1.0, 0),
+    (100, 136, 12345, 40, 1.3, 0),
+    (129, 136, 4099, 20, 1.0, 64),   # chunks smaller than a tile
+    (257, 264, 1000, 0, 1.0, 0),     # no alternatives
+    (300, 264, 5003, 128, 1.0, 128),
+    (513, 256, 1000, 7, 1.3, 200),   # chunks that are not a multiple of the tile
+    (2, 64, 151655, 20, 1.0, 0),     # the unpadded vocabulary
+    (130, 64, 70001, 9, 1.0, 0),
+]
+
+
+@pytest.mark.parametrize("N,d,V,K,T,chunk", SCORE_CASES)
+def test_logprobs(cuda_lib, N, d, V, K, T, chunk):
+    _, H, W, y = make(N, d, V, seed=N + V)
+    Ht, Wt = heads(H, W)
+    out = cuda_lib.lce_logprobs(Ht, Wt, dev(y), top_k=K, temperature=T, chunk_tokens=chunk, sync_check=True)
+    check_scores(out, H, W, y, T, K)
+    if K:   # the statistics do not depend on how many alternatives are asked for
+        logp, lse, ent, tl, ti = cuda_lib.lce_logprobs(Ht, Wt, dev(y), temperature=T, chunk_tokens=chunk, entropy=False)
+        assert ent is None and tl is None and ti is None
+        check_scores((logp, lse, None, None, None), H, W, y, T, 0)
+
+
+@pytest.mark.parametrize("N", [1, 40, 300])
+def test_logprobs_ties_go_to_the_lowest_index(cuda_lib, N):
+    """All logits equal, and logits of three values only: many ties inside and across tiles."""
+    torch = _torch()
+    V, d, K = 1500, 64, 37
+    y = torch.zeros(N, dtype=torch.int64, device="cuda")
+    out = cuda_lib.lce_logprobs(torch.ones(N, d, dtype=torch.bfloat16, device="cuda"),
+                                torch.zeros(V, d, dtype=torch.bfloat16, device="cuda"), y, top_k=K)
+    assert (out[4] == torch.arange(K, device="cuda")).all()
+    assert (out[2] - float(np.log(V))).abs().max() < 13 * 2.0 ** -15
+    W = np.zeros((V, d))
+    W[:, 0] = np.random.default_rng(1).integers(-1, 2, V)
+    H = np.zeros((N, d))
+    H[:, 0] = np.where(np.arange(N) % 2 == 0, 1.0, -1.0)   # the order turns round in every other row
+    Ht, Wt = heads(H, W)
+    check_scores(cuda_lib.lce_logprobs(Ht, Wt, y, top_k=K), H, W, y.cpu().numpy(), 1.0, K)
+
+
+@pytest.mark.parametrize("N", [2, 300])
+def test_logprobs_far_logits(cuda_lib, N):
+    """Spreads of hundreds of nats: probabilities underflow, entropy goes to zero, nothing overflows."""
+    _, H, W, y = make(N, 64, 3000, scale=8.0, peak=0.0)
+    H = H * 8
+    Ht, Wt = heads(H, W)
+    assert np.abs(H @ W.T).max() > 150
+    check_scores(cuda_lib.lce_logprobs(Ht, Wt, dev(y), top_k=12), H, W, y, 1.0, 12)
+
+
+@pytest.mark.parametrize("N", [4, 300])
+def test_logprobs_rows_with_nan_and_inf_leave_the_others_alone(cuda_lib, N):
+    torch = _torch()
+    _, H, W, y = make(N, 64, 2000)
+    Ht, Wt = heads(H, W)
+    clean = cuda_lib.lce_logprobs(Ht, Wt, dev(y), top_k=16)
+    Ht[1, 3] = float("nan")
+    Ht[2, 5] = float("inf")
+    logp, lse, ent, tl, ti = cuda_lib.lce_logprobs(Ht, Wt, dev(y), top_k=16)
+    rest = torch.tensor([i for i in range(N) if i not in (1, 2)], device="cuda")
+    for a, b in zip((logp, lse, ent, tl, ti), clean):
+        assert torch.equal(a[rest], b[rest])
+    assert torch.isnan(lse[1]) and torch.isnan(ent[1])
+    assert ((ti >= 0) & (ti < 2000)).all()
+
+
+def test_logprobs_label_out_of_range(cuda_lib):
+    torch = _torch()
+    _, H, W, y = make(50, 64, 300)
+    Ht, Wt = heads(H, W)
+    yt = dev(y)
+    yt[7], yt[9] = 300, -5
+    with pytest.raises(cuda_lib.LCEError) as err:
+        cuda_lib.lce_logprobs(Ht, Wt, yt, sync_check=True)
+    assert err.value.code == cuda_lib.LCE_ERR_LABEL_RANGE
+    out = cuda_lib.lce_logprobs(Ht, Wt, yt, top_k=4)
+    y[7] = y[9] = oracle.IGNORE_INDEX
+    check_scores(out, H, W, y, 1.0, 4)
+    assert torch.equal(out[0][7], torch.zeros((), device="cuda"))
+
+
+def test_logprobs_no_tokens(cuda_lib):
+    torch = _torch()
+    H, W = torch.zeros(0, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(9, 64, dtype=torch.bfloat16, device="cuda")
+    y = torch.zeros(0, dtype=torch.int64, device="cuda")
+    logp, lse, ent, tl, ti = cuda_lib.lce_logprobs(H, W, y, top_k=3)
+    assert logp.shape == lse.shape == ent.shape == (0,) and tl.shape == ti.shape == (0, 3)
+    dH, dW = cuda_lib.lce_logprobs_backward(H, W, y, lse, ent, logp, ent)
+    assert dH.shape == (0, 64) and not dW.any()
+    idx = torch.zeros(0, 4, dtype=torch.int64, device="cuda")
+    loss, row, dH, dW = cuda_lib.lce_distill_fwd_bwd(H, W, idx, idx.float())
+    assert loss.item() == 0 and row.shape == (0,) and not dW.any()
+
+
+def test_logprobs_logits_buffer_past_32_bits(cuda_lib):
+    """A chunk whose logits take 16384 x 151808 entries (more than 2^31) equals small chunks bit for bit."""
+    torch = _torch()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    H = (torch.randn(16384, 64, generator=g, device="cuda") * 16).round().clamp(-127, 127).div(16).bfloat16()
+    W = (torch.randn(151655, 64, generator=g, device="cuda") * 16).round().clamp(-127, 127).div(64).bfloat16()
+    y = torch.randint(0, 151655, (16384,), generator=g, device="cuda")
+    a = cuda_lib.lce_logprobs(H, W, y, top_k=3, chunk_tokens=16384)
+    b = cuda_lib.lce_logprobs(H, W, y, top_k=3, chunk_tokens=2048)
+    for x, z in zip(a, b):
+        assert torch.equal(x, z)
+
+
+# N, d, V, T, chunk
+GRAD_CASES = [
+    (1, 64, 37, 1.0, 0),
+    (3, 72, 2, 0.7, 0),
+    (129, 136, 4099, 1.0, 64),
+    (129, 8, 37, 1.0, 0),
+    (250, 264, 4099, 0.9, 0),
+    (300, 264, 1000, 2.0, 128),
+    (513, 256, 1000, 1.0, 200),
+]
+
+
+@pytest.mark.parametrize("N,d,V,T,chunk", GRAD_CASES)
+def test_logprobs_backward(cuda_lib, N, d, V, T, chunk):
+    torch = _torch()
+    rng, H, W, y = make(N, d, V, seed=V + N)
+    Ht, Wt = heads(H, W)
+    g1, g2 = rng.standard_normal(N).astype(np.float32) / N, rng.standard_normal(N).astype(np.float32) / N
+    kw = dict(temperature=T, chunk_tokens=chunk)
+    logp, lse, ent, _, _ = cuda_lib.lce_logprobs(Ht, Wt, dev(y), **kw)
+    dH, dW = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), lse, ent, dev(g1), dev(g2), sync_check=True, **kw)
+    check_grads(dH, dW, oracle.logprobs_backward_f64(H, W, y, g1, g2, temperature=T))
+    # one gradient at a time gives the same values
+    only_H, none = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), lse, ent, dev(g1), dev(g2), need_dW=False, **kw)
+    assert none is None and torch.equal(only_H, dH)
+    none, only_W = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), lse, ent, dev(g1), dev(g2), need_dH=False, **kw)
+    assert none is None and torch.equal(only_W, dW)
+    # without the entropy's share; added to a dW that is there
+    ref = oracle.logprobs_backward_f64(H, W, y, g1, None, temperature=T)
+    dH, dW = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), lse, None, dev(g1), **kw)
+    check_grads(dH, dW, ref)
+    base = torch.ones(V, d, device="cuda")
+    _, acc = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), lse, None, dev(g1), dW=base, accumulate_dW=True, **kw)
+    # the sum with 1 rounds to fp32 once per chunk
+    close(acc, 1.0 + np64(dW), 2.0 ** -23 * (1 + (N // chunk if chunk else 0)) * (1 + np.abs(np64(dW))) + 1e-7, "dW added")
+
+
+def teacher(rng, N, V, K, bf16=False):
+    """Top entries with every irregularity: short lists, no list, -inf values, an index twice."""
+    idx = np.stack([rng.permutation(V)[:K] if K <= V else rng.integers(0, V, K) for _ in range(N)]).astype(np.int64)
+    t = (3 * rng.standard_normal((N, K))).astype(np.float32)
+    if bf16:
+        t = np.round(t * 8) / 8
+    for i in range(N):
+        what = rng.integers(0, 8)
+        if what == 0:
+            idx[i, rng.integers(0, K):] = oracle.IGNORE_INDEX
+        elif what == 1:
+            idx[i] = oracle.IGNORE_INDEX
+        elif what == 2:
+            t[i, rng.random(K) < 0.5] = -np.inf
+        elif what == 3 and K > 1:
+            idx[i, K - 1] = idx[i, 0]
+            idx[i, K // 2] = idx[i, 0]
+    return idx, t
+
+
+# N, d, V, K, T, chunk, teacher's type
+DISTILL_CASES = [
+    (1, 8, 1, 1, 1.0, 0, "f32"),
+    (1, 64, 37, 5, 1.0, 0, "f32"),
+    (3, 72, 2, 3, 0.7, 0, "bf16"),      # more entries than words
+    (129, 136, 4099, 128, 1.0, 64, "f32"),
+    (129, 8, 37, 20, 2.0, 0, "bf16"),
+    (300, 264, 1001, 33, 3.0, 128, "f32"),
+    (513, 256, 1000, 1, 1.0, 200, "bf16"),
+    (40, 64, 30011, 64, 1.0, 0, "f32"),
+]
+
+
+@pytest.mark.parametrize("N,d,V,K,T,chunk,kind", DISTILL_CASES)
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_distill(cuda_lib, N, d, V, K, T, chunk, kind, renormalize):
+    torch = _torch()
+    rng, H, W, _ = make(N, d, V, seed=V + K)
+    idx, t = teacher(rng, N, V, K, kind == "bf16")
+    if not renormalize:
+        T, t = 1.0, t - 8
+    Ht, Wt, it = *heads(H, W), dev(idx)
+    tt = dev(t, torch.bfloat16 if kind == "bf16" else torch.float32)
+    kw = dict(temperature=T, renormalize=renormalize, chunk_tokens=chunk)
+    g = dev(np.array([1.5], np.float32))
+    loss, row, dH, dW = cuda_lib.lce_distill_fwd_bwd(Ht, Wt, it, tt, g, sync_check=True, **kw)
+    ref = oracle.distill_f64(H, W, idx, np64(tt), temperature=T, renormalize=renormalize, grad_loss=1.5)
+    # row_loss = T^2 sum q (log q - logp): |log q| errs like lse (exponentials and sums of the same kind)
+    lse = oracle.logprobs_f64(H, W, np.zeros(N, np.int64), temperature=T)["lse"]
+    mass = oracle.teacher_f64(idx, np64(tt), V, temperature=T, renormalize=renormalize)[0].sum(axis=1)
+    tol = T * T * (mass + 1e-3) * (4 * tol_lse(H, W, lse, T) + 2.0 ** -20 * (16 + np.abs(t[np.isfinite(t)]).max(initial=0)))
+    close(row, ref["row_loss"], tol, "row_loss")
+    close(loss, ref["loss"], tol.mean() * N / max(1, (mass > 0).sum()), "loss")
+    check_grads(dH, dW, ref)
+    assert not dH[dev(mass == 0)].any()
+    loss2, row2 = cuda_lib.lce_distill_forward(Ht, Wt, it, tt, **kw)
+    assert torch.equal(loss2, loss) and torch.equal(row2, row)
+    only_H = cuda_lib.lce_distill_fwd_bwd(Ht, Wt, it, tt, g, need_dW=False, **kw)
+    assert only_H[3] is None and torch.equal(only_H[2], dH)
+    only_W = cuda_lib.lce_distill_fwd_bwd(Ht, Wt, it, tt, g, need_dH=False, **kw)
+    assert only_W[2] is None and torch.equal(only_W[3], dW)
+
+
+def test_distill_sum_override_and_accumulation(cuda_lib):
+    torch = _torch()
+    rng, H, W, _ = make(200, 64, 500)
+    idx, t = teacher(rng, 200, 500, 6)
+    Ht, Wt, it, tt = *heads(H, W), dev(idx), dev(t)
+    ref = oracle.distill_f64(H, W, idx, t, reduction=oracle.SUM)
+    loss, _, dH, dW = cuda_lib.lce_distill_fwd_bwd(Ht, Wt, it, tt, reduction="sum")
+    assert abs(loss.item() - ref["loss"]) <= 1e-5 * abs(ref["loss"])
+    check_grads(dH, dW, ref)
+    ref = oracle.distill_f64(H, W, idx, t, n_valid_override=1000)
+    half = [cuda_lib.lce_distill_fwd_bwd(Ht[s], Wt, it[s], tt[s], n_valid_override=1000) for s in
+            (slice(0, 100), slice(100, 200))]
+    assert abs(sum(x[0].item() for x in half) - ref["loss"]) <= 1e-5 * abs(ref["loss"])
+    acc = half[0][3].clone()
+    cuda_lib.lce_distill_fwd_bwd(Ht[100:], Wt, it[100:], tt[100:], n_valid_override=1000, dW=acc, accumulate_dW=True)
+    check_grads(torch.cat([half[0][2], half[1][2]]), acc, ref)
+
+
+def test_distill_all_rows_empty_and_bad_index(cuda_lib):
+    torch = _torch()
+    rng, H, W, _ = make(70, 64, 500)
+    Ht, Wt = heads(H, W)
+    idx = torch.full((70, 5), -100, device="cuda")
+    t = torch.zeros(70, 5, device="cuda")
+    loss, row, dH, dW = cuda_lib.lce_distill_fwd_bwd(Ht, Wt, idx, t, sync_check=True)
+    assert loss.item() == 0 and not row.any() and not dH.any() and not dW.any()
+    idx[:, :2] = torch.tensor([3, 9], device="cuda")
+    want = cuda_lib.lce_distill_fwd_bwd(Ht, Wt, idx, t)
+    idx[5, 3], idx[6, 4] = 500, -7        # not kept, and told
+    with pytest.raises(cuda_lib.LCEError) as err:
+        cuda_lib.lce_distill_fwd_bwd(Ht, Wt, idx, t, sync_check=True)
+    assert err.value.code == cuda_lib.LCE_ERR_LABEL_RANGE
+    for a, b in zip(cuda_lib.lce_distill_fwd_bwd(Ht, Wt, idx, t), want):
+        assert torch.equal(a, b)
+
+
+def test_teacher_to_student(cuda_lib):
+    """The teacher's alternatives are the student's targets; a student equal to
+    its teacher, every word kept, has no loss and (to rounding) no gradient."""
+    torch = _torch()
+    rng, H, W, y = make(150, 64, 2000, seed=1)
+    _, H2, W2, _ = make(150, 128, 2000, seed=2)
+    teacher_H, teacher_W = heads(H, W)
+    student_H, student_W = heads(H2, W2)
+    _, _, _, tl, ti = cuda_lib.lce_logprobs(teacher_H, teacher_W, dev(y), top_k=24)
+    loss, row, dH, dW = cuda_lib.lce_distill_fwd_bwd(student_H, student_W, ti, tl, renormalize=False)
+    ref = oracle.distill_f64(H2, W2, ti.cpu().numpy(), np64(tl), renormalize=False)
+    assert abs(loss.item() - ref["loss"]) <= 1e-5 * abs(ref["loss"])
+    check_grads(dH, dW, ref)
+    small = teacher_W[:100]
+    _, _, _, tl, ti = cuda_lib.lce_logprobs(teacher_H, small, dev(np.zeros(150, np.int64)), top_k=100)
+    loss, row, dH, dW = cuda_lib.lce_distill_fwd_bwd(teacher_H, small, ti, tl, renormalize=False)
+    assert abs(loss.item()) < 2.0 ** -14
+    assert dH.float().abs().max().item() < 1e-5
+
+
+# --------------------------------------------------------------------------- as programs use them
+def test_autograd_modules(cuda_lib):
+    torch = _torch()
+    from chunked_lm_head_linear_gb300.autograd import FusedLinearDistillation, FusedLinearLogProbs
+    rng, H, W, y = make(200, 64, 700)
+    Ht, Wt = heads(H, W)
+    Ht.requires_grad_(True)
+    Wt.requires_grad_(True)
+    w = dev(rng.standard_normal(200).astype(np.float32))
+    logp, ent = FusedLinearLogProbs(temperature=0.8)(Ht, Wt, dev(y))
+    dH, dW = torch.autograd.grad((logp * w).sum() - 0.5 * ent.sum(), [Ht, Wt])
+    assert dH.dtype == dW.dtype == torch.bfloat16
+    ref = oracle.logprobs_backward_f64(H, W, y, np64(w), np.full(200, -0.5), temperature=0.8)
+    check_grads(dH, None, ref)
+    close(dW, ref["dW"], (U + 2.0 ** -10) * ref["dW_bulk"] + U * np.abs(ref["dW"]), "dW in bf16")
+    # outputs used alone; a frozen head
+    logp, ent = FusedLinearLogProbs()(Ht, Wt.detach(), dev(y))
+    check_grads(torch.autograd.grad(logp.sum(), Ht)[0], None,
+                oracle.logprobs_backward_f64(H, W, y, np.ones(200), None))
+    logp, ent = FusedLinearLogProbs()(Ht, Wt, dev(y))
+    check_grads(torch.autograd.grad(ent.sum(), Ht)[0], None,
+                oracle.logprobs_backward_f64(H, W, y, np.zeros(200), np.ones(200)))
+    idx, t = teacher(rng, 200, 700, 9)
+    kd = FusedLinearDistillation(temperature=2.0)
+    loss = kd(Ht, Wt, dev(idx), dev(t))
+    assert loss.shape == ()
+    dH, dW = torch.autograd.grad(3.0 * loss, [Ht, Wt], retain_graph=True)
+    ref = oracle.distill_f64(H, W, idx, t, temperature=2.0, grad_loss=3.0)
+    # scaled after its rounding: one rounding more for dH
+    close(dH, ref["dH"], (U + 2.0 ** -10) * ref["dH_bulk"] + 2.01 * U * np.abs(ref["dH"]) + 1e-30, "dH scaled")
+    with pytest.raises(RuntimeError, match="run the forward again"):
+        torch.autograd.grad(loss, [Ht, Wt])
+    with torch.no_grad():
+        assert torch.equal(kd(Ht, Wt, dev(idx), dev(t)), loss)
+
+
+@pytest.mark.parametrize("N", [8, 300])
+def test_streams_graphs_and_a_shared_workspace(cuda_lib, N):
+    """Calls on a side stream, captured once and replayed on new inputs; two captured
+    graphs that share a workspace, replayed one after the other."""
+    torch = _torch()
+    rng, H, W, y = make(N, 64, 3001)
+    _, H2, _, _ = make(N, 64, 3001, seed=9)
+    idx, t = teacher(rng, N, 3001, 7)
+    Ht, Wt = heads(H, W)
+    other, yt, it, tt = dev(H2, torch.bfloat16), dev(y), dev(idx), dev(t)
+    g1 = dev(rng.standard_normal(N).astype(np.float32))
+    need = max(cuda_lib.lce_logprobs_workspace_size(N, 64, 3001, 5), cuda_lib.workspace_size(1, N, 64, 3001),
+               cuda_lib.lce_distill_workspace_size(N, 64, 3001, 7, True))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def score(h):
+        out = cuda_lib.lce_logprobs(h, Wt, yt, top_k=5, workspace=ws)
+        return list(out) + list(cuda_lib.lce_logprobs_backward(h, Wt, yt, out[1], out[2], g1, g1, workspace=ws))
+
+    def kd(h):
+        return list(cuda_lib.lce_distill_fwd_bwd(h, Wt, it, tt, workspace=ws))
+
+    want = [[score(h), kd(h)] for h in (Ht, other)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = [score(Ht), kd(Ht)]
+    side.synchronize()
+    for a, b in zip(got[0] + got[1], want[0][0] + want[0][1]):
+        assert torch.equal(a, b)
+    x = Ht.clone()
+    graphs, outs = [], []
+    for f in (score, kd):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(f(x))
+        graphs.append(graph)
+    for k, h in ((1, other), (0, Ht), (1, other)):
+        x.copy_(h)
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs[0] + outs[1], want[k][0] + want[k][1]):
+            assert torch.equal(a, b)
+
+
+def test_two_streams_at_once(cuda_lib):
+    """Calls whose work overlaps on the GPU, each with its own workspace and the stream argument."""
+    torch = _torch()
+    rng, H, W, y = make(700, 256, 5000)
+    idx, t = teacher(rng, 700, 5000, 12)
+    Ht, Wt, yt, it, tt = *heads(H, W), dev(y), dev(idx), dev(t)
+    want = [cuda_lib.lce_logprobs(Ht, Wt, yt, top_k=9), cuda_lib.lce_logprobs(Ht[:5], Wt, yt[:5], top_k=9),
+            cuda_lib.lce_distill_fwd_bwd(Ht, Wt, it, tt)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(5):
+        got = [cuda_lib.lce_logprobs(Ht, Wt, yt, top_k=9, stream=streams[0]),
+               cuda_lib.lce_logprobs(Ht[:5], Wt, yt[:5], top_k=9, stream=streams[1]),
+               cuda_lib.lce_distill_fwd_bwd(Ht, Wt, it, tt, stream=streams[2])]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            for x, z in zip(a, b):
+                assert torch.equal(x, z)
+
+
+def test_caller_tensors_are_checked(cuda_lib):
+    torch = _torch()
+    _, H, W, y = make(20, 64, 300)
+    Ht, Wt, yt = *heads(H, W), dev(y)
+    f = torch.zeros(20, device="cuda")
+    idx = torch.zeros(20, 4, dtype=torch.int64, device="cuda")
+    t = torch.zeros(20, 4, device="cuda")
+    for call in (lambda: cuda_lib.lce_logprobs(Ht.float(), Wt, yt), lambda: cuda_lib.lce_logprobs(Ht.t(), Wt, yt),
+                 lambda: cuda_lib.lce_logprobs(Ht, Wt, yt.int()),
+                 lambda: cuda_lib.lce_logprobs_backward(Ht, Wt, yt, f[:5], f, f),
+                 lambda: cuda_lib.lce_logprobs_backward(Ht, Wt, yt, f, None, f, f),
+                 lambda: cuda_lib.lce_logprobs_backward(Ht, Wt, yt, f, f, f.double()),
+                 lambda: cuda_lib.lce_logprobs_backward(Ht, Wt, yt, f, f, f, need_dH=False, need_dW=False),
+                 lambda: cuda_lib.lce_logprobs_backward(Ht, Wt, yt, f, f, f, accumulate_dW=True),
+                 lambda: cuda_lib.lce_distill_forward(Ht, Wt, idx.int(), t),
+                 lambda: cuda_lib.lce_distill_forward(Ht, Wt, idx, t.half()),
+                 lambda: cuda_lib.lce_distill_forward(Ht, Wt, idx, t[:, :3]),
+                 lambda: cuda_lib.lce_distill_forward(Ht, Wt, idx[:, ::2], t[:, ::2]),
+                 lambda: cuda_lib.lce_distill_forward(Ht, Wt, idx, t, temperature=2.0, renormalize=False)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: cuda_lib.lce_logprobs(Ht, Wt, yt, top_k=301), lambda: cuda_lib.lce_logprobs(Ht, Wt, yt, top_k=-1),
+                 lambda: cuda_lib.lce_logprobs(Ht, Wt, yt, temperature=0.0)):
+        with pytest.raises(cuda_lib.LCEError) as err:
+            call()
+        assert err.value.code == cuda_lib.LCE_ERR_INVALID_ARG
+    with pytest.raises(cuda_lib.LCEError) as err:
+        cuda_lib.lce_logprobs(Ht, Wt, yt, top_k=3, workspace=torch.empty(1000, dtype=torch.uint8, device="cuda"))
+    assert err.value.code == cuda_lib.LCE_ERR_WORKSPACE
+    auto = cuda_lib.lce_logprobs(Ht, Wt, yt, top_k=3, chunk_tokens="auto")
+    for a, b in zip(auto, cuda_lib.lce_logprobs(Ht, Wt, yt, top_k=3)):
+        assert torch.equal(a, b)
