@@ -1058,15 +1058,22 @@ lce::TokParams tok_params(const Call& c, int64_t c0, int64_t rows, float tempera
 // TOK_STATS_Z) or gradient tile (bf16, TOK_GRAD) with row stride ldo.
 int tok_logits(const Call& c, int64_t c0, int64_t rows, int mode, void* out, int64_t ldo, const lce::TokParams& p) {
   CUtensorMap mA, mB, mC;
-  LCE_TRY(make_map(&mA, c.H + c0 * c.d, rows, c.d, c.d, lce::kBoxRowsK));
+  const double flops = 2.0 * static_cast<double>(rows) * static_cast<double>(c.V) * static_cast<double>(c.d);
   LCE_TRY(make_map(&mB, c.W, c.V, c.d, c.d, lce::kBoxRowsK));
+  if (rows <= lce::kFewRows && mode != lce::TOK_GRAD) {
+    LCE_TRY(make_map(&mA, c.H + c0 * c.d, rows, c.d, c.d, lce::few_rows_box(rows)));
+    return timed(c.s, K_LOGITS_STATS, flops, [&] {
+      return cuda_rc(lce::launch_rows_logits(mA, mB, mode == lce::TOK_STATS_Z, static_cast<float*>(out), ldo, c.V, c.d,
+                                             p, c.dev.num_sms, c.s));
+    });
+  }
+  LCE_TRY(make_map(&mA, c.H + c0 * c.d, rows, c.d, c.d, lce::kBoxRowsK));
   if (mode == lce::TOK_STATS_Z)
     LCE_TRY(make_map_t(&mC, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, out, rows, c.V, ldo, 32u, kStoreRows));
   else if (mode == lce::TOK_GRAD)
     LCE_TRY(make_map(&mC, out, rows, c.V, ldo, kStoreRows));
   else
     mC = mB;  // this epilogue stores nothing
-  const double flops = 2.0 * static_cast<double>(rows) * static_cast<double>(c.V) * static_cast<double>(c.d);
   return timed(c.s, mode == lce::TOK_GRAD ? K_LOGITS_GRAD : K_LOGITS_STATS, flops, [&] {
     return cuda_rc(lce::launch_tok_logits(mode, mA, mB, mC, rows, c.V, c.d, p, c.dev.num_sms, c.s));
   });

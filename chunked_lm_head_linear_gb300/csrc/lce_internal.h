@@ -280,6 +280,12 @@ struct DistillArgs {
 // map of the logits (TOK_STATS_Z) or the gradient tile (TOK_GRAD).
 cudaError_t launch_tok_logits(int mode, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, long long M,
                               long long N, long long K, const TokParams& ep, int num_sms, cudaStream_t s);
+// The same for at most kFewRows rows (ep.rows), by one pass over W (lce_tokens.cu); h: map of H with
+// boxes of few_rows_box(rows) rows, w: K-major map of W; store_z: the logits too, else the label's.
+constexpr int kFewRows = 64;
+inline uint32_t few_rows_box(long long rows) { return rows <= 32 ? 32u : 64u; }
+cudaError_t launch_rows_logits(const CUtensorMap& h, const CUtensorMap& w, int store_z, float* Z, long long ldz,
+                               long long V, long long d, const TokParams& ep, int num_sms, cudaStream_t s);
 cudaError_t launch_score(const TokScoreArgs& p, cudaStream_t s);
 // Clears the status block and cnt[0, ncnt), then counts the rows of idx [N, K] that keep an entry.
 cudaError_t launch_distill_count(const int64_t* idx, const void* t, int t_bf16, long long N, int K, int V,

@@ -23,6 +23,37 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFloor = -1.0e30f;  // stands in for -inf where it is multiplied by a zero probability
 
 // ----------------------------------------------------------------------------
+// Merging the triples
+// ----------------------------------------------------------------------------
+struct Mst {
+  float m, s, t;
+};
+
+// (m, s, t) of the union: both sides rescaled to the larger maximum M,
+// t' = f (t + s (m - M)/T). An empty side (s = 0) leaves the other as it is.
+__device__ __forceinline__ void merge_mst(Mst& a, const Mst& b, float inv_t) {
+  const float M = fmaxf(a.m, b.m);
+  const float k = inv_t * kLog2e;
+  const float da = a.m == M ? 0.f : a.m - M, db = b.m == M ? 0.f : b.m - M;
+  const float fa = exp2f(da * k), fb = exp2f(db * k);
+  a.t = fa * (a.t + a.s * fmaxf(da * inv_t, kFloor)) + fb * (b.t + b.s * fmaxf(db * inv_t, kFloor));
+  a.s = a.s * fa + b.s * fb;
+  a.m = M;
+}
+
+__device__ __forceinline__ Mst warp_merge_mst(Mst a, float inv_t) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    Mst b;
+    b.m = __shfl_xor_sync(0xffffffffu, a.m, off);
+    b.s = __shfl_xor_sync(0xffffffffu, a.s, off);
+    b.t = __shfl_xor_sync(0xffffffffu, a.t, off);
+    merge_mst(a, b, inv_t);
+  }
+  return a;
+}
+
+// ----------------------------------------------------------------------------
 // Tile epilogue: an epilogue warp owns 32 rows x 128 columns, one thread a row.
 //   TOK_STATS    the triple of each (row, half tile) and the label's logit
 //   TOK_STATS_Z  the triple, and the fp32 logits themselves into the chunk's
@@ -227,34 +258,267 @@ cudaError_t launch_tok_mode(const CUtensorMap& a, const CUtensorMap& b, const CU
 }
 
 // ----------------------------------------------------------------------------
-// Merging the triples
+// Few rows (decoding): the logits are one pass over W, bound by reading it, so
+// the operands change sides. A tile is 128 vocabulary rows of W (the MMA's M,
+// each read once, by one CTA) by all rows of H (its N, 32 or 64, zero-filled
+// by TMA beyond the last), accumulated over d in TMEM; the ring of W blocks
+// keeps 128 to 160 KB a SM on their way from HBM. The pair kernel's 256-row
+// tiles would multiply at least 256 rows and leave fewer bytes in flight.
+//   warp 0      TMA producer, warp 1 MMA issuer, warp 2 TMEM
+//   warps 4-7   epilogue: TMEM lanes (vocabulary) into shared memory as
+//               [row][128], then a warp per row: 4 columns a lane, the triple
+//               by shuffles, the logits to memory in 512-byte runs
+// The triples and logits are laid out as the pair kernel's, and the kernels
+// behind do not know which ran.
 // ----------------------------------------------------------------------------
-struct Mst {
-  float m, s, t;
+template <int NT>
+struct RowsCfg {
+  static constexpr int kABytes = 128 * BK * 2;
+  static constexpr int kBBytes = NT * BK * 2;
+  static constexpr int kStages = NT <= 32 ? 10 : 8;
+  static constexpr int kOut = kStages * (kABytes + kBBytes);
+  static constexpr int kBars = kOut + NT * 128 * 4;
+  static constexpr int kNumBars = 2 * kStages + 4 + 1;
+  static constexpr int kMisc = kBars + kNumBars * 8;
+  static constexpr int kTotal = kMisc + 16;
+  static constexpr int kDynamicBytes = kTotal + 1024;
+  static constexpr int kTmemCols = 2 * NT;
+  static_assert(kDynamicBytes <= 232448, "shared memory budget (few-rows kernel)");
 };
 
-// (m, s, t) of the union: both sides rescaled to the larger maximum M,
-// t' = f (t + s (m - M)/T). An empty side (s = 0) leaves the other as it is.
-__device__ __forceinline__ void merge_mst(Mst& a, const Mst& b, float inv_t) {
-  const float M = fmaxf(a.m, b.m);
-  const float k = inv_t * kLog2e;
-  const float da = a.m == M ? 0.f : a.m - M, db = b.m == M ? 0.f : b.m - M;
-  const float fa = exp2f(da * k), fb = exp2f(db * k);
-  a.t = fa * (a.t + a.s * fmaxf(da * inv_t, kFloor)) + fb * (b.t + b.s * fmaxf(db * inv_t, kFloor));
-  a.s = a.s * fa + b.s * fb;
-  a.m = M;
+struct RowsParams {
+  CUtensorMap w, h;
+  int tiles, k_blocks;
+  int store_z;
+  long long ldz;
+  float* Z;
+  TokParams ep;
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int lane) {
+  int ok = 0;
+  if (lane == 0) ok = mbar_wait(bar, parity, abort) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
-__device__ __forceinline__ Mst warp_merge_mst(Mst a, float inv_t) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    Mst b;
-    b.m = __shfl_xor_sync(0xffffffffu, a.m, off);
-    b.s = __shfl_xor_sync(0xffffffffu, a.s, off);
-    b.t = __shfl_xor_sync(0xffffffffu, a.t, off);
-    merge_mst(a, b, inv_t);
+// Barrier of the four epilogue warps: true if it is true in every thread.
+__device__ __forceinline__ bool epilogue_all(bool ok) {
+  int all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.s32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "selp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(ok ? 1 : 0)
+      : "memory");
+  return all != 0;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(NUM_THREADS, 1) k_rows_logits(const __grid_constant__ RowsParams p) {
+  using Cfg = RowsCfg<NT>;
+  constexpr int S = Cfg::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + S * Cfg::kABytes;
+  float* out = reinterpret_cast<float*>(smem + Cfg::kOut);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::kBars);
+  uint64_t* empty = full + S;
+  uint64_t* tfull = full + 2 * S;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Cfg::kMisc);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + Cfg::kMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], EPI_WARPS);
+    }
+    mbar_init(drain, 1);
+    *abort = 0;
+    fence_mbarrier_init();
   }
-  return a;
+  if (warp == 2) {
+    tmem_alloc(tmem_holder, Cfg::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_holder;
+  grid_dep_wait();  // everything above is the CTA's own; below, memory of earlier kernels
+  grid_dep_launch();
+
+  if (warp == 0 && lane == 0) {
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, armed_parity = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
+      for (int kb = 0; kb < p.k_blocks; ++kb) {
+        if (!mbar_wait(&empty[stage], phase ^ 1u, abort)) {
+          report_timeout(abort, p.ep.flags);
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(&full[stage], Cfg::kABytes + Cfg::kBBytes);
+        tma_load_2d(sA + stage * Cfg::kABytes, &p.w, &full[stage], kb * BK, t * 128);
+        tma_load_2d(sB + stage * Cfg::kBBytes, &p.h, &full[stage], kb * BK, 0);
+        armed |= 1u << stage;
+        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok || *abort) {  // leaving early: the copies under way land before the block ends
+      for (int i = 0; i < S; ++i)
+        if (armed & (1u << i)) mbar_wait_drain(&full[i], (armed_parity >> i) & 1u, 100000000ull);
+    }
+  } else if (warp == 1 && lane == 0) {
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true, issued = false;
+    constexpr uint32_t idesc = idesc_bf16_f32(128, NT, false, false);
+    for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
+      if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, abort)) {
+        report_timeout(abort, p.ep.flags);
+        break;
+      }
+      tc_fence_after_sync();
+      const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * NT);
+      for (int kb = 0; kb < p.k_blocks; ++kb) {
+        if (!mbar_wait(&full[stage], phase, abort)) {
+          report_timeout(abort, p.ep.flags);
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t a_addr = smem_u32(sA + stage * Cfg::kABytes);
+        const uint32_t b_addr = smem_u32(sB + stage * Cfg::kBBytes);
+#pragma unroll
+        for (int k = 0; k < BK / 16; ++k)
+          umma_bf16(d_tmem, desc_k_major(a_addr, k), desc_k_major(b_addr, k), idesc, (kb | k) != 0 ? 1u : 0u);
+        issued = true;
+        umma_commit(&empty[stage]);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      umma_commit(&tfull[acc]);
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    if (*abort && issued) {
+      umma_commit(drain);
+      mbar_wait_drain(drain, 0, 100000000ull);
+    }
+  } else if (warp >= EPI_WARP0) {
+    const int q = warp & 3;
+    const TokParams& e = p.ep;
+    const float k = e.inv_t * kLog2e;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int t = blockIdx.x; t < p.tiles; t += gridDim.x) {
+      // The four warps agree on whether the tile came (a wait that ran out in one ends the loop of
+      // all, so that none is left at the barrier below); everyone has read the tile before by then.
+      const bool came = warp_wait(&tfull[acc], acc_phase, abort, lane);
+      if (!came && lane == 0) report_timeout(abort, e.flags);
+      if (!epilogue_all(came)) break;
+      tc_fence_after_sync();
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * NT);
+#pragma unroll
+      for (int n0 = 0; n0 < NT; n0 += 32) {
+        if (n0 >= e.rows) break;
+        float v[32];
+        tmem_ld_32x32b_x32(taddr + n0, v);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) out[(n0 + c) * 128 + q * 32 + lane] = v[c];
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[acc]);
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");  // the tile is in shared memory
+      const int col = t * 128 + lane * 4;
+      for (int n = q; n < e.rows; n += 4) {
+        const float4 z4 = *reinterpret_cast<const float4*>(out + n * 128 + lane * 4);
+        if (p.store_z) {
+          if (in_bounds(col + 3, p.ldz, e.flags))
+            *reinterpret_cast<float4*>(p.Z + static_cast<long long>(n) * p.ldz + col) = z4;
+        } else {
+          const long long y = e.y[n];
+          const long long c = y - col;
+          if (c >= 0 && c < 4 && y < e.V && y != e.ignore_index)
+            e.ztgt[n] = c == 0 ? z4.x : c == 1 ? z4.y : c == 2 ? z4.z : z4.w;
+        }
+        float v[4] = {z4.x, z4.y, z4.z, z4.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (col + c >= e.V) v[c] = -INFINITY;
+        float m = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        const float mb = m == -INFINITY ? 0.f : m;
+        float s = 0.f, tt = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float dz = v[c] - mb;
+          const float x = ex2_approx(dz * k);
+          s += x;
+          tt = fmaf(x, fmaxf(dz, kFloor), tt);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+          s += __shfl_xor_sync(0xffffffffu, s, off);
+          tt += __shfl_xor_sync(0xffffffffu, tt, off);
+        }
+        if (lane == 0 && in_bounds(t, e.nparts, e.flags))
+          e.partials[static_cast<long long>(n) * e.nparts + t] = make_float4(m, s, tt * e.inv_t, 0.f);
+      }
+    }
+  }
+  tc_fence_before_sync();
+  __syncwarp();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 2) tmem_dealloc(tmem_base, Cfg::kTmemCols);
+}
+
+template <int NT>
+cudaError_t launch_rows_nt(const CUtensorMap& h, const CUtensorMap& w, int store_z, float* Z, long long ldz,
+                           long long V, long long d, const TokParams& ep, int num_sms, cudaStream_t s) {
+  RowsParams p;
+  p.w = w;
+  p.h = h;
+  p.tiles = static_cast<int>((V + 127) / 128);
+  p.k_blocks = static_cast<int>((d + BK - 1) / BK);
+  p.store_z = store_z;
+  p.ldz = ldz;
+  p.Z = Z;
+  p.ep = ep;
+  const int grid = p.tiles < num_sms ? p.tiles : num_sms;
+  auto kern = k_rows_logits<NT>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg<NT>::kDynamicBytes);
+  if (e != cudaSuccess) return e;
+  return launch_k(kern, grid, NUM_THREADS, RowsCfg<NT>::kDynamicBytes, s, p);
 }
 
 // ----------------------------------------------------------------------------
@@ -275,24 +539,36 @@ __device__ __forceinline__ float key_value(Key k) {
 }
 __device__ __forceinline__ uint32_t key_index(Key k) { return ~static_cast<uint32_t>(k); }
 
+// Descending order of 32 keys, one per lane (bitonic sort).
+__device__ __forceinline__ Key sort32(Key k, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2) {
+#pragma unroll
+    for (int stride = size / 2; stride > 0; stride /= 2) {
+      const Key o = __shfl_xor_sync(0xffffffffu, k, stride);
+      const bool low = (lane & stride) == 0, desc = (lane & size) == 0 || size == 32;
+      k = (low == desc) == (o > k) ? o : k;
+    }
+  }
+  return k;
+}
+
 template <int KPL>
 struct TopList {
   Key slot[KPL];
-  Key kth;  // key of slot K - 1: candidates must exceed it
+  Key kth;  // candidates must exceed it: the key of slot K - 1, or a lower bound of it given at the start
 
-  __device__ __forceinline__ void clear() {
+  __device__ __forceinline__ void clear(Key floor = 0) {
 #pragma unroll
     for (int j = 0; j < KPL; ++j) slot[j] = 0;
-    kth = 0;
+    kth = floor;
   }
   __device__ __forceinline__ Key at(int i) const {  // slot i (warp-uniform), in every lane
     Key k = 0;
 #pragma unroll
-    for (int j = 0; j < KPL; ++j) {
-      const Key v = __shfl_sync(0xffffffffu, slot[j], i & 31);
-      if (j == (i >> 5)) k = v;
-    }
-    return k;
+    for (int j = 0; j < KPL; ++j)
+      if (j == (i >> 5)) k = slot[j];
+    return __shfl_sync(0xffffffffu, k, i & 31);
   }
   __device__ __forceinline__ void insert(Key key, int lane) {
     int pos = 0;
@@ -302,60 +578,139 @@ struct TopList {
 #pragma unroll
     for (int j = 0; j < KPL; ++j) {
       const Key up = __shfl_up_sync(0xffffffffu, slot[j], 1);
-      const Key last = __shfl_sync(0xffffffffu, slot[j], 31);
+      const Key last = KPL > 1 ? __shfl_sync(0xffffffffu, slot[j], 31) : 0;
       const int me = 32 * j + lane;
       const Key moved = lane == 0 ? carry : up;
       slot[j] = me < pos ? slot[j] : (me == pos ? key : moved);
       carry = last;
     }
   }
-  // One candidate per lane (0: none), inserted while they exceed the K-th key.
+  // slot is bitonic (falls, then rises): into descending order.
+  __device__ __forceinline__ void bitonic(int lane) {
+#pragma unroll
+    for (int stride = KPL / 2; stride > 0; stride /= 2) {
+#pragma unroll
+      for (int j = 0; j < KPL; ++j)
+        if ((j & stride) == 0 && slot[j + stride] > slot[j]) {
+          const Key o = slot[j];
+          slot[j] = slot[j + stride];
+          slot[j + stride] = o;
+        }
+    }
+#pragma unroll
+    for (int stride = 16; stride > 0; stride /= 2) {
+#pragma unroll
+      for (int j = 0; j < KPL; ++j) {
+        const Key o = __shfl_xor_sync(0xffffffffu, slot[j], stride);
+        slot[j] = ((lane & stride) == 0) == (o > slot[j]) ? o : slot[j];
+      }
+    }
+  }
+  __device__ __forceinline__ void raise(int K) {
+    const Key k = at(K - 1);
+    kth = k > kth ? k : kth;
+  }
+  // One candidate per lane (0: none). Up to three that exceed the K-th key are
+  // inserted one by one; more are sorted and merged at once (of two falling
+  // lists, the larger of each entry of one and its mirror image in the other
+  // are the largest of both, and bitonic).
   __device__ __forceinline__ void offer(Key cand, int K, int lane) {
     uint32_t mask = __ballot_sync(0xffffffffu, cand > kth);
+    if (mask == 0) return;
+    if (__popc(mask) > 3) {
+      cand = sort32(cand > kth ? cand : 0, lane);
+      cand = __shfl_sync(0xffffffffu, cand, 31 - lane);
+      slot[KPL - 1] = cand > slot[KPL - 1] ? cand : slot[KPL - 1];
+      bitonic(lane);
+      raise(K);
+      return;
+    }
     while (mask) {
       const int src = __ffs(mask) - 1;
       insert(__shfl_sync(0xffffffffu, cand, src), lane);
-      kth = at(K - 1);
+      raise(K);
       if (lane == src) cand = 0;
       mask = __ballot_sync(0xffffffffu, cand > kth);
     }
   }
+  // The lists of a block's warps into warp 0's (and back to all through buf).
+  template <int WARPS>
+  __device__ __forceinline__ void gather(Key (*buf)[32 * KPL], int K, int warp, int lane) {
+    if constexpr (WARPS > 1) {
+#pragma unroll
+      for (int j = 0; j < KPL; ++j) buf[warp][32 * j + lane] = slot[j];
+      __syncthreads();
+#pragma unroll
+      for (int step = 1; step < WARPS; step *= 2) {
+        if (warp % (2 * step) == 0) {
+#pragma unroll
+          for (int j = 0; j < KPL; ++j) {
+            const Key o = buf[warp + step][32 * KPL - 1 - (32 * j + lane)];
+            slot[j] = o > slot[j] ? o : slot[j];
+          }
+          bitonic(lane);
+#pragma unroll
+          for (int j = 0; j < KPL; ++j) buf[warp][32 * j + lane] = slot[j];
+        }
+        __syncthreads();
+      }
+#pragma unroll
+      for (int j = 0; j < KPL; ++j) slot[j] = buf[0][32 * j + lane];
+      raise(K);
+    }
+  }
 };
 
-// One warp per row: the row's triples merged in a fixed order into lse, logp
-// and entropy, and the top K alternatives. The K largest logits (ties to the
-// lower index) lie in the K half tiles with the largest maxima (ties to the
-// lower tile): before a half tile outside them come K others, each with an
-// element before all of its own. So only K x 128 of the row's logits are read
-// again.
-template <int KPL>
+// The row's triples merged in a fixed order into lse, logp and entropy, and the
+// top K alternatives. The K largest logits (ties to the lower index) lie in the
+// K half tiles with the largest maxima (ties to the lower tile): before a half
+// tile outside them come K others, each with an element before all of its own.
+// So only K x 128 of the row's logits are read again, and of those only the
+// ones that reach the K-th largest maximum are candidates.
+// WARPS = 1: a warp per row, eight rows a block (many rows: 8192 of them fill
+// the GPU). WARPS = 8: a block per row (few rows: the row's own latency counts).
+template <int KPL, int WARPS>
 __global__ void __launch_bounds__(256) k_score(const TokScoreArgs p) {
   grid_dep_wait();
   grid_dep_launch();
-  const int r = static_cast<int>((blockIdx.x * static_cast<unsigned>(blockDim.x) + threadIdx.x) >> 5);
+  __shared__ Key s_list[WARPS > 1 ? WARPS : 1][32 * KPL];
+  __shared__ Mst s_mst[WARPS > 1 ? WARPS : 1];
   const int lane = threadIdx.x & 31;
-  if (r >= p.rows) return;
+  const int warp = WARPS > 1 ? static_cast<int>(threadIdx.x >> 5) : 0;
+  const int r = WARPS > 1 ? static_cast<int>(blockIdx.x)
+                          : static_cast<int>((blockIdx.x * static_cast<unsigned>(blockDim.x) + threadIdx.x) >> 5);
+  if (r >= p.rows) return;  // a whole warp (WARPS = 1) or nobody
   const float4* pr = p.partials + static_cast<long long>(r) * p.nparts;
   const int tiles = (p.V + EPI_COLS - 1) / EPI_COLS;  // half tiles that hold vocabulary columns
   const float* z = p.Z + static_cast<long long>(r) * p.ldz;
   Mst acc{-INFINITY, 0.f, 0.f};
   TopList<KPL> top;
   top.clear();
-  for (int t0 = 0; t0 < tiles; t0 += 32) {
-    const int t = t0 + lane;
-    Mst q{-INFINITY, 0.f, 0.f};
-    if (t < tiles) {
-      const float4 v = pr[t];
-      q.m = v.x;
-      q.s = v.y;
-      q.t = v.z;
+  constexpr int kBatch = 4;  // loads in flight before their merges
+  for (int t0 = warp * 32; t0 < tiles; t0 += 32 * WARPS * kBatch) {
+    float4 v[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int t = t0 + b * 32 * WARPS + lane;
+      v[b] = t < tiles ? pr[t] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
     }
-    merge_mst(acc, q, p.inv_t);
-    if (p.K > 0) top.offer(t < tiles ? make_key(q.m, static_cast<uint32_t>(t)) : 0, p.K, lane);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int t = t0 + b * 32 * WARPS + lane;
+      merge_mst(acc, Mst{v[b].x, v[b].y, v[b].z}, p.inv_t);
+      if (p.K > 0) top.offer(t < tiles ? make_key(v[b].x, static_cast<uint32_t>(t)) : 0, p.K, lane);
+    }
   }
   acc = warp_merge_mst(acc, p.inv_t);
+  if (WARPS > 1) {
+    if (lane == 0) s_mst[warp] = acc;
+    __syncthreads();
+    acc = s_mst[0];
+#pragma unroll
+    for (int i = 1; i < WARPS; ++i) merge_mst(acc, s_mst[i], p.inv_t);
+  }
   const float logs = logf(acc.s);
-  if (lane == 0) {
+  if (lane == 0 && warp == 0) {
     p.lse[r] = fmaf(acc.m, p.inv_t, logs);
     if (p.entropy != nullptr) p.entropy[r] = logs - acc.t / acc.s;
     const long long y = p.y[r];
@@ -365,10 +720,13 @@ __global__ void __launch_bounds__(256) k_score(const TokScoreArgs p) {
     p.logp[r] = lp;
   }
   if (p.K == 0) return;
+  top.template gather<WARPS>(s_list, p.K, warp, lane);
   TopList<KPL> best;
-  best.clear();
   const int ntop = tiles < p.K ? tiles : p.K;
-  for (int i = 0; i < ntop; ++i) {
+  // with K half tiles, the K-th largest of their maxima bounds the K-th logit from below
+  best.clear(ntop == p.K ? (top.at(p.K - 1) & 0xffffffff00000000ull) : 0);
+  if (WARPS > 1) __syncthreads();  // s_list is written again below
+  for (int i = warp; i < ntop; i += WARPS) {
     const int tile = static_cast<int>(key_index(top.at(i)));
     const int c = tile * EPI_COLS + lane * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -378,13 +736,16 @@ __global__ void __launch_bounds__(256) k_score(const TokScoreArgs p) {
     best.offer(c + 2 < p.V ? make_key(v.z, c + 2) : 0, p.K, lane);
     best.offer(c + 3 < p.V ? make_key(v.w, c + 3) : 0, p.K, lane);
   }
+  best.template gather<WARPS>(s_list, p.K, warp, lane);
+  if (warp != 0) return;
 #pragma unroll
   for (int j = 0; j < KPL; ++j) {
     const int i = 32 * j + lane;
     if (i < p.K) {
       const long long at = static_cast<long long>(r) * p.K + i;
       p.top_logp[at] = (key_value(best.slot[j]) - acc.m) * p.inv_t - logs;
-      p.top_idx[at] = static_cast<int64_t>(key_index(best.slot[j]));
+      const uint32_t v = key_index(best.slot[j]);  // past V only if a row of NaN left the list short
+      p.top_idx[at] = v < static_cast<uint32_t>(p.V) ? v : static_cast<uint32_t>(p.V - 1);
     }
   }
 }
@@ -599,11 +960,24 @@ cudaError_t launch_tok_logits(int mode, const CUtensorMap& a, const CUtensorMap&
   }
 }
 
+cudaError_t launch_rows_logits(const CUtensorMap& h, const CUtensorMap& w, int store_z, float* Z, long long ldz,
+                               long long V, long long d, const TokParams& ep, int num_sms, cudaStream_t s) {
+  if (ep.rows <= 32) return launch_rows_nt<32>(h, w, store_z, Z, ldz, V, d, ep, num_sms, s);
+  return launch_rows_nt<64>(h, w, store_z, Z, ldz, V, d, ep, num_sms, s);
+}
+
+// Up to this many rows take a block each in k_score, more a warp each.
+constexpr int kScoreBlockRows = 1024;
+
 cudaError_t launch_score(const TokScoreArgs& p, cudaStream_t s) {
   if (p.rows <= 0) return cudaSuccess;
+  if (p.rows <= kScoreBlockRows) {
+    if (p.K <= 32) return launch_k(k_score<1, 8>, p.rows, 256, 0, s, p);
+    return launch_k(k_score<kMaxTop / 32, 8>, p.rows, 256, 0, s, p);
+  }
   const int grid = (p.rows + 7) / 8;
-  if (p.K <= 32) return launch_k(k_score<1>, grid, 256, 0, s, p);
-  return launch_k(k_score<kMaxTop / 32>, grid, 256, 0, s, p);
+  if (p.K <= 32) return launch_k(k_score<1, 1>, grid, 256, 0, s, p);
+  return launch_k(k_score<kMaxTop / 32, 1>, grid, 256, 0, s, p);
 }
 
 cudaError_t launch_distill_count(const int64_t* idx, const void* t, int t_bf16, long long N, int K, int V,
