@@ -82,9 +82,12 @@ class FusedLinearCrossEntropy(torch.nn.Module):
 
 class _LogProbs(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, H, W, y, temperature, opts):
-        logp, lse, entropy, _, _ = lce.lce_logprobs(H, W, y, temperature=temperature, **opts)
-        ctx.save_for_backward(H, W, y, lse, entropy)
+    def forward(ctx, H, W, y, temperature, keep, opts):
+        logits = None
+        if keep and any(ctx.needs_input_grad[:2]):
+            logits = torch.empty((H.shape[0], lce.lce_logits_stride(W.shape[0])), dtype=torch.float32, device=H.device)
+        logp, lse, entropy, _, _ = lce.lce_logprobs(H, W, y, temperature=temperature, logits=logits, **opts)
+        ctx.save_for_backward(H, W, y, lse, entropy, logits)
         ctx.temperature, ctx.opts = temperature, opts
         ctx.set_materialize_grads(False)   # an output nobody used comes back as None
         return logp, entropy
@@ -92,26 +95,36 @@ class _LogProbs(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, g_logp, g_entropy):
-        H, W, y, lse, entropy = ctx.saved_tensors
+        H, W, y, lse, entropy, logits = ctx.saved_tensors
         g_logp = torch.zeros_like(lse) if g_logp is None else g_logp.contiguous()
         g_entropy = None if g_entropy is None else g_entropy.contiguous()
         dH, dW = lce.lce_logprobs_backward(H, W, y, lse, entropy, g_logp, g_entropy, temperature=ctx.temperature,
-                                           need_dH=ctx.needs_input_grad[0], need_dW=ctx.needs_input_grad[1],
-                                           **ctx.opts)
-        return dH, dW, None, None, None
+                                           logits=logits, dW_dtype=W.dtype, need_dH=ctx.needs_input_grad[0],
+                                           need_dW=ctx.needs_input_grad[1], **ctx.opts)
+        return dH, dW, None, None, None, None
 
 
 class FusedLinearLogProbs(torch.nn.Module):
     """logp [N] of the tokens y and entropy [N] of softmax(H W^T / temperature),
-    both differentiable in H and W (fp32; logp is 0 where y is ignore_index)."""
+    both differentiable in H and W (fp32; logp is 0 where y is ignore_index).
 
-    def __init__(self, temperature: float = 1.0, ignore_index: int = -100, chunk_tokens=0):
+    ``recompute``: True: the backward recomputes the logits (8 N V d flops in
+    all); False: the forward keeps them for it (4 N V bytes, 6 N V d flops);
+    None: they are kept when the batch is one chunk (of chunk_tokens, or 4096),
+    so that the memory held stays O(chunk V)."""
+
+    def __init__(self, temperature: float = 1.0, ignore_index: int = -100, chunk_tokens=0, recompute=None):
         super().__init__()
         self.temperature = temperature
+        self.recompute = recompute
         self.opts = dict(ignore_index=ignore_index, chunk_tokens=chunk_tokens)
 
     def forward(self, H, W, y):
-        return _LogProbs.apply(H, W, y, self.temperature, self.opts)
+        keep = not self.recompute
+        if self.recompute is None:
+            chunk = self.opts["chunk_tokens"]
+            keep = chunk != "auto" and H.shape[0] <= (chunk or 4096)
+        return _LogProbs.apply(H, W, y, self.temperature, keep, self.opts)
 
 
 class _Distillation(torch.autograd.Function):
@@ -121,7 +134,8 @@ class _Distillation(torch.autograd.Function):
         if not (need_dH or need_dW):
             loss, _ = lce.lce_distill_forward(H, W, idx, t, **kw)
             return loss.reshape(())
-        loss, _, dH, dW = lce.lce_distill_fwd_bwd(H, W, idx, t, need_dH=need_dH, need_dW=need_dW, **kw)
+        loss, _, dH, dW = lce.lce_distill_fwd_bwd(H, W, idx, t, dW_dtype=W.dtype, need_dH=need_dH, need_dW=need_dW,
+                                                  **kw)
         ctx.grads = dH, dW
         return loss.reshape(())
 
@@ -133,14 +147,16 @@ class _Distillation(torch.autograd.Function):
                                "of this graph; run the forward again")
         dH, dW = ctx.grads
         ctx.grads = None
-        lce.lce_scale_grads(dH, dW, g.reshape(1).to(torch.float32).contiguous())
+        lce.lce_scale_grads_bfloat(dH, dW, g.reshape(1).to(torch.float32).contiguous())
         return dH, dW, None, None, None
 
 
 class FusedLinearDistillation(torch.nn.Module):
     """KL divergence of softmax(H W^T / temperature) from a teacher's top tokens
     idx [N, K] with values t [N, K], times temperature^2, mean over the rows that
-    keep an entry (lce.lce_distill_fwd_bwd)."""
+    keep an entry (lce.lce_distill_fwd_bwd). Its gradients are computed in the
+    forward pass in bf16 and scaled by the upstream gradient in the backward,
+    where they are rounded once more unless it is a power of two."""
 
     def __init__(self, temperature: float = 1.0, renormalize: bool = True, ignore_index: int = -100,
                  reduction: str = "mean", chunk_tokens=0):

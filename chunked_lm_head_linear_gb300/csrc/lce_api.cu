@@ -381,11 +381,13 @@ int forward_chunk(const Call& c, int64_t c0, int64_t rows, float* lse, float* lo
 struct BwdPart {
   int64_t v_begin = 0, v_end = -1;
   bool with_dh = true;
+  bool dW_bf16 = false;          // dW is bf16 and stored once: bf16(dW_add + this chunk's dW)
+  const float* dW_add = nullptr;  // fp32 sum of earlier chunks, or none
 };
 
 // dH_c = (g/n) [rowscale] (G W) and dW (+)= (g/n) G^T B, with G [rows, V] in
 // the chunk's tile buffer and B = H_c or Ht: one launch for both GEMMs.
-int dh_dw(const Call& c, int64_t c0, int64_t rows, const float* rowscale, const uint16_t* B, void* dH, float* dW,
+int dh_dw(const Call& c, int64_t c0, int64_t rows, const float* rowscale, const uint16_t* B, void* dH, void* dW,
           bool accumulate, bool dH_f32 = false, const BwdPart& part = BwdPart()) {
   const uint16_t* P = reinterpret_cast<const uint16_t*>(c.ws + c.L.P);
   CUtensorMap mG, mW, mdH, mGt, mB, mdW;
@@ -402,6 +404,8 @@ int dh_dw(const Call& c, int64_t c0, int64_t rows, const float* rowscale, const 
   LCE_TRY(make_map(&mB, B, rows, c.d, c.d, lce::kBoxRowsMN));          // dW: B, N-major
   if (!dW)
     mdW = mW;
+  else if (part.dW_bf16)
+    LCE_TRY(make_map(&mdW, dW, c.V, c.d, c.d, kStoreRows));
   else
     LCE_TRY(make_map_t(&mdW, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, dW, c.V, c.d, c.d, 32u, kStoreRows));
   lce::DhParams dp;
@@ -418,8 +422,10 @@ int dh_dw(const Call& c, int64_t c0, int64_t rows, const float* rowscale, const 
   lce::DwParams wp;
   wp.rows = static_cast<int>(c.V);
   wp.N = static_cast<int>(c.d);
-  wp.out = dW;
+  wp.out = nullptr;  // written through the store map
   wp.ld = c.d;
+  wp.bf16_out = part.dW_bf16 ? 1 : 0;
+  wp.add = part.dW_add;
   wp.accumulate = accumulate ? 1 : 0;
   wp.st = c.st;
   const int64_t v_end = part.v_end < 0 ? c.V : part.v_end;
@@ -987,10 +993,11 @@ struct TokLayout {
   Layout base;         // status, ztgt, partials, P and the dH parts of the call record
   int64_t ldz = 0;     // row stride of the logits buffer
   size_t Z = 0;
+  size_t dW = 0;       // fp32 sum of dW over the chunks before the last (dW_bf16 and several chunks)
   size_t total = 0;
 };
 
-TokLayout tok_layout(int64_t N, int64_t d, int64_t V, bool with_z, bool with_grad, const lce_opts* o) {
+TokLayout tok_layout(int64_t N, int64_t d, int64_t V, bool with_z, bool with_grad, bool dW_bf16, const lce_opts* o) {
   TokLayout T;
   Layout& L = T.base;
   L.C = chunk_of(N, o);
@@ -1012,6 +1019,7 @@ TokLayout tok_layout(int64_t N, int64_t d, int64_t V, bool with_z, bool with_gra
   if (with_grad) {
     L.P = take(2 * C * static_cast<size_t>(L.ldp));
     take_dh_parts(L, d, V, take);
+    if (dW_bf16 && L.chunks > 1) T.dW = take(sizeof(float) * static_cast<size_t>(V) * static_cast<size_t>(d));
   }
   L.total = T.total = off;
   return T;
@@ -1080,17 +1088,26 @@ int tok_logits(const Call& c, int64_t c0, int64_t rows, int mode, void* out, int
 }
 
 // dW of a call without tokens: zero unless it is added to.
-int zero_dW(const Call& c, float* dW) {
+int zero_dW(const Call& c, void* dW, bool dW_bf16) {
   if (!dW || c.o.accumulate_dW) return LCE_OK;
-  const size_t bytes = sizeof(float) * static_cast<size_t>(c.V) * static_cast<size_t>(c.d);
+  const size_t bytes = (dW_bf16 ? 2 : 4) * static_cast<size_t>(c.V) * static_cast<size_t>(c.d);
   return timed(c.s, K_MEMSET, static_cast<double>(bytes), [&] { return cuda_rc(cudaMemsetAsync(dW, 0, bytes, c.s)); });
 }
 
-// The backward GEMMs of a chunk on its exact gradient tile, for the gradients that are wanted.
-int tok_grads(const Call& c, int64_t c0, int64_t rows, void* dH, float* dW) {
+// The backward GEMMs of a chunk on its exact gradient tile, for the gradients that are wanted. A
+// bf16 dW is summed in fp32 in the workspace until the last chunk, which stores it.
+int tok_grads(const Call& c, const TokLayout& T, int64_t c0, int64_t rows, void* dH, void* dW, bool dW_bf16) {
   BwdPart part;
   part.with_dh = dH != nullptr;
   part.v_end = dW ? c.V : 0;
+  float* sum = T.dW ? reinterpret_cast<float*>(c.ws + T.dW) : nullptr;
+  if (dW && dW_bf16) {
+    part.dW_bf16 = c0 + rows >= c.N;
+    if (!part.dW_bf16)
+      dW = sum;
+    else if (c0 > 0)
+      part.dW_add = sum;
+  }
   return dh_dw(c, c0, rows, nullptr, c.H + c0 * c.d, dH, dW, c.o.accumulate_dW || c0 > 0, false, part);
 }
 
@@ -1098,17 +1115,19 @@ int tok_grads(const Call& c, int64_t c0, int64_t rows, void* dH, float* dW) {
 
 extern "C" {
 
+int64_t lce_logits_stride(int64_t V) { return V > 0 ? ceil_div(V, kVocabTile) * kVocabTile : 0; }
+
 size_t lce_logprobs_workspace_size(int64_t N, int64_t d, int64_t V, int32_t top_k, const lce_opts* opts) {
   lce_opts o;
   lce_opts_init(&o);
   if (opts) o = *opts;
   if (check_sizes(N, d, V, &o) != LCE_OK || top_k < 0 || top_k > LCE_MAX_TOP || top_k > V) return 0;
-  return tok_layout(N, d, V, top_k > 0, false, &o).total;
+  return tok_layout(N, d, V, top_k > 0, false, false, &o).total;
 }
 
 int lce_logprobs(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V, float temperature,
                  int32_t top_k, float* logp, float* lse, float* entropy, float* top_logp, int64_t* top_idx,
-                 const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
+                 float* logits, const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
   lce_opts o;
   lce_opts_init(&o);
   if (opts) o = *opts;
@@ -1118,16 +1137,17 @@ int lce_logprobs(const void* H, const void* W, const int64_t* y, int64_t N, int6
   if (!W || !ws || (N > 0 && (!H || !y || !logp || !lse || (top_k > 0 && (!top_logp || !top_idx)))))
     return LCE_ERR_INVALID_ARG;
   if (!aligned(W, 16) || !aligned(H, 16) || !aligned(y, 8) || !aligned(ws, 256) || !aligned(logp, 4) ||
-      !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(top_logp, 4) || !aligned(top_idx, 8))
+      !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(top_logp, 4) || !aligned(top_idx, 8) ||
+      !aligned(logits, 16))
     return LCE_ERR_ALIGNMENT;
-  const TokLayout T = tok_layout(N, d, V, top_k > 0, false, &o);
+  const TokLayout T = tok_layout(N, d, V, top_k > 0 && !logits, false, false, &o);
   Call c;
   LCE_TRY(tok_begin(&c, T, H, W, y, N, d, V, o, ws, ws_bytes, stream));
   LCE_TRY(prepare(c, nullptr));
-  float* Z = top_k > 0 ? reinterpret_cast<float*>(c.ws + T.Z) : nullptr;
   for (int64_t c0 = 0; c0 < N; c0 += c.L.C) {
     const int64_t rows = (N - c0) < c.L.C ? (N - c0) : c.L.C;
     const lce::TokParams p = tok_params(c, c0, rows, temperature);
+    float* Z = logits ? logits + c0 * T.ldz : top_k > 0 ? reinterpret_cast<float*>(c.ws + T.Z) : nullptr;
     LCE_TRY(tok_logits(c, c0, rows, Z ? lce::TOK_STATS_Z : lce::TOK_STATS, Z, T.ldz, p));
     lce::TokScoreArgs a;
     std::memset(&a, 0, sizeof a);
@@ -1154,22 +1174,37 @@ int lce_logprobs(const void* H, const void* W, const int64_t* y, int64_t N, int6
   return finish(c);
 }
 
+size_t lce_logprobs_backward_workspace_size(int64_t N, int64_t d, int64_t V, int32_t grads, const lce_opts* opts) {
+  lce_opts o;
+  lce_opts_init(&o);
+  if (opts) o = *opts;
+  if (check_sizes(N, d, V, &o) != LCE_OK || (grads & ~LCE_DW_BF16) != 0) return 0;
+  return tok_layout(N, d, V, false, true, (grads & LCE_DW_BF16) != 0, &o).total;
+}
+
 int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
                           float temperature, const float* lse, const float* entropy, const float* g_logp,
-                          const float* g_entropy, void* dH, float* dW, const lce_opts* opts, void* ws,
-                          size_t ws_bytes, void* stream) {
-  Call c;
-  LCE_TRY(begin(&c, LCE_OP_BACKWARD, H, W, y, N, d, V, opts, ws, ws_bytes, stream));
+                          const float* g_entropy, const float* logits, int32_t grads, void* dH, void* dW,
+                          const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
+  lce_opts o;
+  lce_opts_init(&o);
+  if (opts) o = *opts;
+  LCE_TRY(check_sizes(N, d, V, &o));
   LCE_TRY(check_temperature(temperature));
-  if (c.o.reserved != 0 || (!dH && !dW) || (N > 0 && (!lse || !g_logp || (g_entropy && !entropy))))
+  const bool dW_bf16 = (grads & LCE_DW_BF16) != 0;
+  if (o.reserved != 0 || (grads & ~LCE_DW_BF16) != 0 || (dW_bf16 && o.accumulate_dW) || !W || !ws || (!dH && !dW) ||
+      (N > 0 && (!H || !y || !lse || !g_logp || (g_entropy && !entropy))))
     return LCE_ERR_INVALID_ARG;
-  if (!aligned(dW, 16) || !aligned(dH, 16) || !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(g_logp, 4) ||
-      !aligned(g_entropy, 4))
+  if (!aligned(W, 16) || !aligned(H, 16) || !aligned(y, 8) || !aligned(ws, 256) || !aligned(dW, 16) ||
+      !aligned(dH, 16) || !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(g_logp, 4) || !aligned(g_entropy, 4) ||
+      !aligned(logits, 16))
     return LCE_ERR_ALIGNMENT;
-  c.o.reduction = LCE_SUM;  // the upstream gradients carry every factor
-  LCE_TRY(device_check(&c.dev));
+  o.reduction = LCE_SUM;  // the upstream gradients carry every factor
+  const TokLayout T = tok_layout(N, d, V, false, true, dW_bf16, &o);
+  Call c;
+  LCE_TRY(tok_begin(&c, T, H, W, y, N, d, V, o, ws, ws_bytes, stream));
   LCE_TRY(prepare(c, nullptr));
-  if (N == 0) LCE_TRY(zero_dW(c, dW));
+  if (N == 0) LCE_TRY(zero_dW(c, dW, dW_bf16));
   uint16_t* G = reinterpret_cast<uint16_t*>(c.ws + c.L.P);
   for (int64_t c0 = 0; c0 < N; c0 += c.L.C) {
     const int64_t rows = (N - c0) < c.L.C ? (N - c0) : c.L.C;
@@ -1178,8 +1213,27 @@ int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_
     p.entropy = entropy ? entropy + c0 : nullptr;
     p.g_logp = g_logp + c0;
     p.g_entropy = g_entropy ? g_entropy + c0 : nullptr;
-    LCE_TRY(tok_logits(c, c0, rows, lce::TOK_GRAD, G, c.L.ldp, p));
-    LCE_TRY(tok_grads(c, c0, rows, dH, dW));
+    if (logits) {
+      lce::ScoreGradArgs a;
+      std::memset(&a, 0, sizeof a);
+      a.V = p.V;
+      a.ldz = T.ldz;
+      a.ldg = c.L.ldp;
+      a.inv_t = p.inv_t;
+      a.ignore_index = p.ignore_index;
+      a.y = p.y;
+      a.lse = p.lse;
+      a.entropy = p.entropy;
+      a.g_logp = p.g_logp;
+      a.g_entropy = p.g_entropy;
+      a.Z = logits + c0 * T.ldz;
+      a.G = reinterpret_cast<__nv_bfloat16*>(G);
+      LCE_TRY(timed(c.s, K_COMBINE, 6.0 * static_cast<double>(rows) * static_cast<double>(V),
+                    [&] { return cuda_rc(lce::launch_score_grad(a, p.rows, c.s)); }));
+    } else {
+      LCE_TRY(tok_logits(c, c0, rows, lce::TOK_GRAD, G, c.L.ldp, p));
+    }
+    LCE_TRY(tok_grads(c, T, c0, rows, dH, dW, dW_bf16));
   }
   return finish(c);
 }
@@ -1189,14 +1243,15 @@ int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_
 namespace {
 
 int distill(const void* H, const void* W, const int64_t* idx, const void* t, int64_t N, int64_t d, int64_t V,
-            int32_t K, int32_t teacher, float temperature, const float* grad_loss, float* loss, float* row_loss,
-            void* dH, float* dW, bool with_grad, const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
+            int32_t K, int32_t teacher, float temperature, const float* grad_loss, int32_t grads, float* loss,
+            float* row_loss, void* dH, void* dW, bool with_grad, const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
   lce_opts o;
   lce_opts_init(&o);
   if (opts) o = *opts;
   LCE_TRY(check_sizes(N, d, V, &o));
   LCE_TRY(check_temperature(temperature));
-  if (o.reserved != 0 || K < 1 || K > LCE_MAX_TOP ||
+  const bool dW_bf16 = (grads & LCE_DW_BF16) != 0;
+  if (o.reserved != 0 || K < 1 || K > LCE_MAX_TOP || (grads & ~LCE_DW_BF16) != 0 || (dW_bf16 && o.accumulate_dW) ||
       (teacher & ~(LCE_TEACHER_BF16 | LCE_TEACHER_LOGPROBS)) != 0 ||
       ((teacher & LCE_TEACHER_LOGPROBS) && temperature != 1.f))
     return LCE_ERR_INVALID_ARG;
@@ -1206,7 +1261,7 @@ int distill(const void* H, const void* W, const int64_t* idx, const void* t, int
   if (!aligned(W, 16) || !aligned(H, 16) || !aligned(idx, 8) || !aligned(t, t_bf16 ? 2 : 4) || !aligned(ws, 256) ||
       !aligned(loss, 4) || !aligned(row_loss, 4) || !aligned(grad_loss, 4) || !aligned(dH, 16) || !aligned(dW, 16))
     return LCE_ERR_ALIGNMENT;
-  const TokLayout T = tok_layout(N, d, V, true, with_grad, &o);
+  const TokLayout T = tok_layout(N, d, V, true, with_grad, dW_bf16, &o);
   Call c;
   LCE_TRY(tok_begin(&c, T, H, W, nullptr, N, d, V, o, ws, ws_bytes, stream));
   int* cnt = with_grad ? reinterpret_cast<int*>(c.ws + c.L.dh_cnt) : nullptr;
@@ -1214,7 +1269,7 @@ int distill(const void* H, const void* W, const int64_t* idx, const void* t, int
     return cuda_rc(lce::launch_distill_count(idx, t, t_bf16, N, K, static_cast<int>(V), o.ignore_index, c.st, cnt,
                                              with_grad ? c.L.dh_ncnt : 0, c.dev.num_sms, c.s));
   }));
-  if (N == 0 && with_grad) LCE_TRY(zero_dW(c, dW));
+  if (N == 0 && with_grad) LCE_TRY(zero_dW(c, dW, dW_bf16));
   float* Z = reinterpret_cast<float*>(c.ws + T.Z);
   for (int64_t c0 = 0; c0 < N; c0 += c.L.C) {
     const int64_t rows = (N - c0) < c.L.C ? (N - c0) : c.L.C;
@@ -1245,7 +1300,7 @@ int distill(const void* H, const void* W, const int64_t* idx, const void* t, int
                                                       (with_grad ? 6.0 * static_cast<double>(V) : 32.0 * K));
     LCE_TRY(timed(c.s, K_COMBINE, bytes,
                   [&] { return cuda_rc(lce::launch_distill_row(a, static_cast<int>(rows), c.s)); }));
-    if (with_grad) LCE_TRY(tok_grads(c, c0, rows, dH, dW));
+    if (with_grad) LCE_TRY(tok_grads(c, T, c0, rows, dH, dW, dW_bf16));
   }
   LCE_TRY(finalize(c, row_loss, loss));
   return finish(c);
@@ -1255,28 +1310,40 @@ int distill(const void* H, const void* W, const int64_t* idx, const void* t, int
 
 extern "C" {
 
-size_t lce_distill_workspace_size(int64_t N, int64_t d, int64_t V, int32_t K, int32_t with_grad,
+size_t lce_distill_workspace_size(int64_t N, int64_t d, int64_t V, int32_t K, int32_t with_grad, int32_t grads,
                                   const lce_opts* opts) {
   lce_opts o;
   lce_opts_init(&o);
   if (opts) o = *opts;
-  if (check_sizes(N, d, V, &o) != LCE_OK || K < 1 || K > LCE_MAX_TOP) return 0;
-  return tok_layout(N, d, V, true, with_grad != 0, &o).total;
+  if (check_sizes(N, d, V, &o) != LCE_OK || K < 1 || K > LCE_MAX_TOP || (grads & ~LCE_DW_BF16) != 0) return 0;
+  return tok_layout(N, d, V, true, with_grad != 0, (grads & LCE_DW_BF16) != 0, &o).total;
 }
 
 int lce_distill_forward(const void* H, const void* W, const int64_t* idx, const void* t, int64_t N, int64_t d,
                         int64_t V, int32_t K, int32_t teacher, float temperature, float* loss, float* row_loss,
                         const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
-  return distill(H, W, idx, t, N, d, V, K, teacher, temperature, nullptr, loss, row_loss, nullptr, nullptr, false,
+  return distill(H, W, idx, t, N, d, V, K, teacher, temperature, nullptr, 0, loss, row_loss, nullptr, nullptr, false,
                  opts, ws, ws_bytes, stream);
 }
 
 int lce_distill_fwd_bwd(const void* H, const void* W, const int64_t* idx, const void* t, int64_t N, int64_t d,
-                        int64_t V, int32_t K, int32_t teacher, float temperature, const float* grad_loss, float* loss,
-                        float* row_loss, void* dH, float* dW, const lce_opts* opts, void* ws, size_t ws_bytes,
-                        void* stream) {
-  return distill(H, W, idx, t, N, d, V, K, teacher, temperature, grad_loss, loss, row_loss, dH, dW, true, opts, ws,
-                 ws_bytes, stream);
+                        int64_t V, int32_t K, int32_t teacher, float temperature, const float* grad_loss,
+                        int32_t grads, float* loss, float* row_loss, void* dH, void* dW, const lce_opts* opts,
+                        void* ws, size_t ws_bytes, void* stream) {
+  return distill(H, W, idx, t, N, d, V, K, teacher, temperature, grad_loss, grads, loss, row_loss, dH, dW, true, opts,
+                 ws, ws_bytes, stream);
+}
+
+int lce_scale_grads_bfloat(void* dH, void* dW, int64_t N, int64_t d, int64_t V, const float* grad_loss, void* stream) {
+  if (N < 0 || d <= 0 || d % 8 != 0 || V < 0 || !grad_loss) return LCE_ERR_INVALID_ARG;
+  if (!aligned(dH, 16) || !aligned(dW, 16) || !aligned(grad_loss, 4)) return LCE_ERR_ALIGNMENT;
+  DeviceInfo dev;
+  LCE_TRY(device_check(&dev));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const long long na = dH ? N * d : 0, nb = dW ? V * d : 0;
+  return timed(s, K_OTHER, 4.0 * static_cast<double>(na + nb), [&] {
+    return cuda_rc(lce::launch_scale_bf16(dH, na, dW, nb, grad_loss, dev.num_sms, s));
+  });
 }
 
 int lce_scale_grads(void* dH, float* dW, int64_t N, int64_t d, int64_t V, const float* grad_loss, void* stream) {

@@ -152,6 +152,8 @@ struct DwParams {
   long long ld;
   int accumulate;        // 1: out += result
   const DevStatus* st;   // gscale
+  int bf16_out;          // 1: bf16 output, stored once: bf16(add + result) (add null: bf16(result))
+  const float* add;      // [V, ld] fp32, the sum over earlier chunks (bf16_out)
 };
 
 // Kernel launches (return cudaGetLastError()).
@@ -214,6 +216,9 @@ cudaError_t launch_rmsnorm_bwd(const void* x, const float* w, const float* rstd,
 // In-place x *= *g of n_bf16 bf16 values (a multiple of 8) and n_f32 fp32 values (a multiple of 4).
 cudaError_t launch_scale(void* bf16, long long n_bf16, float* f32, long long n_f32, const float* g, int num_sms,
                          cudaStream_t s);
+// The same of two bf16 arrays (multiples of 8), in one launch.
+cudaError_t launch_scale_bf16(void* a, long long n_a, void* b, long long n_b, const float* g, int num_sms,
+                              cudaStream_t s);
 cudaError_t launch_finalize(const float* loss_i, long long N, const DevStatus* st, float* loss, cudaStream_t s);
 
 // ----------------------------------------------------------------------------
@@ -250,14 +255,28 @@ struct TokScoreArgs {
   long long ignore_index;
   const int64_t* y;
   const float4* partials;
-  const float* ztgt;     // K == 0
-  const float* Z;        // [rows, ldz] fp32 logits, K > 0
+  const float* ztgt;     // Z null: the label logits
+  const float* Z;        // [rows, ldz] fp32 logits, or null (K == 0)
   float* logp;           // [rows]
   float* lse;            // [rows]
   float* entropy;        // [rows] or null
   float* top_logp;       // [rows, K]
   int64_t* top_idx;      // [rows, K]
   int* flags;
+};
+
+struct ScoreGradArgs {
+  int V;
+  long long ldz, ldg;
+  float inv_t;
+  long long ignore_index;
+  const int64_t* y;      // [rows], as the next four
+  const float* lse;
+  const float* entropy;
+  const float* g_logp;
+  const float* g_entropy;  // or null
+  const float* Z;        // [rows, ldz] logits of the forward
+  __nv_bfloat16* G;      // [rows, ldg]
 };
 
 struct DistillArgs {
@@ -282,11 +301,12 @@ cudaError_t launch_tok_logits(int mode, const CUtensorMap& a, const CUtensorMap&
                               long long N, long long K, const TokParams& ep, int num_sms, cudaStream_t s);
 // The same for at most kFewRows rows (ep.rows), by one pass over W (lce_tokens.cu); h: map of H with
 // boxes of few_rows_box(rows) rows, w: K-major map of W; store_z: the logits too, else the label's.
-constexpr int kFewRows = 64;
-inline uint32_t few_rows_box(long long rows) { return rows <= 32 ? 32u : 64u; }
+constexpr int kFewRows = 96;
+inline uint32_t few_rows_box(long long rows) { return static_cast<uint32_t>((rows + 31) / 32 * 32); }
 cudaError_t launch_rows_logits(const CUtensorMap& h, const CUtensorMap& w, int store_z, float* Z, long long ldz,
                                long long V, long long d, const TokParams& ep, int num_sms, cudaStream_t s);
 cudaError_t launch_score(const TokScoreArgs& p, cudaStream_t s);
+cudaError_t launch_score_grad(const ScoreGradArgs& p, int rows, cudaStream_t s);
 // Clears the status block and cnt[0, ncnt), then counts the rows of idx [N, K] that keep an entry.
 cudaError_t launch_distill_count(const int64_t* idx, const void* t, int t_bf16, long long N, int K, int V,
                                  long long ignore_index, DevStatus* st, int* cnt, int ncnt, int num_sms,

@@ -384,6 +384,54 @@ struct DwEpi {
   }
 };
 
+// dW tile in bf16, stored once: bf16(acc * g/n), plus the fp32 sum of earlier
+// chunks where there are some. Rounded once, behind the whole sum; it saves the
+// fp32 dW and its conversion (4 + 4 + 2 bytes an element) where the caller wants
+// bf16, as autograd does for a bf16 W.
+struct DwBfEpi {
+  using Params = DwParams;
+  using State = DwEpi::State;
+  static __device__ __forceinline__ void init(const Params& p, State& st) { DwEpi::init(p, st); }
+  // rounded as the fp32 path's product and reduce-add are: the result is its dW in bf16
+  static __device__ __forceinline__ float add_scaled(float v, float f, float e) {
+    return __fadd_rn(__fmul_rn(v, f), e);
+  }
+
+  static __device__ __forceinline__ void tile(const Params& p, State& st, const EpiCtx& ctx, int m0, int col0,
+                                              uint32_t taddr) {
+    const float f = st.g;
+    if (m0 + ctx.row0 >= p.rows) return;  // all 32 rows of this warp are past the vocabulary
+    const int r = m0 + ctx.row0 + ctx.lane;
+    const float* add = p.add != nullptr && r < p.rows ? p.add + static_cast<long long>(r) * p.ld : nullptr;
+#pragma unroll 1
+    for (int u = 0; u < EPI_COLS / 64; ++u) {
+      if (col0 + u * 64 >= p.N) break;
+      stage_acquire(ctx);
+#pragma unroll 1
+      for (int hh = 0; hh < 2; ++hh) {
+        const int c = col0 + u * 64 + hh * 32;
+        float4 e[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)  // d % 8 == 0: a group of four lies inside the row or outside it
+          e[q] = add != nullptr && c + 4 * q < p.N ? __ldcs(reinterpret_cast<const float4*>(add + c + 4 * q))
+                                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+        float v[32];
+        tmem_ld_32x32b_x32(taddr + u * 64 + hh * 32, v);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint4 w;
+          w.x = pack_bf16x2(add_scaled(v[8 * q + 0], f, e[2 * q].x), add_scaled(v[8 * q + 1], f, e[2 * q].y));
+          w.y = pack_bf16x2(add_scaled(v[8 * q + 2], f, e[2 * q].z), add_scaled(v[8 * q + 3], f, e[2 * q].w));
+          w.z = pack_bf16x2(add_scaled(v[8 * q + 4], f, e[2 * q + 1].x), add_scaled(v[8 * q + 5], f, e[2 * q + 1].y));
+          w.w = pack_bf16x2(add_scaled(v[8 * q + 6], f, e[2 * q + 1].z), add_scaled(v[8 * q + 7], f, e[2 * q + 1].w));
+          *reinterpret_cast<uint4*>(ctx.stage + stage_off(ctx.lane, hh * 4 + q)) = w;
+        }
+      }
+      stage_release(ctx, col0 + u * 64, m0 + ctx.row0, false);
+    }
+  }
+};
+
 // ----------------------------------------------------------------------------
 // Label scan: n = number of labels in [0, V) that are not ignore_index, the
 // range-error bit, and the scales g/n and 1/n. One block, fixed-order sums.
@@ -734,6 +782,26 @@ __global__ void __launch_bounds__(256) k_scale(uint4* __restrict__ bf, long long
   }
 }
 
+// The same for two bf16 arrays.
+__global__ void __launch_bounds__(256) k_scale_bf16(uint4* __restrict__ a, long long na, uint4* __restrict__ b,
+                                                    long long nb, const float* __restrict__ gptr) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const float g = *gptr;
+  if (g == 1.f) return;
+  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+  for (long long i = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; i < na + nb; i += stride) {
+    uint4* at = i < na ? a + i : b + (i - na);
+    const uint4 v = *at;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      o[q] = pack_bf16x2(__uint_as_float(w[q] << 16) * g, __uint_as_float(w[q] & 0xffff0000u) * g);
+    *at = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
 // loss = (sum_i loss_i) * lscale, fp64 accumulation in a fixed order.
 __global__ void __launch_bounds__(1024) k_finalize(const float* __restrict__ loss_i, long long N,
                                                    const DevStatus* st, float* loss) {
@@ -815,7 +883,8 @@ struct LogitsProb {
 // rows in L2): all clusters start phase 1 together, and the clusters of phase
 // 3 all enter it after the same number of dH tiles. Tiles walk N first, so the
 // pairs running at once share the A rows.
-struct BwdProb {
+template <class Dw>
+struct BwdProbT {
   struct Params {
     CUtensorMap ah, bh, ch, aw, bw, cw;
     int h_m, h_n, h_k;   // dH: 256-row blocks of the chunk, 256-column blocks of d, k-blocks of V
@@ -833,7 +902,7 @@ struct BwdProb {
   };
   struct State {
     DhEpi::State h;
-    DwEpi::State w;
+    typename Dw::State w;
   };
   struct Sched {
     int hcount, q1, li, nlight, count2;
@@ -938,7 +1007,7 @@ struct BwdProb {
   }
   static __device__ __forceinline__ void init(const Params& p, State& st) {
     DhEpi::init(p.h, st.h);
-    DwEpi::init(p.w, st.w);
+    Dw::init(p.w, st.w);
   }
   static __device__ __forceinline__ void epilogue(const Params& p, State& st, const TileJob& tj, EpiCtx ctx, int m0,
                                                   int col0, uint32_t taddr) {
@@ -947,7 +1016,7 @@ struct BwdProb {
       DhEpi::tile(p.h, st.h, ctx, m0, col0, taddr, tj.part, tj.mb * p.h_n + tj.nb);
     } else {
       ctx.out = &p.cw;
-      DwEpi::tile(p.w, st.w, ctx, m0, col0, taddr);
+      Dw::tile(p.w, st.w, ctx, m0, col0, taddr);
     }
   }
 };
@@ -984,11 +1053,14 @@ cudaError_t launch_logits(const CUtensorMap& a, const CUtensorMap& b, const CUte
 constexpr int kOddDhFirstMaxK = 16;  // k-blocks of a dW tile (chunks of up to 1024 rows)
 constexpr double kDhBlockMaxShare = 1.25;
 
-cudaError_t launch_backward(const CUtensorMap& ah, const CUtensorMap& bh, const CUtensorMap& ch, const CUtensorMap& aw,
-                            const CUtensorMap& bw, const CUtensorMap& cw, long long rows, long long V, long long d,
-                            const DhParams& h, const DwParams& w, int* flags, int num_sms, cudaStream_t s,
-                            long long v_begin, long long v_end, bool with_dh) {
-  BwdProb::Params p;
+template <class Dw>
+static cudaError_t launch_backward_t(const CUtensorMap& ah, const CUtensorMap& bh, const CUtensorMap& ch,
+                                     const CUtensorMap& aw, const CUtensorMap& bw, const CUtensorMap& cw,
+                                     long long rows, long long V, long long d, const DhParams& h, const DwParams& w,
+                                     int* flags, int num_sms, cudaStream_t s, long long v_begin, long long v_end,
+                                     bool with_dh) {
+  using BwdProb = BwdProbT<Dw>;
+  typename BwdProb::Params p;
   p.ah = ah;
   p.bh = bh;
   p.ch = ch;
@@ -1067,6 +1139,17 @@ cudaError_t launch_backward(const CUtensorMap& ah, const CUtensorMap& bh, const 
   return launch_pair<BwdProb>(p, P, s);
 }
 
+cudaError_t launch_backward(const CUtensorMap& ah, const CUtensorMap& bh, const CUtensorMap& ch, const CUtensorMap& aw,
+                            const CUtensorMap& bw, const CUtensorMap& cw, long long rows, long long V, long long d,
+                            const DhParams& h, const DwParams& w, int* flags, int num_sms, cudaStream_t s,
+                            long long v_begin, long long v_end, bool with_dh) {
+  if (w.bf16_out)
+    return launch_backward_t<DwBfEpi>(ah, bh, ch, aw, bw, cw, rows, V, d, h, w, flags, num_sms, s, v_begin, v_end,
+                                      with_dh);
+  return launch_backward_t<DwEpi>(ah, bh, ch, aw, bw, cw, rows, V, d, h, w, flags, num_sms, s, v_begin, v_end,
+                                  with_dh);
+}
+
 cudaError_t launch_prepare(const int64_t* y, long long N, int V, long long ignore_index, int reduction,
                            long long n_override, const float* grad_loss, DevStatus* st, int* guards, int nguards,
                            int* cnt, int ncnt, cudaStream_t s) {
@@ -1131,6 +1214,13 @@ cudaError_t launch_scale(void* bf16, long long n_bf16, float* f32, long long n_f
   if (n_bf16 <= 0 && n_f32 <= 0) return cudaSuccess;
   return launch_k(k_scale, num_sms * 4, 256, 0, s, static_cast<uint4*>(bf16), n_bf16 / 8,
                   reinterpret_cast<float4*>(f32), n_f32 / 4, g);
+}
+
+cudaError_t launch_scale_bf16(void* a, long long n_a, void* b, long long n_b, const float* g, int num_sms,
+                              cudaStream_t s) {
+  if (n_a <= 0 && n_b <= 0) return cudaSuccess;
+  return launch_k(k_scale_bf16, num_sms * 4, 256, 0, s, static_cast<uint4*>(a), n_a / 8, static_cast<uint4*>(b),
+                  n_b / 8, g);
 }
 
 cudaError_t launch_finalize(const float* loss_i, long long N, const DevStatus* st, float* loss, cudaStream_t s) {

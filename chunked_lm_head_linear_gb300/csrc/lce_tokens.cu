@@ -65,6 +65,14 @@ __device__ __forceinline__ Mst warp_merge_mst(Mst a, float inv_t) {
 //                rounded to bf16 once (the operand type of the two GEMMs that
 //                follow), everything before it in fp32.
 // ----------------------------------------------------------------------------
+// An entry of the gradient tile (everything over T already): p (c0 + c1 log p)
+// with c0 = -a - e entropy, c1 = -e, and + a at the label.
+__device__ __forceinline__ float grad_entry(float z, float inv_t, float lse, float c0, float c1, float a, bool label) {
+  const float logp = fmaf(z, inv_t, -lse);
+  const float g = __fmul_rn(ex2_approx(logp * kLog2e), fmaf(c1, fmaxf(logp, kFloor), c0));
+  return label ? __fadd_rn(g, a) : g;
+}
+
 template <int MODE>
 struct TokEpi {
   using Params = TokParams;
@@ -173,14 +181,8 @@ struct TokEpi {
         uint32_t pk[16];
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
-          float g[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float dz = fmaf(v[c + h], p.inv_t, -lse);
-            g[h] = ex2_approx(dz * kLog2e) * fmaf(c1, fmaxf(dz, kFloor), c0g);
-            if (c0 + c + h == ycol) g[h] += a;
-          }
-          pk[c / 2] = pack_bf16x2(g[0], g[1]);
+          pk[c / 2] = pack_bf16x2(grad_entry(v[c], p.inv_t, lse, c0g, c1, a, c0 + c == ycol),
+                                  grad_entry(v[c + 1], p.inv_t, lse, c0g, c1, a, c0 + c + 1 == ycol));
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -260,9 +262,9 @@ cudaError_t launch_tok_mode(const CUtensorMap& a, const CUtensorMap& b, const CU
 // ----------------------------------------------------------------------------
 // Few rows (decoding): the logits are one pass over W, bound by reading it, so
 // the operands change sides. A tile is 128 vocabulary rows of W (the MMA's M,
-// each read once, by one CTA) by all rows of H (its N, 32 or 64, zero-filled
+// each read once, by one CTA) by all rows of H (its N, 32, 64 or 96, zero-filled
 // by TMA beyond the last), accumulated over d in TMEM; the ring of W blocks
-// keeps 128 to 160 KB a SM on their way from HBM. The pair kernel's 256-row
+// keeps 112 to 160 KB a SM on their way from HBM. The pair kernel's 256-row
 // tiles would multiply at least 256 rows and leave fewer bytes in flight.
 //   warp 0      TMA producer, warp 1 MMA issuer, warp 2 TMEM
 //   warps 4-7   epilogue: TMEM lanes (vocabulary) into shared memory as
@@ -275,14 +277,14 @@ template <int NT>
 struct RowsCfg {
   static constexpr int kABytes = 128 * BK * 2;
   static constexpr int kBBytes = NT * BK * 2;
-  static constexpr int kStages = NT <= 32 ? 10 : 8;
+  static constexpr int kStages = NT <= 32 ? 10 : NT <= 64 ? 8 : 7;
   static constexpr int kOut = kStages * (kABytes + kBBytes);
-  static constexpr int kBars = kOut + NT * 128 * 4;
+  static constexpr int kBars = kOut + 32 * 128 * 4;
   static constexpr int kNumBars = 2 * kStages + 4 + 1;
   static constexpr int kMisc = kBars + kNumBars * 8;
   static constexpr int kTotal = kMisc + 16;
   static constexpr int kDynamicBytes = kTotal + 1024;
-  static constexpr int kTmemCols = 2 * NT;
+  static constexpr int kTmemCols = NT <= 32 ? 64 : NT <= 64 ? 128 : 256;  // two accumulators, a power of two
   static_assert(kDynamicBytes <= 232448, "shared memory budget (few-rows kernel)");
 };
 
@@ -440,57 +442,62 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_rows_logits(const __grid_con
       if (!epilogue_all(came)) break;
       tc_fence_after_sync();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * NT);
+      const int col = t * 128 + lane * 4;
+      for (int n0 = 0; n0 < e.rows; n0 += 32) {  // 32 rows of H at a time through shared memory
+        if (n0 > 0) epilogue_all(true);          // the 32 before have been read
+        {
+          float v[32];
+          tmem_ld_32x32b_x32(taddr + n0, v);
 #pragma unroll
-      for (int n0 = 0; n0 < NT; n0 += 32) {
-        if (n0 >= e.rows) break;
-        float v[32];
-        tmem_ld_32x32b_x32(taddr + n0, v);
+          for (int c = 0; c < 32; ++c) out[c * 128 + q * 32 + lane] = v[c];
+        }
+        if (n0 + 32 >= e.rows) {  // the accumulator is free for the tile after next
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[acc]);
+        }
+        epilogue_all(true);
+        const int n1 = e.rows - n0 < 32 ? e.rows - n0 : 32;
+        for (int i = q; i < n1; i += 4) {
+          const int n = n0 + i;
+          const float4 z4 = *reinterpret_cast<const float4*>(out + i * 128 + lane * 4);
+          if (p.store_z) {
+            if (in_bounds(col + 3, p.ldz, e.flags))
+              *reinterpret_cast<float4*>(p.Z + static_cast<long long>(n) * p.ldz + col) = z4;
+          } else {
+            const long long y = e.y[n];
+            const long long c = y - col;
+            if (c >= 0 && c < 4 && y < e.V && y != e.ignore_index)
+              e.ztgt[n] = c == 0 ? z4.x : c == 1 ? z4.y : c == 2 ? z4.z : z4.w;
+          }
+          float v[4] = {z4.x, z4.y, z4.z, z4.w};
 #pragma unroll
-        for (int c = 0; c < 32; ++c) out[(n0 + c) * 128 + q * 32 + lane] = v[c];
+          for (int c = 0; c < 4; ++c)
+            if (col + c >= e.V) v[c] = -INFINITY;
+          float m = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+          const float mb = m == -INFINITY ? 0.f : m;
+          float s = 0.f, tt = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float dz = v[c] - mb;
+            const float x = ex2_approx(dz * k);
+            s += x;
+            tt = fmaf(x, fmaxf(dz, kFloor), tt);
+          }
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) {
+            s += __shfl_xor_sync(0xffffffffu, s, off);
+            tt += __shfl_xor_sync(0xffffffffu, tt, off);
+          }
+          if (lane == 0 && in_bounds(t, e.nparts, e.flags))
+            e.partials[static_cast<long long>(n) * e.nparts + t] = make_float4(m, s, tt * e.inv_t, 0.f);
+        }
       }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[acc]);
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1u;
-      }
-      asm volatile("bar.sync 1, 128;" ::: "memory");  // the tile is in shared memory
-      const int col = t * 128 + lane * 4;
-      for (int n = q; n < e.rows; n += 4) {
-        const float4 z4 = *reinterpret_cast<const float4*>(out + n * 128 + lane * 4);
-        if (p.store_z) {
-          if (in_bounds(col + 3, p.ldz, e.flags))
-            *reinterpret_cast<float4*>(p.Z + static_cast<long long>(n) * p.ldz + col) = z4;
-        } else {
-          const long long y = e.y[n];
-          const long long c = y - col;
-          if (c >= 0 && c < 4 && y < e.V && y != e.ignore_index)
-            e.ztgt[n] = c == 0 ? z4.x : c == 1 ? z4.y : c == 2 ? z4.z : z4.w;
-        }
-        float v[4] = {z4.x, z4.y, z4.z, z4.w};
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (col + c >= e.V) v[c] = -INFINITY;
-        float m = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        const float mb = m == -INFINITY ? 0.f : m;
-        float s = 0.f, tt = 0.f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float dz = v[c] - mb;
-          const float x = ex2_approx(dz * k);
-          s += x;
-          tt = fmaf(x, fmaxf(dz, kFloor), tt);
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-          s += __shfl_xor_sync(0xffffffffu, s, off);
-          tt += __shfl_xor_sync(0xffffffffu, tt, off);
-        }
-        if (lane == 0 && in_bounds(t, e.nparts, e.flags))
-          e.partials[static_cast<long long>(n) * e.nparts + t] = make_float4(m, s, tt * e.inv_t, 0.f);
       }
     }
   }
@@ -556,12 +563,16 @@ __device__ __forceinline__ Key sort32(Key k, int lane) {
 template <int KPL>
 struct TopList {
   Key slot[KPL];
-  Key kth;  // candidates must exceed it: the key of slot K - 1, or a lower bound of it given at the start
+  Key kth;   // candidates must exceed it: the key of slot K - 1, or a lower bound of it given at the start
+  Key* buf;  // this warp's 64 entries in shared memory: candidates not merged yet
+  int cnt;
 
-  __device__ __forceinline__ void clear(Key floor = 0) {
+  __device__ __forceinline__ void clear(Key* buffer, Key floor = 0) {
 #pragma unroll
     for (int j = 0; j < KPL; ++j) slot[j] = 0;
     kth = floor;
+    buf = buffer;
+    cnt = 0;
   }
   __device__ __forceinline__ Key at(int i) const {  // slot i (warp-uniform), in every lane
     Key k = 0;
@@ -569,21 +580,6 @@ struct TopList {
     for (int j = 0; j < KPL; ++j)
       if (j == (i >> 5)) k = slot[j];
     return __shfl_sync(0xffffffffu, k, i & 31);
-  }
-  __device__ __forceinline__ void insert(Key key, int lane) {
-    int pos = 0;
-#pragma unroll
-    for (int j = 0; j < KPL; ++j) pos += __popc(__ballot_sync(0xffffffffu, slot[j] > key));
-    Key carry = 0;
-#pragma unroll
-    for (int j = 0; j < KPL; ++j) {
-      const Key up = __shfl_up_sync(0xffffffffu, slot[j], 1);
-      const Key last = KPL > 1 ? __shfl_sync(0xffffffffu, slot[j], 31) : 0;
-      const int me = 32 * j + lane;
-      const Key moved = lane == 0 ? carry : up;
-      slot[j] = me < pos ? slot[j] : (me == pos ? key : moved);
-      carry = last;
-    }
   }
   // slot is bitonic (falls, then rises): into descending order.
   __device__ __forceinline__ void bitonic(int lane) {
@@ -610,54 +606,55 @@ struct TopList {
     const Key k = at(K - 1);
     kth = k > kth ? k : kth;
   }
-  // One candidate per lane (0: none). Up to three that exceed the K-th key are
-  // inserted one by one; more are sorted and merged at once (of two falling
+  // Up to 32 waiting candidates sorted and merged at once: of two falling
   // lists, the larger of each entry of one and its mirror image in the other
-  // are the largest of both, and bitonic).
-  __device__ __forceinline__ void offer(Key cand, int K, int lane) {
-    uint32_t mask = __ballot_sync(0xffffffffu, cand > kth);
-    if (mask == 0) return;
-    if (__popc(mask) > 3) {
-      cand = sort32(cand > kth ? cand : 0, lane);
-      cand = __shfl_sync(0xffffffffu, cand, 31 - lane);
-      slot[KPL - 1] = cand > slot[KPL - 1] ? cand : slot[KPL - 1];
-      bitonic(lane);
-      raise(K);
-      return;
-    }
-    while (mask) {
-      const int src = __ffs(mask) - 1;
-      insert(__shfl_sync(0xffffffffu, cand, src), lane);
-      raise(K);
-      if (lane == src) cand = 0;
-      mask = __ballot_sync(0xffffffffu, cand > kth);
-    }
+  // are the largest of both, and bitonic.
+  __device__ __forceinline__ void merge_waiting(int K, int lane) {
+    __syncwarp();
+    Key k = lane < cnt ? buf[lane] : 0;
+    const Key rest = 32 + lane < cnt ? buf[32 + lane] : 0;
+    __syncwarp();
+    k = sort32(k, lane);
+    k = __shfl_sync(0xffffffffu, k, 31 - lane);
+    slot[KPL - 1] = k > slot[KPL - 1] ? k : slot[KPL - 1];
+    bitonic(lane);
+    raise(K);
+    if (32 + lane < cnt) buf[lane] = rest;
+    cnt = cnt > 32 ? cnt - 32 : 0;
+    __syncwarp();
   }
-  // The lists of a block's warps into warp 0's (and back to all through buf).
+  // One candidate per lane (0: none); those that exceed kth wait until there are 32.
+  __device__ __forceinline__ void offer(Key cand, int K, int lane) {
+    const uint32_t mask = __ballot_sync(0xffffffffu, cand > kth);
+    if (mask == 0) return;
+    if (cand > kth) buf[cnt + __popc(mask & ((1u << lane) - 1u))] = cand;
+    cnt += __popc(mask);
+    if (cnt >= 32) merge_waiting(K, lane);
+  }
+  // What waits, then the lists of the block's warps, merged into everyone's list.
   template <int WARPS>
-  __device__ __forceinline__ void gather(Key (*buf)[32 * KPL], int K, int warp, int lane) {
-    if constexpr (WARPS > 1) {
+  __device__ __forceinline__ void finish(Key (*lists)[32 * KPL], int K, int warp, int lane) {
+    if (cnt > 0) merge_waiting(K, lane);
 #pragma unroll
-      for (int j = 0; j < KPL; ++j) buf[warp][32 * j + lane] = slot[j];
-      __syncthreads();
+    for (int j = 0; j < KPL; ++j) lists[warp][32 * j + lane] = slot[j];
+    __syncthreads();
 #pragma unroll
-      for (int step = 1; step < WARPS; step *= 2) {
-        if (warp % (2 * step) == 0) {
+    for (int step = 1; step < WARPS; step *= 2) {
+      if (warp % (2 * step) == 0) {
 #pragma unroll
-          for (int j = 0; j < KPL; ++j) {
-            const Key o = buf[warp + step][32 * KPL - 1 - (32 * j + lane)];
-            slot[j] = o > slot[j] ? o : slot[j];
-          }
-          bitonic(lane);
-#pragma unroll
-          for (int j = 0; j < KPL; ++j) buf[warp][32 * j + lane] = slot[j];
+        for (int j = 0; j < KPL; ++j) {
+          const Key o = lists[warp + step][32 * KPL - 1 - (32 * j + lane)];
+          slot[j] = o > slot[j] ? o : slot[j];
         }
-        __syncthreads();
-      }
+        bitonic(lane);
 #pragma unroll
-      for (int j = 0; j < KPL; ++j) slot[j] = buf[0][32 * j + lane];
-      raise(K);
+        for (int j = 0; j < KPL; ++j) lists[warp][32 * j + lane] = slot[j];
+      }
+      __syncthreads();
     }
+#pragma unroll
+    for (int j = 0; j < KPL; ++j) slot[j] = lists[0][32 * j + lane];
+    raise(K);
   }
 };
 
@@ -667,68 +664,77 @@ struct TopList {
 // tile outside them come K others, each with an element before all of its own.
 // So only K x 128 of the row's logits are read again, and of those only the
 // ones that reach the K-th largest maximum are candidates.
-// WARPS = 1: a warp per row, eight rows a block (many rows: 8192 of them fill
-// the GPU). WARPS = 8: a block per row (few rows: the row's own latency counts).
+// One block of WARPS warps per row. The triples are merged in an order that
+// does not depend on WARPS (256 running sums, t mod 256, then lanes, then the
+// eight groups of 32), so the results do not depend on how many rows a call or
+// a chunk has.
 template <int KPL, int WARPS>
-__global__ void __launch_bounds__(256) k_score(const TokScoreArgs p) {
+__global__ void __launch_bounds__(32 * WARPS) k_score(const TokScoreArgs p) {
   grid_dep_wait();
   grid_dep_launch();
-  __shared__ Key s_list[WARPS > 1 ? WARPS : 1][32 * KPL];
-  __shared__ Mst s_mst[WARPS > 1 ? WARPS : 1];
-  const int lane = threadIdx.x & 31;
-  const int warp = WARPS > 1 ? static_cast<int>(threadIdx.x >> 5) : 0;
-  const int r = WARPS > 1 ? static_cast<int>(blockIdx.x)
-                          : static_cast<int>((blockIdx.x * static_cast<unsigned>(blockDim.x) + threadIdx.x) >> 5);
-  if (r >= p.rows) return;  // a whole warp (WARPS = 1) or nobody
+  constexpr int kGroups = 8, kMine = kGroups / WARPS;    // groups of 32 running sums, and this warp's
+  constexpr int kBlocks = kMine >= 4 ? 1 : 4 / kMine;    // blocks of 256 triples whose loads are in flight together
+  __shared__ Key s_list[WARPS][32 * KPL];
+  __shared__ Key s_wait[WARPS][64];
+  __shared__ Mst s_mst[kGroups];
+  const int lane = threadIdx.x & 31, warp = static_cast<int>(threadIdx.x >> 5);
+  const int r = static_cast<int>(blockIdx.x);
   const float4* pr = p.partials + static_cast<long long>(r) * p.nparts;
   const int tiles = (p.V + EPI_COLS - 1) / EPI_COLS;  // half tiles that hold vocabulary columns
   const float* z = p.Z + static_cast<long long>(r) * p.ldz;
-  Mst acc{-INFINITY, 0.f, 0.f};
+  Mst sums[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) sums[i] = Mst{-INFINITY, 0.f, 0.f};
   TopList<KPL> top;
-  top.clear();
-  constexpr int kBatch = 4;  // loads in flight before their merges
-  for (int t0 = warp * 32; t0 < tiles; t0 += 32 * WARPS * kBatch) {
-    float4 v[kBatch];
+  top.clear(s_wait[warp]);
+  for (int t0 = warp * 32 + lane; t0 - lane < tiles; t0 += 32 * kGroups * kBlocks) {
+    float4 v[kBlocks][kMine];
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int t = t0 + b * 32 * WARPS + lane;
-      v[b] = t < tiles ? pr[t] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    for (int b = 0; b < kBlocks; ++b) {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int t = t0 + 32 * (b * kGroups + i * WARPS);
+        v[b][i] = t < tiles ? pr[t] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      }
     }
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int t = t0 + b * 32 * WARPS + lane;
-      merge_mst(acc, Mst{v[b].x, v[b].y, v[b].z}, p.inv_t);
-      if (p.K > 0) top.offer(t < tiles ? make_key(v[b].x, static_cast<uint32_t>(t)) : 0, p.K, lane);
+    for (int b = 0; b < kBlocks; ++b) {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int t = t0 + 32 * (b * kGroups + i * WARPS);
+        merge_mst(sums[i], Mst{v[b][i].x, v[b][i].y, v[b][i].z}, p.inv_t);
+        if (p.K > 0) top.offer(t < tiles ? make_key(v[b][i].x, static_cast<uint32_t>(t)) : 0, p.K, lane);
+      }
     }
   }
-  acc = warp_merge_mst(acc, p.inv_t);
-  if (WARPS > 1) {
-    if (lane == 0) s_mst[warp] = acc;
-    __syncthreads();
-    acc = s_mst[0];
 #pragma unroll
-    for (int i = 1; i < WARPS; ++i) merge_mst(acc, s_mst[i], p.inv_t);
+  for (int i = 0; i < kMine; ++i) {
+    sums[i] = warp_merge_mst(sums[i], p.inv_t);
+    if (lane == 0) s_mst[warp + i * WARPS] = sums[i];
   }
+  __syncthreads();
+  Mst acc = s_mst[0];
+#pragma unroll
+  for (int i = 1; i < kGroups; ++i) merge_mst(acc, s_mst[i], p.inv_t);
   const float logs = logf(acc.s);
-  if (lane == 0 && warp == 0) {
+  if (threadIdx.x == 0) {
     p.lse[r] = fmaf(acc.m, p.inv_t, logs);
     if (p.entropy != nullptr) p.entropy[r] = logs - acc.t / acc.s;
     const long long y = p.y[r];
     const bool given = y != p.ignore_index && y >= 0 && y < p.V;
     float lp = 0.f;
-    if (given) lp = ((p.K > 0 ? z[y] : p.ztgt[r]) - acc.m) * p.inv_t - logs;
+    if (given) lp = ((p.Z != nullptr ? z[y] : p.ztgt[r]) - acc.m) * p.inv_t - logs;
     p.logp[r] = lp;
   }
   if (p.K == 0) return;
-  top.template gather<WARPS>(s_list, p.K, warp, lane);
+  top.template finish<WARPS>(s_list, p.K, warp, lane);
   TopList<KPL> best;
   const int ntop = tiles < p.K ? tiles : p.K;
   // with K half tiles, the K-th largest of their maxima bounds the K-th logit from below
-  best.clear(ntop == p.K ? (top.at(p.K - 1) & 0xffffffff00000000ull) : 0);
-  if (WARPS > 1) __syncthreads();  // s_list is written again below
+  best.clear(s_wait[warp], ntop == p.K ? (top.at(p.K - 1) & 0xffffffff00000000ull) : 0);
+  __syncthreads();  // s_list is written again below
   for (int i = warp; i < ntop; i += WARPS) {
-    const int tile = static_cast<int>(key_index(top.at(i)));
-    const int c = tile * EPI_COLS + lane * 4;
+    const int c = static_cast<int>(key_index(top.at(i))) * EPI_COLS + lane * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (c < p.V && in_bounds(c + 3, p.ldz, p.flags)) v = *reinterpret_cast<const float4*>(z + c);
     best.offer(c < p.V ? make_key(v.x, c) : 0, p.K, lane);
@@ -736,7 +742,7 @@ __global__ void __launch_bounds__(256) k_score(const TokScoreArgs p) {
     best.offer(c + 2 < p.V ? make_key(v.z, c + 2) : 0, p.K, lane);
     best.offer(c + 3 < p.V ? make_key(v.w, c + 3) : 0, p.K, lane);
   }
-  best.template gather<WARPS>(s_list, p.K, warp, lane);
+  best.template finish<WARPS>(s_list, p.K, warp, lane);
   if (warp != 0) return;
 #pragma unroll
   for (int j = 0; j < KPL; ++j) {
@@ -747,6 +753,42 @@ __global__ void __launch_bounds__(256) k_score(const TokScoreArgs p) {
       const uint32_t v = key_index(best.slot[j]);  // past V only if a row of NaN left the list short
       p.top_idx[at] = v < static_cast<uint32_t>(p.V) ? v : static_cast<uint32_t>(p.V - 1);
     }
+  }
+}
+
+// The gradient tile of TOK_GRAD from logits kept since the forward: one pass
+// over the row, 4 bytes read and 2 written a logit, in place of the logits
+// GEMM (2 d flops a logit). One block per row; a row whose upstream gradients
+// are zero is written without reading its logits.
+constexpr int kRowThreads = 256;
+
+__global__ void __launch_bounds__(kRowThreads) k_score_grad(const ScoreGradArgs p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int r = blockIdx.x, tid = threadIdx.x;
+  const float* z = p.Z + static_cast<long long>(r) * p.ldz;
+  __nv_bfloat16* g = p.G + static_cast<long long>(r) * p.ldg;
+  const long long y = p.y[r];
+  const bool given = y != p.ignore_index && y >= 0 && y < p.V;
+  const float lse = p.lse[r];
+  const float a = given ? p.g_logp[r] * p.inv_t : 0.f;
+  const float e = p.g_entropy != nullptr ? p.g_entropy[r] * p.inv_t : 0.f;
+  const float c1 = -e, c0 = p.g_entropy != nullptr ? -a - e * p.entropy[r] : -a;
+  const bool zero = a == 0.f && e == 0.f && c0 == 0.f;
+  const int yc = given ? static_cast<int>(y) : -1;
+  for (int c = tid * 8; c < p.V; c += kRowThreads * 8) {
+    // columns past V (up to 7) lie inside the row's padding: never read by the GEMMs
+    uint32_t o[4] = {0u, 0u, 0u, 0u};
+    if (!zero) {
+      const float4 u = __ldcs(reinterpret_cast<const float4*>(z + c));
+      const float4 w = __ldcs(reinterpret_cast<const float4*>(z + c + 4));
+      float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = grad_entry(v[i], p.inv_t, lse, c0, c1, a, c + i == yc);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    }
+    *reinterpret_cast<uint4*>(g + c) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
@@ -808,8 +850,6 @@ __global__ void __launch_bounds__(256) k_distill_count(const int64_t* __restrict
     if (s_bad) atomicOr(&st->flags, kFlagLabelRange);
   }
 }
-
-constexpr int kRowThreads = 256;
 
 __device__ __forceinline__ float block_sum(float v, float* red) {
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
@@ -962,22 +1002,36 @@ cudaError_t launch_tok_logits(int mode, const CUtensorMap& a, const CUtensorMap&
 
 cudaError_t launch_rows_logits(const CUtensorMap& h, const CUtensorMap& w, int store_z, float* Z, long long ldz,
                                long long V, long long d, const TokParams& ep, int num_sms, cudaStream_t s) {
-  if (ep.rows <= 32) return launch_rows_nt<32>(h, w, store_z, Z, ldz, V, d, ep, num_sms, s);
-  return launch_rows_nt<64>(h, w, store_z, Z, ldz, V, d, ep, num_sms, s);
+  switch (few_rows_box(ep.rows)) {
+    case 32: return launch_rows_nt<32>(h, w, store_z, Z, ldz, V, d, ep, num_sms, s);
+    case 64: return launch_rows_nt<64>(h, w, store_z, Z, ldz, V, d, ep, num_sms, s);
+    default: return launch_rows_nt<96>(h, w, store_z, Z, ldz, V, d, ep, num_sms, s);
+  }
 }
 
-// Up to this many rows take a block each in k_score, more a warp each.
-constexpr int kScoreBlockRows = 1024;
+template <int WARPS>
+cudaError_t launch_score_warps(const TokScoreArgs& p, cudaStream_t s) {
+  if (p.K <= 32) return launch_k(k_score<1, WARPS>, p.rows, 32 * WARPS, 0, s, p);
+  if (p.K <= 64) return launch_k(k_score<2, WARPS>, p.rows, 32 * WARPS, 0, s, p);
+  return launch_k(k_score<kMaxTop / 32, WARPS>, p.rows, 32 * WARPS, 0, s, p);
+}
+
+// Warps of a row's block: with few rows the row's own latency counts, with
+// many the GPU is full and every further warp is one more list to merge. At V
+// = 151936 and K = 20, microseconds with 8 / 2 / 1 warps: 32 rows 12.5 / 19.1 /
+// 26.0, 512 rows 20.3 / 24.8 / 32.9, 2048 rows 52.2 / 32.9 / 39.4, 4096 rows
+// 92.5 / 56.9 / 47.4.
+constexpr int kScoreRows8 = 512, kScoreRows2 = 2048;
 
 cudaError_t launch_score(const TokScoreArgs& p, cudaStream_t s) {
   if (p.rows <= 0) return cudaSuccess;
-  if (p.rows <= kScoreBlockRows) {
-    if (p.K <= 32) return launch_k(k_score<1, 8>, p.rows, 256, 0, s, p);
-    return launch_k(k_score<kMaxTop / 32, 8>, p.rows, 256, 0, s, p);
-  }
-  const int grid = (p.rows + 7) / 8;
-  if (p.K <= 32) return launch_k(k_score<1, 1>, grid, 256, 0, s, p);
-  return launch_k(k_score<kMaxTop / 32, 1>, grid, 256, 0, s, p);
+  if (p.rows <= kScoreRows8) return launch_score_warps<8>(p, s);
+  return p.rows <= kScoreRows2 ? launch_score_warps<2>(p, s) : launch_score_warps<1>(p, s);
+}
+
+cudaError_t launch_score_grad(const ScoreGradArgs& p, int rows, cudaStream_t s) {
+  if (rows <= 0) return cudaSuccess;
+  return launch_k(k_score_grad, rows, kRowThreads, 0, s, p);
 }
 
 cudaError_t launch_distill_count(const int64_t* idx, const void* t, int t_bf16, long long N, int K, int V,

@@ -46,6 +46,7 @@ LCE_DEVICE_LABEL_RANGE, LCE_DEVICE_TIMEOUT, LCE_DEVICE_BOUNDS = 1, 2, 4
 LCE_TEST_FORCE_TIMEOUT = 0x7E57
 LCE_MAX_TOP = 128
 LCE_TEACHER_BF16, LCE_TEACHER_LOGPROBS = 1, 2
+LCE_DW_BF16 = 1
 
 # Every symbol include/lce.h declares.
 EXPORTED = ("lce_opts_init", "lce_workspace_size", "lce_forward", "lce_backward", "lce_fwd_bwd",
@@ -54,8 +55,9 @@ EXPORTED = ("lce_opts_init", "lce_workspace_size", "lce_forward", "lce_backward"
             "lce_vshard_forward_stats", "lce_vshard_combine", "lce_vshard_backward",
             "lce_rmsnorm_workspace_size", "lce_rmsnorm_forward", "lce_rmsnorm_backward", "lce_norm_fwd_bwd",
             "lce_scale_grads", "lce_fwd_bwd_sliced", "lce_vshard_chunk_stats", "lce_vshard_chunk_backward",
-            "lce_logprobs_workspace_size", "lce_logprobs", "lce_logprobs_backward", "lce_distill_workspace_size",
-            "lce_distill_forward", "lce_distill_fwd_bwd")
+            "lce_logits_stride", "lce_logprobs_workspace_size", "lce_logprobs", "lce_logprobs_backward_workspace_size",
+            "lce_logprobs_backward", "lce_distill_workspace_size", "lce_distill_forward", "lce_distill_fwd_bwd",
+            "lce_scale_grads_bfloat")
 LCE_KERNEL_KINDS = 11
 # Kernel kinds whose profiled work is flops (tensor-core GEMMs); the others count bytes.
 GEMM_KINDS = ("logits_stats", "logits_grad", "gemm_dH_dW", "logits_ref")
@@ -149,18 +151,24 @@ def load(path: str | None = None):
         lib.lce_forward_noalloc.argtypes = [P, P, P, I64, I64, I64, P, P, OPT, P]
         lib.lce_forward_noalloc.restype = I32
         SZ = ctypes.c_size_t
+        lib.lce_logits_stride.argtypes = [I64]
+        lib.lce_logits_stride.restype = I64
         lib.lce_logprobs_workspace_size.argtypes = [I64, I64, I64, I32, OPT]
         lib.lce_logprobs_workspace_size.restype = SZ
-        lib.lce_logprobs.argtypes = [P, P, P, I64, I64, I64, F32, I32, P, P, P, P, P, OPT, P, SZ, P]
+        lib.lce_logprobs.argtypes = [P, P, P, I64, I64, I64, F32, I32, P, P, P, P, P, P, OPT, P, SZ, P]
         lib.lce_logprobs.restype = I32
-        lib.lce_logprobs_backward.argtypes = [P, P, P, I64, I64, I64, F32, P, P, P, P, P, P, OPT, P, SZ, P]
+        lib.lce_logprobs_backward_workspace_size.argtypes = [I64, I64, I64, I32, OPT]
+        lib.lce_logprobs_backward_workspace_size.restype = SZ
+        lib.lce_logprobs_backward.argtypes = [P, P, P, I64, I64, I64, F32, P, P, P, P, P, I32, P, P, OPT, P, SZ, P]
         lib.lce_logprobs_backward.restype = I32
-        lib.lce_distill_workspace_size.argtypes = [I64, I64, I64, I32, I32, OPT]
+        lib.lce_distill_workspace_size.argtypes = [I64, I64, I64, I32, I32, I32, OPT]
         lib.lce_distill_workspace_size.restype = SZ
         lib.lce_distill_forward.argtypes = [P, P, P, P, I64, I64, I64, I32, I32, F32, P, P, OPT, P, SZ, P]
         lib.lce_distill_forward.restype = I32
-        lib.lce_distill_fwd_bwd.argtypes = [P, P, P, P, I64, I64, I64, I32, I32, F32, P, P, P, P, P, OPT, P, SZ, P]
+        lib.lce_distill_fwd_bwd.argtypes = [P, P, P, P, I64, I64, I64, I32, I32, F32, P, I32, P, P, P, P, OPT, P, SZ, P]
         lib.lce_distill_fwd_bwd.restype = I32
+        lib.lce_scale_grads_bfloat.argtypes = [P, P, I64, I64, I64, P, P]
+        lib.lce_scale_grads_bfloat.restype = I32
         lib.lce_kernel_name.argtypes = [I32]
         lib.lce_kernel_name.restype = ctypes.c_char_p
         _lib = lib
@@ -190,16 +198,10 @@ def _resolve_chunk(chunk_tokens, N, d, V, device):
 
 def make_opts(chunk_tokens=0, ignore_index=-100, reduction="mean", n_valid_override=-1,
               accumulate_dW=False, sync_check=False, reserved=0) -> LceOpts:
-    o = LceOpts()
-    load().lce_opts_init(ctypes.byref(o))
-    o.chunk_tokens = int(chunk_tokens)
-    o.ignore_index = int(ignore_index)
-    o.n_valid_override = int(n_valid_override)
-    o.reduction = {"mean": LCE_MEAN, "sum": LCE_SUM}[reduction] if isinstance(reduction, str) else int(reduction)
-    o.accumulate_dW = int(bool(accumulate_dW))
-    o.sync_check = int(bool(sync_check))
-    o.reserved = int(reserved)
-    return o
+    if isinstance(reduction, str):
+        reduction = {"mean": LCE_MEAN, "sum": LCE_SUM}[reduction]
+    return LceOpts(int(chunk_tokens), int(ignore_index), int(n_valid_override), int(reduction),
+                   int(bool(accumulate_dW)), int(bool(sync_check)), int(reserved))
 
 
 def workspace_size(op: int, N: int, d: int, V: int, opts: LceOpts | None = None) -> int:
@@ -700,91 +702,122 @@ def lce_norm_fwd_bwd(x, w_norm, W, y, grad_loss=None, eps=1e-6, *, dW=None, work
 # ---------------------------------------------------------------------------
 # Token operators (see include/lce.h)
 # ---------------------------------------------------------------------------
+def _opt_ref(opts):
+    return ctypes.byref(opts) if opts is not None else None
+
+
+def lce_logits_stride(V: int) -> int:
+    """Row stride of kept logits: V rounded up to 256."""
+    return int(load().lce_logits_stride(int(V)))
+
+
 def lce_logprobs_workspace_size(N: int, d: int, V: int, top_k: int = 0, opts: LceOpts | None = None) -> int:
-    return int(load().lce_logprobs_workspace_size(int(N), int(d), int(V), int(top_k),
-                                                  ctypes.byref(opts) if opts is not None else None))
+    return load().lce_logprobs_workspace_size(N, d, V, top_k, _opt_ref(opts))
 
 
-def lce_distill_workspace_size(N: int, d: int, V: int, K: int, with_grad: bool = True,
+def lce_logprobs_backward_workspace_size(N: int, d: int, V: int, grads: int = 0, opts: LceOpts | None = None) -> int:
+    return load().lce_logprobs_backward_workspace_size(N, d, V, grads, _opt_ref(opts))
+
+
+def lce_distill_workspace_size(N: int, d: int, V: int, K: int, with_grad: bool = True, grads: int = 0,
                                opts: LceOpts | None = None) -> int:
-    return int(load().lce_distill_workspace_size(int(N), int(d), int(V), int(K), int(bool(with_grad)),
-                                                 ctypes.byref(opts) if opts is not None else None))
+    return load().lce_distill_workspace_size(N, d, V, K, int(bool(with_grad)), grads, _opt_ref(opts))
 
 
-def _token_opts(opt_kw, N, device, size):
-    """Options of a token call; chunk_tokens="auto" takes the largest multiple
-    of 256 (at most 4096) whose workspace, size(opts), fits in half of the
-    device's free memory."""
-    if opt_kw.get("chunk_tokens", 0) != "auto":
-        return make_opts(**opt_kw)
+def _token_plan(opt_kw, N, what, device, workspace, size):
+    """Options and workspace of a token call; size(opts) is what it needs.
+    chunk_tokens="auto" takes the largest multiple of 256 (at most 4096) whose
+    workspace fits in half of the device's free memory."""
     import torch
-    free, _ = torch.cuda.mem_get_info(device)
-    for chunk in range(min(4096, max(256, (N + 255) // 256 * 256)), 0, -256):
-        opts = make_opts(**{**opt_kw, "chunk_tokens": chunk})
-        if size(opts) <= free // 2:
-            return opts
-    raise LCEError(LCE_ERR_WORKSPACE, "chunk_tokens: not even a 256-token chunk fits in half the free memory")
-
-
-def _token_workspace(need, what, device, workspace):
-    """As _workspace, for the calls whose size depends on more than N, d and V."""
-    import torch
+    if opt_kw.get("chunk_tokens", 0) == "auto":
+        free, _ = torch.cuda.mem_get_info(device)
+        for chunk in range(min(4096, max(256, (N + 255) // 256 * 256)), 0, -256):
+            opts = make_opts(**{**opt_kw, "chunk_tokens": chunk})
+            if size(opts) <= free // 2:
+                break
+        else:
+            raise LCEError(LCE_ERR_WORKSPACE, "chunk_tokens: not even a 256-token chunk fits in half the free memory")
+    else:
+        opts = make_opts(**opt_kw)
+    need = size(opts)
     if need == 0:
-        raise LCEError(LCE_ERR_INVALID_ARG, what)
+        raise LCEError(LCE_ERR_INVALID_ARG, what + "_workspace_size")
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    _check_dev(workspace, "workspace", torch.uint8, device=device)
-    if workspace.numel() < need:
-        raise LCEError(LCE_ERR_WORKSPACE, f"workspace of {workspace.numel()} bytes, the call needs {need}")
-    return workspace
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _check_dev(workspace, "workspace", torch.uint8, device=device)
+        if workspace.numel() < need:
+            raise LCEError(LCE_ERR_WORKSPACE, f"workspace of {workspace.numel()} bytes, the call needs {need}")
+    return opts, workspace
 
 
-def _token_grads(H, V, d, opts, dW, need_dH, need_dW):
+def _dW_mode(dW_dtype):
+    """LCE_DW_BF16 for a bf16 dW, 0 for fp32 (the default)."""
+    import torch
+    if dW_dtype in (None, torch.float32):
+        return 0
+    if dW_dtype != torch.bfloat16:
+        raise ValueError(f"dW_dtype must be float32 or bfloat16, got {dW_dtype}")
+    return LCE_DW_BF16
+
+
+def _token_grads(H, V, d, opts, grads, dW, need_dH, need_dW):
     """The gradient outputs of a token call: dH and dW, or None where not wanted."""
     import torch
     if not (need_dH or need_dW):
         raise ValueError("neither dH nor dW is wanted")
+    dtype = torch.bfloat16 if grads & LCE_DW_BF16 else torch.float32
+    if opts.accumulate_dW and dtype != torch.float32:
+        raise ValueError("accumulate_dW=True adds into an fp32 dW")
     if not need_dW:
         if dW is not None:
             raise ValueError("a dW tensor was passed, but need_dW is False")
         _no_accumulate_without_dW(opts)
     elif dW is None:
         _no_accumulate_without_dW(opts)
-        dW = torch.empty((V, d), dtype=torch.float32, device=H.device)
+        dW = torch.empty((V, d), dtype=dtype, device=H.device)
+    else:
+        _check_dev(dW, "dW", dtype, shape=(V, d), device=H.device)
     return (torch.empty_like(H) if need_dH else None), dW
 
 
-def lce_logprobs(H, W, y, *, top_k: int = 0, temperature: float = 1.0, entropy: bool = True, workspace=None,
-                 stream=None, **opt_kw):
+def lce_logprobs(H, W, y, *, top_k: int = 0, temperature: float = 1.0, entropy: bool = True, logits=None,
+                 workspace=None, stream=None, **opt_kw):
     """Log-probabilities of the tokens y [N] under softmax(H W^T / temperature):
     returns logp, lse, entropy (fp32 [N]; entropy None if not wanted) and the
     top_k most likely tokens of each position, top_logp (fp32) and top_idx
-    (int64) [N, top_k] (None if top_k is 0). logp is 0 where y is ignore_index."""
+    (int64) [N, top_k] (None if top_k is 0). logp is 0 where y is ignore_index.
+    ``logits``: an fp32 tensor [N, lce_logits_stride(V)] that keeps z for
+    lce_logprobs_backward."""
     import torch
     N, d, V = _check_inputs(H, W, y)
-    K = int(top_k)
-    opts = _token_opts(opt_kw, N, H.device, lambda o: lce_logprobs_workspace_size(N, d, V, K, o))
-    ws = _token_workspace(lce_logprobs_workspace_size(N, d, V, K, opts), "lce_logprobs_workspace_size", H.device,
-                          workspace)
-    row = lambda: torch.empty(max(N, 1), dtype=torch.float32, device=H.device)[:N]  # noqa: E731
-    logp, lse, ent = row(), row(), row() if entropy else None
+    K, dev = int(top_k), H.device
+    if logits is not None:
+        _check_dev(logits, "logits", torch.float32, shape=(N, lce_logits_stride(V)), device=dev)
+    opts, ws = _token_plan(opt_kw, N, "lce_logprobs", dev, workspace,
+                           lambda o: lce_logprobs_workspace_size(N, d, V, K if logits is None else 0, o))
+    logp = torch.empty(N, dtype=torch.float32, device=dev)
+    lse = torch.empty(N, dtype=torch.float32, device=dev)
+    ent = torch.empty(N, dtype=torch.float32, device=dev) if entropy else None
     top_logp = top_idx = None
     if K > 0:
-        top_logp = torch.empty((max(N, 1), K), dtype=torch.float32, device=H.device)[:N]
-        top_idx = torch.empty((max(N, 1), K), dtype=torch.int64, device=H.device)[:N]
+        top_logp = torch.empty((N, K), dtype=torch.float32, device=dev)
+        top_idx = torch.empty((N, K), dtype=torch.int64, device=dev)
     rc = load().lce_logprobs(_ptr(H), _ptr(W), _ptr(y), N, d, V, float(temperature), K, _ptr(logp), _ptr(lse),
-                             _ptr(ent), _ptr(top_logp), _ptr(top_idx), ctypes.byref(opts), _ptr(ws), ws.numel(),
-                             _stream(stream))
+                             _ptr(ent), _ptr(top_logp), _ptr(top_idx), _ptr(logits), ctypes.byref(opts), _ptr(ws),
+                             ws.numel(), _stream(stream))
     _raise(rc, "lce_logprobs")
-    _keep(stream, H, W, y, ws, logp, lse, ent, top_logp, top_idx)
+    _keep(stream, H, W, y, ws, logp, lse, ent, top_logp, top_idx, logits)
     return logp, lse, ent, top_logp, top_idx
 
 
-def lce_logprobs_backward(H, W, y, lse, entropy, g_logp, g_entropy=None, *, temperature: float = 1.0, dW=None,
-                          need_dH: bool = True, need_dW: bool = True, workspace=None, stream=None, **opt_kw):
-    """dH (bf16 [N, d]) and dW (fp32 [V, d]) of lce_logprobs' logp and entropy for
-    upstream gradients g_logp and g_entropy (fp32 [N]; g_entropy may be None),
-    from its lse and entropy. A gradient that is not wanted is None."""
+def lce_logprobs_backward(H, W, y, lse, entropy, g_logp, g_entropy=None, *, temperature: float = 1.0, logits=None,
+                          dW=None, dW_dtype=None, need_dH: bool = True, need_dW: bool = True, workspace=None,
+                          stream=None, **opt_kw):
+    """dH (bf16 [N, d]) and dW (fp32 [V, d], or bf16 with dW_dtype) of
+    lce_logprobs' logp and entropy for upstream gradients g_logp and g_entropy
+    (fp32 [N]; g_entropy may be None), from its lse and entropy and, if it kept
+    them, its logits. A gradient that is not wanted is None."""
     import torch
     N, d, V = _check_inputs(H, W, y)
     for name, t in (("lse", lse), ("g_logp", g_logp)):
@@ -794,15 +827,17 @@ def lce_logprobs_backward(H, W, y, lse, entropy, g_logp, g_entropy=None, *, temp
         raise ValueError("g_entropy needs the entropy of lce_logprobs")
     for name, t in (("lse", lse), ("entropy", entropy), ("g_logp", g_logp), ("g_entropy", g_entropy)):
         _check_dev(t, name, torch.float32, shape=(N,), device=H.device)
-    _check_dev(dW, "dW", torch.float32, shape=(V, d), device=H.device)
-    opts = _token_opts(opt_kw, N, H.device, lambda o: workspace_size(LCE_OP_BACKWARD, N, d, V, o))
-    ws = _workspace(LCE_OP_BACKWARD, N, d, V, opts, H.device, workspace)
-    dH, dW = _token_grads(H, V, d, opts, dW, need_dH, need_dW)
+    if logits is not None:
+        _check_dev(logits, "logits", torch.float32, shape=(N, lce_logits_stride(V)), device=H.device)
+    grads = _dW_mode(dW_dtype)
+    opts, ws = _token_plan(opt_kw, N, "lce_logprobs_backward", H.device, workspace,
+                           lambda o: lce_logprobs_backward_workspace_size(N, d, V, grads, o))
+    dH, dW = _token_grads(H, V, d, opts, grads, dW, need_dH, need_dW)
     rc = load().lce_logprobs_backward(_ptr(H), _ptr(W), _ptr(y), N, d, V, float(temperature), _ptr(lse),
-                                      _ptr(entropy), _ptr(g_logp), _ptr(g_entropy), _ptr(dH), _ptr(dW),
-                                      ctypes.byref(opts), _ptr(ws), ws.numel(), _stream(stream))
+                                      _ptr(entropy), _ptr(g_logp), _ptr(g_entropy), _ptr(logits), grads, _ptr(dH),
+                                      _ptr(dW), ctypes.byref(opts), _ptr(ws), ws.numel(), _stream(stream))
     _raise(rc, "lce_logprobs_backward")
-    _keep(stream, H, W, y, ws, lse, entropy, g_logp, g_entropy, dH, dW)
+    _keep(stream, H, W, y, ws, lse, entropy, g_logp, g_entropy, logits, dH, dW)
     return dH, dW
 
 
@@ -843,11 +878,10 @@ def lce_distill_forward(H, W, idx, t, *, temperature: float = 1.0, renormalize: 
     import torch
     N, d, V, K, teacher = _check_teacher(H, W, idx, t)
     teacher = _distill_mode(teacher, renormalize, temperature)
-    opts = _token_opts(opt_kw, N, H.device, lambda o: lce_distill_workspace_size(N, d, V, K, False, o))
-    ws = _token_workspace(lce_distill_workspace_size(N, d, V, K, False, opts), "lce_distill_workspace_size", H.device,
-                          workspace)
+    opts, ws = _token_plan(opt_kw, N, "lce_distill", H.device, workspace,
+                           lambda o: lce_distill_workspace_size(N, d, V, K, False, 0, o))
     loss = torch.empty(1, dtype=torch.float32, device=H.device)
-    row_loss = torch.empty(max(N, 1), dtype=torch.float32, device=H.device)[:N]
+    row_loss = torch.empty(N, dtype=torch.float32, device=H.device)
     rc = load().lce_distill_forward(_ptr(H), _ptr(W), _ptr(idx), _ptr(t), N, d, V, K, teacher, float(temperature),
                                     _ptr(loss), _ptr(row_loss), ctypes.byref(opts), _ptr(ws), ws.numel(),
                                     _stream(stream))
@@ -857,25 +891,45 @@ def lce_distill_forward(H, W, idx, t, *, temperature: float = 1.0, renormalize: 
 
 
 def lce_distill_fwd_bwd(H, W, idx, t, grad_loss=None, *, temperature: float = 1.0, renormalize: bool = True, dW=None,
-                        need_dH: bool = True, need_dW: bool = True, workspace=None, stream=None, **opt_kw):
+                        dW_dtype=None, need_dH: bool = True, need_dW: bool = True, workspace=None, stream=None,
+                        **opt_kw):
     """lce_distill_forward and its gradients in one call: loss, row_loss, dH
-    (bf16 [N, d]), dW (fp32 [V, d]); a gradient that is not wanted is None."""
+    (bf16 [N, d]), dW (fp32 [V, d], or bf16 with dW_dtype); a gradient that is
+    not wanted is None."""
     import torch
     N, d, V, K, teacher = _check_teacher(H, W, idx, t)
     teacher = _distill_mode(teacher, renormalize, temperature)
-    _check_grads(H, N, d, V, grad_loss=grad_loss, dW=dW)
-    opts = _token_opts(opt_kw, N, H.device, lambda o: lce_distill_workspace_size(N, d, V, K, True, o))
-    ws = _token_workspace(lce_distill_workspace_size(N, d, V, K, True, opts), "lce_distill_workspace_size", H.device,
-                          workspace)
+    _check_dev(grad_loss, "grad_loss", torch.float32, numel=1, device=H.device)
+    grads = _dW_mode(dW_dtype)
+    opts, ws = _token_plan(opt_kw, N, "lce_distill", H.device, workspace,
+                           lambda o: lce_distill_workspace_size(N, d, V, K, True, grads, o))
     loss = torch.empty(1, dtype=torch.float32, device=H.device)
-    row_loss = torch.empty(max(N, 1), dtype=torch.float32, device=H.device)[:N]
-    dH, dW = _token_grads(H, V, d, opts, dW, need_dH, need_dW)
+    row_loss = torch.empty(N, dtype=torch.float32, device=H.device)
+    dH, dW = _token_grads(H, V, d, opts, grads, dW, need_dH, need_dW)
     rc = load().lce_distill_fwd_bwd(_ptr(H), _ptr(W), _ptr(idx), _ptr(t), N, d, V, K, teacher, float(temperature),
-                                    _ptr(grad_loss), _ptr(loss), _ptr(row_loss), _ptr(dH), _ptr(dW),
+                                    _ptr(grad_loss), grads, _ptr(loss), _ptr(row_loss), _ptr(dH), _ptr(dW),
                                     ctypes.byref(opts), _ptr(ws), ws.numel(), _stream(stream))
     _raise(rc, "lce_distill_fwd_bwd")
     _keep(stream, H, W, idx, t, ws, loss, row_loss, dH, dW, grad_loss)
     return loss, row_loss, dH, dW
+
+
+def lce_scale_grads_bfloat(dH, dW, grad_loss, *, stream=None):
+    """lce_scale_grads for a bf16 dW (either may be None)."""
+    import torch
+    if dH is None and dW is None:
+        return
+    for name, x in (("dH", dH), ("dW", dW)):
+        _check_dev(x, name, torch.bfloat16)
+        if x is not None and x.dim() != 2:
+            raise ValueError(f"{name} must have two dimensions")
+    if dH is not None and dW is not None and dH.shape[1] != dW.shape[1]:
+        raise ValueError("dH must be [N, d] and dW [V, d]")
+    _check_dev(grad_loss, "grad_loss", torch.float32, numel=1)
+    N, d = dH.shape if dH is not None else (0, dW.shape[1])
+    V = dW.shape[0] if dW is not None else 0
+    rc = load().lce_scale_grads_bfloat(_ptr(dH), _ptr(dW), N, d, V, _ptr(grad_loss), _stream(stream))
+    _raise(rc, "lce_scale_grads_bfloat")
 
 
 def lce_scale_grads(dH, dW, grad_loss, *, stream=None):

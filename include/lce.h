@@ -314,8 +314,14 @@ int lce_scale_grads(void* dH, float* dW, int64_t N, int64_t d, int64_t V, const 
  *                every row in falling order of z, the lower index first among
  *                equals, and their log-probabilities; 0 <= top_k <=
  *                LCE_MAX_TOP, top_k <= V; NULL when top_k is 0
+ *   logits [N, lce_logits_stride(V)]  (fp32, 16-byte aligned; NULL: not kept)
+ *                z itself, for lce_logprobs_backward; what lies past column V of
+ *                a row is not defined
  * A row with a NaN or +inf logit has NaN statistics, and its alternatives are
- * some tokens of the vocabulary. Workspace: lce_logprobs_workspace_size.
+ * some tokens of the vocabulary. Up to 96 rows of a chunk take a kernel of
+ * their own, whose logits may differ from those of larger chunks in the order
+ * of their fp32 sums. Workspace: lce_logprobs_workspace_size (with logits, that
+ * of top_k = 0 is enough).
  *
  * lce_logprobs_backward: gradients from upstream g_logp [N] and g_entropy [N]
  * (fp32; g_entropy may be NULL: zero), with lse and entropy of lce_logprobs on
@@ -324,17 +330,23 @@ int lce_scale_grads(void* dH, float* dW, int64_t N, int64_t d, int64_t V, const 
  *   G_iv = ([v = y_i] a_i - p_iv (a_i + e_i (log p_iv + entropy_i))) / temperature
  *   dH = G W (bf16), dW = G^T H (fp32; added to with opts->accumulate_dW).
  * G is rounded to bf16 once. Either of dH, dW may be NULL: not wanted, not
- * computed. Workspace: lce_workspace_size(LCE_OP_BACKWARD, ...).
+ * computed. grads: 0, or LCE_DW_BF16: dW is bf16 [V, d], the fp32 sum rounded
+ * once (not with accumulate_dW; several chunks are summed in fp32 in the
+ * workspace). logits: those of lce_logprobs, or NULL: recomputed chunk by
+ * chunk. Workspace: lce_logprobs_backward_workspace_size.
  */
 #define LCE_MAX_TOP 128
+#define LCE_DW_BF16 1
+int64_t lce_logits_stride(int64_t V); /* V rounded up to 256 */
 size_t lce_logprobs_workspace_size(int64_t N, int64_t d, int64_t V, int32_t top_k, const lce_opts* opts);
 int lce_logprobs(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V, float temperature,
                  int32_t top_k, float* logp, float* lse, float* entropy, float* top_logp, int64_t* top_idx,
-                 const lce_opts* opts, void* ws, size_t ws_bytes, void* stream);
+                 float* logits, const lce_opts* opts, void* ws, size_t ws_bytes, void* stream);
+size_t lce_logprobs_backward_workspace_size(int64_t N, int64_t d, int64_t V, int32_t grads, const lce_opts* opts);
 int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
                           float temperature, const float* lse, const float* entropy, const float* g_logp,
-                          const float* g_entropy, void* dH, float* dW, const lce_opts* opts, void* ws,
-                          size_t ws_bytes, void* stream);
+                          const float* g_entropy, const float* logits, int32_t grads, void* dH, void* dW,
+                          const lce_opts* opts, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Distillation from a teacher's top logits: per row, K tokens idx [N, K]
@@ -350,7 +362,7 @@ int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_
  *   loss = sum_i row_loss_i / n (LCE_MEAN) or without / n (LCE_SUM), n = rows
  *          with a kept entry, or opts->n_valid_override
  *   G_iv = (grad_loss temperature / n) (p_iv sum_k q_ik - sum_k q_ik [v = idx_ik])
- *   dH = G W (bf16), dW = G^T H (fp32; opts->accumulate_dW)
+ *   dH = G W (bf16), dW = G^T H (fp32; opts->accumulate_dW; or bf16: grads as above)
  * Rows without a kept entry have row_loss 0 and a zero gradient. The tile of G
  * without its leading factor is rounded to bf16 once. 1 <= K <= LCE_MAX_TOP.
  * loss [1], row_loss [N] fp32; grad_loss: device fp32 [1] or NULL (1.0); either
@@ -359,14 +371,19 @@ int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_
  */
 #define LCE_TEACHER_BF16 1
 #define LCE_TEACHER_LOGPROBS 2
-size_t lce_distill_workspace_size(int64_t N, int64_t d, int64_t V, int32_t K, int32_t with_grad, const lce_opts* opts);
+size_t lce_distill_workspace_size(int64_t N, int64_t d, int64_t V, int32_t K, int32_t with_grad, int32_t grads,
+                                  const lce_opts* opts);
 int lce_distill_forward(const void* H, const void* W, const int64_t* idx, const void* t, int64_t N, int64_t d,
                         int64_t V, int32_t K, int32_t teacher, float temperature, float* loss, float* row_loss,
                         const lce_opts* opts, void* ws, size_t ws_bytes, void* stream);
 int lce_distill_fwd_bwd(const void* H, const void* W, const int64_t* idx, const void* t, int64_t N, int64_t d,
-                        int64_t V, int32_t K, int32_t teacher, float temperature, const float* grad_loss, float* loss,
-                        float* row_loss, void* dH, float* dW, const lce_opts* opts, void* ws, size_t ws_bytes,
-                        void* stream);
+                        int64_t V, int32_t K, int32_t teacher, float temperature, const float* grad_loss,
+                        int32_t grads, float* loss, float* row_loss, void* dH, void* dW, const lce_opts* opts,
+                        void* ws, size_t ws_bytes, void* stream);
+
+/* lce_scale_grads for a bf16 dW [V, d] (LCE_DW_BF16): both arrays are rounded
+ * once more, unless the factor is a power of two. */
+int lce_scale_grads_bfloat(void* dH, void* dW, int64_t N, int64_t d, int64_t V, const float* grad_loss, void* stream);
 
 /* Synchronise the stream and copy the workspace's device status bits
  * (LCE_DEVICE_*) of the last call that used ws into *flags. */

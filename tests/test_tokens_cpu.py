@@ -116,10 +116,11 @@ def test_oracle_closed_forms():
 def test_logprobs_refusals(lib):
     E, P = lce, FAKE
 
-    def call(H=P, W=P, y=P, N=64, d=64, V=1000, T=1.0, K=5, logp=P, lse=P, ent=P, tl=P, ti=P, opts=None, ws=P,
-             nbytes=1 << 40):
+    def call(H=P, W=P, y=P, N=64, d=64, V=1000, T=1.0, K=5, logp=P, lse=P, ent=P, tl=P, ti=P, kept=None, opts=None,
+             ws=P, nbytes=1 << 40):
         o = opts if opts is not None else lce.make_opts()
-        return lib.lce_logprobs(H, W, y, N, d, V, T, K, logp, lse, ent, tl, ti, ctypes.byref(o), ws, nbytes, None)
+        return lib.lce_logprobs(H, W, y, N, d, V, T, K, logp, lse, ent, tl, ti, kept, ctypes.byref(o), ws, nbytes,
+                                None)
 
     for bad in (dict(H=None), dict(W=None), dict(y=None), dict(logp=None), dict(lse=None), dict(tl=None),
                 dict(ti=None), dict(ws=None), dict(N=-1), dict(d=12), dict(V=0), dict(T=0.0), dict(T=-1.0),
@@ -127,13 +128,17 @@ def test_logprobs_refusals(lib):
                 dict(opts=lce.make_opts(reserved=E.LCE_TEST_FORCE_TIMEOUT)), dict(opts=lce.make_opts(chunk_tokens=-1))):
         assert call(**bad) == E.LCE_ERR_INVALID_ARG, bad
     for bad in (dict(H=P + 8), dict(W=P + 2), dict(y=P + 4), dict(logp=P + 1), dict(lse=P + 2), dict(ent=P + 2),
-                dict(tl=P + 2), dict(ti=P + 4), dict(ws=P + 128)):
+                dict(tl=P + 2), dict(ti=P + 4), dict(ws=P + 128), dict(kept=P + 8)):
         assert call(**bad) == E.LCE_ERR_ALIGNMENT, bad
     need = lce.lce_logprobs_workspace_size(64, 64, 1000, 5)
     assert call(nbytes=need - 1) == E.LCE_ERR_WORKSPACE
+    less = lce.lce_logprobs_workspace_size(64, 64, 1000, 0)   # enough when the caller keeps the logits
+    assert less < need and call(kept=P, nbytes=less - 1) == E.LCE_ERR_WORKSPACE
+    assert [lce.lce_logits_stride(v) for v in (1, 256, 257, 151655)] == [256, 256, 512, 151808]
     torch = pytest.importorskip("torch")
     if not torch.cuda.is_available():   # these get as far as the device check
         for good in (dict(), dict(ent=None), dict(K=0, tl=None, ti=None), dict(nbytes=need),
+                     dict(kept=P, nbytes=less),
                      dict(N=0, H=None, y=None, logp=None, lse=None, tl=None, ti=None)):
             assert call(**good) in (E.LCE_ERR_CUDA, E.LCE_ERR_UNSUPPORTED_DEVICE), good
 
@@ -141,19 +146,26 @@ def test_logprobs_refusals(lib):
 def test_logprobs_backward_refusals(lib):
     E, P = lce, FAKE
 
-    def call(lse=P, ent=P, g1=P, g2=P, dH=P, dW=P, T=1.0, N=64, nbytes=1 << 40):
-        o = lce.make_opts()
-        return lib.lce_logprobs_backward(P, P, P, N, 64, 1000, T, lse, ent, g1, g2, dH, dW, ctypes.byref(o), P, nbytes,
-                                         None)
+    def call(lse=P, ent=P, g1=P, g2=P, kept=None, grads=0, dH=P, dW=P, T=1.0, N=64, acc=False, nbytes=1 << 40):
+        o = lce.make_opts(accumulate_dW=acc, chunk_tokens=32)
+        return lib.lce_logprobs_backward(P, P, P, N, 64, 1000, T, lse, ent, g1, g2, kept, grads, dH, dW,
+                                         ctypes.byref(o), P, nbytes, None)
 
-    for bad in (dict(lse=None), dict(g1=None), dict(ent=None), dict(dH=None, dW=None), dict(T=0.0), dict(N=-2)):
+    for bad in (dict(lse=None), dict(g1=None), dict(ent=None), dict(dH=None, dW=None), dict(T=0.0), dict(N=-2),
+                dict(grads=2), dict(grads=E.LCE_DW_BF16, acc=True)):
         assert call(**bad) == E.LCE_ERR_INVALID_ARG, bad
-    for bad in (dict(lse=P + 2), dict(ent=P + 2), dict(g1=P + 2), dict(g2=P + 1), dict(dH=P + 8), dict(dW=P + 4)):
+    for bad in (dict(kept=P + 4), dict(lse=P + 2), dict(ent=P + 2), dict(g1=P + 2), dict(g2=P + 1), dict(dH=P + 8), dict(dW=P + 4)):
         assert call(**bad) == E.LCE_ERR_ALIGNMENT, bad
-    assert call(nbytes=lce.workspace_size(lce.LCE_OP_BACKWARD, 64, 64, 1000) - 1) == E.LCE_ERR_WORKSPACE
+    o = lce.make_opts(chunk_tokens=32)
+    sizes = [lce.lce_logprobs_backward_workspace_size(64, 64, 1000, g, o) for g in (0, E.LCE_DW_BF16)]
+    assert sizes[1] - sizes[0] >= 1000 * 64 * 4       # two chunks: the fp32 sum of a bf16 dW
+    one = [lce.lce_logprobs_backward_workspace_size(64, 64, 1000, g) for g in (0, E.LCE_DW_BF16)]
+    assert one[0] == one[1] and lce.lce_logprobs_backward_workspace_size(64, 64, 1000, 4) == 0
+    for g in (0, 1):
+        assert call(grads=g, nbytes=sizes[g] - 1) == E.LCE_ERR_WORKSPACE
     torch = pytest.importorskip("torch")
     if not torch.cuda.is_available():
-        for good in (dict(), dict(ent=None, g2=None), dict(dH=None), dict(dW=None), dict(N=0)):
+        for good in (dict(), dict(ent=None, g2=None), dict(dH=None), dict(dW=None), dict(N=0), dict(kept=P), dict(grads=1)):
             assert call(**good) in (E.LCE_ERR_CUDA, E.LCE_ERR_UNSUPPORTED_DEVICE), good
 
 
@@ -161,10 +173,10 @@ def test_distill_refusals(lib):
     E, P = lce, FAKE
 
     def call(grad=True, H=P, W=P, idx=P, t=P, N=64, d=64, V=1000, K=5, teacher=0, T=1.0, loss=P, row=P, dH=P, dW=P,
-             opts=None, nbytes=1 << 40):
+             grads=0, opts=None, nbytes=1 << 40):
         o = opts if opts is not None else lce.make_opts()
         if grad:
-            return lib.lce_distill_fwd_bwd(H, W, idx, t, N, d, V, K, teacher, T, None, loss, row, dH, dW,
+            return lib.lce_distill_fwd_bwd(H, W, idx, t, N, d, V, K, teacher, T, None, grads, loss, row, dH, dW,
                                            ctypes.byref(o), P, nbytes, None)
         return lib.lce_distill_forward(H, W, idx, t, N, d, V, K, teacher, T, loss, row, ctypes.byref(o), P, nbytes,
                                        None)
@@ -179,12 +191,13 @@ def test_distill_refusals(lib):
             assert call(grad, **bad) == E.LCE_ERR_ALIGNMENT, (grad, bad)
         need = lce.lce_distill_workspace_size(64, 64, 1000, 5, grad)
         assert call(grad, nbytes=need - 1) == E.LCE_ERR_WORKSPACE
-    assert call(dH=None, dW=None) == E.LCE_ERR_INVALID_ARG
+    for bad in (dict(dH=None, dW=None), dict(grads=8), dict(grads=1, opts=lce.make_opts(accumulate_dW=True))):
+        assert call(**bad) == E.LCE_ERR_INVALID_ARG, bad
     assert call(dW=P + 4) == E.LCE_ERR_ALIGNMENT
     assert lce.lce_distill_workspace_size(64, 64, 1000, 5, True) > lce.lce_distill_workspace_size(64, 64, 1000, 5, False)
     torch = pytest.importorskip("torch")
     if not torch.cuda.is_available():
-        for good in (dict(), dict(dH=None), dict(dW=None), dict(grad=False), dict(t=P + 2, teacher=1),
+        for good in (dict(), dict(dH=None), dict(dW=None), dict(grad=False), dict(t=P + 2, teacher=1), dict(grads=1),
                      dict(teacher=E.LCE_TEACHER_LOGPROBS)):
             assert call(**good) in (E.LCE_ERR_CUDA, E.LCE_ERR_UNSUPPORTED_DEVICE), good
 
@@ -193,11 +206,21 @@ def test_token_workspaces_grow_with_the_chunk_only():
     o = lce.make_opts(chunk_tokens=1024)
     V, d = 151936, 2048
     for size in (lambda n: lce.lce_logprobs_workspace_size(n, d, V, 20, o),
-                 lambda n: lce.lce_distill_workspace_size(n, d, V, 64, True, o)):
+                 lambda n: lce.lce_logprobs_backward_workspace_size(n, d, V, 0, o),
+                 lambda n: lce.lce_distill_workspace_size(n, d, V, 64, True, 0, o)):
         assert size(65536) == size(8192) > 0
     assert lce.lce_logprobs_workspace_size(8192, d, V, 0, o) < lce.lce_logprobs_workspace_size(8192, d, V, 1, o)
     assert lce.lce_logprobs_workspace_size(64, 7, V, 0) == 0 and lce.lce_logprobs_workspace_size(64, 8, 4, 5) == 0
     assert lce.lce_distill_workspace_size(64, 8, V, 0) == 0 and lce.lce_distill_workspace_size(64, 8, V, 129) == 0
+
+
+def test_scale_refusals(lib):
+    E, P = lce, FAKE
+    call = lib.lce_scale_grads_bfloat
+    assert call(P, P, 4, 12, 4, P, None) == E.LCE_ERR_INVALID_ARG
+    assert call(P, P, 4, 8, 4, None, None) == E.LCE_ERR_INVALID_ARG
+    assert call(P + 8, P, 4, 8, 4, P, None) == E.LCE_ERR_ALIGNMENT
+    assert call(P, P + 2, 4, 8, 4, P, None) == E.LCE_ERR_ALIGNMENT
 
 
 def test_binding_refuses_cpu_tensors_and_bad_modes():
@@ -211,3 +234,5 @@ def test_binding_refuses_cpu_tensors_and_bad_modes():
             call()
     with pytest.raises(ValueError, match="temperature must be 1"):
         lce._distill_mode(0, False, 2.0)
+    with pytest.raises(ValueError, match="dW_dtype"):
+        lce._dW_mode(torch.float16)

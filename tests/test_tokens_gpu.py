@@ -245,6 +245,18 @@ def test_logprobs_backward(cuda_lib, N, d, V, T, chunk):
     assert none is None and torch.equal(only_H, dH)
     none, only_W = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), lse, ent, dev(g1), dev(g2), need_dH=False, **kw)
     assert none is None and torch.equal(only_W, dW)
+    # from logits that the forward kept; a bf16 dW
+    kept = torch.empty(N, cuda_lib.lce_logits_stride(V), device="cuda")
+    again = cuda_lib.lce_logprobs(Ht, Wt, dev(y), logits=kept, **kw)
+    assert torch.equal(kept[:, :V].double().cpu(), torch.from_numpy(H @ W.T))
+    for a, b in zip(again[:3], (logp, lse, ent)):
+        close(a, np64(b), 2.0 ** -20 * (1 + np.abs(np64(b))), "with kept logits")
+    for dt in (torch.float32, torch.bfloat16):
+        dH2, dW2 = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), lse, ent, dev(g1), dev(g2), logits=kept, dW_dtype=dt,
+                                                  **kw)
+        assert torch.equal(dH2, dH) and torch.equal(dW2, dW.to(dt))
+    dH2, dW2 = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), lse, ent, dev(g1), dev(g2), dW_dtype=torch.bfloat16, **kw)
+    assert torch.equal(dH2, dH) and torch.equal(dW2, dW.bfloat16())
     # without the entropy's share; added to a dW that is there
     ref = oracle.logprobs_backward_f64(H, W, y, g1, None, temperature=T)
     dH, dW = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), lse, None, dev(g1), **kw)
@@ -310,6 +322,8 @@ def test_distill(cuda_lib, N, d, V, K, T, chunk, kind, renormalize):
     close(loss, ref["loss"], tol.mean() * N / max(1, (mass > 0).sum()), "loss")
     check_grads(dH, dW, ref)
     assert not dH[dev(mass == 0)].any()
+    narrow = cuda_lib.lce_distill_fwd_bwd(Ht, Wt, it, tt, g, dW_dtype=torch.bfloat16, **kw)
+    assert torch.equal(narrow[2], dH) and torch.equal(narrow[3], dW.bfloat16())
     loss2, row2 = cuda_lib.lce_distill_forward(Ht, Wt, it, tt, **kw)
     assert torch.equal(loss2, loss) and torch.equal(row2, row)
     only_H = cuda_lib.lce_distill_fwd_bwd(Ht, Wt, it, tt, g, need_dW=False, **kw)
@@ -389,6 +403,11 @@ def test_autograd_modules(cuda_lib):
     ref = oracle.logprobs_backward_f64(H, W, y, np64(w), np.full(200, -0.5), temperature=0.8)
     check_grads(dH, None, ref)
     close(dW, ref["dW"], (U + 2.0 ** -10) * ref["dW_bulk"] + U * np.abs(ref["dW"]), "dW in bf16")
+    for recompute in (True, False):   # the same from recomputed and from kept logits
+        logp, ent = FusedLinearLogProbs(temperature=0.8, recompute=recompute, chunk_tokens=96)(Ht, Wt, dev(y))
+        a, b = torch.autograd.grad((logp * w).sum() - 0.5 * ent.sum(), [Ht, Wt])
+        check_grads(a, None, ref)
+        close(b, ref["dW"], (U + 2.0 ** -10) * ref["dW_bulk"] + U * np.abs(ref["dW"]), "dW in bf16")
     # outputs used alone; a frozen head
     logp, ent = FusedLinearLogProbs()(Ht, Wt.detach(), dev(y))
     check_grads(torch.autograd.grad(logp.sum(), Ht)[0], None,
@@ -402,8 +421,10 @@ def test_autograd_modules(cuda_lib):
     assert loss.shape == ()
     dH, dW = torch.autograd.grad(3.0 * loss, [Ht, Wt], retain_graph=True)
     ref = oracle.distill_f64(H, W, idx, t, temperature=2.0, grad_loss=3.0)
-    # scaled after its rounding: one rounding more for dH
-    close(dH, ref["dH"], (U + 2.0 ** -10) * ref["dH_bulk"] + 2.01 * U * np.abs(ref["dH"]) + 1e-30, "dH scaled")
+    # scaled after their rounding: one rounding more
+    for got, name in ((dH, "dH"), (dW, "dW")):
+        assert got.dtype == torch.bfloat16
+        close(got, ref[name], (U + 2.0 ** -10) * ref[name + "_bulk"] + 2.01 * U * np.abs(ref[name]) + 1e-30, name)
     with pytest.raises(RuntimeError, match="run the forward again"):
         torch.autograd.grad(loss, [Ht, Wt])
     with torch.no_grad():
@@ -421,7 +442,7 @@ def test_streams_graphs_and_a_shared_workspace(cuda_lib, N):
     Ht, Wt = heads(H, W)
     other, yt, it, tt = dev(H2, torch.bfloat16), dev(y), dev(idx), dev(t)
     g1 = dev(rng.standard_normal(N).astype(np.float32))
-    need = max(cuda_lib.lce_logprobs_workspace_size(N, 64, 3001, 5), cuda_lib.workspace_size(1, N, 64, 3001),
+    need = max(cuda_lib.lce_logprobs_workspace_size(N, 64, 3001, 5), cuda_lib.lce_logprobs_backward_workspace_size(N, 64, 3001),
                cuda_lib.lce_distill_workspace_size(N, 64, 3001, 7, True))
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
 
