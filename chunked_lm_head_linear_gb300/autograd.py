@@ -84,7 +84,7 @@ class _LogProbs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, H, W, y, temperature, keep, opts):
         logits = None
-        if keep and any(ctx.needs_input_grad[:2]):
+        if keep and (ctx.needs_input_grad[0] or ctx.needs_input_grad[1]):
             logits = torch.empty((H.shape[0], lce.lce_logits_stride(W.shape[0])), dtype=torch.float32, device=H.device)
         logp, lse, entropy, _, _ = lce.lce_logprobs(H, W, y, temperature=temperature, logits=logits, **opts)
         ctx.save_for_backward(H, W, y, lse, entropy, logits)
@@ -110,8 +110,8 @@ class FusedLinearLogProbs(torch.nn.Module):
 
     ``recompute``: True: the backward recomputes the logits (8 N V d flops in
     all); False: the forward keeps them for it (4 N V bytes, 6 N V d flops);
-    None: they are kept when the batch is one chunk (of chunk_tokens, or 4096),
-    so that the memory held stays O(chunk V)."""
+    None: they are kept when the batch is one chunk (chunk_tokens, or fewer than
+    6144 tokens), so that the memory held stays O(chunk V)."""
 
     def __init__(self, temperature: float = 1.0, ignore_index: int = -100, chunk_tokens=0, recompute=None):
         super().__init__()
@@ -123,7 +123,7 @@ class FusedLinearLogProbs(torch.nn.Module):
         keep = not self.recompute
         if self.recompute is None:
             chunk = self.opts["chunk_tokens"]
-            keep = chunk != "auto" and H.shape[0] <= (chunk or 4096)
+            keep = chunk != "auto" and H.shape[0] <= (chunk or 6143)
         return _LogProbs.apply(H, W, y, self.temperature, keep, self.opts)
 
 

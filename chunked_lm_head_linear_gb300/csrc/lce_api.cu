@@ -997,10 +997,20 @@ struct TokLayout {
   size_t total = 0;
 };
 
+// Tokens per chunk: the caller's, or N over its nearest number of 4096-token chunks (at least one)
+// in whole 256-row tiles. Equal chunks of up to 6143 tokens rather than 4096 and a remainder: each
+// further chunk streams W again and adds a read and a write of the fp32 dW.
+int64_t tok_chunk(int64_t N, const lce_opts* o) {
+  if (N <= 0 || (o && o->chunk_tokens > 0)) return chunk_of(N, o);
+  const int64_t n = (N + kDefaultChunk / 2) / kDefaultChunk;
+  const int64_t C = ceil_div(ceil_div(N, n > 0 ? n : 1), 256) * 256;
+  return C < N ? C : N;
+}
+
 TokLayout tok_layout(int64_t N, int64_t d, int64_t V, bool with_z, bool with_grad, bool dW_bf16, const lce_opts* o) {
   TokLayout T;
   Layout& L = T.base;
-  L.C = chunk_of(N, o);
+  L.C = tok_chunk(N, o);
   L.T = ceil_div(V, kVocabTile);
   L.ldp = L.T * kVocabTile;
   L.chunks = N > 0 ? ceil_div(N, L.C) : 0;
@@ -1143,10 +1153,11 @@ int lce_logprobs(const void* H, const void* W, const int64_t* y, int64_t N, int6
   const TokLayout T = tok_layout(N, d, V, top_k > 0 && !logits, false, false, &o);
   Call c;
   LCE_TRY(tok_begin(&c, T, H, W, y, N, d, V, o, ws, ws_bytes, stream));
-  LCE_TRY(prepare(c, nullptr));
+  if (lce::kChecks || N == 0) LCE_TRY(prepare(c, nullptr));
   for (int64_t c0 = 0; c0 < N; c0 += c.L.C) {
     const int64_t rows = (N - c0) < c.L.C ? (N - c0) : c.L.C;
-    const lce::TokParams p = tok_params(c, c0, rows, temperature);
+    lce::TokParams p = tok_params(c, c0, rows, temperature);
+    p.reset = !lce::kChecks && c0 == 0;
     float* Z = logits ? logits + c0 * T.ldz : top_k > 0 ? reinterpret_cast<float*>(c.ws + T.Z) : nullptr;
     LCE_TRY(tok_logits(c, c0, rows, Z ? lce::TOK_STATS_Z : lce::TOK_STATS, Z, T.ldz, p));
     lce::TokScoreArgs a;
@@ -1203,7 +1214,7 @@ int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_
   const TokLayout T = tok_layout(N, d, V, false, true, dW_bf16, &o);
   Call c;
   LCE_TRY(tok_begin(&c, T, H, W, y, N, d, V, o, ws, ws_bytes, stream));
-  LCE_TRY(prepare(c, nullptr));
+  if (N == 0 || !logits) LCE_TRY(prepare(c, nullptr));  // with kept logits the gradient tile's launch does it
   if (N == 0) LCE_TRY(zero_dW(c, dW, dW_bf16));
   uint16_t* G = reinterpret_cast<uint16_t*>(c.ws + c.L.P);
   for (int64_t c0 = 0; c0 < N; c0 += c.L.C) {
@@ -1228,6 +1239,13 @@ int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_
       a.g_entropy = p.g_entropy;
       a.Z = logits + c0 * T.ldz;
       a.G = reinterpret_cast<__nv_bfloat16*>(G);
+      if (c0 == 0) {
+        a.st = c.st;
+        a.y_all = c.y;
+        a.N = N;
+        a.cnt = reinterpret_cast<int*>(c.ws + c.L.dh_cnt);
+        a.ncnt = c.L.dh_ncnt;
+      }
       LCE_TRY(timed(c.s, K_COMBINE, 6.0 * static_cast<double>(rows) * static_cast<double>(V),
                     [&] { return cuda_rc(lce::launch_score_grad(a, p.rows, c.s)); }));
     } else {
@@ -1294,6 +1312,9 @@ int distill(const void* H, const void* W, const int64_t* idx, const void* t, int
     a.Z = Z;
     a.G = with_grad ? reinterpret_cast<__nv_bfloat16*>(c.ws + c.L.P) : nullptr;
     a.row_loss = row_loss + c0;
+    a.all_rows = row_loss;
+    a.N = N;
+    a.loss = loss;
     a.grad_loss = grad_loss;
     a.st = c.st;
     const double bytes = static_cast<double>(rows) * (32.0 * static_cast<double>(c.L.T) + 12.0 * K +
@@ -1302,7 +1323,7 @@ int distill(const void* H, const void* W, const int64_t* idx, const void* t, int
                   [&] { return cuda_rc(lce::launch_distill_row(a, static_cast<int>(rows), c.s)); }));
     if (with_grad) LCE_TRY(tok_grads(c, T, c0, rows, dH, dW, dW_bf16));
   }
-  LCE_TRY(finalize(c, row_loss, loss));
+  if (N == 0) LCE_TRY(finalize(c, row_loss, loss));
   return finish(c);
 }
 

@@ -69,7 +69,7 @@ __device__ __forceinline__ bool in_bounds(long long i, long long n, int* flags) 
 // Device-side status block at the start of the workspace.
 struct DevStatus {
   int flags;              // kFlag* bits
-  int pad0;
+  int rows_done;          // distillation: rows whose loss is written
   long long n_valid;      // denominator n actually used (count or override)
   long long n_counted;    // valid labels counted in this call
   float gscale;           // g / n (mean), g (sum); 0 when n == 0 under mean
@@ -246,6 +246,7 @@ struct TokParams {
   const float* g_logp;   // [rows] upstream gradients
   const float* g_entropy;  // [rows] or null
   int* flags;
+  int reset;             // the first block clears *flags (the call's first launch; k_score reports bad labels)
 };
 
 struct TokScoreArgs {
@@ -277,6 +278,13 @@ struct ScoreGradArgs {
   const float* g_entropy;  // or null
   const float* Z;        // [rows, ldz] logits of the forward
   __nv_bfloat16* G;      // [rows, ldg]
+  // first chunk only (st not null): the status block for N labels y_all and upstream factors of
+  // one, and the dH part counters cnt[0, ncnt) cleared
+  DevStatus* st;
+  const int64_t* y_all;
+  long long N;
+  int* cnt;
+  int ncnt;
 };
 
 struct DistillArgs {
@@ -292,6 +300,9 @@ struct DistillArgs {
   __nv_bfloat16* G;      // [rows, ldg] gradient tile, or null (loss only)
   float* row_loss;       // [rows]
   const float* grad_loss;
+  const float* all_rows;  // [N] row_loss of the whole call; the row finished last sums it into loss
+  long long N;
+  float* loss;
   DevStatus* st;
 };
 

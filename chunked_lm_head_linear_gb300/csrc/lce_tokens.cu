@@ -73,6 +73,13 @@ __device__ __forceinline__ float grad_entry(float z, float inv_t, float lse, flo
   return label ? __fadd_rn(g, a) : g;
 }
 
+// The first launch of a call clears the status word from its first block, before anything can have
+// been reported: a wait that gives up does so after two seconds, a bad label is reported by a later
+// kernel. (The checked build, whose blocks may report an index at once, clears it by a launch.)
+__device__ __forceinline__ void reset_flags(const TokParams& p) {
+  if (p.reset && blockIdx.x == 0 && threadIdx.x == 32 * EPI_WARP0) *p.flags = 0;
+}
+
 template <int MODE>
 struct TokEpi {
   using Params = TokParams;
@@ -226,7 +233,7 @@ struct TokProb {
   static __device__ __forceinline__ uint64_t a_desc(int, uint32_t addr, int k) { return desc_k_major(addr, k); }
   static __device__ __forceinline__ uint64_t b_desc(int, uint32_t addr, int k) { return desc_k_major(addr, k); }
   static __device__ __forceinline__ uint32_t idesc(int) { return idesc_bf16_f32(P_TILE_M, BN, false, false); }
-  static __device__ __forceinline__ void init(const Params&, State&) {}
+  static __device__ __forceinline__ void init(const Params& p, State&) { reset_flags(p.ep); }
   static __device__ __forceinline__ void epilogue(const Params& p, State&, const TileJob&, EpiCtx ctx, int m0,
                                                   int col0, uint32_t taddr) {
     ctx.out = &p.c;
@@ -434,6 +441,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_rows_logits(const __grid_con
     const float k = e.inv_t * kLog2e;
     int acc = 0;
     uint32_t acc_phase = 0;
+    reset_flags(e);
     for (int t = blockIdx.x; t < p.tiles; t += gridDim.x) {
       // The four warps agree on whether the tile came (a wait that ran out in one ends the loop of
       // all, so that none is left at the barrier below); everyone has read the tile before by then.
@@ -722,6 +730,7 @@ __global__ void __launch_bounds__(32 * WARPS) k_score(const TokScoreArgs p) {
     if (p.entropy != nullptr) p.entropy[r] = logs - acc.t / acc.s;
     const long long y = p.y[r];
     const bool given = y != p.ignore_index && y >= 0 && y < p.V;
+    if (!given && y != p.ignore_index) atomicOr(p.flags, kFlagLabelRange);
     float lp = 0.f;
     if (given) lp = ((p.Z != nullptr ? z[y] : p.ztgt[r]) - acc.m) * p.inv_t - logs;
     p.logp[r] = lp;
@@ -766,6 +775,20 @@ __global__ void __launch_bounds__(kRowThreads) k_score_grad(const ScoreGradArgs 
   grid_dep_wait();
   grid_dep_launch();
   const int r = blockIdx.x, tid = threadIdx.x;
+  if (r == 0 && p.st != nullptr) {  // what the label scan would do, without a launch of its own
+    for (int i = tid; i < p.ncnt; i += kRowThreads) p.cnt[i] = 0;
+    int bad = 0;
+    for (long long i = tid; i < p.N; i += kRowThreads) {
+      const long long v = p.y_all[i];
+      bad |= v != p.ignore_index && (v < 0 || v >= p.V);
+    }
+    bad = __syncthreads_or(bad);
+    if (tid == 0) {
+      p.st->flags = bad ? kFlagLabelRange : 0;
+      p.st->gscale = 1.f;
+      p.st->lscale = 1.0;
+    }
+  }
   const float* z = p.Z + static_cast<long long>(r) * p.ldz;
   __nv_bfloat16* g = p.G + static_cast<long long>(r) * p.ldg;
   const long long y = p.y[r];
@@ -799,14 +822,11 @@ __device__ __forceinline__ float teacher_value(const void* t, int bf16, long lon
   return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(t)[i]) : static_cast<const float*>(t)[i];
 }
 
-// Clears the status block and the dH part counters; the row count of
-// k_distill_count adds into it.
-__global__ void __launch_bounds__(1024) k_distill_init(DevStatus* st, int* cnt, int ncnt) {
-  grid_dep_wait();
-  grid_dep_launch();
+__device__ __forceinline__ void clear_status(DevStatus* st, int* cnt, int ncnt) {
   for (int i = threadIdx.x; i < ncnt; i += blockDim.x) cnt[i] = 0;
   if (threadIdx.x == 0) {
     st->flags = 0;
+    st->rows_done = 0;
     st->n_valid = 0;
     st->n_counted = 0;
     st->gscale = 0.f;
@@ -814,16 +834,25 @@ __global__ void __launch_bounds__(1024) k_distill_init(DevStatus* st, int* cnt, 
   }
 }
 
+// Clears the status block and the dH part counters; k_distill_count adds into them.
+__global__ void __launch_bounds__(1024) k_distill_init(DevStatus* st, int* cnt, int ncnt) {
+  grid_dep_wait();
+  grid_dep_launch();
+  clear_status(st, cnt, ncnt);
+}
+
 // Rows with at least one kept entry (an index in [0, V) whose teacher value is
 // above -inf), and the range bit for an index that is neither kept nor
 // ignore_index. One warp per row; the count is a sum of whole numbers, so the
-// order of the atomics does not change it.
-__global__ void __launch_bounds__(256) k_distill_count(const int64_t* __restrict__ idx, const void* __restrict__ tv,
-                                                       int t_bf16, long long N, int K, int V, long long ignore_index,
-                                                       DevStatus* st) {
+// order of the atomics does not change it. A single block also clears what it
+// adds into.
+__global__ void __launch_bounds__(1024) k_distill_count(const int64_t* __restrict__ idx, const void* __restrict__ tv,
+                                                        int t_bf16, long long N, int K, int V, long long ignore_index,
+                                                        DevStatus* st, int* cnt, int ncnt) {
   grid_dep_wait();
   grid_dep_launch();
   __shared__ int s_cnt, s_bad;
+  if (gridDim.x == 1) clear_status(st, cnt, ncnt);
   if (threadIdx.x == 0) s_cnt = s_bad = 0;
   __syncthreads();
   const int lane = threadIdx.x & 31;
@@ -870,6 +899,31 @@ __device__ __forceinline__ float block_max(float v, float* red) {
   return s;
 }
 
+// Writes the row's loss; the block that counts the call's last row sums them
+// all in fp64, in an order that does not depend on which block that is.
+__device__ __forceinline__ void finish_row(const DistillArgs& p, int r, float loss, double weight) {
+  __shared__ int s_last;
+  __shared__ double s_sum[kRowThreads];
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    p.row_loss[r] = loss;
+    __threadfence();
+    s_last = atomicAdd(&p.st->rows_done, 1) == static_cast<int>(p.N - 1);
+  }
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  double sum = 0.0;
+  for (long long i = tid; i < p.N; i += kRowThreads) sum += static_cast<double>(__ldcg(p.all_rows + i));
+  s_sum[tid] = sum;
+  __syncthreads();
+  for (int w = kRowThreads / 2; w > 0; w >>= 1) {
+    if (tid < w) s_sum[tid] += s_sum[tid + w];
+    __syncthreads();
+  }
+  if (tid == 0) *p.loss = static_cast<float>(s_sum[0] * weight);
+}
+
 // One block per row of the chunk. The row's triples give lse; the K entries
 // give the teacher's probabilities q and the row's loss
 //   T^2 sum_k q_k (log q_k - z'_k + lse);
@@ -891,14 +945,13 @@ __global__ void __launch_bounds__(kRowThreads) k_distill_row(const DistillArgs p
   const float* z = p.Z + static_cast<long long>(r) * p.ldz;
   __nv_bfloat16* g = GRAD ? p.G + static_cast<long long>(r) * p.ldg : nullptr;
 
-  // the chunk's first row sets the scales: n is known since the count ran
+  // n is known since the count ran; the first row of a chunk sets the GEMMs' scale
+  const long long n = p.n_override >= 0 ? p.n_override : p.st->n_counted;
+  const double weight = p.mean ? (n > 0 ? 1.0 / static_cast<double>(n) : 0.0) : 1.0;
   if (r == 0 && tid == 0) {
-    const long long n = p.n_override >= 0 ? p.n_override : p.st->n_counted;
-    const double w = p.mean ? (n > 0 ? 1.0 / static_cast<double>(n) : 0.0) : 1.0;
     const float up = p.grad_loss != nullptr ? *p.grad_loss : 1.f;
     p.st->n_valid = n;
-    p.st->lscale = w;
-    p.st->gscale = static_cast<float>(static_cast<double>(up) * w / static_cast<double>(p.inv_t));
+    p.st->gscale = static_cast<float>(static_cast<double>(up) * weight / static_cast<double>(p.inv_t));
   }
 
   // the teacher's entry of this thread
@@ -914,7 +967,7 @@ __global__ void __launch_bounds__(kRowThreads) k_distill_row(const DistillArgs p
   }
   const bool kept = __syncthreads_or(vi >= 0) != 0;
   if (!kept) {  // nothing of the teacher in this row: no loss, a zero gradient
-    if (tid == 0) p.row_loss[r] = 0.f;
+    finish_row(p, r, 0.f, weight);
     if (GRAD)
       for (int c = tid * 8; c < p.V; c += kRowThreads * 8) *reinterpret_cast<uint4*>(g + c) = make_uint4(0, 0, 0, 0);
     return;
@@ -958,7 +1011,7 @@ __global__ void __launch_bounds__(kRowThreads) k_distill_row(const DistillArgs p
     if (q > 0.f || q != q) term = q * (logq - (zk - acc.m) * p.inv_t + logs);
   }
   const float loss = block_sum(term, red);
-  if (tid == 0) p.row_loss[r] = loss / (p.inv_t * p.inv_t);
+  finish_row(p, r, loss / (p.inv_t * p.inv_t), weight);
   if (!GRAD) return;
 
   const float k = p.inv_t * kLog2e, w = mass / acc.s;
@@ -1037,11 +1090,13 @@ cudaError_t launch_score_grad(const ScoreGradArgs& p, int rows, cudaStream_t s) 
 cudaError_t launch_distill_count(const int64_t* idx, const void* t, int t_bf16, long long N, int K, int V,
                                  long long ignore_index, DevStatus* st, int* cnt, int ncnt, int num_sms,
                                  cudaStream_t s) {
+  // up to 32 rounds of one block cost less than a second launch
+  if (N <= 32 * 32) return launch_k(k_distill_count, 1, 1024, 0, s, idx, t, t_bf16, N, K, V, ignore_index, st, cnt, ncnt);
   const cudaError_t e = launch_k(k_distill_init, 1, 1024, 0, s, st, cnt, ncnt);
-  if (e != cudaSuccess || N <= 0) return e;
-  const long long want = (N + 7) / 8;
-  const int grid = static_cast<int>(want < 4ll * num_sms ? want : 4ll * num_sms);
-  return launch_k(k_distill_count, grid, 256, 0, s, idx, t, t_bf16, N, K, V, ignore_index, st);
+  if (e != cudaSuccess) return e;
+  const long long want = (N + 31) / 32;
+  const int grid = static_cast<int>(want < num_sms ? want : num_sms);
+  return launch_k(k_distill_count, grid, 1024, 0, s, idx, t, t_bf16, N, K, V, ignore_index, st, cnt, ncnt);
 }
 
 cudaError_t launch_distill_row(const DistillArgs& p, int rows, cudaStream_t s) {

@@ -209,13 +209,15 @@ def workspace_size(op: int, N: int, d: int, V: int, opts: LceOpts | None = None)
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    # the current stream's handle, without the Stream object (3 us a call) around it
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _check_inputs(H, W, y):
@@ -793,7 +795,7 @@ def lce_logprobs(H, W, y, *, top_k: int = 0, temperature: float = 1.0, entropy: 
     N, d, V = _check_inputs(H, W, y)
     K, dev = int(top_k), H.device
     if logits is not None:
-        _check_dev(logits, "logits", torch.float32, shape=(N, lce_logits_stride(V)), device=dev)
+        _check_dev(logits, "logits", torch.float32, shape=(N, (V + 255) // 256 * 256), device=dev)
     opts, ws = _token_plan(opt_kw, N, "lce_logprobs", dev, workspace,
                            lambda o: lce_logprobs_workspace_size(N, d, V, K if logits is None else 0, o))
     logp = torch.empty(N, dtype=torch.float32, device=dev)
@@ -828,7 +830,7 @@ def lce_logprobs_backward(H, W, y, lse, entropy, g_logp, g_entropy=None, *, temp
     for name, t in (("lse", lse), ("entropy", entropy), ("g_logp", g_logp), ("g_entropy", g_entropy)):
         _check_dev(t, name, torch.float32, shape=(N,), device=H.device)
     if logits is not None:
-        _check_dev(logits, "logits", torch.float32, shape=(N, lce_logits_stride(V)), device=H.device)
+        _check_dev(logits, "logits", torch.float32, shape=(N, (V + 255) // 256 * 256), device=H.device)
     grads = _dW_mode(dW_dtype)
     opts, ws = _token_plan(opt_kw, N, "lce_logprobs_backward", H.device, workspace,
                            lambda o: lce_logprobs_backward_workspace_size(N, d, V, grads, o))

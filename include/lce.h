@@ -303,7 +303,8 @@ int lce_scale_grads(void* dH, float* dW, int64_t N, int64_t d, int64_t V, const 
  * cross-entropy. z = H W^T as above, z' = z / temperature (> 0, finite), p =
  * softmax(z'). H, W, y, dH, dW, opts, ws and stream are those of the calls
  * above; the logits of one chunk at a time are held in the workspace, never
- * [N, V]. opts->reserved must be 0.
+ * [N, V] (chunk_tokens = 0: equal chunks of about 4096 tokens, fewer than 6144).
+ * opts->reserved must be 0.
  *
  * lce_logprobs, per row i (device outputs):
  *   lse [N]      log sum_v exp(z'_iv)

@@ -236,3 +236,11 @@ def test_binding_refuses_cpu_tensors_and_bad_modes():
         lce._distill_mode(0, False, 2.0)
     with pytest.raises(ValueError, match="dW_dtype"):
         lce._dW_mode(torch.float16)
+
+
+def test_token_chunks_are_equal_by_default():
+    """chunk_tokens = 0: the workspace of equal chunks of about 4096 tokens in whole tiles, one chunk below 6144."""
+    size = lambda n, c: lce.lce_logprobs_workspace_size(n, 64, 1000, 1, lce.make_opts(chunk_tokens=c))  # noqa: E731
+    for n, chunk in ((1, 1), (300, 300), (4096, 4096), (5000, 5000), (6143, 6143), (7000, 3584), (8192, 4096),
+                     (10000, 5120), (100000, 4352)):
+        assert size(n, 0) == size(n, chunk), n
