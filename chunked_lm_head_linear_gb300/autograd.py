@@ -98,9 +98,10 @@ class _LogProbs(torch.autograd.Function):
         H, W, y, lse, entropy, logits = ctx.saved_tensors
         g_logp = torch.zeros_like(lse) if g_logp is None else g_logp.contiguous()
         g_entropy = None if g_entropy is None else g_entropy.contiguous()
-        dH, dW = lce.lce_logprobs_backward(H, W, y, lse, entropy, g_logp, g_entropy, temperature=ctx.temperature,
-                                           logits=logits, dW_dtype=W.dtype, need_dH=ctx.needs_input_grad[0],
-                                           need_dW=ctx.needs_input_grad[1], **ctx.opts)
+        # the forward checked its tensors, autograd that the gradients are like the outputs
+        dH, dW = lce._logprobs_backward(H, W, y, lse, entropy, g_logp, g_entropy, logits, ctx.temperature,
+                                        lce.LCE_DW_BF16, None, ctx.needs_input_grad[0], ctx.needs_input_grad[1], None,
+                                        None, ctx.opts)
         return dH, dW, None, None, None, None
 
 

@@ -987,7 +987,7 @@ int lce_norm_fwd_bwd(const void* x, const float* w_norm, float eps, const void* 
 // ---------------------------------------------------------------------------
 namespace {
 
-// Workspace of one token operator: the chunk's triples, its fp32 logits (with_z), its gradient
+// Workspace of one token operator: the chunk's partial sums, its fp32 logits (with_z), its gradient
 // tile and the dH parts (with_grad).
 struct TokLayout {
   Layout base;         // status, ztgt, partials, P and the dH parts of the call record

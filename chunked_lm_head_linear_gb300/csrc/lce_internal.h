@@ -225,8 +225,8 @@ cudaError_t launch_finalize(const float* loss_i, long long N, const DevStatus* s
 // Token operators (lce_tokens.cu)
 // ----------------------------------------------------------------------------
 enum TokMode : int {
-  TOK_STATS = 0,    // triples of each (row, half tile) and the label's logit
-  TOK_STATS_Z = 1,  // the triples and the fp32 logits
+  TOK_STATS = 0,    // partial sums of each (row, half tile) and the label's logit
+  TOK_STATS_Z = 1,  // the partial sums and the fp32 logits
   TOK_GRAD = 2,     // gradient tile of log-probability and entropy
 };
 
@@ -235,11 +235,11 @@ constexpr int kMaxTop = 128;  // most alternatives of a row, most teacher entrie
 struct TokParams {
   int rows;              // rows of this chunk
   int V;
-  int nparts;            // triples per row: two per 256-column vocabulary tile
+  int nparts;            // partials per row: two per 256-column vocabulary tile
   float inv_t;           // 1 / temperature
   long long ignore_index;
   const int64_t* y;      // labels of this chunk (TOK_STATS, TOK_GRAD)
-  float4* partials;      // [rows, nparts] (m, s, t, unused)
+  float4* partials;      // [rows, nparts] (m, s, t, c), see lce_tokens.cu
   float* ztgt;           // [rows] logit of the label (TOK_STATS)
   const float* lse;      // [rows] (TOK_GRAD; the next three too)
   const float* entropy;  // [rows]

@@ -7,10 +7,14 @@
 //
 // Per row i, with z' = z / T:
 //   lse = log sum_v exp z'_v, logp = z'_y - lse, entropy = lse - sum_v p_v z'_v
-// The GEMM's epilogue keeps, per (row, 128 vocabulary columns), the triple
-//   m = max z,  s = sum exp((z - m)/T),  t = sum exp((z - m)/T) (z - m)/T
-// from which entropy = log S - T/S of the merged triple: no difference of two
-// large numbers, and one exponential per logit for both quantities.
+// The GEMM's epilogue keeps, per (row, 128 vocabulary columns), four numbers
+//   m = max z,  c = how many logits equal it,
+//   s = sum exp((z - m)/T) over the others,  t = sum exp((z - m)/T) (z - m)/T
+// from which, merged over the row, log-sum-exp = m/T + log c + log1p(s/c) and
+// entropy = log c + log1p(s/c) - t/(c + s): one exponential per logit for both,
+// no difference of two large numbers, and because the terms that are 1 exactly
+// are counted apart, a log-probability near 0 (a confident model's token) keeps
+// its relative precision instead of the 2^-24 of a sum near 1.
 #include <math.h>
 
 #include "lce_gemm.cuh"
@@ -23,40 +27,62 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFloor = -1.0e30f;  // stands in for -inf where it is multiplied by a zero probability
 
 // ----------------------------------------------------------------------------
-// Merging the triples
+// A row's four numbers and their merge
 // ----------------------------------------------------------------------------
-struct Mst {
-  float m, s, t;
+// Merged under the row's maximum M, found first: a half tile below it moves its
+// c into s, s' = f (s + c) and t' = f (t + (s + c) (m - M)/T), f = exp((m - M)/T).
+struct RowSum {
+  float s, t, c;
 };
 
-// (m, s, t) of the union: both sides rescaled to the larger maximum M,
-// t' = f (t + s (m - M)/T). An empty side (s = 0) leaves the other as it is.
-__device__ __forceinline__ void merge_mst(Mst& a, const Mst& b, float inv_t) {
-  const float M = fmaxf(a.m, b.m);
-  const float k = inv_t * kLog2e;
-  const float da = a.m == M ? 0.f : a.m - M, db = b.m == M ? 0.f : b.m - M;
-  const float fa = exp2f(da * k), fb = exp2f(db * k);
-  a.t = fa * (a.t + a.s * fmaxf(da * inv_t, kFloor)) + fb * (b.t + b.s * fmaxf(db * inv_t, kFloor));
-  a.s = a.s * fa + b.s * fb;
-  a.m = M;
+__device__ __forceinline__ void add_partial(RowSum& a, const float4& q, float M, float inv_t) {
+  if (q.x == M) {
+    a.s += q.y;
+    a.t += q.z;
+    a.c += q.w;
+  } else {
+    const float d = (q.x - M) * inv_t, f = ex2_approx(d * kLog2e), all = q.y + q.w;
+    a.s = fmaf(all, f, a.s);
+    a.t = fmaf(fmaf(all, fmaxf(d, kFloor), q.z), f, a.t);
+  }
 }
 
-__device__ __forceinline__ Mst warp_merge_mst(Mst a, float inv_t) {
+__device__ __forceinline__ RowSum warp_add(RowSum a) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
-    Mst b;
-    b.m = __shfl_xor_sync(0xffffffffu, a.m, off);
-    b.s = __shfl_xor_sync(0xffffffffu, a.s, off);
-    b.t = __shfl_xor_sync(0xffffffffu, a.t, off);
-    merge_mst(a, b, inv_t);
+    a.s += __shfl_xor_sync(0xffffffffu, a.s, off);
+    a.t += __shfl_xor_sync(0xffffffffu, a.t, off);
+    a.c += __shfl_xor_sync(0xffffffffu, a.c, off);
   }
   return a;
 }
 
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+  return v;
+}
+
+constexpr int kGroups = 8;  // groups of 32 running sums a row is merged through
+
+__device__ __forceinline__ RowSum add_groups(const RowSum* g) {
+  RowSum a = g[0];
+#pragma unroll
+  for (int i = 1; i < kGroups; ++i) {
+    a.s += g[i].s;
+    a.t += g[i].t;
+    a.c += g[i].c;
+  }
+  return a;
+}
+
+// log of the sum of exp((z - M)/T): log(c + s).
+__device__ __forceinline__ float log_sum(const RowSum& a) { return logf(a.c) + log1pf(a.s / a.c); }
+
 // ----------------------------------------------------------------------------
 // Tile epilogue: an epilogue warp owns 32 rows x 128 columns, one thread a row.
-//   TOK_STATS    the triple of each (row, half tile) and the label's logit
-//   TOK_STATS_Z  the triple, and the fp32 logits themselves into the chunk's
+//   TOK_STATS    the four numbers of each (row, half tile) and the label's logit
+//   TOK_STATS_Z  the four numbers, and the fp32 logits themselves into the chunk's
 //                buffer (top alternatives and distillation read them again:
 //                4 bytes a logit, written behind a main loop of d/16 MMAs)
 //   TOK_GRAD     the gradient tile of (logp, entropy) in bf16, from the saved
@@ -91,7 +117,7 @@ struct TokEpi {
     const bool live = r < p.rows;
     const int vlim = p.V - col0;  // columns >= vlim are past the vocabulary (warp-uniform)
     const int part = col0 / EPI_COLS;
-    float m = -INFINITY, s = 0.f, t = 0.f, zt = 0.f;
+    float m = -INFINITY, s = 0.f, t = 0.f, cnt = 0.f, zt = 0.f;
     bool have_t = false;
     int ycol = -1;
     if (MODE == TOK_STATS && live) {
@@ -133,10 +159,11 @@ struct TokEpi {
 #pragma unroll
       for (int c = 1; c < 32; ++c) cm = fmaxf(cm, v[c]);
       if (cm > m) {
-        if (s > 0.f) {
+        if (cnt > 0.f) {
           const float f = ex2_approx((m - cm) * k);
-          t = f * (t + s * fmaxf((m - cm) * p.inv_t, kFloor));
-          s *= f;
+          t = f * (t + (s + cnt) * fmaxf((m - cm) * p.inv_t, kFloor));
+          s = (s + cnt) * f;
+          cnt = 0.f;
         }
         m = cm;
       }
@@ -146,14 +173,17 @@ struct TokEpi {
       for (int c = 0; c < 32; ++c) {
         const float dz = v[c] - mb;
         const float e = ex2_approx(dz * k);
-        s2 += e;
+        if (dz == 0.f)
+          cnt += 1.f;
+        else
+          s2 += e;
         t2 = fmaf(e, fmaxf(dz, kFloor), t2);
       }
       s += s2;
       t = fmaf(t2, p.inv_t, t);
     }
     if (!live || !in_bounds(part, p.nparts, p.flags)) return;
-    p.partials[static_cast<long long>(r) * p.nparts + part] = make_float4(m, s, t, 0.f);
+    p.partials[static_cast<long long>(r) * p.nparts + part] = make_float4(m, s, t, cnt);
     if (MODE == TOK_STATS && have_t) p.ztgt[r] = zt;
   }
 
@@ -275,9 +305,9 @@ cudaError_t launch_tok_mode(const CUtensorMap& a, const CUtensorMap& b, const CU
 // tiles would multiply at least 256 rows and leave fewer bytes in flight.
 //   warp 0      TMA producer, warp 1 MMA issuer, warp 2 TMEM
 //   warps 4-7   epilogue: TMEM lanes (vocabulary) into shared memory as
-//               [row][128], then a warp per row: 4 columns a lane, the triple
-//               by shuffles, the logits to memory in 512-byte runs
-// The triples and logits are laid out as the pair kernel's, and the kernels
+//               [row][128], then a warp per row: 4 columns a lane, the four
+//               numbers by shuffles, the logits to memory in 512-byte runs
+// The numbers and logits are laid out as the pair kernel's, and the kernels
 // behind do not know which ran.
 // ----------------------------------------------------------------------------
 template <int NT>
@@ -487,11 +517,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_rows_logits(const __grid_con
           for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
           const float mb = m == -INFINITY ? 0.f : m;
           float s = 0.f, tt = 0.f;
+          int cnt = 0;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const float dz = v[c] - mb;
             const float x = ex2_approx(dz * k);
-            s += x;
+            cnt += __popc(__ballot_sync(0xffffffffu, dz == 0.f));
+            s += dz == 0.f ? 0.f : x;
             tt = fmaf(x, fmaxf(dz, kFloor), tt);
           }
 #pragma unroll
@@ -500,7 +532,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_rows_logits(const __grid_con
             tt += __shfl_xor_sync(0xffffffffu, tt, off);
           }
           if (lane == 0 && in_bounds(t, e.nparts, e.flags))
-            e.partials[static_cast<long long>(n) * e.nparts + t] = make_float4(m, s, tt * e.inv_t, 0.f);
+            e.partials[static_cast<long long>(n) * e.nparts + t] = make_float4(m, s, tt * e.inv_t, static_cast<float>(cnt));
         }
       }
       if (++acc == 2) {
@@ -666,13 +698,13 @@ struct TopList {
   }
 };
 
-// The row's triples merged in a fixed order into lse, logp and entropy, and the
+// The row's partial sums merged in a fixed order into lse, logp and entropy, and the
 // top K alternatives. The K largest logits (ties to the lower index) lie in the
 // K half tiles with the largest maxima (ties to the lower tile): before a half
 // tile outside them come K others, each with an element before all of its own.
 // So only K x 128 of the row's logits are read again, and of those only the
 // ones that reach the K-th largest maximum are candidates.
-// One block of WARPS warps per row. The triples are merged in an order that
+// One block of WARPS warps per row. They are merged in an order that
 // does not depend on WARPS (256 running sums, t mod 256, then lanes, then the
 // eight groups of 32), so the results do not depend on how many rows a call or
 // a chunk has.
@@ -680,29 +712,28 @@ template <int KPL, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) k_score(const TokScoreArgs p) {
   grid_dep_wait();
   grid_dep_launch();
-  constexpr int kGroups = 8, kMine = kGroups / WARPS;    // groups of 32 running sums, and this warp's
-  constexpr int kBlocks = kMine >= 4 ? 1 : 4 / kMine;    // blocks of 256 triples whose loads are in flight together
+  constexpr int kMine = kGroups / WARPS;              // groups of this warp
+  constexpr int kBlocks = kMine >= 4 ? 1 : 4 / kMine;  // blocks of 256 partials whose loads are in flight together
   __shared__ Key s_list[WARPS][32 * KPL];
   __shared__ Key s_wait[WARPS][64];
-  __shared__ Mst s_mst[kGroups];
+  __shared__ RowSum s_sum[kGroups];
+  __shared__ float s_max[WARPS];
   const int lane = threadIdx.x & 31, warp = static_cast<int>(threadIdx.x >> 5);
   const int r = static_cast<int>(blockIdx.x);
   const float4* pr = p.partials + static_cast<long long>(r) * p.nparts;
   const int tiles = (p.V + EPI_COLS - 1) / EPI_COLS;  // half tiles that hold vocabulary columns
   const float* z = p.Z + static_cast<long long>(r) * p.ldz;
-  Mst sums[kMine];
-#pragma unroll
-  for (int i = 0; i < kMine; ++i) sums[i] = Mst{-INFINITY, 0.f, 0.f};
   TopList<KPL> top;
   top.clear(s_wait[warp]);
+  float M = -INFINITY;
   for (int t0 = warp * 32 + lane; t0 - lane < tiles; t0 += 32 * kGroups * kBlocks) {
-    float4 v[kBlocks][kMine];
+    float m[kBlocks][kMine];
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
         const int t = t0 + 32 * (b * kGroups + i * WARPS);
-        v[b][i] = t < tiles ? pr[t] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        m[b][i] = t < tiles ? pr[t].x : -INFINITY;
       }
     }
 #pragma unroll
@@ -710,29 +741,44 @@ __global__ void __launch_bounds__(32 * WARPS) k_score(const TokScoreArgs p) {
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
         const int t = t0 + 32 * (b * kGroups + i * WARPS);
-        merge_mst(sums[i], Mst{v[b][i].x, v[b][i].y, v[b][i].z}, p.inv_t);
-        if (p.K > 0) top.offer(t < tiles ? make_key(v[b][i].x, static_cast<uint32_t>(t)) : 0, p.K, lane);
+        M = fmaxf(M, m[b][i]);
+        if (p.K > 0) top.offer(t < tiles ? make_key(m[b][i], static_cast<uint32_t>(t)) : 0, p.K, lane);
       }
+    }
+  }
+  M = warp_max(M);
+  if (WARPS > 1) {
+    if (lane == 0) s_max[warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) M = fmaxf(M, s_max[i]);
+  }
+  RowSum sums[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) sums[i] = RowSum{0.f, 0.f, 0.f};
+  for (int t0 = warp * 32 + lane; t0 - lane < tiles; t0 += 32 * kGroups) {
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int t = t0 + 32 * i * WARPS;
+      if (t < tiles) add_partial(sums[i], pr[t], M, p.inv_t);
     }
   }
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
-    sums[i] = warp_merge_mst(sums[i], p.inv_t);
-    if (lane == 0) s_mst[warp + i * WARPS] = sums[i];
+    sums[i] = warp_add(sums[i]);
+    if (lane == 0) s_sum[warp + i * WARPS] = sums[i];
   }
   __syncthreads();
-  Mst acc = s_mst[0];
-#pragma unroll
-  for (int i = 1; i < kGroups; ++i) merge_mst(acc, s_mst[i], p.inv_t);
-  const float logs = logf(acc.s);
+  const RowSum acc = add_groups(s_sum);
+  const float logs = log_sum(acc);
   if (threadIdx.x == 0) {
-    p.lse[r] = fmaf(acc.m, p.inv_t, logs);
-    if (p.entropy != nullptr) p.entropy[r] = logs - acc.t / acc.s;
+    p.lse[r] = fmaf(M, p.inv_t, logs);
+    if (p.entropy != nullptr) p.entropy[r] = logs - acc.t / (acc.c + acc.s);
     const long long y = p.y[r];
     const bool given = y != p.ignore_index && y >= 0 && y < p.V;
     if (!given && y != p.ignore_index) atomicOr(p.flags, kFlagLabelRange);
     float lp = 0.f;
-    if (given) lp = ((p.Z != nullptr ? z[y] : p.ztgt[r]) - acc.m) * p.inv_t - logs;
+    if (given) lp = ((p.Z != nullptr ? z[y] : p.ztgt[r]) - M) * p.inv_t - logs;
     p.logp[r] = lp;
   }
   if (p.K == 0) return;
@@ -758,7 +804,7 @@ __global__ void __launch_bounds__(32 * WARPS) k_score(const TokScoreArgs p) {
     const int i = 32 * j + lane;
     if (i < p.K) {
       const long long at = static_cast<long long>(r) * p.K + i;
-      p.top_logp[at] = (key_value(best.slot[j]) - acc.m) * p.inv_t - logs;
+      p.top_logp[at] = (key_value(best.slot[j]) - M) * p.inv_t - logs;
       const uint32_t v = key_index(best.slot[j]);  // past V only if a row of NaN left the list short
       p.top_idx[at] = v < static_cast<uint32_t>(p.V) ? v : static_cast<uint32_t>(p.V - 1);
     }
@@ -769,9 +815,9 @@ __global__ void __launch_bounds__(32 * WARPS) k_score(const TokScoreArgs p) {
 // over the row, 4 bytes read and 2 written a logit, in place of the logits
 // GEMM (2 d flops a logit). One block per row; a row whose upstream gradients
 // are zero is written without reading its logits.
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 32 * kGroups;
 
-__global__ void __launch_bounds__(kRowThreads) k_score_grad(const ScoreGradArgs p) {
+__global__ void __launch_bounds__(kRowThreads, 8) k_score_grad(const ScoreGradArgs p) {
   grid_dep_wait();
   grid_dep_launch();
   const int r = blockIdx.x, tid = threadIdx.x;
@@ -924,7 +970,7 @@ __device__ __forceinline__ void finish_row(const DistillArgs& p, int r, float lo
   if (tid == 0) *p.loss = static_cast<float>(s_sum[0] * weight);
 }
 
-// One block per row of the chunk. The row's triples give lse; the K entries
+// One block per row of the chunk. The row's partial sums give lse; the K entries
 // give the teacher's probabilities q and the row's loss
 //   T^2 sum_k q_k (log q_k - z'_k + lse);
 // with GRAD the row of the gradient tile is written in one pass over the
@@ -934,11 +980,11 @@ __device__ __forceinline__ void finish_row(const DistillArgs& p, int r, float lo
 // it). The kept entries are written last, by one thread each: of entries with
 // the same index the first writes, with the sum of their q.
 template <bool GRAD>
-__global__ void __launch_bounds__(kRowThreads) k_distill_row(const DistillArgs p) {
+__global__ void __launch_bounds__(kRowThreads, 8) k_distill_row(const DistillArgs p) {
   grid_dep_wait();
   grid_dep_launch();
   __shared__ float red[kRowThreads / 32];
-  __shared__ Mst s_mst[kRowThreads / 32];
+  __shared__ RowSum s_sum[kGroups];
   __shared__ int s_idx[kMaxTop];
   __shared__ float s_q[kMaxTop];
   const int r = blockIdx.x, tid = threadIdx.x;
@@ -987,43 +1033,42 @@ __global__ void __launch_bounds__(kRowThreads) k_distill_row(const DistillArgs p
   }
   const float mass = block_sum(q, red);
 
-  Mst acc{-INFINITY, 0.f, 0.f};
   const float4* pr = p.partials + static_cast<long long>(r) * p.nparts;
   const int tiles = (p.V + EPI_COLS - 1) / EPI_COLS;
-  for (int t = tid; t < tiles; t += kRowThreads) {
-    const float4 v = pr[t];
-    merge_mst(acc, Mst{v.x, v.y, v.z}, p.inv_t);
-  }
-  acc = warp_merge_mst(acc, p.inv_t);
-  if ((tid & 31) == 0) s_mst[tid >> 5] = acc;
+  float M = -INFINITY;
+  for (int t = tid; t < tiles; t += kRowThreads) M = fmaxf(M, pr[t].x);
+  M = block_max(M, red);
+  RowSum acc{0.f, 0.f, 0.f};
+  for (int t = tid; t < tiles; t += kRowThreads) add_partial(acc, pr[t], M, p.inv_t);
+  acc = warp_add(acc);
+  if ((tid & 31) == 0) s_sum[tid >> 5] = acc;
   if (tid < kMaxTop) {
     s_idx[tid] = vi;
     s_q[tid] = q;
   }
   __syncthreads();
-  acc = s_mst[0];
-  for (int i = 1; i < kRowThreads / 32; ++i) merge_mst(acc, s_mst[i], p.inv_t);
-  const float logs = logf(acc.s);
+  acc = add_groups(s_sum);
+  const float logs = log_sum(acc);
 
   float zk = 0.f, term = 0.f;
   if (vi >= 0) {
     zk = z[vi];
-    if (q > 0.f || q != q) term = q * (logq - (zk - acc.m) * p.inv_t + logs);
+    if (q > 0.f || q != q) term = q * (logq - (zk - M) * p.inv_t + logs);
   }
   const float loss = block_sum(term, red);
   finish_row(p, r, loss / (p.inv_t * p.inv_t), weight);
   if (!GRAD) return;
 
-  const float k = p.inv_t * kLog2e, w = mass / acc.s;
+  const float k = p.inv_t * kLog2e, w = mass / (acc.c + acc.s);
   for (int c = tid * 8; c < p.V; c += kRowThreads * 8) {
     // columns past V (up to 7) lie inside the row's padding: never read by the GEMMs
     const float4 a = __ldcs(reinterpret_cast<const float4*>(z + c));
     const float4 b = __ldcs(reinterpret_cast<const float4*>(z + c + 4));
     uint4 o;
-    o.x = pack_bf16x2(w * ex2_approx((a.x - acc.m) * k), w * ex2_approx((a.y - acc.m) * k));
-    o.y = pack_bf16x2(w * ex2_approx((a.z - acc.m) * k), w * ex2_approx((a.w - acc.m) * k));
-    o.z = pack_bf16x2(w * ex2_approx((b.x - acc.m) * k), w * ex2_approx((b.y - acc.m) * k));
-    o.w = pack_bf16x2(w * ex2_approx((b.z - acc.m) * k), w * ex2_approx((b.w - acc.m) * k));
+    o.x = pack_bf16x2(w * ex2_approx((a.x - M) * k), w * ex2_approx((a.y - M) * k));
+    o.y = pack_bf16x2(w * ex2_approx((a.z - M) * k), w * ex2_approx((a.w - M) * k));
+    o.z = pack_bf16x2(w * ex2_approx((b.x - M) * k), w * ex2_approx((b.y - M) * k));
+    o.w = pack_bf16x2(w * ex2_approx((b.z - M) * k), w * ex2_approx((b.w - M) * k));
     *reinterpret_cast<uint4*>(g + c) = o;
   }
   __syncthreads();
@@ -1035,7 +1080,7 @@ __global__ void __launch_bounds__(kRowThreads) k_distill_row(const DistillArgs p
       if (j < tid) first = false;
       sum += s_q[j];
     }
-    if (first) g[vi] = __float2bfloat16_rn(w * ex2_approx((zk - acc.m) * k) - sum);
+    if (first) g[vi] = __float2bfloat16_rn(w * ex2_approx((zk - M) * k) - sum);
   }
 }
 
@@ -1070,16 +1115,14 @@ cudaError_t launch_score_warps(const TokScoreArgs& p, cudaStream_t s) {
 }
 
 // Warps of a row's block: with few rows the row's own latency counts, with
-// many the GPU is full and every further warp is one more list to merge. At V
-// = 151936 and K = 20, microseconds with 8 / 2 / 1 warps: 32 rows 12.5 / 19.1 /
-// 26.0, 512 rows 20.3 / 24.8 / 32.9, 2048 rows 52.2 / 32.9 / 39.4, 4096 rows
-// 92.5 / 56.9 / 47.4.
-constexpr int kScoreRows8 = 512, kScoreRows2 = 2048;
+// many the GPU is full and every further warp is one more list to merge
+// (microseconds at V = 151936 and K = 20 with 8 / 2 warps: 32 rows
+// 12 / 18, 512 rows 20 / 24, 1024 rows 29 / 29, 4096 rows 82 / 59).
+constexpr int kScoreRows8 = 512;
 
 cudaError_t launch_score(const TokScoreArgs& p, cudaStream_t s) {
   if (p.rows <= 0) return cudaSuccess;
-  if (p.rows <= kScoreRows8) return launch_score_warps<8>(p, s);
-  return p.rows <= kScoreRows2 ? launch_score_warps<2>(p, s) : launch_score_warps<1>(p, s);
+  return p.rows <= kScoreRows8 ? launch_score_warps<8>(p, s) : launch_score_warps<2>(p, s);
 }
 
 cudaError_t launch_score_grad(const ScoreGradArgs& p, int rows, cudaStream_t s) {

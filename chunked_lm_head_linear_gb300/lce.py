@@ -831,7 +831,15 @@ def lce_logprobs_backward(H, W, y, lse, entropy, g_logp, g_entropy=None, *, temp
         _check_dev(t, name, torch.float32, shape=(N,), device=H.device)
     if logits is not None:
         _check_dev(logits, "logits", torch.float32, shape=(N, (V + 255) // 256 * 256), device=H.device)
-    grads = _dW_mode(dW_dtype)
+    return _logprobs_backward(H, W, y, lse, entropy, g_logp, g_entropy, logits, temperature, _dW_mode(dW_dtype), dW,
+                              need_dH, need_dW, workspace, stream, opt_kw)
+
+
+def _logprobs_backward(H, W, y, lse, entropy, g_logp, g_entropy, logits, temperature, grads, dW, need_dH, need_dW,
+                       workspace, stream, opt_kw):
+    """lce_logprobs_backward on tensors that are known to fit each other (those
+    of a forward that checked them)."""
+    (N, d), V = H.shape, W.shape[0]
     opts, ws = _token_plan(opt_kw, N, "lce_logprobs_backward", H.device, workspace,
                            lambda o: lce_logprobs_backward_workspace_size(N, d, V, grads, o))
     dH, dW = _token_grads(H, V, d, opts, grads, dW, need_dH, need_dW)

@@ -161,6 +161,31 @@ def test_logprobs_far_logits(cuda_lib, N):
     check_scores(cuda_lib.lce_logprobs(Ht, Wt, dev(y), top_k=12), H, W, y, 1.0, 12)
 
 
+@pytest.mark.parametrize("N", [3, 200])
+def test_logprobs_near_zero_keep_their_relative_precision(cuda_lib, N):
+    """A confident row: logp = -log1p(s) with s down to e^-30. Each term of s errs by 2^-22 and by its
+    argument's rounding, 2 eps |z' - m| < 2^-17; the sum and log1p by far less: below 2^-16 relative."""
+    V, d, label = 5000, 64, 1234
+    W = np.zeros((V, d))
+    W[:, 0] = -1.0
+    W[label, 0] = 0.0
+    W[:, 1] = np.random.default_rng(5).integers(-8, 9, V) / 64
+    H = np.zeros((N, d))
+    H[:, 0] = 20 + np.arange(N) % 11      # the label's lead over the others, in nats
+    H[:, 1] = 1.0
+    y = np.full(N, label)
+    Ht, Wt = heads(H, W)
+    logp, _, ent, tl, ti = cuda_lib.lce_logprobs(Ht, Wt, dev(y), top_k=1)
+    ref = oracle.logprobs_f64(H, W, y, top_k=1)
+    z = H @ W.T
+    exact = -np.log1p(np.exp(np.delete(z, label, axis=1) - z[:, [label]]).sum(axis=1))
+    assert exact.max() < 0 and exact.min() > -1e-4 and (ti.cpu().numpy() == label).all()
+    close(logp, exact, 2.0 ** -16 * np.abs(exact), "logp")
+    close(tl[:, 0], exact, 2.0 ** -16 * np.abs(exact), "top_logp")
+    # entropy = log1p(s) - t / (1 + s), two positive parts
+    close(ent, ref["entropy"], 2.0 ** -15 * np.abs(ref["entropy"]) + 1e-12, "entropy")
+
+
 @pytest.mark.parametrize("N", [4, 300])
 def test_logprobs_rows_with_nan_and_inf_leave_the_others_alone(cuda_lib, N):
     torch = _torch()
