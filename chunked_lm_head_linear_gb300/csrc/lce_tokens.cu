@@ -298,30 +298,40 @@ cudaError_t launch_tok_mode(const CUtensorMap& a, const CUtensorMap& b, const CU
 
 // ----------------------------------------------------------------------------
 // Few rows (decoding): the logits are one pass over W, bound by reading it, so
-// the operands change sides. A tile is 128 vocabulary rows of W (the MMA's M,
-// each read once, by one CTA) by all rows of H (its N, 32, 64 or 96, zero-filled
-// by TMA beyond the last), accumulated over d in TMEM; the ring of W blocks
-// keeps 112 to 160 KB a SM on their way from HBM. The pair kernel's 256-row
-// tiles would multiply at least 256 rows and leave fewer bytes in flight.
+// the operands change sides. A tile is 128 MT vocabulary rows of W (the MMA's
+// M, each read once, by one CTA) by all rows of H (its N = NT, zero-filled by
+// TMA beyond the last), accumulated over d in TMEM; the ring of W blocks keeps
+// 112 to 160 KB a SM on their way from HBM. The pair kernel's 256-row tiles
+// would multiply 256 rows whatever their number and leave fewer bytes in
+// flight: 7 rows of d = 7168 and V = 151655 took 517 us with it, 327 us here,
+// 6.6 TB/s; from 97 rows on it is level or ahead (128 rows of d = 2048: 131 us
+// against 133).
+// MT = 2 (NT = 32) halves the reads of H from L2 per byte of W: one row of d =
+// 4096 and V = 151936 187 us against 204. With more rows the last tile's longer
+// epilogue costs more than that gives (64 rows of d = 2048: 114 us against 112).
 //   warp 0      TMA producer, warp 1 MMA issuer, warp 2 TMEM
 //   warps 4-7   epilogue: TMEM lanes (vocabulary) into shared memory as
-//               [row][128], then a warp per row: 4 columns a lane, the four
-//               numbers by shuffles, the logits to memory in 512-byte runs
+//               [32 rows][128]; a thread sums 32 columns of one row (no
+//               shuffles), a warp stores a row's 512 bytes of logits
 // The numbers and logits are laid out as the pair kernel's, and the kernels
 // behind do not know which ran.
 // ----------------------------------------------------------------------------
-template <int NT>
+constexpr int kOutLd = 132;  // row stride of the logits in shared memory: 16-byte reads of 8 rows hit all banks once
+
+template <int NT, int MT>
 struct RowsCfg {
-  static constexpr int kABytes = 128 * BK * 2;
+  static constexpr int kABytes = MT * 128 * BK * 2;
   static constexpr int kBBytes = NT * BK * 2;
-  static constexpr int kStages = NT <= 32 ? 10 : NT <= 64 ? 8 : 7;
+  static constexpr int kStages = 211000 / (kABytes + kBBytes);
   static constexpr int kOut = kStages * (kABytes + kBBytes);
-  static constexpr int kBars = kOut + 32 * 128 * 4;
+  static constexpr int kSums = kOut + 32 * kOutLd * 4;
+  static constexpr int kBars = kSums + 128 * 16;
   static constexpr int kNumBars = 2 * kStages + 4 + 1;
   static constexpr int kMisc = kBars + kNumBars * 8;
   static constexpr int kTotal = kMisc + 16;
   static constexpr int kDynamicBytes = kTotal + 1024;
-  static constexpr int kTmemCols = NT <= 32 ? 64 : NT <= 64 ? 128 : 256;  // two accumulators, a power of two
+  static constexpr int kTmemCols = MT * NT <= 64 ? 128 : 256;  // two accumulators, a power of two
+  static_assert(2 * MT * NT <= kTmemCols, "TMEM columns (few-rows kernel)");
   static_assert(kDynamicBytes <= 232448, "shared memory budget (few-rows kernel)");
 };
 
@@ -354,9 +364,9 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
   return all != 0;
 }
 
-template <int NT>
+template <int NT, int MT>
 __global__ void __launch_bounds__(NUM_THREADS, 1) k_rows_logits(const __grid_constant__ RowsParams p) {
-  using Cfg = RowsCfg<NT>;
+  using Cfg = RowsCfg<NT, MT>;
   constexpr int S = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -364,6 +374,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_rows_logits(const __grid_con
   uint8_t* sA = smem;
   uint8_t* sB = smem + S * Cfg::kABytes;
   float* out = reinterpret_cast<float*>(smem + Cfg::kOut);
+  float4* sums = reinterpret_cast<float4*>(smem + Cfg::kSums);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::kBars);
   uint64_t* empty = full + S;
   uint64_t* tfull = full + 2 * S;
@@ -409,7 +420,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_rows_logits(const __grid_con
           break;
         }
         mbar_arrive_expect_tx(&full[stage], Cfg::kABytes + Cfg::kBBytes);
-        tma_load_2d(sA + stage * Cfg::kABytes, &p.w, &full[stage], kb * BK, t * 128);
+#pragma unroll
+        for (int h = 0; h < MT; ++h)  // (a block past the vocabulary is all zeros)
+          tma_load_2d(sA + stage * Cfg::kABytes + h * 128 * BK * 2, &p.w, &full[stage], kb * BK, (t * MT + h) * 128);
         tma_load_2d(sB + stage * Cfg::kBBytes, &p.h, &full[stage], kb * BK, 0);
         armed |= 1u << stage;
         armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
@@ -434,7 +447,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_rows_logits(const __grid_con
         break;
       }
       tc_fence_after_sync();
-      const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * NT);
+      const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * MT * NT);
       for (int kb = 0; kb < p.k_blocks; ++kb) {
         if (!mbar_wait(&full[stage], phase, abort)) {
           report_timeout(abort, p.ep.flags);
@@ -445,8 +458,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_rows_logits(const __grid_con
         const uint32_t a_addr = smem_u32(sA + stage * Cfg::kABytes);
         const uint32_t b_addr = smem_u32(sB + stage * Cfg::kBBytes);
 #pragma unroll
-        for (int k = 0; k < BK / 16; ++k)
-          umma_bf16(d_tmem, desc_k_major(a_addr, k), desc_k_major(b_addr, k), idesc, (kb | k) != 0 ? 1u : 0u);
+        for (int k = 0; k < BK / 16; ++k) {
+#pragma unroll
+          for (int h = 0; h < MT; ++h)
+            umma_bf16(d_tmem + h * NT, desc_k_major(a_addr + h * 128 * BK * 2, k), desc_k_major(b_addr, k), idesc,
+                      (kb | k) != 0 ? 1u : 0u);
+        }
         issued = true;
         umma_commit(&empty[stage]);
         if (++stage == S) {
@@ -479,60 +496,82 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_rows_logits(const __grid_con
       if (!came && lane == 0) report_timeout(abort, e.flags);
       if (!epilogue_all(came)) break;
       tc_fence_after_sync();
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * NT);
-      const int col = t * 128 + lane * 4;
-      for (int n0 = 0; n0 < e.rows; n0 += 32) {  // 32 rows of H at a time through shared memory
-        if (n0 > 0) epilogue_all(true);          // the 32 before have been read
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * MT * NT);
+#pragma unroll 1
+      for (int g = 0, n0 = 0, h = 0; h < MT; ++g) {  // 32 rows of H by 128 of W at a time through shared memory
+        const int part = t * MT + h, col0 = part * 128;
+        if (g > 0) epilogue_all(true);  // what was there has been read
         {
           float v[32];
-          tmem_ld_32x32b_x32(taddr + n0, v);
+          tmem_ld_32x32b_x32(taddr + h * NT + n0, v);
 #pragma unroll
-          for (int c = 0; c < 32; ++c) out[c * 128 + q * 32 + lane] = v[c];
+          for (int c = 0; c < 32; ++c) out[c * kOutLd + q * 32 + lane] = v[c];
         }
-        if (n0 + 32 >= e.rows) {  // the accumulator is free for the tile after next
+        if (h == MT - 1 && n0 + 32 >= e.rows) {  // the accumulator is free for the tile after next
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&tempty[acc]);
         }
         epilogue_all(true);
-        const int n1 = e.rows - n0 < 32 ? e.rows - n0 : 32;
-        for (int i = q; i < n1; i += 4) {
-          const int n = n0 + i;
-          const float4 z4 = *reinterpret_cast<const float4*>(out + i * 128 + lane * 4);
-          if (p.store_z) {
-            if (in_bounds(col + 3, p.ldz, e.flags))
-              *reinterpret_cast<float4*>(p.Z + static_cast<long long>(n) * p.ldz + col) = z4;
-          } else {
-            const long long y = e.y[n];
-            const long long c = y - col;
-            if (c >= 0 && c < 4 && y < e.V && y != e.ignore_index)
-              e.ztgt[n] = c == 0 ? z4.x : c == 1 ? z4.y : c == 2 ? z4.z : z4.w;
+        // this warp's 32 columns of row n0 + lane
+        const int n = n0 + lane;
+        const float* zr = out + lane * kOutLd + q * 32;
+        float m = -INFINITY, s = 0.f, tt = 0.f, cnt = 0.f;
+        if (n < e.rows) {
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 x = *reinterpret_cast<const float4*>(zr + 4 * j);
+            v[4 * j] = x.x;
+            v[4 * j + 1] = x.y;
+            v[4 * j + 2] = x.z;
+            v[4 * j + 3] = x.w;
           }
-          float v[4] = {z4.x, z4.y, z4.z, z4.w};
+          const int vlim = e.V - col0 - q * 32;
+          if (vlim < 32) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (col + c >= e.V) v[c] = -INFINITY;
-          float m = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+            for (int c = 0; c < 32; ++c)
+              if (c >= vlim) v[c] = -INFINITY;
+          }
 #pragma unroll
-          for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+          for (int c = 0; c < 32; ++c) m = fmaxf(m, v[c]);
           const float mb = m == -INFINITY ? 0.f : m;
-          float s = 0.f, tt = 0.f;
-          int cnt = 0;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 32; ++c) {
             const float dz = v[c] - mb;
             const float x = ex2_approx(dz * k);
-            cnt += __popc(__ballot_sync(0xffffffffu, dz == 0.f));
-            s += dz == 0.f ? 0.f : x;
+            if (dz == 0.f)
+              cnt += 1.f;
+            else
+              s += x;
             tt = fmaf(x, fmaxf(dz, kFloor), tt);
           }
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) {
-            s += __shfl_xor_sync(0xffffffffu, s, off);
-            tt += __shfl_xor_sync(0xffffffffu, tt, off);
+          if (!p.store_z) {
+            const long long y = e.y[n], c = y - col0 - q * 32;
+            if (c >= 0 && c < 32 && y < e.V && y != e.ignore_index) e.ztgt[n] = zr[c];
           }
-          if (lane == 0 && in_bounds(t, e.nparts, e.flags))
-            e.partials[static_cast<long long>(n) * e.nparts + t] = make_float4(m, s, tt * e.inv_t, static_cast<float>(cnt));
+        }
+        sums[q * 32 + lane] = make_float4(m, s, tt * e.inv_t, cnt);
+        if (p.store_z) {  // a warp a row: 512 bytes at a time
+          const int n1 = e.rows - n0 < 32 ? e.rows - n0 : 32;
+          for (int i = q; i < n1; i += 4)
+            if (in_bounds(col0 + lane * 4 + 3, p.ldz, e.flags))
+              *reinterpret_cast<float4*>(p.Z + static_cast<long long>(n0 + i) * p.ldz + col0 + lane * 4) =
+                  *reinterpret_cast<const float4*>(out + i * kOutLd + lane * 4);
+        }
+        epilogue_all(true);
+        if (q == 0 && n < e.rows && in_bounds(part, e.nparts, e.flags)) {  // the four warps' columns together
+          const float4 x[4] = {sums[lane], sums[32 + lane], sums[64 + lane], sums[96 + lane]};
+          const float M = fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x));
+          RowSum a{0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) add_partial(a, x[i], M, e.inv_t);
+          e.partials[static_cast<long long>(n) * e.nparts + part] = make_float4(M, a.s, a.t, a.c);
+        }
+        n0 += 32;
+        if (n0 >= e.rows) {
+          n0 = 0;
+          ++h;
         }
       }
       if (++acc == 2) {
@@ -548,24 +587,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_rows_logits(const __grid_con
   if (warp == 2) tmem_dealloc(tmem_base, Cfg::kTmemCols);
 }
 
-template <int NT>
+template <int NT, int MT>
 cudaError_t launch_rows_nt(const CUtensorMap& h, const CUtensorMap& w, int store_z, float* Z, long long ldz,
                            long long V, long long d, const TokParams& ep, int num_sms, cudaStream_t s) {
   RowsParams p;
   p.w = w;
   p.h = h;
-  p.tiles = static_cast<int>((V + 127) / 128);
+  p.tiles = static_cast<int>((V + MT * 128 - 1) / (MT * 128));
   p.k_blocks = static_cast<int>((d + BK - 1) / BK);
   p.store_z = store_z;
   p.ldz = ldz;
   p.Z = Z;
   p.ep = ep;
   const int grid = p.tiles < num_sms ? p.tiles : num_sms;
-  auto kern = k_rows_logits<NT>;
+  auto kern = k_rows_logits<NT, MT>;
   const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg<NT>::kDynamicBytes);
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg<NT, MT>::kDynamicBytes);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, grid, NUM_THREADS, RowsCfg<NT>::kDynamicBytes, s, p);
+  return launch_k(kern, grid, NUM_THREADS, RowsCfg<NT, MT>::kDynamicBytes, s, p);
 }
 
 // ----------------------------------------------------------------------------
@@ -1101,9 +1140,9 @@ cudaError_t launch_tok_logits(int mode, const CUtensorMap& a, const CUtensorMap&
 cudaError_t launch_rows_logits(const CUtensorMap& h, const CUtensorMap& w, int store_z, float* Z, long long ldz,
                                long long V, long long d, const TokParams& ep, int num_sms, cudaStream_t s) {
   switch (few_rows_box(ep.rows)) {
-    case 32: return launch_rows_nt<32>(h, w, store_z, Z, ldz, V, d, ep, num_sms, s);
-    case 64: return launch_rows_nt<64>(h, w, store_z, Z, ldz, V, d, ep, num_sms, s);
-    default: return launch_rows_nt<96>(h, w, store_z, Z, ldz, V, d, ep, num_sms, s);
+    case 32: return launch_rows_nt<32, 2>(h, w, store_z, Z, ldz, V, d, ep, num_sms, s);
+    case 64: return launch_rows_nt<64, 1>(h, w, store_z, Z, ldz, V, d, ep, num_sms, s);
+    default: return launch_rows_nt<96, 1>(h, w, store_z, Z, ldz, V, d, ep, num_sms, s);
   }
 }
 
