@@ -1035,7 +1035,11 @@ TokLayout tok_layout(int64_t N, int64_t d, int64_t V, bool with_z, bool with_gra
   return T;
 }
 
-int check_temperature(float t) { return t > 0.f && t <= 3.0e38f ? LCE_OK : LCE_ERR_INVALID_ARG; }
+// The temperature is positive and finite, and so is its inverse; a vocabulary within 1024 of 2^31 is
+// refused, so that column numbers rounded up to a tile stay 32-bit.
+int check_token_args(int64_t V, float t) {
+  return V <= (int64_t{1} << 31) - 1024 && t >= 1.0e-30f && t <= 1.0e30f ? LCE_OK : LCE_ERR_INVALID_ARG;
+}
 
 // Fills the call record of a token operator (after its own argument checks).
 int tok_begin(Call* c, const TokLayout& T, const void* H, const void* W, const int64_t* y, int64_t N, int64_t d,
@@ -1142,7 +1146,7 @@ int lce_logprobs(const void* H, const void* W, const int64_t* y, int64_t N, int6
   lce_opts_init(&o);
   if (opts) o = *opts;
   LCE_TRY(check_sizes(N, d, V, &o));
-  LCE_TRY(check_temperature(temperature));
+  LCE_TRY(check_token_args(V, temperature));
   if (o.reserved != 0 || top_k < 0 || top_k > LCE_MAX_TOP || top_k > V) return LCE_ERR_INVALID_ARG;
   if (!W || !ws || (N > 0 && (!H || !y || !logp || !lse || (top_k > 0 && (!top_logp || !top_idx)))))
     return LCE_ERR_INVALID_ARG;
@@ -1201,7 +1205,7 @@ int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_
   lce_opts_init(&o);
   if (opts) o = *opts;
   LCE_TRY(check_sizes(N, d, V, &o));
-  LCE_TRY(check_temperature(temperature));
+  LCE_TRY(check_token_args(V, temperature));
   const bool dW_bf16 = (grads & LCE_DW_BF16) != 0;
   if (o.reserved != 0 || (grads & ~LCE_DW_BF16) != 0 || (dW_bf16 && o.accumulate_dW) || !W || !ws || (!dH && !dW) ||
       (N > 0 && (!H || !y || !lse || !g_logp || (g_entropy && !entropy))))
@@ -1267,7 +1271,7 @@ int distill(const void* H, const void* W, const int64_t* idx, const void* t, int
   lce_opts_init(&o);
   if (opts) o = *opts;
   LCE_TRY(check_sizes(N, d, V, &o));
-  LCE_TRY(check_temperature(temperature));
+  LCE_TRY(check_token_args(V, temperature));
   const bool dW_bf16 = (grads & LCE_DW_BF16) != 0;
   if (o.reserved != 0 || K < 1 || K > LCE_MAX_TOP || (grads & ~LCE_DW_BF16) != 0 || (dW_bf16 && o.accumulate_dW) ||
       (teacher & ~(LCE_TEACHER_BF16 | LCE_TEACHER_LOGPROBS)) != 0 ||

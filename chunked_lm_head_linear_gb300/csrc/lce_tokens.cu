@@ -91,12 +91,37 @@ __device__ __forceinline__ float log_sum(const RowSum& a) { return logf(a.c) + l
 //                rounded to bf16 once (the operand type of the two GEMMs that
 //                follow), everything before it in fp32.
 // ----------------------------------------------------------------------------
-// An entry of the gradient tile (everything over T already): p (c0 + c1 log p)
-// with c0 = -a - e entropy, c1 = -e, and + a at the label.
-__device__ __forceinline__ float grad_entry(float z, float inv_t, float lse, float c0, float c1, float a, bool label) {
-  const float logp = fmaf(z, inv_t, -lse);
-  const float g = __fmul_rn(ex2_approx(logp * kLog2e), fmaf(c1, fmaxf(logp, kFloor), c0));
-  return label ? __fadd_rn(g, a) : g;
+// A row of the gradient tile: entries p (c0 + c1 log p) with c0 = -a - e entropy
+// and c1 = -e, and + a at the label (a = g_logp / T where the label is given,
+// e = g_entropy / T). A row without upstream gradient is zero whatever its
+// logits are: masked tokens may hold anything.
+struct GradRow {
+  float lse = 0.f, a = 0.f, c0 = 0.f, c1 = 0.f;
+  int y = -1;        // the label, -1 where it is not given
+  bool zero = true;
+};
+
+__device__ __forceinline__ GradRow grad_row(int r, const int64_t* labels, long long ignore_index, int V,
+                                            const float* lse, const float* entropy, const float* g_logp,
+                                            const float* g_entropy, float inv_t) {
+  GradRow g;
+  const long long y = labels[r];
+  if (y != ignore_index && y >= 0 && y < V) g.y = static_cast<int>(y);
+  if (g.y >= 0) g.a = g_logp[r] * inv_t;
+  const float e = g_entropy != nullptr ? g_entropy[r] * inv_t : 0.f;
+  g.lse = lse[r];
+  g.c0 = -g.a;
+  g.c1 = -e;
+  if (e != 0.f) g.c0 -= e * entropy[r];
+  g.zero = g.a == 0.f && e == 0.f;
+  return g;
+}
+
+__device__ __forceinline__ float grad_entry(float z, float inv_t, const GradRow& r, bool label) {
+  const float logp = fmaf(z, inv_t, -r.lse);
+  float g = __fmul_rn(ex2_approx(logp * kLog2e), fmaf(r.c1, fmaxf(logp, kFloor), r.c0));
+  if (label) g = __fadd_rn(g, r.a);
+  return r.zero ? 0.f : g;
 }
 
 // The first launch of a call clears the status word from its first block, before anything can have
@@ -192,20 +217,10 @@ struct TokEpi {
     const int r = m0 + ctx.row0 + ctx.lane;
     const int vlim = p.V - col0;
     if (m0 + ctx.row0 >= p.rows || vlim <= 0) return;  // nothing of this half tile is stored
-    float lse = 0.f, a = 0.f, c1 = 0.f, c0g = 0.f;
-    int ycol = -1;
-    if (r < p.rows) {
-      const long long y = p.y[r];
-      const bool given = y != p.ignore_index && y >= 0 && y < p.V;
-      lse = p.lse[r];
-      a = given ? p.g_logp[r] * p.inv_t : 0.f;
-      const float e = p.g_entropy != nullptr ? p.g_entropy[r] * p.inv_t : 0.f;
-      c1 = -e;
-      c0g = -a;
-      if (p.g_entropy != nullptr) c0g -= e * p.entropy[r];
-      const long long yc = y - col0;
-      if (given && yc >= 0 && yc < EPI_COLS) ycol = static_cast<int>(yc);
-    }
+    GradRow g;
+    if (r < p.rows)
+      g = grad_row(r, p.y, p.ignore_index, p.V, p.lse, p.entropy, p.g_logp, p.g_entropy, p.inv_t);
+    const int ycol = g.y - col0;  // a column of this half tile, or outside [0, 128)
 #pragma unroll 1
     for (int u = 0; u < EPI_COLS / 64; ++u) {
       if (u * 64 >= vlim) break;
@@ -218,8 +233,8 @@ struct TokEpi {
         uint32_t pk[16];
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
-          pk[c / 2] = pack_bf16x2(grad_entry(v[c], p.inv_t, lse, c0g, c1, a, c0 + c == ycol),
-                                  grad_entry(v[c + 1], p.inv_t, lse, c0g, c1, a, c0 + c + 1 == ycol));
+          pk[c / 2] = pack_bf16x2(grad_entry(v[c], p.inv_t, g, c0 + c == ycol),
+                                  grad_entry(v[c + 1], p.inv_t, g, c0 + c + 1 == ycol));
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -876,23 +891,16 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_score_grad(const ScoreGradAr
   }
   const float* z = p.Z + static_cast<long long>(r) * p.ldz;
   __nv_bfloat16* g = p.G + static_cast<long long>(r) * p.ldg;
-  const long long y = p.y[r];
-  const bool given = y != p.ignore_index && y >= 0 && y < p.V;
-  const float lse = p.lse[r];
-  const float a = given ? p.g_logp[r] * p.inv_t : 0.f;
-  const float e = p.g_entropy != nullptr ? p.g_entropy[r] * p.inv_t : 0.f;
-  const float c1 = -e, c0 = p.g_entropy != nullptr ? -a - e * p.entropy[r] : -a;
-  const bool zero = a == 0.f && e == 0.f && c0 == 0.f;
-  const int yc = given ? static_cast<int>(y) : -1;
+  const GradRow row = grad_row(r, p.y, p.ignore_index, p.V, p.lse, p.entropy, p.g_logp, p.g_entropy, p.inv_t);
   for (int c = tid * 8; c < p.V; c += kRowThreads * 8) {
     // columns past V (up to 7) lie inside the row's padding: never read by the GEMMs
     uint32_t o[4] = {0u, 0u, 0u, 0u};
-    if (!zero) {
+    if (!row.zero) {
       const float4 u = __ldcs(reinterpret_cast<const float4*>(z + c));
       const float4 w = __ldcs(reinterpret_cast<const float4*>(z + c + 4));
       float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = grad_entry(v[i], p.inv_t, lse, c0, c1, a, c + i == yc);
+      for (int i = 0; i < 8; ++i) v[i] = grad_entry(v[i], p.inv_t, row, c + i == row.y);
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
     }

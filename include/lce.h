@@ -300,7 +300,7 @@ int lce_scale_grads(void* dH, float* dW, int64_t N, int64_t d, int64_t V, const 
 
 /*
  * Token operators of the head: what a model needs of its logits besides the
- * cross-entropy. z = H W^T as above, z' = z / temperature (> 0, finite), p =
+ * cross-entropy. z = H W^T as above, z' = z / temperature (1e-30 to 1e30), p =
  * softmax(z'). H, W, y, dH, dW, opts, ws and stream are those of the calls
  * above; the logits of one chunk at a time are held in the workspace, never
  * [N, V] (chunk_tokens = 0: equal chunks of about 4096 tokens, fewer than 6144).
@@ -330,7 +330,8 @@ int lce_scale_grads(void* dH, float* dW, int64_t N, int64_t d, int64_t V, const 
  * where y_i is ignored) and e_i = g_entropy_i
  *   G_iv = ([v = y_i] a_i - p_iv (a_i + e_i (log p_iv + entropy_i))) / temperature
  *   dH = G W (bf16), dW = G^T H (fp32; added to with opts->accumulate_dW).
- * G is rounded to bf16 once. Either of dH, dW may be NULL: not wanted, not
+ * G is rounded to bf16 once; a row whose upstream gradients are zero is zero in
+ * G and dH whatever its logits are. Either of dH, dW may be NULL: not wanted, not
  * computed. grads: 0, or LCE_DW_BF16: dW is bf16 [V, d], the fp32 sum rounded
  * once (not with accumulate_dW; several chunks are summed in fp32 in the
  * workspace). logits: those of lce_logprobs, or NULL: recomputed chunk by
@@ -364,7 +365,8 @@ int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_
  *          with a kept entry, or opts->n_valid_override
  *   G_iv = (grad_loss temperature / n) (p_iv sum_k q_ik - sum_k q_ik [v = idx_ik])
  *   dH = G W (bf16), dW = G^T H (fp32; opts->accumulate_dW; or bf16: grads as above)
- * Rows without a kept entry have row_loss 0 and a zero gradient. The tile of G
+ * Rows without a kept entry have row_loss 0 and a zero gradient; a NaN or +inf
+ * value, or a row of NaN logits, makes its row's loss and gradient NaN. The tile of G
  * without its leading factor is rounded to bf16 once. 1 <= K <= LCE_MAX_TOP.
  * loss [1], row_loss [N] fp32; grad_loss: device fp32 [1] or NULL (1.0); either
  * of dH, dW may be NULL: not wanted, not computed. Workspace:

@@ -292,6 +292,31 @@ def test_logprobs_backward(cuda_lib, N, d, V, T, chunk):
     close(acc, 1.0 + np64(dW), 2.0 ** -23 * (1 + (N // chunk if chunk else 0)) * (1 + np.abs(np64(dW))) + 1e-7, "dW added")
 
 
+@pytest.mark.parametrize("keep", [False, True])
+def test_masked_rows_of_nan_have_zero_gradients(cuda_lib, keep):
+    """Rows without upstream gradient (padding that holds NaN and infinities): dH is zero there and the
+    other rows are not touched. (dW sums over all rows of H, as the formula does, so it is not asked for.)"""
+    torch = _torch()
+    rng, H, W, y = make(150, 64, 1000)
+    y[:] = rng.integers(0, 1000, 150)
+    Ht, Wt = heads(H, W)
+    g1, g2 = rng.standard_normal(150).astype(np.float32), rng.standard_normal(150).astype(np.float32)
+    masked = np.zeros(150, bool)
+    masked[[3, 77, 149]] = True
+    y[masked], g2[masked] = oracle.IGNORE_INDEX, 0.0
+    g1[masked] = np.nan      # and its upstream gradient may be anything
+    kept = torch.empty(150, 1024, device="cuda") if keep else None
+
+    def run(h):
+        _, lse, ent, _, _ = cuda_lib.lce_logprobs(h, Wt, dev(y), logits=kept)
+        return cuda_lib.lce_logprobs_backward(h, Wt, dev(y), lse, ent, dev(g1), dev(g2), logits=kept, need_dW=False)[0]
+
+    want = run(Ht)
+    Ht[3], Ht[77], Ht[149, 5] = float("nan"), float("inf"), -float("inf")
+    got = run(Ht)
+    assert torch.equal(got, want) and not got[dev(masked)].any()
+
+
 def teacher(rng, N, V, K, bf16=False):
     """Top entries with every irregularity: short lists, no list, -inf values, an index twice."""
     idx = np.stack([rng.permutation(V)[:K] if K <= V else rng.integers(0, V, K) for _ in range(N)]).astype(np.int64)
@@ -554,3 +579,44 @@ def test_caller_tensors_are_checked(cuda_lib):
     auto = cuda_lib.lce_logprobs(Ht, Wt, yt, top_k=3, chunk_tokens="auto")
     for a, b in zip(auto, cuda_lib.lce_logprobs(Ht, Wt, yt, top_k=3)):
         assert torch.equal(a, b)
+
+
+# --------------------------------------------------------------------------- the bounds-checking build
+def _child():
+    """Every kind of call on the bounds-checking build (a process loads one library): sync_check turns an
+    index outside its buffer into LCE_ERR_BOUNDS."""
+    import torch
+
+    from chunked_lm_head_linear_gb300 import build, lce
+    lce.load(build.build(checks=True))
+    for N, d, V, K, chunk in [(1, 64, 37, 5, 0), (3, 72, 2, 2, 0), (33, 136, 129, 100, 0), (96, 64, 4099, 3, 0),
+                              (97, 8, 257, 128, 0), (129, 136, 70001, 20, 64), (513, 256, 1000, 33, 200)]:
+        rng, H, W, y = make(N, d, V, seed=N)
+        idx, t = teacher(rng, N, V, K)
+        Ht, Wt = heads(H, W)
+        g = dev(rng.standard_normal(N).astype(np.float32))
+        kept = torch.empty(N, lce.lce_logits_stride(V), device="cuda")
+        for logits in (None, kept):
+            kw = dict(logits=logits, chunk_tokens=chunk, sync_check=True)
+            out = lce.lce_logprobs(Ht, Wt, dev(y), top_k=K, **kw)
+            check_scores(out, H, W, y, 1.0, K)
+            for dt in (torch.float32, torch.bfloat16):
+                dH, dW = lce.lce_logprobs_backward(Ht, Wt, dev(y), out[1], out[2], g, g, dW_dtype=dt, **kw)
+                check_grads(dH, dW if dt == torch.float32 else None,
+                            oracle.logprobs_backward_f64(H, W, y, np64(g), np64(g)))
+        lce.lce_logprobs(Ht, Wt, dev(y), chunk_tokens=chunk, sync_check=True)
+        out = lce.lce_distill_fwd_bwd(Ht, Wt, dev(idx), dev(t), chunk_tokens=chunk, sync_check=True)
+        check_grads(out[2], out[3], oracle.distill_f64(H, W, idx, t))
+        lce.lce_distill_forward(Ht, Wt, dev(idx), dev(t), chunk_tokens=chunk, sync_check=True)
+    print("checked build: ok")
+
+
+def test_bounds_checking_build(cuda_lib):
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([os.path.dirname(here), here]))
+    r = subprocess.run([sys.executable, "-c", "import test_tokens_gpu as t; t._child()"], env=env, cwd=here,
+                       capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and "checked build: ok" in r.stdout, (r.stdout + r.stderr)[-3000:]
