@@ -23,7 +23,8 @@ ranks) call ``lce.lce_fwd_bwd`` with their fp32 buffer as ``dW`` and
 FusedLinearLogProbs and FusedLinearDistillation wrap the token operators
 (lce_logprobs, lce_distill_fwd_bwd) the same way: log-probabilities and
 entropies of given tokens, whose upstream gradients are known only in the
-backward, save lse and entropy and recompute the logits there; the distillation
+backward, save logp, lse and entropy, and the logits of a batch of one chunk
+(else they are recomputed there); the distillation
 loss computes its gradients in the forward and scales them in the backward.
 Gradients nobody needs (a frozen W) are not computed.
 """
@@ -87,7 +88,7 @@ class _LogProbs(torch.autograd.Function):
         if keep and (ctx.needs_input_grad[0] or ctx.needs_input_grad[1]):
             logits = torch.empty((H.shape[0], lce.lce_logits_stride(W.shape[0])), dtype=torch.float32, device=H.device)
         logp, lse, entropy, _, _ = lce.lce_logprobs(H, W, y, temperature=temperature, logits=logits, **opts)
-        ctx.save_for_backward(H, W, y, lse, entropy, logits)
+        ctx.save_for_backward(H, W, y, logp, lse, entropy, logits)
         ctx.temperature, ctx.opts = temperature, opts
         ctx.set_materialize_grads(False)   # an output nobody used comes back as None
         return logp, entropy
@@ -95,11 +96,11 @@ class _LogProbs(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, g_logp, g_entropy):
-        H, W, y, lse, entropy, logits = ctx.saved_tensors
+        H, W, y, logp, lse, entropy, logits = ctx.saved_tensors
         g_logp = torch.zeros_like(lse) if g_logp is None else g_logp.contiguous()
         g_entropy = None if g_entropy is None else g_entropy.contiguous()
         # the forward checked its tensors, autograd that the gradients are like the outputs
-        dH, dW = lce._logprobs_backward(H, W, y, lse, entropy, g_logp, g_entropy, logits, ctx.temperature,
+        dH, dW = lce._logprobs_backward(H, W, y, logp, lse, entropy, g_logp, g_entropy, logits, ctx.temperature,
                                         lce.LCE_DW_BF16, None, ctx.needs_input_grad[0], ctx.needs_input_grad[1], None,
                                         None, ctx.opts)
         return dH, dW, None, None, None, None

@@ -1007,7 +1007,8 @@ int64_t tok_chunk(int64_t N, const lce_opts* o) {
   return C < N ? C : N;
 }
 
-TokLayout tok_layout(int64_t N, int64_t d, int64_t V, bool with_z, bool with_grad, bool dW_bf16, const lce_opts* o) {
+TokLayout tok_layout(int64_t N, int64_t d, int64_t V, bool with_z, bool with_grad, bool dW_bf16, bool with_scale,
+                     const lce_opts* o) {
   TokLayout T;
   Layout& L = T.base;
   L.C = tok_chunk(N, o);
@@ -1026,6 +1027,10 @@ TokLayout tok_layout(int64_t N, int64_t d, int64_t V, bool with_z, bool with_gra
   L.ztgt = take(sizeof(float) * C);
   L.partials = take(sizeof(float4) * C * static_cast<size_t>(2 * L.T));
   if (with_z) T.Z = take(sizeof(float) * C * static_cast<size_t>(T.ldz));
+  if (with_scale) {  // row scales and bf16(scale H)
+    L.alpha = take(sizeof(float) * C);
+    L.Ht = take(2 * C * static_cast<size_t>(d));
+  }
   if (with_grad) {
     L.P = take(2 * C * static_cast<size_t>(L.ldp));
     take_dh_parts(L, d, V, take);
@@ -1108,9 +1113,10 @@ int zero_dW(const Call& c, void* dW, bool dW_bf16) {
   return timed(c.s, K_MEMSET, static_cast<double>(bytes), [&] { return cuda_rc(cudaMemsetAsync(dW, 0, bytes, c.s)); });
 }
 
-// The backward GEMMs of a chunk on its exact gradient tile, for the gradients that are wanted. A
-// bf16 dW is summed in fp32 in the workspace until the last chunk, which stores it.
-int tok_grads(const Call& c, const TokLayout& T, int64_t c0, int64_t rows, void* dH, void* dW, bool dW_bf16) {
+// The backward GEMMs of a chunk on its gradient tile, for the gradients that are wanted: dH =
+// rowscale (G W), dW = G^T B. A bf16 dW is summed in fp32 in the workspace until the last chunk, which stores it.
+int tok_grads(const Call& c, const TokLayout& T, int64_t c0, int64_t rows, const float* rowscale, const uint16_t* B,
+              void* dH, void* dW, bool dW_bf16) {
   BwdPart part;
   part.with_dh = dH != nullptr;
   part.v_end = dW ? c.V : 0;
@@ -1122,7 +1128,7 @@ int tok_grads(const Call& c, const TokLayout& T, int64_t c0, int64_t rows, void*
     else if (c0 > 0)
       part.dW_add = sum;
   }
-  return dh_dw(c, c0, rows, nullptr, c.H + c0 * c.d, dH, dW, c.o.accumulate_dW || c0 > 0, false, part);
+  return dh_dw(c, c0, rows, rowscale, B, dH, dW, c.o.accumulate_dW || c0 > 0, false, part);
 }
 
 }  // namespace
@@ -1136,7 +1142,7 @@ size_t lce_logprobs_workspace_size(int64_t N, int64_t d, int64_t V, int32_t top_
   lce_opts_init(&o);
   if (opts) o = *opts;
   if (check_sizes(N, d, V, &o) != LCE_OK || top_k < 0 || top_k > LCE_MAX_TOP || top_k > V) return 0;
-  return tok_layout(N, d, V, top_k > 0, false, false, &o).total;
+  return tok_layout(N, d, V, top_k > 0, false, false, false, &o).total;
 }
 
 int lce_logprobs(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V, float temperature,
@@ -1154,7 +1160,7 @@ int lce_logprobs(const void* H, const void* W, const int64_t* y, int64_t N, int6
       !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(top_logp, 4) || !aligned(top_idx, 8) ||
       !aligned(logits, 16))
     return LCE_ERR_ALIGNMENT;
-  const TokLayout T = tok_layout(N, d, V, top_k > 0 && !logits, false, false, &o);
+  const TokLayout T = tok_layout(N, d, V, top_k > 0 && !logits, false, false, false, &o);
   Call c;
   LCE_TRY(tok_begin(&c, T, H, W, y, N, d, V, o, ws, ws_bytes, stream));
   if (lce::kChecks || N == 0) LCE_TRY(prepare(c, nullptr));
@@ -1194,13 +1200,13 @@ size_t lce_logprobs_backward_workspace_size(int64_t N, int64_t d, int64_t V, int
   lce_opts_init(&o);
   if (opts) o = *opts;
   if (check_sizes(N, d, V, &o) != LCE_OK || (grads & ~LCE_DW_BF16) != 0) return 0;
-  return tok_layout(N, d, V, false, true, (grads & LCE_DW_BF16) != 0, &o).total;
+  return tok_layout(N, d, V, false, true, (grads & LCE_DW_BF16) != 0, true, &o).total;
 }
 
 int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
-                          float temperature, const float* lse, const float* entropy, const float* g_logp,
-                          const float* g_entropy, const float* logits, int32_t grads, void* dH, void* dW,
-                          const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
+                          float temperature, const float* logp, const float* lse, const float* entropy,
+                          const float* g_logp, const float* g_entropy, const float* logits, int32_t grads, void* dH,
+                          void* dW, const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
   lce_opts o;
   lce_opts_init(&o);
   if (opts) o = *opts;
@@ -1208,19 +1214,23 @@ int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_
   LCE_TRY(check_token_args(V, temperature));
   const bool dW_bf16 = (grads & LCE_DW_BF16) != 0;
   if (o.reserved != 0 || (grads & ~LCE_DW_BF16) != 0 || (dW_bf16 && o.accumulate_dW) || !W || !ws || (!dH && !dW) ||
-      (N > 0 && (!H || !y || !lse || !g_logp || (g_entropy && !entropy))))
+      (N > 0 && (!H || !y || !logp || !lse || !g_logp || (g_entropy && !entropy))))
     return LCE_ERR_INVALID_ARG;
   if (!aligned(W, 16) || !aligned(H, 16) || !aligned(y, 8) || !aligned(ws, 256) || !aligned(dW, 16) ||
-      !aligned(dH, 16) || !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(g_logp, 4) || !aligned(g_entropy, 4) ||
-      !aligned(logits, 16))
+      !aligned(dH, 16) || !aligned(logp, 4) || !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(g_logp, 4) ||
+      !aligned(g_entropy, 4) || !aligned(logits, 16))
     return LCE_ERR_ALIGNMENT;
-  o.reduction = LCE_SUM;  // the upstream gradients carry every factor
-  const TokLayout T = tok_layout(N, d, V, false, true, dW_bf16, &o);
+  const TokLayout T = tok_layout(N, d, V, false, true, dW_bf16, true, &o);
   Call c;
   LCE_TRY(tok_begin(&c, T, H, W, y, N, d, V, o, ws, ws_bytes, stream));
-  if (N == 0 || !logits) LCE_TRY(prepare(c, nullptr));  // with kept logits the gradient tile's launch does it
-  if (N == 0) LCE_TRY(zero_dW(c, dW, dW_bf16));
+  if (N == 0) {
+    c.o.reduction = LCE_SUM;
+    LCE_TRY(prepare(c, nullptr));
+    LCE_TRY(zero_dW(c, dW, dW_bf16));
+  }
   uint16_t* G = reinterpret_cast<uint16_t*>(c.ws + c.L.P);
+  float* rowscale = reinterpret_cast<float*>(c.ws + c.L.alpha);
+  uint16_t* Ht = reinterpret_cast<uint16_t*>(c.ws + c.L.Ht);
   for (int64_t c0 = 0; c0 < N; c0 += c.L.C) {
     const int64_t rows = (N - c0) < c.L.C ? (N - c0) : c.L.C;
     lce::TokParams p = tok_params(c, c0, rows, temperature);
@@ -1228,34 +1238,38 @@ int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_
     p.entropy = entropy ? entropy + c0 : nullptr;
     p.g_logp = g_logp + c0;
     p.g_entropy = g_entropy ? g_entropy + c0 : nullptr;
-    if (logits) {
-      lce::ScoreGradArgs a;
-      std::memset(&a, 0, sizeof a);
-      a.V = p.V;
-      a.ldz = T.ldz;
-      a.ldg = c.L.ldp;
-      a.inv_t = p.inv_t;
-      a.ignore_index = p.ignore_index;
-      a.y = p.y;
-      a.lse = p.lse;
-      a.entropy = p.entropy;
-      a.g_logp = p.g_logp;
-      a.g_entropy = p.g_entropy;
-      a.Z = logits + c0 * T.ldz;
-      a.G = reinterpret_cast<__nv_bfloat16*>(G);
-      if (c0 == 0) {
-        a.st = c.st;
-        a.y_all = c.y;
-        a.N = N;
-        a.cnt = reinterpret_cast<int*>(c.ws + c.L.dh_cnt);
-        a.ncnt = c.L.dh_ncnt;
-      }
-      LCE_TRY(timed(c.s, K_COMBINE, 6.0 * static_cast<double>(rows) * static_cast<double>(V),
-                    [&] { return cuda_rc(lce::launch_score_grad(a, p.rows, c.s)); }));
-    } else {
-      LCE_TRY(tok_logits(c, c0, rows, lce::TOK_GRAD, G, c.L.ldp, p));
+    p.rowscale = rowscale;
+    lce::ScoreGradArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.V = p.V;
+    a.d = static_cast<int>(d);
+    a.ldz = T.ldz;
+    a.ldg = c.L.ldp;
+    a.inv_t = p.inv_t;
+    a.ignore_index = p.ignore_index;
+    a.y = p.y;
+    a.logp = logp + c0;
+    a.lse = p.lse;
+    a.entropy = p.entropy;
+    a.g_logp = p.g_logp;
+    a.g_entropy = p.g_entropy;
+    a.rowscale = rowscale;
+    a.H = reinterpret_cast<const uint4*>(c.H + c0 * d);
+    a.Ht = dW ? reinterpret_cast<uint4*>(Ht) : nullptr;
+    a.Z = logits ? logits + c0 * T.ldz : nullptr;
+    a.G = reinterpret_cast<__nv_bfloat16*>(G);
+    if (c0 == 0) {
+      a.st = c.st;
+      a.y_all = c.y;
+      a.N = N;
+      a.cnt = reinterpret_cast<int*>(c.ws + c.L.dh_cnt);
+      a.ncnt = c.L.dh_ncnt;
     }
-    LCE_TRY(tok_grads(c, T, c0, rows, dH, dW, dW_bf16));
+    const double bytes = static_cast<double>(rows) * (4.0 * static_cast<double>(d) + 32.0 +
+                                                      (logits ? 6.0 * static_cast<double>(V) : 0.0));
+    LCE_TRY(timed(c.s, K_COMBINE, bytes, [&] { return cuda_rc(lce::launch_score_grad(a, p.rows, c.s)); }));
+    if (!logits) LCE_TRY(tok_logits(c, c0, rows, lce::TOK_GRAD, G, c.L.ldp, p));
+    LCE_TRY(tok_grads(c, T, c0, rows, rowscale, Ht, dH, dW, dW_bf16));
   }
   return finish(c);
 }
@@ -1283,7 +1297,7 @@ int distill(const void* H, const void* W, const int64_t* idx, const void* t, int
   if (!aligned(W, 16) || !aligned(H, 16) || !aligned(idx, 8) || !aligned(t, t_bf16 ? 2 : 4) || !aligned(ws, 256) ||
       !aligned(loss, 4) || !aligned(row_loss, 4) || !aligned(grad_loss, 4) || !aligned(dH, 16) || !aligned(dW, 16))
     return LCE_ERR_ALIGNMENT;
-  const TokLayout T = tok_layout(N, d, V, true, with_grad, dW_bf16, &o);
+  const TokLayout T = tok_layout(N, d, V, true, with_grad, dW_bf16, false, &o);
   Call c;
   LCE_TRY(tok_begin(&c, T, H, W, nullptr, N, d, V, o, ws, ws_bytes, stream));
   int* cnt = with_grad ? reinterpret_cast<int*>(c.ws + c.L.dh_cnt) : nullptr;
@@ -1325,7 +1339,7 @@ int distill(const void* H, const void* W, const int64_t* idx, const void* t, int
                                                       (with_grad ? 6.0 * static_cast<double>(V) : 32.0 * K));
     LCE_TRY(timed(c.s, K_COMBINE, bytes,
                   [&] { return cuda_rc(lce::launch_distill_row(a, static_cast<int>(rows), c.s)); }));
-    if (with_grad) LCE_TRY(tok_grads(c, T, c0, rows, dH, dW, dW_bf16));
+    if (with_grad) LCE_TRY(tok_grads(c, T, c0, rows, nullptr, c.H + c0 * d, dH, dW, dW_bf16));
   }
   if (N == 0) LCE_TRY(finalize(c, row_loss, loss));
   return finish(c);
@@ -1341,7 +1355,7 @@ size_t lce_distill_workspace_size(int64_t N, int64_t d, int64_t V, int32_t K, in
   lce_opts_init(&o);
   if (opts) o = *opts;
   if (check_sizes(N, d, V, &o) != LCE_OK || K < 1 || K > LCE_MAX_TOP || (grads & ~LCE_DW_BF16) != 0) return 0;
-  return tok_layout(N, d, V, true, with_grad != 0, (grads & LCE_DW_BF16) != 0, &o).total;
+  return tok_layout(N, d, V, true, with_grad != 0, (grads & LCE_DW_BF16) != 0, false, &o).total;
 }
 
 int lce_distill_forward(const void* H, const void* W, const int64_t* idx, const void* t, int64_t N, int64_t d,

@@ -245,6 +245,7 @@ struct TokParams {
   const float* entropy;  // [rows]
   const float* g_logp;   // [rows] upstream gradients
   const float* g_entropy;  // [rows] or null
+  const float* rowscale;   // [rows] what the row's gradient tile is divided by
   int* flags;
   int reset;             // the first block clears *flags (the call's first launch; k_score reports bad labels)
 };
@@ -267,16 +268,20 @@ struct TokScoreArgs {
 };
 
 struct ScoreGradArgs {
-  int V;
+  int V, d;
   long long ldz, ldg;
   float inv_t;
   long long ignore_index;
-  const int64_t* y;      // [rows], as the next four
+  const int64_t* y;      // [rows], as the next five
+  const float* logp;
   const float* lse;
   const float* entropy;
   const float* g_logp;
   const float* g_entropy;  // or null
-  const float* Z;        // [rows, ldz] logits of the forward
+  float* rowscale;         // [rows] out
+  const uint4* H;          // [rows, d] bf16
+  uint4* Ht;               // [rows, d] bf16(rowscale H) out, or null
+  const float* Z;        // [rows, ldz] logits of the forward, or null: no gradient tile
   __nv_bfloat16* G;      // [rows, ldg]
   // first chunk only (st not null): the status block for N labels y_all and upstream factors of
   // one, and the dH part counters cnt[0, ncnt) cleared
@@ -317,6 +322,7 @@ inline uint32_t few_rows_box(long long rows) { return static_cast<uint32_t>((row
 cudaError_t launch_rows_logits(const CUtensorMap& h, const CUtensorMap& w, int store_z, float* Z, long long ldz,
                                long long V, long long d, const TokParams& ep, int num_sms, cudaStream_t s);
 cudaError_t launch_score(const TokScoreArgs& p, cudaStream_t s);
+// Per row: rowscale and Ht, and with Z the gradient tile too.
 cudaError_t launch_score_grad(const ScoreGradArgs& p, int rows, cudaStream_t s);
 // Clears the status block and cnt[0, ncnt), then counts the rows of idx [N, K] that keep an entry.
 cudaError_t launch_distill_count(const int64_t* idx, const void* t, int t_bf16, long long N, int K, int V,

@@ -86,41 +86,72 @@ __device__ __forceinline__ float log_sum(const RowSum& a) { return logf(a.c) + l
 //                buffer (top alternatives and distillation read them again:
 //                4 bytes a logit, written behind a main loop of d/16 MMAs)
 //   TOK_GRAD     the gradient tile of (logp, entropy) in bf16, from the saved
-//                lse and entropy:
+//                lse and entropy, over the row's scale (see GradRow):
 //                  G_v = ([v = y] a - p_v (a + e (z'_v - lse + entropy))) / T
 //                rounded to bf16 once (the operand type of the two GEMMs that
 //                follow), everything before it in fp32.
 // ----------------------------------------------------------------------------
 // A row of the gradient tile: entries p (c0 + c1 log p) with c0 = -a - e entropy
 // and c1 = -e, and + a at the label (a = g_logp / T where the label is given,
-// e = g_entropy / T). A row without upstream gradient is zero whatever its
-// logits are: masked tokens may hold anything.
+// e = g_entropy / T), all over the row's scale. A row without upstream gradient
+// is zero whatever its logits are: masked tokens may hold anything.
+//
+// The scale is the label's entry: usually by far the row's largest, it is 1 in
+// the tile and not rounded, and dH, multiplied by the scale in fp32 behind its
+// GEMM, is left with the rounding of its result. dW's operand is bf16(scale H):
+// one rounding in place of the label entry's, but of every element on its own
+// and so averaged over the row (errors against fp64, in units of one bf16
+// rounding, 250 rows: dH 1.3-1.6 -> 1.0, bf16 dW 1.3-1.5 -> 1.2-1.3).
 struct GradRow {
   float lse = 0.f, a = 0.f, c0 = 0.f, c1 = 0.f;
-  int y = -1;        // the label, -1 where it is not given
-  bool zero = true;
+  int y = -1;          // the label, -1 where it is not given
+  bool zero = true;    // no upstream gradient
+  bool scaled = false;  // divided by the label's entry, which is then 1
 };
 
-__device__ __forceinline__ GradRow grad_row(int r, const int64_t* labels, long long ignore_index, int V,
-                                            const float* lse, const float* entropy, const float* g_logp,
-                                            const float* g_entropy, float inv_t) {
-  GradRow g;
+struct Upstream {
+  float a, e;  // g_logp (0 where the label is not given) and g_entropy, over T
+  int y;
+};
+
+__device__ __forceinline__ Upstream upstream(int r, const int64_t* labels, long long ignore_index, int V,
+                                             const float* g_logp, const float* g_entropy, float inv_t) {
   const long long y = labels[r];
-  if (y != ignore_index && y >= 0 && y < V) g.y = static_cast<int>(y);
-  if (g.y >= 0) g.a = g_logp[r] * inv_t;
-  const float e = g_entropy != nullptr ? g_entropy[r] * inv_t : 0.f;
-  g.lse = lse[r];
+  Upstream u;
+  u.y = y != ignore_index && y >= 0 && y < V ? static_cast<int>(y) : -1;
+  u.a = u.y >= 0 ? g_logp[r] * inv_t : 0.f;
+  u.e = g_entropy != nullptr ? g_entropy[r] * inv_t : 0.f;
+  return u;
+}
+
+// The label's entry a (1 - p) - p e (log p + entropy), from its log-probability; 1 where there is
+// none or it is too small, or not a number, to divide by.
+__device__ __forceinline__ float row_scale(const Upstream& u, float logp, const float* entropy, int r) {
+  if (u.y < 0) return 1.f;
+  float g = -expm1f(logp) * u.a;
+  if (u.e != 0.f) g -= expf(logp) * u.e * (logp + entropy[r]);
+  const float size = fabsf(g);
+  return size >= 1.0e-30f && size <= 1.0e30f && size >= 1.0e-12f * (fabsf(u.a) + fabsf(u.e)) ? g : 1.f;
+}
+
+__device__ __forceinline__ GradRow grad_row(const Upstream& u, float scale, float lse, const float* entropy, int r) {
+  GradRow g;
+  const float inv = 1.f / scale;
+  g.y = u.y;
+  g.lse = lse;
+  g.a = u.a * inv;
+  g.c1 = -u.e * inv;
   g.c0 = -g.a;
-  g.c1 = -e;
-  if (e != 0.f) g.c0 -= e * entropy[r];
-  g.zero = g.a == 0.f && e == 0.f;
+  if (u.e != 0.f) g.c0 += g.c1 * entropy[r];
+  g.zero = u.a == 0.f && u.e == 0.f;
+  g.scaled = scale != 1.f;
   return g;
 }
 
 __device__ __forceinline__ float grad_entry(float z, float inv_t, const GradRow& r, bool label) {
   const float logp = fmaf(z, inv_t, -r.lse);
   float g = __fmul_rn(ex2_approx(logp * kLog2e), fmaf(r.c1, fmaxf(logp, kFloor), r.c0));
-  if (label) g = __fadd_rn(g, r.a);
+  if (label) g = r.scaled ? 1.f : __fadd_rn(g, r.a);
   return r.zero ? 0.f : g;
 }
 
@@ -219,7 +250,8 @@ struct TokEpi {
     if (m0 + ctx.row0 >= p.rows || vlim <= 0) return;  // nothing of this half tile is stored
     GradRow g;
     if (r < p.rows)
-      g = grad_row(r, p.y, p.ignore_index, p.V, p.lse, p.entropy, p.g_logp, p.g_entropy, p.inv_t);
+      g = grad_row(upstream(r, p.y, p.ignore_index, p.V, p.g_logp, p.g_entropy, p.inv_t), p.rowscale[r], p.lse[r],
+                   p.entropy, r);
     const int ycol = g.y - col0;  // a column of this half tile, or outside [0, 128)
 #pragma unroll 1
     for (int u = 0; u < EPI_COLS / 64; ++u) {
@@ -865,12 +897,15 @@ __global__ void __launch_bounds__(32 * WARPS) k_score(const TokScoreArgs p) {
   }
 }
 
-// The gradient tile of TOK_GRAD from logits kept since the forward: one pass
-// over the row, 4 bytes read and 2 written a logit, in place of the logits
-// GEMM (2 d flops a logit). One block per row; a row whose upstream gradients
-// are zero is written without reading its logits.
+// One block per row: the row's scale, Ht = bf16(scale H), and, from logits kept
+// since the forward (TILE), the gradient tile of TOK_GRAD: one pass over the row,
+// 4 bytes read and 2 written a logit, in place of the logits GEMM (2 d flops a
+// logit; 2048 rows of V = 151936: 302 us, 92% of the copy bandwidth, against 700
+// at d = 2048). A row without upstream gradient is written without reading its
+// logits.
 constexpr int kRowThreads = 32 * kGroups;
 
+template <bool TILE>
 __global__ void __launch_bounds__(kRowThreads, 8) k_score_grad(const ScoreGradArgs p) {
   grid_dep_wait();
   grid_dep_launch();
@@ -889,16 +924,34 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_score_grad(const ScoreGradAr
       p.st->lscale = 1.0;
     }
   }
+  const Upstream u = upstream(r, p.y, p.ignore_index, p.V, p.g_logp, p.g_entropy, p.inv_t);
+  const float scale = row_scale(u, p.logp[r], p.entropy, r);
+  if (tid == 0) p.rowscale[r] = scale;
+  if (p.Ht != nullptr) {
+    const int groups = p.d / 8;
+    const uint4* hr = p.H + static_cast<long long>(r) * groups;
+    uint4* tr = p.Ht + static_cast<long long>(r) * groups;
+    for (int i = tid; i < groups; i += kRowThreads) {
+      const uint4 h = hr[i];
+      const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+      uint32_t o[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        o[q] = pack_bf16x2(__uint_as_float(w[q] << 16) * scale, __uint_as_float(w[q] & 0xffff0000u) * scale);
+      tr[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+  if (!TILE) return;
   const float* z = p.Z + static_cast<long long>(r) * p.ldz;
   __nv_bfloat16* g = p.G + static_cast<long long>(r) * p.ldg;
-  const GradRow row = grad_row(r, p.y, p.ignore_index, p.V, p.lse, p.entropy, p.g_logp, p.g_entropy, p.inv_t);
+  const GradRow row = grad_row(u, scale, p.lse[r], p.entropy, r);
   for (int c = tid * 8; c < p.V; c += kRowThreads * 8) {
     // columns past V (up to 7) lie inside the row's padding: never read by the GEMMs
     uint32_t o[4] = {0u, 0u, 0u, 0u};
     if (!row.zero) {
-      const float4 u = __ldcs(reinterpret_cast<const float4*>(z + c));
+      const float4 x = __ldcs(reinterpret_cast<const float4*>(z + c));
       const float4 w = __ldcs(reinterpret_cast<const float4*>(z + c + 4));
-      float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+      float v[8] = {x.x, x.y, x.z, x.w, w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = grad_entry(v[i], p.inv_t, row, c + i == row.y);
 #pragma unroll
@@ -1174,7 +1227,8 @@ cudaError_t launch_score(const TokScoreArgs& p, cudaStream_t s) {
 
 cudaError_t launch_score_grad(const ScoreGradArgs& p, int rows, cudaStream_t s) {
   if (rows <= 0) return cudaSuccess;
-  return launch_k(k_score_grad, rows, kRowThreads, 0, s, p);
+  return p.Z != nullptr ? launch_k(k_score_grad<true>, rows, kRowThreads, 0, s, p)
+                        : launch_k(k_score_grad<false>, rows, kRowThreads, 0, s, p);
 }
 
 cudaError_t launch_distill_count(const int64_t* idx, const void* t, int t_bf16, long long N, int K, int V,

@@ -15,7 +15,7 @@ Entry points (same names as the C ABI):
   lce_vshard_chunk_stats / lce_vshard_chunk_backward   the same per chunk, the exp tile kept between them
   lce_rmsnorm_forward / lce_rmsnorm_backward / lce_norm_fwd_bwd         the final RMSNorm, alone or fused
   lce_logprobs(H, W, y, top_k=..)        -> logp, lse, entropy, top_logp, top_idx
-  lce_logprobs_backward(H, W, y, lse, entropy, g_logp, g_entropy) -> dH, dW
+  lce_logprobs_backward(H, W, y, logp, lse, entropy, g_logp, g_entropy) -> dH, dW
   lce_distill_forward(H, W, idx, t)      -> loss, row_loss against a teacher's top logits
   lce_distill_fwd_bwd(H, W, idx, t, g)   -> loss, row_loss, dH, dW
   lce_scale_grads, auto_chunk (lce_auto_chunk), workspace_size, read_device_status, profile_begin/end
@@ -159,7 +159,7 @@ def load(path: str | None = None):
         lib.lce_logprobs.restype = I32
         lib.lce_logprobs_backward_workspace_size.argtypes = [I64, I64, I64, I32, OPT]
         lib.lce_logprobs_backward_workspace_size.restype = SZ
-        lib.lce_logprobs_backward.argtypes = [P, P, P, I64, I64, I64, F32, P, P, P, P, P, I32, P, P, OPT, P, SZ, P]
+        lib.lce_logprobs_backward.argtypes = [P, P, P, I64, I64, I64, F32, P, P, P, P, P, P, I32, P, P, OPT, P, SZ, P]
         lib.lce_logprobs_backward.restype = I32
         lib.lce_distill_workspace_size.argtypes = [I64, I64, I64, I32, I32, I32, OPT]
         lib.lce_distill_workspace_size.restype = SZ
@@ -813,41 +813,41 @@ def lce_logprobs(H, W, y, *, top_k: int = 0, temperature: float = 1.0, entropy: 
     return logp, lse, ent, top_logp, top_idx
 
 
-def lce_logprobs_backward(H, W, y, lse, entropy, g_logp, g_entropy=None, *, temperature: float = 1.0, logits=None,
+def lce_logprobs_backward(H, W, y, logp, lse, entropy, g_logp, g_entropy=None, *, temperature: float = 1.0, logits=None,
                           dW=None, dW_dtype=None, need_dH: bool = True, need_dW: bool = True, workspace=None,
                           stream=None, **opt_kw):
     """dH (bf16 [N, d]) and dW (fp32 [V, d], or bf16 with dW_dtype) of
     lce_logprobs' logp and entropy for upstream gradients g_logp and g_entropy
-    (fp32 [N]; g_entropy may be None), from its lse and entropy and, if it kept
-    them, its logits. A gradient that is not wanted is None."""
+    (fp32 [N]; g_entropy may be None), from its logp, lse and entropy and, if it
+    kept them, its logits. A gradient that is not wanted is None."""
     import torch
     N, d, V = _check_inputs(H, W, y)
-    for name, t in (("lse", lse), ("g_logp", g_logp)):
+    for name, t in (("logp", logp), ("lse", lse), ("g_logp", g_logp)):
         if t is None:
             raise ValueError(f"{name} is required")
     if g_entropy is not None and entropy is None:
         raise ValueError("g_entropy needs the entropy of lce_logprobs")
-    for name, t in (("lse", lse), ("entropy", entropy), ("g_logp", g_logp), ("g_entropy", g_entropy)):
+    for name, t in (("logp", logp), ("lse", lse), ("entropy", entropy), ("g_logp", g_logp), ("g_entropy", g_entropy)):
         _check_dev(t, name, torch.float32, shape=(N,), device=H.device)
     if logits is not None:
         _check_dev(logits, "logits", torch.float32, shape=(N, (V + 255) // 256 * 256), device=H.device)
-    return _logprobs_backward(H, W, y, lse, entropy, g_logp, g_entropy, logits, temperature, _dW_mode(dW_dtype), dW,
-                              need_dH, need_dW, workspace, stream, opt_kw)
+    return _logprobs_backward(H, W, y, logp, lse, entropy, g_logp, g_entropy, logits, temperature,
+                              _dW_mode(dW_dtype), dW, need_dH, need_dW, workspace, stream, opt_kw)
 
 
-def _logprobs_backward(H, W, y, lse, entropy, g_logp, g_entropy, logits, temperature, grads, dW, need_dH, need_dW,
-                       workspace, stream, opt_kw):
+def _logprobs_backward(H, W, y, logp, lse, entropy, g_logp, g_entropy, logits, temperature, grads, dW, need_dH,
+                       need_dW, workspace, stream, opt_kw):
     """lce_logprobs_backward on tensors that are known to fit each other (those
     of a forward that checked them)."""
     (N, d), V = H.shape, W.shape[0]
     opts, ws = _token_plan(opt_kw, N, "lce_logprobs_backward", H.device, workspace,
                            lambda o: lce_logprobs_backward_workspace_size(N, d, V, grads, o))
     dH, dW = _token_grads(H, V, d, opts, grads, dW, need_dH, need_dW)
-    rc = load().lce_logprobs_backward(_ptr(H), _ptr(W), _ptr(y), N, d, V, float(temperature), _ptr(lse),
+    rc = load().lce_logprobs_backward(_ptr(H), _ptr(W), _ptr(y), N, d, V, float(temperature), _ptr(logp), _ptr(lse),
                                       _ptr(entropy), _ptr(g_logp), _ptr(g_entropy), _ptr(logits), grads, _ptr(dH),
                                       _ptr(dW), ctypes.byref(opts), _ptr(ws), ws.numel(), _stream(stream))
     _raise(rc, "lce_logprobs_backward")
-    _keep(stream, H, W, y, ws, lse, entropy, g_logp, g_entropy, logits, dH, dW)
+    _keep(stream, H, W, y, ws, logp, lse, entropy, g_logp, g_entropy, logits, dH, dW)
     return dH, dW
 
 

@@ -325,13 +325,14 @@ int lce_scale_grads(void* dH, float* dW, int64_t N, int64_t d, int64_t V, const 
  * of top_k = 0 is enough).
  *
  * lce_logprobs_backward: gradients from upstream g_logp [N] and g_entropy [N]
- * (fp32; g_entropy may be NULL: zero), with lse and entropy of lce_logprobs on
- * the same inputs (entropy may be NULL if g_entropy is). With a_i = g_logp_i (0
+ * (fp32; g_entropy may be NULL: zero), with logp, lse and entropy of lce_logprobs
+ * on the same inputs (entropy may be NULL if g_entropy is). With a_i = g_logp_i (0
  * where y_i is ignored) and e_i = g_entropy_i
  *   G_iv = ([v = y_i] a_i - p_iv (a_i + e_i (log p_iv + entropy_i))) / temperature
  *   dH = G W (bf16), dW = G^T H (fp32; added to with opts->accumulate_dW).
- * G is rounded to bf16 once; a row whose upstream gradients are zero is zero in
- * G and dH whatever its logits are. Either of dH, dW may be NULL: not wanted, not
+ * G is held in bf16 over a scale per row, its label's entry, by which dH is
+ * multiplied in fp32; dW is its product with bf16(scale H). A row whose upstream
+ * gradients are zero is zero in G and dH whatever its logits are. Either of dH, dW may be NULL: not wanted, not
  * computed. grads: 0, or LCE_DW_BF16: dW is bf16 [V, d], the fp32 sum rounded
  * once (not with accumulate_dW; several chunks are summed in fp32 in the
  * workspace). logits: those of lce_logprobs, or NULL: recomputed chunk by
@@ -346,9 +347,9 @@ int lce_logprobs(const void* H, const void* W, const int64_t* y, int64_t N, int6
                  float* logits, const lce_opts* opts, void* ws, size_t ws_bytes, void* stream);
 size_t lce_logprobs_backward_workspace_size(int64_t N, int64_t d, int64_t V, int32_t grads, const lce_opts* opts);
 int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
-                          float temperature, const float* lse, const float* entropy, const float* g_logp,
-                          const float* g_entropy, const float* logits, int32_t grads, void* dH, void* dW,
-                          const lce_opts* opts, void* ws, size_t ws_bytes, void* stream);
+                          float temperature, const float* logp, const float* lse, const float* entropy,
+                          const float* g_logp, const float* g_entropy, const float* logits, int32_t grads, void* dH,
+                          void* dW, const lce_opts* opts, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Distillation from a teacher's top logits: per row, K tokens idx [N, K]

@@ -146,15 +146,16 @@ def test_logprobs_refusals(lib):
 def test_logprobs_backward_refusals(lib):
     E, P = lce, FAKE
 
-    def call(lse=P, ent=P, g1=P, g2=P, kept=None, grads=0, dH=P, dW=P, T=1.0, N=64, acc=False, nbytes=1 << 40):
+    def call(logp=P, lse=P, ent=P, g1=P, g2=P, kept=None, grads=0, dH=P, dW=P, T=1.0, N=64, acc=False,
+             nbytes=1 << 40):
         o = lce.make_opts(accumulate_dW=acc, chunk_tokens=32)
-        return lib.lce_logprobs_backward(P, P, P, N, 64, 1000, T, lse, ent, g1, g2, kept, grads, dH, dW,
+        return lib.lce_logprobs_backward(P, P, P, N, 64, 1000, T, logp, lse, ent, g1, g2, kept, grads, dH, dW,
                                          ctypes.byref(o), P, nbytes, None)
 
-    for bad in (dict(lse=None), dict(g1=None), dict(ent=None), dict(dH=None, dW=None), dict(T=0.0), dict(N=-2),
+    for bad in (dict(logp=None), dict(lse=None), dict(g1=None), dict(ent=None), dict(dH=None, dW=None), dict(T=0.0), dict(N=-2),
                 dict(grads=2), dict(grads=E.LCE_DW_BF16, acc=True)):
         assert call(**bad) == E.LCE_ERR_INVALID_ARG, bad
-    for bad in (dict(kept=P + 4), dict(lse=P + 2), dict(ent=P + 2), dict(g1=P + 2), dict(g2=P + 1), dict(dH=P + 8), dict(dW=P + 4)):
+    for bad in (dict(kept=P + 4), dict(logp=P + 1), dict(lse=P + 2), dict(ent=P + 2), dict(g1=P + 2), dict(g2=P + 1), dict(dH=P + 8), dict(dW=P + 4)):
         assert call(**bad) == E.LCE_ERR_ALIGNMENT, bad
     o = lce.make_opts(chunk_tokens=32)
     sizes = [lce.lce_logprobs_backward_workspace_size(64, 64, 1000, g, o) for g in (0, E.LCE_DW_BF16)]
@@ -228,7 +229,7 @@ def test_binding_refuses_cpu_tensors_and_bad_modes():
     H, W = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(3, 8, dtype=torch.bfloat16)
     y, f = torch.zeros(4, dtype=torch.int64), torch.zeros(4)
     idx, t = torch.zeros(4, 2, dtype=torch.int64), torch.zeros(4, 2)
-    for call in (lambda: lce.lce_logprobs(H, W, y), lambda: lce.lce_logprobs_backward(H, W, y, f, f, f),
+    for call in (lambda: lce.lce_logprobs(H, W, y), lambda: lce.lce_logprobs_backward(H, W, y, f, f, f, f),
                  lambda: lce.lce_distill_forward(H, W, idx, t), lambda: lce.lce_distill_fwd_bwd(H, W, idx, t)):
         with pytest.raises(ValueError, match="CUDA tensors"):
             call()

@@ -16,10 +16,12 @@ u = 2^-8 (bf16):
                ln V <= 12: 13 times the bound above
   gradients    each entry of G is rounded to bf16 once (u), its factors err by
                less than 2^-10 relative (lse and entropy as above, up to 13
-               nats): every element of dW lies within (u + 2^-10) bulk, bulk the
-               sum of the absolute terms it is made of, of dH within that plus
-               its own rounding u |dH|; whole tensors within 5e-3 (rounding
-               errors average: 2 u / sqrt(3)).
+               nats): every element of distillation's dW lies within (u + 2^-10)
+               bulk, bulk the sum of the absolute terms it is made of; dW of
+               log-probabilities within (2 u + u^2 + 2^-10) bulk, its other
+               operand bf16(scale H) being rounded as well; dH within (u + 2^-10)
+               bulk plus its own rounding u |dH|; whole tensors within 5e-3
+               (rounding errors average: u / sqrt(3) each).
 """
 import numpy as np
 import pytest
@@ -91,12 +93,14 @@ def check_scores(out, H, W, y, T, K):
     return ref
 
 
-def check_grads(dH, dW, ref):
+def check_grads(dH, dW, ref, scaled=False):
+    """scaled: dW's second operand is rounded too (log-probabilities)."""
     for got, name in ((dH, "dH"), (dW, "dW")):
         if got is None:
             continue
-        out = U * np.abs(ref[name]) if name == "dH" else 0.0
-        close(got, ref[name], (U + 2.0 ** -10) * ref[name + "_bulk"] + out + 1e-30, name)
+        u = 2 * U + U * U if scaled and name == "dW" else U
+        out = U * np.abs(ref[name]) if got.dtype == _torch().bfloat16 else 0.0
+        close(got, ref[name], (u + 2.0 ** -10) * ref[name + "_bulk"] + out + 1e-30, name)
         norm = np.linalg.norm(ref[name])
         assert np.linalg.norm(np64(got) - ref[name]) <= 5e-3 * norm, name
 
@@ -223,7 +227,7 @@ def test_logprobs_no_tokens(cuda_lib):
     y = torch.zeros(0, dtype=torch.int64, device="cuda")
     logp, lse, ent, tl, ti = cuda_lib.lce_logprobs(H, W, y, top_k=3)
     assert logp.shape == lse.shape == ent.shape == (0,) and tl.shape == ti.shape == (0, 3)
-    dH, dW = cuda_lib.lce_logprobs_backward(H, W, y, lse, ent, logp, ent)
+    dH, dW = cuda_lib.lce_logprobs_backward(H, W, y, logp, lse, ent, logp, ent)
     assert dH.shape == (0, 64) and not dW.any()
     idx = torch.zeros(0, 4, dtype=torch.int64, device="cuda")
     loss, row, dH, dW = cuda_lib.lce_distill_fwd_bwd(H, W, idx, idx.float())
@@ -263,12 +267,12 @@ def test_logprobs_backward(cuda_lib, N, d, V, T, chunk):
     g1, g2 = rng.standard_normal(N).astype(np.float32) / N, rng.standard_normal(N).astype(np.float32) / N
     kw = dict(temperature=T, chunk_tokens=chunk)
     logp, lse, ent, _, _ = cuda_lib.lce_logprobs(Ht, Wt, dev(y), **kw)
-    dH, dW = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), lse, ent, dev(g1), dev(g2), sync_check=True, **kw)
-    check_grads(dH, dW, oracle.logprobs_backward_f64(H, W, y, g1, g2, temperature=T))
+    dH, dW = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), logp, lse, ent, dev(g1), dev(g2), sync_check=True, **kw)
+    check_grads(dH, dW, oracle.logprobs_backward_f64(H, W, y, g1, g2, temperature=T), scaled=True)
     # one gradient at a time gives the same values
-    only_H, none = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), lse, ent, dev(g1), dev(g2), need_dW=False, **kw)
+    only_H, none = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), logp, lse, ent, dev(g1), dev(g2), need_dW=False, **kw)
     assert none is None and torch.equal(only_H, dH)
-    none, only_W = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), lse, ent, dev(g1), dev(g2), need_dH=False, **kw)
+    none, only_W = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), logp, lse, ent, dev(g1), dev(g2), need_dH=False, **kw)
     assert none is None and torch.equal(only_W, dW)
     # from logits that the forward kept; a bf16 dW
     kept = torch.empty(N, cuda_lib.lce_logits_stride(V), device="cuda")
@@ -277,17 +281,17 @@ def test_logprobs_backward(cuda_lib, N, d, V, T, chunk):
     for a, b in zip(again[:3], (logp, lse, ent)):
         close(a, np64(b), 2.0 ** -20 * (1 + np.abs(np64(b))), "with kept logits")
     for dt in (torch.float32, torch.bfloat16):
-        dH2, dW2 = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), lse, ent, dev(g1), dev(g2), logits=kept, dW_dtype=dt,
+        dH2, dW2 = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), logp, lse, ent, dev(g1), dev(g2), logits=kept, dW_dtype=dt,
                                                   **kw)
         assert torch.equal(dH2, dH) and torch.equal(dW2, dW.to(dt))
-    dH2, dW2 = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), lse, ent, dev(g1), dev(g2), dW_dtype=torch.bfloat16, **kw)
+    dH2, dW2 = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), logp, lse, ent, dev(g1), dev(g2), dW_dtype=torch.bfloat16, **kw)
     assert torch.equal(dH2, dH) and torch.equal(dW2, dW.bfloat16())
     # without the entropy's share; added to a dW that is there
     ref = oracle.logprobs_backward_f64(H, W, y, g1, None, temperature=T)
-    dH, dW = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), lse, None, dev(g1), **kw)
-    check_grads(dH, dW, ref)
+    dH, dW = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), logp, lse, None, dev(g1), **kw)
+    check_grads(dH, dW, ref, scaled=True)
     base = torch.ones(V, d, device="cuda")
-    _, acc = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), lse, None, dev(g1), dW=base, accumulate_dW=True, **kw)
+    _, acc = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), logp, lse, None, dev(g1), dW=base, accumulate_dW=True, **kw)
     # the sum with 1 rounds to fp32 once per chunk
     close(acc, 1.0 + np64(dW), 2.0 ** -23 * (1 + (N // chunk if chunk else 0)) * (1 + np.abs(np64(dW))) + 1e-7, "dW added")
 
@@ -308,8 +312,8 @@ def test_masked_rows_of_nan_have_zero_gradients(cuda_lib, keep):
     kept = torch.empty(150, 1024, device="cuda") if keep else None
 
     def run(h):
-        _, lse, ent, _, _ = cuda_lib.lce_logprobs(h, Wt, dev(y), logits=kept)
-        return cuda_lib.lce_logprobs_backward(h, Wt, dev(y), lse, ent, dev(g1), dev(g2), logits=kept, need_dW=False)[0]
+        logp, lse, ent, _, _ = cuda_lib.lce_logprobs(h, Wt, dev(y), logits=kept)
+        return cuda_lib.lce_logprobs_backward(h, Wt, dev(y), logp, lse, ent, dev(g1), dev(g2), logits=kept, need_dW=False)[0]
 
     want = run(Ht)
     Ht[3], Ht[77], Ht[149, 5] = float("nan"), float("inf"), -float("inf")
@@ -451,13 +455,11 @@ def test_autograd_modules(cuda_lib):
     dH, dW = torch.autograd.grad((logp * w).sum() - 0.5 * ent.sum(), [Ht, Wt])
     assert dH.dtype == dW.dtype == torch.bfloat16
     ref = oracle.logprobs_backward_f64(H, W, y, np64(w), np.full(200, -0.5), temperature=0.8)
-    check_grads(dH, None, ref)
-    close(dW, ref["dW"], (U + 2.0 ** -10) * ref["dW_bulk"] + U * np.abs(ref["dW"]), "dW in bf16")
+    check_grads(dH, dW, ref, scaled=True)
     for recompute in (True, False):   # the same from recomputed and from kept logits
         logp, ent = FusedLinearLogProbs(temperature=0.8, recompute=recompute, chunk_tokens=96)(Ht, Wt, dev(y))
         a, b = torch.autograd.grad((logp * w).sum() - 0.5 * ent.sum(), [Ht, Wt])
-        check_grads(a, None, ref)
-        close(b, ref["dW"], (U + 2.0 ** -10) * ref["dW_bulk"] + U * np.abs(ref["dW"]), "dW in bf16")
+        check_grads(a, b, ref, scaled=True)
     # outputs used alone; a frozen head
     logp, ent = FusedLinearLogProbs()(Ht, Wt.detach(), dev(y))
     check_grads(torch.autograd.grad(logp.sum(), Ht)[0], None,
@@ -498,7 +500,7 @@ def test_streams_graphs_and_a_shared_workspace(cuda_lib, N):
 
     def score(h):
         out = cuda_lib.lce_logprobs(h, Wt, yt, top_k=5, workspace=ws)
-        return list(out) + list(cuda_lib.lce_logprobs_backward(h, Wt, yt, out[1], out[2], g1, g1, workspace=ws))
+        return list(out) + list(cuda_lib.lce_logprobs_backward(h, Wt, yt, out[0], out[1], out[2], g1, g1, workspace=ws))
 
     def kd(h):
         return list(cuda_lib.lce_distill_fwd_bwd(h, Wt, it, tt, workspace=ws))
@@ -556,11 +558,11 @@ def test_caller_tensors_are_checked(cuda_lib):
     t = torch.zeros(20, 4, device="cuda")
     for call in (lambda: cuda_lib.lce_logprobs(Ht.float(), Wt, yt), lambda: cuda_lib.lce_logprobs(Ht.t(), Wt, yt),
                  lambda: cuda_lib.lce_logprobs(Ht, Wt, yt.int()),
-                 lambda: cuda_lib.lce_logprobs_backward(Ht, Wt, yt, f[:5], f, f),
-                 lambda: cuda_lib.lce_logprobs_backward(Ht, Wt, yt, f, None, f, f),
-                 lambda: cuda_lib.lce_logprobs_backward(Ht, Wt, yt, f, f, f.double()),
-                 lambda: cuda_lib.lce_logprobs_backward(Ht, Wt, yt, f, f, f, need_dH=False, need_dW=False),
-                 lambda: cuda_lib.lce_logprobs_backward(Ht, Wt, yt, f, f, f, accumulate_dW=True),
+                 lambda: cuda_lib.lce_logprobs_backward(Ht, Wt, yt, f, f[:5], f, f),
+                 lambda: cuda_lib.lce_logprobs_backward(Ht, Wt, yt, f, f, None, f, f),
+                 lambda: cuda_lib.lce_logprobs_backward(Ht, Wt, yt, f, f, f, f.double()),
+                 lambda: cuda_lib.lce_logprobs_backward(Ht, Wt, yt, f, f, f, f, need_dH=False, need_dW=False),
+                 lambda: cuda_lib.lce_logprobs_backward(Ht, Wt, yt, f, f, f, f, accumulate_dW=True),
                  lambda: cuda_lib.lce_distill_forward(Ht, Wt, idx.int(), t),
                  lambda: cuda_lib.lce_distill_forward(Ht, Wt, idx, t.half()),
                  lambda: cuda_lib.lce_distill_forward(Ht, Wt, idx, t[:, :3]),
@@ -601,9 +603,9 @@ def _child():
             out = lce.lce_logprobs(Ht, Wt, dev(y), top_k=K, **kw)
             check_scores(out, H, W, y, 1.0, K)
             for dt in (torch.float32, torch.bfloat16):
-                dH, dW = lce.lce_logprobs_backward(Ht, Wt, dev(y), out[1], out[2], g, g, dW_dtype=dt, **kw)
+                dH, dW = lce.lce_logprobs_backward(Ht, Wt, dev(y), out[0], out[1], out[2], g, g, dW_dtype=dt, **kw)
                 check_grads(dH, dW if dt == torch.float32 else None,
-                            oracle.logprobs_backward_f64(H, W, y, np64(g), np64(g)))
+                            oracle.logprobs_backward_f64(H, W, y, np64(g), np64(g)), scaled=True)
         lce.lce_logprobs(Ht, Wt, dev(y), chunk_tokens=chunk, sync_check=True)
         out = lce.lce_distill_fwd_bwd(Ht, Wt, dev(idx), dev(t), chunk_tokens=chunk, sync_check=True)
         check_grads(out[2], out[3], oracle.distill_f64(H, W, idx, t))
