@@ -1301,15 +1301,25 @@ int distill(const void* H, const void* W, const int64_t* idx, const void* t, int
   Call c;
   LCE_TRY(tok_begin(&c, T, H, W, nullptr, N, d, V, o, ws, ws_bytes, stream));
   int* cnt = with_grad ? reinterpret_cast<int*>(c.ws + c.L.dh_cnt) : nullptr;
-  LCE_TRY(timed(c.s, K_PREPARE, static_cast<double>(N) * K * (t_bf16 ? 10.0 : 12.0), [&] {
-    return cuda_rc(lce::launch_distill_count(idx, t, t_bf16, N, K, static_cast<int>(V), o.ignore_index, c.st, cnt,
-                                             with_grad ? c.L.dh_ncnt : 0, c.dev.num_sms, c.s));
-  }));
+  const int ncnt = with_grad ? c.L.dh_ncnt : 0;
+  // With one chunk its rows count themselves, before the GEMMs that need n; with several n is
+  // needed by the first chunk's.
+  const bool count_here = !lce::kChecks && c.L.chunks == 1;
+  if (!count_here)
+    LCE_TRY(timed(c.s, K_PREPARE, static_cast<double>(N) * K * (t_bf16 ? 10.0 : 12.0), [&] {
+      return cuda_rc(lce::launch_distill_count(idx, t, t_bf16, N, K, static_cast<int>(V), o.ignore_index, c.st, cnt,
+                                               ncnt, c.dev.num_sms, c.s));
+    }));
   if (N == 0 && with_grad) LCE_TRY(zero_dW(c, dW, dW_bf16));
   float* Z = reinterpret_cast<float*>(c.ws + T.Z);
   for (int64_t c0 = 0; c0 < N; c0 += c.L.C) {
     const int64_t rows = (N - c0) < c.L.C ? (N - c0) : c.L.C;
-    const lce::TokParams p = tok_params(c, c0, rows, temperature);
+    lce::TokParams p = tok_params(c, c0, rows, temperature);
+    if (count_here) {
+      p.clear_st = c.st;
+      p.cnt = cnt;
+      p.ncnt = ncnt;
+    }
     LCE_TRY(tok_logits(c, c0, rows, lce::TOK_STATS_Z, Z, T.ldz, p));
     lce::DistillArgs a;
     std::memset(&a, 0, sizeof a);
@@ -1319,6 +1329,7 @@ int distill(const void* H, const void* W, const int64_t* idx, const void* t, int
     a.renormalize = (teacher & LCE_TEACHER_LOGPROBS) ? 0 : 1;
     a.mean = o.reduction == LCE_MEAN ? 1 : 0;
     a.t_bf16 = t_bf16;
+    a.count_here = count_here ? 1 : 0;
     a.ldz = T.ldz;
     a.ldg = c.L.ldp;
     a.inv_t = p.inv_t;

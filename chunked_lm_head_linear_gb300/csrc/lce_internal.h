@@ -248,6 +248,9 @@ struct TokParams {
   const float* rowscale;   // [rows] what the row's gradient tile is divided by
   int* flags;
   int reset;             // the first block clears *flags (the call's first launch; k_score reports bad labels)
+  DevStatus* clear_st;   // not null: the first block clears the status block and cnt[0, ncnt) (distillation)
+  int* cnt;
+  int ncnt;
 };
 
 struct TokScoreArgs {
@@ -295,6 +298,7 @@ struct ScoreGradArgs {
 struct DistillArgs {
   int V, K, nparts;
   int renormalize, mean, t_bf16;
+  int count_here;        // one chunk: the rows themselves count the kept ones, and the last sets the scales
   long long ldz, ldg;
   float inv_t;
   long long ignore_index, n_override;

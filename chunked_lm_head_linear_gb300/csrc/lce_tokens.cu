@@ -155,11 +155,29 @@ __device__ __forceinline__ float grad_entry(float z, float inv_t, const GradRow&
   return r.zero ? 0.f : g;
 }
 
-// The first launch of a call clears the status word from its first block, before anything can have
-// been reported: a wait that gives up does so after two seconds, a bad label is reported by a later
-// kernel. (The checked build, whose blocks may report an index at once, clears it by a launch.)
-__device__ __forceinline__ void reset_flags(const TokParams& p) {
-  if (p.reset && blockIdx.x == 0 && threadIdx.x == 32 * EPI_WARP0) *p.flags = 0;
+__device__ __forceinline__ void clear_status(DevStatus* st, int* cnt, int ncnt, int thread, int threads) {
+  for (int i = thread; i < ncnt; i += threads) cnt[i] = 0;
+  if (thread == 0) {
+    st->flags = 0;
+    st->rows_done = 0;
+    st->n_valid = 0;
+    st->n_counted = 0;
+    st->gscale = 0.f;
+    st->lscale = 0.0;
+  }
+}
+
+// The first launch of a call clears the status word (or block) from its first block's epilogue warps,
+// before anything can have been reported: a wait that gives up does so after two seconds, a bad label
+// is reported by a later kernel. (The checked build, whose blocks may report an index at once, clears
+// it by a launch.)
+__device__ __forceinline__ void reset_status(const TokParams& p) {
+  if (blockIdx.x != 0) return;
+  const int thread = static_cast<int>(threadIdx.x) - 32 * EPI_WARP0;
+  if (p.clear_st != nullptr)
+    clear_status(p.clear_st, p.cnt, p.ncnt, thread, 32 * EPI_WARPS);
+  else if (p.reset && thread == 0)
+    *p.flags = 0;
 }
 
 template <int MODE>
@@ -310,7 +328,7 @@ struct TokProb {
   static __device__ __forceinline__ uint64_t a_desc(int, uint32_t addr, int k) { return desc_k_major(addr, k); }
   static __device__ __forceinline__ uint64_t b_desc(int, uint32_t addr, int k) { return desc_k_major(addr, k); }
   static __device__ __forceinline__ uint32_t idesc(int) { return idesc_bf16_f32(P_TILE_M, BN, false, false); }
-  static __device__ __forceinline__ void init(const Params& p, State&) { reset_flags(p.ep); }
+  static __device__ __forceinline__ void init(const Params& p, State&) { reset_status(p.ep); }
   static __device__ __forceinline__ void epilogue(const Params& p, State&, const TileJob&, EpiCtx ctx, int m0,
                                                   int col0, uint32_t taddr) {
     ctx.out = &p.c;
@@ -535,7 +553,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_rows_logits(const __grid_con
     const float k = e.inv_t * kLog2e;
     int acc = 0;
     uint32_t acc_phase = 0;
-    reset_flags(e);
+    reset_status(e);
     for (int t = blockIdx.x; t < p.tiles; t += gridDim.x) {
       // The four warps agree on whether the tile came (a wait that ran out in one ends the loop of
       // all, so that none is left at the barrier below); everyone has read the tile before by then.
@@ -968,23 +986,11 @@ __device__ __forceinline__ float teacher_value(const void* t, int bf16, long lon
   return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(t)[i]) : static_cast<const float*>(t)[i];
 }
 
-__device__ __forceinline__ void clear_status(DevStatus* st, int* cnt, int ncnt) {
-  for (int i = threadIdx.x; i < ncnt; i += blockDim.x) cnt[i] = 0;
-  if (threadIdx.x == 0) {
-    st->flags = 0;
-    st->rows_done = 0;
-    st->n_valid = 0;
-    st->n_counted = 0;
-    st->gscale = 0.f;
-    st->lscale = 0.0;
-  }
-}
-
 // Clears the status block and the dH part counters; k_distill_count adds into them.
 __global__ void __launch_bounds__(1024) k_distill_init(DevStatus* st, int* cnt, int ncnt) {
   grid_dep_wait();
   grid_dep_launch();
-  clear_status(st, cnt, ncnt);
+  clear_status(st, cnt, ncnt, threadIdx.x, blockDim.x);
 }
 
 // Rows with at least one kept entry (an index in [0, V) whose teacher value is
@@ -998,7 +1004,7 @@ __global__ void __launch_bounds__(1024) k_distill_count(const int64_t* __restric
   grid_dep_wait();
   grid_dep_launch();
   __shared__ int s_cnt, s_bad;
-  if (gridDim.x == 1) clear_status(st, cnt, ncnt);
+  if (gridDim.x == 1) clear_status(st, cnt, ncnt, threadIdx.x, blockDim.x);
   if (threadIdx.x == 0) s_cnt = s_bad = 0;
   __syncthreads();
   const int lane = threadIdx.x & 31;
@@ -1045,14 +1051,29 @@ __device__ __forceinline__ float block_max(float v, float* red) {
   return s;
 }
 
+// n, 1/n (1 for a sum) and the factor of the GEMMs behind, g T / n.
+__device__ __forceinline__ double set_scales(const DistillArgs& p, long long counted, bool write) {
+  const long long n = p.n_override >= 0 ? p.n_override : counted;
+  const double weight = p.mean ? (n > 0 ? 1.0 / static_cast<double>(n) : 0.0) : 1.0;
+  if (write) {
+    const float up = p.grad_loss != nullptr ? *p.grad_loss : 1.f;
+    p.st->n_valid = n;
+    p.st->gscale = static_cast<float>(static_cast<double>(up) * weight / static_cast<double>(p.inv_t));
+  }
+  return weight;
+}
+
 // Writes the row's loss; the block that counts the call's last row sums them
-// all in fp64, in an order that does not depend on which block that is.
-__device__ __forceinline__ void finish_row(const DistillArgs& p, int r, float loss, double weight) {
+// all in fp64, in an order that does not depend on which block that is. With
+// one chunk n is known only then (whole numbers, so their order does not
+// change it), and that block sets the scales.
+__device__ __forceinline__ void finish_row(const DistillArgs& p, int r, float loss, bool kept) {
   __shared__ int s_last;
   __shared__ double s_sum[kRowThreads];
   const int tid = threadIdx.x;
   if (tid == 0) {
     p.row_loss[r] = loss;
+    if (p.count_here && kept) atomicAdd(reinterpret_cast<unsigned long long*>(&p.st->n_counted), 1ull);
     __threadfence();
     s_last = atomicAdd(&p.st->rows_done, 1) == static_cast<int>(p.N - 1);
   }
@@ -1067,7 +1088,10 @@ __device__ __forceinline__ void finish_row(const DistillArgs& p, int r, float lo
     if (tid < w) s_sum[tid] += s_sum[tid + w];
     __syncthreads();
   }
-  if (tid == 0) *p.loss = static_cast<float>(s_sum[0] * weight);
+  if (tid == 0) {
+    const long long counted = __ldcg(&p.st->n_counted);
+    *p.loss = static_cast<float>(s_sum[0] * set_scales(p, counted, p.count_here != 0));
+  }
 }
 
 // One block per row of the chunk. The row's partial sums give lse; the K entries
@@ -1091,14 +1115,8 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_distill_row(const DistillArg
   const float* z = p.Z + static_cast<long long>(r) * p.ldz;
   __nv_bfloat16* g = GRAD ? p.G + static_cast<long long>(r) * p.ldg : nullptr;
 
-  // n is known since the count ran; the first row of a chunk sets the GEMMs' scale
-  const long long n = p.n_override >= 0 ? p.n_override : p.st->n_counted;
-  const double weight = p.mean ? (n > 0 ? 1.0 / static_cast<double>(n) : 0.0) : 1.0;
-  if (r == 0 && tid == 0) {
-    const float up = p.grad_loss != nullptr ? *p.grad_loss : 1.f;
-    p.st->n_valid = n;
-    p.st->gscale = static_cast<float>(static_cast<double>(up) * weight / static_cast<double>(p.inv_t));
-  }
+  // several chunks: n is known since the count ran, and the first row of each sets the scales
+  if (!p.count_here && r == 0 && tid == 0) set_scales(p, p.st->n_counted, true);
 
   // the teacher's entry of this thread
   const long long at = static_cast<long long>(r) * p.K + tid;
@@ -1106,14 +1124,16 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_distill_row(const DistillArg
   float tv = -INFINITY;
   if (tid < p.K) {
     const long long v = p.idx[at];
-    if (v != p.ignore_index && v >= 0 && v < p.V) {
+    if (v >= 0 && v < p.V && v != p.ignore_index) {
       tv = teacher_value(p.t, p.t_bf16, at);
       if (!(tv == -INFINITY)) vi = static_cast<int>(v);
+    } else if (v != p.ignore_index && p.count_here) {
+      atomicOr(&p.st->flags, kFlagLabelRange);
     }
   }
   const bool kept = __syncthreads_or(vi >= 0) != 0;
   if (!kept) {  // nothing of the teacher in this row: no loss, a zero gradient
-    finish_row(p, r, 0.f, weight);
+    finish_row(p, r, 0.f, false);
     if (GRAD)
       for (int c = tid * 8; c < p.V; c += kRowThreads * 8) *reinterpret_cast<uint4*>(g + c) = make_uint4(0, 0, 0, 0);
     return;
@@ -1156,7 +1176,7 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_distill_row(const DistillArg
     if (q > 0.f || q != q) term = q * (logq - (zk - M) * p.inv_t + logs);
   }
   const float loss = block_sum(term, red);
-  finish_row(p, r, loss / (p.inv_t * p.inv_t), weight);
+  finish_row(p, r, loss / (p.inv_t * p.inv_t), true);
   if (!GRAD) return;
 
   const float k = p.inv_t * kLog2e, w = mass / (acc.c + acc.s);
