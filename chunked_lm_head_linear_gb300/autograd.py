@@ -86,7 +86,7 @@ class _LogProbs(torch.autograd.Function):
     def forward(ctx, H, W, y, temperature, keep, opts):
         logits = None
         if keep and (ctx.needs_input_grad[0] or ctx.needs_input_grad[1]):
-            logits = torch.empty((H.shape[0], lce.lce_logits_stride(W.shape[0])), dtype=torch.float32, device=H.device)
+            logits = torch.empty((H.shape[0], (W.shape[0] + 255) // 256 * 256), dtype=torch.float32, device=H.device)
         logp, lse, entropy, _, _ = lce.lce_logprobs(H, W, y, temperature=temperature, logits=logits, **opts)
         ctx.save_for_backward(H, W, y, logp, lse, entropy, logits)
         ctx.temperature, ctx.opts = temperature, opts
