@@ -1153,7 +1153,7 @@ int lce_logprobs(const void* H, const void* W, const int64_t* y, int64_t N, int6
   if (opts) o = *opts;
   LCE_TRY(check_sizes(N, d, V, &o));
   LCE_TRY(check_token_args(V, temperature));
-  if (o.reserved != 0 || top_k < 0 || top_k > LCE_MAX_TOP || top_k > V) return LCE_ERR_INVALID_ARG;
+  if (top_k < 0 || top_k > LCE_MAX_TOP || top_k > V) return LCE_ERR_INVALID_ARG;
   if (!W || !ws || (N > 0 && (!H || !y || !logp || !lse || (top_k > 0 && (!top_logp || !top_idx)))))
     return LCE_ERR_INVALID_ARG;
   if (!aligned(W, 16) || !aligned(H, 16) || !aligned(y, 8) || !aligned(ws, 256) || !aligned(logp, 4) ||
@@ -1168,6 +1168,7 @@ int lce_logprobs(const void* H, const void* W, const int64_t* y, int64_t N, int6
     const int64_t rows = (N - c0) < c.L.C ? (N - c0) : c.L.C;
     lce::TokParams p = tok_params(c, c0, rows, temperature);
     p.reset = !lce::kChecks && c0 == 0;
+    p.no_loads = o.reserved == LCE_TEST_FORCE_TIMEOUT ? 1 : 0;
     float* Z = logits ? logits + c0 * T.ldz : top_k > 0 ? reinterpret_cast<float*>(c.ws + T.Z) : nullptr;
     LCE_TRY(tok_logits(c, c0, rows, Z ? lce::TOK_STATS_Z : lce::TOK_STATS, Z, T.ldz, p));
     lce::TokScoreArgs a;

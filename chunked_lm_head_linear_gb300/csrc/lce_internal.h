@@ -251,6 +251,7 @@ struct TokParams {
   DevStatus* clear_st;   // not null: the first block clears the status block and cnt[0, ncnt) (distillation)
   int* cnt;
   int ncnt;
+  int no_loads;          // timeout test only: no operand is loaded, so the waits run out
 };
 
 struct TokScoreArgs {

@@ -307,7 +307,7 @@ struct TokProb {
   };
   struct State {};
   static __device__ __forceinline__ bool skip(const Params&) { return false; }
-  static __device__ __forceinline__ bool no_loads(const Params&) { return false; }
+  static __device__ __forceinline__ bool no_loads(const Params& p) { return p.ep.no_loads != 0; }
   static __device__ __forceinline__ int* flags(const Params& p) { return p.ep.flags; }
   static __device__ __forceinline__ int num_jobs(const Params& p, int c, int P) {
     const int tiles = p.m_tiles * p.n_tiles;
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_rows_logits(const __grid_con
   if (warp == 0 && lane == 0) {
     int stage = 0;
     uint32_t phase = 0, armed = 0, armed_parity = 0;
-    bool ok = true;
+    bool ok = p.ep.no_loads == 0;
     for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
       for (int kb = 0; kb < p.k_blocks; ++kb) {
         if (!mbar_wait(&empty[stage], phase ^ 1u, abort)) {
@@ -808,10 +808,10 @@ struct TopList {
 // tile outside them come K others, each with an element before all of its own.
 // So only K x 128 of the row's logits are read again, and of those only the
 // ones that reach the K-th largest maximum are candidates.
-// One block of WARPS warps per row. They are merged in an order that
-// does not depend on WARPS (256 running sums, t mod 256, then lanes, then the
-// eight groups of 32), so the results do not depend on how many rows a call or
-// a chunk has.
+// One block of WARPS warps per row. The sums are merged in an order that does
+// not depend on WARPS (256 running sums, t mod 256, then lanes, then the eight
+// groups of 32), so the results do not depend on how many rows a call or a
+// chunk has.
 template <int KPL, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) k_score(const TokScoreArgs p) {
   grid_dep_wait();
@@ -851,12 +851,10 @@ __global__ void __launch_bounds__(32 * WARPS) k_score(const TokScoreArgs p) {
     }
   }
   M = warp_max(M);
-  if (WARPS > 1) {
-    if (lane == 0) s_max[warp] = M;
-    __syncthreads();
+  if (lane == 0) s_max[warp] = M;
+  __syncthreads();
 #pragma unroll
-    for (int i = 0; i < WARPS; ++i) M = fmaxf(M, s_max[i]);
-  }
+  for (int i = 0; i < WARPS; ++i) M = fmaxf(M, s_max[i]);
   RowSum sums[kMine];
 #pragma unroll
   for (int i = 0; i < kMine; ++i) sums[i] = RowSum{0.f, 0.f, 0.f};

@@ -97,8 +97,8 @@ typedef struct lce_opts {
   int32_t reserved;         /* 0, or LCE_TEST_FORCE_TIMEOUT (tests only, see below) */
 } lce_opts;
 
-/* Test value for lce_opts.reserved: lce_forward's logits kernel then loads
- * no operands, so its bounded device waits run out (about 2 s); the kernel
+/* Test value for lce_opts.reserved: the logits kernel of lce_forward (and of
+ * lce_logprobs) then loads no operands, so its bounded device waits run out (about 2 s); the kernel
  * records LCE_DEVICE_TIMEOUT, releases its resources and returns, and the
  * call reports LCE_ERR_TIMEOUT (with sync_check, or via
  * lce_read_device_status). Outputs are meaningless. It exists to test the
@@ -304,7 +304,7 @@ int lce_scale_grads(void* dH, float* dW, int64_t N, int64_t d, int64_t V, const 
  * softmax(z'). H, W, y, dH, dW, opts, ws and stream are those of the calls
  * above; the logits of one chunk at a time are held in the workspace, never
  * [N, V] (chunk_tokens = 0: equal chunks of about 4096 tokens, fewer than 6144).
- * opts->reserved must be 0.
+ * opts->reserved must be 0 (lce_logprobs also takes LCE_TEST_FORCE_TIMEOUT).
  *
  * lce_logprobs, per row i (device outputs):
  *   lse [N]      log sum_v exp(z'_iv)

@@ -125,7 +125,7 @@ def test_logprobs_refusals(lib):
     for bad in (dict(H=None), dict(W=None), dict(y=None), dict(logp=None), dict(lse=None), dict(tl=None),
                 dict(ti=None), dict(ws=None), dict(N=-1), dict(d=12), dict(V=0), dict(T=0.0), dict(T=-1.0),
                 dict(T=float("nan")), dict(T=float("inf")), dict(T=1e-31), dict(V=2 ** 31 - 1), dict(K=-1), dict(K=E.LCE_MAX_TOP + 1), dict(K=6, V=5),
-                dict(opts=lce.make_opts(reserved=E.LCE_TEST_FORCE_TIMEOUT)), dict(opts=lce.make_opts(chunk_tokens=-1))):
+                dict(opts=lce.make_opts(reserved=1)), dict(opts=lce.make_opts(chunk_tokens=-1))):
         assert call(**bad) == E.LCE_ERR_INVALID_ARG, bad
     for bad in (dict(H=P + 8), dict(W=P + 2), dict(y=P + 4), dict(logp=P + 1), dict(lse=P + 2), dict(ent=P + 2),
                 dict(tl=P + 2), dict(ti=P + 4), dict(ws=P + 128), dict(kept=P + 8)):
@@ -147,13 +147,13 @@ def test_logprobs_backward_refusals(lib):
     E, P = lce, FAKE
 
     def call(logp=P, lse=P, ent=P, g1=P, g2=P, kept=None, grads=0, dH=P, dW=P, T=1.0, N=64, acc=False,
-             nbytes=1 << 40):
-        o = lce.make_opts(accumulate_dW=acc, chunk_tokens=32)
+             reserved=0, nbytes=1 << 40):
+        o = lce.make_opts(accumulate_dW=acc, chunk_tokens=32, reserved=reserved)
         return lib.lce_logprobs_backward(P, P, P, N, 64, 1000, T, logp, lse, ent, g1, g2, kept, grads, dH, dW,
                                          ctypes.byref(o), P, nbytes, None)
 
     for bad in (dict(logp=None), dict(lse=None), dict(g1=None), dict(ent=None), dict(dH=None, dW=None), dict(T=0.0), dict(N=-2),
-                dict(grads=2), dict(grads=E.LCE_DW_BF16, acc=True)):
+                dict(grads=2), dict(grads=E.LCE_DW_BF16, acc=True), dict(reserved=E.LCE_TEST_FORCE_TIMEOUT)):
         assert call(**bad) == E.LCE_ERR_INVALID_ARG, bad
     for bad in (dict(kept=P + 4), dict(logp=P + 1), dict(lse=P + 2), dict(ent=P + 2), dict(g1=P + 2), dict(g2=P + 1), dict(dH=P + 8), dict(dW=P + 4)):
         assert call(**bad) == E.LCE_ERR_ALIGNMENT, bad

@@ -221,6 +221,36 @@ def test_logprobs_label_out_of_range(cuda_lib):
     assert torch.equal(out[0][7], torch.zeros((), device="cuda"))
 
 
+def test_ignore_index_inside_the_vocabulary(cuda_lib):
+    """A padding id that is a word: equality with it comes first, in labels and in teacher entries."""
+    rng, H, W, y = make(120, 64, 300)
+    y = rng.integers(0, 8, 120)
+    Ht, Wt = heads(H, W)
+    out = cuda_lib.lce_logprobs(Ht, Wt, dev(y), top_k=3, ignore_index=5, sync_check=True)
+    ref = oracle.logprobs_f64(H, W, y, top_k=3, ignore_index=5)
+    close(out[0], ref["logp"], 2 * tol_lse(H, W, ref["lse"], 1.0), "logp")
+    assert not out[0][dev(y == 5)].any() and (y == 5).any()
+    g = rng.standard_normal(120).astype(np.float32)
+    dH, dW = cuda_lib.lce_logprobs_backward(Ht, Wt, dev(y), *out[:3], dev(g), dev(g), ignore_index=5)
+    check_grads(dH, dW, oracle.logprobs_backward_f64(H, W, y, g, g, ignore_index=5), scaled=True)
+    idx = rng.integers(0, 8, (120, 4))
+    t = rng.standard_normal((120, 4)).astype(np.float32)
+    _, _, dH, dW = cuda_lib.lce_distill_fwd_bwd(Ht, Wt, dev(idx), dev(t), ignore_index=5, sync_check=True)
+    check_grads(dH, dW, oracle.distill_f64(H, W, idx, t, ignore_index=5))
+
+
+@pytest.mark.parametrize("N", [40, 300])
+def test_a_wait_that_runs_out_is_reported(cuda_lib, N):
+    """No operand is loaded, so the bounded waits of the logits kernels run out (about 2 s): the call
+    returns LCE_ERR_TIMEOUT, and the next one works."""
+    _, H, W, y = make(N, 64, 1000)
+    Ht, Wt = heads(H, W)
+    with pytest.raises(cuda_lib.LCEError) as err:
+        cuda_lib.lce_logprobs(Ht, Wt, dev(y), top_k=4, sync_check=True, reserved=cuda_lib.LCE_TEST_FORCE_TIMEOUT)
+    assert err.value.code == cuda_lib.LCE_ERR_TIMEOUT
+    check_scores(cuda_lib.lce_logprobs(Ht, Wt, dev(y), top_k=4, sync_check=True), H, W, y, 1.0, 4)
+
+
 def test_logprobs_no_tokens(cuda_lib):
     torch = _torch()
     H, W = torch.zeros(0, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(9, 64, dtype=torch.bfloat16, device="cuda")
