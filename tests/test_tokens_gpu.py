@@ -472,6 +472,60 @@ def test_teacher_to_student(cuda_lib):
     assert dH.float().abs().max().item() < 1e-5
 
 
+@pytest.mark.parametrize("N,d,V,chunk", [(6500, 2048, 151936, 0), (700, 7168, 151655, 512)])
+def test_full_heads_sampled(cuda_lib, N, d, V, chunk):
+    """The heads' real sizes, two chunks: rows of both sides of the chunk boundary and of both ends, and
+    vocabulary rows of the tails, against the definition in fp64."""
+    torch = _torch()
+    g = torch.Generator(device="cuda").manual_seed(N)
+    sigma = 0.02 if d <= 2048 else 0.01
+    W = (torch.randn(V, d, generator=g, device="cuda") * (sigma * 1024)).round().clamp(-127, 127).div(1024).bfloat16()
+    y = torch.randint(0, V, (N,), generator=g, device="cuda")
+    H = torch.randn(N, d, generator=g, device="cuda")
+    H += W[y].float() * (14.0 * torch.rand(N, 1, generator=g, device="cuda") / (sigma * sigma * d))
+    H = (H * 16).round().clamp(-127, 127).div(16).bfloat16()
+    y[::17] = oracle.IGNORE_INDEX
+    edge = chunk or 3328   # equal chunks by default: ceil(6500 / 2) in whole tiles
+    rows = np.array([0, 1, edge - 1, edge, edge + 1, N // 3, N - 2, N - 1])
+    cols = np.array([0, 127, 128, 255, 256, V // 2, V - 130, V - 2, V - 1])
+    Hn, Wn, yn = np64(H), np64(W), y.cpu().numpy()
+    out = cuda_lib.lce_logprobs(H, W, y, top_k=20, chunk_tokens=chunk, sync_check=True)
+    logp, lse, ent = out[:3]
+    check_scores([x[torch.from_numpy(rows).cuda()] for x in out], Hn[rows], Wn, yn[rows], 1.0, 20)
+    a = torch.randn(N, generator=g, device="cuda")
+    e = 0.1 * torch.randn(N, generator=g, device="cuda")
+    dH, dW = cuda_lib.lce_logprobs_backward(H, W, y, logp, lse, ent, a, e, chunk_tokens=chunk)
+    part = oracle.logprobs_backward_f64(Hn[rows], Wn, yn[rows], np64(a)[rows], np64(e)[rows])
+    check_grads(dH[torch.from_numpy(rows).cuda()], None, part)
+
+    def sampled_dW(G, size, got, scaled):   # columns of G [N, cols] in fp64 from the call's lse
+        check_grads(None, got[torch.from_numpy(cols).cuda()],
+                    {"dW": G.T @ Hn, "dW_bulk": size.T @ np.abs(Hn)}, scaled=scaled)
+
+    logq = Hn @ Wn[cols].T - np64(lse)[:, None]
+    p, hot = np.exp(logq), (yn[:, None] == cols[None, :]).astype(float)
+    an = np.where(yn >= 0, np64(a), 0.0)[:, None]
+    dev_ = np64(e)[:, None] * (logq + np64(ent)[:, None])
+    sampled_dW(hot * an - p * (an + dev_), hot * np.abs(an) + p * (np.abs(an) + np.abs(dev_)), dW, True)
+    # distillation from these alternatives
+    idx, t = out[4].clone(), out[3]
+    idx[5::11, 7:] = oracle.IGNORE_INDEX
+    idx[3::13] = oracle.IGNORE_INDEX
+    idx[:9, 0] = torch.from_numpy(cols).cuda()
+    loss, row, dH, dW = cuda_lib.lce_distill_fwd_bwd(H, W, idx, t, renormalize=False, chunk_tokens=chunk,
+                                                     sync_check=True)
+    n = int((idx >= 0).any(1).sum())
+    part = oracle.distill_f64(Hn[rows], Wn, idx.cpu().numpy()[rows], np64(t)[rows], renormalize=False,
+                              n_valid_override=n)
+    close(row[torch.from_numpy(rows).cuda()], part["row_loss"], 2.0 ** -14, "row_loss")
+    check_grads(dH[torch.from_numpy(rows).cuda()], None, part)
+    assert abs(loss.item() - row.double().sum().item() / n) <= 2.0 ** -22 * abs(loss.item())
+    q = np.where(idx.cpu().numpy() >= 0, np.exp(np64(t)), 0.0)
+    hot = np.stack([np.where(idx.cpu().numpy() == c, q, 0.0).sum(1) for c in cols], axis=1)
+    mass = q.sum(1, keepdims=True)
+    sampled_dW((mass * p - hot) / n, (mass * p + hot) / n, dW, False)
+
+
 # --------------------------------------------------------------------------- as programs use them
 def test_autograd_modules(cuda_lib):
     torch = _torch()
