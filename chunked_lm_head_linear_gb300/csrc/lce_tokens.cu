@@ -8,12 +8,12 @@
 // Per row i, with z' = z / T:
 //   lse = log sum_v exp z'_v, logp = z'_y - lse, entropy = lse - sum_v p_v z'_v
 // The GEMM's epilogue keeps, per (row, 128 vocabulary columns), four numbers
-//   m = max z,  c = how many logits equal it,
+//   m = max z, with c = 1 (merged: how many half tiles reach the row's maximum),
 //   s = sum exp((z - m)/T) over the others,  t = sum exp((z - m)/T) (z - m)/T
 // from which, merged over the row, log-sum-exp = m/T + log c + log1p(s/c) and
 // entropy = log c + log1p(s/c) - t/(c + s): one exponential per logit for both,
-// no difference of two large numbers, and because the terms that are 1 exactly
-// are counted apart, a log-probability near 0 (a confident model's token) keeps
+// no difference of two large numbers, and because the terms of the maxima, 1
+// exactly, are counted apart, a log-probability near 0 (a confident model's token) keeps
 // its relative precision instead of the 2^-24 of a sum near 1.
 #include <math.h>
 
@@ -24,7 +24,8 @@ namespace lce {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kFloor = -1.0e30f;  // stands in for -inf where it is multiplied by a zero probability
+constexpr float kFloor = -1.0e30f;   // stands in for -inf where it is multiplied by a zero probability
+constexpr float kMasked = -3.0e38f;  // the logit of a column past the vocabulary: its probability is zero
 
 // ----------------------------------------------------------------------------
 // A row's four numbers and their merge
@@ -45,6 +46,61 @@ __device__ __forceinline__ void add_partial(RowSum& a, const float4& q, float M,
     a.s = fmaf(all, f, a.s);
     a.t = fmaf(fmaf(all, fmaxf(d, kFloor), q.z), f, a.t);
   }
+}
+
+// A tile's running maximum and the sums over the logits other than it (m = kMasked: nothing yet).
+struct Mst {
+  float m, s, t;
+};
+
+// 32 logits added to them; v is overwritten. A pass of maxima and minima leaves the maximum of all,
+// the old one included, apart from the 32 that lose against it, so that no comparison is needed to
+// leave it out of the sums; they run in strands, two logits an instruction, because a warp has its
+// issue slots to itself and waits for its own chains.
+__device__ __forceinline__ void add_columns(Mst& a, float (&v)[32], float inv_t) {
+  const float k = inv_t * kLog2e;
+  float x[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+  for (int c = 4; c < 32; c += 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float hi = max_nan(x[i], v[c + i]);
+      v[c + i] = min_nan(x[i], v[c + i]);
+      x[i] = hi;
+    }
+  }
+  float m = a.m;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float hi = max_nan(m, x[i]);
+    v[i] = min_nan(m, x[i]);
+    m = hi;
+  }
+  if (m != a.m) {
+    const float d = a.m - m, f = ex2_approx(d * k);
+    a.t = f * fmaf(a.s, fmaxf(d * inv_t, kFloor), a.t);
+    a.s *= f;
+    a.m = m;
+  }
+  const uint64_t m2 = pair_f32(-m, -m), k2 = pair_f32(k, k);
+  uint64_t s[2] = {0, 0}, t[2] = {0, 0};
+#pragma unroll
+  for (int c = 0; c < 32; c += 4) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t dz = add_pair(pair_f32(v[c + 2 * i], v[c + 2 * i + 1]), m2);
+      float x0, x1;
+      unpair_f32(mul_pair(dz, k2), x0, x1);
+      const uint64_t e = pair_f32(ex2_approx(x0), ex2_approx(x1));
+      s[i] = add_pair(s[i], e);
+      t[i] = fma_pair(e, dz, t[i]);
+    }
+  }
+  float lo, hi;
+  unpair_f32(add_pair(s[0], s[1]), lo, hi);
+  a.s += lo + hi;
+  unpair_f32(add_pair(t[0], t[1]), lo, hi);
+  a.t = fmaf(lo + hi, inv_t, a.t);
 }
 
 __device__ __forceinline__ RowSum warp_add(RowSum a) {
@@ -185,13 +241,47 @@ struct TokEpi {
   using Params = TokParams;
   struct State {};
 
+  // 32 columns c0.. of the half tile: their logits stored, the row's four numbers brought up to date.
+  // The maximum and the sums run in four strands each: a warp has its sub-partition's issue slots to
+  // itself, and what bounds it is the latency of its chains.
+  static __device__ __forceinline__ void stats_group(const Params& p, const EpiCtx& ctx, float (&v)[32], int c0,
+                                                     int col0, int row, int vlim, bool rows_in, int ycol, Mst& a,
+                                                     float& zt, bool& have_t) {
+    if (MODE == TOK_STATS_Z && rows_in) {
+      stage_acquire(ctx);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        *reinterpret_cast<float4*>(ctx.stage + stage_off(ctx.lane, q)) =
+            make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+      stage_release(ctx, col0 + c0, row, false);
+    }
+    if (vlim < c0 + 32) {
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        if (c0 + c >= vlim) v[c] = kMasked;
+    }
+    if (MODE == TOK_STATS) {
+      const int yo = ycol - c0;
+      if (yo >= 0 && yo < 32) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (c == yo) {
+            zt = v[c];
+            have_t = true;
+          }
+      }
+    }
+    add_columns(a, v, p.inv_t);
+  }
+
   static __device__ __forceinline__ void stats_tile(const Params& p, const EpiCtx& ctx, int m0, int col0,
                                                     uint32_t taddr) {
     const int r = m0 + ctx.row0 + ctx.lane;
     const bool live = r < p.rows;
     const int vlim = p.V - col0;  // columns >= vlim are past the vocabulary (warp-uniform)
     const int part = col0 / EPI_COLS;
-    float m = -INFINITY, s = 0.f, t = 0.f, cnt = 0.f, zt = 0.f;
+    Mst acc{kMasked, 0.f, 0.f};
+    float zt = 0.f;
     bool have_t = false;
     int ycol = -1;
     if (MODE == TOK_STATS && live) {
@@ -199,65 +289,26 @@ struct TokEpi {
       if (yc >= 0 && yc < EPI_COLS && p.y[r] != p.ignore_index) ycol = static_cast<int>(yc);
     }
     const bool rows_in = m0 + ctx.row0 < p.rows;  // a store box never starts past the rows
-    const float k = p.inv_t * kLog2e;
+    const int row = m0 + ctx.row0;
+    if (vlim > 0) {
+      // two groups of 32 columns in flight (a group past the vocabulary holds zeros and is not used)
+      float va[32], vb[32];
+      tmem_ld_issue_x32(taddr, va);
 #pragma unroll 1
-    for (int c0 = 0; c0 < EPI_COLS; c0 += 32) {
-      if (c0 >= vlim) break;
-      float v[32];
-      tmem_ld_32x32b_x32(taddr + c0, v);
-      if (MODE == TOK_STATS_Z && rows_in) {
-        stage_acquire(ctx);
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<float4*>(ctx.stage + stage_off(ctx.lane, q)) =
-              make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-        stage_release(ctx, col0 + c0, m0 + ctx.row0, false);
+      for (int c0 = 0; c0 < EPI_COLS; c0 += 64) {
+        tmem_ld_wait(va);
+        tmem_ld_issue_x32(taddr + c0 + 32, vb);
+        stats_group(p, ctx, va, c0, col0, row, vlim, rows_in, ycol, acc, zt, have_t);
+        tmem_ld_wait(vb);
+        if (c0 + 64 < EPI_COLS) tmem_ld_issue_x32(taddr + c0 + 64, va);
+        if (c0 + 32 < vlim) stats_group(p, ctx, vb, c0 + 32, col0, row, vlim, rows_in, ycol, acc, zt, have_t);
+        if (c0 + 64 >= vlim) break;
       }
-      if (vlim < c0 + 32) {
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (c0 + c >= vlim) v[c] = -INFINITY;
-      }
-      if (MODE == TOK_STATS) {
-        const int yo = ycol - c0;
-        if (yo >= 0 && yo < 32) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (c == yo) {
-              zt = v[c];
-              have_t = true;
-            }
-        }
-      }
-      float cm = v[0];
-#pragma unroll
-      for (int c = 1; c < 32; ++c) cm = fmaxf(cm, v[c]);
-      if (cm > m) {
-        if (cnt > 0.f) {
-          const float f = ex2_approx((m - cm) * k);
-          t = f * (t + (s + cnt) * fmaxf((m - cm) * p.inv_t, kFloor));
-          s = (s + cnt) * f;
-          cnt = 0.f;
-        }
-        m = cm;
-      }
-      const float mb = m == -INFINITY ? 0.f : m;  // a group of -inf only: every term is zero
-      float s2 = 0.f, t2 = 0.f;
-#pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const float dz = v[c] - mb;
-        const float e = ex2_approx(dz * k);
-        if (dz == 0.f)
-          cnt += 1.f;
-        else
-          s2 += e;
-        t2 = fmaf(e, fmaxf(dz, kFloor), t2);
-      }
-      s += s2;
-      t = fmaf(t2, p.inv_t, t);
+      tmem_ld_wait(va);  // a load that a break left under way
     }
     if (!live || !in_bounds(part, p.nparts, p.flags)) return;
-    p.partials[static_cast<long long>(r) * p.nparts + part] = make_float4(m, s, t, cnt);
+    p.partials[static_cast<long long>(r) * p.nparts + part] =
+        vlim > 0 ? make_float4(acc.m, acc.s, acc.t, 1.f) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
     if (MODE == TOK_STATS && have_t) p.ztgt[r] = zt;
   }
 
@@ -550,7 +601,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_rows_logits(const __grid_con
   } else if (warp >= EPI_WARP0) {
     const int q = warp & 3;
     const TokParams& e = p.ep;
-    const float k = e.inv_t * kLog2e;
     int acc = 0;
     uint32_t acc_phase = 0;
     reset_status(e);
@@ -581,7 +631,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_rows_logits(const __grid_con
         // this warp's 32 columns of row n0 + lane
         const int n = n0 + lane;
         const float* zr = out + lane * kOutLd + q * 32;
-        float m = -INFINITY, s = 0.f, tt = 0.f, cnt = 0.f;
+        Mst a{kMasked, 0.f, 0.f};
+        const int vlim = e.V - col0 - q * 32;
         if (n < e.rows) {
           float v[32];
 #pragma unroll
@@ -592,31 +643,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_rows_logits(const __grid_con
             v[4 * j + 2] = x.z;
             v[4 * j + 3] = x.w;
           }
-          const int vlim = e.V - col0 - q * 32;
           if (vlim < 32) {
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-              if (c >= vlim) v[c] = -INFINITY;
+              if (c >= vlim) v[c] = kMasked;
           }
-#pragma unroll
-          for (int c = 0; c < 32; ++c) m = fmaxf(m, v[c]);
-          const float mb = m == -INFINITY ? 0.f : m;
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float dz = v[c] - mb;
-            const float x = ex2_approx(dz * k);
-            if (dz == 0.f)
-              cnt += 1.f;
-            else
-              s += x;
-            tt = fmaf(x, fmaxf(dz, kFloor), tt);
-          }
+          if (vlim > 0) add_columns(a, v, e.inv_t);
           if (!p.store_z) {
             const long long y = e.y[n], c = y - col0 - q * 32;
             if (c >= 0 && c < 32 && y < e.V && y != e.ignore_index) e.ztgt[n] = zr[c];
           }
         }
-        sums[q * 32 + lane] = make_float4(m, s, tt * e.inv_t, cnt);
+        sums[q * 32 + lane] = vlim > 0 ? make_float4(a.m, a.s, a.t, 1.f) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
         if (p.store_z) {  // a warp a row: 512 bytes at a time
           const int n1 = e.rows - n0 < 32 ? e.rows - n0 : 32;
           for (int i = q; i < n1; i += 4)
@@ -628,10 +666,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_rows_logits(const __grid_con
         if (q == 0 && n < e.rows && in_bounds(part, e.nparts, e.flags)) {  // the four warps' columns together
           const float4 x[4] = {sums[lane], sums[32 + lane], sums[64 + lane], sums[96 + lane]};
           const float M = fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x));
-          RowSum a{0.f, 0.f, 0.f};
+          RowSum all{0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) add_partial(a, x[i], M, e.inv_t);
-          e.partials[static_cast<long long>(n) * e.nparts + part] = make_float4(M, a.s, a.t, a.c);
+          for (int i = 0; i < 4; ++i) add_partial(all, x[i], M, e.inv_t);
+          e.partials[static_cast<long long>(n) * e.nparts + part] = make_float4(M, all.s, all.t, all.c);
         }
         n0 += 32;
         if (n0 >= e.rows) {
