@@ -993,6 +993,7 @@ struct TokLayout {
   Layout base;         // status, ztgt, partials, P and the dH parts of the call record
   int64_t ldz = 0;     // row stride of the logits buffer
   size_t Z = 0;
+  size_t label = 0;    // the labels' entries of the gradient tile
   size_t dW = 0;       // fp32 sum of dW over the chunks before the last (dW_bf16 and several chunks)
   size_t total = 0;
 };
@@ -1027,8 +1028,9 @@ TokLayout tok_layout(int64_t N, int64_t d, int64_t V, bool with_z, bool with_gra
   L.ztgt = take(sizeof(float) * C);
   L.partials = take(sizeof(float4) * C * static_cast<size_t>(2 * L.T));
   if (with_z) T.Z = take(sizeof(float) * C * static_cast<size_t>(T.ldz));
-  if (with_scale) {  // row scales and bf16(scale H)
+  if (with_scale) {  // row scales, the labels' entries and bf16(scale H)
     L.alpha = take(sizeof(float) * C);
+    T.label = take(sizeof(float) * C);
     L.Ht = take(2 * C * static_cast<size_t>(d));
   }
   if (with_grad) {
@@ -1040,10 +1042,10 @@ TokLayout tok_layout(int64_t N, int64_t d, int64_t V, bool with_z, bool with_gra
   return T;
 }
 
-// The temperature is positive and finite, and so is its inverse; a vocabulary within 1024 of 2^31 is
-// refused, so that column numbers rounded up to a tile stay 32-bit.
+// Temperatures from 1e-6 to 1e6 (the masked columns' -1e30 stays finite over them); a vocabulary within
+// 1024 of 2^31 is refused, so that column numbers rounded up to a tile stay 32-bit.
 int check_token_args(int64_t V, float t) {
-  return V <= (int64_t{1} << 31) - 1024 && t >= 1.0e-30f && t <= 1.0e30f ? LCE_OK : LCE_ERR_INVALID_ARG;
+  return V <= (int64_t{1} << 31) - 1024 && t >= 1.0e-6f && t <= 1.0e6f ? LCE_OK : LCE_ERR_INVALID_ARG;
 }
 
 // Fills the call record of a token operator (after its own argument checks).
@@ -1231,6 +1233,7 @@ int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_
   }
   uint16_t* G = reinterpret_cast<uint16_t*>(c.ws + c.L.P);
   float* rowscale = reinterpret_cast<float*>(c.ws + c.L.alpha);
+  float* label = reinterpret_cast<float*>(c.ws + T.label);
   uint16_t* Ht = reinterpret_cast<uint16_t*>(c.ws + c.L.Ht);
   for (int64_t c0 = 0; c0 < N; c0 += c.L.C) {
     const int64_t rows = (N - c0) < c.L.C ? (N - c0) : c.L.C;
@@ -1240,6 +1243,7 @@ int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_
     p.g_logp = g_logp + c0;
     p.g_entropy = g_entropy ? g_entropy + c0 : nullptr;
     p.rowscale = rowscale;
+    p.label = label;
     lce::ScoreGradArgs a;
     std::memset(&a, 0, sizeof a);
     a.V = p.V;
@@ -1255,6 +1259,7 @@ int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_
     a.g_logp = p.g_logp;
     a.g_entropy = p.g_entropy;
     a.rowscale = rowscale;
+    a.label = label;
     a.H = reinterpret_cast<const uint4*>(c.H + c0 * d);
     a.Ht = dW ? reinterpret_cast<uint4*>(Ht) : nullptr;
     a.Z = logits ? logits + c0 * T.ldz : nullptr;

@@ -246,6 +246,7 @@ struct TokParams {
   const float* g_logp;   // [rows] upstream gradients
   const float* g_entropy;  // [rows] or null
   const float* rowscale;   // [rows] what the row's gradient tile is divided by
+  const float* label;      // [rows] the label's entry of the tile
   int* flags;
   int reset;             // the first block clears *flags (the call's first launch; k_score reports bad labels)
   DevStatus* clear_st;   // not null: the first block clears the status block and cnt[0, ncnt) (distillation)
@@ -283,6 +284,7 @@ struct ScoreGradArgs {
   const float* g_logp;
   const float* g_entropy;  // or null
   float* rowscale;         // [rows] out
+  float* label;            // [rows] out: the label's entry of the tile
   const uint4* H;          // [rows, d] bf16
   uint4* Ht;               // [rows, d] bf16(rowscale H) out, or null
   const float* Z;        // [rows, ldz] logits of the forward, or null: no gradient tile

@@ -24,8 +24,9 @@ namespace lce {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -1.0e30f;   // stands in for -inf where it is multiplied by a zero probability
-constexpr float kMasked = -3.0e38f;  // the logit of a column past the vocabulary: its probability is zero
+constexpr float kMasked = -1.0e30f;  // the logit of a column past the vocabulary: no probability, and finite over T
 
 // ----------------------------------------------------------------------------
 // A row's four numbers and their merge
@@ -82,25 +83,29 @@ __device__ __forceinline__ void add_columns(Mst& a, float (&v)[32], float inv_t)
     a.s *= f;
     a.m = m;
   }
-  const uint64_t m2 = pair_f32(-m, -m), k2 = pair_f32(k, k);
+  // Exponents to base 2 in one fma, z k - fl(m k); what m k loses by its rounding, the same for all,
+  // is made good once behind the sums.
+  const float mk = m * k, lost = fmaf(m, k, -mk);
+  const uint64_t m2 = pair_f32(-mk, -mk), k2 = pair_f32(k, k);
   uint64_t s[2] = {0, 0}, t[2] = {0, 0};
 #pragma unroll
   for (int c = 0; c < 32; c += 4) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint64_t dz = add_pair(pair_f32(v[c + 2 * i], v[c + 2 * i + 1]), m2);
-      float x0, x1;
-      unpair_f32(mul_pair(dz, k2), x0, x1);
-      const uint64_t e = pair_f32(ex2_approx(x0), ex2_approx(x1));
+      const uint64_t y = fma_pair(pair_f32(v[c + 2 * i], v[c + 2 * i + 1]), k2, m2);
+      float y0, y1;
+      unpair_f32(y, y0, y1);
+      const uint64_t e = pair_f32(ex2_approx(y0), ex2_approx(y1));
       s[i] = add_pair(s[i], e);
-      t[i] = fma_pair(e, dz, t[i]);
+      t[i] = fma_pair(e, y, t[i]);
     }
   }
-  float lo, hi;
-  unpair_f32(add_pair(s[0], s[1]), lo, hi);
-  a.s += lo + hi;
-  unpair_f32(add_pair(t[0], t[1]), lo, hi);
-  a.t = fmaf(lo + hi, inv_t, a.t);
+  float s0, s1, t0, t1;
+  unpair_f32(add_pair(s[0], s[1]), s0, s1);
+  unpair_f32(add_pair(t[0], t[1]), t0, t1);
+  const float fix = ex2_approx(-lost), sum = s0 + s1;
+  a.s = fmaf(sum, fix, a.s);
+  a.t = fmaf(fmaf(-lost, sum, t0 + t1) * kLn2, fix, a.t);
 }
 
 __device__ __forceinline__ RowSum warp_add(RowSum a) {
@@ -158,11 +163,12 @@ __device__ __forceinline__ float log_sum(const RowSum& a) { return logf(a.c) + l
 // one rounding in place of the label entry's, but of every element on its own
 // and so averaged over the row (errors against fp64, in units of one bf16
 // rounding, 250 rows: dH 1.3-1.6 -> 1.0, bf16 dW 1.3-1.5 -> 1.2-1.3).
+// An entry costs two fma, an exponential and a product: x = z k - lse log2 e, p = 2^x, g = p (c0 + c1 x).
 struct GradRow {
-  float lse = 0.f, a = 0.f, c0 = 0.f, c1 = 0.f;
-  int y = -1;          // the label, -1 where it is not given
-  bool zero = true;    // no upstream gradient
-  bool scaled = false;  // divided by the label's entry, which is then 1
+  float k = 0.f, shift = 0.f;  // x = z k + shift
+  float c0 = 0.f, c1 = 0.f;    // (-a - e entropy, -e ln 2) over the scale
+  int y = -1;                  // the label, -1 where it is not given
+  uint32_t keep = 0;           // 0: no upstream gradient, all bits: some
 };
 
 struct Upstream {
@@ -180,35 +186,42 @@ __device__ __forceinline__ Upstream upstream(int r, const int64_t* labels, long 
   return u;
 }
 
-// The label's entry a (1 - p) - p e (log p + entropy), from its log-probability; 1 where there is
-// none or it is too small, or not a number, to divide by.
-__device__ __forceinline__ float row_scale(const Upstream& u, float logp, const float* entropy, int r) {
-  if (u.y < 0) return 1.f;
+// The label's entry a (1 - p) - p e (log p + entropy), from its log-probability.
+__device__ __forceinline__ float label_entry(const Upstream& u, float logp, const float* entropy, int r) {
+  if (u.y < 0) return 0.f;
   float g = -expm1f(logp) * u.a;
   if (u.e != 0.f) g -= expf(logp) * u.e * (logp + entropy[r]);
-  const float size = fabsf(g);
-  return size >= 1.0e-30f && size <= 1.0e30f && size >= 1.0e-12f * (fabsf(u.a) + fabsf(u.e)) ? g : 1.f;
-}
-
-__device__ __forceinline__ GradRow grad_row(const Upstream& u, float scale, float lse, const float* entropy, int r) {
-  GradRow g;
-  const float inv = 1.f / scale;
-  g.y = u.y;
-  g.lse = lse;
-  g.a = u.a * inv;
-  g.c1 = -u.e * inv;
-  g.c0 = -g.a;
-  if (u.e != 0.f) g.c0 += g.c1 * entropy[r];
-  g.zero = u.a == 0.f && u.e == 0.f;
-  g.scaled = scale != 1.f;
   return g;
 }
 
-__device__ __forceinline__ float grad_entry(float z, float inv_t, const GradRow& r, bool label) {
-  const float logp = fmaf(z, inv_t, -r.lse);
-  float g = __fmul_rn(ex2_approx(logp * kLog2e), fmaf(r.c1, fmaxf(logp, kFloor), r.c0));
-  if (label) g = r.scaled ? 1.f : __fadd_rn(g, r.a);
-  return r.zero ? 0.f : g;
+// The row's scale: that entry, or 1 where it is too small, or not a number, to divide by.
+__device__ __forceinline__ float row_scale(const Upstream& u, float entry) {
+  const float size = fabsf(entry);
+  return size >= 1.0e-30f && size <= 1.0e30f && size >= 1.0e-12f * (fabsf(u.a) + fabsf(u.e)) ? entry : 1.f;
+}
+
+__device__ __forceinline__ GradRow grad_row(const Upstream& u, float scale, float lse, const float* entropy, int r,
+                                            float inv_t) {
+  GradRow g;
+  const float inv = 1.f / scale, e = u.e * inv;
+  g.y = u.y;
+  g.k = inv_t * kLog2e;
+  g.shift = -lse * kLog2e;
+  g.c0 = -u.a * inv;
+  if (u.e != 0.f) g.c0 -= e * entropy[r];
+  g.c1 = -e * kLn2;
+  g.keep = u.a == 0.f && u.e == 0.f ? 0u : ~0u;
+  return g;
+}
+
+// Two entries, in bf16.
+__device__ __forceinline__ uint32_t grad_pair(float z0, float z1, const GradRow& r) {
+  const uint64_t x = fma_pair(pair_f32(z0, z1), pair_f32(r.k, r.k), pair_f32(r.shift, r.shift));
+  float x0, x1, g0, g1;
+  unpair_f32(x, x0, x1);
+  const uint64_t p = pair_f32(ex2_approx(x0), ex2_approx(x1));
+  unpair_f32(mul_pair(p, fma_pair(x, pair_f32(r.c1, r.c1), pair_f32(r.c0, r.c0))), g0, g1);
+  return pack_bf16x2(g0, g1) & r.keep;
 }
 
 __device__ __forceinline__ void clear_status(DevStatus* st, int* cnt, int ncnt, int thread, int threads) {
@@ -318,9 +331,12 @@ struct TokEpi {
     const int vlim = p.V - col0;
     if (m0 + ctx.row0 >= p.rows || vlim <= 0) return;  // nothing of this half tile is stored
     GradRow g;
-    if (r < p.rows)
+    float label = 0.f;
+    if (r < p.rows) {
       g = grad_row(upstream(r, p.y, p.ignore_index, p.V, p.g_logp, p.g_entropy, p.inv_t), p.rowscale[r], p.lse[r],
-                   p.entropy, r);
+                   p.entropy, r, p.inv_t);
+      label = p.label[r];
+    }
     const int ycol = g.y - col0;  // a column of this half tile, or outside [0, 128)
 #pragma unroll 1
     for (int u = 0; u < EPI_COLS / 64; ++u) {
@@ -333,15 +349,16 @@ struct TokEpi {
         tmem_ld_32x32b_x32(taddr + c0, v);
         uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          pk[c / 2] = pack_bf16x2(grad_entry(v[c], p.inv_t, g, c0 + c == ycol),
-                                  grad_entry(v[c + 1], p.inv_t, g, c0 + c + 1 == ycol));
-        }
+        for (int c = 0; c < 32; c += 2) pk[c / 2] = grad_pair(v[c], v[c + 1], g);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           *reinterpret_cast<uint4*>(ctx.stage + stage_off(ctx.lane, hh * 4 + q)) =
               make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
       }
+      const int yo = ycol - u * 64;  // the label's entry, by the thread that holds its row
+      if (g.y >= 0 && g.keep != 0 && yo >= 0 && yo < 64)
+        *reinterpret_cast<__nv_bfloat16*>(ctx.stage + stage_off(ctx.lane, yo / 8) + (yo % 8) * 2) =
+            __float2bfloat16_rn(label);
       stage_release(ctx, col0 + u * 64, m0 + ctx.row0, false);
     }
   }
@@ -979,8 +996,12 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_score_grad(const ScoreGradAr
     }
   }
   const Upstream u = upstream(r, p.y, p.ignore_index, p.V, p.g_logp, p.g_entropy, p.inv_t);
-  const float scale = row_scale(u, p.logp[r], p.entropy, r);
-  if (tid == 0) p.rowscale[r] = scale;
+  const float entry = label_entry(u, p.logp[r], p.entropy, r), scale = row_scale(u, entry);
+  const float label = scale == 1.f ? entry : 1.f;  // the label's entry of the tile
+  if (tid == 0) {
+    p.rowscale[r] = scale;
+    p.label[r] = label;
+  }
   if (p.Ht != nullptr) {
     const int groups = p.d / 8;
     const uint4* hr = p.H + static_cast<long long>(r) * groups;
@@ -998,20 +1019,21 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_score_grad(const ScoreGradAr
   if (!TILE) return;
   const float* z = p.Z + static_cast<long long>(r) * p.ldz;
   __nv_bfloat16* g = p.G + static_cast<long long>(r) * p.ldg;
-  const GradRow row = grad_row(u, scale, p.lse[r], p.entropy, r);
+  const GradRow row = grad_row(u, scale, p.lse[r], p.entropy, r, p.inv_t);
   for (int c = tid * 8; c < p.V; c += kRowThreads * 8) {
     // columns past V (up to 7) lie inside the row's padding: never read by the GEMMs
     uint32_t o[4] = {0u, 0u, 0u, 0u};
-    if (!row.zero) {
+    if (row.keep != 0) {
       const float4 x = __ldcs(reinterpret_cast<const float4*>(z + c));
       const float4 w = __ldcs(reinterpret_cast<const float4*>(z + c + 4));
-      float v[8] = {x.x, x.y, x.z, x.w, w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = grad_entry(v[i], p.inv_t, row, c + i == row.y);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      o[0] = grad_pair(x.x, x.y, row);
+      o[1] = grad_pair(x.z, x.w, row);
+      o[2] = grad_pair(w.x, w.y, row);
+      o[3] = grad_pair(w.z, w.w, row);
     }
     *reinterpret_cast<uint4*>(g + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    const int yo = row.y - c;  // the label's entry, by the thread that holds its eight columns
+    if (row.y >= 0 && row.keep != 0 && yo >= 0 && yo < 8) g[row.y] = __float2bfloat16_rn(label);
   }
 }
 

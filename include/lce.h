@@ -300,7 +300,7 @@ int lce_scale_grads(void* dH, float* dW, int64_t N, int64_t d, int64_t V, const 
 
 /*
  * Token operators of the head: what a model needs of its logits besides the
- * cross-entropy. z = H W^T as above, z' = z / temperature (1e-30 to 1e30), p =
+ * cross-entropy. z = H W^T as above, z' = z / temperature (1e-6 to 1e6), p =
  * softmax(z'). H, W, y, dH, dW, opts, ws and stream are those of the calls
  * above; the logits of one chunk at a time are held in the workspace, never
  * [N, V] (chunk_tokens = 0: equal chunks of about 4096 tokens, fewer than 6144).

@@ -124,7 +124,7 @@ def test_logprobs_refusals(lib):
 
     for bad in (dict(H=None), dict(W=None), dict(y=None), dict(logp=None), dict(lse=None), dict(tl=None),
                 dict(ti=None), dict(ws=None), dict(N=-1), dict(d=12), dict(V=0), dict(T=0.0), dict(T=-1.0),
-                dict(T=float("nan")), dict(T=float("inf")), dict(T=1e-31), dict(V=2 ** 31 - 1), dict(K=-1), dict(K=E.LCE_MAX_TOP + 1), dict(K=6, V=5),
+                dict(T=float("nan")), dict(T=float("inf")), dict(T=9e-7), dict(T=2e6), dict(V=2 ** 31 - 1), dict(K=-1), dict(K=E.LCE_MAX_TOP + 1), dict(K=6, V=5),
                 dict(opts=lce.make_opts(reserved=1)), dict(opts=lce.make_opts(chunk_tokens=-1))):
         assert call(**bad) == E.LCE_ERR_INVALID_ARG, bad
     for bad in (dict(H=P + 8), dict(W=P + 2), dict(y=P + 4), dict(logp=P + 1), dict(lse=P + 2), dict(ent=P + 2),

@@ -122,6 +122,8 @@ SCORE_CASES = [
     (513, 256, 1000, 7, 1.3, 200),   # chunks that are not a multiple of the tile
     (2, 64, 151655, 20, 1.0, 0),     # the unpadded vocabulary
     (130, 64, 70001, 9, 1.0, 0),
+    (37, 64, 333, 5, 1e-6, 0),       # the coldest: one token, or several equal ones, have all of it
+    (130, 64, 333, 5, 1e6, 0),       # the hottest: all but uniform
 ]
 
 
