@@ -1000,7 +1000,8 @@ struct TokLayout {
 
 // Tokens per chunk: the caller's, or N over its nearest number of 4096-token chunks (at least one)
 // in whole 256-row tiles. Equal chunks of up to 6143 tokens rather than 4096 and a remainder: each
-// further chunk streams W again and adds a read and a write of the fp32 dW.
+// further chunk streams W again and adds a read and a write of the fp32 dW (distillation of 4500 tokens
+// at d = 2048, V = 151936: 5.86 ms in one chunk, 6.72 in 4096 + 404; 6100 tokens 7.84 and 8.19).
 int64_t tok_chunk(int64_t N, const lce_opts* o) {
   if (N <= 0 || (o && o->chunk_tokens > 0)) return chunk_of(N, o);
   const int64_t n = (N + kDefaultChunk / 2) / kDefaultChunk;

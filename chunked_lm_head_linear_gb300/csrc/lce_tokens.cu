@@ -1054,15 +1054,13 @@ __global__ void __launch_bounds__(1024) k_distill_init(DevStatus* st, int* cnt, 
 // Rows with at least one kept entry (an index in [0, V) whose teacher value is
 // above -inf), and the range bit for an index that is neither kept nor
 // ignore_index. One warp per row; the count is a sum of whole numbers, so the
-// order of the atomics does not change it. A single block also clears what it
-// adds into.
+// order of the atomics does not change it.
 __global__ void __launch_bounds__(1024) k_distill_count(const int64_t* __restrict__ idx, const void* __restrict__ tv,
                                                         int t_bf16, long long N, int K, int V, long long ignore_index,
-                                                        DevStatus* st, int* cnt, int ncnt) {
+                                                        DevStatus* st) {
   grid_dep_wait();
   grid_dep_launch();
   __shared__ int s_cnt, s_bad;
-  if (gridDim.x == 1) clear_status(st, cnt, ncnt, threadIdx.x, blockDim.x);
   if (threadIdx.x == 0) s_cnt = s_bad = 0;
   __syncthreads();
   const int lane = threadIdx.x & 31;
@@ -1312,13 +1310,11 @@ cudaError_t launch_score_grad(const ScoreGradArgs& p, int rows, cudaStream_t s) 
 cudaError_t launch_distill_count(const int64_t* idx, const void* t, int t_bf16, long long N, int K, int V,
                                  long long ignore_index, DevStatus* st, int* cnt, int ncnt, int num_sms,
                                  cudaStream_t s) {
-  // up to 32 rounds of one block cost less than a second launch
-  if (N <= 32 * 32) return launch_k(k_distill_count, 1, 1024, 0, s, idx, t, t_bf16, N, K, V, ignore_index, st, cnt, ncnt);
   const cudaError_t e = launch_k(k_distill_init, 1, 1024, 0, s, st, cnt, ncnt);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || N <= 0) return e;
   const long long want = (N + 31) / 32;
   const int grid = static_cast<int>(want < num_sms ? want : num_sms);
-  return launch_k(k_distill_count, grid, 1024, 0, s, idx, t, t_bf16, N, K, V, ignore_index, st, cnt, ncnt);
+  return launch_k(k_distill_count, grid, 1024, 0, s, idx, t, t_bf16, N, K, V, ignore_index, st);
 }
 
 cudaError_t launch_distill_row(const DistillArgs& p, int rows, cudaStream_t s) {

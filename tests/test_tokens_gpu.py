@@ -615,6 +615,44 @@ def test_streams_graphs_and_a_shared_workspace(cuda_lib, N):
             assert torch.equal(a, b)
 
 
+def test_autograd_captured_and_replayed(cuda_lib):
+    """A training step of both modules, forward and torch.autograd.grad, captured once and replayed on new
+    hidden states."""
+    torch = _torch()
+    from chunked_lm_head_linear_gb300.autograd import FusedLinearDistillation, FusedLinearLogProbs
+    rng, H, W, y = make(200, 1024, 700)
+    idx, t = teacher(rng, 200, 700, 9)
+    Ht, Wt = heads(H, W)
+    it, tt, yt = dev(idx), dev(t), dev(y)
+    g = dev(rng.standard_normal(200).astype(np.float32))
+    x, w = Ht.clone().requires_grad_(True), Wt.clone().requires_grad_(True)
+
+    def step():
+        logp, ent = FusedLinearLogProbs()(x, w, yt)
+        loss = FusedLinearDistillation()(x, w, it, tt)
+        return [logp, ent, loss, *torch.autograd.grad([logp, ent], [x, w], [g, g]), *torch.autograd.grad(loss, [x, w])]
+
+    want = []
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for k in range(2):
+            with torch.no_grad():
+                x.copy_(Ht if k == 0 else -Ht)
+            want.append([o.detach().clone() for o in step()])
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for k in (0, 1, 0):
+        with torch.no_grad():
+            x.copy_(Ht if k == 0 else -Ht)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want[k]):
+            assert torch.equal(a, b)
+
+
 def test_two_streams_at_once(cuda_lib):
     """Calls whose work overlaps on the GPU, each with its own workspace and the stream argument."""
     torch = _torch()
