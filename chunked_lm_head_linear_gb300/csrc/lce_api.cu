@@ -1044,9 +1044,10 @@ TokLayout tok_layout(int64_t N, int64_t d, int64_t V, bool with_z, bool with_gra
 }
 
 // Temperatures from 1e-6 to 1e6 (the masked columns' -1e30 stays finite over them); a vocabulary within
-// 1024 of 2^31 is refused, so that column numbers rounded up to a tile stay 32-bit.
+// 65536 of 2^31 is refused, so that column numbers rounded up to a tile, or a stride past the end, stay
+// 32-bit.
 int check_token_args(int64_t V, float t) {
-  return V <= (int64_t{1} << 31) - 1024 && t >= 1.0e-6f && t <= 1.0e6f ? LCE_OK : LCE_ERR_INVALID_ARG;
+  return V <= (int64_t{1} << 31) - 65536 && t >= 1.0e-6f && t <= 1.0e6f ? LCE_OK : LCE_ERR_INVALID_ARG;
 }
 
 // Fills the call record of a token operator (after its own argument checks).

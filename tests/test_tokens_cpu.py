@@ -124,7 +124,7 @@ def test_logprobs_refusals(lib):
 
     for bad in (dict(H=None), dict(W=None), dict(y=None), dict(logp=None), dict(lse=None), dict(tl=None),
                 dict(ti=None), dict(ws=None), dict(N=-1), dict(d=12), dict(V=0), dict(T=0.0), dict(T=-1.0),
-                dict(T=float("nan")), dict(T=float("inf")), dict(T=9e-7), dict(T=2e6), dict(V=2 ** 31 - 1), dict(K=-1), dict(K=E.LCE_MAX_TOP + 1), dict(K=6, V=5),
+                dict(T=float("nan")), dict(T=float("inf")), dict(T=9e-7), dict(T=2e6), dict(V=2 ** 31 - 1), dict(V=2 ** 31 - 65535), dict(K=-1), dict(K=E.LCE_MAX_TOP + 1), dict(K=6, V=5),
                 dict(opts=lce.make_opts(reserved=1)), dict(opts=lce.make_opts(chunk_tokens=-1))):
         assert call(**bad) == E.LCE_ERR_INVALID_ARG, bad
     for bad in (dict(H=P + 8), dict(W=P + 2), dict(y=P + 4), dict(logp=P + 1), dict(lse=P + 2), dict(ent=P + 2),
@@ -137,7 +137,7 @@ def test_logprobs_refusals(lib):
     assert [lce.lce_logits_stride(v) for v in (1, 256, 257, 151655)] == [256, 256, 512, 151808]
     torch = pytest.importorskip("torch")
     if not torch.cuda.is_available():   # these get as far as the device check
-        for good in (dict(), dict(ent=None), dict(K=0, tl=None, ti=None), dict(nbytes=need),
+        for good in (dict(), dict(ent=None), dict(K=0, tl=None, ti=None), dict(nbytes=need), dict(V=2 ** 31 - 65536, nbytes=1 << 50),
                      dict(kept=P, nbytes=less),
                      dict(N=0, H=None, y=None, logp=None, lse=None, tl=None, ti=None)):
             assert call(**good) in (E.LCE_ERR_CUDA, E.LCE_ERR_UNSUPPORTED_DEVICE), good

@@ -567,6 +567,18 @@ def test_autograd_modules(cuda_lib):
         torch.autograd.grad(loss, [Ht, Wt])
     with torch.no_grad():
         assert torch.equal(kd(Ht, Wt, dev(idx), dev(t)), loss)
+    # one side frozen; a loss scale that is a power of two rounds nothing
+    for h, w_, k in ((Ht, Wt.detach(), 0), (Ht.detach(), Wt, 1)):
+        got, = torch.autograd.grad(1024.0 * kd(h, w_, dev(idx), dev(t)), (h, w_)[k])
+        want = oracle.distill_f64(H, W, idx, t, temperature=2.0, grad_loss=1024.0)
+        check_grads(got if k == 0 else None, got if k == 1 else None, want)
+    # no tokens
+    none = torch.zeros(0, 64, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    dH, dW = torch.autograd.grad(kd(none, Wt, dev(idx[:0]), dev(t[:0])), [none, Wt])
+    assert dH.shape == (0, 64) and not dW.any()
+    logp, ent = FusedLinearLogProbs()(none, Wt, dev(y[:0]))
+    dH, dW = torch.autograd.grad(logp.sum() + ent.sum(), [none, Wt])
+    assert dH.shape == (0, 64) and not dW.any()
 
 
 @pytest.mark.parametrize("N", [8, 300])
