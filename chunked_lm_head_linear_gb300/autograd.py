@@ -81,6 +81,18 @@ class FusedLinearCrossEntropy(torch.nn.Module):
         return fn.apply(H, W, y, self.opts)
 
 
+def _first_order(gradients):
+    """A Function's backward whose gradients are not differentiable themselves:
+    once_differentiable, whose bookkeeping is left out where no graph of the
+    backward is asked for."""
+    checked = once_differentiable(gradients)
+
+    def backward(ctx, *g):
+        return checked(ctx, *g) if torch.is_grad_enabled() else gradients(ctx, *g)
+
+    return staticmethod(backward)
+
+
 class _LogProbs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, H, W, y, temperature, keep, opts):
@@ -88,22 +100,22 @@ class _LogProbs(torch.autograd.Function):
         if keep and (ctx.needs_input_grad[0] or ctx.needs_input_grad[1]):
             logits = torch.empty((H.shape[0], (W.shape[0] + 255) // 256 * 256), dtype=torch.float32, device=H.device)
         logp, lse, entropy, _, _ = lce.lce_logprobs(H, W, y, temperature=temperature, logits=logits, **opts)
-        ctx.save_for_backward(H, W, y, logp, lse, entropy, logits)
-        ctx.temperature, ctx.opts = temperature, opts
+        ctx.save_for_backward(H, W, y, logp, entropy)
+        ctx.lse, ctx.logits, ctx.temperature, ctx.opts = lse, logits, temperature, opts
         ctx.set_materialize_grads(False)   # an output nobody used comes back as None
         return logp, entropy
 
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, g_logp, g_entropy):
-        H, W, y, logp, lse, entropy, logits = ctx.saved_tensors
-        g_logp = torch.zeros_like(lse) if g_logp is None else g_logp.contiguous()
+    def _gradients(ctx, g_logp, g_entropy):
+        H, W, y, logp, entropy = ctx.saved_tensors
+        g_logp = torch.zeros_like(logp) if g_logp is None else g_logp.contiguous()
         g_entropy = None if g_entropy is None else g_entropy.contiguous()
         # the forward checked its tensors, autograd that the gradients are like the outputs
-        dH, dW = lce._logprobs_backward(H, W, y, logp, lse, entropy, g_logp, g_entropy, logits, ctx.temperature,
-                                        lce.LCE_DW_BF16, None, ctx.needs_input_grad[0], ctx.needs_input_grad[1], None,
-                                        None, ctx.opts)
+        need_dH, need_dW = ctx.needs_input_grad[:2]
+        dH, dW = lce._logprobs_backward(H, W, y, logp, ctx.lse, entropy, g_logp, g_entropy, ctx.logits,
+                                        ctx.temperature, lce.LCE_DW_BF16, None, need_dH, need_dW, None, None, ctx.opts)
         return dH, dW, None, None, None, None
+
+    backward = _first_order(_gradients)
 
 
 class FusedLinearLogProbs(torch.nn.Module):
@@ -143,16 +155,16 @@ class _Distillation(torch.autograd.Function):
         ctx.grads = dH, dW
         return loss.reshape(())
 
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, g):
+    def _gradients(ctx, g):
         if ctx.grads is None:
             raise RuntimeError("FusedLinearDistillation: the gradients were handed out by an earlier backward pass "
                                "of this graph; run the forward again")
         dH, dW = ctx.grads
         ctx.grads = None
-        lce.lce_scale_grads_bfloat(dH, dW, g.reshape(1).to(torch.float32).contiguous())
+        lce.lce_scale_grads_bfloat(dH, dW, g)
         return dH, dW, None, None, None
+
+    backward = _first_order(_gradients)
 
 
 class FusedLinearDistillation(torch.nn.Module):
