@@ -7,7 +7,9 @@ definitions with numpy on whole [N, V] arrays (small cases only).
 The gradients come with ``bulk``: the sum of the absolute values of the terms
 whose sum the gradient is, dH_bulk = |G| |W| and dW_bulk = |G|^T |H| with |G|
 the absolute values of each part of G. A bound on the relative error of every
-term, times the bulk, bounds the error of the element.
+term, times the bulk, bounds the error of the element. Log-probabilities add
+``slack``, the same sums over p |e|: what an absolute error of log p + entropy,
+which cancels in confident rows, is multiplied by.
 """
 from __future__ import annotations
 
@@ -54,7 +56,9 @@ def logprobs_backward_f64(H, W, y, g_logp, g_entropy, *, temperature=1.0, ignore
     hot[np.arange(N)[told], y[told]] = 1.0
     G = (hot * a - p * (a + e * dev)) / temperature
     size = (hot * np.abs(a) + p * (np.abs(a) + np.abs(e) * np.abs(dev))) / temperature
-    return {"dH": G @ W, "dW": G.T @ H, "dH_bulk": size @ np.abs(W), "dW_bulk": size.T @ np.abs(H)}
+    slack = p * np.abs(e) / temperature
+    return {"dH": G @ W, "dW": G.T @ H, "dH_bulk": size @ np.abs(W), "dW_bulk": size.T @ np.abs(H),
+            "dH_slack": slack @ np.abs(W), "dW_slack": slack.T @ np.abs(H)}
 
 
 def teacher_f64(idx, t, V, *, temperature=1.0, renormalize=True, ignore_index=IGNORE_INDEX):

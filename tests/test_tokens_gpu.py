@@ -21,7 +21,9 @@ u = 2^-8 (bf16):
                log-probabilities within (2 u + u^2 + 2^-10) bulk, its other
                operand bf16(scale H) being rounded as well; dH within (u + 2^-10)
                bulk plus its own rounding u |dH|; whole tensors within 5e-3
-               (rounding errors average: u / sqrt(3) each).
+               (rounding errors average: u / sqrt(3) each). Where log p + entropy
+               cancels, its absolute error, 14 times that of lse (2^-12), stays:
+               2^-12 times the sums over p |e| on top.
 """
 import numpy as np
 import pytest
@@ -100,7 +102,8 @@ def check_grads(dH, dW, ref, scaled=False):
             continue
         u = 2 * U + U * U if scaled and name == "dW" else U
         out = U * np.abs(ref[name]) if got.dtype == _torch().bfloat16 else 0.0
-        close(got, ref[name], (u + 2.0 ** -10) * ref[name + "_bulk"] + out + 1e-30, name)
+        slack = 2.0 ** -12 * ref[name + "_slack"] if scaled and name + "_slack" in ref else 0.0
+        close(got, ref[name], (u + 2.0 ** -10) * ref[name + "_bulk"] + slack + out + 1e-30, name)
         norm = np.linalg.norm(ref[name])
         assert np.linalg.norm(np64(got) - ref[name]) <= 5e-3 * norm, name
 
