@@ -83,16 +83,16 @@ __device__ __forceinline__ void add_columns(Mst& a, float (&v)[32], float inv_t)
     a.s *= f;
     a.m = m;
   }
-  // Exponents to base 2 in one fma, z k - fl(m k); what m k loses by its rounding, the same for all,
-  // is made good once behind the sums.
-  const float mk = m * k, lost = fmaf(m, k, -mk);
-  const uint64_t m2 = pair_f32(-mk, -mk), k2 = pair_f32(k, k);
+  // The maximum is subtracted before the product with k, as in the merges behind: exponents
+  // err by their own rounding only, whatever the size of z / T. (One fma, z k - fl(m k), with what m k
+  // loses made good behind the sums, saves 1% at d = 256 and overflows at |m| / T above 3e9.)
+  const uint64_t m2 = pair_f32(-m, -m), k2 = pair_f32(k, k);
   uint64_t s[2] = {0, 0}, t[2] = {0, 0};
 #pragma unroll
   for (int c = 0; c < 32; c += 4) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint64_t y = fma_pair(pair_f32(v[c + 2 * i], v[c + 2 * i + 1]), k2, m2);
+      const uint64_t y = mul_pair(add_pair(pair_f32(v[c + 2 * i], v[c + 2 * i + 1]), m2), k2);
       float y0, y1;
       unpair_f32(y, y0, y1);
       const uint64_t e = pair_f32(ex2_approx(y0), ex2_approx(y1));
@@ -103,9 +103,8 @@ __device__ __forceinline__ void add_columns(Mst& a, float (&v)[32], float inv_t)
   float s0, s1, t0, t1;
   unpair_f32(add_pair(s[0], s[1]), s0, s1);
   unpair_f32(add_pair(t[0], t[1]), t0, t1);
-  const float fix = ex2_approx(-lost), sum = s0 + s1;
-  a.s = fmaf(sum, fix, a.s);
-  a.t = fmaf(fmaf(-lost, sum, t0 + t1) * kLn2, fix, a.t);
+  a.s += s0 + s1;
+  a.t = fmaf(t0 + t1, kLn2, a.t);
 }
 
 __device__ __forceinline__ RowSum warp_add(RowSum a) {

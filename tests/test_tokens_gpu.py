@@ -722,6 +722,35 @@ def test_caller_tensors_are_checked(cuda_lib):
         assert torch.equal(a, b)
 
 
+# --------------------------------------------------------------------------- cold, confident and masked rows
+@pytest.mark.parametrize("N", [5, 130])
+@pytest.mark.parametrize("T", [1e-6, 1e-4])
+def test_logprobs_of_large_logits_at_low_temperatures(cuda_lib, N, T):
+    """Logits of up to 7000 of either sign, ties among them, over temperatures that make them 7e9. z - max is exact,
+    so log-probabilities err by the roundings of 1 / T, the product and the last sum, 3 eps of themselves,
+    and by what lse - max / T errs by, below 2^-16 (13 times that in the entropy)."""
+    V, d = 3000, 512
+    rng = np.random.default_rng(N)
+    W = np.full((V, d), 1.5)
+    W[:, 64:] = grid(rng.standard_normal((V, 1)) / 8 + 1.25, 64)
+    H = np.repeat(rng.integers(60, 121, (N, 1)) / 16 * rng.choice([-1.0, 1.0], (N, 1)), d, axis=1)
+    y = rng.integers(0, V, N)
+    T = float(np.float32(T))
+    Ht, Wt, yt = *heads(H, W), dev(y)
+    assert np.abs(H @ W.T).max() > 4000
+    logp, lse, ent, tl, ti = cuda_lib.lce_logprobs(Ht, Wt, yt, top_k=9, temperature=T)
+    ref = oracle.logprobs_f64(H, W, y, temperature=T, top_k=9)
+    assert (ti.cpu().numpy() == ref["top_idx"]).all()
+    for got, name, part in ((logp, "logp", 1.0), (tl, "top_logp", 1.0), (lse, "lse", 1.0), (ent, "entropy", 13.0)):
+        assert np.isfinite(np64(got)).all(), name
+        close(got, ref[name], part * 2.0 ** -16 + 2.0 ** -22 * np.abs(ref[name]), name)
+    idx, t = ti, (tl * 0.0).contiguous()
+    loss, row = cuda_lib.lce_distill_forward(Ht, Wt, idx, t, temperature=T)
+    want = oracle.distill_f64(H, W, ref["top_idx"], np.zeros((N, 9)), temperature=T)
+    # T^2 (log q - mean of nine log-probabilities)
+    close(row, want["row_loss"], T * T * (2.0 ** -15 + 2.0 ** -21 * np.abs(ref["top_logp"]).max(axis=1)), "row_loss")
+
+
 # --------------------------------------------------------------------------- the bounds-checking build
 def _child():
     """Every kind of call on the bounds-checking build (a process loads one library): sync_check turns an
