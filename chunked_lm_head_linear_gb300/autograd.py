@@ -21,11 +21,11 @@ ranks) call ``lce.lce_fwd_bwd`` with their fp32 buffer as ``dW`` and
 ``accumulate_dW=True`` instead.
 
 FusedLinearLogProbs and FusedLinearDistillation wrap the token operators
-(lce_logprobs, lce_distill_fwd_bwd) the same way: log-probabilities and
+(lce_logprobs_keep, lce_distill_fwd_bwd) the same way: log-probabilities and
 entropies of given tokens, whose upstream gradients are known only in the
-backward, save logp, lse and entropy, and the logits of a batch of one chunk
-(else they are recomputed there); the distillation
-loss computes its gradients in the forward and scales them in the backward.
+backward, save logp, entropy and the rows' statistics, and the logits of a
+batch of one chunk (else they are recomputed there); the distillation loss
+computes its gradients in the forward and scales them in the backward.
 Gradients nobody needs (a frozen W) are not computed.
 """
 from __future__ import annotations
@@ -99,9 +99,9 @@ class _LogProbs(torch.autograd.Function):
         logits = None
         if keep and (ctx.needs_input_grad[0] or ctx.needs_input_grad[1]):
             logits = torch.empty((H.shape[0], (W.shape[0] + 255) // 256 * 256), dtype=torch.float32, device=H.device)
-        logp, lse, entropy, _, _ = lce.lce_logprobs(H, W, y, temperature=temperature, logits=logits, **opts)
+        logp, _, entropy, _, _, stats = lce.lce_logprobs_keep(H, W, y, temperature=temperature, logits=logits, **opts)
         ctx.save_for_backward(H, W, y, logp, entropy)
-        ctx.lse, ctx.logits, ctx.temperature, ctx.opts = lse, logits, temperature, opts
+        ctx.stats, ctx.logits, ctx.temperature, ctx.opts = stats, logits, temperature, opts
         ctx.set_materialize_grads(False)   # an output nobody used comes back as None
         return logp, entropy
 
@@ -111,7 +111,7 @@ class _LogProbs(torch.autograd.Function):
         g_entropy = None if g_entropy is None else g_entropy.contiguous()
         # the forward checked its tensors, autograd that the gradients are like the outputs
         need_dH, need_dW = ctx.needs_input_grad[:2]
-        dH, dW = lce._logprobs_backward(H, W, y, logp, ctx.lse, entropy, g_logp, g_entropy, ctx.logits,
+        dH, dW = lce._logprobs_backward(H, W, y, logp, None, ctx.stats, entropy, g_logp, g_entropy, ctx.logits,
                                         ctx.temperature, lce.LCE_DW_BF16, None, need_dH, need_dW, None, None, ctx.opts)
         return dH, dW, None, None, None, None
 

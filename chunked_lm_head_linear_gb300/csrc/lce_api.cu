@@ -994,6 +994,7 @@ struct TokLayout {
   int64_t ldz = 0;     // row stride of the logits buffer
   size_t Z = 0;
   size_t label = 0;    // the labels' entries of the gradient tile
+  size_t stats = 0;    // row statistics, where the backward computes them
   size_t dW = 0;       // fp32 sum of dW over the chunks before the last (dW_bf16 and several chunks)
   size_t total = 0;
 };
@@ -1029,9 +1030,10 @@ TokLayout tok_layout(int64_t N, int64_t d, int64_t V, bool with_z, bool with_gra
   L.ztgt = take(sizeof(float) * C);
   L.partials = take(sizeof(float4) * C * static_cast<size_t>(2 * L.T));
   if (with_z) T.Z = take(sizeof(float) * C * static_cast<size_t>(T.ldz));
-  if (with_scale) {  // row scales, the labels' entries and bf16(scale H)
+  if (with_scale) {  // row scales, the labels' entries, row statistics and bf16(scale H)
     L.alpha = take(sizeof(float) * C);
     T.label = take(sizeof(float) * C);
+    T.stats = take(sizeof(float2) * C);
     L.Ht = take(2 * C * static_cast<size_t>(d));
   }
   if (with_grad) {
@@ -1135,23 +1137,9 @@ int tok_grads(const Call& c, const TokLayout& T, int64_t c0, int64_t rows, const
   return dh_dw(c, c0, rows, rowscale, B, dH, dW, c.o.accumulate_dW || c0 > 0, false, part);
 }
 
-}  // namespace
-
-extern "C" {
-
-int64_t lce_logits_stride(int64_t V) { return V > 0 ? ceil_div(V, kVocabTile) * kVocabTile : 0; }
-
-size_t lce_logprobs_workspace_size(int64_t N, int64_t d, int64_t V, int32_t top_k, const lce_opts* opts) {
-  lce_opts o;
-  lce_opts_init(&o);
-  if (opts) o = *opts;
-  if (check_sizes(N, d, V, &o) != LCE_OK || top_k < 0 || top_k > LCE_MAX_TOP || top_k > V) return 0;
-  return tok_layout(N, d, V, top_k > 0, false, false, false, &o).total;
-}
-
-int lce_logprobs(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V, float temperature,
-                 int32_t top_k, float* logp, float* lse, float* entropy, float* top_logp, int64_t* top_idx,
-                 float* logits, const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
+int logprobs(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V, float temperature,
+             int32_t top_k, float* logp, float* lse, float* entropy, float* top_logp, int64_t* top_idx, float* logits,
+             float* stats, const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
   lce_opts o;
   lce_opts_init(&o);
   if (opts) o = *opts;
@@ -1162,7 +1150,7 @@ int lce_logprobs(const void* H, const void* W, const int64_t* y, int64_t N, int6
     return LCE_ERR_INVALID_ARG;
   if (!aligned(W, 16) || !aligned(H, 16) || !aligned(y, 8) || !aligned(ws, 256) || !aligned(logp, 4) ||
       !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(top_logp, 4) || !aligned(top_idx, 8) ||
-      !aligned(logits, 16))
+      !aligned(logits, 16) || !aligned(stats, 8))
     return LCE_ERR_ALIGNMENT;
   const TokLayout T = tok_layout(N, d, V, top_k > 0 && !logits, false, false, false, &o);
   Call c;
@@ -1191,6 +1179,7 @@ int lce_logprobs(const void* H, const void* W, const int64_t* y, int64_t N, int6
     a.logp = logp + c0;
     a.lse = lse + c0;
     a.entropy = entropy ? entropy + c0 : nullptr;
+    a.stats = stats ? reinterpret_cast<float2*>(stats) + c0 : nullptr;
     a.top_logp = top_k > 0 ? top_logp + c0 * top_k : nullptr;
     a.top_idx = top_k > 0 ? top_idx + c0 * top_k : nullptr;
     a.flags = p.flags;
@@ -1200,18 +1189,36 @@ int lce_logprobs(const void* H, const void* W, const int64_t* y, int64_t N, int6
   return finish(c);
 }
 
-size_t lce_logprobs_backward_workspace_size(int64_t N, int64_t d, int64_t V, int32_t grads, const lce_opts* opts) {
-  lce_opts o;
-  lce_opts_init(&o);
-  if (opts) o = *opts;
-  if (check_sizes(N, d, V, &o) != LCE_OK || (grads & ~LCE_DW_BF16) != 0) return 0;
-  return tok_layout(N, d, V, false, true, (grads & LCE_DW_BF16) != 0, true, &o).total;
+// Temperatures from which on lse alone serves the backward: its rounding is a relative error of p of 2^-23 |z / T|,
+// 2^-12 for logits of 128 at this one.
+constexpr float kLseCold = 0.0625f;
+
+// The row statistics (max z, log sum exp((z - max)/T)) of chunk rows [c0, c0 + rows): one pass over the logits.
+int row_stats(const Call& c, int64_t c0, int64_t rows, lce::TokParams p, float2* stats) {
+  p.reset = !lce::kChecks && c0 == 0;
+  LCE_TRY(tok_logits(c, c0, rows, lce::TOK_STATS, nullptr, 0, p));
+  lce::TokScoreArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.rows = p.rows;
+  a.V = p.V;
+  a.nparts = p.nparts;
+  a.inv_t = p.inv_t;
+  a.ignore_index = p.ignore_index;
+  a.y = p.y;
+  a.partials = p.partials;
+  a.ztgt = p.ztgt;
+  a.stats = stats;
+  a.flags = p.flags;
+  const double bytes = static_cast<double>(rows) * (32.0 * static_cast<double>(c.L.T) + 20.0);
+  return timed(c.s, K_COMBINE, bytes, [&] { return cuda_rc(lce::launch_score(a, c.s)); });
 }
 
-int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
-                          float temperature, const float* logp, const float* lse, const float* entropy,
-                          const float* g_logp, const float* g_entropy, const float* logits, int32_t grads, void* dH,
-                          void* dW, const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
+// stats: those of the forward, or null: lse takes their place (see GradRow in lce_tokens.cu), or, at temperatures
+// below kLseCold, they are computed anew, chunk by chunk.
+int logprobs_backward(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
+                      float temperature, const float* logp, const float* lse, const float* stats, const float* entropy,
+                      const float* g_logp, const float* g_entropy, const float* logits, int32_t grads, void* dH,
+                      void* dW, const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
   lce_opts o;
   lce_opts_init(&o);
   if (opts) o = *opts;
@@ -1219,11 +1226,11 @@ int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_
   LCE_TRY(check_token_args(V, temperature));
   const bool dW_bf16 = (grads & LCE_DW_BF16) != 0;
   if (o.reserved != 0 || (grads & ~LCE_DW_BF16) != 0 || (dW_bf16 && o.accumulate_dW) || !W || !ws || (!dH && !dW) ||
-      (N > 0 && (!H || !y || !logp || !lse || !g_logp || (g_entropy && !entropy))))
+      (N > 0 && (!H || !y || !logp || (!lse && !stats) || !g_logp || (g_entropy && !entropy))))
     return LCE_ERR_INVALID_ARG;
   if (!aligned(W, 16) || !aligned(H, 16) || !aligned(y, 8) || !aligned(ws, 256) || !aligned(dW, 16) ||
       !aligned(dH, 16) || !aligned(logp, 4) || !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(g_logp, 4) ||
-      !aligned(g_entropy, 4) || !aligned(logits, 16))
+      !aligned(g_entropy, 4) || !aligned(logits, 16) || !aligned(stats, 8))
     return LCE_ERR_ALIGNMENT;
   const TokLayout T = tok_layout(N, d, V, false, true, dW_bf16, true, &o);
   Call c;
@@ -1237,10 +1244,15 @@ int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_
   float* rowscale = reinterpret_cast<float*>(c.ws + c.L.alpha);
   float* label = reinterpret_cast<float*>(c.ws + T.label);
   uint16_t* Ht = reinterpret_cast<uint16_t*>(c.ws + c.L.Ht);
+  const bool anew = !stats && temperature < kLseCold;
+  if (anew && lce::kChecks && N > 0) LCE_TRY(prepare(c, nullptr));
   for (int64_t c0 = 0; c0 < N; c0 += c.L.C) {
     const int64_t rows = (N - c0) < c.L.C ? (N - c0) : c.L.C;
     lce::TokParams p = tok_params(c, c0, rows, temperature);
-    p.lse = lse + c0;
+    float2* found = reinterpret_cast<float2*>(c.ws + T.stats);
+    if (anew) LCE_TRY(row_stats(c, c0, rows, p, found));
+    p.lse = lse ? lse + c0 : nullptr;
+    p.stats = anew ? found : stats ? reinterpret_cast<const float2*>(stats) + c0 : nullptr;
     p.entropy = entropy ? entropy + c0 : nullptr;
     p.g_logp = g_logp + c0;
     p.g_entropy = g_entropy ? g_entropy + c0 : nullptr;
@@ -1257,6 +1269,7 @@ int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_
     a.y = p.y;
     a.logp = logp + c0;
     a.lse = p.lse;
+    a.stats = p.stats;
     a.entropy = p.entropy;
     a.g_logp = p.g_logp;
     a.g_entropy = p.g_entropy;
@@ -1268,6 +1281,7 @@ int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_
     a.G = reinterpret_cast<__nv_bfloat16*>(G);
     if (c0 == 0) {
       a.st = c.st;
+      a.keep_flags = anew ? 1 : 0;
       a.y_all = c.y;
       a.N = N;
       a.cnt = reinterpret_cast<int*>(c.ws + c.L.dh_cnt);
@@ -1280,6 +1294,60 @@ int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_
     LCE_TRY(tok_grads(c, T, c0, rows, rowscale, Ht, dH, dW, dW_bf16));
   }
   return finish(c);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t lce_logits_stride(int64_t V) { return V > 0 ? ceil_div(V, kVocabTile) * kVocabTile : 0; }
+
+size_t lce_logprobs_workspace_size(int64_t N, int64_t d, int64_t V, int32_t top_k, const lce_opts* opts) {
+  lce_opts o;
+  lce_opts_init(&o);
+  if (opts) o = *opts;
+  if (check_sizes(N, d, V, &o) != LCE_OK || top_k < 0 || top_k > LCE_MAX_TOP || top_k > V) return 0;
+  return tok_layout(N, d, V, top_k > 0, false, false, false, &o).total;
+}
+
+int lce_logprobs(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V, float temperature,
+                 int32_t top_k, float* logp, float* lse, float* entropy, float* top_logp, int64_t* top_idx,
+                 float* logits, const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
+  return logprobs(H, W, y, N, d, V, temperature, top_k, logp, lse, entropy, top_logp, top_idx, logits, nullptr, opts, ws,
+                  ws_bytes, stream);
+}
+
+int lce_logprobs_keep(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
+                      float temperature, int32_t top_k, float* logp, float* lse, float* entropy, float* top_logp,
+                      int64_t* top_idx, float* logits, float* stats, const lce_opts* opts, void* ws, size_t ws_bytes,
+                      void* stream) {
+  if (N > 0 && !stats) return LCE_ERR_INVALID_ARG;
+  return logprobs(H, W, y, N, d, V, temperature, top_k, logp, lse, entropy, top_logp, top_idx, logits, stats, opts, ws,
+                  ws_bytes, stream);
+}
+
+size_t lce_logprobs_backward_workspace_size(int64_t N, int64_t d, int64_t V, int32_t grads, const lce_opts* opts) {
+  lce_opts o;
+  lce_opts_init(&o);
+  if (opts) o = *opts;
+  if (check_sizes(N, d, V, &o) != LCE_OK || (grads & ~LCE_DW_BF16) != 0) return 0;
+  return tok_layout(N, d, V, false, true, (grads & LCE_DW_BF16) != 0, true, &o).total;
+}
+
+int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
+                          float temperature, const float* logp, const float* lse, const float* entropy,
+                          const float* g_logp, const float* g_entropy, const float* logits, int32_t grads, void* dH,
+                          void* dW, const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
+  return logprobs_backward(H, W, y, N, d, V, temperature, logp, lse, nullptr, entropy, g_logp, g_entropy, logits, grads,
+                           dH, dW, opts, ws, ws_bytes, stream);
+}
+
+int lce_logprobs_keep_backward(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
+                               float temperature, const float* logp, const float* stats, const float* entropy,
+                               const float* g_logp, const float* g_entropy, const float* logits, int32_t grads,
+                               void* dH, void* dW, const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
+  return logprobs_backward(H, W, y, N, d, V, temperature, logp, nullptr, stats, entropy, g_logp, g_entropy, logits,
+                           grads, dH, dW, opts, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

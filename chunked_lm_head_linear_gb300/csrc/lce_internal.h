@@ -241,7 +241,8 @@ struct TokParams {
   const int64_t* y;      // labels of this chunk (TOK_STATS, TOK_GRAD)
   float4* partials;      // [rows, nparts] (m, s, t, c), see lce_tokens.cu
   float* ztgt;           // [rows] logit of the label (TOK_STATS)
-  const float* lse;      // [rows] (TOK_GRAD; the next three too)
+  const float* lse;      // [rows] (TOK_GRAD; the next four too), used without stats
+  const float2* stats;   // [rows] (max z, log sum exp((z - max)/T)), or null
   const float* entropy;  // [rows]
   const float* g_logp;   // [rows] upstream gradients
   const float* g_entropy;  // [rows] or null
@@ -264,9 +265,10 @@ struct TokScoreArgs {
   const float4* partials;
   const float* ztgt;     // Z null: the label logits
   const float* Z;        // [rows, ldz] fp32 logits, or null (K == 0)
-  float* logp;           // [rows]
+  float* logp;           // [rows] or null, as the next three
   float* lse;            // [rows]
-  float* entropy;        // [rows] or null
+  float* entropy;        // [rows]
+  float2* stats;         // [rows] (max z, log sum exp((z - max)/T))
   float* top_logp;       // [rows, K]
   int64_t* top_idx;      // [rows, K]
   int* flags;
@@ -277,9 +279,10 @@ struct ScoreGradArgs {
   long long ldz, ldg;
   float inv_t;
   long long ignore_index;
-  const int64_t* y;      // [rows], as the next five
+  const int64_t* y;      // [rows], as the next six
   const float* logp;
   const float* lse;
+  const float2* stats;     // or null: lse
   const float* entropy;
   const float* g_logp;
   const float* g_entropy;  // or null
@@ -292,6 +295,7 @@ struct ScoreGradArgs {
   // first chunk only (st not null): the status block for N labels y_all and upstream factors of
   // one, and the dH part counters cnt[0, ncnt) cleared
   DevStatus* st;
+  int keep_flags;          // 1: an earlier launch of the call cleared the status bits and may have set some
   const int64_t* y_all;
   long long N;
   int* cnt;

@@ -146,7 +146,7 @@ __device__ __forceinline__ float log_sum(const RowSum& a) { return logf(a.c) + l
 //                buffer (top alternatives and distillation read them again:
 //                4 bytes a logit, written behind a main loop of d/16 MMAs)
 //   TOK_GRAD     the gradient tile of (logp, entropy) in bf16, from the saved
-//                lse and entropy, over the row's scale (see GradRow):
+//                statistics and entropy, over the row's scale (see GradRow):
 //                  G_v = ([v = y] a - p_v (a + e (z'_v - lse + entropy))) / T
 //                rounded to bf16 once (the operand type of the two GEMMs that
 //                follow), everything before it in fp32.
@@ -162,9 +162,13 @@ __device__ __forceinline__ float log_sum(const RowSum& a) { return logf(a.c) + l
 // one rounding in place of the label entry's, but of every element on its own
 // and so averaged over the row (errors against fp64, in units of one bf16
 // rounding, 250 rows: dH 1.3-1.6 -> 1.0, bf16 dW 1.3-1.5 -> 1.2-1.3).
-// An entry costs two fma, an exponential and a product: x = z k - lse log2 e, p = 2^x, g = p (c0 + c1 x).
+// An entry costs a sum, two fma, an exponential and a product: x = (z - m) k - L log2 e, p = 2^x,
+// g = p (c0 + c1 x), with the row's maximum m and L = log sum exp((z - m)/T): x errs by its own
+// rounding only, and log p + entropy keeps its relative precision in confident rows. Without them
+// m = 0 and L = lse, whose rounding at the size of z / T is an error of all of the row's p alike
+// (2^-23 |z / T|): the calls that have only lse take it for temperatures where that is small.
 struct GradRow {
-  float k = 0.f, shift = 0.f;  // x = z k + shift
+  float m = 0.f, k = 0.f, shift = 0.f;  // x = (z - m) k + shift
   float c0 = 0.f, c1 = 0.f;    // (-a - e entropy, -e ln 2) over the scale
   int y = -1;                  // the label, -1 where it is not given
   uint32_t keep = 0;           // 0: no upstream gradient, all bits: some
@@ -199,13 +203,15 @@ __device__ __forceinline__ float row_scale(const Upstream& u, float entry) {
   return size >= 1.0e-30f && size <= 1.0e30f && size >= 1.0e-12f * (fabsf(u.a) + fabsf(u.e)) ? entry : 1.f;
 }
 
-__device__ __forceinline__ GradRow grad_row(const Upstream& u, float scale, float lse, const float* entropy, int r,
-                                            float inv_t) {
+__device__ __forceinline__ GradRow grad_row(const Upstream& u, float scale, const float2* stats, const float* lse,
+                                            const float* entropy, int r, float inv_t) {
   GradRow g;
+  const float2 st = stats != nullptr ? stats[r] : make_float2(0.f, lse[r]);
   const float inv = 1.f / scale, e = u.e * inv;
   g.y = u.y;
   g.k = inv_t * kLog2e;
-  g.shift = -lse * kLog2e;
+  g.m = st.x;
+  g.shift = -st.y * kLog2e;
   g.c0 = -u.a * inv;
   if (u.e != 0.f) g.c0 -= e * entropy[r];
   g.c1 = -e * kLn2;
@@ -215,7 +221,8 @@ __device__ __forceinline__ GradRow grad_row(const Upstream& u, float scale, floa
 
 // Two entries, in bf16.
 __device__ __forceinline__ uint32_t grad_pair(float z0, float z1, const GradRow& r) {
-  const uint64_t x = fma_pair(pair_f32(z0, z1), pair_f32(r.k, r.k), pair_f32(r.shift, r.shift));
+  const uint64_t x = fma_pair(add_pair(pair_f32(z0, z1), pair_f32(-r.m, -r.m)), pair_f32(r.k, r.k),
+                              pair_f32(r.shift, r.shift));
   float x0, x1, g0, g1;
   unpair_f32(x, x0, x1);
   const uint64_t p = pair_f32(ex2_approx(x0), ex2_approx(x1));
@@ -332,8 +339,8 @@ struct TokEpi {
     GradRow g;
     float label = 0.f;
     if (r < p.rows) {
-      g = grad_row(upstream(r, p.y, p.ignore_index, p.V, p.g_logp, p.g_entropy, p.inv_t), p.rowscale[r], p.lse[r],
-                   p.entropy, r, p.inv_t);
+      g = grad_row(upstream(r, p.y, p.ignore_index, p.V, p.g_logp, p.g_entropy, p.inv_t), p.rowscale[r], p.stats,
+                   p.lse, p.entropy, r, p.inv_t);
       label = p.label[r];
     }
     const int ycol = g.y - col0;  // a column of this half tile, or outside [0, 128)
@@ -928,14 +935,15 @@ __global__ void __launch_bounds__(32 * WARPS) k_score(const TokScoreArgs p) {
   const RowSum acc = add_groups(s_sum);
   const float logs = log_sum(acc);
   if (threadIdx.x == 0) {
-    p.lse[r] = fmaf(M, p.inv_t, logs);
+    if (p.lse != nullptr) p.lse[r] = fmaf(M, p.inv_t, logs);
+    if (p.stats != nullptr) p.stats[r] = make_float2(M, logs);
     if (p.entropy != nullptr) p.entropy[r] = logs - acc.t / (acc.c + acc.s);
     const long long y = p.y[r];
     const bool given = y != p.ignore_index && y >= 0 && y < p.V;
     if (!given && y != p.ignore_index) atomicOr(p.flags, kFlagLabelRange);
     float lp = 0.f;
     if (given) lp = ((p.Z != nullptr ? z[y] : p.ztgt[r]) - M) * p.inv_t - logs;
-    p.logp[r] = lp;
+    if (p.logp != nullptr) p.logp[r] = lp;
   }
   if (p.K == 0) return;
   top.template finish<WARPS>(s_list, p.K, warp, lane);
@@ -989,7 +997,7 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_score_grad(const ScoreGradAr
     }
     bad = __syncthreads_or(bad);
     if (tid == 0) {
-      p.st->flags = bad ? kFlagLabelRange : 0;
+      p.st->flags = (p.keep_flags ? p.st->flags : 0) | (bad ? kFlagLabelRange : 0);
       p.st->gscale = 1.f;
       p.st->lscale = 1.0;
     }
@@ -1018,7 +1026,7 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_score_grad(const ScoreGradAr
   if (!TILE) return;
   const float* z = p.Z + static_cast<long long>(r) * p.ldz;
   __nv_bfloat16* g = p.G + static_cast<long long>(r) * p.ldg;
-  const GradRow row = grad_row(u, scale, p.lse[r], p.entropy, r, p.inv_t);
+  const GradRow row = grad_row(u, scale, p.stats, p.lse, p.entropy, r, p.inv_t);
   for (int c = tid * 8; c < p.V; c += kRowThreads * 8) {
     // columns past V (up to 7) lie inside the row's padding: never read by the GEMMs
     uint32_t o[4] = {0u, 0u, 0u, 0u};

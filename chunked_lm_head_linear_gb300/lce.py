@@ -16,6 +16,7 @@ Entry points (same names as the C ABI):
   lce_rmsnorm_forward / lce_rmsnorm_backward / lce_norm_fwd_bwd         the final RMSNorm, alone or fused
   lce_logprobs(H, W, y, top_k=..)        -> logp, lse, entropy, top_logp, top_idx
   lce_logprobs_backward(H, W, y, logp, lse, entropy, g_logp, g_entropy) -> dH, dW
+  lce_logprobs_keep / lce_logprobs_keep_backward   the same with the rows' statistics in place of lse
   lce_distill_forward(H, W, idx, t)      -> loss, row_loss against a teacher's top logits
   lce_distill_fwd_bwd(H, W, idx, t, g)   -> loss, row_loss, dH, dW
   lce_scale_grads, auto_chunk (lce_auto_chunk), workspace_size, read_device_status, profile_begin/end
@@ -56,7 +57,7 @@ EXPORTED = ("lce_opts_init", "lce_workspace_size", "lce_forward", "lce_backward"
             "lce_rmsnorm_workspace_size", "lce_rmsnorm_forward", "lce_rmsnorm_backward", "lce_norm_fwd_bwd",
             "lce_scale_grads", "lce_fwd_bwd_sliced", "lce_vshard_chunk_stats", "lce_vshard_chunk_backward",
             "lce_logits_stride", "lce_logprobs_workspace_size", "lce_logprobs", "lce_logprobs_backward_workspace_size",
-            "lce_logprobs_backward", "lce_distill_workspace_size", "lce_distill_forward", "lce_distill_fwd_bwd",
+            "lce_logprobs_backward", "lce_logprobs_keep", "lce_logprobs_keep_backward", "lce_distill_workspace_size", "lce_distill_forward", "lce_distill_fwd_bwd",
             "lce_scale_grads_bfloat")
 LCE_KERNEL_KINDS = 11
 # Kernel kinds whose profiled work is flops (tensor-core GEMMs); the others count bytes.
@@ -161,6 +162,10 @@ def load(path: str | None = None):
         lib.lce_logprobs_backward_workspace_size.restype = SZ
         lib.lce_logprobs_backward.argtypes = [P, P, P, I64, I64, I64, F32, P, P, P, P, P, P, I32, P, P, OPT, P, SZ, P]
         lib.lce_logprobs_backward.restype = I32
+        lib.lce_logprobs_keep.argtypes = [P, P, P, I64, I64, I64, F32, I32, P, P, P, P, P, P, P, OPT, P, SZ, P]
+        lib.lce_logprobs_keep.restype = I32
+        lib.lce_logprobs_keep_backward.argtypes = lib.lce_logprobs_backward.argtypes
+        lib.lce_logprobs_keep_backward.restype = I32
         lib.lce_distill_workspace_size.argtypes = [I64, I64, I64, I32, I32, I32, OPT]
         lib.lce_distill_workspace_size.restype = SZ
         lib.lce_distill_forward.argtypes = [P, P, P, P, I64, I64, I64, I32, I32, F32, P, P, OPT, P, SZ, P]
@@ -791,6 +796,18 @@ def lce_logprobs(H, W, y, *, top_k: int = 0, temperature: float = 1.0, entropy: 
     (int64) [N, top_k] (None if top_k is 0). logp is 0 where y is ignore_index.
     ``logits``: an fp32 tensor [N, lce_logits_stride(V)] that keeps z for
     lce_logprobs_backward."""
+    return _logprobs(H, W, y, top_k, temperature, entropy, logits, False, workspace, stream, opt_kw)[:5]
+
+
+def lce_logprobs_keep(H, W, y, *, top_k: int = 0, temperature: float = 1.0, entropy: bool = True, logits=None,
+                      workspace=None, stream=None, **opt_kw):
+    """lce_logprobs with one more result, stats (fp32 [N, 2]): each row's largest
+    logit and log sum exp((z - largest) / temperature), from which
+    lce_logprobs_keep_backward forms p without what lse loses by its rounding."""
+    return _logprobs(H, W, y, top_k, temperature, entropy, logits, True, workspace, stream, opt_kw)
+
+
+def _logprobs(H, W, y, top_k, temperature, entropy, logits, keep, workspace, stream, opt_kw):
     import torch
     N, d, V = _check_inputs(H, W, y)
     K, dev = int(top_k), H.device
@@ -802,15 +819,19 @@ def lce_logprobs(H, W, y, *, top_k: int = 0, temperature: float = 1.0, entropy: 
     lse = torch.empty(N, dtype=torch.float32, device=dev)
     ent = torch.empty(N, dtype=torch.float32, device=dev) if entropy else None
     top_logp = top_idx = None
+    stats = torch.empty((N, 2), dtype=torch.float32, device=dev) if keep else None
     if K > 0:
         top_logp = torch.empty((N, K), dtype=torch.float32, device=dev)
         top_idx = torch.empty((N, K), dtype=torch.int64, device=dev)
-    rc = load().lce_logprobs(_ptr(H), _ptr(W), _ptr(y), N, d, V, float(temperature), K, _ptr(logp), _ptr(lse),
-                             _ptr(ent), _ptr(top_logp), _ptr(top_idx), _ptr(logits), ctypes.byref(opts), _ptr(ws),
-                             ws.numel(), _stream(stream))
-    _raise(rc, "lce_logprobs")
-    _keep(stream, H, W, y, ws, logp, lse, ent, top_logp, top_idx, logits)
-    return logp, lse, ent, top_logp, top_idx
+    args = (_ptr(H), _ptr(W), _ptr(y), N, d, V, float(temperature), K, _ptr(logp), _ptr(lse), _ptr(ent),
+            _ptr(top_logp), _ptr(top_idx), _ptr(logits))
+    tail = (ctypes.byref(opts), _ptr(ws), ws.numel(), _stream(stream))
+    if keep:
+        _raise(load().lce_logprobs_keep(*args, _ptr(stats), *tail), "lce_logprobs_keep")
+    else:
+        _raise(load().lce_logprobs(*args, *tail), "lce_logprobs")
+    _keep(stream, H, W, y, ws, logp, lse, ent, top_logp, top_idx, logits, stats)
+    return logp, lse, ent, top_logp, top_idx, stats
 
 
 def lce_logprobs_backward(H, W, y, logp, lse, entropy, g_logp, g_entropy=None, *, temperature: float = 1.0, logits=None,
@@ -819,35 +840,56 @@ def lce_logprobs_backward(H, W, y, logp, lse, entropy, g_logp, g_entropy=None, *
     """dH (bf16 [N, d]) and dW (fp32 [V, d], or bf16 with dW_dtype) of
     lce_logprobs' logp and entropy for upstream gradients g_logp and g_entropy
     (fp32 [N]; g_entropy may be None), from its logp, lse and entropy and, if it
-    kept them, its logits. A gradient that is not wanted is None."""
+    kept them, its logits. A gradient that is not wanted is None. p errs by up to
+    2^-23 |z / temperature| with lse, and temperatures below 1/16 cost one more
+    pass over the logits: lce_logprobs_keep_backward has neither."""
+    _check_upstream(H, W, y, dict(logp=logp, lse=lse, g_logp=g_logp), entropy, g_entropy, logits)
+    return _logprobs_backward(H, W, y, logp, lse, None, entropy, g_logp, g_entropy, logits, temperature,
+                              _dW_mode(dW_dtype), dW, need_dH, need_dW, workspace, stream, opt_kw)
+
+
+def lce_logprobs_keep_backward(H, W, y, logp, stats, entropy, g_logp, g_entropy=None, *, temperature: float = 1.0,
+                               logits=None, dW=None, dW_dtype=None, need_dH: bool = True, need_dW: bool = True,
+                               workspace=None, stream=None, **opt_kw):
+    """lce_logprobs_backward from lce_logprobs_keep's stats in place of lse."""
+    import torch
+    if stats is None:
+        raise ValueError("stats is required")
+    _check_upstream(H, W, y, dict(logp=logp, g_logp=g_logp), entropy, g_entropy, logits)
+    _check_dev(stats, "stats", torch.float32, shape=(H.shape[0], 2), device=H.device)
+    return _logprobs_backward(H, W, y, logp, None, stats, entropy, g_logp, g_entropy, logits, temperature,
+                              _dW_mode(dW_dtype), dW, need_dH, need_dW, workspace, stream, opt_kw)
+
+
+def _check_upstream(H, W, y, required, entropy, g_entropy, logits):
     import torch
     N, d, V = _check_inputs(H, W, y)
-    for name, t in (("logp", logp), ("lse", lse), ("g_logp", g_logp)):
+    for name, t in required.items():
         if t is None:
             raise ValueError(f"{name} is required")
     if g_entropy is not None and entropy is None:
         raise ValueError("g_entropy needs the entropy of lce_logprobs")
-    for name, t in (("logp", logp), ("lse", lse), ("entropy", entropy), ("g_logp", g_logp), ("g_entropy", g_entropy)):
+    for name, t in dict(required, entropy=entropy, g_entropy=g_entropy).items():
         _check_dev(t, name, torch.float32, shape=(N,), device=H.device)
     if logits is not None:
         _check_dev(logits, "logits", torch.float32, shape=(N, (V + 255) // 256 * 256), device=H.device)
-    return _logprobs_backward(H, W, y, logp, lse, entropy, g_logp, g_entropy, logits, temperature,
-                              _dW_mode(dW_dtype), dW, need_dH, need_dW, workspace, stream, opt_kw)
 
 
-def _logprobs_backward(H, W, y, logp, lse, entropy, g_logp, g_entropy, logits, temperature, grads, dW, need_dH,
+def _logprobs_backward(H, W, y, logp, lse, stats, entropy, g_logp, g_entropy, logits, temperature, grads, dW, need_dH,
                        need_dW, workspace, stream, opt_kw):
-    """lce_logprobs_backward on tensors that are known to fit each other (those
-    of a forward that checked them)."""
+    """lce_logprobs_backward (from lse) or lce_logprobs_keep_backward (from stats)
+    on tensors that are known to fit each other (those of a forward that checked
+    them)."""
     (N, d), V = H.shape, W.shape[0]
     opts, ws = _token_plan(opt_kw, N, "lce_logprobs_backward", H.device, workspace,
                            lambda o: lce_logprobs_backward_workspace_size(N, d, V, grads, o))
     dH, dW = _token_grads(H, V, d, opts, grads, dW, need_dH, need_dW)
-    rc = load().lce_logprobs_backward(_ptr(H), _ptr(W), _ptr(y), N, d, V, float(temperature), _ptr(logp), _ptr(lse),
-                                      _ptr(entropy), _ptr(g_logp), _ptr(g_entropy), _ptr(logits), grads, _ptr(dH),
-                                      _ptr(dW), ctypes.byref(opts), _ptr(ws), ws.numel(), _stream(stream))
-    _raise(rc, "lce_logprobs_backward")
-    _keep(stream, H, W, y, ws, logp, lse, entropy, g_logp, g_entropy, logits, dH, dW)
+    call = load().lce_logprobs_backward if stats is None else load().lce_logprobs_keep_backward
+    rc = call(_ptr(H), _ptr(W), _ptr(y), N, d, V, float(temperature), _ptr(logp), _ptr(lse if stats is None else stats),
+              _ptr(entropy), _ptr(g_logp), _ptr(g_entropy), _ptr(logits), grads, _ptr(dH), _ptr(dW), ctypes.byref(opts),
+              _ptr(ws), ws.numel(), _stream(stream))
+    _raise(rc, "lce_logprobs_backward" if stats is None else "lce_logprobs_keep_backward")
+    _keep(stream, H, W, y, ws, logp, lse, entropy, g_logp, g_entropy, logits, stats, dH, dW)
     return dH, dW
 
 

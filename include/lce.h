@@ -330,6 +330,9 @@ int lce_scale_grads(void* dH, float* dW, int64_t N, int64_t d, int64_t V, const 
  * where y_i is ignored) and e_i = g_entropy_i
  *   G_iv = ([v = y_i] a_i - p_iv (a_i + e_i (log p_iv + entropy_i))) / temperature
  *   dH = G W (bf16), dW = G^T H (fp32; added to with opts->accumulate_dW).
+ * p is formed from lse, whose rounding becomes a relative error of p of up to
+ * 2^-23 max |z'|; at temperatures below 1/16, where that would count, the call
+ * computes the row statistics below anew (one more pass over the logits of H and W).
  * G is held in bf16 over a scale per row, its label's entry, by which dH is
  * multiplied in fp32; dW is its product with bf16(scale H). A row whose upstream
  * gradients are zero is zero in G and dH whatever its logits are. Either of dH, dW may be NULL: not wanted, not
@@ -337,6 +340,13 @@ int lce_scale_grads(void* dH, float* dW, int64_t N, int64_t d, int64_t V, const 
  * once (not with accumulate_dW; several chunks are summed in fp32 in the
  * workspace). logits: those of lce_logprobs, or NULL: recomputed chunk by
  * chunk. Workspace: lce_logprobs_backward_workspace_size.
+ *
+ * lce_logprobs_keep is lce_logprobs with one more output, stats [N, 2] (fp32,
+ * 8-byte aligned): max_v z_iv and log sum_v exp((z_iv - max_v z_iv) / temperature),
+ * which hold lse without the rounding of max / temperature.
+ * lce_logprobs_keep_backward is lce_logprobs_backward with them in place of lse:
+ * p keeps its relative precision for logits and temperatures of any size, and
+ * log p + entropy in rows where one token has nearly all of p.
  */
 #define LCE_MAX_TOP 128
 #define LCE_DW_BF16 1
@@ -345,11 +355,19 @@ size_t lce_logprobs_workspace_size(int64_t N, int64_t d, int64_t V, int32_t top_
 int lce_logprobs(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V, float temperature,
                  int32_t top_k, float* logp, float* lse, float* entropy, float* top_logp, int64_t* top_idx,
                  float* logits, const lce_opts* opts, void* ws, size_t ws_bytes, void* stream);
+int lce_logprobs_keep(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
+                      float temperature, int32_t top_k, float* logp, float* lse, float* entropy, float* top_logp,
+                      int64_t* top_idx, float* logits, float* stats, const lce_opts* opts, void* ws, size_t ws_bytes,
+                      void* stream);
 size_t lce_logprobs_backward_workspace_size(int64_t N, int64_t d, int64_t V, int32_t grads, const lce_opts* opts);
 int lce_logprobs_backward(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
                           float temperature, const float* logp, const float* lse, const float* entropy,
                           const float* g_logp, const float* g_entropy, const float* logits, int32_t grads, void* dH,
                           void* dW, const lce_opts* opts, void* ws, size_t ws_bytes, void* stream);
+int lce_logprobs_keep_backward(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
+                               float temperature, const float* logp, const float* stats, const float* entropy,
+                               const float* g_logp, const float* g_entropy, const float* logits, int32_t grads,
+                               void* dH, void* dW, const lce_opts* opts, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Distillation from a teacher's top logits: per row, K tokens idx [N, K]

@@ -245,3 +245,34 @@ def test_token_chunks_are_equal_by_default():
     for n, chunk in ((1, 1), (300, 300), (4096, 4096), (5000, 5000), (6143, 6143), (7000, 3584), (8192, 4096),
                      (10000, 5120), (100000, 4352)):
         assert size(n, 0) == size(n, chunk), n
+
+
+def test_kept_statistics_refusals(lib):
+    """lce_logprobs_keep and lce_logprobs_keep_backward check what their plain forms check, and their stats."""
+    E, P = lce, FAKE
+
+    def fwd(stats=P, lse=P, kept=None, N=64, nbytes=1 << 40):
+        o = lce.make_opts()
+        return lib.lce_logprobs_keep(P, P, P, N, 64, 1000, 1.0, 0, P, lse, P, None, None, kept, stats, ctypes.byref(o), P,
+                                     nbytes, None)
+
+    def bwd(stats=P, logp=P, ent=P, g2=P, T=1.0, N=64, nbytes=1 << 40):
+        o = lce.make_opts()
+        return lib.lce_logprobs_keep_backward(P, P, P, N, 64, 1000, T, logp, stats, ent, P, g2, None, 0, P, P,
+                                              ctypes.byref(o), P, nbytes, None)
+
+    for rc in (fwd(stats=None), fwd(lse=None), bwd(stats=None), bwd(logp=None), bwd(ent=None), bwd(T=9e-7)):
+        assert rc == E.LCE_ERR_INVALID_ARG
+    for rc in (fwd(stats=P + 4), fwd(kept=P + 4), bwd(stats=P + 4), bwd(g2=P + 1)):
+        assert rc == E.LCE_ERR_ALIGNMENT
+    assert fwd(nbytes=lce.lce_logprobs_workspace_size(64, 64, 1000, 0) - 1) == E.LCE_ERR_WORKSPACE
+    assert bwd(nbytes=lce.lce_logprobs_backward_workspace_size(64, 64, 1000) - 1) == E.LCE_ERR_WORKSPACE
+    torch = pytest.importorskip("torch")
+    f = torch.zeros(4)
+    H, W, y = torch.zeros(4, 8).bfloat16(), torch.zeros(3, 8).bfloat16(), torch.zeros(4, dtype=torch.int64)
+    for call in (lambda: lce.lce_logprobs_keep(H, W, y), lambda: lce.lce_logprobs_keep_backward(H, W, y, f, f, f, f)):
+        with pytest.raises(ValueError, match="CUDA tensors"):
+            call()
+    if not torch.cuda.is_available():   # these get as far as the device check
+        for rc in (fwd(), bwd(), bwd(T=1e-6), fwd(N=0, stats=None), bwd(N=0, stats=None)):
+            assert rc in (E.LCE_ERR_CUDA, E.LCE_ERR_UNSUPPORTED_DEVICE)

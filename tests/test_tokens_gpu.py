@@ -751,6 +751,163 @@ def test_logprobs_of_large_logits_at_low_temperatures(cuda_lib, N, T):
     close(row, want["row_loss"], T * T * (2.0 ** -15 + 2.0 ** -21 * np.abs(ref["top_logp"]).max(axis=1)), "row_loss")
 
 
+def near_ties(N, T, seed=0, boost=1.0):
+    """Rows whose largest logits, boost * 16 to 31, lie a few steps of boost * 2^-18 apart or are equal: a
+    distribution over many words however low the temperature. Exact in fp32 in any order of the sum
+    (whole multiples of boost * 2^-18 below boost * 64). The words' other features meet zeros of H."""
+    rng = np.random.default_rng(seed)
+    V, d = 700, 64
+    W = grid(rng.standard_normal((V, d)), 64)
+    W[:, 0] = np.where(np.arange(V) % 2 == 0, 8.0, rng.integers(-32, 31, V) / 4)
+    W[:, 1] = rng.integers(0, 64, V) * 2.0 ** -18
+    H = np.zeros((N, d))
+    H[:, 0] = 2 + rng.integers(0, 31, N) / 16
+    H[:, 1] = 1.0
+    y = 2 * rng.integers(0, V // 2, N)
+    y[::7] += 1                          # an unlikely label
+    y[3::11] = oracle.IGNORE_INDEX
+    return rng, H * boost, W, y, float(np.float32(T * boost))
+
+
+def with_underflow(ref, H, W, T):
+    """The bounds of check_grads with what fp32 cannot hold. An entry of G is p c with |c| <= (|a| + |e| (|log p|
+    + entropy)) / T. p below 2^-126 may be 0, where |log p| is 88 (p |log p| only falls with p), the entropy
+    below 7 and |a|, |e| below 5: 2^-126 5 96 / T < 2^-117 / T is lost; as much again where the entry over its
+    row's scale, itself at most such a c, is below 2^-126. Sums over rows and words follow."""
+    lost = 2.0 ** -116 / T / U      # the bounds take at least U of the bulk
+    return dict(ref, dH_bulk=ref["dH_bulk"] + lost * np.abs(W).sum(axis=0),
+                dW_bulk=ref["dW_bulk"] + lost * np.abs(H).sum(axis=0))
+
+
+COLD = [1.0, 1e-2, 1e-3, 1e-4, 1e-5, 1e-6]
+
+
+@pytest.mark.parametrize("N", [5, 130])
+@pytest.mark.parametrize("T", COLD)
+def test_gradients_at_low_temperatures(cuda_lib, N, T):
+    """p does not lose what z / T is rounded by: logits of 20 to 30 with near-ties, down to the coldest
+    temperature, recomputed and kept. The bounds are those of ordinary temperatures: with exact logits
+    the exponents (z - max) / T err by 2^-23 of themselves only."""
+    torch = _torch()
+    rng, H, W, y, T = near_ties(N, T, seed=N)
+    Ht, Wt, yt = *heads(H, W), dev(y)
+    g1, g2 = rng.standard_normal(N).astype(np.float32), rng.standard_normal(N).astype(np.float32)
+    ref = oracle.logprobs_backward_f64(H, W, y, g1, g2, temperature=T)
+    ref = with_underflow(ref, H, W, T)
+    kept = torch.empty(N, cuda_lib.lce_logits_stride(len(W)), device="cuda")
+    logp, lse, ent, _, _ = cuda_lib.lce_logprobs(Ht, Wt, yt, temperature=T, logits=kept)
+    for logits in (None, kept):
+        dH, dW = cuda_lib.lce_logprobs_backward(Ht, Wt, yt, logp, lse, ent, dev(g1), dev(g2), temperature=T,
+                                                logits=logits)
+        check_grads(dH, dW, ref, scaled=True)
+
+
+@pytest.mark.parametrize("N", [5, 130])
+@pytest.mark.parametrize("T,boost", [(t, 1.0) for t in COLD] + [(2.0 ** -15, 2.0 ** 15), (1e-4, 2.0 ** 17)])
+def test_autograd_at_low_temperatures_and_large_logits(cuda_lib, N, T, boost):
+    """The same through the module, and with logits of up to 2^22 at temperatures near 1."""
+    torch = _torch()
+    from chunked_lm_head_linear_gb300.autograd import FusedLinearLogProbs
+    rng, H, W, y, T = near_ties(N, T, seed=N + 1, boost=boost)
+    Ht, Wt = (x.requires_grad_(True) for x in heads(H, W))
+    g = [dev(rng.standard_normal(N).astype(np.float32)) for _ in range(2)]
+    ref = oracle.logprobs_backward_f64(H, W, y, np64(g[0]), np64(g[1]), temperature=T)
+    ref = with_underflow(ref, H, W, T)
+    for recompute in (True, False):
+        out = FusedLinearLogProbs(temperature=T, recompute=recompute, chunk_tokens=100)(Ht, Wt, dev(y))
+        dH, dW = torch.autograd.grad(out, [Ht, Wt], g)
+        check_grads(dH, dW, ref, scaled=True)
+
+
+@pytest.mark.parametrize("N", [12, 200])
+def test_entropy_gradient_of_confident_rows(cuda_lib, N):
+    """One token has nearly all of p: log p + entropy is of the size of 1 - p there, and so is every entry
+    of G. Both keep their relative precision (2^-15, see the log-probabilities near zero; their sum is
+    20 to 30 times each, positive), so that no absolute error stays: the bound is the relative one alone."""
+    torch = _torch()
+    from chunked_lm_head_linear_gb300.autograd import FusedLinearLogProbs
+    V, d, label = 5000, 64, 1234
+    rng = np.random.default_rng(5)
+    W = grid(rng.standard_normal((V, d)), 64)
+    W[:, 0] = -1.0
+    W[label, 0] = 0.0
+    W[:, 1] = rng.integers(-8, 9, V) / 64
+    H = np.zeros((N, d))
+    H[:, 0] = 20 + np.arange(N) % 10
+    H[:, 1] = 1.0
+    y = np.where(np.arange(N) % 3 < 2, 77, label)
+    Ht, Wt = (x.requires_grad_(True) for x in heads(H, W))
+    g = rng.standard_normal(N).astype(np.float32)
+    ref = oracle.logprobs_backward_f64(H, W, y, np.zeros(N), g)
+    ref = {k: v for k, v in ref.items() if not k.endswith("_slack")}
+    for recompute in (True, False):
+        _, ent = FusedLinearLogProbs(recompute=recompute)(Ht, Wt, dev(y))
+        dH, dW = torch.autograd.grad(ent, [Ht, Wt], dev(g))
+        check_grads(dH, dW, ref, scaled=True)
+
+
+def _cold_child():
+    """The backward that computes the rows' statistics itself, and the one that is given them, on the
+    bounds-checking build."""
+    import torch
+
+    from chunked_lm_head_linear_gb300 import build, lce
+    lce.load(build.build(checks=True))
+    for N, chunk in [(1, 0), (96, 0), (130, 0), (300, 100)]:
+        rng, H, W, y, T = near_ties(N, 1e-4, seed=N)
+        Ht, Wt, yt = *heads(H, W), dev(y)
+        g = dev(rng.standard_normal(N).astype(np.float32))
+        ref = oracle.logprobs_backward_f64(H, W, y, np64(g), np64(g), temperature=T)
+        ref = with_underflow(ref, H, W, T)
+        kept = torch.empty(N, lce.lce_logits_stride(len(W)), device="cuda")
+        for logits in (None, kept):
+            kw = dict(temperature=T, chunk_tokens=chunk, logits=logits, sync_check=True)
+            logp, lse, ent, _, _, stats = lce.lce_logprobs_keep(Ht, Wt, yt, **kw)
+            check_grads(*lce.lce_logprobs_keep_backward(Ht, Wt, yt, logp, stats, ent, g, g, **kw), ref, scaled=True)
+            check_grads(*lce.lce_logprobs_backward(Ht, Wt, yt, logp, lse, ent, g, g, **kw), ref, scaled=True)
+    print("checked build: ok")
+
+
+def test_bounds_checking_build_at_a_low_temperature(cuda_lib):
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([os.path.dirname(here), here]))
+    r = subprocess.run([sys.executable, "-c", "import test_tokens_gpu as t; t._cold_child()"], env=env, cwd=here,
+                       capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and "checked build: ok" in r.stdout, (r.stdout + r.stderr)[-3000:]
+
+
+def test_cold_backward_tells_of_labels_and_captures(cuda_lib):
+    """The statistics pass leaves the status bits to the call: a label out of range is told and has no
+    gradient; and the call can be captured and replayed."""
+    torch = _torch()
+    rng, H, W, y, T = near_ties(130, 1e-4)
+    Ht, Wt, yt = *heads(H, W), dev(y)
+    g = dev(rng.standard_normal(130).astype(np.float32))
+    kw = dict(temperature=T, chunk_tokens=50)
+    logp, lse, ent, _, _ = cuda_lib.lce_logprobs(Ht, Wt, yt, **kw)
+    yt[3] = oracle.IGNORE_INDEX
+    want = cuda_lib.lce_logprobs_backward(Ht, Wt, yt, logp, lse, ent, g, g, **kw)
+    yt[3] = 700
+    with pytest.raises(cuda_lib.LCEError) as err:
+        cuda_lib.lce_logprobs_backward(Ht, Wt, yt, logp, lse, ent, g, g, sync_check=True, **kw)
+    assert err.value.code == cuda_lib.LCE_ERR_LABEL_RANGE
+    for a, b in zip(cuda_lib.lce_logprobs_backward(Ht, Wt, yt, logp, lse, ent, g, g, **kw), want):
+        assert torch.equal(a, b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = cuda_lib.lce_logprobs_backward(Ht, Wt, yt, logp, lse, ent, g, g, **kw)
+    for x in out:
+        x.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(out, want):
+        assert torch.equal(a, b)
+
+
 # --------------------------------------------------------------------------- the bounds-checking build
 def _child():
     """Every kind of call on the bounds-checking build (a process loads one library): sync_check turns an
