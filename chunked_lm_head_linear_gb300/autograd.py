@@ -26,7 +26,8 @@ entropies of given tokens, whose upstream gradients are known only in the
 backward, save logp, entropy and the rows' statistics, and the logits of a
 batch of one chunk (else they are recomputed there); the distillation loss
 computes its gradients in the forward and scales them in the backward.
-Gradients nobody needs (a frozen W) are not computed.
+Gradients nobody needs (a frozen W, torch.no_grad) are not computed, and nothing
+is kept for them.
 """
 from __future__ import annotations
 
@@ -136,6 +137,9 @@ class FusedLinearLogProbs(torch.nn.Module):
         self.opts = dict(ignore_index=ignore_index, chunk_tokens=chunk_tokens)
 
     def forward(self, H, W, y):
+        if not torch.is_grad_enabled():   # inside a Function grad mode is always off: only here it is the caller's
+            logp, _, entropy, _, _ = lce.lce_logprobs(H, W, y, temperature=self.temperature, **self.opts)
+            return logp, entropy
         keep = not self.recompute
         if self.recompute is None:
             chunk = self.opts["chunk_tokens"]
@@ -181,4 +185,6 @@ class FusedLinearDistillation(torch.nn.Module):
                        reduction=reduction, chunk_tokens=chunk_tokens)
 
     def forward(self, H, W, idx, t):
+        if not torch.is_grad_enabled():
+            return lce.lce_distill_forward(H, W, idx, t, **self.kw)[0].reshape(())
         return _Distillation.apply(H, W, idx, t, self.kw)

@@ -276,3 +276,59 @@ def test_kept_statistics_refusals(lib):
     if not torch.cuda.is_available():   # these get as far as the device check
         for rc in (fwd(), bwd(), bwd(T=1e-6), fwd(N=0, stats=None), bwd(N=0, stats=None)):
             assert rc in (E.LCE_ERR_CUDA, E.LCE_ERR_UNSUPPORTED_DEVICE)
+
+
+# --------------------------------------------------------------------------- the autograd modules, on fakes of the calls
+@pytest.fixture
+def fakes(monkeypatch):
+    """The binding's calls replaced by ones that record themselves and return tensors of the right shapes."""
+    torch = pytest.importorskip("torch")
+    seen = []
+
+    def logprobs(H, W, y, *, temperature=1.0, logits=None, **kw):
+        seen.append(("logprobs", logits is not None))
+        return tuple(torch.zeros(len(H)) for _ in range(3)) + (None, None)
+
+    def logprobs_keep(H, W, y, **kw):
+        return logprobs(H, W, y, **kw) + (torch.zeros(len(H), 2),)
+
+    def logprobs_backward(H, W, *args):
+        seen.append(("logprobs_backward",))
+        return torch.zeros_like(H), torch.zeros_like(W)
+
+    def distill_forward(H, W, idx, t, **kw):
+        seen.append(("distill_forward",))
+        return torch.zeros(1), torch.zeros(len(H))
+
+    def distill_fwd_bwd(H, W, idx, t, *, need_dH=True, need_dW=True, **kw):
+        seen.append(("distill_fwd_bwd", need_dH, need_dW))
+        return (torch.zeros(1), torch.zeros(len(H)), torch.zeros_like(H) if need_dH else None,
+                torch.zeros_like(W) if need_dW else None)
+
+    monkeypatch.setattr(lce, "lce_logprobs", logprobs)
+    monkeypatch.setattr(lce, "lce_logprobs_keep", logprobs_keep)
+    monkeypatch.setattr(lce, "_logprobs_backward", logprobs_backward)
+    monkeypatch.setattr(lce, "lce_distill_forward", distill_forward)
+    monkeypatch.setattr(lce, "lce_distill_fwd_bwd", distill_fwd_bwd)
+    monkeypatch.setattr(lce, "lce_scale_grads_bfloat", lambda dH, dW, g: None)
+    H = torch.zeros(4, 8, dtype=torch.bfloat16, requires_grad=True)
+    W = torch.zeros(30, 8, dtype=torch.bfloat16, requires_grad=True)
+    return seen, H, W, torch.zeros(4, dtype=torch.int64), torch.zeros(4, 2, dtype=torch.int64), torch.zeros(4, 2)
+
+
+@pytest.mark.parametrize("mode", ["no_grad", "inference_mode"])
+def test_modules_without_grad_mode_run_the_forward_alone(fakes, mode):
+    """Trainable tensors, but no graph: nothing is kept for a backward and no gradient computed."""
+    import torch
+
+    from chunked_lm_head_linear_gb300.autograd import FusedLinearDistillation, FusedLinearLogProbs
+    seen, H, W, y, idx, t = fakes
+    with getattr(torch, mode)():
+        logp, ent = FusedLinearLogProbs(recompute=False)(H, W, y)
+        loss = FusedLinearDistillation()(H, W, idx, t)
+    assert not (logp.requires_grad or ent.requires_grad or loss.requires_grad)
+    assert seen == [("logprobs", False), ("distill_forward",)]
+    del seen[:]
+    FusedLinearLogProbs(recompute=False)(H, W, y)
+    FusedLinearDistillation()(H, W.detach(), idx, t)
+    assert seen == [("logprobs", True), ("distill_fwd_bwd", True, False)]

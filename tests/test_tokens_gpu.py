@@ -908,6 +908,37 @@ def test_cold_backward_tells_of_labels_and_captures(cuda_lib):
         assert torch.equal(a, b)
 
 
+def _memory_case():
+    """Trainable inputs of both modules: 60 MB of logits, 6 MB of dW."""
+    torch = _torch()
+    N, V = 300, 50000
+    rng, H, W, y = make(N, 64, V)
+    Ht, Wt = (x.requires_grad_(True) for x in heads(H, W))
+    return (N, V, Ht, Wt, dev(y), dev(rng.integers(0, V, (N, 5))), dev(rng.standard_normal((N, 5)).astype(np.float32)),
+            torch.ones(N, device="cuda"))
+
+
+def test_no_grad_keeps_and_computes_nothing_for_a_backward(cuda_lib):
+    torch = _torch()
+    from chunked_lm_head_linear_gb300.autograd import FusedLinearDistillation, FusedLinearLogProbs
+    N, V, Ht, Wt, yt, idx, t, _ = _memory_case()
+    mod, kd = FusedLinearLogProbs(recompute=False), FusedLinearDistillation()
+    want = [x.detach() for x in (*mod(Ht, Wt, yt), kd(Ht, Wt, idx, t))]
+    for mode in (torch.no_grad, torch.inference_mode):
+        with mode():
+            for call, need in ((lambda: mod(Ht, Wt, yt), cuda_lib.lce_logprobs_workspace_size(N, 64, V)),
+                               (lambda: (kd(Ht, Wt, idx, t),), cuda_lib.lce_distill_workspace_size(N, 64, V, 5, False))):
+                torch.cuda.synchronize()
+                torch.cuda.reset_peak_memory_stats()
+                before = torch.cuda.memory_allocated()
+                got = call()
+                # the forward's workspace and its few results; memory is handed out in blocks of up to 2 MB
+                assert torch.cuda.max_memory_allocated() - before < need + (1 << 21)
+                assert not any(x.requires_grad for x in got)
+                for a, b in zip(got, want[:2] if len(got) == 2 else want[2:]):
+                    assert torch.equal(a, b) if len(got) == 1 else (a - b).abs().max() < 2.0 ** -14
+
+
 # --------------------------------------------------------------------------- the bounds-checking build
 def _child():
     """Every kind of call on the bounds-checking build (a process loads one library): sync_check turns an
