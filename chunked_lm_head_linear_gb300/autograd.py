@@ -101,19 +101,19 @@ class _LogProbs(torch.autograd.Function):
         if keep and (ctx.needs_input_grad[0] or ctx.needs_input_grad[1]):
             logits = torch.empty((H.shape[0], (W.shape[0] + 255) // 256 * 256), dtype=torch.float32, device=H.device)
         logp, _, entropy, _, _, stats = lce.lce_logprobs_keep(H, W, y, temperature=temperature, logits=logits, **opts)
-        ctx.save_for_backward(H, W, y, logp, entropy)
-        ctx.stats, ctx.logits, ctx.temperature, ctx.opts = stats, logits, temperature, opts
+        ctx.save_for_backward(H, W, y, logp, entropy, stats, logits)
+        ctx.temperature, ctx.opts = temperature, opts
         ctx.set_materialize_grads(False)   # an output nobody used comes back as None
         return logp, entropy
 
     def _gradients(ctx, g_logp, g_entropy):
-        H, W, y, logp, entropy = ctx.saved_tensors
+        H, W, y, logp, entropy, stats, logits = ctx.saved_tensors
         g_logp = torch.zeros_like(logp) if g_logp is None else g_logp.contiguous()
         g_entropy = None if g_entropy is None else g_entropy.contiguous()
         # the forward checked its tensors, autograd that the gradients are like the outputs
         need_dH, need_dW = ctx.needs_input_grad[:2]
-        dH, dW = lce._logprobs_backward(H, W, y, logp, None, ctx.stats, entropy, g_logp, g_entropy, ctx.logits,
-                                        ctx.temperature, lce.LCE_DW_BF16, None, need_dH, need_dW, None, None, ctx.opts)
+        dH, dW = lce._logprobs_backward(H, W, y, logp, None, stats, entropy, g_logp, g_entropy, logits, ctx.temperature,
+                                        lce.LCE_DW_BF16, None, need_dH, need_dW, None, None, ctx.opts)
         return dH, dW, None, None, None, None
 
     backward = _first_order(_gradients)

@@ -332,3 +332,21 @@ def test_modules_without_grad_mode_run_the_forward_alone(fakes, mode):
     FusedLinearLogProbs(recompute=False)(H, W, y)
     FusedLinearDistillation()(H, W.detach(), idx, t)
     assert seen == [("logprobs", True), ("distill_fwd_bwd", True, False)]
+
+
+def test_what_the_forward_keeps_is_freed_by_the_backward(fakes):
+    """The kept logits are saved tensors: freed with the graph's other ones, though an output lives on."""
+    import weakref
+
+    import torch
+
+    from chunked_lm_head_linear_gb300.autograd import FusedLinearLogProbs
+    _, H, W, y, _, _ = fakes
+    kept = []
+    keep = lce.lce_logprobs_keep
+    lce.lce_logprobs_keep = lambda *a, **kw: (kept.append(weakref.ref(kw["logits"])), keep(*a, **kw))[1]   # fakes undoes it
+    logp, _ = FusedLinearLogProbs(recompute=False)(H, W, y)
+    torch.autograd.grad(logp.sum(), [H, W], retain_graph=True)
+    assert kept[0]() is not None
+    torch.autograd.grad(logp.sum(), [H, W])
+    assert kept[0]() is None

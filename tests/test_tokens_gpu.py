@@ -939,6 +939,32 @@ def test_no_grad_keeps_and_computes_nothing_for_a_backward(cuda_lib):
                     assert torch.equal(a, b) if len(got) == 1 else (a - b).abs().max() < 2.0 ** -14
 
 
+def test_kept_logits_are_freed_by_the_backward(cuda_lib):
+    """After a backward that does not retain the graph nothing of the call is held but its outputs."""
+    import gc
+    torch = _torch()
+    from chunked_lm_head_linear_gb300.autograd import FusedLinearLogProbs
+    N, V, Ht, Wt, yt, _, _, w = _memory_case()
+    mod = FusedLinearLogProbs(recompute=False)
+    gc.collect()
+    torch.cuda.synchronize()
+    base = torch.cuda.memory_allocated()
+    logp, ent = mod(Ht, Wt, yt)
+    assert torch.cuda.memory_allocated() - base > 4 * N * V           # the logits wait for the backward
+    want = torch.autograd.grad(logp, [Ht, Wt], w, retain_graph=True)
+    got = torch.autograd.grad(logp, [Ht, Wt], w)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    del want, got
+    assert torch.cuda.memory_allocated() - base < 1 << 16             # logp and entropy are still here
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(logp, [Ht, Wt], w)
+    # saved-tensor hooks see them
+    seen = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda x: seen.append(x.numel()) or x, lambda x: x):
+        mod(Ht, Wt, yt)
+    assert N * cuda_lib.lce_logits_stride(V) in seen
+
+
 # --------------------------------------------------------------------------- the bounds-checking build
 def _child():
     """Every kind of call on the bounds-checking build (a process loads one library): sync_check turns an
