@@ -1232,7 +1232,7 @@ int logprobs_backward(const void* H, const void* W, const int64_t* y, int64_t N,
       !aligned(dH, 16) || !aligned(logp, 4) || !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(g_logp, 4) ||
       !aligned(g_entropy, 4) || !aligned(logits, 16) || !aligned(stats, 8))
     return LCE_ERR_ALIGNMENT;
-  const TokLayout T = tok_layout(N, d, V, false, true, dW_bf16, true, &o);
+  const TokLayout T = tok_layout(N, d, V, false, true, dW_bf16 && dW, true, &o);
   Call c;
   LCE_TRY(tok_begin(&c, T, H, W, y, N, d, V, o, ws, ws_bytes, stream));
   if (N == 0) {
@@ -1373,7 +1373,7 @@ int distill(const void* H, const void* W, const int64_t* idx, const void* t, int
   if (!aligned(W, 16) || !aligned(H, 16) || !aligned(idx, 8) || !aligned(t, t_bf16 ? 2 : 4) || !aligned(ws, 256) ||
       !aligned(loss, 4) || !aligned(row_loss, 4) || !aligned(grad_loss, 4) || !aligned(dH, 16) || !aligned(dW, 16))
     return LCE_ERR_ALIGNMENT;
-  const TokLayout T = tok_layout(N, d, V, true, with_grad, dW_bf16, false, &o);
+  const TokLayout T = tok_layout(N, d, V, true, with_grad, dW_bf16 && dW, false, &o);
   Call c;
   LCE_TRY(tok_begin(&c, T, H, W, nullptr, N, d, V, o, ws, ws_bytes, stream));
   int* cnt = with_grad ? reinterpret_cast<int*>(c.ws + c.L.dh_cnt) : nullptr;

@@ -881,6 +881,7 @@ def _logprobs_backward(H, W, y, logp, lse, stats, entropy, g_logp, g_entropy, lo
     on tensors that are known to fit each other (those of a forward that checked
     them)."""
     (N, d), V = H.shape, W.shape[0]
+    grads = grads if need_dW else 0
     opts, ws = _token_plan(opt_kw, N, "lce_logprobs_backward", H.device, workspace,
                            lambda o: lce_logprobs_backward_workspace_size(N, d, V, grads, o))
     dH, dW = _token_grads(H, V, d, opts, grads, dW, need_dH, need_dW)
@@ -953,6 +954,7 @@ def lce_distill_fwd_bwd(H, W, idx, t, grad_loss=None, *, temperature: float = 1.
     teacher = _distill_mode(teacher, renormalize, temperature)
     _check_dev(grad_loss, "grad_loss", torch.float32, numel=1, device=H.device)
     grads = _dW_mode(dW_dtype)
+    grads = grads if need_dW else 0
     opts, ws = _token_plan(opt_kw, N, "lce_distill", H.device, workspace,
                            lambda o: lce_distill_workspace_size(N, d, V, K, True, grads, o))
     loss = torch.empty(1, dtype=torch.float32, device=H.device)

@@ -338,7 +338,7 @@ int lce_scale_grads(void* dH, float* dW, int64_t N, int64_t d, int64_t V, const 
  * gradients are zero is zero in G and dH whatever its logits are. Either of dH, dW may be NULL: not wanted, not
  * computed. grads: 0, or LCE_DW_BF16: dW is bf16 [V, d], the fp32 sum rounded
  * once (not with accumulate_dW; several chunks are summed in fp32 in the
- * workspace). logits: those of lce_logprobs, or NULL: recomputed chunk by
+ * workspace, for which a call without dW needs no room: grads = 0 sizes it). logits: those of lce_logprobs, or NULL: recomputed chunk by
  * chunk. Workspace: lce_logprobs_backward_workspace_size.
  *
  * lce_logprobs_keep is lce_logprobs with one more output, stats [N, 2] (fp32,

@@ -278,6 +278,37 @@ def test_kept_statistics_refusals(lib):
             assert rc in (E.LCE_ERR_CUDA, E.LCE_ERR_UNSUPPORTED_DEVICE)
 
 
+def test_a_frozen_head_needs_no_room_for_its_gradient(lib, monkeypatch):
+    """Without dW neither the C calls nor the binding want the fp32 sum of a bf16 dW over the chunks."""
+    E, P, o = lce, FAKE, lce.make_opts(chunk_tokens=32)
+    small, large = [lce.lce_logprobs_backward_workspace_size(64, 64, 1000, g, o) for g in (0, E.LCE_DW_BF16)]
+    kd_small, kd_large = [lce.lce_distill_workspace_size(64, 64, 1000, 5, True, g, o) for g in (0, E.LCE_DW_BF16)]
+    assert large - small >= 4 * 1000 * 64 and kd_large - kd_small >= 4 * 1000 * 64
+
+    def bwd(dW, nbytes):
+        return lib.lce_logprobs_backward(P, P, P, 64, 64, 1000, 1.0, P, P, P, P, P, None, E.LCE_DW_BF16, P, dW,
+                                         ctypes.byref(o), P, nbytes, None)
+
+    def kd(dW, nbytes):
+        return lib.lce_distill_fwd_bwd(P, P, P, P, 64, 64, 1000, 5, 0, 1.0, None, E.LCE_DW_BF16, P, P, P, dW,
+                                       ctypes.byref(o), P, nbytes, None)
+
+    assert bwd(P, small) == kd(P, kd_small) == E.LCE_ERR_WORKSPACE
+    assert bwd(None, small - 1) == kd(None, kd_small - 1) == E.LCE_ERR_WORKSPACE
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():   # these get as far as the device check
+        for rc in (bwd(P, large), kd(P, kd_large), bwd(None, small), kd(None, kd_small)):
+            assert rc in (E.LCE_ERR_CUDA, E.LCE_ERR_UNSUPPORTED_DEVICE)
+    asked = []
+    monkeypatch.setattr(lce, "lce_logprobs_backward_workspace_size", lambda N, d, V, grads, o: asked.append(grads) or 0)
+    H, W, f = torch.zeros(4, 8).bfloat16(), torch.zeros(3, 8).bfloat16(), torch.zeros(4)
+    for need_dW in (True, False):
+        with pytest.raises(lce.LCEError):   # a size of 0 ends the call
+            lce._logprobs_backward(H, W, None, f, f, None, f, f, None, None, 1.0, E.LCE_DW_BF16, None, True, need_dW,
+                                   None, None, {})
+    assert asked == [E.LCE_DW_BF16, 0]
+
+
 # --------------------------------------------------------------------------- the autograd modules, on fakes of the calls
 @pytest.fixture
 def fakes(monkeypatch):
