@@ -1013,8 +1013,9 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_score_grad(const ScoreGradAr
     const int groups = p.d / 8;
     const uint4* hr = p.H + static_cast<long long>(r) * groups;
     uint4* tr = p.Ht + static_cast<long long>(r) * groups;
+    const bool share = u.a != 0.f || u.e != 0.f;  // without one the row is zero here too: 0 x NaN is not 0
     for (int i = tid; i < groups; i += kRowThreads) {
-      const uint4 h = hr[i];
+      const uint4 h = share ? hr[i] : make_uint4(0u, 0u, 0u, 0u);
       const uint32_t w[4] = {h.x, h.y, h.z, h.w};
       uint32_t o[4];
 #pragma unroll

@@ -335,7 +335,8 @@ int lce_scale_grads(void* dH, float* dW, int64_t N, int64_t d, int64_t V, const 
  * computes the row statistics below anew (one more pass over the logits of H and W).
  * G is held in bf16 over a scale per row, its label's entry, by which dH is
  * multiplied in fp32; dW is its product with bf16(scale H). A row whose upstream
- * gradients are zero is zero in G and dH whatever its logits are. Either of dH, dW may be NULL: not wanted, not
+ * gradients are zero is zero in G, dH and its share of dW whatever its row of H
+ * and its logits are. Either of dH, dW may be NULL: not wanted, not
  * computed. grads: 0, or LCE_DW_BF16: dW is bf16 [V, d], the fp32 sum rounded
  * once (not with accumulate_dW; several chunks are summed in fp32 in the
  * workspace, for which a call without dW needs no room: grads = 0 sizes it). logits: those of lce_logprobs, or NULL: recomputed chunk by

@@ -965,6 +965,32 @@ def test_kept_logits_are_freed_by_the_backward(cuda_lib):
     assert N * cuda_lib.lce_logits_stride(V) in seen
 
 
+@pytest.mark.parametrize("keep", [False, True])
+def test_masked_rows_of_nan_leave_dW_alone(cuda_lib, keep):
+    """Rows without upstream gradient have no share of dW either, whatever their hidden states hold."""
+    torch = _torch()
+    rng, H, W, y = make(150, 64, 1000)
+    y[:] = rng.integers(0, 1000, 150)
+    Ht, Wt = heads(H, W)
+    g1, g2 = rng.standard_normal(150).astype(np.float32), rng.standard_normal(150).astype(np.float32)
+    masked = np.zeros(150, bool)
+    masked[[3, 77, 149]] = True
+    y[masked], g2[masked] = oracle.IGNORE_INDEX, 0.0
+    kept = torch.empty(150, 1024, device="cuda") if keep else None
+
+    def run(h, **kw):
+        logp, lse, ent, _, _ = cuda_lib.lce_logprobs(h, Wt, dev(y), logits=kept, chunk_tokens=100)
+        return cuda_lib.lce_logprobs_backward(h, Wt, dev(y), logp, lse, ent, dev(g1), dev(g2), logits=kept,
+                                              chunk_tokens=100, **kw)
+
+    for dtype in (torch.float32, torch.bfloat16):
+        want = run(Ht, dW_dtype=dtype)
+        nan = Ht.clone()
+        nan[3], nan[77], nan[149, 5] = float("nan"), float("inf"), -float("inf")
+        for a, b in zip(run(nan, dW_dtype=dtype), want):
+            assert torch.equal(a, b)
+
+
 # --------------------------------------------------------------------------- the bounds-checking build
 def _child():
     """Every kind of call on the bounds-checking build (a process loads one library): sync_check turns an
