@@ -1030,13 +1030,13 @@ TokLayout tok_layout(int64_t N, int64_t d, int64_t V, bool with_z, bool with_gra
   L.ztgt = take(sizeof(float) * C);
   L.partials = take(sizeof(float4) * C * static_cast<size_t>(2 * L.T));
   if (with_z) T.Z = take(sizeof(float) * C * static_cast<size_t>(T.ldz));
-  if (with_scale) {  // row scales, the labels' entries, row statistics and bf16(scale H)
+  if (with_scale) {  // row scales, the labels' entries and row statistics
     L.alpha = take(sizeof(float) * C);
     T.label = take(sizeof(float) * C);
     T.stats = take(sizeof(float2) * C);
-    L.Ht = take(2 * C * static_cast<size_t>(d));
   }
   if (with_grad) {
+    L.Ht = take(2 * C * static_cast<size_t>(d));  // dW's second operand: bf16(scale H), or H without its masked rows
     L.P = take(2 * C * static_cast<size_t>(L.ldp));
     take_dh_parts(L, d, V, take);
     if (dW_bf16 && L.chunks > 1) T.dW = take(sizeof(float) * static_cast<size_t>(V) * static_cast<size_t>(d));
@@ -1416,6 +1416,10 @@ int distill(const void* H, const void* W, const int64_t* idx, const void* t, int
     a.partials = p.partials;
     a.Z = Z;
     a.G = with_grad ? reinterpret_cast<__nv_bfloat16*>(c.ws + c.L.P) : nullptr;
+    uint16_t* Ht = reinterpret_cast<uint16_t*>(c.ws + c.L.Ht);
+    a.H = reinterpret_cast<const uint4*>(c.H + c0 * d);
+    a.Ht = with_grad && dW ? reinterpret_cast<uint4*>(Ht) : nullptr;
+    a.d = static_cast<int>(d);
     a.row_loss = row_loss + c0;
     a.all_rows = row_loss;
     a.N = N;
@@ -1423,10 +1427,11 @@ int distill(const void* H, const void* W, const int64_t* idx, const void* t, int
     a.grad_loss = grad_loss;
     a.st = c.st;
     const double bytes = static_cast<double>(rows) * (32.0 * static_cast<double>(c.L.T) + 12.0 * K +
-                                                      (with_grad ? 6.0 * static_cast<double>(V) : 32.0 * K));
+                                                      (with_grad ? 6.0 * static_cast<double>(V) : 32.0 * K) +
+                                                      (a.Ht ? 4.0 * static_cast<double>(d) : 0.0));
     LCE_TRY(timed(c.s, K_COMBINE, bytes,
                   [&] { return cuda_rc(lce::launch_distill_row(a, static_cast<int>(rows), c.s)); }));
-    if (with_grad) LCE_TRY(tok_grads(c, T, c0, rows, nullptr, c.H + c0 * d, dH, dW, dW_bf16));
+    if (with_grad) LCE_TRY(tok_grads(c, T, c0, rows, nullptr, Ht, dH, dW, dW_bf16));
   }
   if (N == 0) LCE_TRY(finalize(c, row_loss, loss));
   return finish(c);

@@ -314,6 +314,9 @@ struct DistillArgs {
   const float4* partials;
   const float* Z;        // [rows, ldz]
   __nv_bfloat16* G;      // [rows, ldg] gradient tile, or null (loss only)
+  const uint4* H;        // [rows, d] bf16
+  uint4* Ht;             // [rows, d] H with zeros in the rows that keep no entry, out, or null (no dW)
+  int d;
   float* row_loss;       // [rows]
   const float* grad_loss;
   const float* all_rows;  // [N] row_loss of the whole call; the row finished last sums it into loss

@@ -1158,6 +1158,17 @@ __device__ __forceinline__ void finish_row(const DistillArgs& p, int r, float lo
   }
 }
 
+// dW's second operand: the row of H, or zeros where the row keeps no entry, as its
+// zeros in G times a NaN in H would not be zero (4 bytes an element of H next to 6 an
+// entry of G).
+__device__ __forceinline__ void copy_row(const DistillArgs& p, int r, bool kept) {
+  if (p.Ht == nullptr) return;
+  const int groups = p.d / 8;
+  const long long at = static_cast<long long>(r) * groups;
+  for (int i = threadIdx.x; i < groups; i += kRowThreads)
+    p.Ht[at + i] = kept ? p.H[at + i] : make_uint4(0u, 0u, 0u, 0u);
+}
+
 // One block per row of the chunk. The row's partial sums give lse; the K entries
 // give the teacher's probabilities q and the row's loss
 //   T^2 sum_k q_k (log q_k - z'_k + lse);
@@ -1198,8 +1209,10 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_distill_row(const DistillArg
   const bool kept = __syncthreads_or(vi >= 0) != 0;
   if (!kept) {  // nothing of the teacher in this row: no loss, a zero gradient
     finish_row(p, r, 0.f, false);
-    if (GRAD)
+    if (GRAD) {
+      copy_row(p, r, false);
       for (int c = tid * 8; c < p.V; c += kRowThreads * 8) *reinterpret_cast<uint4*>(g + c) = make_uint4(0, 0, 0, 0);
+    }
     return;
   }
   float q = 0.f, logq = 0.f;
@@ -1243,6 +1256,7 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_distill_row(const DistillArg
   finish_row(p, r, loss / (p.inv_t * p.inv_t), true);
   if (!GRAD) return;
 
+  copy_row(p, r, true);
   const float k = p.inv_t * kLog2e, w = mass / (acc.c + acc.s);
   for (int c = tid * 8; c < p.V; c += kRowThreads * 8) {
     // columns past V (up to 7) lie inside the row's padding: never read by the GEMMs

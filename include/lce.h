@@ -336,8 +336,7 @@ int lce_scale_grads(void* dH, float* dW, int64_t N, int64_t d, int64_t V, const 
  * G is held in bf16 over a scale per row, its label's entry, by which dH is
  * multiplied in fp32; dW is its product with bf16(scale H). A row whose upstream
  * gradients are zero is zero in G, dH and its share of dW whatever its row of H
- * and its logits are. Either of dH, dW may be NULL: not wanted, not
- * computed. grads: 0, or LCE_DW_BF16: dW is bf16 [V, d], the fp32 sum rounded
+ * and its logits are. Either of dH, dW may be NULL: not wanted, not computed. grads: 0, or LCE_DW_BF16: dW is bf16 [V, d], the fp32 sum rounded
  * once (not with accumulate_dW; several chunks are summed in fp32 in the
  * workspace, for which a call without dW needs no room: grads = 0 sizes it). logits: those of lce_logprobs, or NULL: recomputed chunk by
  * chunk. Workspace: lce_logprobs_backward_workspace_size.
@@ -385,9 +384,10 @@ int lce_logprobs_keep_backward(const void* H, const void* W, const int64_t* y, i
  *          with a kept entry, or opts->n_valid_override
  *   G_iv = (grad_loss temperature / n) (p_iv sum_k q_ik - sum_k q_ik [v = idx_ik])
  *   dH = G W (bf16), dW = G^T H (fp32; opts->accumulate_dW; or bf16: grads as above)
- * Rows without a kept entry have row_loss 0 and a zero gradient; a NaN or +inf
- * value, or a row of NaN logits, makes its row's loss and gradient NaN. The tile of G
- * without its leading factor is rounded to bf16 once. 1 <= K <= LCE_MAX_TOP.
+ * Rows without a kept entry have row_loss 0, a zero gradient and no share of dW,
+ * whatever their rows of H hold; a NaN or +inf value, or a row of NaN logits, makes
+ * its row's loss and gradient NaN. The tile of G without its leading factor is
+ * rounded to bf16 once. 1 <= K <= LCE_MAX_TOP.
  * loss [1], row_loss [N] fp32; grad_loss: device fp32 [1] or NULL (1.0); either
  * of dH, dW may be NULL: not wanted, not computed. Workspace:
  * lce_distill_workspace_size (with_grad: 0 for the forward, 1 for both).

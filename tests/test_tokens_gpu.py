@@ -991,6 +991,23 @@ def test_masked_rows_of_nan_leave_dW_alone(cuda_lib, keep):
             assert torch.equal(a, b)
 
 
+def test_distill_rows_without_a_teacher_may_hold_nan(cuda_lib):
+    """Rows that keep no entry have no share of the loss, dH or dW, whatever their hidden states hold."""
+    torch = _torch()
+    rng, H, W, _ = make(150, 72, 500)
+    idx, t = teacher(rng, 150, 500, 6)
+    Ht, Wt = heads(H, W)
+    idx[3], t[77] = oracle.IGNORE_INDEX, -np.inf
+    idx[149] = oracle.IGNORE_INDEX
+    it, tt = dev(idx), dev(t)
+    nan = Ht.clone()
+    nan[3], nan[77], nan[149, 5] = float("nan"), float("inf"), -float("inf")
+    for kw in (dict(), dict(chunk_tokens=100), dict(dW_dtype=torch.bfloat16, chunk_tokens=64), dict(need_dH=False)):
+        want = cuda_lib.lce_distill_fwd_bwd(Ht, Wt, it, tt, **kw)
+        for a, b in zip(cuda_lib.lce_distill_fwd_bwd(nan, Wt, it, tt, **kw), want):
+            assert a is b is None or torch.equal(a, b)
+
+
 # --------------------------------------------------------------------------- the bounds-checking build
 def _child():
     """Every kind of call on the bounds-checking build (a process loads one library): sync_check turns an
