@@ -127,8 +127,17 @@ class FusedLinearLogProbs(torch.nn.Module):
     all); False: the forward keeps them for it (4 N V bytes, 6 N V d flops);
     None: they are kept when the batch is one chunk (chunk_tokens, or fewer than
     6144 tokens), so that the memory held stays O(chunk V), and d is at least
-    1024: below, reading them costs more than the product (4096 tokens of V =
-    151936: d = 768 2.41 ms recomputed and 2.58 kept, d = 1536 4.47 and 4.07)."""
+    1536: below, reading them costs more than the product, or as much. Forward and
+    backward at V = 151936, microseconds recomputed and kept:
+
+        rows        512           1024          2048          4096
+        d =  768    398 /  471    659 /  726    1235 / 1344   2492 /  2601
+        d = 1024    482 /  536    799 /  847    1570 / 1592   3081 /  3070
+        d = 1536    724 /  741   1150 / 1095    2205 / 2047   4475 /  4205
+        d = 2048    952 /  918   1515 / 1379    2944 / 2602   6011 /  5336
+        d = 4096   1779 / 1531   3129 / 2598    6101 / 4962  12359 / 10055
+
+    (128 rows: kept is ahead from d = 1024 on, 338 / 318, with 78 MB of logits.)"""
 
     def __init__(self, temperature: float = 1.0, ignore_index: int = -100, chunk_tokens=0, recompute=None):
         super().__init__()
@@ -143,7 +152,7 @@ class FusedLinearLogProbs(torch.nn.Module):
         keep = not self.recompute
         if self.recompute is None:
             chunk = self.opts["chunk_tokens"]
-            keep = chunk != "auto" and H.shape[0] <= (chunk or 6143) and H.shape[1] >= 1024
+            keep = chunk != "auto" and H.shape[0] <= (chunk or 6143) and H.shape[1] >= 1536
         return _LogProbs.apply(H, W, y, self.temperature, keep, self.opts)
 
 

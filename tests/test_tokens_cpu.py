@@ -381,3 +381,17 @@ def test_what_the_forward_keeps_is_freed_by_the_backward(fakes):
     assert kept[0]() is not None
     torch.autograd.grad(logp.sum(), [H, W])
     assert kept[0]() is None
+
+
+@pytest.mark.parametrize("N,d,chunk,kept", [(64, 1024, 0, False), (64, 1536, 0, True), (6143, 1536, 0, True),
+                                            (6144, 1536, 0, False), (65, 2048, 64, False), (64, 2048, 64, True),
+                                            (64, 2048, "auto", False)])
+def test_which_logits_are_kept(fakes, N, d, chunk, kept):
+    """recompute=None: those of a batch of one chunk, from d = 1536 on."""
+    import torch
+
+    from chunked_lm_head_linear_gb300.autograd import FusedLinearLogProbs
+    seen, _, _, _, _, _ = fakes
+    H, W = torch.zeros(N, d, dtype=torch.bfloat16, requires_grad=True), torch.zeros(9, d, dtype=torch.bfloat16)
+    FusedLinearLogProbs(chunk_tokens=chunk)(H, W, torch.zeros(N, dtype=torch.int64))
+    assert seen == [("logprobs", kept)]

@@ -1008,6 +1008,40 @@ def test_distill_rows_without_a_teacher_may_hold_nan(cuda_lib):
             assert a is b is None or torch.equal(a, b)
 
 
+def test_kept_logits_captured_and_replayed(cuda_lib):
+    """The module's step with kept logits and statistics, captured once and replayed on other hidden states."""
+    torch = _torch()
+    from chunked_lm_head_linear_gb300.autograd import FusedLinearLogProbs
+    rng, H, W, y = make(100, 64, 700)
+    Ht, Wt = heads(H, W)
+    yt, g = dev(y), dev(rng.standard_normal(100).astype(np.float32))
+    x, w = Ht.clone().requires_grad_(True), Wt.clone().requires_grad_(True)
+
+    def step():
+        out = FusedLinearLogProbs(recompute=False, temperature=0.01)(x, w, yt)
+        return [*out, *torch.autograd.grad(out, [x, w], [g, g])]
+
+    want = []
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for h in (Ht, -Ht):
+            with torch.no_grad():
+                x.copy_(h)
+            want.append([o.detach().clone() for o in step()])
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for k in (0, 1, 0):
+        with torch.no_grad():
+            x.copy_(Ht if k == 0 else -Ht)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want[k]):
+            assert torch.equal(a, b)
+
+
 # --------------------------------------------------------------------------- the bounds-checking build
 def _child():
     """Every kind of call on the bounds-checking build (a process loads one library): sync_check turns an
