@@ -185,7 +185,9 @@ class FusedLinearDistillation(torch.nn.Module):
     idx [N, K] with values t [N, K], times temperature^2, mean over the rows that
     keep an entry (lce.lce_distill_fwd_bwd). Its gradients are computed in the
     forward pass in bf16 and scaled by the upstream gradient in the backward,
-    where they are rounded once more unless it is a power of two."""
+    where they are rounded once more unless it is a power of two (a weight given
+    to lce.lce_distill_fwd_bwd as grad_loss is in their one rounding). The
+    teacher's values get no gradient."""
 
     def __init__(self, temperature: float = 1.0, renormalize: bool = True, ignore_index: int = -100,
                  reduction: str = "mean", chunk_tokens=0):

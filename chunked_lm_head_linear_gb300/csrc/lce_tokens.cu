@@ -444,7 +444,7 @@ cudaError_t launch_tok_mode(const CUtensorMap& a, const CUtensorMap& b, const CU
 // would multiply 256 rows whatever their number and leave fewer bytes in
 // flight: 7 rows of d = 7168 and V = 151655 took 517 us with it, 327 us here,
 // 6.6 TB/s; from 97 rows on it is level or ahead (128 rows of d = 2048: 131 us
-// against 133).
+// against 133 when they were compared, 111 now).
 // MT = 2 (NT = 32) halves the reads of H from L2 per byte of W: one row of d =
 // 4096 and V = 151936 187 us against 204. With more rows the last tile's longer
 // epilogue costs more than that gives (64 rows of d = 2048: 114 us against 112).

@@ -318,10 +318,10 @@ int lce_scale_grads(void* dH, float* dW, int64_t N, int64_t d, int64_t V, const 
  *   logits [N, lce_logits_stride(V)]  (fp32, 16-byte aligned; NULL: not kept)
  *                z itself, for lce_logprobs_backward; what lies past column V of
  *                a row is not defined
- * A row with a NaN logit has NaN statistics, one with an infinite logit no
- * meaningful ones; its alternatives are some tokens of the vocabulary. Up to 96 rows of a chunk take a kernel of
- * their own, whose logits may differ from those of larger chunks in the order
- * of their fp32 sums. Workspace: lce_logprobs_workspace_size (with logits, that
+ * A row with a NaN logit has NaN statistics, one with an infinite logit (of a
+ * magnitude of 1e30 or more) no meaningful ones; its alternatives are some tokens
+ * of the vocabulary. Up to 96 rows of a chunk take a kernel of their own, whose
+ * logits may differ from those of larger chunks in the order of their fp32 sums. Workspace: lce_logprobs_workspace_size (with logits, that
  * of top_k = 0 is enough).
  *
  * lce_logprobs_backward: gradients from upstream g_logp [N] and g_entropy [N]
