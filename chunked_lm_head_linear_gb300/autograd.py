@@ -26,6 +26,9 @@ entropies of given tokens, whose upstream gradients are known only in the
 backward, save logp, entropy and the rows' statistics, and the logits of a
 batch of one chunk (else they are recomputed there); the distillation loss
 computes its gradients in the forward and scales them in the backward.
+FusedLinearPolicyLoss and FusedLinearPreferenceLoss wrap lce_policy_fwd_bwd and
+lce_preference_fwd_bwd as the distillation loss is wrapped. FusedLayerNorm is
+the norm in front of any of them (lce_layernorm_forward / _backward).
 Gradients nobody needs (a frozen W, torch.no_grad) are not computed, and nothing
 is kept for them.
 """
@@ -156,6 +159,17 @@ class FusedLinearLogProbs(torch.nn.Module):
         return _LogProbs.apply(H, W, y, self.temperature, keep, self.opts)
 
 
+def _scaled(ctx, g, what):
+    """The gradients that the forward computed, times the upstream one; handed out once, as they are scaled in place."""
+    if ctx.grads is None:
+        raise RuntimeError(f"{what}: the gradients were handed out by an earlier backward pass of this graph; run the "
+                           "forward again")
+    dH, dW = ctx.grads
+    ctx.grads = None
+    lce.lce_scale_grads_bfloat(dH, dW, g)
+    return dH, dW
+
+
 class _Distillation(torch.autograd.Function):
     @staticmethod
     def forward(ctx, H, W, idx, t, kw):
@@ -169,13 +183,7 @@ class _Distillation(torch.autograd.Function):
         return loss.reshape(())
 
     def _gradients(ctx, g):
-        if ctx.grads is None:
-            raise RuntimeError("FusedLinearDistillation: the gradients were handed out by an earlier backward pass "
-                               "of this graph; run the forward again")
-        dH, dW = ctx.grads
-        ctx.grads = None
-        lce.lce_scale_grads_bfloat(dH, dW, g)
-        return dH, dW, None, None, None
+        return *_scaled(ctx, g, "FusedLinearDistillation"), None, None, None
 
     backward = _first_order(_gradients)
 
@@ -199,3 +207,119 @@ class FusedLinearDistillation(torch.nn.Module):
         if not torch.is_grad_enabled():
             return lce.lce_distill_forward(H, W, idx, t, **self.kw)[0].reshape(())
         return _Distillation.apply(H, W, idx, t, self.kw)
+
+
+class _PolicyLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, H, W, y, advantages, old_logp, ref_logp, weights, kw):
+        need_dH, need_dW = ctx.needs_input_grad[:2]
+        if need_dH or need_dW:
+            loss, logp, _, dH, dW = lce.lce_policy_fwd_bwd(H, W, y, advantages, old_logp, ref_logp, weights=weights,
+                                                           dW_dtype=W.dtype, need_dH=need_dH, need_dW=need_dW, **kw)
+            ctx.grads = dH, dW
+        else:
+            loss, logp, _ = lce.lce_policy_forward(H, W, y, advantages, old_logp, ref_logp, weights=weights, **kw)
+        ctx.mark_non_differentiable(logp)
+        return loss.reshape(()), logp
+
+    def _gradients(ctx, g, _):
+        return *_scaled(ctx, g, "FusedLinearPolicyLoss"), None, None, None, None, None, None
+
+    backward = _first_order(_gradients)
+
+
+class FusedLinearPolicyLoss(torch.nn.Module):
+    """The clipped policy loss with a KL term (lce.lce_policy_fwd_bwd) of the tokens
+    y [N] under softmax(H W^T / temperature), and their log-probabilities logp
+    [N] (without a gradient: for ratios and KL divergences to look at). The
+    gradients are computed in the forward pass in bf16 and scaled by the
+    upstream gradient in the backward, where they are rounded once more unless
+    it is a power of two. advantages, old_logp, ref_logp and weights (fp32 [N])
+    get no gradient."""
+
+    def __init__(self, temperature: float = 1.0, clip_low: float = 0.2, clip_high: float = 0.2, dual_clip: float = 0.0,
+                 kl: str = "none", kl_coef: float = 0.0, ignore_index: int = -100, reduction: str = "mean",
+                 chunk_tokens=0):
+        super().__init__()
+        self.kw = dict(temperature=temperature, clip_low=clip_low, clip_high=clip_high, dual_clip=dual_clip, kl=kl,
+                       kl_coef=kl_coef, ignore_index=ignore_index, reduction=reduction, chunk_tokens=chunk_tokens)
+
+    def forward(self, H, W, y, advantages, old_logp=None, ref_logp=None, weights=None):
+        if not torch.is_grad_enabled():
+            loss, logp, _ = lce.lce_policy_forward(H, W, y, advantages, old_logp, ref_logp, weights=weights, **self.kw)
+            return loss.reshape(()), logp
+        return _PolicyLoss.apply(H, W, y, advantages, old_logp, ref_logp, weights, self.kw)
+
+
+class _PreferenceLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, H, W, y, cu_seqlens, ref_logp, kw):
+        need_dH, need_dW = ctx.needs_input_grad[:2]
+        if need_dH or need_dW:
+            loss, _, seq_logp, dH, dW = lce.lce_preference_fwd_bwd(H, W, y, cu_seqlens, ref_logp, dW_dtype=W.dtype,
+                                                                   need_dH=need_dH, need_dW=need_dW, **kw)
+            ctx.grads = dH, dW
+        else:
+            loss, _, seq_logp = lce.lce_preference_forward(H, W, y, cu_seqlens, ref_logp, **kw)
+        ctx.mark_non_differentiable(seq_logp)
+        return loss.reshape(()), seq_logp
+
+    def _gradients(ctx, g, _):
+        return *_scaled(ctx, g, "FusedLinearPreferenceLoss"), None, None, None, None
+
+    backward = _first_order(_gradients)
+
+
+class FusedLinearPreferenceLoss(torch.nn.Module):
+    """The loss of paired sequences' log ratios (lce.lce_preference_fwd_bwd), and the
+    sequences' log-probabilities seq_logp [2 P] (without a gradient: times beta,
+    less the reference's, they are the rewards). cu_seqlens [2 P + 1] bounds
+    chosen and rejected sequences in turn. The gradients are computed in the
+    forward pass, as FusedLinearPolicyLoss's."""
+
+    def __init__(self, kind: str = "sigmoid", beta: float = 0.1, label_smoothing: float = 0.0, margin: float = 0.0,
+                 average: bool = False, temperature: float = 1.0, ignore_index: int = -100, reduction: str = "mean",
+                 chunk_tokens=0):
+        super().__init__()
+        self.kw = dict(kind=kind, beta=beta, label_smoothing=label_smoothing, margin=margin, average=average,
+                       temperature=temperature, ignore_index=ignore_index, reduction=reduction,
+                       chunk_tokens=chunk_tokens)
+
+    def forward(self, H, W, y, cu_seqlens, ref_logp=None):
+        if not torch.is_grad_enabled():
+            loss, _, seq_logp = lce.lce_preference_forward(H, W, y, cu_seqlens, ref_logp, **self.kw)
+            return loss.reshape(()), seq_logp
+        return _PreferenceLoss.apply(H, W, y, cu_seqlens, ref_logp, self.kw)
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, b, eps):
+        H, mean, rstd = lce.lce_layernorm_forward(x, w, b, eps)
+        ctx.save_for_backward(x, w, mean, rstd)
+        ctx.bias = None if b is None else b.dtype
+        return H
+
+    def _gradients(ctx, dH):
+        x, w, mean, rstd = ctx.saved_tensors
+        need_dx, need_dw, need_db = ctx.needs_input_grad[:3]
+        dx, dw, db = lce.lce_layernorm_backward(x, w, mean, rstd, dH.contiguous(), bias=need_db, need_dx=need_dx,
+                                                need_dw=need_dw)
+        return dx, None if dw is None else dw.to(w.dtype), None if db is None else db.to(ctx.bias), None
+
+    backward = _first_order(_gradients)
+
+
+class FusedLayerNorm(torch.nn.Module):
+    """Layer norm in front of the head: H (bf16 [N, d]) of x (bf16 or fp32 [N, d]) with
+    weight w and bias b (fp32 or bf16 [d], or None), differentiable in all three
+    (lce.lce_layernorm_forward / lce_layernorm_backward)."""
+
+    def __init__(self, eps: float = 1e-5):
+        super().__init__()
+        self.eps = eps
+
+    def forward(self, x, w=None, b=None):
+        if not torch.is_grad_enabled():
+            return lce.lce_layernorm_forward(x, w, b, self.eps)[0]
+        return _LayerNorm.apply(x, w, b, self.eps)

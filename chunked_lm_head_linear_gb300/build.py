@@ -25,7 +25,7 @@ CHECKED_LIB = os.path.join(CHECKED_BUILD, "liblce.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr"]
 INCLUDE = ["-I" + os.path.join(ROOT, "include")]
-SOURCES = ["lce_kernels.cu", "lce_api.cu", "lce_noalloc.cu", "lce_rmsnorm.cu", "lce_tokens.cu"]
+SOURCES = ["lce_kernels.cu", "lce_api.cu", "lce_noalloc.cu", "lce_rmsnorm.cu", "lce_tokens.cu", "lce_losses.cu", "lce_layernorm.cu"]
 
 
 def nvcc() -> str:

@@ -28,6 +28,8 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cfloat>
+#include <cmath>
 #include <cstring>
 #include <functional>
 #include <mutex>
@@ -248,12 +250,12 @@ enum Kind : int {
   K_COMBINE = 2,
   K_LOGITS_GRAD = 3,    // unconditional FWD_GRAD (lce_backward)
   K_GEMM_BWD = 4,       // dH and dW GEMMs of a chunk (one launch)
-  K_RMSNORM_FWD = 5,
+  K_RMSNORM_FWD = 5,    // and the layer norm's forward
   K_FINALIZE = 6,
   K_OTHER = 7,          // the guard-conditional passes (work counted as 0), gradient scaling
   K_LOGITS_REF = 8,
   K_MEMSET = 9,         // zeroing dW when there are no tokens (a copy-engine memset, not a kernel)
-  K_RMSNORM_BWD = 10,   // norm backward and the column sum of its dw partials
+  K_RMSNORM_BWD = 10,   // norm backward (RMS or layer norm) and the column sum of its dw partials
 };
 const char* const kKindNames[LCE_KERNEL_KINDS] = {"prepare",    "logits_stats", "combine",  "logits_grad",
                                                   "gemm_dH_dW", "rmsnorm_fwd",  "finalize", "other",
@@ -1464,6 +1466,398 @@ int lce_distill_fwd_bwd(const void* H, const void* W, const int64_t* idx, const 
   return distill(H, W, idx, t, N, d, V, K, teacher, temperature, grad_loss, grads, loss, row_loss, dH, dW, true, opts,
                  ws, ws_bytes, stream);
 }
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Losses on log-probabilities
+// ---------------------------------------------------------------------------
+namespace {
+
+// Workspace of a policy or preference call: the token operators' for its chunks, and what the preference
+// loss keeps between its two passes over the rows.
+struct LossLayout {
+  TokLayout tok;
+  size_t logp = 0, stats = 0, a = 0, coef = 0;  // [N], [N] pairs, [C], [2 P]
+  size_t total = 0;
+};
+
+// pairs < 0: the policy loss.
+LossLayout loss_layout(int64_t N, int64_t d, int64_t V, int64_t pairs, bool with_grad, bool dW_bf16, const lce_opts* o) {
+  LossLayout L;
+  const bool one = N <= tok_chunk(N, o);
+  L.tok = tok_layout(N, d, V, with_grad && (pairs < 0 || one), with_grad, dW_bf16, with_grad, o);
+  size_t off = L.tok.total;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align256(bytes);
+    return at;
+  };
+  if (pairs >= 0) {
+    const size_t rows = static_cast<size_t>(N > 0 ? N : 1);
+    L.logp = take(sizeof(float) * rows);
+    L.stats = take(sizeof(float2) * rows);
+    L.a = take(sizeof(float) * static_cast<size_t>(L.tok.base.C));
+    L.coef = take(sizeof(float) * 2 * static_cast<size_t>(pairs > 0 ? pairs : 1));
+  }
+  L.total = off;
+  return L;
+}
+
+constexpr int64_t kMaxPairs = (int64_t{1} << 30) - 1;
+
+// The parts of a row kernel's arguments that both losses fill alike.
+lce::LossRowArgs loss_row(const Call& c, const TokLayout& T, int64_t c0, const lce::TokParams& p, const float* Z,
+                          bool with_grad, bool with_dW) {
+  lce::LossRowArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.V = p.V;
+  a.d = static_cast<int>(c.d);
+  a.nparts = p.nparts;
+  a.ldz = T.ldz;
+  a.ldg = c.L.ldp;
+  a.inv_t = p.inv_t;
+  a.ignore_index = p.ignore_index;
+  a.y = p.y;
+  a.partials = p.partials;
+  a.ztgt = p.ztgt;
+  a.Z = Z;
+  a.st = c.st;
+  if (!with_grad) return a;
+  a.G = reinterpret_cast<__nv_bfloat16*>(c.ws + c.L.P);
+  a.H = reinterpret_cast<const uint4*>(c.H + c0 * c.d);
+  a.Ht = with_dW ? reinterpret_cast<uint4*>(c.ws + c.L.Ht) : nullptr;
+  a.rowscale = reinterpret_cast<float*>(c.ws + c.L.alpha);
+  a.label = reinterpret_cast<float*>(c.ws + T.label);
+  return a;
+}
+
+double loss_row_bytes(const Call& c, int64_t rows, bool with_grad) {
+  return static_cast<double>(rows) * (32.0 * static_cast<double>(c.L.T) + 40.0 +
+                                      (with_grad ? 6.0 * static_cast<double>(c.V) + 4.0 * static_cast<double>(c.d) : 0.0));
+}
+
+int policy_loss(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V, float temperature,
+                const lce_policy* policy, const float* advantages, const float* old_logp, const float* ref_logp,
+                const float* weights, const float* grad_loss, int32_t grads, float* loss, float* logp, float* row_loss,
+                void* dH, void* dW, bool with_grad, const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
+  lce_opts o;
+  lce_opts_init(&o);
+  if (opts) o = *opts;
+  LCE_TRY(check_sizes(N, d, V, &o));
+  LCE_TRY(check_token_args(V, temperature));
+  const bool dW_bf16 = (grads & LCE_DW_BF16) != 0;
+  if (o.reserved != 0 || (grads & ~LCE_DW_BF16) != 0 || (dW_bf16 && o.accumulate_dW)) return LCE_ERR_INVALID_ARG;
+  if (!policy || !(policy->clip_low >= 0.f) || !(policy->clip_high >= 0.f) ||
+      !(policy->dual_clip == 0.f || policy->dual_clip >= 1.f) || !(std::fabs(policy->kl_coef) <= FLT_MAX) ||
+      policy->kl < LCE_KL_NONE || policy->kl > LCE_KL_K3 || policy->reserved != 0 ||
+      (policy->kl != LCE_KL_NONE && N > 0 && !ref_logp))
+    return LCE_ERR_INVALID_ARG;
+  if (!W || !ws || !loss || (with_grad && !dH && !dW) ||
+      (N > 0 && (!H || !y || !advantages || !logp || !row_loss)))
+    return LCE_ERR_INVALID_ARG;
+  if (!aligned(W, 16) || !aligned(H, 16) || !aligned(y, 8) || !aligned(ws, 256) || !aligned(loss, 4) ||
+      !aligned(logp, 4) || !aligned(row_loss, 4) || !aligned(advantages, 4) || !aligned(old_logp, 4) ||
+      !aligned(ref_logp, 4) || !aligned(weights, 4) || !aligned(grad_loss, 4) || !aligned(dH, 16) || !aligned(dW, 16))
+    return LCE_ERR_ALIGNMENT;
+  const LossLayout L = loss_layout(N, d, V, -1, with_grad, dW_bf16 && dW, &o);
+  if (ws_bytes < L.total) return LCE_ERR_WORKSPACE;
+  const TokLayout& T = L.tok;
+  Call c;
+  LCE_TRY(tok_begin(&c, T, H, W, y, N, d, V, o, ws, ws_bytes, stream));
+  // With one chunk its rows count themselves, before the GEMMs that need n; with several n is needed by
+  // the first chunk's.
+  const bool count_here = !lce::kChecks && c.L.chunks == 1;
+  if (!count_here) LCE_TRY(prepare(c, grad_loss));
+  if (N == 0 && with_grad) LCE_TRY(zero_dW(c, dW, dW_bf16));
+  for (int64_t c0 = 0; c0 < N; c0 += c.L.C) {
+    const int64_t rows = (N - c0) < c.L.C ? (N - c0) : c.L.C;
+    lce::TokParams p = tok_params(c, c0, rows, temperature);
+    if (count_here) {
+      p.clear_st = c.st;
+      p.cnt = with_grad ? reinterpret_cast<int*>(c.ws + c.L.dh_cnt) : nullptr;
+      p.ncnt = with_grad ? c.L.dh_ncnt : 0;
+    }
+    float* Z = with_grad ? reinterpret_cast<float*>(c.ws + T.Z) : nullptr;
+    LCE_TRY(tok_logits(c, c0, rows, Z ? lce::TOK_STATS_Z : lce::TOK_STATS, Z, T.ldz, p));
+    lce::PolicyArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.row = loss_row(c, T, c0, p, Z, with_grad, dW != nullptr);
+    a.row.logp = logp + c0;
+    a.advantages = advantages + c0;
+    a.old_logp = old_logp ? old_logp + c0 : nullptr;
+    a.ref_logp = policy->kl != LCE_KL_NONE ? ref_logp + c0 : nullptr;
+    a.weights = weights ? weights + c0 : nullptr;
+    a.row_loss = row_loss + c0;
+    a.clip_low = policy->clip_low;
+    a.clip_high = policy->clip_high;
+    a.dual_clip = policy->dual_clip;
+    a.kl_coef = policy->kl_coef;
+    a.kl = policy->kl;
+    a.loss = count_here ? loss : nullptr;
+    a.grad_loss = grad_loss;
+    a.mean = o.reduction == LCE_MEAN ? 1 : 0;
+    a.n_override = o.n_valid_override;
+    a.N = N;
+    LCE_TRY(timed(c.s, K_COMBINE, loss_row_bytes(c, rows, with_grad),
+                  [&] { return cuda_rc(lce::launch_policy_row(a, static_cast<int>(rows), c.s)); }));
+    if (with_grad)
+      LCE_TRY(tok_grads(c, T, c0, rows, a.row.rowscale, reinterpret_cast<uint16_t*>(c.ws + c.L.Ht), dH, dW, dW_bf16));
+  }
+  if (!count_here) LCE_TRY(finalize(c, row_loss, loss));
+  return finish(c);
+}
+
+int preference_loss(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V, const void* cu,
+                    int64_t pairs, float temperature, const lce_preference* pref, const float* ref_logp,
+                    const float* grad_loss, int32_t grads, float* loss, float* pair_loss, float* seq_logp, void* dH,
+                    void* dW, bool with_grad, const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
+  lce_opts o;
+  lce_opts_init(&o);
+  if (opts) o = *opts;
+  LCE_TRY(check_sizes(N, d, V, &o));
+  LCE_TRY(check_token_args(V, temperature));
+  const bool dW_bf16 = (grads & LCE_DW_BF16) != 0;
+  if (o.reserved != 0 || (grads & ~LCE_DW_BF16) != 0 || (dW_bf16 && o.accumulate_dW) || pairs < 0 || pairs > kMaxPairs)
+    return LCE_ERR_INVALID_ARG;
+  if (!pref || !(pref->beta > 0.f && pref->beta <= FLT_MAX) || !(pref->label_smoothing >= 0.f && pref->label_smoothing < 0.5f) ||
+      !(std::fabs(pref->margin) <= FLT_MAX) || pref->kind < LCE_PREFERENCE_SIGMOID || pref->kind > LCE_PREFERENCE_IPO ||
+      (pref->flags & ~(LCE_PREFERENCE_AVERAGE | LCE_PREFERENCE_CU_INT32)) != 0 || pref->reserved != 0 ||
+      (pref->kind != LCE_PREFERENCE_SIGMOID && pref->label_smoothing != 0.f) ||
+      (pref->kind == LCE_PREFERENCE_IPO && pref->margin != 0.f))
+    return LCE_ERR_INVALID_ARG;
+  if (!W || !ws || !loss || (with_grad && !dH && !dW) || (N > 0 && (!H || !y)) ||
+      (pairs > 0 && (!cu || !pair_loss || !seq_logp)))
+    return LCE_ERR_INVALID_ARG;
+  const int cu32 = (pref->flags & LCE_PREFERENCE_CU_INT32) ? 1 : 0;
+  if (!aligned(W, 16) || !aligned(H, 16) || !aligned(y, 8) || !aligned(ws, 256) || !aligned(cu, cu32 ? 4 : 8) ||
+      !aligned(ref_logp, 4) || !aligned(grad_loss, 4) || !aligned(loss, 4) || !aligned(pair_loss, 4) ||
+      !aligned(seq_logp, 4) || !aligned(dH, 16) || !aligned(dW, 16))
+    return LCE_ERR_ALIGNMENT;
+  const LossLayout L = loss_layout(N, d, V, pairs, with_grad, dW_bf16 && dW, &o);
+  if (ws_bytes < L.total) return LCE_ERR_WORKSPACE;
+  const TokLayout& T = L.tok;
+  Call c;
+  LCE_TRY(tok_begin(&c, T, H, W, y, N, d, V, o, ws, ws_bytes, stream));
+  float* logp = reinterpret_cast<float*>(c.ws + L.logp);
+  float2* stats = reinterpret_cast<float2*>(c.ws + L.stats);
+  float* coef = reinterpret_cast<float*>(c.ws + L.coef);
+  const bool one = N > 0 && c.L.chunks == 1;
+  float* Z = with_grad && one ? reinterpret_cast<float*>(c.ws + T.Z) : nullptr;
+  if (lce::kChecks || N == 0) LCE_TRY(prepare(c, grad_loss));
+  if (N == 0 && with_grad) LCE_TRY(zero_dW(c, dW, dW_bf16));
+  // every row's log-probability
+  for (int64_t c0 = 0; c0 < N; c0 += c.L.C) {
+    const int64_t rows = (N - c0) < c.L.C ? (N - c0) : c.L.C;
+    lce::TokParams p = tok_params(c, c0, rows, temperature);
+    if (!lce::kChecks && c0 == 0) {
+      p.clear_st = c.st;
+      p.cnt = with_grad ? reinterpret_cast<int*>(c.ws + c.L.dh_cnt) : nullptr;
+      p.ncnt = with_grad ? c.L.dh_ncnt : 0;
+    }
+    LCE_TRY(tok_logits(c, c0, rows, Z ? lce::TOK_STATS_Z : lce::TOK_STATS, Z, T.ldz, p));
+    lce::TokScoreArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.rows = p.rows;
+    a.V = p.V;
+    a.nparts = p.nparts;
+    a.ldz = T.ldz;
+    a.inv_t = p.inv_t;
+    a.ignore_index = p.ignore_index;
+    a.y = p.y;
+    a.partials = p.partials;
+    a.ztgt = p.ztgt;
+    a.Z = Z;
+    a.logp = logp + c0;
+    a.stats = stats + c0;
+    a.flags = p.flags;
+    LCE_TRY(timed(c.s, K_COMBINE, loss_row_bytes(c, rows, false), [&] { return cuda_rc(lce::launch_score(a, c.s)); }));
+  }
+  lce::PairArgs q;
+  std::memset(&q, 0, sizeof q);
+  q.cu = cu;
+  q.cu32 = cu32;
+  q.P = pairs;
+  q.N = N;
+  q.V = static_cast<int>(V);
+  q.ignore_index = o.ignore_index;
+  q.y = y;
+  q.logp = logp;
+  q.ref = ref_logp;
+  q.beta = pref->beta;
+  q.margin = pref->margin;
+  q.smoothing = pref->label_smoothing;
+  q.kind = pref->kind;
+  q.average = (pref->flags & LCE_PREFERENCE_AVERAGE) ? 1 : 0;
+  q.pair_loss = pair_loss;
+  q.seq_logp = seq_logp;
+  q.coef = coef;
+  q.loss = loss;
+  q.grad_loss = grad_loss;
+  const int64_t n = o.n_valid_override >= 0 ? o.n_valid_override : pairs;
+  q.weight = o.reduction == LCE_SUM ? 1.0 : n > 0 ? 1.0 / static_cast<double>(n) : 0.0;
+  q.st = c.st;
+  LCE_TRY(timed(c.s, K_COMBINE, 12.0 * static_cast<double>(N) + 28.0 * static_cast<double>(pairs),
+                [&] { return cuda_rc(lce::launch_pairs(q, c.s)); }));
+  for (int64_t c0 = 0; with_grad && c0 < N; c0 += c.L.C) {
+    const int64_t rows = (N - c0) < c.L.C ? (N - c0) : c.L.C;
+    lce::TokParams p = tok_params(c, c0, rows, temperature);
+    lce::PreferenceArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.row = loss_row(c, T, c0, p, Z, true, dW != nullptr);
+    a.row.logp = logp + c0;
+    a.row.stats = stats + c0;
+    a.row.a = reinterpret_cast<float*>(c.ws + L.a);
+    a.c0 = c0;
+    a.cu = cu;
+    a.cu32 = cu32;
+    a.P = pairs;
+    a.coef = coef;
+    LCE_TRY(timed(c.s, K_COMBINE, loss_row_bytes(c, rows, Z != nullptr),
+                  [&] { return cuda_rc(lce::launch_preference_row(a, static_cast<int>(rows), c.s)); }));
+    if (!Z) {
+      p.stats = stats + c0;
+      p.g_logp = a.row.a;
+      p.rowscale = a.row.rowscale;
+      p.label = a.row.label;
+      LCE_TRY(tok_logits(c, c0, rows, lce::TOK_GRAD, c.ws + c.L.P, c.L.ldp, p));
+    }
+    LCE_TRY(tok_grads(c, T, c0, rows, a.row.rowscale, reinterpret_cast<uint16_t*>(c.ws + c.L.Ht), dH, dW, dW_bf16));
+  }
+  return finish(c);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lce_policy_workspace_size(int64_t N, int64_t d, int64_t V, int32_t with_grad, int32_t grads,
+                                 const lce_opts* opts) {
+  lce_opts o;
+  lce_opts_init(&o);
+  if (opts) o = *opts;
+  if (check_sizes(N, d, V, &o) != LCE_OK || (grads & ~LCE_DW_BF16) != 0) return 0;
+  return loss_layout(N, d, V, -1, with_grad != 0, (grads & LCE_DW_BF16) != 0, &o).total;
+}
+
+int lce_policy_forward(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
+                       float temperature, const lce_policy* policy, const float* advantages, const float* old_logp,
+                       const float* ref_logp, const float* weights, float* loss, float* logp, float* row_loss,
+                       const lce_opts* opts, void* ws, size_t ws_bytes, void* stream) {
+  return policy_loss(H, W, y, N, d, V, temperature, policy, advantages, old_logp, ref_logp, weights, nullptr, 0, loss,
+                     logp, row_loss, nullptr, nullptr, false, opts, ws, ws_bytes, stream);
+}
+
+int lce_policy_fwd_bwd(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
+                       float temperature, const lce_policy* policy, const float* advantages, const float* old_logp,
+                       const float* ref_logp, const float* weights, const float* grad_loss, int32_t grads, float* loss,
+                       float* logp, float* row_loss, void* dH, void* dW, const lce_opts* opts, void* ws,
+                       size_t ws_bytes, void* stream) {
+  return policy_loss(H, W, y, N, d, V, temperature, policy, advantages, old_logp, ref_logp, weights, grad_loss, grads,
+                     loss, logp, row_loss, dH, dW, true, opts, ws, ws_bytes, stream);
+}
+
+size_t lce_preference_workspace_size(int64_t N, int64_t d, int64_t V, int64_t pairs, int32_t with_grad, int32_t grads,
+                                     const lce_opts* opts) {
+  lce_opts o;
+  lce_opts_init(&o);
+  if (opts) o = *opts;
+  if (check_sizes(N, d, V, &o) != LCE_OK || (grads & ~LCE_DW_BF16) != 0 || pairs < 0 || pairs > kMaxPairs) return 0;
+  return loss_layout(N, d, V, pairs, with_grad != 0, (grads & LCE_DW_BF16) != 0, &o).total;
+}
+
+int lce_preference_forward(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
+                           const void* cu_seqlens, int64_t pairs, float temperature, const lce_preference* preference,
+                           const float* ref_logp, float* loss, float* pair_loss, float* seq_logp, const lce_opts* opts,
+                           void* ws, size_t ws_bytes, void* stream) {
+  return preference_loss(H, W, y, N, d, V, cu_seqlens, pairs, temperature, preference, ref_logp, nullptr, 0, loss,
+                         pair_loss, seq_logp, nullptr, nullptr, false, opts, ws, ws_bytes, stream);
+}
+
+int lce_preference_fwd_bwd(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
+                           const void* cu_seqlens, int64_t pairs, float temperature, const lce_preference* preference,
+                           const float* ref_logp, const float* grad_loss, int32_t grads, float* loss, float* pair_loss,
+                           float* seq_logp, void* dH, void* dW, const lce_opts* opts, void* ws, size_t ws_bytes,
+                           void* stream) {
+  return preference_loss(H, W, y, N, d, V, cu_seqlens, pairs, temperature, preference, ref_logp, grad_loss, grads, loss,
+                         pair_loss, seq_logp, dH, dW, true, opts, ws, ws_bytes, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Layer norm
+// ---------------------------------------------------------------------------
+size_t lce_layernorm_workspace_size(int64_t N, int64_t d) {
+  if (check_sizes(N, d, 1, nullptr) != LCE_OK || d > kNormMaxD) return 0;
+  return align256(sizeof(float) * 2 * static_cast<size_t>(lce::layernorm_parts(N, d)) * static_cast<size_t>(d));
+}
+
+static int layernorm_args(int64_t N, int64_t d, int32_t types) {
+  if (check_sizes(N, d, 1, nullptr) != LCE_OK || d > kNormMaxD) return LCE_ERR_INVALID_ARG;
+  return (types & ~(LCE_NORM_X_F32 | LCE_NORM_W_BF16)) != 0 ? LCE_ERR_INVALID_ARG : LCE_OK;
+}
+
+int lce_layernorm_forward(const void* x, const void* w, const void* b, int64_t N, int64_t d, float eps, int32_t types,
+                          void* H, float* mean, float* rstd, void* stream) {
+  LCE_TRY(layernorm_args(N, d, types));
+  if (!(eps >= 0.f && eps <= FLT_MAX) || (N > 0 && (!x || !H))) return LCE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(b, 16) || !aligned(H, 16) || !aligned(mean, 4) ||
+      !aligned(rstd, 4))
+    return LCE_ERR_ALIGNMENT;
+  DeviceInfo dev;
+  LCE_TRY(device_check(&dev));
+  lce::LayerNormArgs p;
+  std::memset(&p, 0, sizeof p);
+  p.x = x;
+  p.w = w;
+  p.b = b;
+  p.x_f32 = (types & LCE_NORM_X_F32) ? 1 : 0;
+  p.w_bf16 = (types & LCE_NORM_W_BF16) ? 1 : 0;
+  p.N = N;
+  p.d = static_cast<int>(d);
+  p.eps = eps;
+  p.H = H;
+  p.mean = mean;
+  p.rstd = rstd;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return timed(s, K_RMSNORM_FWD, static_cast<double>(N * d) * (p.x_f32 ? 6.0 : 4.0) + 8.0 * static_cast<double>(N + d),
+               [&] { return cuda_rc(lce::launch_layernorm_fwd(p, dev.num_sms, s)); });
+}
+
+int lce_layernorm_backward(const void* x, const void* w, const float* mean, const float* rstd, const void* dH, int64_t N,
+                           int64_t d, int32_t types, void* dx, float* dw, float* db, void* ws, size_t ws_bytes,
+                           void* stream) {
+  LCE_TRY(layernorm_args(N, d, types));
+  if ((!dx && !dw && !db) || (N > 0 && (!x || !mean || !rstd || !dH)) || ((dw || db) && !ws))
+    return LCE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dH, 16) ||
+      !aligned(dx, 16) || !aligned(dw, 4) || !aligned(db, 4) || !aligned(ws, 256))
+    return LCE_ERR_ALIGNMENT;
+  if ((dw || db) && ws_bytes < lce_layernorm_workspace_size(N, d)) return LCE_ERR_WORKSPACE;
+  DeviceInfo dev;
+  LCE_TRY(device_check(&dev));
+  lce::LayerNormArgs p;
+  std::memset(&p, 0, sizeof p);
+  p.x = x;
+  p.w = w;
+  p.x_f32 = (types & LCE_NORM_X_F32) ? 1 : 0;
+  p.w_bf16 = (types & LCE_NORM_W_BF16) ? 1 : 0;
+  p.N = N;
+  p.d = static_cast<int>(d);
+  p.mean = const_cast<float*>(mean);
+  p.rstd = const_cast<float*>(rstd);
+  p.dH = dH;
+  p.dx = dx;
+  p.dw = dw;
+  p.db = db;
+  p.part = static_cast<float*>(ws);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return timed(s, K_RMSNORM_BWD, static_cast<double>(N * d) * (p.x_f32 ? 10.0 : 6.0) + 8.0 * static_cast<double>(N + d),
+               [&] { return cuda_rc(lce::launch_layernorm_bwd(p, dev.num_sms, s)); });
+}
+
+}  // extern "C"
+
+extern "C" {
 
 int lce_scale_grads_bfloat(void* dH, void* dW, int64_t N, int64_t d, int64_t V, const float* grad_loss, void* stream) {
   if (N < 0 || d <= 0 || d % 8 != 0 || V < 0 || !grad_loss) return LCE_ERR_INVALID_ARG;

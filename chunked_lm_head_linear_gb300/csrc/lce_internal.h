@@ -69,7 +69,7 @@ __device__ __forceinline__ bool in_bounds(long long i, long long n, int* flags) 
 // Device-side status block at the start of the workspace.
 struct DevStatus {
   int flags;              // kFlag* bits
-  int rows_done;          // distillation: rows whose loss is written
+  int rows_done;          // distillation and the losses: rows (pairs) whose loss is written
   long long n_valid;      // denominator n actually used (count or override)
   long long n_counted;    // valid labels counted in this call
   float gscale;           // g / n (mean), g (sum); 0 when n == 0 under mean
@@ -213,6 +213,27 @@ cudaError_t launch_rmsnorm_fwd(const void* x, const float* w, long long N, int d
                                cudaStream_t s);
 cudaError_t launch_rmsnorm_bwd(const void* x, const float* w, const float* rstd, const void* dH, long long N, int d,
                                void* dx, float* dw, float* part, cudaStream_t s);
+// Layer norm (lce_layernorm.cu). x in bf16 or fp32; w and b in fp32 or bf16, either may be null.
+struct LayerNormArgs {
+  const void* x;           // [N, d]
+  const void* w;           // [d] or null (ones)
+  const void* b;           // [d] or null (zeros), forward only
+  int x_f32, w_bf16;
+  long long N;
+  int d;
+  float eps;
+  void* H;                 // [N, d] bf16 (forward)
+  float* mean;             // [N]: out (or null) of the forward, in for the backward
+  float* rstd;             // [N]
+  const void* dH;          // [N, d] bf16 (backward)
+  void* dx;                // [N, d] as x, or null
+  float* dw;               // [d] or null
+  float* db;               // [d] or null
+  float* part;             // [2, layernorm_parts(N, d), d] partial sums of dw and db
+};
+int layernorm_parts(long long N, long long d);
+cudaError_t launch_layernorm_fwd(const LayerNormArgs& p, int num_sms, cudaStream_t s);
+cudaError_t launch_layernorm_bwd(const LayerNormArgs& p, int num_sms, cudaStream_t s);
 // In-place x *= *g of n_bf16 bf16 values (a multiple of 8) and n_f32 fp32 values (a multiple of 4).
 cudaError_t launch_scale(void* bf16, long long n_bf16, float* f32, long long n_f32, const float* g, int num_sms,
                          cudaStream_t s);
@@ -343,6 +364,84 @@ cudaError_t launch_distill_count(const int64_t* idx, const void* t, int t_bf16, 
                                  long long ignore_index, DevStatus* st, int* cnt, int ncnt, int num_sms,
                                  cudaStream_t s);
 cudaError_t launch_distill_row(const DistillArgs& p, int rows, cudaStream_t s);
+
+// ----------------------------------------------------------------------------
+// Losses on log-probabilities (lce_losses.cu)
+// ----------------------------------------------------------------------------
+// Rows of a chunk of the policy and preference losses: from the logits' partial
+// sums (or the statistics found from them) to the row's factor a = dloss/dlogp
+// over T, its scale, its row of dW's second operand and of the gradient tile.
+struct LossRowArgs {
+  int V, d, nparts;
+  long long ldz, ldg;
+  float inv_t;
+  long long ignore_index;
+  const int64_t* y;        // [rows] labels of this chunk
+  const float4* partials;  // [rows, nparts]
+  const float* ztgt;       // Z null: the label logits
+  const float* Z;          // [rows, ldz] fp32 logits, or null: no gradient tile here
+  __nv_bfloat16* G;        // [rows, ldg]
+  const uint4* H;          // [rows, d] bf16
+  uint4* Ht;               // [rows, d] bf16(scale H) out, or null (no dW)
+  float* logp;             // [rows]: out (policy), in (preference)
+  float2* stats;           // [rows] (max z, log sum exp((z - max)/T)): out (policy, or null), in (preference)
+  float* rowscale;         // [rows] out, or null: no gradient (policy)
+  float* label;            // [rows] out: the label's entry of the tile
+  float* a;                // [rows] out: the upstream factor that a gradient epilogue reads, or null
+  DevStatus* st;
+};
+
+struct PolicyArgs {
+  LossRowArgs row;
+  const float* advantages;  // [rows], as the next four
+  const float* old_logp;    // or null: the ratio is 1
+  const float* ref_logp;    // or null: no KL term
+  const float* weights;     // or null: 1
+  float* row_loss;          // [rows] out
+  float clip_low, clip_high, dual_clip, kl_coef;
+  int kl;
+  // one chunk (loss not null): the row finished last counts the tokens, sums the rows' losses and sets the scales
+  float* loss;
+  const float* grad_loss;
+  int mean;
+  long long n_override;
+  long long N;
+};
+
+// The pairs of the preference loss: sequences' log-probabilities, the pairs' losses and the factor of
+// each sequence's tokens (without 1/n).
+struct PairArgs {
+  const void* cu;          // [2 P + 1] sequence bounds, int64 or int32
+  int cu32;
+  long long P, N;
+  int V;
+  long long ignore_index;
+  const int64_t* y;        // [N]
+  const float* logp;       // [N]
+  const float* ref;        // [2 P] or null
+  float beta, margin, smoothing;
+  int kind, average;
+  float* pair_loss;        // [P]
+  float* seq_logp;         // [2 P]
+  float* coef;             // [2 P]
+  float* loss;
+  const float* grad_loss;
+  double weight;           // 1/n, or 1 for a sum
+  DevStatus* st;
+};
+
+struct PreferenceArgs {
+  LossRowArgs row;
+  long long c0;            // first row of the chunk
+  const void* cu;
+  int cu32;
+  long long P;
+  const float* coef;       // [2 P]
+};
+
+cudaError_t launch_policy_row(const PolicyArgs& p, int rows, cudaStream_t s);
+cudaError_t launch_pairs(const PairArgs& p, cudaStream_t s);
+cudaError_t launch_preference_row(const PreferenceArgs& p, int rows, cudaStream_t s);
 
 // GEMM tile geometry (must match the kernels): each CTA of a pair loads 128
 // rows of a K-major operand per box and 64 rows of an MN-major one.

@@ -477,6 +477,7 @@ __global__ void __launch_bounds__(1024) k_prepare(const int64_t* __restrict__ y,
     const long long n = n_override >= 0 ? n_override : total;
     const float g = grad_loss != nullptr ? *grad_loss : 1.f;
     st->flags = anybad ? kFlagLabelRange : 0;
+    st->rows_done = 0;
     st->n_counted = total;
     st->n_valid = n;
     if (reduction == 0) {

@@ -1,0 +1,322 @@
+// Losses on the log-probabilities of given tokens, with their gradients: the
+// clipped policy loss with a KL term and the loss of paired sequences' log
+// ratios. Both are, per row, a factor a_i = dloss/dlogp_i; the gradient of the
+// logits is then
+//   G_v = a_i ([v = y_i] - p_v) / T,   dH = G W,   dW = G^T H
+// and everything but a_i is the token operators': the logits GEMM with its
+// partial sums, the gradient tile over the row's scale (lce_rows.cuh) and the
+// backward GEMMs. A policy row knows its factor as soon as its log-probability
+// is known; a pair's factor needs all rows of its two sequences.
+#include "lce_rows.cuh"
+
+namespace lce {
+namespace {
+
+// ----------------------------------------------------------------------------
+// The parts of a row kernel
+// ----------------------------------------------------------------------------
+struct RowStats {
+  float M, logs;  // max z, log sum exp((z - M)/T)
+};
+
+// A row's partial sums merged in a fixed order by the block.
+__device__ __forceinline__ RowStats merge_row(const LossRowArgs& p, int r, float* red, RowSum* sums) {
+  const float4* pr = p.partials + static_cast<long long>(r) * p.nparts;
+  const int tid = threadIdx.x, tiles = (p.V + 127) / 128;
+  float M = -INFINITY;
+  for (int t = tid; t < tiles; t += kRowThreads) M = fmaxf(M, pr[t].x);
+  M = block_max(M, red);
+  RowSum acc{0.f, 0.f, 0.f};
+  for (int t = tid; t < tiles; t += kRowThreads) add_partial(acc, pr[t], M, p.inv_t);
+  acc = warp_add(acc);
+  if ((tid & 31) == 0) sums[tid >> 5] = acc;
+  __syncthreads();
+  return RowStats{M, log_sum(add_groups(sums))};
+}
+
+// The row's scale, its row of dW's second operand and of the gradient tile (TILE), for the factor a.
+template <bool TILE>
+__device__ __forceinline__ void row_gradient(const LossRowArgs& p, int r, int y, float a, float logp, const RowStats& s) {
+  const int tid = threadIdx.x;
+  const Upstream u{a * p.inv_t, 0.f, y};
+  const float entry = label_entry(u, logp, nullptr, r), scale = row_scale(u, entry);
+  const float label = scale == 1.f ? entry : 1.f;
+  if (tid == 0) {
+    p.rowscale[r] = scale;
+    p.label[r] = label;
+    if (p.a != nullptr) p.a[r] = a;
+  }
+  if (p.Ht != nullptr) {
+    const int groups = p.d / 8;
+    const long long at = static_cast<long long>(r) * groups;
+    scale_row(p.H + at, p.Ht + at, groups, scale, u.a != 0.f, tid, kRowThreads);
+  }
+  if (!TILE) return;
+  GradRow g;
+  g.m = s.M;
+  g.k = p.inv_t * kLog2e;
+  g.shift = -s.logs * kLog2e;
+  g.c0 = -u.a * (1.f / scale);
+  g.y = y;
+  g.keep = u.a == 0.f ? 0u : ~0u;
+  write_grad_row(g, label, p.Z + static_cast<long long>(r) * p.ldz, p.G + static_cast<long long>(r) * p.ldg, p.V, tid,
+                 kRowThreads);
+}
+
+// The label of row r, -1 where none is given.
+__device__ __forceinline__ int given_label(const int64_t* y, long long r, long long ignore_index, int V) {
+  const long long v = y[r];
+  return v != ignore_index && v >= 0 && v < V ? static_cast<int>(v) : -1;
+}
+
+// Sum of n floats in fp64, in an order that depends on n alone.
+__device__ __forceinline__ double block_total(const float* x, long long n, double* red) {
+  const int tid = threadIdx.x;
+  double sum = 0.0;
+  for (long long i = tid; i < n; i += kRowThreads) sum += static_cast<double>(__ldcg(x + i));
+  red[tid] = sum;
+  __syncthreads();
+  for (int w = kRowThreads / 2; w > 0; w >>= 1) {
+    if (tid < w) red[tid] += red[tid + w];
+    __syncthreads();
+  }
+  return red[0];
+}
+
+// True in the block that finishes last of `total`, which then sees what the others wrote.
+__device__ __forceinline__ bool last_block(DevStatus* st, int total) {
+  __shared__ int s_last;
+  if (threadIdx.x == 0) {
+    __threadfence();
+    s_last = atomicAdd(&st->rows_done, 1) == total - 1;
+  }
+  __syncthreads();
+  if (s_last) __threadfence();
+  return s_last != 0;
+}
+
+// ----------------------------------------------------------------------------
+// Policy loss
+// ----------------------------------------------------------------------------
+// With l = logp, r = exp(l - old) (1 without old) and s = min(r A, clip(r) A),
+// for A < 0 not below dual A:
+//   row = w (kl_coef KL - s),   a = w (kl_coef dKL/dl - [the unclipped side] r A)
+//   KL of u = l - ref: k1 = u, k2 = u^2 / 2, k3 = exp(-u) - 1 + u
+// A weight of zero leaves nothing, whatever the row holds; an advantage of zero
+// has no share even of an infinite ratio.
+__device__ __forceinline__ void policy_row(const PolicyArgs& p, int r, float logp, float& row, float& a) {
+  row = a = 0.f;
+  const float w = p.weights != nullptr ? p.weights[r] : 1.f;
+  if (w == 0.f) return;
+  const float A = p.advantages[r];
+  float gain = 0.f, slope = 0.f;
+  if (A != 0.f) {
+    const float ratio = p.old_logp != nullptr ? expf(logp - p.old_logp[r]) : 1.f;
+    const float open = ratio * A, bound = fminf(fmaxf(ratio, 1.f - p.clip_low), 1.f + p.clip_high) * A;
+    const bool clipped = bound < open;
+    gain = clipped ? bound : open;
+    slope = clipped ? 0.f : open;
+    if (A < 0.f && p.dual_clip > 0.f && gain < p.dual_clip * A) {
+      gain = p.dual_clip * A;
+      slope = 0.f;
+    }
+  }
+  row = -gain;
+  a = -slope;
+  if (p.ref_logp != nullptr) {
+    const float u = logp - p.ref_logp[r];
+    // exp(-u) - 1 without what the difference loses near 0
+    const float e = expm1f(-u), kl = p.kl == 1 ? u : p.kl == 2 ? 0.5f * u * u : e + u;
+    row = fmaf(p.kl_coef, kl, row);
+    a = fmaf(p.kl_coef, p.kl == 1 ? 1.f : p.kl == 2 ? u : -e, a);
+  }
+  row *= w;
+  a *= w;
+}
+
+// One block per row of the chunk.
+template <bool GRAD, bool TILE>
+__global__ void __launch_bounds__(kRowThreads, 8) k_policy_row(const PolicyArgs p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  __shared__ float red[kRowThreads / 32];
+  __shared__ RowSum s_sum[kGroups];
+  __shared__ double s_total[kRowThreads];
+  const int r = blockIdx.x, tid = threadIdx.x;
+  const LossRowArgs& q = p.row;
+  const int y = given_label(q.y, r, q.ignore_index, q.V);
+  float logp = 0.f, row = 0.f, a = 0.f;
+  RowStats s{0.f, 0.f};
+  if (y >= 0) {
+    s = merge_row(q, r, red, s_sum);
+    const float z = q.Z != nullptr ? q.Z[static_cast<long long>(r) * q.ldz + y] : q.ztgt[r];
+    logp = (z - s.M) * q.inv_t - s.logs;
+    policy_row(p, r, logp, row, a);
+  }
+  if (tid == 0) {
+    q.logp[r] = logp;
+    p.row_loss[r] = row;
+    if (GRAD && q.stats != nullptr) q.stats[r] = make_float2(s.M, s.logs);
+    if (p.loss != nullptr) {
+      if (y >= 0) atomicAdd(reinterpret_cast<unsigned long long*>(&q.st->n_counted), 1ull);
+      if (y < 0 && q.y[r] != q.ignore_index) atomicOr(&q.st->flags, kFlagLabelRange);
+    }
+  }
+  if (GRAD) row_gradient<TILE>(q, r, y, a, logp, s);
+  if (p.loss == nullptr) return;
+  if (!last_block(q.st, static_cast<int>(p.N))) return;
+  const double sum = block_total(p.row_loss, p.N, s_total);
+  if (tid == 0) {
+    const long long counted = __ldcg(&q.st->n_counted), n = p.n_override >= 0 ? p.n_override : counted;
+    const double weight = p.mean ? (n > 0 ? 1.0 / static_cast<double>(n) : 0.0) : 1.0;
+    q.st->n_valid = n;
+    q.st->gscale = static_cast<float>((p.grad_loss != nullptr ? static_cast<double>(*p.grad_loss) : 1.0) * weight);
+    *p.loss = static_cast<float>(sum * weight);
+  }
+}
+
+// ----------------------------------------------------------------------------
+// Preference loss
+// ----------------------------------------------------------------------------
+__device__ __forceinline__ long long bound_at(const void* cu, int cu32, long long i) {
+  return cu32 ? static_cast<long long>(static_cast<const int32_t*>(cu)[i]) : static_cast<const int64_t*>(cu)[i];
+}
+
+__device__ __forceinline__ double softplus(double x) { return fmax(x, 0.0) + log1p(exp(-fabs(x))); }
+__device__ __forceinline__ double sigmoid(double x) {
+  const double e = exp(-fabs(x));
+  return (x >= 0 ? 1.0 : e) / (1.0 + e);
+}
+
+// One block per pair p: sequences 2 p (chosen) and 2 p + 1 (rejected). With S
+// their log-probabilities (sums in fp64, or means, over the given tokens),
+// delta = (S_c - S_r) - (ref_c - ref_r) and x = beta delta - margin
+//   sigmoid  -(1 - e) log sig(x) - e log sig(-x),   hinge  max(0, 1 - x)
+//   ipo      (delta - 1 / (2 beta))^2
+// Bounds that fall or leave [0, N] set the status bit; the pair then has no part in loss and gradient.
+__global__ void __launch_bounds__(kRowThreads) k_pairs(const PairArgs p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  __shared__ double s_red[kRowThreads];
+  __shared__ double s_sum[2];
+  __shared__ int s_cnt[2];
+  const int tid = threadIdx.x;
+  const long long pair = blockIdx.x;
+  if (pair == 0 && tid == 0)
+    p.st->gscale = static_cast<float>((p.grad_loss != nullptr ? static_cast<double>(*p.grad_loss) : 1.0) * p.weight);
+  if (p.P == 0) {
+    if (tid == 0) *p.loss = 0.f;
+    return;
+  }
+  long long c[3];
+  for (int i = 0; i < 3; ++i) c[i] = bound_at(p.cu, p.cu32, 2 * pair + i);
+  const bool ok = c[0] >= 0 && c[0] <= c[1] && c[1] <= c[2] && c[2] <= p.N;
+  if (!ok) {
+    if (tid == 0) atomicOr(&p.st->flags, kFlagLabelRange);
+    c[0] = c[1] = c[2] = 0;
+  }
+  for (int h = 0; h < 2; ++h) {
+    double sum = 0.0;
+    int cnt = 0;
+    for (long long r = c[h] + tid; r < c[h + 1]; r += kRowThreads)
+      if (given_label(p.y, r, p.ignore_index, p.V) >= 0) {
+        sum += static_cast<double>(p.logp[r]);
+        ++cnt;
+      }
+    s_red[tid] = sum;
+    __syncthreads();
+    for (int w = kRowThreads / 2; w > 0; w >>= 1) {
+      if (tid < w) s_red[tid] += s_red[tid + w];
+      __syncthreads();
+    }
+    if (tid == 0) {
+      s_sum[h] = s_red[0];
+      s_cnt[h] = 0;
+    }
+    __syncthreads();
+    for (int off = 16; off > 0; off >>= 1) cnt += __shfl_xor_sync(0xffffffffu, cnt, off);
+    if ((tid & 31) == 0) atomicAdd(&s_cnt[h], cnt);
+    __syncthreads();
+  }
+  if (tid == 0) {
+    double per[2], S[2];
+    for (int h = 0; h < 2; ++h) {
+      per[h] = p.average ? (s_cnt[h] > 0 ? 1.0 / s_cnt[h] : 0.0) : 1.0;
+      S[h] = s_sum[h] * per[h];
+      p.seq_logp[2 * pair + h] = static_cast<float>(S[h]);
+    }
+    double delta = S[0] - S[1];
+    if (p.ref != nullptr) delta -= static_cast<double>(p.ref[2 * pair]) - static_cast<double>(p.ref[2 * pair + 1]);
+    const double beta = p.beta, x = beta * delta - p.margin, e = p.smoothing;
+    double loss, slope;
+    if (p.kind == 0) {
+      loss = (1.0 - e) * softplus(-x) + (e > 0.0 ? e * softplus(x) : 0.0);
+      slope = beta * (e * sigmoid(x) - (1.0 - e) * sigmoid(-x));
+    } else if (p.kind == 1) {
+      loss = x < 1.0 ? 1.0 - x : x != x ? x : 0.0;
+      slope = x < 1.0 ? -beta : x != x ? x : 0.0;
+    } else {
+      const double far = delta - 0.5 / beta;
+      loss = far * far;
+      slope = 2.0 * far;
+    }
+    if (!ok) loss = slope = 0.0;
+    p.pair_loss[pair] = static_cast<float>(loss);
+    p.coef[2 * pair] = static_cast<float>(slope * per[0]);
+    p.coef[2 * pair + 1] = static_cast<float>(-slope * per[1]);
+  }
+  if (!last_block(p.st, static_cast<int>(p.P))) return;
+  const double sum = block_total(p.pair_loss, p.P, s_red);
+  if (tid == 0) *p.loss = static_cast<float>(sum * p.weight);
+}
+
+// The sequence that holds row r: the last whose first row is not behind r. -1 before the first, >= S behind the last.
+__device__ __forceinline__ long long sequence_of(const void* cu, int cu32, long long S, long long r) {
+  long long lo = 0, hi = S + 1;  // bounds [0, lo) are <= r, [hi, S] are > r
+  while (lo < hi) {
+    const long long mid = (lo + hi) >> 1;
+    if (bound_at(cu, cu32, mid) <= r)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo - 1;
+}
+
+// One block per row of the chunk, once the pairs' factors are known.
+template <bool TILE>
+__global__ void __launch_bounds__(kRowThreads, 8) k_preference_row(const PreferenceArgs p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int r = blockIdx.x;
+  const LossRowArgs& q = p.row;
+  const int y = given_label(q.y, r, q.ignore_index, q.V);
+  float a = 0.f;
+  if (y >= 0) {
+    const long long s = sequence_of(p.cu, p.cu32, 2 * p.P, p.c0 + r);
+    if (s >= 0 && s < 2 * p.P) a = p.coef[s];
+  }
+  const float2 st = q.stats[r];
+  row_gradient<TILE>(q, r, y, a, q.logp[r], RowStats{st.x, st.y});
+}
+
+}  // namespace
+
+cudaError_t launch_policy_row(const PolicyArgs& p, int rows, cudaStream_t s) {
+  if (rows <= 0) return cudaSuccess;
+  if (p.row.rowscale == nullptr) return launch_k(k_policy_row<false, false>, rows, kRowThreads, 0, s, p);
+  return p.row.Z != nullptr ? launch_k(k_policy_row<true, true>, rows, kRowThreads, 0, s, p)
+                            : launch_k(k_policy_row<true, false>, rows, kRowThreads, 0, s, p);
+}
+
+cudaError_t launch_pairs(const PairArgs& p, cudaStream_t s) {
+  return launch_k(k_pairs, static_cast<unsigned>(p.P > 0 ? p.P : 1), kRowThreads, 0, s, p);
+}
+
+cudaError_t launch_preference_row(const PreferenceArgs& p, int rows, cudaStream_t s) {
+  if (rows <= 0) return cudaSuccess;
+  return p.row.Z != nullptr ? launch_k(k_preference_row<true>, rows, kRowThreads, 0, s, p)
+                            : launch_k(k_preference_row<false>, rows, kRowThreads, 0, s, p);
+}
+
+}  // namespace lce

@@ -19,6 +19,12 @@ Entry points (same names as the C ABI):
   lce_logprobs_keep / lce_logprobs_keep_backward   the same with the rows' statistics in place of lse
   lce_distill_forward(H, W, idx, t)      -> loss, row_loss against a teacher's top logits
   lce_distill_fwd_bwd(H, W, idx, t, g)   -> loss, row_loss, dH, dW
+  lce_policy_forward(H, W, y, adv, ..)   -> loss, logp, row_loss of the clipped policy loss with a KL term
+  lce_policy_fwd_bwd(H, W, y, adv, ..)   -> loss, logp, row_loss, dH, dW
+  lce_preference_forward(H, W, y, cu)    -> loss, pair_loss, seq_logp of paired sequences' log ratios
+  lce_preference_fwd_bwd(H, W, y, cu)    -> loss, pair_loss, seq_logp, dH, dW
+  lce_layernorm_forward(x, w, b)         -> H, mean, rstd: layer norm in front of the head
+  lce_layernorm_backward(x, w, mean, rstd, dH) -> dx, dw, db
   lce_scale_grads, auto_chunk (lce_auto_chunk), workspace_size, read_device_status, profile_begin/end
 """
 from __future__ import annotations
@@ -48,6 +54,10 @@ LCE_TEST_FORCE_TIMEOUT = 0x7E57
 LCE_MAX_TOP = 128
 LCE_TEACHER_BF16, LCE_TEACHER_LOGPROBS = 1, 2
 LCE_DW_BF16 = 1
+LCE_KL = {None: 0, "none": 0, "k1": 1, "k2": 2, "k3": 3}
+LCE_PREFERENCE = {"sigmoid": 0, "hinge": 1, "ipo": 2}
+LCE_PREFERENCE_AVERAGE, LCE_PREFERENCE_CU_INT32 = 1, 2
+LCE_NORM_X_F32, LCE_NORM_W_BF16 = 1, 2
 
 # Every symbol include/lce.h declares.
 EXPORTED = ("lce_opts_init", "lce_workspace_size", "lce_forward", "lce_backward", "lce_fwd_bwd",
@@ -58,7 +68,9 @@ EXPORTED = ("lce_opts_init", "lce_workspace_size", "lce_forward", "lce_backward"
             "lce_scale_grads", "lce_fwd_bwd_sliced", "lce_vshard_chunk_stats", "lce_vshard_chunk_backward",
             "lce_logits_stride", "lce_logprobs_workspace_size", "lce_logprobs", "lce_logprobs_backward_workspace_size",
             "lce_logprobs_backward", "lce_logprobs_keep", "lce_logprobs_keep_backward", "lce_distill_workspace_size", "lce_distill_forward", "lce_distill_fwd_bwd",
-            "lce_scale_grads_bfloat")
+            "lce_scale_grads_bfloat", "lce_policy_workspace_size", "lce_policy_forward", "lce_policy_fwd_bwd",
+            "lce_preference_workspace_size", "lce_preference_forward", "lce_preference_fwd_bwd",
+            "lce_layernorm_workspace_size", "lce_layernorm_forward", "lce_layernorm_backward")
 LCE_KERNEL_KINDS = 11
 # Kernel kinds whose profiled work is flops (tensor-core GEMMs); the others count bytes.
 GEMM_KINDS = ("logits_stats", "logits_grad", "gemm_dH_dW", "logits_ref")
@@ -71,6 +83,16 @@ class LceOpts(ctypes.Structure):
                 ("n_valid_override", ctypes.c_int64), ("reduction", ctypes.c_int32),
                 ("accumulate_dW", ctypes.c_int32), ("sync_check", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class LcePolicy(ctypes.Structure):
+    _fields_ = [("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float), ("dual_clip", ctypes.c_float),
+                ("kl_coef", ctypes.c_float), ("kl", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class LcePreference(ctypes.Structure):
+    _fields_ = [("beta", ctypes.c_float), ("label_smoothing", ctypes.c_float), ("margin", ctypes.c_float),
+                ("kind", ctypes.c_int32), ("flags", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class LceProfile(ctypes.Structure):
@@ -174,6 +196,27 @@ def load(path: str | None = None):
         lib.lce_distill_fwd_bwd.restype = I32
         lib.lce_scale_grads_bfloat.argtypes = [P, P, I64, I64, I64, P, P]
         lib.lce_scale_grads_bfloat.restype = I32
+        POL, PREF = ctypes.POINTER(LcePolicy), ctypes.POINTER(LcePreference)
+        lib.lce_policy_workspace_size.argtypes = [I64, I64, I64, I32, I32, OPT]
+        lib.lce_policy_workspace_size.restype = SZ
+        lib.lce_policy_forward.argtypes = [P, P, P, I64, I64, I64, F32, POL, P, P, P, P, P, P, P, OPT, P, SZ, P]
+        lib.lce_policy_forward.restype = I32
+        lib.lce_policy_fwd_bwd.argtypes = [P, P, P, I64, I64, I64, F32, POL, P, P, P, P, P, I32, P, P, P, P, P, OPT, P, SZ,
+                                           P]
+        lib.lce_policy_fwd_bwd.restype = I32
+        lib.lce_preference_workspace_size.argtypes = [I64, I64, I64, I64, I32, I32, OPT]
+        lib.lce_preference_workspace_size.restype = SZ
+        lib.lce_preference_forward.argtypes = [P, P, P, I64, I64, I64, P, I64, F32, PREF, P, P, P, P, OPT, P, SZ, P]
+        lib.lce_preference_forward.restype = I32
+        lib.lce_preference_fwd_bwd.argtypes = [P, P, P, I64, I64, I64, P, I64, F32, PREF, P, P, I32, P, P, P, P, P, OPT, P,
+                                               SZ, P]
+        lib.lce_preference_fwd_bwd.restype = I32
+        lib.lce_layernorm_workspace_size.argtypes = [I64, I64]
+        lib.lce_layernorm_workspace_size.restype = SZ
+        lib.lce_layernorm_forward.argtypes = [P, P, P, I64, I64, F32, I32, P, P, P, P]
+        lib.lce_layernorm_forward.restype = I32
+        lib.lce_layernorm_backward.argtypes = [P, P, P, P, P, I64, I64, I32, P, P, P, P, SZ, P]
+        lib.lce_layernorm_backward.restype = I32
         lib.lce_kernel_name.argtypes = [I32]
         lib.lce_kernel_name.restype = ctypes.c_char_p
         _lib = lib
@@ -966,6 +1009,240 @@ def lce_distill_fwd_bwd(H, W, idx, t, grad_loss=None, *, temperature: float = 1.
     _raise(rc, "lce_distill_fwd_bwd")
     _keep(stream, H, W, idx, t, ws, loss, row_loss, dH, dW, grad_loss)
     return loss, row_loss, dH, dW
+
+
+# ---------------------------------------------------------------------------
+# Losses on log-probabilities (see include/lce.h)
+# ---------------------------------------------------------------------------
+def lce_policy_workspace_size(N: int, d: int, V: int, with_grad: bool = True, grads: int = 0,
+                              opts: LceOpts | None = None) -> int:
+    return load().lce_policy_workspace_size(N, d, V, int(bool(with_grad)), grads, _opt_ref(opts))
+
+
+def lce_preference_workspace_size(N: int, d: int, V: int, pairs: int, with_grad: bool = True, grads: int = 0,
+                                  opts: LceOpts | None = None) -> int:
+    return load().lce_preference_workspace_size(N, d, V, pairs, int(bool(with_grad)), grads, _opt_ref(opts))
+
+
+def _check_policy(H, W, y, advantages, old_logp, ref_logp, weights, kl, kl_coef, clip_low, clip_high, dual_clip):
+    import torch
+    N, d, V = _check_inputs(H, W, y)
+    if kl not in LCE_KL:
+        raise ValueError(f"kl must be one of 'none', 'k1', 'k2', 'k3', got {kl!r}")
+    if LCE_KL[kl] and ref_logp is None:
+        raise ValueError("a KL term needs ref_logp")
+    if advantages is None:
+        raise ValueError("advantages is required")
+    for name, t in (("advantages", advantages), ("old_logp", old_logp), ("ref_logp", ref_logp), ("weights", weights)):
+        _check_dev(t, name, torch.float32, shape=(N,), device=H.device)
+    return N, d, V, LcePolicy(float(clip_low), float(clip_high), float(dual_clip or 0.0), float(kl_coef), LCE_KL[kl], 0)
+
+
+def lce_policy_forward(H, W, y, advantages, old_logp=None, ref_logp=None, *, weights=None, temperature: float = 1.0,
+                       clip_low: float = 0.2, clip_high: float = 0.2, dual_clip: float = 0.0, kl="none",
+                       kl_coef: float = 0.0, workspace=None, stream=None, **opt_kw):
+    """The clipped policy loss of the tokens y [N] under softmax(H W^T / temperature):
+    loss (fp32 [1]), logp and row_loss (fp32 [N], 0 where y is ignore_index).
+    advantages, old_logp (of the policy that sampled; None: this one), ref_logp
+    (of the reference model of the KL term) and weights are fp32 [N]. The ratio
+    exp(logp - old_logp) is clipped to [1 - clip_low, 1 + clip_high]; dual_clip
+    (0 or None: off) bounds the loss of negative advantages; kl is "none", "k1",
+    "k2" or "k3". reduction="mean" divides by the number of given tokens (or
+    n_valid_override)."""
+    import torch
+    N, d, V, policy = _check_policy(H, W, y, advantages, old_logp, ref_logp, weights, kl, kl_coef, clip_low, clip_high,
+                                    dual_clip)
+    opts, ws = _token_plan(opt_kw, N, "lce_policy", H.device, workspace,
+                           lambda o: lce_policy_workspace_size(N, d, V, False, 0, o))
+    loss = torch.empty(1, dtype=torch.float32, device=H.device)
+    logp = torch.empty(N, dtype=torch.float32, device=H.device)
+    row_loss = torch.empty(N, dtype=torch.float32, device=H.device)
+    rc = load().lce_policy_forward(_ptr(H), _ptr(W), _ptr(y), N, d, V, float(temperature), ctypes.byref(policy),
+                                   _ptr(advantages), _ptr(old_logp), _ptr(ref_logp), _ptr(weights), _ptr(loss),
+                                   _ptr(logp), _ptr(row_loss), ctypes.byref(opts), _ptr(ws), ws.numel(), _stream(stream))
+    _raise(rc, "lce_policy_forward")
+    _keep(stream, H, W, y, advantages, old_logp, ref_logp, weights, ws, loss, logp, row_loss)
+    return loss, logp, row_loss
+
+
+def lce_policy_fwd_bwd(H, W, y, advantages, old_logp=None, ref_logp=None, grad_loss=None, *, weights=None,
+                       temperature: float = 1.0, clip_low: float = 0.2, clip_high: float = 0.2, dual_clip: float = 0.0,
+                       kl="none", kl_coef: float = 0.0, dW=None, dW_dtype=None, need_dH: bool = True,
+                       need_dW: bool = True, workspace=None, stream=None, **opt_kw):
+    """lce_policy_forward and its gradients in one call: loss, logp, row_loss, dH
+    (bf16 [N, d]), dW (fp32 [V, d], or bf16 with dW_dtype); a gradient that is
+    not wanted is None."""
+    import torch
+    N, d, V, policy = _check_policy(H, W, y, advantages, old_logp, ref_logp, weights, kl, kl_coef, clip_low, clip_high,
+                                    dual_clip)
+    _check_dev(grad_loss, "grad_loss", torch.float32, numel=1, device=H.device)
+    grads = _dW_mode(dW_dtype)
+    grads = grads if need_dW else 0
+    opts, ws = _token_plan(opt_kw, N, "lce_policy", H.device, workspace,
+                           lambda o: lce_policy_workspace_size(N, d, V, True, grads, o))
+    loss = torch.empty(1, dtype=torch.float32, device=H.device)
+    logp = torch.empty(N, dtype=torch.float32, device=H.device)
+    row_loss = torch.empty(N, dtype=torch.float32, device=H.device)
+    dH, dW = _token_grads(H, V, d, opts, grads, dW, need_dH, need_dW)
+    rc = load().lce_policy_fwd_bwd(_ptr(H), _ptr(W), _ptr(y), N, d, V, float(temperature), ctypes.byref(policy),
+                                   _ptr(advantages), _ptr(old_logp), _ptr(ref_logp), _ptr(weights), _ptr(grad_loss),
+                                   grads, _ptr(loss), _ptr(logp), _ptr(row_loss), _ptr(dH), _ptr(dW),
+                                   ctypes.byref(opts), _ptr(ws), ws.numel(), _stream(stream))
+    _raise(rc, "lce_policy_fwd_bwd")
+    _keep(stream, H, W, y, advantages, old_logp, ref_logp, weights, ws, grad_loss, loss, logp, row_loss, dH, dW)
+    return loss, logp, row_loss, dH, dW
+
+
+def _check_preference(H, W, y, cu_seqlens, ref_logp, kind, beta, label_smoothing, margin, average):
+    import torch
+    N, d, V = _check_inputs(H, W, y)
+    if kind not in LCE_PREFERENCE:
+        raise ValueError(f"kind must be one of {', '.join(map(repr, LCE_PREFERENCE))}, got {kind!r}")
+    if kind != "sigmoid" and label_smoothing != 0.0:
+        raise ValueError('label_smoothing belongs to kind="sigmoid"')
+    if kind == "ipo" and margin != 0.0:
+        raise ValueError('kind="ipo" has no margin')
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dtype not in (torch.int64, torch.int32):
+        raise ValueError("cu_seqlens must be an int64 or int32 CUDA tensor")
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] % 2 != 1:
+        raise ValueError("cu_seqlens must hold the 2 pairs + 1 bounds of the sequences (chosen, rejected, chosen, ...)")
+    pairs = cu_seqlens.shape[0] // 2
+    _check_dev(cu_seqlens, "cu_seqlens", cu_seqlens.dtype, device=H.device)
+    _check_dev(ref_logp, "ref_logp", torch.float32, shape=(2 * pairs,), device=H.device)
+    flags = (LCE_PREFERENCE_AVERAGE if average else 0) | (LCE_PREFERENCE_CU_INT32 if cu_seqlens.dtype == torch.int32 else 0)
+    return N, d, V, pairs, LcePreference(float(beta), float(label_smoothing), float(margin), LCE_PREFERENCE[kind], flags, 0)
+
+
+def lce_preference_forward(H, W, y, cu_seqlens, ref_logp=None, *, kind: str = "sigmoid", beta: float = 0.1,
+                           label_smoothing: float = 0.0, margin: float = 0.0, average: bool = False,
+                           temperature: float = 1.0, workspace=None, stream=None, **opt_kw):
+    """Loss of paired sequences' log ratios: loss (fp32 [1]), pair_loss (fp32 [P])
+    and seq_logp (fp32 [2 P], the sequences' summed, or with average=True mean,
+    log-probabilities). cu_seqlens (int64 or int32 [2 P + 1]) bounds the sequences
+    in the rows, chosen and rejected in turn; ref_logp (fp32 [2 P]) is their
+    seq_logp under the reference model, None without one. Tokens whose y is
+    ignore_index (prompts) and rows in no sequence do not count. kind is
+    "sigmoid", "hinge" or "ipo"; reduction="mean" divides by P (or
+    n_valid_override)."""
+    import torch
+    N, d, V, P, pref = _check_preference(H, W, y, cu_seqlens, ref_logp, kind, beta, label_smoothing, margin, average)
+    opts, ws = _token_plan(opt_kw, N, "lce_preference", H.device, workspace,
+                           lambda o: lce_preference_workspace_size(N, d, V, P, False, 0, o))
+    loss = torch.empty(1, dtype=torch.float32, device=H.device)
+    pair_loss = torch.empty(P, dtype=torch.float32, device=H.device)
+    seq_logp = torch.empty(2 * P, dtype=torch.float32, device=H.device)
+    rc = load().lce_preference_forward(_ptr(H), _ptr(W), _ptr(y), N, d, V, _ptr(cu_seqlens), P, float(temperature),
+                                       ctypes.byref(pref), _ptr(ref_logp), _ptr(loss), _ptr(pair_loss), _ptr(seq_logp),
+                                       ctypes.byref(opts), _ptr(ws), ws.numel(), _stream(stream))
+    _raise(rc, "lce_preference_forward")
+    _keep(stream, H, W, y, cu_seqlens, ref_logp, ws, loss, pair_loss, seq_logp)
+    return loss, pair_loss, seq_logp
+
+
+def lce_preference_fwd_bwd(H, W, y, cu_seqlens, ref_logp=None, grad_loss=None, *, kind: str = "sigmoid",
+                           beta: float = 0.1, label_smoothing: float = 0.0, margin: float = 0.0, average: bool = False,
+                           temperature: float = 1.0, dW=None, dW_dtype=None, need_dH: bool = True,
+                           need_dW: bool = True, workspace=None, stream=None, **opt_kw):
+    """lce_preference_forward and its gradients in one call: loss, pair_loss,
+    seq_logp, dH (bf16 [N, d]), dW (fp32 [V, d], or bf16 with dW_dtype); a
+    gradient that is not wanted is None. Rows of more than one chunk
+    (chunk_tokens, by default 6143) have their logits computed twice."""
+    import torch
+    N, d, V, P, pref = _check_preference(H, W, y, cu_seqlens, ref_logp, kind, beta, label_smoothing, margin, average)
+    _check_dev(grad_loss, "grad_loss", torch.float32, numel=1, device=H.device)
+    grads = _dW_mode(dW_dtype)
+    grads = grads if need_dW else 0
+    opts, ws = _token_plan(opt_kw, N, "lce_preference", H.device, workspace,
+                           lambda o: lce_preference_workspace_size(N, d, V, P, True, grads, o))
+    loss = torch.empty(1, dtype=torch.float32, device=H.device)
+    pair_loss = torch.empty(P, dtype=torch.float32, device=H.device)
+    seq_logp = torch.empty(2 * P, dtype=torch.float32, device=H.device)
+    dH, dW = _token_grads(H, V, d, opts, grads, dW, need_dH, need_dW)
+    rc = load().lce_preference_fwd_bwd(_ptr(H), _ptr(W), _ptr(y), N, d, V, _ptr(cu_seqlens), P, float(temperature),
+                                       ctypes.byref(pref), _ptr(ref_logp), _ptr(grad_loss), grads, _ptr(loss),
+                                       _ptr(pair_loss), _ptr(seq_logp), _ptr(dH), _ptr(dW), ctypes.byref(opts),
+                                       _ptr(ws), ws.numel(), _stream(stream))
+    _raise(rc, "lce_preference_fwd_bwd")
+    _keep(stream, H, W, y, cu_seqlens, ref_logp, ws, grad_loss, loss, pair_loss, seq_logp, dH, dW)
+    return loss, pair_loss, seq_logp, dH, dW
+
+
+# ---------------------------------------------------------------------------
+# Layer norm (see include/lce.h)
+# ---------------------------------------------------------------------------
+def lce_layernorm_workspace_size(N: int, d: int) -> int:
+    return int(load().lce_layernorm_workspace_size(N, d))
+
+
+def _check_layernorm(x, w, b):
+    import torch
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("x must be a bf16 or fp32 CUDA tensor [N, d] (there is no CPU path)")
+    if x.dim() != 2 or not x.is_contiguous():
+        raise ValueError("x must be a contiguous [N, d] tensor")
+    if x.device.index != torch.cuda.current_device():
+        raise ValueError(f"x is on {x.device}; make it the current device (torch.cuda.set_device)")
+    types = LCE_NORM_X_F32 if x.dtype == torch.float32 else 0
+    params = [t for t in (w, b) if t is not None]
+    if any(not isinstance(t, torch.Tensor) or t.dtype not in (torch.bfloat16, torch.float32) for t in params) or \
+            len({t.dtype for t in params}) > 1:
+        raise ValueError("w and b must both be fp32 or both bf16 CUDA tensors [d], or None")
+    for name, t in (("w", w), ("b", b)):
+        if t is not None:
+            _check_dev(t, name, t.dtype, shape=(x.shape[1],), device=x.device)
+            types |= LCE_NORM_W_BF16 if t.dtype == torch.bfloat16 else 0
+    return x.shape[0], x.shape[1], types
+
+
+def lce_layernorm_forward(x, w=None, b=None, eps=1e-5, *, stream=None):
+    """Layer norm H = bf16((x - mean) rstd w + b) of the rows of x (bf16 or fp32
+    [N, d]), and the rows' mean and rstd (fp32 [N]). w and b (fp32 or bf16 [d])
+    may be None."""
+    import torch
+    N, d, types = _check_layernorm(x, w, b)
+    H = torch.empty((N, d), dtype=torch.bfloat16, device=x.device)
+    mean = torch.empty(N, dtype=torch.float32, device=x.device)
+    rstd = torch.empty(N, dtype=torch.float32, device=x.device)
+    _raise(load().lce_layernorm_forward(_ptr(x), _ptr(w), _ptr(b), N, d, float(eps), types, _ptr(H), _ptr(mean),
+                                        _ptr(rstd), _stream(stream)), "lce_layernorm_forward")
+    _keep(stream, x, w, b, H, mean, rstd)
+    return H, mean, rstd
+
+
+def lce_layernorm_backward(x, w, mean, rstd, dH, *, bias: bool = True, need_dx: bool = True, need_dw: bool = True,
+                           workspace=None, stream=None):
+    """dx (as x), dw and db (fp32 [d]) of lce_layernorm_forward from dH (bf16
+    [N, d]) and its mean and rstd; what is not wanted is None, and so is dw
+    without a w."""
+    import torch
+    N, d, types = _check_layernorm(x, w, None)
+    _check_dev(mean, "mean", torch.float32, shape=(N,), device=x.device)
+    _check_dev(rstd, "rstd", torch.float32, shape=(N,), device=x.device)
+    _check_dev(dH, "dH", torch.bfloat16, shape=(N, d), device=x.device)
+    if mean is None or rstd is None or dH is None:
+        raise ValueError("mean, rstd and dH are required")
+    need_dw = need_dw and w is not None
+    if not (need_dx or need_dw or bias):
+        raise ValueError("none of dx, dw and db is wanted")
+    dx = torch.empty_like(x) if need_dx else None
+    dw = torch.empty(d, dtype=torch.float32, device=x.device) if need_dw else None
+    db = torch.empty(d, dtype=torch.float32, device=x.device) if bias else None
+    if need_dw or bias:
+        need = lce_layernorm_workspace_size(N, d)
+        if need == 0:
+            raise LCEError(LCE_ERR_INVALID_ARG, "lce_layernorm_workspace_size")
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        else:
+            _check_dev(workspace, "workspace", torch.uint8, device=x.device)
+            if workspace.numel() < need:
+                raise LCEError(LCE_ERR_WORKSPACE, f"workspace of {workspace.numel()} bytes, the call needs {need}")
+    rc = load().lce_layernorm_backward(_ptr(x), _ptr(w), _ptr(mean), _ptr(rstd), _ptr(dH), N, d, types, _ptr(dx),
+                                       _ptr(dw), _ptr(db), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                                       _stream(stream))
+    _raise(rc, "lce_layernorm_backward")
+    _keep(stream, x, w, mean, rstd, dH, dx, dw, db, workspace)
+    return dx, dw, db
 
 
 def lce_scale_grads_bfloat(dH, dW, grad_loss, *, stream=None):

@@ -408,6 +408,129 @@ int lce_distill_fwd_bwd(const void* H, const void* W, const int64_t* idx, const 
  * once more, unless the factor is a power of two. */
 int lce_scale_grads_bfloat(void* dH, void* dW, int64_t N, int64_t d, int64_t V, const float* grad_loss, void* stream);
 
+/*
+ * Losses on the log-probabilities of given tokens, with their gradients in one
+ * call (6 N V d flops, as lce_fwd_bwd). z, z', p, logp, H, W, y, opts, grads, ws
+ * and stream are those of the token operators; chunk_tokens = 0 cuts the rows as
+ * they do. grad_loss: device fp32 [1] or NULL (1.0); either of dH, dW may be
+ * NULL: not wanted, not computed. opts->reserved must be 0. All arrays of floats
+ * are fp32, on the device.
+ *
+ * lce_policy_forward, lce_policy_fwd_bwd: the clipped policy loss. Per row with a
+ * given token (y neither ignore_index nor out of range), A = advantages_i, w =
+ * weights_i (NULL: 1), l = logp_i:
+ *   r = exp(l - old_logp_i)      (old_logp NULL: the tokens were sampled by the
+ *                                 model as it is, r = 1 with gradient r A)
+ *   s = min(r A, clip(r, 1 - clip_low, 1 + clip_high) A); for A < 0 and dual_clip
+ *       >= 1 not below dual_clip A (0: no such bound)
+ *   row_loss_i = w (kl_coef KL(u) - s), u = l - ref_logp_i
+ *   KL: LCE_KL_NONE 0 (ref_logp is not read), LCE_KL_K1 u, LCE_KL_K2 u^2 / 2,
+ *       LCE_KL_K3 exp(-u) - 1 + u
+ *   loss = sum_i row_loss_i / n (LCE_MEAN) or without / n, n = rows with a given
+ *          token (weights do not count), or opts->n_valid_override
+ *   a_i = grad_loss d loss / d l,  G_iv = a_i ([v = y_i] - p_iv) / temperature
+ *   dH = G W (bf16), dW = G^T H
+ * The gradient of min and max is that of the side taken (of the unclipped one
+ * where both are equal). Outputs: loss [1], logp [N] and row_loss [N], 0 where no
+ * token is given. Rows without a given token, with a weight of 0, or whose a_i is
+ * 0 (clipped) have a zero gradient and no share of dW whatever their row of H
+ * holds, and the first two no loss.
+ * clip_low, clip_high >= 0 (clip_high may be infinite). Workspace:
+ * lce_policy_workspace_size.
+ */
+#define LCE_KL_NONE 0
+#define LCE_KL_K1 1
+#define LCE_KL_K2 2
+#define LCE_KL_K3 3
+typedef struct lce_policy {
+  float clip_low, clip_high;
+  float dual_clip;  /* 0: none */
+  float kl_coef;
+  int32_t kl;       /* LCE_KL_* */
+  int32_t reserved; /* 0 */
+} lce_policy;
+size_t lce_policy_workspace_size(int64_t N, int64_t d, int64_t V, int32_t with_grad, int32_t grads,
+                                 const lce_opts* opts);
+int lce_policy_forward(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
+                       float temperature, const lce_policy* policy, const float* advantages, const float* old_logp,
+                       const float* ref_logp, const float* weights, float* loss, float* logp, float* row_loss,
+                       const lce_opts* opts, void* ws, size_t ws_bytes, void* stream);
+int lce_policy_fwd_bwd(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
+                       float temperature, const lce_policy* policy, const float* advantages, const float* old_logp,
+                       const float* ref_logp, const float* weights, const float* grad_loss, int32_t grads, float* loss,
+                       float* logp, float* row_loss, void* dH, void* dW, const lce_opts* opts, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/*
+ * lce_preference_forward, lce_preference_fwd_bwd: the loss of paired sequences'
+ * log ratios. cu_seqlens [2 pairs + 1] (device int64, or int32 with
+ * LCE_PREFERENCE_CU_INT32) bounds 2 pairs sequences of rows: sequence s is
+ * rows [cu_s, cu_{s+1}), and pair j is the sequences 2 j (chosen) and 2 j + 1
+ * (rejected). Rows before cu_0 and behind the last bound are in no sequence. With
+ * S_s the sum of logp over the given tokens of s (LCE_PREFERENCE_AVERAGE: their
+ * mean; 0 without any) and ref_logp [2 pairs] the same of a reference model (NULL:
+ * none):
+ *   delta = (S_{2j} - S_{2j+1}) - (ref_{2j} - ref_{2j+1}), x = beta delta - margin
+ *   LCE_PREFERENCE_SIGMOID  -(1 - e) log sigmoid(x) - e log sigmoid(-x), e =
+ *                           label_smoothing (0 <= e < 0.5)
+ *   LCE_PREFERENCE_HINGE    max(0, 1 - x)
+ *   LCE_PREFERENCE_IPO      (delta - 1 / (2 beta))^2 (margin must be 0)
+ *   loss = sum_j pair_loss_j / n (LCE_MEAN) or without / n, n = pairs, or
+ *          opts->n_valid_override
+ * label_smoothing must be 0 but for the first. beta > 0. Outputs: loss [1],
+ * pair_loss [pairs], seq_logp [2 pairs] (S), dH, dW as above; rows in no sequence
+ * have a zero gradient. S is summed in fp64. Bounds that fall, or leave [0, N],
+ * set LCE_DEVICE_LABEL_RANGE; that pair then has no loss and no gradient. Where
+ * the rows are one chunk their logits are kept for the gradient, else they are
+ * computed twice (8 N V d flops). Workspace: lce_preference_workspace_size.
+ */
+#define LCE_PREFERENCE_SIGMOID 0
+#define LCE_PREFERENCE_HINGE 1
+#define LCE_PREFERENCE_IPO 2
+#define LCE_PREFERENCE_AVERAGE 1   /* flags */
+#define LCE_PREFERENCE_CU_INT32 2
+typedef struct lce_preference {
+  float beta, label_smoothing, margin;
+  int32_t kind;     /* LCE_PREFERENCE_SIGMOID, _HINGE or _IPO */
+  int32_t flags;    /* LCE_PREFERENCE_AVERAGE | LCE_PREFERENCE_CU_INT32 */
+  int32_t reserved; /* 0 */
+} lce_preference;
+size_t lce_preference_workspace_size(int64_t N, int64_t d, int64_t V, int64_t pairs, int32_t with_grad, int32_t grads,
+                                     const lce_opts* opts);
+int lce_preference_forward(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
+                           const void* cu_seqlens, int64_t pairs, float temperature, const lce_preference* preference,
+                           const float* ref_logp, float* loss, float* pair_loss, float* seq_logp, const lce_opts* opts,
+                           void* ws, size_t ws_bytes, void* stream);
+int lce_preference_fwd_bwd(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V,
+                           const void* cu_seqlens, int64_t pairs, float temperature, const lce_preference* preference,
+                           const float* ref_logp, const float* grad_loss, int32_t grads, float* loss, float* pair_loss,
+                           float* seq_logp, void* dH, void* dW, const lce_opts* opts, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/*
+ * Layer norm in front of the head. x [N, d] is bf16, or fp32 with LCE_NORM_X_F32;
+ * w and b [d] (either may be NULL: ones, zeros) are fp32, or both bf16 with
+ * LCE_NORM_W_BF16. d is a multiple of 8, at most 32768; x, w, b, H, dH and dx are
+ * 16-byte aligned.
+ *   mean_i = sum_k x_ik / d, rstd_i = 1 / sqrt(sum_k (x_ik - mean_i)^2 / d + eps)
+ *   H = bf16((x - mean) rstd w + b)
+ * lce_layernorm_forward: H [N, d] (bf16), mean and rstd [N] (fp32; either may be
+ * NULL). lce_layernorm_backward, from dH [N, d] (bf16), mean and rstd:
+ *   g = dH w, dx = rstd (g - sum_k g / d - xh sum_k (g xh) / d), xh = (x - mean) rstd
+ *   dw = sum_i dH_i xh_i, db = sum_i dH_i
+ * dx as x; dw and db fp32 [d] (overwritten), summed in a fixed order; any of the three
+ * may be NULL: not wanted. Outputs do not overlap inputs. Scratch for dw and db:
+ * lce_layernorm_workspace_size.
+ */
+#define LCE_NORM_X_F32 1
+#define LCE_NORM_W_BF16 2
+size_t lce_layernorm_workspace_size(int64_t N, int64_t d);
+int lce_layernorm_forward(const void* x, const void* w, const void* b, int64_t N, int64_t d, float eps, int32_t types,
+                          void* H, float* mean, float* rstd, void* stream);
+int lce_layernorm_backward(const void* x, const void* w, const float* mean, const float* rstd, const void* dH, int64_t N,
+                           int64_t d, int32_t types, void* dx, float* dw, float* db, void* ws, size_t ws_bytes,
+                           void* stream);
+
 /* Synchronise the stream and copy the workspace's device status bits
  * (LCE_DEVICE_*) of the last call that used ws into *flags. */
 int lce_read_device_status(const void* ws, void* stream, int* flags);

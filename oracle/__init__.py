@@ -23,6 +23,15 @@ from .lce_oracle import (  # noqa: F401
     lce_f64, norm_lce_bf16, rmsnorm_backward_f64, rmsnorm_f64, round_bf16_bits,
     vshard_backward_f64, vshard_merge_f64, vshard_stats_f64,
 )
+from .losses_oracle import (  # noqa: F401
+    head_gradients_f64,
+    layernorm_backward_f64,
+    layernorm_f64,
+    policy_f64,
+    policy_rows_f64,
+    preference_f64,
+    preference_pairs_f64,
+)
 from .tokens_oracle import (  # noqa: F401
     distill_f64, logprobs_backward_f64, logprobs_f64, teacher_f64,
 )
