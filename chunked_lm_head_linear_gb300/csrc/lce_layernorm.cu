@@ -23,6 +23,9 @@ namespace {
 
 constexpr int kLnThreads = 256;
 constexpr int kLnWarps = kLnThreads / 32;
+constexpr int kSumWarps = 32;
+constexpr int kSms = 152;        // the one-pass backward runs one or two persistent blocks a SM
+constexpr int kLnFusedD = 8192;  // longest row whose backward is one pass
 
 // Eight neighbouring elements of a row, as they are held in registers.
 template <bool F32>
@@ -30,7 +33,6 @@ struct Group;
 template <>
 struct Group<false> {
   uint4 v;
-  static constexpr int kBytes = 16;
   __device__ __forceinline__ void load(const void* p, long long i) { v = static_cast<const uint4*>(p)[i]; }
   __device__ __forceinline__ void clear() { v = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void get(float (&f)[8]) const {
@@ -45,7 +47,6 @@ struct Group<false> {
 template <>
 struct Group<true> {
   float4 a, b;
-  static constexpr int kBytes = 32;
   __device__ __forceinline__ void load(const void* p, long long i) {
     a = static_cast<const float4*>(p)[2 * i];
     b = static_cast<const float4*>(p)[2 * i + 1];
@@ -89,111 +90,310 @@ __device__ __forceinline__ float warp_total(float v) {
   return v;
 }
 
-// Persistent warps, R rows at a time; lane l owns the column groups l, l + 32,
-// ... of a row, of which the first G stay in registers through the three passes
-// (sum, squares, result) and the rest, of rows longer than 256 G, is read again.
-template <bool F32, int G, int R>
-__global__ void __launch_bounds__(kLnThreads) k_layernorm_fwd(const LayerNormArgs p) {
-  grid_dep_wait();
-  grid_dep_launch();
-  const int lane = threadIdx.x & 31, groups = p.d / 8;
-  const long long warps = static_cast<long long>(gridDim.x) * kLnWarps;
-  const float d = static_cast<float>(p.d);
-  for (long long i0 = (static_cast<long long>(blockIdx.x) * kLnWarps + (threadIdx.x >> 5)) * R; i0 < p.N; i0 += warps * R) {
-    Group<F32> v[R][G];
-    float sum[R], sq[R];
-#pragma unroll
-    for (int q = 0; q < R; ++q) {
-#pragma unroll
-      for (int j = 0; j < G; ++j) {
-        const int gI = lane + 32 * j;
-        if (i0 + q < p.N && gI < groups)
-          v[q][j].load(p.x, (i0 + q) * groups + gI);
-        else
-          v[q][j].clear();
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < R; ++q) {
-      sum[q] = sq[q] = 0.f;
-      float f[8];
-#pragma unroll
-      for (int j = 0; j < G; ++j) {
-        v[q][j].get(f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sum[q] += f[k];
-      }
-      if (R == 1)
-        for (int gI = lane + 32 * G; gI < groups; gI += 32) {
-          Group<F32> t;
-          t.load(p.x, i0 * groups + gI);
-          t.get(f);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) sum[q] += f[k];
-        }
-    }
-#pragma unroll
-    for (int q = 0; q < R; ++q) sum[q] = warp_total(sum[q]) / d;  // the mean from here on
-#pragma unroll
-    for (int q = 0; q < R; ++q) {
-      float f[8];
-#pragma unroll
-      for (int j = 0; j < G; ++j) {
-        v[q][j].get(f);
-        if (lane + 32 * j < groups) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) sq[q] = fmaf(f[k] - sum[q], f[k] - sum[q], sq[q]);
-        }
-      }
-      if (R == 1)
-        for (int gI = lane + 32 * G; gI < groups; gI += 32) {
-          Group<F32> t;
-          t.load(p.x, i0 * groups + gI);
-          t.get(f);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) sq[q] = fmaf(f[k] - sum[q], f[k] - sum[q], sq[q]);
-        }
-    }
-#pragma unroll
-    for (int q = 0; q < R; ++q) {
-      sq[q] = 1.f / sqrtf(warp_total(sq[q]) / d + p.eps);  // 1 / deviation from here on
-      if (lane == 0 && i0 + q < p.N) {
-        if (p.mean != nullptr) p.mean[i0 + q] = sum[q];
-        if (p.rstd != nullptr) p.rstd[i0 + q] = sq[q];
-      }
-    }
-    auto result = [&](const Group<F32>& x, int gI, int q, const float (&w)[8], const float (&b)[8]) {
-      float f[8];
-      x.get(f);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = fmaf((f[k] - sum[q]) * sq[q], w[k], b[k]);
-      store8(p.H, (i0 + q) * groups + gI, f, false);
-    };
-#pragma unroll
-    for (int j = 0; j < G; ++j) {
-      const int gI = lane + 32 * j;
-      if (gI < groups) {
-        float w[8], b[8];
-        param8(p.w, p.w_bf16, gI, 1.f, w);
-        param8(p.b, p.w_bf16, gI, 0.f, b);
-#pragma unroll
-        for (int q = 0; q < R; ++q)
-          if (i0 + q < p.N) result(v[q][j], gI, q, w, b);
-      }
-    }
-    if (R == 1)
-      for (int gI = lane + 32 * G; gI < groups; gI += 32) {
-        float w[8], b[8];
-        param8(p.w, p.w_bf16, gI, 1.f, w);
-        param8(p.b, p.w_bf16, gI, 0.f, b);
-        Group<F32> t;
-        t.load(p.x, i0 * groups + gI);
-        result(t, gI, 0, w, b);
-      }
+// ----------------------------------------------------------------------------
+// Rows through shared memory. A block holds teams of T threads; a team takes R
+// rows at a time and its thread t owns their column groups t, t + T, ... (at most
+// K). Every warp copies its own threads' groups ahead of their use into its own
+// part of a ring of D turns (cp.async, 16 bytes a lane, neighbouring lanes
+// neighbouring pieces) and reads only those back: the copies need no barrier
+// beyond the warp, and what is on its way from HBM does not take registers.
+// ----------------------------------------------------------------------------
+__device__ __forceinline__ void copy16(uint4* dst, const void* src, long long i, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+               :
+               : "r"(smem_u32(dst)), "l"(static_cast<const uint4*>(src) + i), "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <bool F32, int T, int K, int R, int PER>
+struct Ring {
+  static constexpr int kBlock = T < 256 ? 256 : T;
+  static constexpr int kSlots = R * K * PER;  // 16-byte slots of a thread and turn
+  static constexpr int bytes(int D) { return D * kSlots * kBlock * 16; }
+};
+
+// The eight elements of this thread's group in a slot of 32 (bf16) or 64 (fp32) pieces of its warp.
+template <bool F32>
+__device__ __forceinline__ void slot_get(const uint4* warp_slot, int lane, float (&f)[8]) {
+  if constexpr (F32) {
+    const float4 a = reinterpret_cast<const float4*>(warp_slot)[2 * lane], b = reinterpret_cast<const float4*>(warp_slot)[2 * lane + 1];
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  } else {
+    Group<false> g;
+    g.v = warp_slot[lane];
+    g.get(f);
   }
 }
 
-// dx, one warp per row, in two passes over it.
+// The copies of that slot: group g0 + lane of a row whose groups begin at `row`, groups at or behind `groups` (or all,
+// for a row that does not exist) as zeros.
+template <bool F32>
+__device__ __forceinline__ void slot_copy(uint4* warp_slot, int lane, const void* src, long long row, int g0, int groups,
+                                          bool on) {
+  constexpr int PER = F32 ? 2 : 1;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    const int piece = e * 32 + lane;
+    const bool in = on && g0 + piece / PER < groups;
+    copy16(warp_slot + piece, src, in ? (row + g0) * PER + piece : 0, in);
+  }
+}
+
+// Sums of R values over a team of W warps, in order; buf is not used again before a barrier.
+template <int W, int R>
+__device__ __forceinline__ void team_total(float (&v)[R], float (*buf)[R], int warp, int lane) {
+#pragma unroll
+  for (int q = 0; q < R; ++q) v[q] = warp_total(v[q]);
+  if (W > 1) {
+    if (lane == 0) {
+#pragma unroll
+      for (int q = 0; q < R; ++q) buf[warp][q] = v[q];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      v[q] = buf[0][q];
+#pragma unroll
+      for (int i = 1; i < W; ++i) v[q] += buf[i][q];
+    }
+  }
+}
+
+template <bool F32, int T, int K, int R, int D, int B>
+__global__ void __launch_bounds__(T < 256 ? 256 : T, B) k_layernorm_fwd(const LayerNormArgs p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  constexpr int PER = F32 ? 2 : 1;
+  using Rg = Ring<F32, T, K, R, PER>;
+  constexpr int BL = Rg::kBlock, S = BL / T, W = T / 32;
+  constexpr bool kHold = T <= 256;  // weights and biases in registers
+  extern __shared__ uint4 ring[];
+  __shared__ float red[2][S][W][R];
+  const int tid = threadIdx.x, team = tid / T, t = tid % T, lane = tid & 31, warp = t >> 5;
+  const int groups = p.d / 8;
+  const float d = static_cast<float>(p.d), inv_d = 1.f / d;
+  float w[K][8], b[K][8];
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    if (kHold && t + T * j < groups) {
+      param8(p.w, p.w_bf16, t + T * j, 1.f, w[j]);
+      param8(p.b, p.w_bf16, t + T * j, 0.f, b[j]);
+    }
+  }
+  const long long first = (static_cast<long long>(blockIdx.x) * S + team) * R, step = static_cast<long long>(gridDim.x) * S * R;
+  // this warp's 32 PER pieces of slot (q, j)
+  auto slot = [&](int turn, int q, int j) {
+    return ring + ((turn * R + q) * K + j) * PER * BL + (tid >> 5) * 32 * PER;
+  };
+  auto fetch = [&](long long i, int turn) {
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        slot_copy<F32>(slot(turn, q, j), lane, p.x, (i + q) * groups, warp * 32 + T * j, groups, i + q < p.N);
+    }
+    copies_commit();
+  };
+#pragma unroll
+  for (int n = 0; n < D - 1; ++n) fetch(first + n * step, n);
+  int turn = 0;
+  // the loop's length is the block's, so that its teams meet at the barriers
+  for (long long i0 = static_cast<long long>(blockIdx.x) * S * R, i = first; i0 < p.N; i0 += step, i += step) {
+    fetch(i + (D - 1) * step, turn == 0 ? D - 1 : turn - 1);
+    copies_wait<D - 1>();
+    __syncwarp();
+    float x[R][K][8], mean[R], rstd[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      mean[q] = 0.f;
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        slot_get<F32>(slot(turn, q, j), lane, x[q][j]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mean[q] += x[q][j][k];
+      }
+    }
+    __syncwarp();  // read by all of the warp before the next turn's copies
+    team_total<W, R>(mean, red[0][team], warp, lane);
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const float s = mean[q] * inv_d;
+      mean[q] = fmaf(fmaf(-s, d, mean[q]), inv_d, s);  // sum / d without the rounding of 1 / d: exact for flat rows
+      rstd[q] = 0.f;
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        if (t + T * j < groups) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            x[q][j][k] -= mean[q];
+            rstd[q] = fmaf(x[q][j][k], x[q][j][k], rstd[q]);
+          }
+        }
+      }
+    }
+    team_total<W, R>(rstd, red[1][team], warp, lane);
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      rstd[q] = rsqrtf(fmaf(rstd[q], inv_d, p.eps));
+      if (t == 0 && i + q < p.N) {
+        if (p.mean != nullptr) p.mean[i + q] = mean[q];
+        if (p.rstd != nullptr) p.rstd[i + q] = rstd[q];
+      }
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        const int gI = t + T * j;
+        if (i + q < p.N && gI < groups) {
+          if (!kHold) {
+            param8(p.w, p.w_bf16, gI, 1.f, w[j]);
+            param8(p.b, p.w_bf16, gI, 0.f, b[j]);
+          }
+          float f[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] = fmaf(x[q][j][k] * rstd[q], w[j][k], b[j][k]);
+          store8(p.H, (i + q) * groups + gI, f, false);
+        }
+      }
+    }
+    turn = turn == D - 1 ? 0 : turn + 1;
+  }
+  copies_wait<0>();
+}
+
+// dx, dw and db in one pass over x and dH (d up to 2048 K): the two sums of a row
+// are one exchange in its team, x and dH stay in registers between them and dx,
+// and dw and db grow in registers over all of the block's rows. At the end the
+// teams' shares are added in order and the block writes one partial row of each.
+template <bool F32, int T, int K, int R, int D, int B>
+__global__ void __launch_bounds__(kLnThreads, B) k_layernorm_bwd(const LayerNormArgs p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  constexpr int PX = F32 ? 2 : 1, PER = PX + 1;
+  using Rg = Ring<F32, T, K, R, PER>;
+  constexpr int S = kLnThreads / T, W = T / 32;
+  static_assert(S == 1 || K == 1, "teams' shares are added one column group a thread");
+  extern __shared__ uint4 ring[];
+  __shared__ float red[2][S][W][2 * R];
+  __shared__ float share[S][T][17];
+  const int tid = threadIdx.x, team = tid / T, t = tid % T, lane = tid & 31, warp = t >> 5;
+  const int groups = p.d / 8;
+  const float inv_d = 1.f / static_cast<float>(p.d);
+  float aw[K][8], ab[K][8], w[K][8];
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) aw[j][k] = ab[j][k] = w[j][k] = 0.f;
+    if (t + T * j < groups) param8(p.w, p.w_bf16, t + T * j, 1.f, w[j]);
+  }
+  const long long first = (static_cast<long long>(blockIdx.x) * S + team) * R, step = static_cast<long long>(gridDim.x) * S * R;
+  // this warp's pieces of slot (q, j): 32 PX of x, then 32 of dH
+  auto slot = [&](int turn, int q, int j) {
+    return ring + ((turn * R + q) * K + j) * PER * kLnThreads + (tid >> 5) * 32 * PER;
+  };
+  auto fetch = [&](long long i, int turn) {
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        uint4* s = slot(turn, q, j);
+        slot_copy<F32>(s, lane, p.x, (i + q) * groups, warp * 32 + T * j, groups, i + q < p.N);
+        slot_copy<false>(s + 32 * PX, lane, p.dH, (i + q) * groups, warp * 32 + T * j, groups, i + q < p.N);
+      }
+    }
+    copies_commit();
+  };
+  float mu_next[R], r_next[R];
+  auto statistics = [&](long long i) {
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      mu_next[q] = i + q < p.N ? p.mean[i + q] : 0.f;
+      r_next[q] = i + q < p.N ? p.rstd[i + q] : 0.f;
+    }
+  };
+#pragma unroll
+  for (int n = 0; n < D - 1; ++n) fetch(first + n * step, n);
+  statistics(first);
+  int turn = 0, half = 0;
+  for (long long i0 = static_cast<long long>(blockIdx.x) * S * R, i = first; i0 < p.N; i0 += step, i += step, half ^= 1) {
+    fetch(i + (D - 1) * step, turn == 0 ? D - 1 : turn - 1);
+    copies_wait<D - 1>();
+    __syncwarp();
+    float xh[R][K][8], g[R][K][8], r[R], sums[2 * R];  // (x - mean) rstd, dH w
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const float mu = mu_next[q];
+      r[q] = r_next[q];
+      sums[2 * q] = sums[2 * q + 1] = 0.f;
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        slot_get<F32>(slot(turn, q, j), lane, xh[q][j]);
+        slot_get<false>(slot(turn, q, j) + 32 * PX, lane, g[q][j]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float h = g[q][j][k];
+          xh[q][j][k] = (xh[q][j][k] - mu) * r[q];
+          g[q][j][k] = h * w[j][k];
+          sums[2 * q] += g[q][j][k];
+          sums[2 * q + 1] = fmaf(g[q][j][k], xh[q][j][k], sums[2 * q + 1]);
+          aw[j][k] = fmaf(h, xh[q][j][k], aw[j][k]);
+          ab[j][k] += h;
+        }
+      }
+    }
+    statistics(i + step);
+    __syncwarp();  // read by all of the warp before the next turn's copies
+    turn = turn == D - 1 ? 0 : turn + 1;
+    if (p.dx == nullptr) continue;
+    team_total<W, 2 * R>(sums, red[half][team], warp, lane);  // two buffers: one barrier a turn is enough
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const float c0 = sums[2 * q] * inv_d * r[q], c1 = sums[2 * q + 1] * inv_d * r[q];
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        const int gI = t + T * j;
+        if (i + q < p.N && gI < groups) {
+          float f[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] = fmaf(-xh[q][j][k], c1, fmaf(g[q][j][k], r[q], -c0));
+          store8(p.dx, (i + q) * groups + gI, f, F32);
+        }
+      }
+    }
+  }
+  copies_wait<0>();
+  if (p.part == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    if (S > 1) {  // (K is 1 there)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        share[team][t][k] = aw[j][k];
+        share[team][t][8 + k] = ab[j][k];
+      }
+      __syncthreads();
+      if (team != 0) return;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        for (int s = 1; s < S; ++s) {
+          aw[j][k] += share[s][t][k];
+          ab[j][k] += share[s][t][8 + k];
+        }
+    }
+    const int gI = t + T * j;
+    if (gI < groups) {
+      const long long at = static_cast<long long>(blockIdx.x) * groups + gI;
+      store8(p.part, at, aw[j], true);
+      store8(p.part, static_cast<long long>(gridDim.x) * groups + at, ab[j], true);
+    }
+  }
+}
+
+// dx alone, one warp per row, in two passes over it (rows of more than kLnFusedD).
 template <bool F32>
 __global__ void __launch_bounds__(kLnThreads) k_layernorm_dx(const LayerNormArgs p) {
   grid_dep_wait();
@@ -238,7 +438,7 @@ __global__ void __launch_bounds__(kLnThreads) k_layernorm_dx(const LayerNormArgs
   }
 }
 
-// Partial sums of dw and db: block (c, s) owns 256 columns and every gridDim.y-th
+// Partial sums of dw and db alone (d above kLnFusedD): block (c, s) owns 256 columns and every gridDim.y-th
 // group of 8 rows from the s-th on; warp q of it takes the rows q of its groups.
 template <bool F32>
 __global__ void __launch_bounds__(kLnThreads) k_layernorm_dw(const LayerNormArgs p) {
@@ -284,61 +484,102 @@ __global__ void __launch_bounds__(kLnThreads) k_layernorm_dw(const LayerNormArgs
 }
 
 // dw and db from their partial sums, in a fixed order: a block covers 32
-// columns of one of them, warp s sums the parts s, s + 8, ... in order.
-__global__ void __launch_bounds__(kLnThreads) k_layernorm_sum(const LayerNormArgs p, int parts) {
+// columns of one of them, warp s sums the parts s, s + 32, ... in order.
+__global__ void __launch_bounds__(32 * kSumWarps) k_layernorm_sum(const LayerNormArgs p, int parts) {
   grid_dep_wait();
   grid_dep_launch();
-  __shared__ float red[kLnWarps][33];
+  __shared__ float red[kSumWarps][33];
   float* out = blockIdx.y == 0 ? p.dw : p.db;
   if (out == nullptr) return;
   const int lane = threadIdx.x & 31, s = threadIdx.x >> 5, k = blockIdx.x * 32 + lane;
   const float* part = p.part + static_cast<long long>(blockIdx.y) * parts * p.d;
   float t = 0.f;
   if (k < p.d)
-    for (int b = s; b < parts; b += kLnWarps) t += part[static_cast<long long>(b) * p.d + k];
+#pragma unroll 4
+    for (int b = s; b < parts; b += kSumWarps) t += part[static_cast<long long>(b) * p.d + k];
   red[s][lane] = t;
   __syncthreads();
   if (s == 0 && k < p.d) {
-    for (int q = 1; q < kLnWarps; ++q) t += red[q][lane];
+    for (int q = 1; q < kSumWarps; ++q) t += red[q][lane];
     out[k] = t;
   }
 }
 
-template <bool F32, int G, int R>
+template <typename Kern>
+cudaError_t launch_ring(Kern kern, int blocks, int threads, int bytes, const LayerNormArgs& p, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  return launch_k(kern, static_cast<unsigned>(blocks), threads, bytes, s, p);
+}
+
+template <bool F32, int T, int K, int R, int D, int B>
 cudaError_t fwd(const LayerNormArgs& p, int num_sms, cudaStream_t s) {
-  const long long need = (p.N + kLnWarps * R - 1) / (kLnWarps * R), most = 8LL * num_sms;
-  return launch_k(k_layernorm_fwd<F32, G, R>, static_cast<unsigned>(need < most ? need : most), kLnThreads, 0, s, p);
+  using Rg = Ring<F32, T, K, R, F32 ? 2 : 1>;
+  constexpr int rows = Rg::kBlock / T * R;
+  const long long need = (p.N + rows - 1) / rows, most = static_cast<long long>(B) * num_sms;
+  return launch_ring(k_layernorm_fwd<F32, T, K, R, D, B>, static_cast<int>(need < most ? need : most), Rg::kBlock,
+                     Rg::bytes(D), p, s);
 }
 
 template <bool F32>
 cudaError_t fwd_rows(const LayerNormArgs& p, int num_sms, cudaStream_t s) {
-  if (p.d <= 256) return fwd<F32, 1, 4>(p, num_sms, s);
-  if (p.d <= 512) return fwd<F32, 2, 2>(p, num_sms, s);
-  if (p.d <= 1024) return fwd<F32, 4, 1>(p, num_sms, s);
-  if (p.d <= 2048) return fwd<F32, 8, 1>(p, num_sms, s);
-  return fwd<F32, 16, 1>(p, num_sms, s);
+  if (p.d <= 256) return fwd<F32, 32, 1, 2, 4, 3>(p, num_sms, s);
+  if (p.d <= 512) return fwd<F32, 64, 1, 2, 4, 3>(p, num_sms, s);
+  if (p.d <= 1024) return fwd<F32, 128, 1, 2, 4, 3>(p, num_sms, s);
+  if (p.d <= 2048) return fwd<F32, 256, 1, 2, 4, 3>(p, num_sms, s);
+  if (p.d <= 4096) return fwd<F32, 256, 2, 1, 4, 3>(p, num_sms, s);
+  if (p.d <= 8192) return fwd<F32, 256, 4, 1, 3, 2>(p, num_sms, s);
+  if (p.d <= 16384) return fwd<F32, 512, 4, 1, 3, 1>(p, num_sms, s);
+  return fwd<F32, 1024, 4, 1, F32 ? 1 : 2, 1>(p, num_sms, s);
+}
+
+template <bool F32, int T, int K, int R, int D, int B = 2>
+cudaError_t bwd_pass(const LayerNormArgs& p, int parts, cudaStream_t s) {
+  return launch_ring(k_layernorm_bwd<F32, T, K, R, D, B>, parts, kLnThreads, Ring<F32, T, K, R, F32 ? 3 : 2>::bytes(D), p, s);
+}
+
+// Rows that a block of the one-pass backward takes at a time.
+int bwd_rows(long long d) {
+  return d <= 256 ? 8 * 2 : d <= 512 ? 4 * 2 : d <= 1024 ? 2 * 2 : d <= 2048 ? 2 : 1;
 }
 
 template <bool F32>
-cudaError_t bwd(const LayerNormArgs& p, int num_sms, cudaStream_t s) {
-  if (p.dx != nullptr && p.N > 0) {
-    const long long need = (p.N + kLnWarps - 1) / kLnWarps, most = 8LL * num_sms;
-    const cudaError_t e =
-        launch_k(k_layernorm_dx<F32>, static_cast<unsigned>(need < most ? need : most), kLnThreads, 0, s, p);
-    if (e != cudaSuccess) return e;
-  }
-  if (p.dw == nullptr && p.db == nullptr) return cudaSuccess;
+cudaError_t bwd(const LayerNormArgs& q, int num_sms, cudaStream_t s) {
+  LayerNormArgs p = q;
+  const bool sums = p.dw != nullptr || p.db != nullptr;
+  if (!sums) p.part = nullptr;
   const int parts = layernorm_parts(p.N, p.d);
-  const cudaError_t e = launch_k(k_layernorm_dw<F32>, dim3((p.d + 255) / 256, parts), kLnThreads, 0, s, p);
-  if (e != cudaSuccess) return e;
-  return launch_k(k_layernorm_sum, dim3((p.d + 31) / 32, 2), kLnThreads, 0, s, p, parts);
+  cudaError_t e = cudaSuccess;
+  if (p.d <= 256)
+    e = bwd_pass<F32, 32, 1, 2, F32 ? 3 : 4>(p, parts, s);
+  else if (p.d <= 512)
+    e = bwd_pass<F32, 64, 1, 2, F32 ? 3 : 4>(p, parts, s);
+  else if (p.d <= 1024)
+    e = bwd_pass<F32, 128, 1, 2, F32 ? 3 : 4>(p, parts, s);
+  else if (p.d <= 2048)
+    e = bwd_pass<F32, 256, 1, 2, 4>(p, parts, s);
+  else if (p.d <= 4096)
+    e = bwd_pass<F32, 256, 2, 1, 4>(p, parts, s);
+  else if (p.d <= kLnFusedD)
+    e = bwd_pass<F32, 256, 4, 1, 4, 1>(p, parts, s);
+  else {
+    if (p.dx != nullptr && p.N > 0) {
+      const long long need = (p.N + kLnWarps - 1) / kLnWarps, most = 8LL * num_sms;
+      e = launch_k(k_layernorm_dx<F32>, static_cast<unsigned>(need < most ? need : most), kLnThreads, 0, s, p);
+    }
+    if (e == cudaSuccess && sums) e = launch_k(k_layernorm_dw<F32>, dim3((p.d + 255) / 256, parts), kLnThreads, 0, s, p);
+  }
+  if (e != cudaSuccess || !sums) return e;
+  return launch_k(k_layernorm_sum, dim3((p.d + 31) / 32, 2), 32 * kSumWarps, 0, s, p, parts);
 }
 
 }  // namespace
 
+// Blocks of the backward, each with a partial row of dw and db.
 int layernorm_parts(long long N, long long d) {
-  const long long rows = (N + kLnWarps - 1) / kLnWarps, most = 512 / ((d + 255) / 256) + 1;
-  const long long parts = rows < most ? rows : most;
+  const long long rows = d <= kLnFusedD ? bwd_rows(d) : kLnWarps;
+  const long long need = (N + rows - 1) / rows, most = d <= 4096 ? 2 * kSms : d <= kLnFusedD ? kSms : 512 / ((d + 255) / 256) + 1;
+  const long long parts = need < most ? need : most;
   return static_cast<int>(parts > 0 ? parts : 1);
 }
 
