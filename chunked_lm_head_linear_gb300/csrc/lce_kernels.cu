@@ -259,24 +259,34 @@ struct DhEpi {
 #pragma unroll 1
       for (int hh = 0; hh < width / 32; ++hh) {
         const int g0 = (u * width + hh * 32) / 4;  // first 4-column group of these 32 columns
+        // All parts' sums of these columns are on their way before the first is added: one wait for L2
+        // a group of columns instead of one a part (backward of 250 rows, V = 4099: 29.8 -> 26.8 us).
+        float4 a[kDhParts][8];
+#pragma unroll
+        for (int s = 0; s < kDhParts; ++s) {
+          if (s < from_mem) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a[s][j] = __ldcg(slot(s) + (g0 + j) * 32 + lane);
+          }
+        }
         float v[32];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float4 a = __ldcg(slot(0) + (g0 + j) * 32 + lane);
-          v[4 * j] = a.x;
-          v[4 * j + 1] = a.y;
-          v[4 * j + 2] = a.z;
-          v[4 * j + 3] = a.w;
+          v[4 * j] = a[0][j].x;
+          v[4 * j + 1] = a[0][j].y;
+          v[4 * j + 2] = a[0][j].z;
+          v[4 * j + 3] = a[0][j].w;
         }
-#pragma unroll 1
-        for (int s = 1; s < from_mem; ++s) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 a = __ldcg(slot(s) + (g0 + j) * 32 + lane);
-            v[4 * j] += a.x;
-            v[4 * j + 1] += a.y;
-            v[4 * j + 2] += a.z;
-            v[4 * j + 3] += a.w;
+        for (int s = 1; s < kDhParts; ++s) {
+          if (s < from_mem) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              v[4 * j] += a[s][j].x;
+              v[4 * j + 1] += a[s][j].y;
+              v[4 * j + 2] += a[s][j].z;
+              v[4 * j + 3] += a[s][j].w;
+            }
           }
         }
         if (last_in_order) {  // the last part's own sum, still in TMEM, added last
