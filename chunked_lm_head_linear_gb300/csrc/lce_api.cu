@@ -1090,12 +1090,12 @@ lce::TokParams tok_params(const Call& c, int64_t c0, int64_t rows, float tempera
 }
 
 // Logits of chunk rows [c0, c0 + rows) with a token epilogue. out: the chunk's logits buffer (fp32,
-// TOK_STATS_Z) or gradient tile (bf16, TOK_GRAD) with row stride ldo.
+// TOK_STATS_Z), gradient tile or exp tile (bf16, TOK_GRAD, TOK_EXP) with row stride ldo.
 int tok_logits(const Call& c, int64_t c0, int64_t rows, int mode, void* out, int64_t ldo, const lce::TokParams& p) {
   CUtensorMap mA, mB, mC;
   const double flops = 2.0 * static_cast<double>(rows) * static_cast<double>(c.V) * static_cast<double>(c.d);
   LCE_TRY(make_map(&mB, c.W, c.V, c.d, c.d, lce::kBoxRowsK));
-  if (rows <= lce::kFewRows && mode != lce::TOK_GRAD) {
+  if (rows <= lce::kFewRows && (mode == lce::TOK_STATS || mode == lce::TOK_STATS_Z) && !p.only_if) {
     LCE_TRY(make_map(&mA, c.H + c0 * c.d, rows, c.d, c.d, lce::few_rows_box(rows)));
     return timed(c.s, K_LOGITS_STATS, flops, [&] {
       return cuda_rc(lce::launch_rows_logits(mA, mB, mode == lce::TOK_STATS_Z, static_cast<float*>(out), ldo, c.V, c.d,
@@ -1105,11 +1105,11 @@ int tok_logits(const Call& c, int64_t c0, int64_t rows, int mode, void* out, int
   LCE_TRY(make_map(&mA, c.H + c0 * c.d, rows, c.d, c.d, lce::kBoxRowsK));
   if (mode == lce::TOK_STATS_Z)
     LCE_TRY(make_map_t(&mC, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, out, rows, c.V, ldo, 32u, kStoreRows));
-  else if (mode == lce::TOK_GRAD)
+  else if (mode == lce::TOK_GRAD || mode == lce::TOK_EXP)
     LCE_TRY(make_map(&mC, out, rows, c.V, ldo, kStoreRows));
   else
     mC = mB;  // this epilogue stores nothing
-  return timed(c.s, mode == lce::TOK_GRAD ? K_LOGITS_GRAD : K_LOGITS_STATS, flops, [&] {
+  return timed(c.s, p.only_if ? K_OTHER : mode == lce::TOK_GRAD ? K_LOGITS_GRAD : K_LOGITS_STATS, p.only_if ? 0.0 : flops, [&] {
     return cuda_rc(lce::launch_tok_logits(mode, mA, mB, mC, rows, c.V, c.d, p, c.dev.num_sms, c.s));
   });
 }
@@ -1474,30 +1474,54 @@ int lce_distill_fwd_bwd(const void* H, const void* W, const int64_t* idx, const 
 // ---------------------------------------------------------------------------
 namespace {
 
-// Workspace of a policy or preference call: the token operators' for its chunks, and what the preference
-// loss keeps between its two passes over the rows.
+// Workspace of a policy or preference call: the token operators' for its chunks, the exp tile's sums and
+// guards (exp), and what the preference loss keeps between its two passes over the rows.
 struct LossLayout {
   TokLayout tok;
+  bool exp = false;                             // gradient tiles from exp tiles, not from kept logits
+  int64_t step = 0;                             // rows of a logits launch (C, or less where the exp tiles of all rows are kept)
+  size_t ref = 0, sums = 0, guard = 0;          // [N], [C, nparts], [launches]
   size_t logp = 0, stats = 0, a = 0, coef = 0;  // [N], [N] pairs, [C], [2 P]
+  size_t rest = 0;                              // [C]
   size_t total = 0;
 };
 
+// Logits of a chunk from which on the exp tile is the faster way to a gradient tile: the pass over kept logits costs 6
+// bytes each, the exp tile's further launches about 20 us.
+constexpr int64_t kExpLogits = 24000000;
+
+// Most rows whose exp tiles the preference loss keeps by default until its factors are known: 2 bytes a logit, as much
+// as the kept logits and the gradient tile of one chunk of 6144 rows take.
+constexpr int64_t kPreferenceRows = 3 * 6144;
+
 // pairs < 0: the policy loss.
-LossLayout loss_layout(int64_t N, int64_t d, int64_t V, int64_t pairs, bool with_grad, bool dW_bf16, const lce_opts* o) {
+LossLayout loss_layout(int64_t N, int64_t d, int64_t V, int64_t pairs, bool with_grad, bool dW_bf16, const lce_opts* opts) {
   LossLayout L;
-  const bool one = N <= tok_chunk(N, o);
-  L.tok = tok_layout(N, d, V, with_grad && (pairs < 0 || one), with_grad, dW_bf16, with_grad, o);
+  lce_opts o = *opts;
+  L.step = tok_chunk(N, &o);
+  const bool large = with_grad && L.step > lce::kFewRows && L.step * V >= kExpLogits;
+  if (large && pairs >= 0 && o.chunk_tokens == 0 && N <= kPreferenceRows) o.chunk_tokens = N;
+  const bool one = N <= tok_chunk(N, &o);
+  L.exp = large && (pairs < 0 || one);
+  L.tok = tok_layout(N, d, V, with_grad && (pairs < 0 || one) && !L.exp, with_grad, dW_bf16, with_grad, &o);
   size_t off = L.tok.total;
   auto take = [&](size_t bytes) {
     const size_t at = off;
     off += align256(bytes);
     return at;
   };
+  const size_t rows = static_cast<size_t>(N > 0 ? N : 1), chunk = static_cast<size_t>(L.tok.base.C);
+  if (L.exp) {
+    L.ref = take(sizeof(float) * rows);
+    L.sums = take(sizeof(float) * chunk * static_cast<size_t>(2 * L.tok.base.T));
+    L.guard = take(sizeof(int) * static_cast<size_t>(ceil_div(N, L.step)));
+    L.a = take(sizeof(float) * chunk);
+    L.rest = take(sizeof(float) * chunk);
+  }
   if (pairs >= 0) {
-    const size_t rows = static_cast<size_t>(N > 0 ? N : 1);
     L.logp = take(sizeof(float) * rows);
     L.stats = take(sizeof(float2) * rows);
-    L.a = take(sizeof(float) * static_cast<size_t>(L.tok.base.C));
+    if (!L.exp) L.a = take(sizeof(float) * chunk);
     L.coef = take(sizeof(float) * 2 * static_cast<size_t>(pairs > 0 ? pairs : 1));
   }
   L.total = off;
@@ -1506,9 +1530,9 @@ LossLayout loss_layout(int64_t N, int64_t d, int64_t V, int64_t pairs, bool with
 
 constexpr int64_t kMaxPairs = (int64_t{1} << 30) - 1;
 
-// The parts of a row kernel's arguments that both losses fill alike.
+// The parts of a row kernel's arguments that both losses fill alike (at: the rows' place in the chunk's buffers).
 lce::LossRowArgs loss_row(const Call& c, const TokLayout& T, int64_t c0, const lce::TokParams& p, const float* Z,
-                          bool with_grad, bool with_dW) {
+                          bool with_grad, bool with_dW, int64_t at) {
   lce::LossRowArgs a;
   std::memset(&a, 0, sizeof a);
   a.V = p.V;
@@ -1524,17 +1548,57 @@ lce::LossRowArgs loss_row(const Call& c, const TokLayout& T, int64_t c0, const l
   a.Z = Z;
   a.st = c.st;
   if (!with_grad) return a;
-  a.G = reinterpret_cast<__nv_bfloat16*>(c.ws + c.L.P);
+  a.G = reinterpret_cast<__nv_bfloat16*>(c.ws + c.L.P) + at * c.L.ldp;
   a.H = reinterpret_cast<const uint4*>(c.H + c0 * c.d);
-  a.Ht = with_dW ? reinterpret_cast<uint4*>(c.ws + c.L.Ht) : nullptr;
-  a.rowscale = reinterpret_cast<float*>(c.ws + c.L.alpha);
-  a.label = reinterpret_cast<float*>(c.ws + T.label);
+  a.Ht = with_dW ? reinterpret_cast<uint4*>(c.ws + c.L.Ht + 2 * static_cast<size_t>(at * c.d)) : nullptr;
+  a.rowscale = reinterpret_cast<float*>(c.ws + c.L.alpha) + at;
+  a.label = reinterpret_cast<float*>(c.ws + T.label) + at;
   return a;
 }
 
-double loss_row_bytes(const Call& c, int64_t rows, bool with_grad) {
-  return static_cast<double>(rows) * (32.0 * static_cast<double>(c.L.T) + 40.0 +
-                                      (with_grad ? 6.0 * static_cast<double>(c.V) + 4.0 * static_cast<double>(c.d) : 0.0));
+// Before the chunks of a call by exp tiles: the status block, the count of given tokens and the scales, the
+// guards cleared, and the labels' logits.
+int exp_prepare(Call& c, const LossLayout& L, const float* grad_loss) {
+  c.L.guard = L.guard;  // prepare clears them
+  c.L.chunks = ceil_div(c.N, L.step);
+  LCE_TRY(prepare(c, grad_loss));
+  return timed(c.s, K_PREPARE, static_cast<double>(c.N) * (4.0 * static_cast<double>(c.d) + 12.0), [&] {
+    return cuda_rc(lce::launch_label_logits(c.H, c.W, c.y, c.N, static_cast<int>(c.d), static_cast<int>(c.V),
+                                            c.o.ignore_index, reinterpret_cast<float*>(c.ws + L.ref), c.s));
+  });
+}
+
+// The exp tile of a chunk, and its exact statistics if the tile sets the guard.
+int exp_tile(const Call& c, const LossLayout& L, int64_t c0, int64_t rows, lce::TokParams p, int* guard, int64_t at) {
+  p.ref = reinterpret_cast<float*>(c.ws + L.ref) + c0;
+  p.sums = reinterpret_cast<float*>(c.ws + L.sums) + at * p.nparts;
+  p.guard = guard;
+  LCE_TRY(tok_logits(c, c0, rows, lce::TOK_EXP, c.ws + c.L.P + 2 * static_cast<size_t>(at * c.L.ldp), c.L.ldp, p));
+  p.only_if = guard;
+  return tok_logits(c, c0, rows, lce::TOK_STATS, nullptr, 0, p);
+}
+
+// The exact gradient tile, from what the row kernel left, if the guard is set.
+int exp_fallback(const Call& c, int64_t c0, int64_t rows, lce::TokParams p, const lce::LossRowArgs& a, const int* guard) {
+  p.only_if = guard;
+  p.stats = a.stats;
+  p.g_logp = a.a;
+  p.rowscale = a.rowscale;
+  p.label = a.label;
+  return tok_logits(c, c0, rows, lce::TOK_GRAD, a.G, c.L.ldp, p);
+}
+
+void loss_row_exp(lce::LossRowArgs* a, const Call& c, const LossLayout& L, const int* guard, int64_t at) {
+  a->sums = reinterpret_cast<const float*>(c.ws + L.sums) + at * a->nparts;
+  a->guard = guard;
+  a->a = reinterpret_cast<float*>(c.ws + L.a) + at;
+  a->rest = reinterpret_cast<float*>(c.ws + L.rest) + at;
+}
+
+double loss_row_bytes(const Call& c, int64_t rows, bool with_grad, bool with_z) {
+  return static_cast<double>(rows) * ((with_grad && !with_z ? 8.0 : 32.0) * static_cast<double>(c.L.T) + 40.0 +
+                                      (with_z ? 6.0 * static_cast<double>(c.V) : 0.0) +
+                                      (with_grad ? 4.0 * static_cast<double>(c.d) : 0.0));
 }
 
 int policy_loss(const void* H, const void* W, const int64_t* y, int64_t N, int64_t d, int64_t V, float temperature,
@@ -1567,23 +1631,34 @@ int policy_loss(const void* H, const void* W, const int64_t* y, int64_t N, int64
   LCE_TRY(tok_begin(&c, T, H, W, y, N, d, V, o, ws, ws_bytes, stream));
   // With one chunk its rows count themselves, before the GEMMs that need n; with several n is needed by
   // the first chunk's.
-  const bool count_here = !lce::kChecks && c.L.chunks == 1;
-  if (!count_here) LCE_TRY(prepare(c, grad_loss));
+  const bool count_here = !lce::kChecks && c.L.chunks == 1 && !L.exp;
+  if (L.exp)
+    LCE_TRY(exp_prepare(c, L, grad_loss));
+  else if (!count_here)
+    LCE_TRY(prepare(c, grad_loss));
   if (N == 0 && with_grad) LCE_TRY(zero_dW(c, dW, dW_bf16));
-  for (int64_t c0 = 0; c0 < N; c0 += c.L.C) {
+  for (int64_t k = 0, c0 = 0; c0 < N; ++k, c0 += c.L.C) {
     const int64_t rows = (N - c0) < c.L.C ? (N - c0) : c.L.C;
     lce::TokParams p = tok_params(c, c0, rows, temperature);
+    int* guard = L.exp ? reinterpret_cast<int*>(c.ws + L.guard) + k : nullptr;
     if (count_here) {
       p.clear_st = c.st;
       p.cnt = with_grad ? reinterpret_cast<int*>(c.ws + c.L.dh_cnt) : nullptr;
       p.ncnt = with_grad ? c.L.dh_ncnt : 0;
     }
-    float* Z = with_grad ? reinterpret_cast<float*>(c.ws + T.Z) : nullptr;
-    LCE_TRY(tok_logits(c, c0, rows, Z ? lce::TOK_STATS_Z : lce::TOK_STATS, Z, T.ldz, p));
+    float* Z = with_grad && !L.exp ? reinterpret_cast<float*>(c.ws + T.Z) : nullptr;
+    if (L.exp)
+      LCE_TRY(exp_tile(c, L, c0, rows, p, guard, 0));
+    else
+      LCE_TRY(tok_logits(c, c0, rows, Z ? lce::TOK_STATS_Z : lce::TOK_STATS, Z, T.ldz, p));
     lce::PolicyArgs a;
     std::memset(&a, 0, sizeof a);
-    a.row = loss_row(c, T, c0, p, Z, with_grad, dW != nullptr);
+    a.row = loss_row(c, T, c0, p, Z, with_grad, dW != nullptr, 0);
     a.row.logp = logp + c0;
+    if (L.exp) {
+      loss_row_exp(&a.row, c, L, guard, 0);
+      a.row.stats = reinterpret_cast<float2*>(c.ws + T.stats);
+    }
     a.advantages = advantages + c0;
     a.old_logp = old_logp ? old_logp + c0 : nullptr;
     a.ref_logp = policy->kl != LCE_KL_NONE ? ref_logp + c0 : nullptr;
@@ -1599,8 +1674,9 @@ int policy_loss(const void* H, const void* W, const int64_t* y, int64_t N, int64
     a.mean = o.reduction == LCE_MEAN ? 1 : 0;
     a.n_override = o.n_valid_override;
     a.N = N;
-    LCE_TRY(timed(c.s, K_COMBINE, loss_row_bytes(c, rows, with_grad),
+    LCE_TRY(timed(c.s, K_COMBINE, loss_row_bytes(c, rows, with_grad, Z != nullptr),
                   [&] { return cuda_rc(lce::launch_policy_row(a, static_cast<int>(rows), c.s)); }));
+    if (L.exp) LCE_TRY(exp_fallback(c, c0, rows, p, a.row, guard));
     if (with_grad)
       LCE_TRY(tok_grads(c, T, c0, rows, a.row.rowscale, reinterpret_cast<uint16_t*>(c.ws + c.L.Ht), dH, dW, dW_bf16));
   }
@@ -1643,13 +1719,29 @@ int preference_loss(const void* H, const void* W, const int64_t* y, int64_t N, i
   float2* stats = reinterpret_cast<float2*>(c.ws + L.stats);
   float* coef = reinterpret_cast<float*>(c.ws + L.coef);
   const bool one = N > 0 && c.L.chunks == 1;
-  float* Z = with_grad && one ? reinterpret_cast<float*>(c.ws + T.Z) : nullptr;
-  if (lce::kChecks || N == 0) LCE_TRY(prepare(c, grad_loss));
+  float* Z = with_grad && one && !L.exp ? reinterpret_cast<float*>(c.ws + T.Z) : nullptr;
+  int* guard = L.exp ? reinterpret_cast<int*>(c.ws + L.guard) : nullptr;
+  if (L.exp)
+    LCE_TRY(exp_prepare(c, L, grad_loss));
+  else if (lce::kChecks || N == 0)
+    LCE_TRY(prepare(c, grad_loss));
   if (N == 0 && with_grad) LCE_TRY(zero_dW(c, dW, dW_bf16));
   // every row's log-probability
-  for (int64_t c0 = 0; c0 < N; c0 += c.L.C) {
-    const int64_t rows = (N - c0) < c.L.C ? (N - c0) : c.L.C;
+  for (int64_t k = 0, c0 = 0; c0 < N; ++k, c0 += L.step) {
+    const int64_t rows = (N - c0) < L.step ? (N - c0) : L.step;
     lce::TokParams p = tok_params(c, c0, rows, temperature);
+    if (L.exp) {
+      p.partials += c0 * p.nparts;
+      p.ztgt += c0;
+      LCE_TRY(exp_tile(c, L, c0, rows, p, guard + k, c0));
+      lce::LossRowArgs a = loss_row(c, T, c0, p, nullptr, true, false, c0);
+      a.logp = logp + c0;
+      a.stats = stats + c0;
+      loss_row_exp(&a, c, L, guard + k, c0);
+      LCE_TRY(timed(c.s, K_COMBINE, static_cast<double>(rows) * (8.0 * static_cast<double>(c.L.T) + 28.0),
+                    [&] { return cuda_rc(lce::launch_exp_logp(a, static_cast<int>(rows), c.s)); }));
+      continue;
+    }
     if (!lce::kChecks && c0 == 0) {
       p.clear_st = c.st;
       p.cnt = with_grad ? reinterpret_cast<int*>(c.ws + c.L.dh_cnt) : nullptr;
@@ -1671,7 +1763,7 @@ int preference_loss(const void* H, const void* W, const int64_t* y, int64_t N, i
     a.logp = logp + c0;
     a.stats = stats + c0;
     a.flags = p.flags;
-    LCE_TRY(timed(c.s, K_COMBINE, loss_row_bytes(c, rows, false), [&] { return cuda_rc(lce::launch_score(a, c.s)); }));
+    LCE_TRY(timed(c.s, K_COMBINE, loss_row_bytes(c, rows, false, false), [&] { return cuda_rc(lce::launch_score(a, c.s)); }));
   }
   lce::PairArgs q;
   std::memset(&q, 0, sizeof q);
@@ -1699,12 +1791,13 @@ int preference_loss(const void* H, const void* W, const int64_t* y, int64_t N, i
   q.st = c.st;
   LCE_TRY(timed(c.s, K_COMBINE, 12.0 * static_cast<double>(N) + 28.0 * static_cast<double>(pairs),
                 [&] { return cuda_rc(lce::launch_pairs(q, c.s)); }));
-  for (int64_t c0 = 0; with_grad && c0 < N; c0 += c.L.C) {
-    const int64_t rows = (N - c0) < c.L.C ? (N - c0) : c.L.C;
+  for (int64_t k = 0, c0 = 0; with_grad && c0 < N; ++k, c0 += L.step) {
+    const int64_t rows = (N - c0) < L.step ? (N - c0) : L.step;
+    const int64_t at = L.exp ? c0 : 0;
     lce::TokParams p = tok_params(c, c0, rows, temperature);
     lce::PreferenceArgs a;
     std::memset(&a, 0, sizeof a);
-    a.row = loss_row(c, T, c0, p, Z, true, dW != nullptr);
+    a.row = loss_row(c, T, c0, p, Z, true, dW != nullptr, at);
     a.row.logp = logp + c0;
     a.row.stats = stats + c0;
     a.row.a = reinterpret_cast<float*>(c.ws + L.a);
@@ -1713,8 +1806,16 @@ int preference_loss(const void* H, const void* W, const int64_t* y, int64_t N, i
     a.cu32 = cu32;
     a.P = pairs;
     a.coef = coef;
-    LCE_TRY(timed(c.s, K_COMBINE, loss_row_bytes(c, rows, Z != nullptr),
+    if (L.exp) loss_row_exp(&a.row, c, L, guard + k, at);
+    LCE_TRY(timed(c.s, K_COMBINE, static_cast<double>(rows) * (4.0 * static_cast<double>(d) + (Z ? 6.0 * static_cast<double>(V) : 0.0)),
                   [&] { return cuda_rc(lce::launch_preference_row(a, static_cast<int>(rows), c.s)); }));
+    if (L.exp) {  // the tiles of all rows are there: one backward launch behind the last of them
+      LCE_TRY(exp_fallback(c, c0, rows, p, a.row, guard + k));
+      if (c0 + rows < N) continue;
+      LCE_TRY(tok_grads(c, T, 0, N, reinterpret_cast<float*>(c.ws + c.L.alpha), reinterpret_cast<uint16_t*>(c.ws + c.L.Ht),
+                        dH, dW, dW_bf16));
+      break;
+    }
     if (!Z) {
       p.stats = stats + c0;
       p.g_logp = a.row.a;

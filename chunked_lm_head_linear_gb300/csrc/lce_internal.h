@@ -249,6 +249,7 @@ enum TokMode : int {
   TOK_STATS = 0,    // partial sums of each (row, half tile) and the label's logit
   TOK_STATS_Z = 1,  // the partial sums and the fp32 logits
   TOK_GRAD = 2,     // gradient tile of log-probability and entropy
+  TOK_EXP = 3,      // exp tile exp((z - z_y) / T) of the label's logit z_y in bf16, and its sums
 };
 
 constexpr int kMaxTop = 128;  // most alternatives of a row, most teacher entries of a row
@@ -275,7 +276,15 @@ struct TokParams {
   int* cnt;
   int ncnt;
   int no_loads;          // timeout test only: no operand is loaded, so the waits run out
+  const float* ref;      // [rows] the labels' logits (TOK_EXP; the next two too)
+  float* sums;           // [rows, nparts] sums of the exp tile, the label's column left out
+  int* guard;            // set to 1 where a sum of a row with a given token is not below kExpGuard
+  const int* only_if;    // not null: the launch does nothing unless *only_if != 0 (TOK_STATS, TOK_GRAD)
 };
+
+// An exp tile is used while its half tiles' sums stay below this: entries and sums are then finite, and what
+// they are scaled by, 1 / (1 + their sum), is a normal number.
+constexpr float kExpGuard = 1.0e26f;
 
 struct TokScoreArgs {
   int rows, V, nparts, K;
@@ -389,6 +398,10 @@ struct LossRowArgs {
   float* label;            // [rows] out: the label's entry of the tile
   float* a;                // [rows] out: the upstream factor that a gradient epilogue reads, or null
   DevStatus* st;
+  // from the exp tile (sums not null): used where *guard == 0, else the row comes from partials and ztgt
+  const float* sums;       // [rows, nparts]
+  const int* guard;
+  float* rest;             // [rows] sum of exp((z_v - z_y)/T) over v != y: out, then in (preference)
 };
 
 struct PolicyArgs {
@@ -439,6 +452,11 @@ struct PreferenceArgs {
   const float* coef;       // [2 P]
 };
 
+// The labels' logits z_{i,y_i} of N rows (0 where none is given).
+cudaError_t launch_label_logits(const void* H, const void* W, const int64_t* y, long long N, int d, int V,
+                                long long ignore_index, float* z, cudaStream_t s);
+// Preference loss from the exp tile: logp, and rest or (where *guard is set) stats.
+cudaError_t launch_exp_logp(const LossRowArgs& p, int rows, cudaStream_t s);
 cudaError_t launch_policy_row(const PolicyArgs& p, int rows, cudaStream_t s);
 cudaError_t launch_pairs(const PairArgs& p, cudaStream_t s);
 cudaError_t launch_preference_row(const PreferenceArgs& p, int rows, cudaStream_t s);

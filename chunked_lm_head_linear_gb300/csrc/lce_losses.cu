@@ -7,6 +7,17 @@
 // partial sums, the gradient tile over the row's scale (lce_rows.cuh) and the
 // backward GEMMs. A policy row knows its factor as soon as its log-probability
 // is known; a pair's factor needs all rows of its two sequences.
+//
+// Two ways to the gradient tile. Small calls keep the fp32 logits and write the
+// tile in a pass over them. Large ones never store logits: the label's logit z_y
+// is a product of two rows, known before the GEMM, so that its epilogue can write
+// E_v = exp((z_v - z_y)/T) in bf16 at once. With R the sum of E over v != y
+//   logp = -log1p(R),  p_v = E_v / (1 + R),  G_v = -(a / T) / (1 + R) (E_v, at y: -R)
+// so E with -R in the label's place is the tile, the factor the row's scale, and
+// neither p_y near 1 (R keeps its relative precision) nor a far label loses
+// anything as long as the sums are finite. Where one is not (a label more than 60
+// nats below its row's maximum, at T = 1), a guard turns on three launches that
+// otherwise return at once: exact statistics, and the exact gradient tile.
 #include "lce_rows.cuh"
 
 namespace lce {
@@ -32,6 +43,39 @@ __device__ __forceinline__ RowStats merge_row(const LossRowArgs& p, int r, float
   if ((tid & 31) == 0) sums[tid >> 5] = acc;
   __syncthreads();
   return RowStats{M, log_sum(add_groups(sums))};
+}
+
+// Sum of a row of the exp tile without its label, in a fixed order.
+__device__ __forceinline__ float exp_rest(const LossRowArgs& p, int r, float* red) {
+  const float* pr = p.sums + static_cast<long long>(r) * p.nparts;
+  float s = 0.f;
+  for (int t = threadIdx.x; t < p.nparts; t += kRowThreads) s += pr[t];
+  return block_sum(s, red);
+}
+
+// The row's scale, the label's entry of the exp tile and the row of dW's second operand. The entry is
+// rounded to bf16; the scale makes up for that, as the label's is as a rule the row's largest share.
+__device__ __forceinline__ void exp_gradient(const LossRowArgs& p, int r, int y, float a, float rest) {
+  const int tid = threadIdx.x;
+  const __nv_bfloat16 label = __float2bfloat16_rn(rest);
+  const float held = __bfloat162float(label);
+  float scale = -a * p.inv_t / (1.f + rest);
+  if (held >= 1.0e-30f) scale *= rest / held;
+  if (tid == 0) {
+    p.rowscale[r] = scale;
+    if (y >= 0 && in_bounds(y, p.ldg, &p.st->flags)) p.G[static_cast<long long>(r) * p.ldg + y] = __hneg(label);
+  }
+  if (p.Ht != nullptr) {
+    const int groups = p.d / 8;
+    const long long at = static_cast<long long>(r) * groups;
+    scale_row(p.H + at, p.Ht + at, groups, scale, a != 0.f, tid, kRowThreads);
+  }
+}
+
+// The label of row r, -1 where none is given.
+__device__ __forceinline__ int given_label(const int64_t* y, long long r, long long ignore_index, int V) {
+  const long long v = y[r];
+  return v != ignore_index && v >= 0 && v < V ? static_cast<int>(v) : -1;
 }
 
 // The row's scale, its row of dW's second operand and of the gradient tile (TILE), for the factor a.
@@ -61,12 +105,6 @@ __device__ __forceinline__ void row_gradient(const LossRowArgs& p, int r, int y,
   g.keep = u.a == 0.f ? 0u : ~0u;
   write_grad_row(g, label, p.Z + static_cast<long long>(r) * p.ldz, p.G + static_cast<long long>(r) * p.ldg, p.V, tid,
                  kRowThreads);
-}
-
-// The label of row r, -1 where none is given.
-__device__ __forceinline__ int given_label(const int64_t* y, long long r, long long ignore_index, int V) {
-  const long long v = y[r];
-  return v != ignore_index && v >= 0 && v < V ? static_cast<int>(v) : -1;
 }
 
 // Sum of n floats in fp64, in an order that depends on n alone.
@@ -134,8 +172,8 @@ __device__ __forceinline__ void policy_row(const PolicyArgs& p, int r, float log
   a *= w;
 }
 
-// One block per row of the chunk.
-template <bool GRAD, bool TILE>
+// One block per row of the chunk. EXP: from the exp tile, or, where its guard is set, from the partial sums.
+template <bool GRAD, bool TILE, bool EXP>
 __global__ void __launch_bounds__(kRowThreads, 8) k_policy_row(const PolicyArgs p) {
   grid_dep_wait();
   grid_dep_launch();
@@ -145,12 +183,18 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_policy_row(const PolicyArgs 
   const int r = blockIdx.x, tid = threadIdx.x;
   const LossRowArgs& q = p.row;
   const int y = given_label(q.y, r, q.ignore_index, q.V);
-  float logp = 0.f, row = 0.f, a = 0.f;
+  float logp = 0.f, row = 0.f, a = 0.f, rest = 0.f;
   RowStats s{0.f, 0.f};
+  const bool by_exp = EXP && *q.guard == 0;
   if (y >= 0) {
-    s = merge_row(q, r, red, s_sum);
-    const float z = q.Z != nullptr ? q.Z[static_cast<long long>(r) * q.ldz + y] : q.ztgt[r];
-    logp = (z - s.M) * q.inv_t - s.logs;
+    if (by_exp) {
+      rest = exp_rest(q, r, red);
+      logp = -log1pf(rest);
+    } else {
+      s = merge_row(q, r, red, s_sum);
+      const float z = q.Z != nullptr ? q.Z[static_cast<long long>(r) * q.ldz + y] : q.ztgt[r];
+      logp = (z - s.M) * q.inv_t - s.logs;
+    }
     policy_row(p, r, logp, row, a);
   }
   if (tid == 0) {
@@ -162,7 +206,12 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_policy_row(const PolicyArgs 
       if (y < 0 && q.y[r] != q.ignore_index) atomicOr(&q.st->flags, kFlagLabelRange);
     }
   }
-  if (GRAD) row_gradient<TILE>(q, r, y, a, logp, s);
+  if (GRAD) {
+    if (by_exp)
+      exp_gradient(q, r, y, a, rest);
+    else
+      row_gradient<TILE>(q, r, y, a, logp, s);
+  }
   if (p.loss == nullptr) return;
   if (!last_block(q.st, static_cast<int>(p.N))) return;
   const double sum = block_total(p.row_loss, p.N, s_total);
@@ -283,8 +332,34 @@ __device__ __forceinline__ long long sequence_of(const void* cu, int cu32, long 
   return lo - 1;
 }
 
+// The rows' log-probabilities from the exp tile, with what the gradient needs of them again.
+__global__ void __launch_bounds__(kRowThreads, 8) k_exp_logp(const LossRowArgs p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  __shared__ float red[kRowThreads / 32];
+  __shared__ RowSum s_sum[kGroups];
+  const int r = blockIdx.x;
+  const int y = given_label(p.y, r, p.ignore_index, p.V);
+  float logp = 0.f, rest = 0.f;
+  RowStats s{0.f, 0.f};
+  if (y >= 0) {
+    if (*p.guard == 0) {
+      rest = exp_rest(p, r, red);
+      logp = -log1pf(rest);
+    } else {
+      s = merge_row(p, r, red, s_sum);
+      logp = (p.ztgt[r] - s.M) * p.inv_t - s.logs;
+    }
+  }
+  if (threadIdx.x == 0) {
+    p.logp[r] = logp;
+    p.rest[r] = rest;
+    p.stats[r] = make_float2(s.M, s.logs);
+  }
+}
+
 // One block per row of the chunk, once the pairs' factors are known.
-template <bool TILE>
+template <bool TILE, bool EXP>
 __global__ void __launch_bounds__(kRowThreads, 8) k_preference_row(const PreferenceArgs p) {
   grid_dep_wait();
   grid_dep_launch();
@@ -296,17 +371,62 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_preference_row(const Prefere
     const long long s = sequence_of(p.cu, p.cu32, 2 * p.P, p.c0 + r);
     if (s >= 0 && s < 2 * p.P) a = p.coef[s];
   }
+  if (EXP && *q.guard == 0) {
+    exp_gradient(q, r, y, a, q.rest[r]);
+    return;
+  }
   const float2 st = q.stats[r];
   row_gradient<TILE>(q, r, y, a, q.logp[r], RowStats{st.x, st.y});
 }
 
+// One warp per row: H_i . W_{y_i} in fp32.
+__global__ void __launch_bounds__(256) k_label_logits(const uint4* __restrict__ H, const uint4* __restrict__ W,
+                                                      const int64_t* __restrict__ y, long long N, int groups, int V,
+                                                      long long ignore_index, float* __restrict__ z) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const long long r = (blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  if (r >= N) return;
+  const int v = given_label(y, r, ignore_index, V);
+  float s = 0.f;
+  if (v >= 0) {
+    const uint4 *h = H + r * groups, *w = W + static_cast<long long>(v) * groups;
+#pragma unroll 4
+    for (int i = lane; i < groups; i += 32) {
+      const uint4 a = h[i], b = w[i];
+      const uint32_t x[4] = {a.x, a.y, a.z, a.w}, u[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        s = fmaf(__uint_as_float(x[q] << 16), __uint_as_float(u[q] << 16), s);
+        s = fmaf(__uint_as_float(x[q] & 0xffff0000u), __uint_as_float(u[q] & 0xffff0000u), s);
+      }
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  if (lane == 0) z[r] = s;
+}
+
 }  // namespace
+
+cudaError_t launch_label_logits(const void* H, const void* W, const int64_t* y, long long N, int d, int V,
+                                long long ignore_index, float* z, cudaStream_t s) {
+  if (N <= 0) return cudaSuccess;
+  return launch_k(k_label_logits, static_cast<unsigned>((N + 7) / 8), 256, 0, s, static_cast<const uint4*>(H),
+                  static_cast<const uint4*>(W), y, N, d / 8, V, ignore_index, z);
+}
+
+cudaError_t launch_exp_logp(const LossRowArgs& p, int rows, cudaStream_t s) {
+  if (rows <= 0) return cudaSuccess;
+  return launch_k(k_exp_logp, rows, kRowThreads, 0, s, p);
+}
 
 cudaError_t launch_policy_row(const PolicyArgs& p, int rows, cudaStream_t s) {
   if (rows <= 0) return cudaSuccess;
-  if (p.row.rowscale == nullptr) return launch_k(k_policy_row<false, false>, rows, kRowThreads, 0, s, p);
-  return p.row.Z != nullptr ? launch_k(k_policy_row<true, true>, rows, kRowThreads, 0, s, p)
-                            : launch_k(k_policy_row<true, false>, rows, kRowThreads, 0, s, p);
+  if (p.row.rowscale == nullptr) return launch_k(k_policy_row<false, false, false>, rows, kRowThreads, 0, s, p);
+  return p.row.sums != nullptr ? launch_k(k_policy_row<true, false, true>, rows, kRowThreads, 0, s, p)
+                               : launch_k(k_policy_row<true, true, false>, rows, kRowThreads, 0, s, p);
 }
 
 cudaError_t launch_pairs(const PairArgs& p, cudaStream_t s) {
@@ -315,8 +435,9 @@ cudaError_t launch_pairs(const PairArgs& p, cudaStream_t s) {
 
 cudaError_t launch_preference_row(const PreferenceArgs& p, int rows, cudaStream_t s) {
   if (rows <= 0) return cudaSuccess;
-  return p.row.Z != nullptr ? launch_k(k_preference_row<true>, rows, kRowThreads, 0, s, p)
-                            : launch_k(k_preference_row<false>, rows, kRowThreads, 0, s, p);
+  if (p.row.sums != nullptr) return launch_k(k_preference_row<false, true>, rows, kRowThreads, 0, s, p);
+  return p.row.Z != nullptr ? launch_k(k_preference_row<true, false>, rows, kRowThreads, 0, s, p)
+                            : launch_k(k_preference_row<false, false>, rows, kRowThreads, 0, s, p);
 }
 
 }  // namespace lce

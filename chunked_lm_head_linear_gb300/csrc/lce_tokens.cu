@@ -93,6 +93,11 @@ __device__ __forceinline__ void add_columns(Mst& a, float (&v)[32], float inv_t)
 //                  G_v = ([v = y] a - p_v (a + e (z'_v - lse + entropy))) / T
 //                rounded to bf16 once (the operand type of the two GEMMs that
 //                follow), everything before it in fp32.
+//   TOK_EXP      E_v = exp((z_v - z_y)/T) in bf16 against the label's logit, known
+//                before the GEMM, and the sums of E without the label's column: with
+//                R their sum logp = -log1p(R) and p_v = E_v / (1 + R), so that the
+//                tile is the gradient's up to a factor per row and nothing needs the
+//                logits again. A sum that is too large, or NaN, sets the guard.
 // ----------------------------------------------------------------------------
 __device__ __forceinline__ void clear_status(DevStatus* st, int* cnt, int ncnt, int thread, int threads) {
   for (int i = thread; i < ncnt; i += threads) cnt[i] = 0;
@@ -195,6 +200,74 @@ struct TokEpi {
     if (MODE == TOK_STATS && have_t) p.ztgt[r] = zt;
   }
 
+  // 32 columns c0.. of the exp tile into half `hh` of the staged 64; their sum is added to s.
+  static __device__ __forceinline__ void exp_group(const EpiCtx& ctx, float (&v)[32], int c0, int hh, int vlim, int ycol,
+                                                   float z, float k, uint32_t keep, uint64_t (&s)[2]) {
+    if (vlim < c0 + 32) {
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        if (c0 + c >= vlim) v[c] = kMasked;
+    }
+    const int yo = ycol - c0;
+    if (yo >= 0 && yo < 32) {  // the label's own column has no part in the sum; its entry is written later
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        if (c == yo) v[c] = kMasked;
+    }
+    const uint64_t z2 = pair_f32(-z, -z), k2 = pair_f32(k, k);
+    uint32_t pk[16];
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+      float x0, x1;
+      unpair_f32(mul_pair(add_pair(pair_f32(v[c], v[c + 1]), z2), k2), x0, x1);
+      const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
+      s[(c / 2) & 1] = add_pair(s[(c / 2) & 1], pair_f32(e0, e1));
+      pk[c / 2] = pack_bf16x2(e0, e1) & keep;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<uint4*>(ctx.stage + stage_off(ctx.lane, hh * 4 + q)) =
+          make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+  }
+
+  static __device__ __forceinline__ void exp_tile(const Params& p, const EpiCtx& ctx, int m0, int col0, uint32_t taddr) {
+    const int r = m0 + ctx.row0 + ctx.lane;
+    const int vlim = p.V - col0, part = col0 / EPI_COLS;
+    if (m0 + ctx.row0 >= p.rows) return;  // no row of this warp
+    const bool live = r < p.rows;
+    const long long y = live ? static_cast<long long>(p.y[r]) : p.ignore_index;
+    const bool given = live && y != p.ignore_index && y >= 0 && y < p.V;
+    float sum = 0.f;
+    if (vlim > 0) {
+      const long long yc = y - col0;
+      const int ycol = given && yc >= 0 && yc < EPI_COLS ? static_cast<int>(yc) : -1;
+      const float z = given ? p.ref[r] : 0.f, k = p.inv_t * kLog2e;
+      const uint32_t keep = given ? ~0u : 0u;  // rows without a token are zero whatever they hold
+      uint64_t s[2] = {0, 0};
+      float va[32], vb[32];
+      tmem_ld_issue_x32(taddr, va);
+#pragma unroll 1
+      for (int c0 = 0; c0 < EPI_COLS; c0 += 64) {  // two groups of 32 columns in flight, a staged tile of 64
+        if (c0 >= vlim) break;
+        tmem_ld_wait(va);
+        tmem_ld_issue_x32(taddr + c0 + 32, vb);
+        stage_acquire(ctx);
+        exp_group(ctx, va, c0, 0, vlim, ycol, z, k, keep, s);
+        tmem_ld_wait(vb);
+        if (c0 + 64 < EPI_COLS) tmem_ld_issue_x32(taddr + c0 + 64, va);
+        exp_group(ctx, vb, c0 + 32, 1, vlim, ycol, z, k, keep, s);
+        stage_release(ctx, col0 + c0, m0 + ctx.row0, false);
+      }
+      tmem_ld_wait(va);  // a load that a break left under way
+      float s0, s1;
+      unpair_f32(add_pair(s[0], s[1]), s0, s1);
+      sum = s0 + s1;
+    }
+    if (!live || !in_bounds(part, p.nparts, p.flags)) return;
+    p.sums[static_cast<long long>(r) * p.nparts + part] = sum;
+    if (given && !(sum <= kExpGuard)) *p.guard = 1;
+  }
+
   static __device__ __forceinline__ void grad_tile(const Params& p, const EpiCtx& ctx, int m0, int col0,
                                                    uint32_t taddr) {
     const int r = m0 + ctx.row0 + ctx.lane;
@@ -244,7 +317,7 @@ struct TokProb {
     TokParams ep;
   };
   struct State {};
-  static __device__ __forceinline__ bool skip(const Params&) { return false; }
+  static __device__ __forceinline__ bool skip(const Params& p) { return p.ep.only_if != nullptr && *p.ep.only_if == 0; }
   static __device__ __forceinline__ bool no_loads(const Params& p) { return p.ep.no_loads != 0; }
   static __device__ __forceinline__ int* flags(const Params& p) { return p.ep.flags; }
   static __device__ __forceinline__ int num_jobs(const Params& p, int c, int P) {
@@ -272,6 +345,8 @@ struct TokProb {
     ctx.out = &p.c;
     if constexpr (MODE == TOK_GRAD)
       TokEpi<MODE>::grad_tile(p.ep, ctx, m0, col0, taddr);
+    else if constexpr (MODE == TOK_EXP)
+      TokEpi<MODE>::exp_tile(p.ep, ctx, m0, col0, taddr);
     else
       TokEpi<MODE>::stats_tile(p.ep, ctx, m0, col0, taddr);
   }
@@ -1110,6 +1185,7 @@ cudaError_t launch_tok_logits(int mode, const CUtensorMap& a, const CUtensorMap&
   switch (mode) {
     case TOK_STATS: return launch_tok_mode<TOK_STATS>(a, b, c, M, N, K, ep, num_sms, s);
     case TOK_STATS_Z: return launch_tok_mode<TOK_STATS_Z>(a, b, c, M, N, K, ep, num_sms, s);
+    case TOK_EXP: return launch_tok_mode<TOK_EXP>(a, b, c, M, N, K, ep, num_sms, s);
     default: return launch_tok_mode<TOK_GRAD>(a, b, c, M, N, K, ep, num_sms, s);
   }
 }

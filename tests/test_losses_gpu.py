@@ -19,7 +19,11 @@ eps = 2^-24 and u = 2^-8:
              |slope| td (+ td^2 for ipo) + 2^-22 |loss|
   gradients  each entry of G is rounded to bf16 once (u) behind factors that err by less
              than 2^-10; dW's other operand bf16(scale H) is rounded as well: (2 u + u^2
-             + 2^-10) bulk; dH (u + 2^-10) bulk and its own rounding; whole tensors 5e-3
+             + 2^-10) bulk; dH (u + 2^-10) bulk and its own rounding; whole tensors 5e-3.
+             From exp tiles (large calls) an entry is rounded (u) and its row's scale
+             times rest / bf16(rest), which makes up for the rounding of the label's
+             entry -bf16(rest) and is itself off 1 by at most u: (1 + u)^2 - 1 = 2 u + u^2
+             for dH, with bf16(scale H) (1 + u)^3 - 1 = 3 u + 3 u^2 + u^3 for dW
   loss       the rows' (pairs') bounds summed, and eps |loss|
   layer norm a sum of d terms in fp32 over lanes and five shuffles errs by g = (d / 32 +
              16) eps of its absolute terms: the mean by em = g mean|x|, the variance by 2
@@ -62,11 +66,15 @@ def head(H, W, y, T):
     return logp, told, 2 * tol_lse(H, W, lse, T)
 
 
-def check_gradients(dH, dW, ref, slack):
+def uses_exp_tiles(N, V, chunk):
+    return min(N, chunk or N) > 96 and min(N, chunk or N) * V >= 16_000_000
+
+
+def check_gradients(dH, dW, ref, slack, exp=False):
     for got, name in ((dH, "dH"), (dW, "dW")):
         if got is None:
             continue
-        rounding = U if name == "dH" else 2 * U + U * U
+        rounding = (1 + U) ** ((1 if name == "dH" else 2) + (1 if exp else 0)) - 1
         out = U * np.abs(ref[name]) if got.dtype == _torch().bfloat16 else 0.0
         close(got, ref[name], (rounding + 2.0 ** -10) * ref[name + "_bulk"] + slack[name + "_bulk"] + out + 1e-30, name)
         norm = np.linalg.norm(ref[name])
@@ -96,7 +104,7 @@ def call_policy(lce, Ht, Wt, yt, inp, grad=True, **kw):
     return lce.lce_policy_forward(Ht, Wt, yt, *args[:3], weights=args[3], **kw)
 
 
-def check_policy(out, H, W, y, inp, *, T=1.0, ignore=-100, **kw):
+def check_policy(out, H, W, y, inp, *, T=1.0, ignore=-100, chunk=0, **kw):
     reduction = dict(mean=oracle.MEAN, sum=1)[kw.pop("reduction", "mean")]
     args = [None if inp[k] is None else np.nan_to_num(inp[k].astype(np.float64)) for k in
             ("advantages", "old_logp", "ref_logp", "weights")]
@@ -130,7 +138,7 @@ def check_policy(out, H, W, y, inp, *, T=1.0, ignore=-100, **kw):
     if len(out) == 5:
         slack = oracle.head_gradients_f64(H, W, y, a_tol * weight * abs(scale_kw.get("grad_loss", 1.0)), temperature=T,
                                           ignore_index=ignore)
-        check_gradients(out[3], out[4], ref, slack)
+        check_gradients(out[3], out[4], ref, slack, uses_exp_tiles(*H.shape[:1], W.shape[0], chunk))
     return ref
 
 
@@ -149,6 +157,12 @@ POLICY_CASES = [
     (513, 264, 1000, 0.9, 200, "none", True, False, 0.0),
     (700, 128, 20011, 1.0, 0, "k3", True, True, 3.0),
     (1000, 512, 9000, 1.0, 0, "k3", False, True, 0.0),
+    # enough logits for exp tiles
+    (97, 64, 250007, 1.0, 0, "k3", True, True, 0.0),
+    (300, 136, 80101, 0.8, 0, "k2", True, True, 3.0),
+    (501, 64, 100003, 1.0, 250, "k3", True, False, 0.0),   # three chunks, the last of one row
+    (400, 64, 65537, 1.0, 0, "none", False, True, 0.0),
+    (300, 64, 80101, 0.1, 0, "k3", True, True, 0.0),       # labels far below the largest logit: exact tiles
 ]
 
 
@@ -161,7 +175,7 @@ def test_policy(cuda_lib, N, d, V, T, chunk, kl, old, weights, dual):
     kw = dict(clip_low=0.2, clip_high=0.28, dual_clip=dual, kl=kl, kl_coef=0.0 if kl == "none" else 0.3)
     for dt in (torch.float32, torch.bfloat16):
         out = call_policy(cuda_lib, Ht, Wt, dev(y), inp, temperature=T, chunk_tokens=chunk, dW_dtype=dt, sync_check=True, **kw)
-        check_policy(out, H, W, y, inp, T=T, **kw)
+        check_policy(out, H, W, y, inp, T=T, chunk=chunk, **kw)
     fwd = call_policy(cuda_lib, Ht, Wt, dev(y), inp, grad=False, temperature=T, chunk_tokens=chunk, sync_check=True, **kw)
     check_policy(fwd, H, W, y, inp, T=T, **kw)
     again = call_policy(cuda_lib, Ht, Wt, dev(y), inp, temperature=T, chunk_tokens=chunk, dW_dtype=torch.bfloat16, **kw)
@@ -294,7 +308,7 @@ def call_preference(lce, Ht, Wt, y, cu, ref, grad=True, **kw):
     return lce.lce_preference_forward(Ht, Wt, dev(y), dev(cu), r, **kw)
 
 
-def check_preference(out, H, W, y, cu, ref_logp, *, T=1.0, average=False, **kw):
+def check_preference(out, H, W, y, cu, ref_logp, *, T=1.0, average=False, chunk=0, **kw):
     reduction = dict(mean=oracle.MEAN, sum=1)[kw.pop("reduction", "mean")]
     rl = None if ref_logp is None else f32(ref_logp).astype(np.float64)
     ref = oracle.preference_f64(H, W, y, cu, rl, temperature=T, average=average, reduction=reduction, **kw)
@@ -333,7 +347,7 @@ def check_preference(out, H, W, y, cu, ref_logp, *, T=1.0, average=False, **kw):
             a[cu[s]:cu[s + 1]] = (slope_tol[s // 2] + 2.0 ** -22 * abs(slope[s // 2])) * per[s] * weight
         a = np.where(told, a, 0.0) * abs(kw.get("grad_loss", 1.0))
         slack = oracle.head_gradients_f64(H, W, y, a, temperature=T)
-        check_gradients(out[3], out[4], ref, slack)
+        check_gradients(out[3], out[4], ref, slack, uses_exp_tiles(len(y), W.shape[0], chunk))
         outside = np.ones(len(y), bool)
         outside[cu[0]:cu[-1]] = False
         if out[3] is not None:
@@ -354,6 +368,12 @@ PREFERENCE_CASES = [
     (513, 264, 1000, 20, 0.9, 200, "hinge", False, True),
     (700, 128, 20011, 3, 1.0, 0, "sigmoid", False, True),
     (600, 64, 700, 290, 1.0, 0, "sigmoid", False, True),    # sequences of a token or none
+    # enough logits for exp tiles
+    (97, 64, 250007, 2, 1.0, 0, "sigmoid", False, True),
+    (300, 136, 80101, 4, 0.8, 0, "ipo", True, True),
+    (501, 64, 100003, 3, 1.0, 250, "hinge", False, True),   # three chunks: the logits are computed twice
+    (6200, 64, 7301, 5, 1.0, 0, "sigmoid", True, False),    # exp tiles of two launches, kept for one backward
+    (300, 64, 80101, 3, 0.1, 0, "sigmoid", True, True),     # labels far below the largest logit: exact tiles
 ]
 
 
@@ -377,7 +397,7 @@ def test_preference(cuda_lib, N, d, V, pairs, T, chunk, kind, average, ref, int3
     c = cu.astype(np.int32) if int32 else cu
     for dt in (torch.float32, torch.bfloat16):
         out = call_preference(cuda_lib, Ht, Wt, y, c, rl, temperature=T, chunk_tokens=chunk, dW_dtype=dt, sync_check=True, **kw)
-        check_preference(out, H, W, y, cu, rl, T=T, **kw)
+        check_preference(out, H, W, y, cu, rl, T=T, chunk=chunk, **kw)
     fwd = call_preference(cuda_lib, Ht, Wt, y, c, rl, grad=False, temperature=T, chunk_tokens=chunk, sync_check=True, **kw)
     check_preference(fwd, H, W, y, cu, rl, T=T, **kw)
     again = call_preference(cuda_lib, Ht, Wt, y, c, rl, temperature=T, chunk_tokens=chunk, dW_dtype=torch.bfloat16, **kw)
@@ -459,6 +479,86 @@ def test_preference_bad_bounds_no_pairs_and_no_rows(cuda_lib):
         inp = dict(advantages=f32([]), old_logp=None, ref_logp=None, weights=None)
         out = call_policy(cuda_lib, Ht[:0], Wt, dev(y[:0]), inp, dW_dtype=dt, sync_check=True)
         assert out[0].item() == 0 and out[3].shape == (0, 64) and not out[4].any()
+
+
+# --------------------------------------------------------------------------- exp tiles
+def test_exp_tiles_masked_rows_of_nan(cuda_lib):
+    """Masked and weightless rows may hold NaN where exp tiles are used; a given row of NaN has a loss of NaN and leaves
+    the other rows' dH alone."""
+    torch = _torch()
+    N, V = 300, 80101
+    rng, H, W, y = make(N, 64, V)
+    Ht, Wt = heads(H, W)
+    inp = policy_inputs(rng, H, W, y, 1.0, "none")
+    masked = torch.from_numpy(y < 0).cuda()
+    clean = call_policy(cuda_lib, Ht, Wt, dev(y), inp)
+    bad = Ht.clone()
+    bad[masked] = float("nan")
+    for a, b in zip(call_policy(cuda_lib, bad, Wt, dev(y), inp, sync_check=True), clean):
+        assert torch.equal(a, b)
+    cu = bounds(rng, N, 3, 4, 9)
+    clean = call_preference(cuda_lib, Ht, Wt, y, cu, None)
+    for a, b in zip(call_preference(cuda_lib, bad, Wt, y, cu, None, sync_check=True), clean):
+        assert torch.equal(a, b)
+    # a weight of 0, or no sequence, on a row with a given token: the exact tiles take over
+    row = int(np.flatnonzero(y >= 0)[3])
+    inp["weights"] = f32(np.ones(N))
+    inp["weights"][row] = 0.0
+    bad[row] = float("nan")
+    got = call_policy(cuda_lib, bad, Wt, dev(y), inp, sync_check=True)
+    zero = Ht.clone()
+    zero[row] = 0
+    want = call_policy(cuda_lib, zero, Wt, dev(y), inp)
+    assert got[2][row] == 0 and not got[3][row].any() and torch.isfinite(got[4]).all()
+    assert torch.linalg.vector_norm(got[4] - want[4]) <= 5e-3 * torch.linalg.vector_norm(want[4])
+    assert torch.linalg.vector_norm((got[3] - want[3]).float()) <= 5e-3 * torch.linalg.vector_norm(want[3].float())
+    inp["weights"][row] = 1.0
+    got = call_policy(cuda_lib, bad, Wt, dev(y), inp)
+    rest = torch.arange(N, device="cuda") != row
+    assert got[0].isnan().all() and got[2][row].isnan() and torch.isfinite(got[3][rest]).all() and got[3][row].isnan().all()
+
+
+@pytest.mark.parametrize("shift", [50.0, 70.0, 200.0])
+def test_exp_tiles_of_one_far_label(cuda_lib, shift):
+    """A single row whose label lies below the other logits, within the tile's range (50 nats) and beyond it."""
+    torch = _torch()
+    N, d, V = 300, 64, 80101
+    rng, H, W, y = make(N, d, V, seed=5)
+    row = int(np.flatnonzero(y >= 0)[10])
+    W[:, 0] = 0.0
+    H[:, 0] = 0.0
+    W[y[row], 0] = -1.0
+    H[row, 0] = shift                       # z_y of this row falls by that much; no other row sees it
+    Ht, Wt = heads(H, W)
+    inp = policy_inputs(rng, H, W, y, 1.0)
+    kw = dict(clip_low=0.2, clip_high=0.28, kl="k3", kl_coef=0.1)
+    check_policy(call_policy(cuda_lib, Ht, Wt, dev(y), inp, sync_check=True, **kw), H, W, y, inp, **kw)
+    cu = bounds(rng, N, 3)
+    check_preference(call_preference(cuda_lib, Ht, Wt, y, cu, None, average=True, sync_check=True), H, W, y, cu, None, average=True)
+
+
+def test_exp_tiles_of_confident_rows(cuda_lib):
+    """A label with nearly all of the probability: logp near 0 and the gradient of 1 - p keep their relative precision."""
+    N, d, V = 300, 64, 80101
+    rng, H, W, _ = make(N, d, V, seed=6, peak=0.0)
+    y = np.full(N, 7)
+    W[:, 0] = 0.0
+    W[7] = 0.0
+    W[7, 0] = 1.0
+    H[:, 0] = np.round(4 * (20.0 + 40.0 * rng.random(N))) / 4    # z_y; the others are below 20: 1 - p from 1e-2 to 1e-18
+    Ht, Wt = heads(H, W)
+    inp = dict(advantages=f32(np.ones(N)), old_logp=None, ref_logp=None, weights=None)
+    _, logp, _, dH, _ = call_policy(cuda_lib, Ht, Wt, dev(y), inp)
+    z = H @ W.T
+    others = np.exp(z - z[:, 7:8])
+    others[:, 7] = 0.0
+    rest = others.sum(axis=1)
+    assert rest.min() < 1e-10
+    np.testing.assert_allclose(np64(logp), -np.log1p(rest), rtol=2.0 ** -15)
+    G = others / (1 + rest)[:, None]
+    G[:, 7] = -rest / (1 + rest)
+    want, bulk = G @ W / N, np.abs(G) @ np.abs(W) / N
+    close(dH, want, (2 * U + U * U + 2.0 ** -10) * bulk + U * np.abs(want), "dH")
 
 
 # --------------------------------------------------------------------------- layer norm
@@ -769,17 +869,17 @@ def _child():
     lce.load(build.build(checks=True))
     torch = _torch()
     for N, d, V, chunk in [(1, 64, 37, 0), (3, 72, 2, 0), (96, 64, 4099, 0), (97, 8, 257, 0), (129, 136, 70001, 64),
-                           (513, 256, 1000, 200), (400, 64, 30001, 0)]:
+                           (513, 256, 1000, 200), (400, 64, 30001, 0), (100, 64, 250007, 0), (300, 64, 100003, 250)]:
         rng, H, W, y = make(N, d, V, seed=N)
         Ht, Wt = heads(H, W)
         inp = policy_inputs(rng, H, W, y, 1.0, "k3")
         kw = dict(clip_low=0.2, clip_high=0.28, kl="k3", kl_coef=0.1)
         for grad in (True, False):
             out = call_policy(lce, Ht, Wt, dev(y), inp, grad=grad, chunk_tokens=chunk, sync_check=True, **kw)
-            check_policy(out, H, W, y, inp, **kw)
+            check_policy(out, H, W, y, inp, chunk=chunk, **kw)
             cu = bounds(rng, N, 2)
             out = call_preference(lce, Ht, Wt, y, cu, None, grad=grad, chunk_tokens=chunk, sync_check=True)
-            check_preference(out, H, W, y, cu, None)
+            check_preference(out, H, W, y, cu, None, chunk=chunk)
         check_norm(lce, Ht, torch.ones(d, device="cuda"), None, Ht)
     print("checked build: ok")
 
