@@ -74,6 +74,7 @@ struct Layout {
   int64_t chunks = 0;  // number of chunks
   size_t status = 0, loss_i = 0, lse = 0, ztgt = 0, partials = 0, P = 0;
   size_t ref = 0, alpha = 0, guard = 0, Ht = 0, total = 0;
+  int dh_parts = 0;                // vocabulary parts of a dH tile; 0: dh_parts_for(V)
   size_t dh_cnt = 0, dh_part = 0;  // dH part counters and part sums (backward calls)
   int dh_ncnt = 0;                 // number of dH part counters
 };
@@ -85,6 +86,10 @@ void take_dh_parts(Layout& L, int64_t d, int64_t V, const std::function<size_t(s
   const int64_t tiles = ceil_div(L.C, 256) * ceil_div(d, 256);
   L.dh_ncnt = static_cast<int>(tiles * 8);
   L.dh_cnt = take(sizeof(int) * static_cast<size_t>(L.dh_ncnt));
+  if (L.dh_parts > 1)  // stored as [parts, rows, d]
+    L.dh_part = take(sizeof(float) * static_cast<size_t>(L.dh_parts) * static_cast<size_t>(ceil_div(L.C, 256) * 256) *
+                     static_cast<size_t>(d));
+  if (L.dh_parts > 0) return;
   const int parts = lce::dh_parts_for(V);
   if (parts > 1) L.dh_part = take(sizeof(float) * 256 * 256 * static_cast<size_t>(tiles) * static_cast<size_t>(parts));
 }
@@ -395,8 +400,12 @@ int dh_dw(const Call& c, int64_t c0, int64_t rows, const float* rowscale, const 
   CUtensorMap mG, mW, mdH, mGt, mB, mdW;
   LCE_TRY(make_map(&mG, P, rows, c.V, c.L.ldp, lce::kBoxRowsK));      // dH: A, K-major
   LCE_TRY(make_map(&mW, c.W, c.V, c.d, c.d, lce::kBoxRowsMN));        // dH: B, N-major
+  const int64_t split_rows = c.L.dh_parts > 1 ? ceil_div(c.L.C, 256) * 256 : 0;  // dH parts stored and added behind the launch
   if (!dH)                                                              // not wanted: no tile stores through it
     mdH = mW;
+  else if (split_rows)
+    LCE_TRY(make_map_t(&mdH, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, c.ws + c.L.dh_part, c.L.dh_parts * split_rows, c.d, c.d, 32u,
+                       kStoreRows));
   else if (dH_f32)                                                      // dH store
     LCE_TRY(make_map_t(&mdH, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, static_cast<float*>(dH) + c0 * c.d, rows, c.d, c.d,
                        32u, kStoreRows));
@@ -418,6 +427,8 @@ int dh_dw(const Call& c, int64_t c0, int64_t rows, const float* rowscale, const 
   dp.ld = c.d;
   dp.rowscale = rowscale;
   dp.st = c.st;
+  dp.parts = c.L.dh_parts;
+  dp.split_rows = static_cast<int>(split_rows);
   dp.part_buf = c.L.dh_part ? reinterpret_cast<float4*>(c.ws + c.L.dh_part) : nullptr;
   dp.part_cnt = reinterpret_cast<int*>(c.ws + c.L.dh_cnt);
   dp.part_slices = c.L.dh_ncnt;
@@ -434,9 +445,15 @@ int dh_dw(const Call& c, int64_t c0, int64_t rows, const float* rowscale, const 
   const double dw_rows = static_cast<double>(v_end - part.v_begin);
   const double flops = 2.0 * static_cast<double>(rows) * static_cast<double>(c.d) *
                        ((part.with_dh ? static_cast<double>(c.V) : 0.0) + dw_rows);
-  return timed(c.s, K_GEMM_BWD, flops, [&] {
+  LCE_TRY(timed(c.s, K_GEMM_BWD, flops, [&] {
     return cuda_rc(lce::launch_backward(mG, mW, mdH, mGt, mB, mdW, rows, c.V, c.d, dp, wp, &c.st->flags,
                                         c.dev.num_sms, c.s, part.v_begin, v_end, part.with_dh));
+  }));
+  if (!split_rows || !dH || !part.with_dh) return LCE_OK;
+  const double bytes = static_cast<double>(rows) * static_cast<double>(c.d) * (4.0 * c.L.dh_parts + 2.0);
+  return timed(c.s, K_OTHER, bytes, [&] {
+    return cuda_rc(lce::launch_dh_sum(reinterpret_cast<const float*>(c.ws + c.L.dh_part), c.L.dh_parts, split_rows, rows,
+                                      static_cast<int>(c.d), rowscale, c.st, static_cast<uint16_t*>(dH) + c0 * c.d, c.s));
   });
 }
 
@@ -1013,10 +1030,11 @@ int64_t tok_chunk(int64_t N, const lce_opts* o) {
 }
 
 TokLayout tok_layout(int64_t N, int64_t d, int64_t V, bool with_z, bool with_grad, bool dW_bf16, bool with_scale,
-                     const lce_opts* o) {
+                     const lce_opts* o, bool balanced_parts = false) {
   TokLayout T;
   Layout& L = T.base;
   L.C = tok_chunk(N, o);
+  if (balanced_parts) L.dh_parts = lce::dh_parts_balanced(L.C, V, d);
   L.T = ceil_div(V, kVocabTile);
   L.ldp = L.T * kVocabTile;
   L.chunks = N > 0 ? ceil_div(N, L.C) : 0;
@@ -1483,12 +1501,15 @@ struct LossLayout {
   size_t ref = 0, sums = 0, guard = 0;          // [N], [C, nparts], [launches]
   size_t logp = 0, stats = 0, a = 0, coef = 0;  // [N], [N] pairs, [C], [2 P]
   size_t rest = 0;                              // [C]
+  size_t row64 = 0;                             // [N] doubles
   size_t total = 0;
 };
 
 // Logits of a chunk from which on the exp tile is the faster way to a gradient tile: the pass over kept logits costs 6
-// bytes each, the exp tile's further launches about 20 us.
-constexpr int64_t kExpLogits = 24000000;
+// bytes each, the exp tile's further launches about 4 us that the launches around them do not hide. Policy steps with
+// kept logits / exp tiles, us: 256 x 8192 x 256 (rows, V, d) 43.7 / 46.9, 1024 x 8192 x 256 54.5 / 54.2, 256 x 32000 x 256
+// 79 / 76, 1024 x 32000 x 256 140 / 103, 512 x 151936 x 256 461 / 282, 1024 x 151936 x 2048 1327 / 1167.
+constexpr int64_t kExpLogits = 8000000;
 
 // Most rows whose exp tiles the preference loss keeps by default until its factors are known: 2 bytes a logit, as much
 // as the kept logits and the gradient tile of one chunk of 6144 rows take.
@@ -1503,7 +1524,7 @@ LossLayout loss_layout(int64_t N, int64_t d, int64_t V, int64_t pairs, bool with
   if (large && pairs >= 0 && o.chunk_tokens == 0 && N <= kPreferenceRows) o.chunk_tokens = N;
   const bool one = N <= tok_chunk(N, &o);
   L.exp = large && (pairs < 0 || one);
-  L.tok = tok_layout(N, d, V, with_grad && (pairs < 0 || one) && !L.exp, with_grad, dW_bf16, with_grad, &o);
+  L.tok = tok_layout(N, d, V, with_grad && (pairs < 0 || one) && !L.exp, with_grad, dW_bf16, with_grad, &o, true);
   size_t off = L.tok.total;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -1518,6 +1539,7 @@ LossLayout loss_layout(int64_t N, int64_t d, int64_t V, int64_t pairs, bool with
     L.a = take(sizeof(float) * chunk);
     L.rest = take(sizeof(float) * chunk);
   }
+  if (pairs < 0) L.row64 = take(sizeof(double) * rows);
   if (pairs >= 0) {
     L.logp = take(sizeof(float) * rows);
     L.stats = take(sizeof(float2) * rows);
@@ -1664,6 +1686,8 @@ int policy_loss(const void* H, const void* W, const int64_t* y, int64_t N, int64
     a.ref_logp = policy->kl != LCE_KL_NONE ? ref_logp + c0 : nullptr;
     a.weights = weights ? weights + c0 : nullptr;
     a.row_loss = row_loss + c0;
+    a.row64 = reinterpret_cast<double*>(c.ws + L.row64) + c0;
+    a.all_rows = reinterpret_cast<const double*>(c.ws + L.row64);
     a.clip_low = policy->clip_low;
     a.clip_high = policy->clip_high;
     a.dual_clip = policy->dual_clip;
@@ -1680,7 +1704,10 @@ int policy_loss(const void* H, const void* W, const int64_t* y, int64_t N, int64
     if (with_grad)
       LCE_TRY(tok_grads(c, T, c0, rows, a.row.rowscale, reinterpret_cast<uint16_t*>(c.ws + c.L.Ht), dH, dW, dW_bf16));
   }
-  if (!count_here) LCE_TRY(finalize(c, row_loss, loss));
+  if (!count_here)
+    LCE_TRY(timed(c.s, K_FINALIZE, 8.0 * static_cast<double>(N), [&] {
+      return cuda_rc(lce::launch_policy_total(reinterpret_cast<const double*>(c.ws + L.row64), N, c.st, loss, c.s));
+    }));
   return finish(c);
 }
 

@@ -174,9 +174,6 @@ __device__ __forceinline__ void pause_ns(uint64_t ns) {
 template <class Prob>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     gemm_pair_kernel(const __grid_constant__ typename Prob::Params p) {
-  grid_dep_wait();    // everything below reads or writes what earlier kernels of the stream touch
-  grid_dep_launch();
-  if (Prob::skip(p)) return;  // same value in both CTAs of the pair (one global word)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -198,7 +195,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   const uint32_t rank = cluster_ctarank();
   const int cluster = static_cast<int>(blockIdx.x >> 1);
   const int nclusters = static_cast<int>(gridDim.x >> 1);
-  const int njobs = Prob::num_jobs(p, cluster, nclusters);
+  int njobs = Prob::num_jobs(p, cluster, nclusters);
   int* flags = Prob::flags(p);
 
   if (threadIdx.x == 0) {
@@ -223,6 +220,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   cluster_sync_all();  // both CTAs' barriers exist before anything signals them
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_holder;
+  // Everything above is the pair's own and overlaps the end of the kernel before this one (cross-entropy step of 250 rows,
+  // V = 4099: 48.2 -> 46.7 us); below, memory that earlier kernels of the stream touch.
+  grid_dep_wait();
+  grid_dep_launch();
+  if (Prob::skip(p)) njobs = 0;  // same value in both CTAs of the pair (one global word)
 
   if (warp == 0 && lane == 0) {
     // ---------------- TMA producer (both CTAs) ----------------

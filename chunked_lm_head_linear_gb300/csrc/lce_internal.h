@@ -122,12 +122,14 @@ struct DhParams {
   // The K = V reduction of a dH tile runs as `parts` tiles over fixed vocabulary
   // parts (dh_parts_for(V)); each stores its fp32 sum, and the last of them to
   // arrive adds the parts in part order and writes the tile.
-  int parts;             // 1: one tile over the whole vocabulary
+  int parts;             // 1: one tile over the whole vocabulary; 0 (in): dh_parts_for(V)
   int tiles_n;           // 256-column blocks of d (tile index = row block * tiles_n + column block)
   float4* part_buf;      // [tiles, parts, 2 CTAs, 4 warps, 64 column groups, 32 lanes] fp32 part sums
   int* part_cnt;         // [tiles, 2, 4] arrivals per warp slice; zero before and after each launch
   long long part_slices; // counters (warp slices) the workspace holds (checked build)
   int block_major;       // the parts of each block run back to back on one cluster, in part order
+  int split_rows;        // not 0: the parts are stored as they are, part s in rows [s split_rows, (s + 1) split_rows)
+                         // of the fp32 output, and added behind the launch (launch_dh_sum)
 };
 
 // dH parts: the vocabulary's k-blocks (64 words each) are cut into at most
@@ -143,6 +145,39 @@ inline int dh_parts_for(long long V) {
   const long long kb = (V + 63) / 64;
   const long long per = dh_kblocks_per_part(V);
   return per > 0 ? static_cast<int>((kb + per - 1) / per) : 1;
+}
+
+// Time of a dW tile in units of one of its k-blocks (w_k of them): short ones are bound by their epilogue and by writing
+// dW. Weighed as their k-blocks alone, short batches piled dW tiles onto the clusters that share no dH tile (policy steps
+// at V = 151936, d = 4096 with four dH parts, us before / after: 64 rows 2344 / 881, 256 rows 1180 / 953, 512 rows 1338 /
+// 1315; from 1024 rows on nothing changes).
+inline double dw_tile_cost(long long w_k) {
+  return w_k >= 14 ? static_cast<double>(w_k) : w_k >= 8 ? 14.0 : static_cast<double>(w_k + 6);
+}
+
+// dH parts where no such promise is made (the policy and preference losses). Each is stored as an fp32 tile of its own
+// and a launch behind the GEMMs adds them. In k-blocks of time (0.31 us), a part takes its share of the kb there are and
+// kDhStore more, the sum kDhSum and what it reads and writes, and a cluster's fair share of the launch is `fair`: the fewest
+// parts that stay within a tenth of the best. Short batches have few dH tiles, and four parts of V = 151936 run 594 k-blocks each
+// on one cluster, 207 us whatever the rest takes; long ones do without parts.
+constexpr int kMaxDhParts = 32;
+constexpr double kDhStore = 8.0, kDhSum = 10.0;
+inline int dh_parts_balanced(long long rows, long long V, long long d) {
+  const long long kb = (V + 63) / 64, cols = (d + 255) / 256;
+  const double k = static_cast<double>(kb);
+  const double fair = (static_cast<double>((rows + 255) / 256 * cols) * k +
+                       static_cast<double>((V + 255) / 256 * cols) * dw_tile_cost((rows + 63) / 64)) / 76.0;
+  const double bytes = 8.0 * static_cast<double>(rows) * static_cast<double>(d);  // of a part, written and read
+  auto time = [&](int p) {
+    const double longest = p == 1 ? k : k / p + kDhStore;
+    return (longest > fair ? longest : fair) + (p == 1 ? 0.0 : kDhSum + p * bytes / (5.0e12 * 0.31e-6));
+  };
+  double best = time(1);
+  for (int p = 2; p <= kMaxDhParts; ++p) best = time(p) < best ? time(p) : best;
+  long long parts = 1;
+  while (parts < kMaxDhParts && time(static_cast<int>(parts)) > 1.1 * best) ++parts;
+  const long long per = (kb + parts - 1) / parts;
+  return static_cast<int>((kb + per - 1) / per);
 }
 
 struct DwParams {
@@ -177,6 +212,9 @@ cudaError_t launch_backward(const CUtensorMap& ah, const CUtensorMap& bh, const 
                             const CUtensorMap& bw, const CUtensorMap& cw, long long rows, long long V, long long d,
                             const DhParams& h, const DwParams& w, int* flags, int num_sms, cudaStream_t s,
                             long long v_begin = 0, long long v_end = -1, bool with_dh = true);
+// dH of `rows` rows: bf16(gscale rowscale sum_s part[s]), the parts [parts, split_rows, d] added in order.
+cudaError_t launch_dh_sum(const float* part, int parts, long long split_rows, long long rows, int d,
+                          const float* rowscale, const DevStatus* st, void* dH, cudaStream_t s);
 cudaError_t launch_combine(const float2* partials, int nparts, int rows, const float* ztgt, const int64_t* y,
                            int V, long long ignore_index, float* lse, float* loss_i, cudaStream_t s);
 // Per row of a chunk: lse, loss_i, alpha_i = exp(ref_i - lse_i) (1 if the chunk's guard is set,
@@ -411,6 +449,8 @@ struct PolicyArgs {
   const float* ref_logp;    // or null: no KL term
   const float* weights;     // or null: 1
   float* row_loss;          // [rows] out
+  double* row64;            // [rows] out: the same, summed into the loss
+  const double* all_rows;   // [N] of the whole call
   float clip_low, clip_high, dual_clip, kl_coef;
   int kl;
   // one chunk (loss not null): the row finished last counts the tokens, sums the rows' losses and sets the scales
@@ -458,6 +498,7 @@ cudaError_t launch_label_logits(const void* H, const void* W, const int64_t* y, 
 // Preference loss from the exp tile: logp, and rest or (where *guard is set) stats.
 cudaError_t launch_exp_logp(const LossRowArgs& p, int rows, cudaStream_t s);
 cudaError_t launch_policy_row(const PolicyArgs& p, int rows, cudaStream_t s);
+cudaError_t launch_policy_total(const double* rows, long long N, const DevStatus* st, float* loss, cudaStream_t s);
 cudaError_t launch_pairs(const PairArgs& p, cudaStream_t s);
 cudaError_t launch_preference_row(const PreferenceArgs& p, int rows, cudaStream_t s);
 

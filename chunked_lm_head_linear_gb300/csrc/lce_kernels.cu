@@ -323,11 +323,12 @@ struct DhEpi {
     if (m0 + ctx.row0 >= p.rows) return;  // all 32 rows of this warp are past the chunk
     float f = st.g;
     if (r < p.rows && p.rowscale != nullptr) f *= p.rowscale[r];
-    if (p.parts > 1) {
+    if (p.split_rows == 0 && p.parts > 1) {
       part_half(p, ctx, m0, col0, taddr, part, tile_index, f);
       return;
     }
-    if (p.f32_out) {  // fp32 tiles of 32 columns, like the dW epilogue
+    if (p.split_rows != 0) f = 1.f;  // (the sum is scaled)
+    if (p.f32_out || p.split_rows != 0) {  // fp32 tiles of 32 columns, like the dW epilogue
 #pragma unroll 1
       for (int u = 0; u < EPI_COLS / 32; ++u) {
         if (col0 + u * 32 >= p.N) break;
@@ -338,7 +339,7 @@ struct DhEpi {
         for (int q = 0; q < 8; ++q)
           *reinterpret_cast<float4*>(ctx.stage + stage_off(ctx.lane, q)) =
               make_float4(v[4 * q] * f, v[4 * q + 1] * f, v[4 * q + 2] * f, v[4 * q + 3] * f);
-        stage_release(ctx, col0 + u * 32, m0 + ctx.row0, false);
+        stage_release(ctx, col0 + u * 32, part * p.split_rows + m0 + ctx.row0, false);
       }
       return;
     }
@@ -813,6 +814,26 @@ __global__ void __launch_bounds__(256) k_scale_bf16(uint4* __restrict__ a, long 
   }
 }
 
+// dH from the parts of its sum over the vocabulary, eight columns a thread (see launch_dh_sum).
+__global__ void __launch_bounds__(256) k_dh_sum(const float4* __restrict__ part, int parts, long long stride, long long rows,
+                                                int groups, const float* __restrict__ rowscale, const DevStatus* st,
+                                                uint4* __restrict__ dH) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const long long i = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x;
+  if (i >= rows * groups) return;
+  const float f = st->gscale * rowscale[i / groups];
+  float4 a = part[2 * i], b = part[2 * i + 1];
+#pragma unroll 4
+  for (int s = 1; s < parts; ++s) {
+    const float4 x = part[s * stride + 2 * i], y = part[s * stride + 2 * i + 1];
+    a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+    b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
+  }
+  dH[i] = make_uint4(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f), pack_bf16x2(b.x * f, b.y * f),
+                     pack_bf16x2(b.z * f, b.w * f));
+}
+
 // loss = (sum_i loss_i) * lscale, fp64 accumulation in a fixed order.
 __global__ void __launch_bounds__(1024) k_finalize(const float* __restrict__ loss_i, long long N,
                                                    const DevStatus* st, float* loss) {
@@ -1081,8 +1102,8 @@ static cudaError_t launch_backward_t(const CUtensorMap& ah, const CUtensorMap& b
   p.h_m = with_dh ? ceil_div_i(rows, P_TILE_M) : 0;
   p.h_n = ceil_div_i(d, BN);
   p.h_k = ceil_div_i(V, BK);
-  p.h_kpart = dh_kblocks_per_part(V);
-  p.h_parts = dh_parts_for(V);
+  p.h_parts = h.parts > 0 ? h.parts : dh_parts_for(V);
+  p.h_kpart = h.parts > 0 ? ceil_div_i(p.h_k, h.parts) : dh_kblocks_per_part(V);
   p.w_m = ceil_div_i(V, P_TILE_M);
   p.w_n = ceil_div_i(d, BN);
   p.w_k = ceil_div_i(rows, BK);
@@ -1116,7 +1137,7 @@ static cudaError_t launch_backward_t(const CUtensorMap& ah, const CUtensorMap& b
   // K-major, B N-major) runs in ~0.98 of a dW k-block's time (both N-major): 584 vs 594 SM cycles
   // per 64-deep k-block, measured on the Qwen3.5-2B-like head with cycle counters in the MMA issuer.
   constexpr double kDhKblockCost = 0.98;
-  const double w_cost = p.w_k;
+  const double w_cost = dw_tile_cost(p.w_k);
   // The parts of a dH block go to one cluster back to back when the whole block is no longer than
   // kDhBlockMaxShare of a cluster's fair share: the blocks then run side by side on some clusters,
   // each W and exp-tile block read by all the tiles that need it at once, while the other clusters
@@ -1124,7 +1145,7 @@ static cudaError_t launch_backward_t(const CUtensorMap& ah, const CUtensorMap& b
   // chunks, equal at 2048 and 4096). Otherwise the parts are dealt one by one, which balances the
   // clusters when the blocks are fewer than them (540K vs 470K tokens/s at 512-token chunks).
   const double fair = (static_cast<double>(nParts) * kDhKblockCost * p.h_kpart + static_cast<double>(nW) * w_cost) / P;
-  p.h_group = (p.h_parts > 1 && kDhKblockCost * p.h_k <= kDhBlockMaxShare * fair) ? p.h_parts : 1;
+  p.h_group = (p.h_parts > 1 && h.split_rows == 0 && kDhKblockCost * p.h_k <= kDhBlockMaxShare * fair) ? p.h_parts : 1;
   p.h.block_major = p.h_group > 1 ? 1 : 0;
   const long long nH = nParts / p.h_group;
   const double h_cost = kDhKblockCost * (p.h_group == 1 ? p.h_kpart : p.h_k);
@@ -1232,6 +1253,14 @@ cudaError_t launch_scale_bf16(void* a, long long n_a, void* b, long long n_b, co
   if (n_a <= 0 && n_b <= 0) return cudaSuccess;
   return launch_k(k_scale_bf16, num_sms * 4, 256, 0, s, static_cast<uint4*>(a), n_a / 8, static_cast<uint4*>(b),
                   n_b / 8, g);
+}
+
+cudaError_t launch_dh_sum(const float* part, int parts, long long split_rows, long long rows, int d,
+                          const float* rowscale, const DevStatus* st, void* dH, cudaStream_t s) {
+  const long long n = rows * (d / 8);
+  if (n <= 0) return cudaSuccess;
+  return launch_k(k_dh_sum, static_cast<unsigned>((n + 255) / 256), 256, 0, s, reinterpret_cast<const float4*>(part), parts,
+                  split_rows * (d / 4), rows, d / 8, rowscale, st, static_cast<uint4*>(dH));
 }
 
 cudaError_t launch_finalize(const float* loss_i, long long N, const DevStatus* st, float* loss, cudaStream_t s) {

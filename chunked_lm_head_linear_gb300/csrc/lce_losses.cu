@@ -107,8 +107,9 @@ __device__ __forceinline__ void row_gradient(const LossRowArgs& p, int r, int y,
                  kRowThreads);
 }
 
-// Sum of n floats in fp64, in an order that depends on n alone.
-__device__ __forceinline__ double block_total(const float* x, long long n, double* red) {
+// Sum of n numbers in fp64, in an order that depends on n alone.
+template <typename X>
+__device__ __forceinline__ double block_total(const X* x, long long n, double* red) {
   const int tid = threadIdx.x;
   double sum = 0.0;
   for (long long i = tid; i < n; i += kRowThreads) sum += static_cast<double>(__ldcg(x + i));
@@ -141,35 +142,42 @@ __device__ __forceinline__ bool last_block(DevStatus* st, int total) {
 //   row = w (kl_coef KL - s),   a = w (kl_coef dKL/dl - [the unclipped side] r A)
 //   KL of u = l - ref: k1 = u, k2 = u^2 / 2, k3 = exp(-u) - 1 + u
 // A weight of zero leaves nothing, whatever the row holds; an advantage of zero
-// has no share even of an infinite ratio.
-__device__ __forceinline__ void policy_row(const PolicyArgs& p, int r, float logp, float& row, float& a) {
-  row = a = 0.f;
-  const float w = p.weights != nullptr ? p.weights[r] : 1.f;
-  if (w == 0.f) return;
-  const float A = p.advantages[r];
-  float gain = 0.f, slope = 0.f;
-  if (A != 0.f) {
-    const float ratio = p.old_logp != nullptr ? expf(logp - p.old_logp[r]) : 1.f;
-    const float open = ratio * A, bound = fminf(fmaxf(ratio, 1.f - p.clip_low), 1.f + p.clip_high) * A;
-    const bool clipped = bound < open;
-    gain = clipped ? bound : open;
-    slope = clipped ? 0.f : open;
-    if (A < 0.f && p.dual_clip > 0.f && gain < p.dual_clip * A) {
-      gain = p.dual_clip * A;
-      slope = 0.f;
+// has no share even of an infinite ratio. r and u are fp32, as logp is; the
+// row's loss is formed from them in fp64, as the rows' losses cancel in their sum.
+struct PolicyRow {
+  float w, A, ratio, side, u, e;  // side: what A is multiplied by; e = exp(-u) - 1
+  float a;
+};
+
+__device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& p, int r, float logp) {
+  PolicyRow x{p.weights != nullptr ? p.weights[r] : 1.f, 0.f, 1.f, 0.f, 0.f, 0.f, 0.f};
+  if (x.w == 0.f) return x;
+  x.A = p.advantages[r];
+  if (x.A != 0.f) {
+    if (p.old_logp != nullptr) x.ratio = expf(logp - p.old_logp[r]);
+    const float clipped = fminf(fmaxf(x.ratio, 1.f - p.clip_low), 1.f + p.clip_high);
+    x.side = clipped * x.A < x.ratio * x.A ? clipped : x.ratio;
+    x.a = clipped * x.A < x.ratio * x.A ? 0.f : -x.ratio * x.A;
+    if (x.A < 0.f && p.dual_clip > 0.f && x.side > p.dual_clip) {
+      x.side = p.dual_clip;
+      x.a = 0.f;
     }
   }
-  row = -gain;
-  a = -slope;
   if (p.ref_logp != nullptr) {
-    const float u = logp - p.ref_logp[r];
-    // exp(-u) - 1 without what the difference loses near 0
-    const float e = expm1f(-u), kl = p.kl == 1 ? u : p.kl == 2 ? 0.5f * u * u : e + u;
-    row = fmaf(p.kl_coef, kl, row);
-    a = fmaf(p.kl_coef, p.kl == 1 ? 1.f : p.kl == 2 ? u : -e, a);
+    x.u = logp - p.ref_logp[r];
+    x.e = expm1f(-x.u);  // exp(-u) - 1 without what the difference loses near 0
+    x.a = fmaf(p.kl_coef, p.kl == 1 ? 1.f : p.kl == 2 ? x.u : -x.e, x.a);
   }
-  row *= w;
-  a *= w;
+  x.a *= x.w;
+  return x;
+}
+
+__device__ __forceinline__ double policy_loss(const PolicyArgs& p, const PolicyRow& x) {
+  if (x.w == 0.f) return 0.0;
+  const double u = x.u, kl = p.kl == 1 ? u : p.kl == 2 ? 0.5 * u * u : static_cast<double>(x.e) + u;
+  double row = x.A != 0.f ? -static_cast<double>(x.side) * static_cast<double>(x.A) : 0.0;
+  if (p.ref_logp != nullptr) row += static_cast<double>(p.kl_coef) * kl;
+  return row * static_cast<double>(x.w);
 }
 
 // One block per row of the chunk. EXP: from the exp tile, or, where its guard is set, from the partial sums.
@@ -183,7 +191,8 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_policy_row(const PolicyArgs 
   const int r = blockIdx.x, tid = threadIdx.x;
   const LossRowArgs& q = p.row;
   const int y = given_label(q.y, r, q.ignore_index, q.V);
-  float logp = 0.f, row = 0.f, a = 0.f, rest = 0.f;
+  float logp = 0.f, a = 0.f, rest = 0.f;
+  double row = 0.0;  // thread 0's
   RowStats s{0.f, 0.f};
   const bool by_exp = EXP && *q.guard == 0;
   if (y >= 0) {
@@ -195,11 +204,14 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_policy_row(const PolicyArgs 
       const float z = q.Z != nullptr ? q.Z[static_cast<long long>(r) * q.ldz + y] : q.ztgt[r];
       logp = (z - s.M) * q.inv_t - s.logs;
     }
-    policy_row(p, r, logp, row, a);
+    const PolicyRow x = policy_row(p, r, logp);
+    a = x.a;
+    if (tid == 0) row = policy_loss(p, x);
   }
   if (tid == 0) {
     q.logp[r] = logp;
-    p.row_loss[r] = row;
+    p.row_loss[r] = static_cast<float>(row);
+    p.row64[r] = row;
     if (GRAD && q.stats != nullptr) q.stats[r] = make_float2(s.M, s.logs);
     if (p.loss != nullptr) {
       if (y >= 0) atomicAdd(reinterpret_cast<unsigned long long*>(&q.st->n_counted), 1ull);
@@ -214,7 +226,7 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_policy_row(const PolicyArgs 
   }
   if (p.loss == nullptr) return;
   if (!last_block(q.st, static_cast<int>(p.N))) return;
-  const double sum = block_total(p.row_loss, p.N, s_total);
+  const double sum = block_total(p.all_rows, p.N, s_total);
   if (tid == 0) {
     const long long counted = __ldcg(&q.st->n_counted), n = p.n_override >= 0 ? p.n_override : counted;
     const double weight = p.mean ? (n > 0 ? 1.0 / static_cast<double>(n) : 0.0) : 1.0;
@@ -222,6 +234,16 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_policy_row(const PolicyArgs 
     q.st->gscale = static_cast<float>((p.grad_loss != nullptr ? static_cast<double>(*p.grad_loss) : 1.0) * weight);
     *p.loss = static_cast<float>(sum * weight);
   }
+}
+
+// The rows' losses of a call of several chunks, summed.
+__global__ void __launch_bounds__(kRowThreads) k_policy_total(const double* __restrict__ rows, long long N,
+                                                              const DevStatus* st, float* __restrict__ loss) {
+  grid_dep_wait();
+  grid_dep_launch();
+  __shared__ double red[kRowThreads];
+  const double sum = block_total(rows, N, red);
+  if (threadIdx.x == 0) *loss = static_cast<float>(sum * st->lscale);
 }
 
 // ----------------------------------------------------------------------------
@@ -427,6 +449,10 @@ cudaError_t launch_policy_row(const PolicyArgs& p, int rows, cudaStream_t s) {
   if (p.row.rowscale == nullptr) return launch_k(k_policy_row<false, false, false>, rows, kRowThreads, 0, s, p);
   return p.row.sums != nullptr ? launch_k(k_policy_row<true, false, true>, rows, kRowThreads, 0, s, p)
                                : launch_k(k_policy_row<true, true, false>, rows, kRowThreads, 0, s, p);
+}
+
+cudaError_t launch_policy_total(const double* rows, long long N, const DevStatus* st, float* loss, cudaStream_t s) {
+  return launch_k(k_policy_total, 1, kRowThreads, 0, s, rows, N, st, loss);
 }
 
 cudaError_t launch_pairs(const PairArgs& p, cudaStream_t s) {

@@ -67,7 +67,7 @@ def head(H, W, y, T):
 
 
 def uses_exp_tiles(N, V, chunk):
-    return min(N, chunk or N) > 96 and min(N, chunk or N) * V >= 16_000_000
+    return min(N, chunk or N) > 96 and min(N, chunk or N) * V >= 8_000_000
 
 
 def check_gradients(dH, dW, ref, slack, exp=False):
