@@ -1511,9 +1511,12 @@ struct LossLayout {
 // 79 / 76, 1024 x 32000 x 256 140 / 103, 512 x 151936 x 256 461 / 282, 1024 x 151936 x 2048 1327 / 1167.
 constexpr int64_t kExpLogits = 8000000;
 
-// Most rows whose exp tiles the preference loss keeps by default until its factors are known: 2 bytes a logit, as much
-// as the kept logits and the gradient tile of one chunk of 6144 rows take.
-constexpr int64_t kPreferenceRows = 3 * 6144;
+// Most rows whose exp tiles are kept together by default (logits launches of at most 6143 rows each, so that a launch's
+// H stays in L2): 2 bytes a logit, as much as the kept logits and the gradient tile of one chunk of 6144 rows take. One
+// backward launch for all of them writes dW once (policy step of 7000 rows of d = 1024, V = 151936, at the power limit: 4.0
+// to 4.4 ms, in two chunks 4.3; 9000 of d = 2048: 9.8 to 10.0, 10.1), and the preference loss, whose factors need all rows,
+// computes the logits once (9000 rows: 9.0 ms, twice 12.1).
+constexpr int64_t kExpRows = 3 * 6144;
 
 // pairs < 0: the policy loss.
 LossLayout loss_layout(int64_t N, int64_t d, int64_t V, int64_t pairs, bool with_grad, bool dW_bf16, const lce_opts* opts) {
@@ -1521,7 +1524,7 @@ LossLayout loss_layout(int64_t N, int64_t d, int64_t V, int64_t pairs, bool with
   lce_opts o = *opts;
   L.step = tok_chunk(N, &o);
   const bool large = with_grad && L.step > lce::kFewRows && L.step * V >= kExpLogits;
-  if (large && pairs >= 0 && o.chunk_tokens == 0 && N <= kPreferenceRows) o.chunk_tokens = N;
+  if (large && o.chunk_tokens == 0 && N <= kExpRows) o.chunk_tokens = N;
   const bool one = N <= tok_chunk(N, &o);
   L.exp = large && (pairs < 0 || one);
   L.tok = tok_layout(N, d, V, with_grad && (pairs < 0 || one) && !L.exp, with_grad, dW_bf16, with_grad, &o, true);
@@ -1659,9 +1662,13 @@ int policy_loss(const void* H, const void* W, const int64_t* y, int64_t N, int64
   else if (!count_here)
     LCE_TRY(prepare(c, grad_loss));
   if (N == 0 && with_grad) LCE_TRY(zero_dW(c, dW, dW_bf16));
-  for (int64_t k = 0, c0 = 0; c0 < N; ++k, c0 += c.L.C) {
-    const int64_t rows = (N - c0) < c.L.C ? (N - c0) : c.L.C;
+  const bool together = c.L.C > L.step;  // several logits launches, one backward
+  for (int64_t k = 0, c0 = 0; c0 < N; ++k, c0 += L.step) {
+    const int64_t rows = (N - c0) < L.step ? (N - c0) : L.step;
+    const int64_t at = together ? c0 : 0;
     lce::TokParams p = tok_params(c, c0, rows, temperature);
+    p.partials += at * p.nparts;
+    p.ztgt += at;
     int* guard = L.exp ? reinterpret_cast<int*>(c.ws + L.guard) + k : nullptr;
     if (count_here) {
       p.clear_st = c.st;
@@ -1670,16 +1677,16 @@ int policy_loss(const void* H, const void* W, const int64_t* y, int64_t N, int64
     }
     float* Z = with_grad && !L.exp ? reinterpret_cast<float*>(c.ws + T.Z) : nullptr;
     if (L.exp)
-      LCE_TRY(exp_tile(c, L, c0, rows, p, guard, 0));
+      LCE_TRY(exp_tile(c, L, c0, rows, p, guard, at));
     else
       LCE_TRY(tok_logits(c, c0, rows, Z ? lce::TOK_STATS_Z : lce::TOK_STATS, Z, T.ldz, p));
     lce::PolicyArgs a;
     std::memset(&a, 0, sizeof a);
-    a.row = loss_row(c, T, c0, p, Z, with_grad, dW != nullptr, 0);
+    a.row = loss_row(c, T, c0, p, Z, with_grad, dW != nullptr, at);
     a.row.logp = logp + c0;
     if (L.exp) {
-      loss_row_exp(&a.row, c, L, guard, 0);
-      a.row.stats = reinterpret_cast<float2*>(c.ws + T.stats);
+      loss_row_exp(&a.row, c, L, guard, at);
+      a.row.stats = reinterpret_cast<float2*>(c.ws + T.stats) + at;
     }
     a.advantages = advantages + c0;
     a.old_logp = old_logp ? old_logp + c0 : nullptr;
@@ -1701,8 +1708,9 @@ int policy_loss(const void* H, const void* W, const int64_t* y, int64_t N, int64
     LCE_TRY(timed(c.s, K_COMBINE, loss_row_bytes(c, rows, with_grad, Z != nullptr),
                   [&] { return cuda_rc(lce::launch_policy_row(a, static_cast<int>(rows), c.s)); }));
     if (L.exp) LCE_TRY(exp_fallback(c, c0, rows, p, a.row, guard));
-    if (with_grad)
-      LCE_TRY(tok_grads(c, T, c0, rows, a.row.rowscale, reinterpret_cast<uint16_t*>(c.ws + c.L.Ht), dH, dW, dW_bf16));
+    if (!with_grad || (together && c0 + rows < N)) continue;
+    LCE_TRY(tok_grads(c, T, c0 - at, at + rows, reinterpret_cast<float*>(c.ws + c.L.alpha),
+                      reinterpret_cast<uint16_t*>(c.ws + c.L.Ht), dH, dW, dW_bf16));
   }
   if (!count_here)
     LCE_TRY(timed(c.s, K_FINALIZE, 8.0 * static_cast<double>(N), [&] {

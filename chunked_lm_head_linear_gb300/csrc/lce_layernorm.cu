@@ -521,13 +521,17 @@ cudaError_t fwd(const LayerNormArgs& p, int num_sms, cudaStream_t s) {
                      Rg::bytes(D), p, s);
 }
 
+// Teams of a warp (no barrier) up to rows of 1024, then as few threads as keep a row in registers; rows a turn, turns and
+// blocks a SM as measured (65536 rows bf16, 32768 fp32, us; the copy rate would take 10, 20, 40, 79, 158 and 59, 119):
+// 256: 11. 512: warps 22, teams of 64 25. 1024: 43, 45. 2048: teams of 128 in two blocks a SM 84, of 256 in three 92; fp32
+// 61, 67. 4096: two blocks a SM 164, three 191, four 197; fp32 four 121, three 138.
 template <bool F32>
 cudaError_t fwd_rows(const LayerNormArgs& p, int num_sms, cudaStream_t s) {
   if (p.d <= 256) return fwd<F32, 32, 1, 2, 4, 3>(p, num_sms, s);
-  if (p.d <= 512) return fwd<F32, 64, 1, 2, 4, 3>(p, num_sms, s);
-  if (p.d <= 1024) return fwd<F32, 128, 1, 2, 4, 3>(p, num_sms, s);
-  if (p.d <= 2048) return fwd<F32, 256, 1, 2, 4, 3>(p, num_sms, s);
-  if (p.d <= 4096) return fwd<F32, 256, 2, 1, 4, 3>(p, num_sms, s);
+  if (p.d <= 512) return fwd<F32, 32, 2, 1, 4, 2>(p, num_sms, s);
+  if (p.d <= 1024) return fwd<F32, 32, 4, 1, F32 ? 3 : 4, 1>(p, num_sms, s);
+  if (p.d <= 2048) return fwd<F32, F32 ? 256 : 128, F32 ? 1 : 2, F32 ? 4 : 1, F32 ? 2 : 4, 2>(p, num_sms, s);
+  if (p.d <= 4096) return fwd<F32, 256, 2, 1, F32 ? 3 : 4, F32 ? 4 : 2>(p, num_sms, s);
   if (p.d <= 8192) return fwd<F32, 256, 4, 1, 3, 2>(p, num_sms, s);
   if (p.d <= 16384) return fwd<F32, 512, 4, 1, 3, 1>(p, num_sms, s);
   return fwd<F32, 1024, 4, 1, F32 ? 1 : 2, 1>(p, num_sms, s);

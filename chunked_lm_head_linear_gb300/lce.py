@@ -313,6 +313,12 @@ def _check_dev(t, name, dtype, numel=None, shape=None, device=None):
         raise ValueError(f"{name} needs at least {numel} elements, has {t.numel()}")
 
 
+def _check_vector(t, name, dtype, n, device):
+    """_check_dev of a vector of n elements; one expression where there is nothing to say."""
+    if not (getattr(t, "dtype", None) is dtype and t.shape == (n,) and t.device == device and t.is_contiguous()):
+        _check_dev(t, name, dtype, shape=(n,), device=device)
+
+
 def _workspace(op, N, d, V, opts, device, workspace=None):
     """The caller's workspace if it is large enough (else LCE_ERR_WORKSPACE, as
     the C ABI answers: a caller that sized its own workspace, to bound memory or
@@ -1033,8 +1039,10 @@ def _check_policy(H, W, y, advantages, old_logp, ref_logp, weights, kl, kl_coef,
         raise ValueError("a KL term needs ref_logp")
     if advantages is None:
         raise ValueError("advantages is required")
+    dev, f32 = H.device, torch.float32
     for name, t in (("advantages", advantages), ("old_logp", old_logp), ("ref_logp", ref_logp), ("weights", weights)):
-        _check_dev(t, name, torch.float32, shape=(N,), device=H.device)
+        if t is not None:
+            _check_vector(t, name, f32, N, dev)
     return N, d, V, LcePolicy(float(clip_low), float(clip_high), float(dual_clip or 0.0), float(kl_coef), LCE_KL[kl], 0)
 
 
@@ -1180,18 +1188,21 @@ def _check_layernorm(x, w, b):
         raise ValueError("x must be a bf16 or fp32 CUDA tensor [N, d] (there is no CPU path)")
     if x.dim() != 2 or not x.is_contiguous():
         raise ValueError("x must be a contiguous [N, d] tensor")
-    if x.device.index != torch.cuda.current_device():
-        raise ValueError(f"x is on {x.device}; make it the current device (torch.cuda.set_device)")
-    types = LCE_NORM_X_F32 if x.dtype == torch.float32 else 0
-    params = [t for t in (w, b) if t is not None]
-    if any(not isinstance(t, torch.Tensor) or t.dtype not in (torch.bfloat16, torch.float32) for t in params) or \
-            len({t.dtype for t in params}) > 1:
-        raise ValueError("w and b must both be fp32 or both bf16 CUDA tensors [d], or None")
+    device = x.device
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"x is on {device}; make it the current device (torch.cuda.set_device)")
+    N, d = x.shape
+    types = LCE_NORM_X_F32 if x.dtype is torch.float32 else 0
+    kind = None
     for name, t in (("w", w), ("b", b)):
-        if t is not None:
-            _check_dev(t, name, t.dtype, shape=(x.shape[1],), device=x.device)
-            types |= LCE_NORM_W_BF16 if t.dtype == torch.bfloat16 else 0
-    return x.shape[0], x.shape[1], types
+        if t is None:
+            continue
+        dtype = getattr(t, "dtype", None)
+        if dtype not in (torch.bfloat16, torch.float32) or kind not in (None, dtype):
+            raise ValueError("w and b must both be fp32 or both bf16 CUDA tensors [d], or None")
+        kind = dtype
+        _check_vector(t, name, dtype, d, device)
+    return N, d, types | LCE_NORM_W_BF16 if kind is torch.bfloat16 else types
 
 
 def lce_layernorm_forward(x, w=None, b=None, eps=1e-5, *, stream=None):
@@ -1200,9 +1211,10 @@ def lce_layernorm_forward(x, w=None, b=None, eps=1e-5, *, stream=None):
     may be None."""
     import torch
     N, d, types = _check_layernorm(x, w, b)
-    H = torch.empty((N, d), dtype=torch.bfloat16, device=x.device)
-    mean = torch.empty(N, dtype=torch.float32, device=x.device)
-    rstd = torch.empty(N, dtype=torch.float32, device=x.device)
+    device = x.device
+    H = torch.empty((N, d), dtype=torch.bfloat16, device=device)
+    mean = torch.empty(N, dtype=torch.float32, device=device)
+    rstd = torch.empty(N, dtype=torch.float32, device=device)
     _raise(load().lce_layernorm_forward(_ptr(x), _ptr(w), _ptr(b), N, d, float(eps), types, _ptr(H), _ptr(mean),
                                         _ptr(rstd), _stream(stream)), "lce_layernorm_forward")
     _keep(stream, x, w, b, H, mean, rstd)
@@ -1216,11 +1228,12 @@ def lce_layernorm_backward(x, w, mean, rstd, dH, *, bias: bool = True, need_dx: 
     without a w."""
     import torch
     N, d, types = _check_layernorm(x, w, None)
-    _check_dev(mean, "mean", torch.float32, shape=(N,), device=x.device)
-    _check_dev(rstd, "rstd", torch.float32, shape=(N,), device=x.device)
-    _check_dev(dH, "dH", torch.bfloat16, shape=(N, d), device=x.device)
     if mean is None or rstd is None or dH is None:
         raise ValueError("mean, rstd and dH are required")
+    device = x.device
+    _check_vector(mean, "mean", torch.float32, N, device)
+    _check_vector(rstd, "rstd", torch.float32, N, device)
+    _check_dev(dH, "dH", torch.bfloat16, shape=(N, d), device=device)
     need_dw = need_dw and w is not None
     if not (need_dx or need_dw or bias):
         raise ValueError("none of dx, dw and db is wanted")
