@@ -500,6 +500,9 @@ cudaError_t launch_exp_logp(const LossRowArgs& p, int rows, cudaStream_t s);
 cudaError_t launch_policy_row(const PolicyArgs& p, int rows, cudaStream_t s);
 cudaError_t launch_policy_total(const double* rows, long long N, const DevStatus* st, float* loss, cudaStream_t s);
 cudaError_t launch_pairs(const PairArgs& p, cudaStream_t s);
+// The statistics and log-probabilities of a call's rows (one chunk) and its pairs, at most kPairsHere, in one launch.
+constexpr int kPairsHere = 4;
+cudaError_t launch_logp_pairs(const LossRowArgs& p, const PairArgs& q, int rows, cudaStream_t s);
 cudaError_t launch_preference_row(const PreferenceArgs& p, int rows, cudaStream_t s);
 
 // GEMM tile geometry (must match the kernels): each CTA of a pair loads 128

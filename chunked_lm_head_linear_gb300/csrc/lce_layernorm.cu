@@ -26,6 +26,7 @@ constexpr int kLnWarps = kLnThreads / 32;
 constexpr int kSumWarps = 32;
 constexpr int kSms = 152;        // the one-pass backward runs one or two persistent blocks a SM
 constexpr int kLnFusedD = 8192;  // longest row whose backward is one pass
+constexpr int kLnCluster = 16;    // blocks of a backward that is one cluster
 
 // Eight neighbouring elements of a row, as they are held in registers.
 template <bool F32>
@@ -269,14 +270,15 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T, B) k_layernorm_fwd(const La
 // are one exchange in its team, x and dH stay in registers between them and dx,
 // and dw and db grow in registers over all of the block's rows. At the end the
 // teams' shares are added in order and the block writes one partial row of each.
-template <bool F32, int T, int K, int R, int D, int B>
+// ONE: the launch is one cluster, whose blocks add their shares through each
+// other's shared memory, in order; there is nothing left for another launch.
+template <bool F32, int T, int K, int R, int D, int B, bool ONE>
 __global__ void __launch_bounds__(kLnThreads, B) k_layernorm_bwd(const LayerNormArgs p) {
   grid_dep_wait();
   grid_dep_launch();
   constexpr int PX = F32 ? 2 : 1, PER = PX + 1;
   using Rg = Ring<F32, T, K, R, PER>;
   constexpr int S = kLnThreads / T, W = T / 32;
-  static_assert(S == 1 || K == 1, "teams' shares are added one column group a thread");
   extern __shared__ uint4 ring[];
   __shared__ float red[2][S][W][2 * R];
   __shared__ float share[S][T][17];
@@ -366,30 +368,49 @@ __global__ void __launch_bounds__(kLnThreads, B) k_layernorm_bwd(const LayerNorm
     }
   }
   copies_wait<0>();
-  if (p.part == nullptr) return;
+  if (p.dw == nullptr && p.db == nullptr) return;
+  if (ONE) __syncthreads();  // the ring is free
+  float* mine = reinterpret_cast<float*>(ring);  // ONE: this block's dw and db
 #pragma unroll
   for (int j = 0; j < K; ++j) {
-    if (S > 1) {  // (K is 1 there)
+    if (S > 1) {
+      if (j > 0) __syncthreads();
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         share[team][t][k] = aw[j][k];
         share[team][t][8 + k] = ab[j][k];
       }
       __syncthreads();
-      if (team != 0) return;
+      if (team == 0) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        for (int s = 1; s < S; ++s) {
-          aw[j][k] += share[s][t][k];
-          ab[j][k] += share[s][t][8 + k];
-        }
+        for (int k = 0; k < 8; ++k)
+          for (int s = 1; s < S; ++s) {
+            aw[j][k] += share[s][t][k];
+            ab[j][k] += share[s][t][8 + k];
+          }
+      }
     }
     const int gI = t + T * j;
-    if (gI < groups) {
-      const long long at = static_cast<long long>(blockIdx.x) * groups + gI;
-      store8(p.part, at, aw[j], true);
-      store8(p.part, static_cast<long long>(gridDim.x) * groups + at, ab[j], true);
+    if (team == 0 && gI < groups) {
+      const long long at = ONE ? gI : static_cast<long long>(blockIdx.x) * groups + gI;
+      store8(ONE ? mine : p.part, at, aw[j], true);
+      store8(ONE ? mine : p.part, (ONE ? groups : static_cast<long long>(gridDim.x) * groups) + at, ab[j], true);
     }
+  }
+  if (ONE) {
+    cluster_sync_all();
+    const int per = (2 * p.d + kLnCluster - 1) / kLnCluster, c0 = static_cast<int>(cluster_ctarank()) * per;
+    const uint32_t base = smem_u32(mine);
+    for (int c = c0 + tid; c < c0 + per && c < 2 * p.d; c += kLnThreads) {
+      float v[kLnCluster];
+#pragma unroll
+      for (int r = 0; r < kLnCluster; ++r) v[r] = ld_shared_cluster(mapa_shared(base + 4 * c, r));
+#pragma unroll
+      for (int r = 1; r < kLnCluster; ++r) v[0] += v[r];
+      float* out = c < p.d ? p.dw : p.db;
+      if (out != nullptr) out[c < p.d ? c : c - p.d] = v[0];
+    }
+    cluster_sync_all();  // no block leaves while its memory is read
   }
 }
 
@@ -537,29 +558,54 @@ cudaError_t fwd_rows(const LayerNormArgs& p, int num_sms, cudaStream_t s) {
   return fwd<F32, 1024, 4, 1, F32 ? 1 : 2, 1>(p, num_sms, s);
 }
 
+// Elements of x up to which the backward is one cluster of sixteen blocks: one launch, which is what small calls wait for
+// (1531 x 264: 20 us a call, 25 with a second launch that adds the blocks' partial rows; on the device alone 9.0 and 5.5).
+constexpr long long kLnOneLaunch = 1 << 19;
+
+bool one_launch(long long N, long long d) { return d <= kLnFusedD && N * d <= kLnOneLaunch; }
+
 template <bool F32, int T, int K, int R, int D, int B = 2>
 cudaError_t bwd_pass(const LayerNormArgs& p, int parts, cudaStream_t s) {
-  return launch_ring(k_layernorm_bwd<F32, T, K, R, D, B>, parts, kLnThreads, Ring<F32, T, K, R, F32 ? 3 : 2>::bytes(D), p, s);
+  constexpr int bytes = Ring<F32, T, K, R, F32 ? 3 : 2>::bytes(D);
+  if (!one_launch(p.N, p.d)) return launch_ring(k_layernorm_bwd<F32, T, K, R, D, B, false>, parts, kLnThreads, bytes, p, s);
+  auto kern = k_layernorm_bwd<F32, T, K, R, D, B, true>;
+  static_assert(bytes >= 2 * 4 * 8 * T * K, "a block's dw and db fit the ring");
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  const cudaError_t wide = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);  // above 8 blocks
+  if (wide != cudaSuccess) return wide;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kLnCluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kLnCluster);
+  cfg.blockDim = dim3(kLnThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 // Rows that a block of the one-pass backward takes at a time.
 int bwd_rows(long long d) {
-  return d <= 256 ? 8 * 2 : d <= 512 ? 4 * 2 : d <= 1024 ? 2 * 2 : d <= 2048 ? 2 : 1;
+  return d <= 256 ? 8 * 2 : d <= 512 ? 8 : d <= 1024 ? 4 : d <= 2048 ? 2 : 1;
 }
 
 template <bool F32>
-cudaError_t bwd(const LayerNormArgs& q, int num_sms, cudaStream_t s) {
-  LayerNormArgs p = q;
+cudaError_t bwd(const LayerNormArgs& p, int num_sms, cudaStream_t s) {
   const bool sums = p.dw != nullptr || p.db != nullptr;
-  if (!sums) p.part = nullptr;
   const int parts = layernorm_parts(p.N, p.d);
   cudaError_t e = cudaSuccess;
   if (p.d <= 256)
     e = bwd_pass<F32, 32, 1, 2, F32 ? 3 : 4>(p, parts, s);
   else if (p.d <= 512)
-    e = bwd_pass<F32, 64, 1, 2, F32 ? 3 : 4>(p, parts, s);
+    e = bwd_pass<F32, 32, 2, 1, F32 ? 3 : 4>(p, parts, s);
   else if (p.d <= 1024)
-    e = bwd_pass<F32, 128, 1, 2, F32 ? 3 : 4>(p, parts, s);
+    e = bwd_pass<F32, 64, 2, 1, F32 ? 3 : 4>(p, parts, s);
   else if (p.d <= 2048)
     e = bwd_pass<F32, 256, 1, 2, 4>(p, parts, s);
   else if (p.d <= 4096)
@@ -573,7 +619,7 @@ cudaError_t bwd(const LayerNormArgs& q, int num_sms, cudaStream_t s) {
     }
     if (e == cudaSuccess && sums) e = launch_k(k_layernorm_dw<F32>, dim3((p.d + 255) / 256, parts), kLnThreads, 0, s, p);
   }
-  if (e != cudaSuccess || !sums) return e;
+  if (e != cudaSuccess || !sums || one_launch(p.N, p.d)) return e;
   return launch_k(k_layernorm_sum, dim3((p.d + 31) / 32, 2), 32 * kSumWarps, 0, s, p, parts);
 }
 
@@ -581,6 +627,7 @@ cudaError_t bwd(const LayerNormArgs& q, int num_sms, cudaStream_t s) {
 
 // Blocks of the backward, each with a partial row of dw and db.
 int layernorm_parts(long long N, long long d) {
+  if (one_launch(N, d)) return 1;
   const long long rows = d <= kLnFusedD ? bwd_rows(d) : kLnWarps;
   const long long need = (N + rows - 1) / rows, most = d <= 4096 ? 2 * kSms : d <= kLnFusedD ? kSms : 512 / ((d + 255) / 256) + 1;
   const long long parts = need < most ? need : most;

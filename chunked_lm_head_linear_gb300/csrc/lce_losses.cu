@@ -265,6 +265,61 @@ __device__ __forceinline__ double sigmoid(double x) {
 //   sigmoid  -(1 - e) log sig(x) - e log sig(-x),   hinge  max(0, 1 - x)
 //   ipo      (delta - 1 / (2 beta))^2
 // Bounds that fall or leave [0, N] set the status bit; the pair then has no part in loss and gradient.
+__device__ __forceinline__ void pair_scales(const PairArgs& p) {
+  p.st->gscale = static_cast<float>((p.grad_loss != nullptr ? static_cast<double>(*p.grad_loss) : 1.0) * p.weight);
+}
+
+// Rows [c[h], c[h + 1]) of pair's two sequences; false, and no rows, where the bounds fall or leave [0, N].
+__device__ __forceinline__ bool pair_bounds(const PairArgs& p, long long pair, long long (&c)[3]) {
+  for (int i = 0; i < 3; ++i) c[i] = bound_at(p.cu, p.cu32, 2 * pair + i);
+  if (c[0] >= 0 && c[0] <= c[1] && c[1] <= c[2] && c[2] <= p.N) return true;
+  c[0] = c[1] = c[2] = 0;
+  return false;
+}
+
+// This thread's share of a sequence's sum and count: rows from + first, + first + step, ...
+__device__ __forceinline__ void sequence_share(const PairArgs& p, long long from, long long to, int first, int step,
+                                               double& sum, int& cnt) {
+  sum = 0.0;
+  cnt = 0;
+#pragma unroll 4
+  for (long long r = from + first; r < to; r += step)
+    if (given_label(p.y, r, p.ignore_index, p.V) >= 0) {
+      sum += static_cast<double>(__ldcg(p.logp + r));
+      ++cnt;
+    }
+}
+
+// A pair's results from its sequences' sums and counts (one thread).
+__device__ __forceinline__ void pair_result(const PairArgs& p, long long pair, bool ok, const double* sum, const int* cnt) {
+  if (!ok) atomicOr(&p.st->flags, kFlagLabelRange);
+  double per[2], S[2];
+  for (int h = 0; h < 2; ++h) {
+    per[h] = p.average ? (cnt[h] > 0 ? 1.0 / cnt[h] : 0.0) : 1.0;
+    S[h] = sum[h] * per[h];
+    p.seq_logp[2 * pair + h] = static_cast<float>(S[h]);
+  }
+  double delta = S[0] - S[1];
+  if (p.ref != nullptr) delta -= static_cast<double>(p.ref[2 * pair]) - static_cast<double>(p.ref[2 * pair + 1]);
+  const double beta = p.beta, x = beta * delta - p.margin, e = p.smoothing;
+  double loss, slope;
+  if (p.kind == 0) {
+    loss = (1.0 - e) * softplus(-x) + (e > 0.0 ? e * softplus(x) : 0.0);
+    slope = beta * (e * sigmoid(x) - (1.0 - e) * sigmoid(-x));
+  } else if (p.kind == 1) {
+    loss = x < 1.0 ? 1.0 - x : x != x ? x : 0.0;
+    slope = x < 1.0 ? -beta : x != x ? x : 0.0;
+  } else {
+    const double far = delta - 0.5 / beta;
+    loss = far * far;
+    slope = 2.0 * far;
+  }
+  if (!ok) loss = slope = 0.0;
+  p.pair_loss[pair] = static_cast<float>(loss);
+  p.coef[2 * pair] = static_cast<float>(slope * per[0]);
+  p.coef[2 * pair + 1] = static_cast<float>(-slope * per[1]);
+}
+
 __global__ void __launch_bounds__(kRowThreads) k_pairs(const PairArgs p) {
   grid_dep_wait();
   grid_dep_launch();
@@ -272,73 +327,84 @@ __global__ void __launch_bounds__(kRowThreads) k_pairs(const PairArgs p) {
   __shared__ double s_sum[2];
   __shared__ int s_cnt[2];
   const int tid = threadIdx.x;
-  const long long pair = blockIdx.x;
-  if (pair == 0 && tid == 0)
-    p.st->gscale = static_cast<float>((p.grad_loss != nullptr ? static_cast<double>(*p.grad_loss) : 1.0) * p.weight);
+  if (blockIdx.x == 0 && tid == 0) pair_scales(p);
   if (p.P == 0) {
     if (tid == 0) *p.loss = 0.f;
     return;
   }
+  if (tid < 2) s_cnt[tid] = 0;
   long long c[3];
-  for (int i = 0; i < 3; ++i) c[i] = bound_at(p.cu, p.cu32, 2 * pair + i);
-  const bool ok = c[0] >= 0 && c[0] <= c[1] && c[1] <= c[2] && c[2] <= p.N;
-  if (!ok) {
-    if (tid == 0) atomicOr(&p.st->flags, kFlagLabelRange);
-    c[0] = c[1] = c[2] = 0;
-  }
+  const bool ok = pair_bounds(p, blockIdx.x, c);
   for (int h = 0; h < 2; ++h) {
-    double sum = 0.0;
-    int cnt = 0;
-    for (long long r = c[h] + tid; r < c[h + 1]; r += kRowThreads)
-      if (given_label(p.y, r, p.ignore_index, p.V) >= 0) {
-        sum += static_cast<double>(p.logp[r]);
-        ++cnt;
-      }
+    double sum;
+    int cnt;
+    sequence_share(p, c[h], c[h + 1], tid, kRowThreads, sum, cnt);
+    __syncthreads();
     s_red[tid] = sum;
+    cnt = __reduce_add_sync(0xffffffffu, cnt);
+    if ((tid & 31) == 0) atomicAdd(&s_cnt[h], cnt);
     __syncthreads();
     for (int w = kRowThreads / 2; w > 0; w >>= 1) {
       if (tid < w) s_red[tid] += s_red[tid + w];
       __syncthreads();
     }
-    if (tid == 0) {
-      s_sum[h] = s_red[0];
-      s_cnt[h] = 0;
-    }
-    __syncthreads();
-    for (int off = 16; off > 0; off >>= 1) cnt += __shfl_xor_sync(0xffffffffu, cnt, off);
-    if ((tid & 31) == 0) atomicAdd(&s_cnt[h], cnt);
-    __syncthreads();
+    if (tid == 0) s_sum[h] = s_red[0];
   }
-  if (tid == 0) {
-    double per[2], S[2];
-    for (int h = 0; h < 2; ++h) {
-      per[h] = p.average ? (s_cnt[h] > 0 ? 1.0 / s_cnt[h] : 0.0) : 1.0;
-      S[h] = s_sum[h] * per[h];
-      p.seq_logp[2 * pair + h] = static_cast<float>(S[h]);
-    }
-    double delta = S[0] - S[1];
-    if (p.ref != nullptr) delta -= static_cast<double>(p.ref[2 * pair]) - static_cast<double>(p.ref[2 * pair + 1]);
-    const double beta = p.beta, x = beta * delta - p.margin, e = p.smoothing;
-    double loss, slope;
-    if (p.kind == 0) {
-      loss = (1.0 - e) * softplus(-x) + (e > 0.0 ? e * softplus(x) : 0.0);
-      slope = beta * (e * sigmoid(x) - (1.0 - e) * sigmoid(-x));
-    } else if (p.kind == 1) {
-      loss = x < 1.0 ? 1.0 - x : x != x ? x : 0.0;
-      slope = x < 1.0 ? -beta : x != x ? x : 0.0;
-    } else {
-      const double far = delta - 0.5 / beta;
-      loss = far * far;
-      slope = 2.0 * far;
-    }
-    if (!ok) loss = slope = 0.0;
-    p.pair_loss[pair] = static_cast<float>(loss);
-    p.coef[2 * pair] = static_cast<float>(slope * per[0]);
-    p.coef[2 * pair + 1] = static_cast<float>(-slope * per[1]);
-  }
+  if (tid == 0) pair_result(p, blockIdx.x, ok, s_sum, s_cnt);
   if (!last_block(p.st, static_cast<int>(p.P))) return;
   const double sum = block_total(p.pair_loss, p.P, s_red);
   if (tid == 0) *p.loss = static_cast<float>(sum * p.weight);
+}
+
+// The rows' log-probabilities and statistics from the partial sums, one block a row; the block that finishes last goes
+// through the few pairs (at most kPairsHere), a warp a sequence.
+__global__ void __launch_bounds__(kRowThreads) k_logp_pairs(const LossRowArgs p, const PairArgs q) {
+  grid_dep_wait();
+  grid_dep_launch();
+  __shared__ float red[kRowThreads / 32];
+  __shared__ RowSum s_rows[kGroups];
+  __shared__ double s_red[kRowThreads], s_sum[2 * kPairsHere];
+  __shared__ int s_cnt[2 * kPairsHere];
+  const int r = blockIdx.x, tid = threadIdx.x;
+  const int y = given_label(p.y, r, p.ignore_index, p.V);
+  float logp = 0.f;
+  RowStats s{0.f, 0.f};
+  if (y >= 0) {
+    s = merge_row(p, r, red, s_rows);
+    const float z = p.Z != nullptr ? p.Z[static_cast<long long>(r) * p.ldz + y] : p.ztgt[r];
+    logp = (z - s.M) * p.inv_t - s.logs;
+  }
+  if (tid == 0) {
+    p.logp[r] = logp;
+    p.stats[r] = make_float2(s.M, s.logs);
+    if (y < 0 && p.y[r] != p.ignore_index) atomicOr(&p.st->flags, kFlagLabelRange);
+  }
+  if (!last_block(p.st, static_cast<int>(q.N))) return;
+  if (tid == 0) pair_scales(q);
+  const int warp = tid >> 5;
+  if (warp < 2 * q.P) {
+    long long c[3];
+    pair_bounds(q, warp / 2, c);
+    double sum;
+    int cnt;
+    sequence_share(q, c[warp & 1], c[(warp & 1) + 1], tid & 31, 32, sum, cnt);
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    cnt = __reduce_add_sync(0xffffffffu, cnt);
+    if ((tid & 31) == 0) {
+      s_sum[warp] = sum;
+      s_cnt[warp] = cnt;
+    }
+  }
+  __syncthreads();
+  if (tid < q.P) {
+    long long c[3];
+    const bool ok = pair_bounds(q, tid, c);
+    pair_result(q, tid, ok, s_sum + 2 * tid, s_cnt + 2 * tid);
+    __threadfence();
+  }
+  __syncthreads();
+  const double sum = block_total(q.pair_loss, q.P, s_red);
+  if (tid == 0) *q.loss = static_cast<float>(sum * q.weight);
 }
 
 // The sequence that holds row r: the last whose first row is not behind r. -1 before the first, >= S behind the last.
@@ -457,6 +523,10 @@ cudaError_t launch_policy_total(const double* rows, long long N, const DevStatus
 
 cudaError_t launch_pairs(const PairArgs& p, cudaStream_t s) {
   return launch_k(k_pairs, static_cast<unsigned>(p.P > 0 ? p.P : 1), kRowThreads, 0, s, p);
+}
+
+cudaError_t launch_logp_pairs(const LossRowArgs& p, const PairArgs& q, int rows, cudaStream_t s) {
+  return launch_k(k_logp_pairs, rows, kRowThreads, 0, s, p, q);
 }
 
 cudaError_t launch_preference_row(const PreferenceArgs& p, int rows, cudaStream_t s) {

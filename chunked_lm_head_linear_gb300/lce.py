@@ -30,6 +30,7 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -807,6 +808,27 @@ def _token_plan(opt_kw, N, what, device, workspace, size):
     return opts, workspace
 
 
+_DEFAULT_OPTS = LceOpts(0, -100, -1, LCE_MEAN, 0, 0, 0)
+
+
+@functools.lru_cache(maxsize=256)
+def _default_size(what, *sizes):
+    """Workspace of a call with default options (small calls are bound by what happens here, a size by a C call)."""
+    return getattr(load(), what + "_workspace_size")(*sizes, None)
+
+
+def _loss_plan(opt_kw, what, sizes, device, workspace):
+    """_token_plan of a call whose workspace size is a function of sizes (N first) and the options."""
+    if opt_kw or workspace is not None:
+        return _token_plan(opt_kw, sizes[0], what, device, workspace,
+                           lambda o: getattr(load(), what + "_workspace_size")(*sizes, ctypes.byref(o)))
+    import torch
+    need = _default_size(what, *sizes)
+    if need == 0:
+        raise LCEError(LCE_ERR_INVALID_ARG, what + "_workspace_size")
+    return _DEFAULT_OPTS, torch.empty(need, dtype=torch.uint8, device=device)
+
+
 def _dW_mode(dW_dtype):
     """LCE_DW_BF16 for a bf16 dW, 0 for fp32 (the default)."""
     import torch
@@ -1046,6 +1068,11 @@ def _check_policy(H, W, y, advantages, old_logp, ref_logp, weights, kl, kl_coef,
     return N, d, V, LcePolicy(float(clip_low), float(clip_high), float(dual_clip or 0.0), float(kl_coef), LCE_KL[kl], 0)
 
 
+def _rows(device, *counts):
+    import torch
+    return [torch.empty(n, dtype=torch.float32, device=device) for n in counts]
+
+
 def lce_policy_forward(H, W, y, advantages, old_logp=None, ref_logp=None, *, weights=None, temperature: float = 1.0,
                        clip_low: float = 0.2, clip_high: float = 0.2, dual_clip: float = 0.0, kl="none",
                        kl_coef: float = 0.0, workspace=None, stream=None, **opt_kw):
@@ -1057,14 +1084,10 @@ def lce_policy_forward(H, W, y, advantages, old_logp=None, ref_logp=None, *, wei
     (0 or None: off) bounds the loss of negative advantages; kl is "none", "k1",
     "k2" or "k3". reduction="mean" divides by the number of given tokens (or
     n_valid_override)."""
-    import torch
     N, d, V, policy = _check_policy(H, W, y, advantages, old_logp, ref_logp, weights, kl, kl_coef, clip_low, clip_high,
                                     dual_clip)
-    opts, ws = _token_plan(opt_kw, N, "lce_policy", H.device, workspace,
-                           lambda o: lce_policy_workspace_size(N, d, V, False, 0, o))
-    loss = torch.empty(1, dtype=torch.float32, device=H.device)
-    logp = torch.empty(N, dtype=torch.float32, device=H.device)
-    row_loss = torch.empty(N, dtype=torch.float32, device=H.device)
+    opts, ws = _loss_plan(opt_kw, "lce_policy", (N, d, V, 0, 0), H.device, workspace)
+    loss, logp, row_loss = _rows(H.device, 1, N, N)
     rc = load().lce_policy_forward(_ptr(H), _ptr(W), _ptr(y), N, d, V, float(temperature), ctypes.byref(policy),
                                    _ptr(advantages), _ptr(old_logp), _ptr(ref_logp), _ptr(weights), _ptr(loss),
                                    _ptr(logp), _ptr(row_loss), ctypes.byref(opts), _ptr(ws), ws.numel(), _stream(stream))
@@ -1086,11 +1109,8 @@ def lce_policy_fwd_bwd(H, W, y, advantages, old_logp=None, ref_logp=None, grad_l
     _check_dev(grad_loss, "grad_loss", torch.float32, numel=1, device=H.device)
     grads = _dW_mode(dW_dtype)
     grads = grads if need_dW else 0
-    opts, ws = _token_plan(opt_kw, N, "lce_policy", H.device, workspace,
-                           lambda o: lce_policy_workspace_size(N, d, V, True, grads, o))
-    loss = torch.empty(1, dtype=torch.float32, device=H.device)
-    logp = torch.empty(N, dtype=torch.float32, device=H.device)
-    row_loss = torch.empty(N, dtype=torch.float32, device=H.device)
+    opts, ws = _loss_plan(opt_kw, "lce_policy", (N, d, V, 1, grads), H.device, workspace)
+    loss, logp, row_loss = _rows(H.device, 1, N, N)
     dH, dW = _token_grads(H, V, d, opts, grads, dW, need_dH, need_dW)
     rc = load().lce_policy_fwd_bwd(_ptr(H), _ptr(W), _ptr(y), N, d, V, float(temperature), ctypes.byref(policy),
                                    _ptr(advantages), _ptr(old_logp), _ptr(ref_logp), _ptr(weights), _ptr(grad_loss),
@@ -1132,13 +1152,9 @@ def lce_preference_forward(H, W, y, cu_seqlens, ref_logp=None, *, kind: str = "s
     ignore_index (prompts) and rows in no sequence do not count. kind is
     "sigmoid", "hinge" or "ipo"; reduction="mean" divides by P (or
     n_valid_override)."""
-    import torch
     N, d, V, P, pref = _check_preference(H, W, y, cu_seqlens, ref_logp, kind, beta, label_smoothing, margin, average)
-    opts, ws = _token_plan(opt_kw, N, "lce_preference", H.device, workspace,
-                           lambda o: lce_preference_workspace_size(N, d, V, P, False, 0, o))
-    loss = torch.empty(1, dtype=torch.float32, device=H.device)
-    pair_loss = torch.empty(P, dtype=torch.float32, device=H.device)
-    seq_logp = torch.empty(2 * P, dtype=torch.float32, device=H.device)
+    opts, ws = _loss_plan(opt_kw, "lce_preference", (N, d, V, P, 0, 0), H.device, workspace)
+    loss, pair_loss, seq_logp = _rows(H.device, 1, P, 2 * P)
     rc = load().lce_preference_forward(_ptr(H), _ptr(W), _ptr(y), N, d, V, _ptr(cu_seqlens), P, float(temperature),
                                        ctypes.byref(pref), _ptr(ref_logp), _ptr(loss), _ptr(pair_loss), _ptr(seq_logp),
                                        ctypes.byref(opts), _ptr(ws), ws.numel(), _stream(stream))
@@ -1160,11 +1176,8 @@ def lce_preference_fwd_bwd(H, W, y, cu_seqlens, ref_logp=None, grad_loss=None, *
     _check_dev(grad_loss, "grad_loss", torch.float32, numel=1, device=H.device)
     grads = _dW_mode(dW_dtype)
     grads = grads if need_dW else 0
-    opts, ws = _token_plan(opt_kw, N, "lce_preference", H.device, workspace,
-                           lambda o: lce_preference_workspace_size(N, d, V, P, True, grads, o))
-    loss = torch.empty(1, dtype=torch.float32, device=H.device)
-    pair_loss = torch.empty(P, dtype=torch.float32, device=H.device)
-    seq_logp = torch.empty(2 * P, dtype=torch.float32, device=H.device)
+    opts, ws = _loss_plan(opt_kw, "lce_preference", (N, d, V, P, 1, grads), H.device, workspace)
+    loss, pair_loss, seq_logp = _rows(H.device, 1, P, 2 * P)
     dH, dW = _token_grads(H, V, d, opts, grads, dW, need_dH, need_dW)
     rc = load().lce_preference_fwd_bwd(_ptr(H), _ptr(W), _ptr(y), N, d, V, _ptr(cu_seqlens), P, float(temperature),
                                        ctypes.byref(pref), _ptr(ref_logp), _ptr(grad_loss), grads, _ptr(loss),
@@ -1180,6 +1193,9 @@ def lce_preference_fwd_bwd(H, W, y, cu_seqlens, ref_logp=None, grad_loss=None, *
 # ---------------------------------------------------------------------------
 def lce_layernorm_workspace_size(N: int, d: int) -> int:
     return int(load().lce_layernorm_workspace_size(N, d))
+
+
+_norm_size = functools.lru_cache(maxsize=256)(lce_layernorm_workspace_size)
 
 
 def _check_layernorm(x, w, b):
@@ -1241,7 +1257,7 @@ def lce_layernorm_backward(x, w, mean, rstd, dH, *, bias: bool = True, need_dx: 
     dw = torch.empty(d, dtype=torch.float32, device=x.device) if need_dw else None
     db = torch.empty(d, dtype=torch.float32, device=x.device) if bias else None
     if need_dw or bias:
-        need = lce_layernorm_workspace_size(N, d)
+        need = _norm_size(N, d)
         if need == 0:
             raise LCEError(LCE_ERR_INVALID_ARG, "lce_layernorm_workspace_size")
         if workspace is None:
