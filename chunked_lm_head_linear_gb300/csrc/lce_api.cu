@@ -1581,15 +1581,26 @@ lce::LossRowArgs loss_row(const Call& c, const TokLayout& T, int64_t c0, const l
   return a;
 }
 
-// Before the chunks of a call by exp tiles: the status block, the count of given tokens and the scales, the
-// guards cleared, and the labels' logits.
-int exp_prepare(Call& c, const LossLayout& L, const float* grad_loss) {
-  c.L.guard = L.guard;  // prepare clears them
-  c.L.chunks = ceil_div(c.N, L.step);
-  LCE_TRY(prepare(c, grad_loss));
+// Before the chunks of a call by exp tiles: the labels' logits, with the status block, the guards and the dH part counters
+// cleared; counted: the given tokens counted and the scales set too, by a launch of its own.
+int exp_prepare(Call& c, const LossLayout& L, const float* grad_loss, bool counted) {
+  const int launches = static_cast<int>(ceil_div(c.N, L.step));
+  lce::LossClear clear;
+  std::memset(&clear, 0, sizeof clear);
+  if (counted || lce::kChecks) {
+    c.L.guard = L.guard;  // prepare clears them
+    c.L.chunks = launches;
+    LCE_TRY(prepare(c, grad_loss));
+  } else {
+    clear.st = c.st;
+    clear.guards = reinterpret_cast<int*>(c.ws + L.guard);
+    clear.nguards = launches;
+    clear.cnt = reinterpret_cast<int*>(c.ws + c.L.dh_cnt);
+    clear.ncnt = c.L.dh_ncnt;
+  }
   return timed(c.s, K_PREPARE, static_cast<double>(c.N) * (4.0 * static_cast<double>(c.d) + 12.0), [&] {
     return cuda_rc(lce::launch_label_logits(c.H, c.W, c.y, c.N, static_cast<int>(c.d), static_cast<int>(c.V),
-                                            c.o.ignore_index, reinterpret_cast<float*>(c.ws + L.ref), c.s));
+                                            c.o.ignore_index, reinterpret_cast<float*>(c.ws + L.ref), clear, c.s));
   });
 }
 
@@ -1658,11 +1669,10 @@ int policy_loss(const void* H, const void* W, const int64_t* y, int64_t N, int64
   const TokLayout& T = L.tok;
   Call c;
   LCE_TRY(tok_begin(&c, T, H, W, y, N, d, V, o, ws, ws_bytes, stream));
-  // With one chunk its rows count themselves, before the GEMMs that need n; with several n is needed by
-  // the first chunk's.
-  const bool count_here = !lce::kChecks && c.L.chunks == 1 && !L.exp;
+  // With one backward launch the rows before it count themselves; with several n is needed by the first chunk's.
+  const bool count_here = !lce::kChecks && c.L.chunks == 1;
   if (L.exp)
-    LCE_TRY(exp_prepare(c, L, grad_loss));
+    LCE_TRY(exp_prepare(c, L, grad_loss, !count_here));
   else if (!count_here)
     LCE_TRY(prepare(c, grad_loss));
   if (N == 0 && with_grad) LCE_TRY(zero_dW(c, dW, dW_bf16));
@@ -1674,7 +1684,7 @@ int policy_loss(const void* H, const void* W, const int64_t* y, int64_t N, int64
     p.partials += at * p.nparts;
     p.ztgt += at;
     int* guard = L.exp ? reinterpret_cast<int*>(c.ws + L.guard) + k : nullptr;
-    if (count_here) {
+    if (count_here && !L.exp) {
       p.clear_st = c.st;
       p.cnt = with_grad ? reinterpret_cast<int*>(c.ws + c.L.dh_cnt) : nullptr;
       p.ncnt = with_grad ? c.L.dh_ncnt : 0;
@@ -1761,7 +1771,7 @@ int preference_loss(const void* H, const void* W, const int64_t* y, int64_t N, i
   float* Z = with_grad && one && !L.exp ? reinterpret_cast<float*>(c.ws + T.Z) : nullptr;
   int* guard = L.exp ? reinterpret_cast<int*>(c.ws + L.guard) : nullptr;
   if (L.exp)
-    LCE_TRY(exp_prepare(c, L, grad_loss));
+    LCE_TRY(exp_prepare(c, L, grad_loss, false));
   else if (lce::kChecks || N == 0)
     LCE_TRY(prepare(c, grad_loss));
   if (N == 0 && with_grad) LCE_TRY(zero_dW(c, dW, dW_bf16));

@@ -492,9 +492,17 @@ struct PreferenceArgs {
   const float* coef;       // [2 P]
 };
 
+// What the first launch of a call by exp tiles clears (st null: nothing).
+struct LossClear {
+  DevStatus* st;
+  int* guards;
+  int nguards;
+  int* cnt;
+  int ncnt;
+};
 // The labels' logits z_{i,y_i} of N rows (0 where none is given).
 cudaError_t launch_label_logits(const void* H, const void* W, const int64_t* y, long long N, int d, int V,
-                                long long ignore_index, float* z, cudaStream_t s);
+                                long long ignore_index, float* z, const LossClear& clear, cudaStream_t s);
 // Preference loss from the exp tile: logp, and rest or (where *guard is set) stats.
 cudaError_t launch_exp_logp(const LossRowArgs& p, int rows, cudaStream_t s);
 cudaError_t launch_policy_row(const PolicyArgs& p, int rows, cudaStream_t s);

@@ -443,6 +443,7 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_exp_logp(const LossRowArgs p
     p.logp[r] = logp;
     p.rest[r] = rest;
     p.stats[r] = make_float2(s.M, s.logs);
+    if (y < 0 && p.y[r] != p.ignore_index) atomicOr(&p.st->flags, kFlagLabelRange);
   }
 }
 
@@ -467,12 +468,18 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_preference_row(const Prefere
   row_gradient<TILE>(q, r, y, a, q.logp[r], RowStats{st.x, st.y});
 }
 
-// One warp per row: H_i . W_{y_i} in fp32.
+// One warp per row: H_i . W_{y_i} in fp32. The call's first launch: its first block clears the status block, the
+// guards and the dH part counters (clear.st null: an earlier launch did).
 __global__ void __launch_bounds__(256) k_label_logits(const uint4* __restrict__ H, const uint4* __restrict__ W,
                                                       const int64_t* __restrict__ y, long long N, int groups, int V,
-                                                      long long ignore_index, float* __restrict__ z) {
+                                                      long long ignore_index, float* __restrict__ z, const LossClear clear) {
   grid_dep_wait();
   grid_dep_launch();
+  if (clear.st != nullptr && blockIdx.x == 0) {
+    for (int i = threadIdx.x; i < clear.nguards; i += blockDim.x) clear.guards[i] = 0;
+    for (int i = threadIdx.x; i < clear.ncnt; i += blockDim.x) clear.cnt[i] = 0;
+    if (threadIdx.x == 0) *clear.st = DevStatus{};
+  }
   const long long r = (blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (r >= N) return;
@@ -499,10 +506,10 @@ __global__ void __launch_bounds__(256) k_label_logits(const uint4* __restrict__ 
 }  // namespace
 
 cudaError_t launch_label_logits(const void* H, const void* W, const int64_t* y, long long N, int d, int V,
-                                long long ignore_index, float* z, cudaStream_t s) {
+                                long long ignore_index, float* z, const LossClear& clear, cudaStream_t s) {
   if (N <= 0) return cudaSuccess;
   return launch_k(k_label_logits, static_cast<unsigned>((N + 7) / 8), 256, 0, s, static_cast<const uint4*>(H),
-                  static_cast<const uint4*>(W), y, N, d / 8, V, ignore_index, z);
+                  static_cast<const uint4*>(W), y, N, d / 8, V, ignore_index, z, clear);
 }
 
 cudaError_t launch_exp_logp(const LossRowArgs& p, int rows, cudaStream_t s) {

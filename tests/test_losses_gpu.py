@@ -104,7 +104,8 @@ def call_policy(lce, Ht, Wt, yt, inp, grad=True, **kw):
     return lce.lce_policy_forward(Ht, Wt, yt, *args[:3], weights=args[3], **kw)
 
 
-def check_policy(out, H, W, y, inp, *, T=1.0, ignore=-100, chunk=0, **kw):
+def check_policy(outs, H, W, y, inp, *, T=1.0, ignore=-100, chunk=0, **kw):
+    """One call's outputs, or a list of such, against the oracle."""
     reduction = dict(mean=oracle.MEAN, sum=1)[kw.pop("reduction", "mean")]
     args = [None if inp[k] is None else np.nan_to_num(inp[k].astype(np.float64)) for k in
             ("advantages", "old_logp", "ref_logp", "weights")]
@@ -126,19 +127,20 @@ def check_policy(out, H, W, y, inp, *, T=1.0, ignore=-100, chunk=0, **kw):
         row_tol = row_tol + beta * (np.abs(d) * e_u + e_u ** 2 + 2.0 ** -20 * (np.abs(value) + np.abs(u) + np.exp(-u)))
         a_tol = a_tol + beta * ((1 + np.abs(d)) * e_u + 2.0 ** -20 * (1 + np.abs(d)))
     row_tol, a_tol = np.where(told, row_tol * np.abs(w), 0.0), np.where(told, a_tol * np.abs(w), 0.0)
-    loss, got_logp, row = out[:3]
-    close(got_logp, ref["logp"], np.where(told, tol, 0.0), "logp")
-    close(row, ref["row_loss"], row_tol + 2.0 ** -22 * np.abs(ref["row_loss"]), "row_loss")
     n = kw.get("n_valid_override", -1)
     weight = 1.0 if reduction == 1 else 1.0 / max(n if n >= 0 else int(told.sum()), 1)
     if n == 0 and reduction != 1:
         weight = 0.0
-    close(loss, np.array([ref["loss"]]), row_tol.sum() * weight + 2 * EPS * (abs(ref["loss"]) + np.abs(ref["row_loss"]).sum() * weight) + 1e-30,
-          "loss")
-    if len(out) == 5:
-        slack = oracle.head_gradients_f64(H, W, y, a_tol * weight * abs(scale_kw.get("grad_loss", 1.0)), temperature=T,
-                                          ignore_index=ignore)
-        check_gradients(out[3], out[4], ref, slack, uses_exp_tiles(*H.shape[:1], W.shape[0], chunk))
+    slack = oracle.head_gradients_f64(H, W, y, a_tol * weight * abs(scale_kw.get("grad_loss", 1.0)), temperature=T,
+                                      ignore_index=ignore)
+    for out in outs if isinstance(outs, list) else [outs]:
+        loss, got_logp, row = out[:3]
+        close(got_logp, ref["logp"], np.where(told, tol, 0.0), "logp")
+        close(row, ref["row_loss"], row_tol + 2.0 ** -22 * np.abs(ref["row_loss"]), "row_loss")
+        close(loss, np.array([ref["loss"]]), row_tol.sum() * weight + 2 * EPS * (abs(ref["loss"]) + np.abs(ref["row_loss"]).sum() * weight) + 1e-30,
+              "loss")
+        if len(out) == 5:
+            check_gradients(out[3], out[4], ref, slack, uses_exp_tiles(len(y), W.shape[0], chunk))
     return ref
 
 
@@ -173,11 +175,11 @@ def test_policy(cuda_lib, N, d, V, T, chunk, kl, old, weights, dual):
     Ht, Wt = heads(H, W)
     inp = policy_inputs(rng, H, W, y, T, kl, old, weights, dual=dual)
     kw = dict(clip_low=0.2, clip_high=0.28, dual_clip=dual, kl=kl, kl_coef=0.0 if kl == "none" else 0.3)
-    for dt in (torch.float32, torch.bfloat16):
-        out = call_policy(cuda_lib, Ht, Wt, dev(y), inp, temperature=T, chunk_tokens=chunk, dW_dtype=dt, sync_check=True, **kw)
-        check_policy(out, H, W, y, inp, T=T, chunk=chunk, **kw)
-    fwd = call_policy(cuda_lib, Ht, Wt, dev(y), inp, grad=False, temperature=T, chunk_tokens=chunk, sync_check=True, **kw)
-    check_policy(fwd, H, W, y, inp, T=T, **kw)
+    outs = [call_policy(cuda_lib, Ht, Wt, dev(y), inp, temperature=T, chunk_tokens=chunk, dW_dtype=dt, sync_check=True, **kw)
+            for dt in (torch.float32, torch.bfloat16)]
+    out = outs[-1]
+    outs.append(call_policy(cuda_lib, Ht, Wt, dev(y), inp, grad=False, temperature=T, chunk_tokens=chunk, sync_check=True, **kw))
+    check_policy(outs, H, W, y, inp, T=T, chunk=chunk, **kw)
     again = call_policy(cuda_lib, Ht, Wt, dev(y), inp, temperature=T, chunk_tokens=chunk, dW_dtype=torch.bfloat16, **kw)
     for a, b in zip(out, again):
         assert torch.equal(a, b)
@@ -308,7 +310,8 @@ def call_preference(lce, Ht, Wt, y, cu, ref, grad=True, **kw):
     return lce.lce_preference_forward(Ht, Wt, dev(y), dev(cu), r, **kw)
 
 
-def check_preference(out, H, W, y, cu, ref_logp, *, T=1.0, average=False, chunk=0, **kw):
+def check_preference(outs, H, W, y, cu, ref_logp, *, T=1.0, average=False, chunk=0, **kw):
+    """One call's outputs, or a list of such, against the oracle."""
     reduction = dict(mean=oracle.MEAN, sum=1)[kw.pop("reduction", "mean")]
     rl = None if ref_logp is None else f32(ref_logp).astype(np.float64)
     ref = oracle.preference_f64(H, W, y, cu, rl, temperature=T, average=average, reduction=reduction, **kw)
@@ -320,7 +323,6 @@ def check_preference(out, H, W, y, cu, ref_logp, *, T=1.0, average=False, chunk=
         rows = rows[told[rows]]
         per[s] = 1.0 / max(len(rows), 1) if average else 1.0
         ts[s] = tol[rows].sum() * per[s]
-    close(out[2], ref["seq_logp"], ts + 2 * EPS * np.abs(ref["seq_logp"]), "seq_logp")
     td = ts[0::2] + ts[1::2] + (0 if rl is None else EPS * (np.abs(rl[0::2]) + np.abs(rl[1::2])))
     beta = float(np.float32(kw.get("beta", 0.1)))
     kind = kw.get("kind", "sigmoid")
@@ -336,22 +338,24 @@ def check_preference(out, H, W, y, cu, ref_logp, *, T=1.0, average=False, chunk=
     else:
         pair_tol = tx * (1.0 if kind == "hinge" else np.minimum(1.0, np.abs(slope) / beta + tx)) + 2 * EPS * (1 + beta * delta)
         slope_tol = 0 * td if kind == "hinge" else beta * np.minimum(1.0, np.abs(slope) / beta + tx) * tx + 4 * EPS * beta
-    close(out[1], ref["pair_loss"], pair_tol + 2.0 ** -22 * np.abs(ref["pair_loss"]), "pair_loss")
     n = kw.get("n_valid_override", -1)
     n = n if n >= 0 else S // 2
     weight = 1.0 if reduction == 1 else (1.0 / n if n else 0.0)
-    close(out[0], np.array([ref["loss"]]), (pair_tol.sum() + 2.0 ** -22 * np.abs(ref["pair_loss"]).sum()) * weight + 1e-30, "loss")
-    if len(out) == 5:
-        a = np.zeros(len(y))
-        for s in range(S):
-            a[cu[s]:cu[s + 1]] = (slope_tol[s // 2] + 2.0 ** -22 * abs(slope[s // 2])) * per[s] * weight
-        a = np.where(told, a, 0.0) * abs(kw.get("grad_loss", 1.0))
-        slack = oracle.head_gradients_f64(H, W, y, a, temperature=T)
-        check_gradients(out[3], out[4], ref, slack, uses_exp_tiles(len(y), W.shape[0], chunk))
-        outside = np.ones(len(y), bool)
-        outside[cu[0]:cu[-1]] = False
-        if out[3] is not None:
-            assert not np64(out[3])[outside | ~told].any()
+    a = np.zeros(len(y))
+    for s in range(S):
+        a[cu[s]:cu[s + 1]] = (slope_tol[s // 2] + 2.0 ** -22 * abs(slope[s // 2])) * per[s] * weight
+    a = np.where(told, a, 0.0) * abs(kw.get("grad_loss", 1.0))
+    slack = oracle.head_gradients_f64(H, W, y, a, temperature=T)
+    outside = np.ones(len(y), bool)
+    outside[cu[0]:cu[-1]] = False
+    for out in outs if isinstance(outs, list) else [outs]:
+        close(out[2], ref["seq_logp"], ts + 2 * EPS * np.abs(ref["seq_logp"]), "seq_logp")
+        close(out[1], ref["pair_loss"], pair_tol + 2.0 ** -22 * np.abs(ref["pair_loss"]), "pair_loss")
+        close(out[0], np.array([ref["loss"]]), (pair_tol.sum() + 2.0 ** -22 * np.abs(ref["pair_loss"]).sum()) * weight + 1e-30, "loss")
+        if len(out) == 5:
+            check_gradients(out[3], out[4], ref, slack, uses_exp_tiles(len(y), W.shape[0], chunk))
+            if out[3] is not None:
+                assert not np64(out[3])[outside | ~told].any()
     return ref
 
 
@@ -378,8 +382,7 @@ PREFERENCE_CASES = [
 
 
 @pytest.mark.parametrize("N,d,V,pairs,T,chunk,kind,average,ref", PREFERENCE_CASES)
-@pytest.mark.parametrize("int32", [False, True])
-def test_preference(cuda_lib, N, d, V, pairs, T, chunk, kind, average, ref, int32):
+def test_preference(cuda_lib, N, d, V, pairs, T, chunk, kind, average, ref):
     torch = _torch()
     rng, H, W, y = make(N, d, V, seed=N + V)
     Ht, Wt = heads(H, W)
@@ -394,13 +397,13 @@ def test_preference(cuda_lib, N, d, V, pairs, T, chunk, kind, average, ref, int3
         x = np.where(np.abs(x - 0.25 - 1.0) < 0.05, 1.4, x)      # away from the hinge's corner
         rl = f32(seq + rng.standard_normal(2 * pairs))
         rl[0::2] = (seq[0::2] - seq[1::2]) + rl[1::2].astype(np.float64) - x / beta
-    c = cu.astype(np.int32) if int32 else cu
-    for dt in (torch.float32, torch.bfloat16):
-        out = call_preference(cuda_lib, Ht, Wt, y, c, rl, temperature=T, chunk_tokens=chunk, dW_dtype=dt, sync_check=True, **kw)
-        check_preference(out, H, W, y, cu, rl, T=T, chunk=chunk, **kw)
-    fwd = call_preference(cuda_lib, Ht, Wt, y, c, rl, grad=False, temperature=T, chunk_tokens=chunk, sync_check=True, **kw)
-    check_preference(fwd, H, W, y, cu, rl, T=T, **kw)
-    again = call_preference(cuda_lib, Ht, Wt, y, c, rl, temperature=T, chunk_tokens=chunk, dW_dtype=torch.bfloat16, **kw)
+    narrow = cu.astype(np.int32)
+    outs = [call_preference(cuda_lib, Ht, Wt, y, c, rl, temperature=T, chunk_tokens=chunk, dW_dtype=dt, sync_check=True, **kw)
+            for dt, c in ((torch.float32, narrow), (torch.bfloat16, cu))]
+    out = outs[-1]
+    outs.append(call_preference(cuda_lib, Ht, Wt, y, narrow, rl, grad=False, temperature=T, chunk_tokens=chunk, sync_check=True, **kw))
+    check_preference(outs, H, W, y, cu, rl, T=T, chunk=chunk, **kw)
+    again = call_preference(cuda_lib, Ht, Wt, y, narrow, rl, temperature=T, chunk_tokens=chunk, dW_dtype=torch.bfloat16, **kw)
     for a, b in zip(out, again):
         assert torch.equal(a, b)
 
@@ -479,6 +482,72 @@ def test_preference_bad_bounds_no_pairs_and_no_rows(cuda_lib):
         inp = dict(advantages=f32([]), old_logp=None, ref_logp=None, weights=None)
         out = call_policy(cuda_lib, Ht[:0], Wt, dev(y[:0]), inp, dW_dtype=dt, sync_check=True)
         assert out[0].item() == 0 and out[3].shape == (0, 64) and not out[4].any()
+
+
+# --------------------------------------------------------------------------- the heads' real sizes
+@pytest.mark.parametrize("N,d,V,chunk", [(70, 2048, 151936, 0), (6500, 2048, 151936, 0), (700, 7168, 151655, 512),
+                                         (16500, 64, 151655, 0)])
+def test_full_heads_sampled(cuda_lib, N, d, V, chunk):
+    """Few rows with kept logits, exp tiles of two launches behind one backward, two chunks of the widest head, a tile of
+    more than 2^31 entries: rows of both sides of every boundary and vocabulary rows of the tails, against fp64."""
+    torch = _torch()
+    g = torch.Generator(device="cuda").manual_seed(N)
+    sigma = 0.02 if d <= 2048 else 0.01
+    if d == 64:
+        sigma = 0.1
+    W = (torch.randn(V, d, generator=g, device="cuda") * (sigma * 1024)).round().clamp(-127, 127).div(1024).bfloat16()
+    y = torch.randint(0, V, (N,), generator=g, device="cuda")
+    H = torch.randn(N, d, generator=g, device="cuda")
+    H += W[y].float() * (14.0 * torch.rand(N, 1, generator=g, device="cuda") / (sigma * sigma * d))
+    H = (H * 16).round().clamp(-127, 127).div(16).bfloat16()
+    y[::17] = oracle.IGNORE_INDEX
+    edge = chunk or {70: 35, 6500: 3328, 16500: 4352}[N]
+    rows = np.unique([0, 1, edge - 1, edge, edge + 1, N // 3, N - 2, N - 1])
+    cols = np.array([0, 127, 128, 255, 256, V // 2, V - 130, V - 2, V - 1])
+    Hn, Wn, yn = np64(H), np64(W), y.cpu().numpy()
+    lse = torch.cat([torch.logsumexp(H[r:r + 512].double() @ W.double().t(), 1) for r in range(0, N, 512)]).cpu().numpy()
+    told = yn >= 0
+    logp = np.where(told, (Hn * Wn[np.where(told, yn, 0)]).sum(1) - lse, 0.0)
+    p = np.exp(Hn @ Wn[cols].T - lse[:, None])
+    hot = (yn[:, None] == cols[None, :]).astype(float)
+    exp = uses_exp_tiles(N, V, chunk)
+    at = torch.from_numpy(rows).cuda()
+
+    def check(dH, dW, a):   # a: d loss / d logp
+        a = np.where(told, a, 0.0)
+        part = oracle.head_gradients_f64(Hn[rows], Wn, yn[rows], a[rows])
+        none = {"dH_bulk": 2.0 ** -11 * part["dH_bulk"]}          # what logp's error does to a
+        check_gradients(dH[at], None, part, none, exp)
+        G = (hot - p) * a[:, None]
+        size = (hot + p) * np.abs(a)[:, None]
+        bulk = size.T @ np.abs(Hn)
+        check_gradients(None, dW[torch.from_numpy(cols).cuda()], {"dW": G.T @ Hn, "dW_bulk": bulk}, {"dW_bulk": 2.0 ** -11 * bulk}, exp)
+
+    rng = np.random.default_rng(1)
+    A = f32(rng.standard_normal(N))
+    old = f32(logp - 0.05)                                        # every ratio inside the range
+    loss, got, row, dH, dW = cuda_lib.lce_policy_fwd_bwd(H, W, y, dev(A), dev(old), dW_dtype=torch.bfloat16, chunk_tokens=chunk,
+                                                         sync_check=True)
+    n = int(told.sum())
+    r = np.exp(logp - old)
+    close(got, logp, 2.0 ** -14, "logp")
+    close(row, np.where(told, -r * A, 0.0), 2.0 ** -12 * np.abs(A) + 1e-30, "row_loss")
+    close(loss, np.array([-(r * A)[told].sum() / n]), 2.0 ** -12 * np.abs(A[told]).mean(), "loss")
+    check(dH, dW, -r * A / n)
+    fwd = cuda_lib.lce_policy_forward(H, W, y, dev(A), dev(old), chunk_tokens=chunk)
+    close(fwd[1], logp, 2.0 ** -14, "logp of the forward")
+    pairs = 3
+    cu = bounds(rng, N, pairs, 0, N // 20)
+    out = cuda_lib.lce_preference_fwd_bwd(H, W, y, dev(cu), average=True, beta=2.0, chunk_tokens=chunk, sync_check=True)
+    seq = np.array([logp[cu[s]:cu[s + 1]][told[cu[s]:cu[s + 1]]].mean() for s in range(2 * pairs)])
+    count = np.array([told[cu[s]:cu[s + 1]].sum() for s in range(2 * pairs)])
+    pl, slope = oracle.preference_pairs_f64(seq, beta=2.0)
+    close(out[2], seq, 2.0 ** -14, "seq_logp")
+    close(out[1], pl, 2.0 ** -11, "pair_loss")
+    a = np.zeros(N)
+    for s in range(2 * pairs):
+        a[cu[s]:cu[s + 1]] = (slope[s // 2] if s % 2 == 0 else -slope[s // 2]) / pairs / count[s]
+    check(out[3], out[4], a)
 
 
 # --------------------------------------------------------------------------- exp tiles
