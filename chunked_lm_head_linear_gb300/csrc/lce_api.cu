@@ -1633,7 +1633,7 @@ void loss_row_exp(lce::LossRowArgs* a, const Call& c, const LossLayout& L, const
 
 // Few short pairs: the last of the rows' blocks goes through them in place of a launch (250 rows in 2 pairs: 50 -> 43 us a
 // call, bound by the host).
-bool with_pairs(int64_t N, int64_t pairs) { return pairs <= lce::kPairsHere && N <= 4096; }
+bool with_pairs(int64_t N, int64_t pairs) { return pairs <= lce::kPairsHere && N <= 1024; }
 
 double loss_row_bytes(const Call& c, int64_t rows, bool with_grad, bool with_z) {
   return static_cast<double>(rows) * ((with_grad && !with_z ? 8.0 : 32.0) * static_cast<double>(c.L.T) + 40.0 +
@@ -1799,7 +1799,7 @@ int preference_loss(const void* H, const void* W, const int64_t* y, int64_t N, i
   const int64_t n = o.n_valid_override >= 0 ? o.n_valid_override : pairs;
   q.weight = o.reduction == LCE_SUM ? 1.0 : n > 0 ? 1.0 / static_cast<double>(n) : 0.0;
   q.st = c.st;
-  const bool pairs_here = with_pairs(N, pairs) && one && !L.exp;  // the rows' launch goes through the pairs
+  const bool pairs_here = with_pairs(N, pairs) && N > 0 && N <= L.step;  // the rows' launch goes through the pairs
   // every row's log-probability
   for (int64_t k = 0, c0 = 0; c0 < N; ++k, c0 += L.step) {
     const int64_t rows = (N - c0) < L.step ? (N - c0) : L.step;
@@ -1813,7 +1813,7 @@ int preference_loss(const void* H, const void* W, const int64_t* y, int64_t N, i
       a.stats = stats + c0;
       loss_row_exp(&a, c, L, guard + k, c0);
       LCE_TRY(timed(c.s, K_COMBINE, static_cast<double>(rows) * (8.0 * static_cast<double>(c.L.T) + 28.0),
-                    [&] { return cuda_rc(lce::launch_exp_logp(a, static_cast<int>(rows), c.s)); }));
+                    [&] { return cuda_rc(lce::launch_logp_rows(a, q, pairs_here, static_cast<int>(rows), c.s)); }));
       continue;
     }
     if (!lce::kChecks && c0 == 0) {
@@ -1822,30 +1822,11 @@ int preference_loss(const void* H, const void* W, const int64_t* y, int64_t N, i
       p.ncnt = with_grad ? c.L.dh_ncnt : 0;
     }
     LCE_TRY(tok_logits(c, c0, rows, Z ? lce::TOK_STATS_Z : lce::TOK_STATS, Z, T.ldz, p));
-    if (pairs_here) {
-      lce::LossRowArgs a = loss_row(c, T, c0, p, Z, false, false, 0);
-      a.logp = logp;
-      a.stats = stats;
-      LCE_TRY(timed(c.s, K_COMBINE, loss_row_bytes(c, rows, false, false) + 12.0 * static_cast<double>(N),
-                    [&] { return cuda_rc(lce::launch_logp_pairs(a, q, static_cast<int>(rows), c.s)); }));
-      continue;
-    }
-    lce::TokScoreArgs a;
-    std::memset(&a, 0, sizeof a);
-    a.rows = p.rows;
-    a.V = p.V;
-    a.nparts = p.nparts;
-    a.ldz = T.ldz;
-    a.inv_t = p.inv_t;
-    a.ignore_index = p.ignore_index;
-    a.y = p.y;
-    a.partials = p.partials;
-    a.ztgt = p.ztgt;
-    a.Z = Z;
+    lce::LossRowArgs a = loss_row(c, T, c0, p, Z, false, false, 0);
     a.logp = logp + c0;
     a.stats = stats + c0;
-    a.flags = p.flags;
-    LCE_TRY(timed(c.s, K_COMBINE, loss_row_bytes(c, rows, false, false), [&] { return cuda_rc(lce::launch_score(a, c.s)); }));
+    LCE_TRY(timed(c.s, K_COMBINE, loss_row_bytes(c, rows, false, false),
+                  [&] { return cuda_rc(lce::launch_logp_rows(a, q, pairs_here, static_cast<int>(rows), c.s)); }));
   }
   if (!pairs_here)
     LCE_TRY(timed(c.s, K_COMBINE, 12.0 * static_cast<double>(N) + 28.0 * static_cast<double>(pairs),

@@ -503,14 +503,13 @@ struct LossClear {
 // The labels' logits z_{i,y_i} of N rows (0 where none is given).
 cudaError_t launch_label_logits(const void* H, const void* W, const int64_t* y, long long N, int d, int V,
                                 long long ignore_index, float* z, const LossClear& clear, cudaStream_t s);
-// Preference loss from the exp tile: logp, and rest or (where *guard is set) stats.
-cudaError_t launch_exp_logp(const LossRowArgs& p, int rows, cudaStream_t s);
 cudaError_t launch_policy_row(const PolicyArgs& p, int rows, cudaStream_t s);
 cudaError_t launch_policy_total(const double* rows, long long N, const DevStatus* st, float* loss, cudaStream_t s);
 cudaError_t launch_pairs(const PairArgs& p, cudaStream_t s);
-// The statistics and log-probabilities of a call's rows (one chunk) and its pairs, at most kPairsHere, in one launch.
+// Preference loss: logp and stats (or, by an exp tile, rest) of rows; with_pairs: those of a whole call, whose pairs, at
+// most kPairsHere, are done in the same launch.
 constexpr int kPairsHere = 4;
-cudaError_t launch_logp_pairs(const LossRowArgs& p, const PairArgs& q, int rows, cudaStream_t s);
+cudaError_t launch_logp_rows(const LossRowArgs& p, const PairArgs& q, bool with_pairs, int rows, cudaStream_t s);
 cudaError_t launch_preference_row(const PreferenceArgs& p, int rows, cudaStream_t s);
 
 // GEMM tile geometry (must match the kernels): each CTA of a pair loads 128

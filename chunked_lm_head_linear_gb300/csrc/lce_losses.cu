@@ -356,9 +356,11 @@ __global__ void __launch_bounds__(kRowThreads) k_pairs(const PairArgs p) {
   if (tid == 0) *p.loss = static_cast<float>(sum * p.weight);
 }
 
-// The rows' log-probabilities and statistics from the partial sums, one block a row; the block that finishes last goes
-// through the few pairs (at most kPairsHere), a warp a sequence.
-__global__ void __launch_bounds__(kRowThreads) k_logp_pairs(const LossRowArgs p, const PairArgs q) {
+// The rows' log-probabilities with what the gradient needs of them again, one block a row: from the exp tile's sums
+// (EXP, unless its guard is set) or the partial sums. PAIRS: the block that finishes last goes through the few pairs (at
+// most kPairsHere), a warp a sequence.
+template <bool EXP, bool PAIRS>
+__global__ void __launch_bounds__(kRowThreads) k_logp_rows(const LossRowArgs p, const PairArgs q) {
   grid_dep_wait();
   grid_dep_launch();
   __shared__ float red[kRowThreads / 32];
@@ -367,18 +369,25 @@ __global__ void __launch_bounds__(kRowThreads) k_logp_pairs(const LossRowArgs p,
   __shared__ int s_cnt[2 * kPairsHere];
   const int r = blockIdx.x, tid = threadIdx.x;
   const int y = given_label(p.y, r, p.ignore_index, p.V);
-  float logp = 0.f;
+  float logp = 0.f, rest = 0.f;
   RowStats s{0.f, 0.f};
   if (y >= 0) {
-    s = merge_row(p, r, red, s_rows);
-    const float z = p.Z != nullptr ? p.Z[static_cast<long long>(r) * p.ldz + y] : p.ztgt[r];
-    logp = (z - s.M) * p.inv_t - s.logs;
+    if (EXP && *p.guard == 0) {
+      rest = exp_rest(p, r, red);
+      logp = -log1pf(rest);
+    } else {
+      s = merge_row(p, r, red, s_rows);
+      const float z = p.Z != nullptr ? p.Z[static_cast<long long>(r) * p.ldz + y] : p.ztgt[r];
+      logp = (z - s.M) * p.inv_t - s.logs;
+    }
   }
   if (tid == 0) {
     p.logp[r] = logp;
     p.stats[r] = make_float2(s.M, s.logs);
+    if (EXP) p.rest[r] = rest;
     if (y < 0 && p.y[r] != p.ignore_index) atomicOr(&p.st->flags, kFlagLabelRange);
   }
+  if (!PAIRS) return;
   if (!last_block(p.st, static_cast<int>(q.N))) return;
   if (tid == 0) pair_scales(q);
   const int warp = tid >> 5;
@@ -418,33 +427,6 @@ __device__ __forceinline__ long long sequence_of(const void* cu, int cu32, long 
       hi = mid;
   }
   return lo - 1;
-}
-
-// The rows' log-probabilities from the exp tile, with what the gradient needs of them again.
-__global__ void __launch_bounds__(kRowThreads, 8) k_exp_logp(const LossRowArgs p) {
-  grid_dep_wait();
-  grid_dep_launch();
-  __shared__ float red[kRowThreads / 32];
-  __shared__ RowSum s_sum[kGroups];
-  const int r = blockIdx.x;
-  const int y = given_label(p.y, r, p.ignore_index, p.V);
-  float logp = 0.f, rest = 0.f;
-  RowStats s{0.f, 0.f};
-  if (y >= 0) {
-    if (*p.guard == 0) {
-      rest = exp_rest(p, r, red);
-      logp = -log1pf(rest);
-    } else {
-      s = merge_row(p, r, red, s_sum);
-      logp = (p.ztgt[r] - s.M) * p.inv_t - s.logs;
-    }
-  }
-  if (threadIdx.x == 0) {
-    p.logp[r] = logp;
-    p.rest[r] = rest;
-    p.stats[r] = make_float2(s.M, s.logs);
-    if (y < 0 && p.y[r] != p.ignore_index) atomicOr(&p.st->flags, kFlagLabelRange);
-  }
 }
 
 // One block per row of the chunk, once the pairs' factors are known.
@@ -512,11 +494,6 @@ cudaError_t launch_label_logits(const void* H, const void* W, const int64_t* y, 
                   static_cast<const uint4*>(W), y, N, d / 8, V, ignore_index, z, clear);
 }
 
-cudaError_t launch_exp_logp(const LossRowArgs& p, int rows, cudaStream_t s) {
-  if (rows <= 0) return cudaSuccess;
-  return launch_k(k_exp_logp, rows, kRowThreads, 0, s, p);
-}
-
 cudaError_t launch_policy_row(const PolicyArgs& p, int rows, cudaStream_t s) {
   if (rows <= 0) return cudaSuccess;
   if (p.row.rowscale == nullptr) return launch_k(k_policy_row<false, false, false>, rows, kRowThreads, 0, s, p);
@@ -532,8 +509,13 @@ cudaError_t launch_pairs(const PairArgs& p, cudaStream_t s) {
   return launch_k(k_pairs, static_cast<unsigned>(p.P > 0 ? p.P : 1), kRowThreads, 0, s, p);
 }
 
-cudaError_t launch_logp_pairs(const LossRowArgs& p, const PairArgs& q, int rows, cudaStream_t s) {
-  return launch_k(k_logp_pairs, rows, kRowThreads, 0, s, p, q);
+cudaError_t launch_logp_rows(const LossRowArgs& p, const PairArgs& q, bool with_pairs, int rows, cudaStream_t s) {
+  if (rows <= 0) return cudaSuccess;
+  if (p.sums != nullptr)
+    return with_pairs ? launch_k(k_logp_rows<true, true>, rows, kRowThreads, 0, s, p, q)
+                      : launch_k(k_logp_rows<true, false>, rows, kRowThreads, 0, s, p, q);
+  return with_pairs ? launch_k(k_logp_rows<false, true>, rows, kRowThreads, 0, s, p, q)
+                    : launch_k(k_logp_rows<false, false>, rows, kRowThreads, 0, s, p, q);
 }
 
 cudaError_t launch_preference_row(const PreferenceArgs& p, int rows, cudaStream_t s) {

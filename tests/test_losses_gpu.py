@@ -165,6 +165,9 @@ POLICY_CASES = [
     (501, 64, 100003, 1.0, 250, "k3", True, False, 0.0),   # three chunks, the last of one row
     (400, 64, 65537, 1.0, 0, "none", False, True, 0.0),
     (300, 64, 80101, 0.1, 0, "k3", True, True, 0.0),       # labels far below the largest logit: exact tiles
+    (501, 64, 100003, 0.1, 250, "k2", True, True, 0.0),    # the same in three chunks
+    (6200, 64, 7301, 1.0, 0, "k3", True, True, 3.0),       # exp tiles of two launches, one backward
+    (6200, 64, 7301, 0.1, 0, "none", True, False, 0.0),    # the same by exact tiles
 ]
 
 
@@ -378,6 +381,8 @@ PREFERENCE_CASES = [
     (501, 64, 100003, 3, 1.0, 250, "hinge", False, True),   # three chunks: the logits are computed twice
     (6200, 64, 7301, 5, 1.0, 0, "sigmoid", True, False),    # exp tiles of two launches, kept for one backward
     (300, 64, 80101, 3, 0.1, 0, "sigmoid", True, True),     # labels far below the largest logit: exact tiles
+    (300, 64, 80101, 30, 0.1, 0, "hinge", True, True),      # the same with more pairs than the rows' launch takes
+    (6200, 64, 7301, 5, 0.1, 0, "sigmoid", True, True),     # exact tiles of two launches
 ]
 
 
