@@ -20,7 +20,8 @@
 //               tile with TMA stores (or reduce-adds). One epilogue warp per
 //               sub-partition: with two, the producer and MMA issuer (which
 //               share sub-partitions 0 and 1 with them) lost issue slots
-//               (measured 1.9% slower).
+//               (measured 1.9% slower). Tiles of a short K take warps 4-11,
+//               two per sub-partition (EPI_WARPS_SHORT).
 // The two accumulators alternate so the epilogue of tile t overlaps the main
 // loop of tile t+1. What is multiplied, how operands are loaded and what the
 // epilogue does come from a problem type (see lce_kernels.cu): one GEMM, or
@@ -61,16 +62,22 @@ constexpr int P_A_BYTES = 128 * BK * 2;   // 16 KiB: this CTA's 128 rows of A
 constexpr int P_B_BYTES = 128 * BK * 2;   // 16 KiB: this CTA's 128 columns of B
 constexpr int P_TILE_M = 256;
 
-struct PairSmemLayout {
+template <int EW>
+struct PairSmemLayoutT {
   static constexpr int kTiles = P_STAGES * (P_A_BYTES + P_B_BYTES);
   static constexpr int kStaging = kTiles;
-  static constexpr int kBars = kStaging + EPI_WARPS * STAGE_TILE_BYTES;
+  static constexpr int kBars = kStaging + EW * STAGE_TILE_BYTES;
   static constexpr int kNumBars = 2 * P_STAGES + 4 + 1;
   static constexpr int kMisc = kBars + kNumBars * 8;
   static constexpr int kTotal = kMisc + 16;
   static constexpr int kDynamicBytes = kTotal + 1024;
 };
-static_assert(PairSmemLayout::kDynamicBytes <= 232448, "shared memory budget (pair kernel)");
+using PairSmemLayout = PairSmemLayoutT<EPI_WARPS>;
+// Eight epilogue warps, two a sub-partition: each takes one 128-column half of a tile. They hide each other's latencies,
+// which is what bounds tiles of a short K (their figures stand at the launches that choose them); with a long K the
+// producer and the MMA issuer lose issue slots to them and nothing is gained.
+constexpr int EPI_WARPS_SHORT = 8;
+static_assert(PairSmemLayoutT<EPI_WARPS_SHORT>::kDynamicBytes <= 232448, "shared memory budget (pair kernel)");
 
 // A tile of work: which GEMM of the problem (kind), its 256-row block, its
 // 256-column block, its number of k-blocks, the first of them (k-block kb0 of
@@ -171,8 +178,8 @@ __device__ __forceinline__ void pause_ns(uint64_t ns) {
 //   load(p, kind, a, b, bar, m0, n0, k0)  this CTA's half of the k-block (TMA, pair form)
 //   a_desc / b_desc(kind, addr, k), idesc(kind)   MMA descriptors
 //   init(p, st), epilogue(p, st, job, ctx, m0, col0, taddr)
-template <class Prob>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+template <class Prob, int EW = EPI_WARPS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (EPI_WARP0 + EW), 1)
     gemm_pair_kernel(const __grid_constant__ typename Prob::Params p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -180,15 +187,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 
   uint8_t* sA = smem;
   uint8_t* sB = smem + P_STAGES * P_A_BYTES;
-  uint8_t* staging = smem + PairSmemLayout::kStaging;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + PairSmemLayout::kBars);
+  uint8_t* staging = smem + PairSmemLayoutT<EW>::kStaging;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + PairSmemLayoutT<EW>::kBars);
   uint64_t* full = bars;
   uint64_t* empty = bars + P_STAGES;
   uint64_t* tfull = bars + 2 * P_STAGES;
   uint64_t* tempty = bars + 2 * P_STAGES + 2;
   uint64_t* drain = bars + 2 * P_STAGES + 4;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + PairSmemLayout::kMisc);
-  volatile int* abort = reinterpret_cast<volatile int*>(smem + PairSmemLayout::kMisc + 4);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + PairSmemLayoutT<EW>::kMisc);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + PairSmemLayoutT<EW>::kMisc + 4);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -205,7 +212,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 2 * EPI_WARPS);
+      mbar_init(&tempty[a], 2 * EW);
     }
     mbar_init(drain, 1);
     *abort = 0;
@@ -330,7 +337,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       }
       tc_fence_after_sync();
       const TileJob tj = Prob::job(p, cluster, nclusters, j);
-      for (int h = half; h < 2; h += EPI_WARPS / 4) {  // the 128-column halves this warp owns
+      for (int h = half; h < 2; h += EW / 4) {  // the 128-column halves this warp owns
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                static_cast<uint32_t>(acc * BN + h * EPI_COLS);
         Prob::epilogue(p, st, tj, ctx, tj.mb * P_TILE_M + static_cast<int>(rank) * 128, tj.nb * BN + h * EPI_COLS,

@@ -317,15 +317,19 @@ struct DhEpi {
     if (!p.block_major && lane == 0) p.part_cnt[slice] = 0;  // ready for the next launch
   }
 
+  // PARTS: the vocabulary's parts may be added here (part_half)
+  template <bool PARTS>
   static __device__ __forceinline__ void tile(const Params& p, State& st, const EpiCtx& ctx, int m0, int col0,
                                               uint32_t taddr, int part, int tile_index) {
     const int r = m0 + ctx.row0 + ctx.lane;
     if (m0 + ctx.row0 >= p.rows) return;  // all 32 rows of this warp are past the chunk
     float f = st.g;
     if (r < p.rows && p.rowscale != nullptr) f *= p.rowscale[r];
-    if (p.split_rows == 0 && p.parts > 1) {
-      part_half(p, ctx, m0, col0, taddr, part, tile_index, f);
-      return;
+    if constexpr (PARTS) {
+      if (p.parts > 1) {
+        part_half(p, ctx, m0, col0, taddr, part, tile_index, f);
+        return;
+      }
     }
     if (p.split_rows != 0) f = 1.f;  // (the sum is scaled)
     if (p.f32_out || p.split_rows != 0) {  // fp32 tiles of 32 columns, like the dW epilogue
@@ -921,7 +925,7 @@ struct LogitsProb {
 // rows in L2): all clusters start phase 1 together, and the clusters of phase
 // 3 all enter it after the same number of dH tiles. Tiles walk N first, so the
 // pairs running at once share the A rows.
-template <class Dw>
+template <class Dw, bool PARTS = true>
 struct BwdProbT {
   struct Params {
     CUtensorMap ah, bh, ch, aw, bw, cw;
@@ -1051,7 +1055,7 @@ struct BwdProbT {
                                                   int col0, uint32_t taddr) {
     if (tj.kind == KIND_DH) {
       ctx.out = &p.ch;
-      DhEpi::tile(p.h, st.h, ctx, m0, col0, taddr, tj.part, tj.mb * p.h_n + tj.nb);
+      DhEpi::tile<PARTS>(p.h, st.h, ctx, m0, col0, taddr, tj.part, tj.mb * p.h_n + tj.nb);
     } else {
       ctx.out = &p.cw;
       Dw::tile(p.w, st.w, ctx, m0, col0, taddr);
@@ -1059,14 +1063,14 @@ struct BwdProbT {
   }
 };
 
-template <class Prob>
+template <class Prob, int EW = EPI_WARPS>
 static cudaError_t launch_pair(const typename Prob::Params& p, int clusters, cudaStream_t s) {
   if (clusters <= 0) return cudaSuccess;
-  auto kern = gemm_pair_kernel<Prob>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PairSmemLayout::kDynamicBytes);
+  auto kern = gemm_pair_kernel<Prob, EW>;
+  constexpr int bytes = PairSmemLayoutT<EW>::kDynamicBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, 2 * clusters, NUM_THREADS, PairSmemLayout::kDynamicBytes, s, p);
+  return launch_k(kern, 2 * clusters, 32 * (EPI_WARP0 + EW), bytes, s, p);
 }
 
 static int ceil_div_i(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
@@ -1091,13 +1095,13 @@ cudaError_t launch_logits(const CUtensorMap& a, const CUtensorMap& b, const CUte
 constexpr int kOddDhFirstMaxK = 16;  // k-blocks of a dW tile (chunks of up to 1024 rows)
 constexpr double kDhBlockMaxShare = 1.25;
 
-template <class Dw>
+template <class Dw, bool PARTS = true, int EW = EPI_WARPS>
 static cudaError_t launch_backward_t(const CUtensorMap& ah, const CUtensorMap& bh, const CUtensorMap& ch,
                                      const CUtensorMap& aw, const CUtensorMap& bw, const CUtensorMap& cw,
                                      long long rows, long long V, long long d, const DhParams& h, const DwParams& w,
                                      int* flags, int num_sms, cudaStream_t s, long long v_begin, long long v_end,
                                      bool with_dh) {
-  using BwdProb = BwdProbT<Dw>;
+  using BwdProb = BwdProbT<Dw, PARTS>;
   typename BwdProb::Params p;
   p.ah = ah;
   p.bh = bh;
@@ -1174,13 +1178,31 @@ static cudaError_t launch_backward_t(const CUtensorMap& ah, const CUtensorMap& b
   for (long long q = q0 > 0 ? q0 - 1 : 0; q <= q0 + 1 && q <= nW / P; ++q)
     if (longest(q) < longest(q1)) q1 = q;
   p.w_phase1 = static_cast<int>(q1 * P);
-  return launch_pair<BwdProb>(p, P, s);
+  return launch_pair<BwdProb, EW>(p, P, s);
 }
+
+// Rows of a chunk up to which the backward's epilogue takes eight warps: a dW tile has as many k-blocks as the chunk has
+// rows, so a short chunk's launch is bound by its epilogue. V = 151936, d = 2048, bf16 dW, eight warps and four: 128 rows
+// 319-336 and 399 us, 256 rows 309 and 333, 512 rows 433 and 440, 768 rows 616 and 600, 1024 rows 803-832 and 770-780;
+// 256 rows of d = 4096 660-670 and 723-756.
+constexpr long long kShortRows = 512;
 
 cudaError_t launch_backward(const CUtensorMap& ah, const CUtensorMap& bh, const CUtensorMap& ch, const CUtensorMap& aw,
                             const CUtensorMap& bw, const CUtensorMap& cw, long long rows, long long V, long long d,
                             const DhParams& h, const DwParams& w, int* flags, int num_sms, cudaStream_t s,
                             long long v_begin, long long v_end, bool with_dh) {
+  if (h.parts > 0) {  // parts that are not added in the epilogue (dh_parts_balanced)
+    const bool few = rows <= kShortRows;
+    if (w.bf16_out)
+      return few ? launch_backward_t<DwBfEpi, false, EPI_WARPS_SHORT>(ah, bh, ch, aw, bw, cw, rows, V, d, h, w, flags, num_sms,
+                                                                      s, v_begin, v_end, with_dh)
+                 : launch_backward_t<DwBfEpi, false>(ah, bh, ch, aw, bw, cw, rows, V, d, h, w, flags, num_sms, s, v_begin,
+                                                     v_end, with_dh);
+    return few ? launch_backward_t<DwEpi, false, EPI_WARPS_SHORT>(ah, bh, ch, aw, bw, cw, rows, V, d, h, w, flags, num_sms, s,
+                                                                  v_begin, v_end, with_dh)
+               : launch_backward_t<DwEpi, false>(ah, bh, ch, aw, bw, cw, rows, V, d, h, w, flags, num_sms, s, v_begin, v_end,
+                                                 with_dh);
+  }
   if (w.bf16_out)
     return launch_backward_t<DwBfEpi>(ah, bh, ch, aw, bw, cw, rows, V, d, h, w, flags, num_sms, s, v_begin, v_end,
                                       with_dh);

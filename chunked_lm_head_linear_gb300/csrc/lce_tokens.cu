@@ -200,9 +200,9 @@ struct TokEpi {
     if (MODE == TOK_STATS && have_t) p.ztgt[r] = zt;
   }
 
-  // 32 columns c0.. of the exp tile into half `hh` of the staged 64; their sum is added to s.
-  static __device__ __forceinline__ void exp_group(const EpiCtx& ctx, float (&v)[32], int c0, int hh, int vlim, int ycol,
-                                                   float z, float k, uint32_t keep, uint64_t (&s)[2]) {
+  // 32 columns c0.. of the exp tile in bf16; their sum is added to s.
+  static __device__ __forceinline__ void exp_group(float (&v)[32], int c0, int vlim, int ycol, float z, float k,
+                                                   uint32_t keep, uint64_t (&s)[2], uint32_t (&pk)[16]) {
     if (vlim < c0 + 32) {
 #pragma unroll
       for (int c = 0; c < 32; ++c)
@@ -215,7 +215,6 @@ struct TokEpi {
         if (c == yo) v[c] = kMasked;
     }
     const uint64_t z2 = pair_f32(-z, -z), k2 = pair_f32(k, k);
-    uint32_t pk[16];
 #pragma unroll
     for (int c = 0; c < 32; c += 2) {
       float x0, x1;
@@ -224,10 +223,6 @@ struct TokEpi {
       s[(c / 2) & 1] = add_pair(s[(c / 2) & 1], pair_f32(e0, e1));
       pk[c / 2] = pack_bf16x2(e0, e1) & keep;
     }
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      *reinterpret_cast<uint4*>(ctx.stage + stage_off(ctx.lane, hh * 4 + q)) =
-          make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
   }
 
   static __device__ __forceinline__ void exp_tile(const Params& p, const EpiCtx& ctx, int m0, int col0, uint32_t taddr) {
@@ -249,13 +244,22 @@ struct TokEpi {
 #pragma unroll 1
       for (int c0 = 0; c0 < EPI_COLS; c0 += 64) {  // two groups of 32 columns in flight, a staged tile of 64
         if (c0 >= vlim) break;
+        uint32_t pa[16], pb[16];
         tmem_ld_wait(va);
         tmem_ld_issue_x32(taddr + c0 + 32, vb);
-        stage_acquire(ctx);
-        exp_group(ctx, va, c0, 0, vlim, ycol, z, k, keep, s);
+        exp_group(va, c0, vlim, ycol, z, k, keep, s, pa);
         tmem_ld_wait(vb);
         if (c0 + 64 < EPI_COLS) tmem_ld_issue_x32(taddr + c0 + 64, va);
-        exp_group(ctx, vb, c0 + 32, 1, vlim, ycol, z, k, keep, s);
+        exp_group(vb, c0 + 32, vlim, ycol, z, k, keep, s, pb);
+        // The store before this one is read while the exponentials are computed.
+        stage_acquire(ctx);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          *reinterpret_cast<uint4*>(ctx.stage + stage_off(ctx.lane, q)) =
+              make_uint4(pa[4 * q], pa[4 * q + 1], pa[4 * q + 2], pa[4 * q + 3]);
+          *reinterpret_cast<uint4*>(ctx.stage + stage_off(ctx.lane, 4 + q)) =
+              make_uint4(pb[4 * q], pb[4 * q + 1], pb[4 * q + 2], pb[4 * q + 3]);
+        }
         stage_release(ctx, col0 + c0, m0 + ctx.row0, false);
       }
       tmem_ld_wait(va);  // a load that a break left under way
@@ -352,7 +356,7 @@ struct TokProb {
   }
 };
 
-template <int MODE>
+template <int MODE, int EW = EPI_WARPS>
 cudaError_t launch_tok_mode(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, long long M, long long N,
                             long long K, const TokParams& ep, int num_sms, cudaStream_t s) {
   using Prob = TokProb<MODE>;
@@ -367,11 +371,11 @@ cudaError_t launch_tok_mode(const CUtensorMap& a, const CUtensorMap& b, const CU
   const long long tiles = static_cast<long long>(p.m_tiles) * p.n_tiles;
   const int clusters = static_cast<int>(tiles < num_sms / 2 ? tiles : num_sms / 2);
   if (clusters <= 0) return cudaSuccess;
-  auto kern = gemm_pair_kernel<Prob>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PairSmemLayout::kDynamicBytes);
+  auto kern = gemm_pair_kernel<Prob, EW>;
+  constexpr int bytes = PairSmemLayoutT<EW>::kDynamicBytes;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, 2 * clusters, NUM_THREADS, PairSmemLayout::kDynamicBytes, s, p);
+  return launch_k(kern, 2 * clusters, 32 * (EPI_WARP0 + EW), bytes, s, p);
 }
 
 // ----------------------------------------------------------------------------
@@ -1180,12 +1184,19 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_distill_row(const DistillArg
 // ----------------------------------------------------------------------------
 // Launch wrappers
 // ----------------------------------------------------------------------------
+// Hidden size up to which the exp tile's epilogue takes eight warps: a tile of few k-blocks is bound by the latencies of
+// its epilogue, a tile of many by the MMA. 2048 rows of V = 151936, eight warps and four: d = 256 225 and 253 us, 512 270
+// and 278, 1024 level; at 2048 the difference is within the noise and four leave more issue slots.
+constexpr long long kExpShortK = 512;
+
 cudaError_t launch_tok_logits(int mode, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, long long M,
                               long long N, long long K, const TokParams& ep, int num_sms, cudaStream_t s) {
   switch (mode) {
     case TOK_STATS: return launch_tok_mode<TOK_STATS>(a, b, c, M, N, K, ep, num_sms, s);
     case TOK_STATS_Z: return launch_tok_mode<TOK_STATS_Z>(a, b, c, M, N, K, ep, num_sms, s);
-    case TOK_EXP: return launch_tok_mode<TOK_EXP>(a, b, c, M, N, K, ep, num_sms, s);
+    case TOK_EXP:
+      return K <= kExpShortK ? launch_tok_mode<TOK_EXP, EPI_WARPS_SHORT>(a, b, c, M, N, K, ep, num_sms, s)
+                             : launch_tok_mode<TOK_EXP>(a, b, c, M, N, K, ep, num_sms, s);
     default: return launch_tok_mode<TOK_GRAD>(a, b, c, M, N, K, ep, num_sms, s);
   }
 }
