@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_preference_row(const Prefere
   const LossRowArgs& q = p.row;
   const int y = given_label(q.y, r, q.ignore_index, q.V);
   float a = 0.f;
-  if (y >= 0) {
+  if (y >= 0 && p.P > 0) {  // (without pairs there may be no bounds)
     const long long s = sequence_of(p.cu, p.cu32, 2 * p.P, p.c0 + r);
     if (s >= 0 && s < 2 * p.P) a = p.coef[s];
   }

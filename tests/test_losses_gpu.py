@@ -489,6 +489,26 @@ def test_preference_bad_bounds_no_pairs_and_no_rows(cuda_lib):
         assert out[0].item() == 0 and out[3].shape == (0, 64) and not out[4].any()
 
 
+@pytest.mark.parametrize("N", [40, 300])
+def test_preference_without_pairs_needs_no_bounds(cuda_lib, N):
+    """The C call with pairs = 0 and no pointers of pairs: loss 0, gradients 0 (kept logits, exp tiles, two chunks)."""
+    import ctypes
+    torch = _torch()
+    V, d = 80101, 64
+    _, H, W, y = make(N, d, V)
+    Ht, Wt, yt = *heads(H, W), dev(y)
+    lib, p = cuda_lib.load(), lambda t: ctypes.c_void_p(t.data_ptr())
+    for chunk in (0, 32):
+        opts = cuda_lib.make_opts(chunk_tokens=chunk, sync_check=True)
+        pref = cuda_lib.LcePreference(0.1, 0.0, 0.0, 0, 0, 0)
+        ws = torch.empty(cuda_lib.lce_preference_workspace_size(N, d, V, 0, opts=opts), dtype=torch.uint8, device="cuda")
+        loss, dH, dW = torch.ones(1, device="cuda"), torch.ones_like(Ht), torch.ones(V, d, device="cuda")
+        rc = lib.lce_preference_fwd_bwd(p(Ht), p(Wt), p(yt), N, d, V, None, 0, 1.0, ctypes.byref(pref), None, None, 0, p(loss),
+                                        None, None, p(dH), p(dW), ctypes.byref(opts), p(ws), ws.numel(),
+                                        ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        assert rc == 0 and loss.item() == 0 and not dH.any() and not dW.any()
+
+
 # --------------------------------------------------------------------------- the heads' real sizes
 @pytest.mark.parametrize("N,d,V,chunk", [(70, 2048, 151936, 0), (6500, 2048, 151936, 0), (700, 7168, 151655, 512),
                                          (16500, 64, 151655, 0)])
