@@ -265,7 +265,7 @@ struct TokEpi {
       tmem_ld_wait(va);  // a load that a break left under way
       float s0, s1;
       unpair_f32(add_pair(s[0], s[1]), s0, s1);
-      sum = s0 + s1;
+      sum = s0 + s1 + (z - z);  // NaN, and so the guard, where the label's logit is not finite
     }
     if (!live || !in_bounds(part, p.nparts, p.flags)) return;
     p.sums[static_cast<long long>(r) * p.nparts + part] = sum;

@@ -612,6 +612,36 @@ def test_exp_tiles_masked_rows_of_nan(cuda_lib):
     assert got[0].isnan().all() and got[2][row].isnan() and torch.isfinite(got[3][rest]).all() and got[3][row].isnan().all()
 
 
+def test_exp_tiles_of_a_label_past_fp32(cuda_lib):
+    """A label's logit that overflows to infinity, the others finite: NaN, as inf - inf is, in that row alone."""
+    torch = _torch()
+    N, d, V = 300, 64, 80101
+    rng, H, W, y = make(N, d, V, seed=7)
+    rows = np.flatnonzero(y >= 0)
+    row, label = int(rows[10]), 70000
+    y[rows[y[rows] == label]] = 5
+    y[row] = label
+    W[:, 0] = 0.0
+    H[:, 0] = 0.0
+    W[label, 0] = 2.0 ** 127
+    Ht, Wt = heads(H, W)
+    inp = policy_inputs(rng, H, W, y, 1.0, weights=False)
+    inp["advantages"][row] = 1.0
+    want = call_policy(cuda_lib, Ht, Wt, dev(y), inp)
+    cu = bounds(rng, N, 3)
+    seq = int(np.searchsorted(cu, row, side="right")) - 1
+    want_seq = call_preference(cuda_lib, Ht, Wt, y, cu, None)[2]
+    Ht[row, 0] = 2.0 ** 127
+    got = call_policy(cuda_lib, Ht, Wt, dev(y), inp, sync_check=True)
+    rest = torch.arange(N, device="cuda") != row
+    assert got[0].isnan().all() and got[1][row].isnan() and got[2][row].isnan()
+    assert ((got[1] - want[1])[rest].abs() <= 2.0 ** -14).all() and torch.isfinite(got[3][rest]).all()
+    got = call_preference(cuda_lib, Ht, Wt, y, cu, None, sync_check=True)
+    others = torch.arange(6, device="cuda") != seq
+    assert got[0].isnan().all() and (0 <= seq < 6) and got[2][seq].isnan() and torch.isfinite(got[2][others]).all()
+    assert torch.isfinite(want_seq).all()
+
+
 @pytest.mark.parametrize("shift", [50.0, 70.0, 200.0])
 def test_exp_tiles_of_one_far_label(cuda_lib, shift):
     """A single row whose label lies below the other logits, within the tile's range (50 nats) and beyond it."""
