@@ -560,9 +560,11 @@ cudaError_t fwd_rows(const LayerNormArgs& p, int num_sms, cudaStream_t s) {
 
 // Elements of x up to which the backward is one cluster of sixteen blocks: one launch, which is what small calls wait for
 // (1531 x 264: 20 us a call, 25 with a second launch that adds the blocks' partial rows; on the device alone 9.0 and 5.5).
+// A row of fewer than 256 elements takes a team's turn as one of 256 does, and counts as one (60001 x 8 on the device: 114 us
+// as one cluster, 16 with many blocks; 4000 x 128 10.0 and 5.5).
 constexpr long long kLnOneLaunch = 1 << 19;
 
-bool one_launch(long long N, long long d) { return d <= kLnFusedD && N * d <= kLnOneLaunch; }
+bool one_launch(long long N, long long d) { return d <= kLnFusedD && N * (d > 256 ? d : 256) <= kLnOneLaunch; }
 
 template <bool F32, int T, int K, int R, int D, int B = 2>
 cudaError_t bwd_pass(const LayerNormArgs& p, int parts, cudaStream_t s) {

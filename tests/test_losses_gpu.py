@@ -811,6 +811,28 @@ def test_layernorm_past_32_bits(cuda_lib):
     assert ((db - dbt).abs() <= 200 * EPS * tail.float().abs().sum(0)).all()
 
 
+def test_layernorm_short_rows_and_long_batches(cuda_lib):
+    """Many rows of few elements, whose gradients many blocks share, and the one-pass backward past 2^31 elements."""
+    torch = _torch()
+    for N in (2048, 2049, 60001):
+        rng, x, dH = norm_inputs(N, 8, seed=N)
+        check_norm(cuda_lib, x, dev(f32(1 + 0.1 * rng.standard_normal(8))), dev(f32(rng.standard_normal(8))), dH)
+    N, d = 270000, 8192
+    x = torch.zeros(N, d, dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn(100, d, device="cuda").bfloat16()
+    x[-100:] = tail
+    w = torch.ones(d, device="cuda")
+    H, mean, rstd = cuda_lib.lce_layernorm_forward(x, w)
+    Ht, mt, rt = cuda_lib.lce_layernorm_forward(tail, w)
+    assert torch.equal(H[-100:], Ht) and torch.equal(mean[-100:], mt) and torch.equal(rstd[-100:], rt) and not H[:-100].any()
+    dx, dw, db = cuda_lib.lce_layernorm_backward(x, w, mean, rstd, x)
+    dxt, dwt, dbt = cuda_lib.lce_layernorm_backward(tail, w, mt, rt, tail)
+    assert torch.equal(dx[-100:], dxt) and not dx[:-100].any()
+    assert ((db - dbt).abs() <= 200 * EPS * tail.float().abs().sum(0)).all()
+    xh = (tail.float() - mt[:, None]) * rt[:, None]
+    assert ((dw - dwt).abs() <= 200 * EPS * (xh * tail.float()).abs().sum(0)).all()
+
+
 # --------------------------------------------------------------------------- together
 def step_inputs(N, d, V, seed=3):
     torch = _torch()
