@@ -1506,9 +1506,10 @@ struct LossLayout {
 };
 
 // Logits of a chunk from which on the exp tile is the faster way to a gradient tile: the pass over kept logits costs 6
-// bytes each, the exp tile's further launches about 4 us that the launches around them do not hide. Policy steps with
-// kept logits / exp tiles, us: 256 x 8192 x 256 (rows, V, d) 43.7 / 46.9, 1024 x 8192 x 256 54.5 / 54.2, 256 x 32000 x 256
-// 79 / 76, 1024 x 32000 x 256 140 / 103, 512 x 151936 x 256 461 / 282, 1024 x 151936 x 2048 1327 / 1167.
+// bytes each, the exp tile's further launches some 4 us that the launches around them do not hide. Policy steps (replayed
+// from a graph) with kept logits / exp tiles, us: 256 x 8192 x 256 (rows, V, d) 31.3 / 32.3, 416 x 16818 x 2032 92.0 / 93.9,
+// 256 x 32000 x 256 47.2 / 43.1, 1024 x 8192 x 256 43.2 / 40.5, 512 x 16384 x 2048 96.8 / 93.0, 1024 x 32000 x 256 110 / 68,
+// 512 x 151936 x 256 330 / 140, 1024 x 151936 x 2048 1344 / 1142.
 constexpr int64_t kExpLogits = 8000000;
 
 // Most rows whose exp tiles are kept together by default (logits launches of at most 6143 rows each, so that a launch's

@@ -73,9 +73,9 @@ struct PairSmemLayoutT {
   static constexpr int kDynamicBytes = kTotal + 1024;
 };
 using PairSmemLayout = PairSmemLayoutT<EPI_WARPS>;
-// Eight epilogue warps, two a sub-partition: each takes one 128-column half of a tile. They hide each other's latencies,
-// which is what bounds tiles of a short K (their figures stand at the launches that choose them); with a long K the
-// producer and the MMA issuer lose issue slots to them and nothing is gained.
+// Eight epilogue warps, two a sub-partition, four to each accumulator: they hide each other's latencies, which is what
+// bounds tiles of a short K (figures stand at the launches that choose them); with a long K the producer and the MMA
+// issuer lose issue slots to them and nothing is gained.
 constexpr int EPI_WARPS_SHORT = 8;
 static_assert(PairSmemLayoutT<EPI_WARPS_SHORT>::kDynamicBytes <= 232448, "shared memory budget (pair kernel)");
 
@@ -85,6 +85,14 @@ static_assert(PairSmemLayoutT<EPI_WARPS_SHORT>::kDynamicBytes <= 232448, "shared
 struct TileJob {
   int kind, mb, nb, k_blocks, kb0, part;
 };
+
+// The plan of a problem whose tiles are dealt to the clusters in turn.
+struct RoundRobin {
+  int c, P, jobs;
+};
+__device__ __forceinline__ RoundRobin round_robin(int tiles, int c, int P) {
+  return RoundRobin{c, P, c < tiles ? (tiles - 1 - c) / P + 1 : 0};
+}
 
 // What an epilogue warp needs besides its tile: its staging tile, the store
 // map and where its 32 rows start.
@@ -99,6 +107,15 @@ struct EpiCtx {
 // Byte offset of 16-byte chunk j of row r in a 128-byte-swizzled staging tile.
 __device__ __forceinline__ uint32_t stage_off(int r, int j) {
   return static_cast<uint32_t>(r * 128 + ((j ^ (r & 7)) << 4));
+}
+
+// 64 columns of a row in bf16 (columns 2 q and 2 q + 1 in word q of `a`, the other 32 columns in `b`) into the staging tile.
+__device__ __forceinline__ void stage_bf16(const EpiCtx& c, const uint32_t (&a)[16], const uint32_t (&b)[16]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    *reinterpret_cast<uint4*>(c.stage + stage_off(c.lane, q)) = make_uint4(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
+    *reinterpret_cast<uint4*>(c.stage + stage_off(c.lane, 4 + q)) = make_uint4(b[4 * q], b[4 * q + 1], b[4 * q + 2], b[4 * q + 3]);
+  }
 }
 
 // Before rewriting the staging tile: the previous TMA store must have read it.
@@ -172,12 +189,15 @@ __device__ __forceinline__ void pause_ns(uint64_t ns) {
 //   skip(p)                     conditional launch: true = do nothing
 //   no_loads(p)                 timeout test: the producer issues no loads
 //   flags(p)                    device status word
-//   num_jobs(p, cluster, P)     number of tiles of this cluster (P clusters in the grid)
-//   job(p, cluster, P, j)       its j-th tile
+//   Plan, plan(p, cluster, P)   what its cluster (of P in the grid) does: found once, since divisions cost each role of the
+//                               kernel up to 1000 cycles a tile (the backward's have nine)
+//   num_jobs(plan)              number of tiles of this cluster
+//   job(p, plan, j)             its j-th tile
 //   job_ok(p, job)              the tile lies inside the problem (checked build only)
 //   load(p, kind, a, b, bar, m0, n0, k0)  this CTA's half of the k-block (TMA, pair form)
 //   a_desc / b_desc(kind, addr, k), idesc(kind)   MMA descriptors
 //   init(p, st), epilogue(p, st, job, ctx, m0, col0, taddr)
+//   ahead(p, st, job, r)        what row r of the tile needs and can be read before its accumulator is there
 template <class Prob, int EW = EPI_WARPS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (EPI_WARP0 + EW), 1)
     gemm_pair_kernel(const __grid_constant__ typename Prob::Params p) {
@@ -202,7 +222,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (EPI_WARP0 + EW
   const uint32_t rank = cluster_ctarank();
   const int cluster = static_cast<int>(blockIdx.x >> 1);
   const int nclusters = static_cast<int>(gridDim.x >> 1);
-  int njobs = Prob::num_jobs(p, cluster, nclusters);
+  const typename Prob::Plan plan = Prob::plan(p, cluster, nclusters);
+  int njobs = Prob::num_jobs(plan);
   int* flags = Prob::flags(p);
 
   if (threadIdx.x == 0) {
@@ -212,7 +233,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (EPI_WARP0 + EW
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 2 * EW);
+      mbar_init(&tempty[a], 2 * EPI_WARPS);
     }
     mbar_init(drain, 1);
     *abort = 0;
@@ -240,7 +261,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (EPI_WARP0 + EW
     uint32_t armed = 0, armed_parity = 0;
     bool ok = !Prob::no_loads(p);  // (timeout test: issue nothing)
     for (int j = 0; j < njobs && ok; ++j) {
-      const TileJob tj = Prob::job(p, cluster, nclusters, j);
+      const TileJob tj = Prob::job(p, plan, j);
       if (kChecks && !Prob::job_ok(p, tj)) {  // checked build: every role skips a bad tile
         atomicOr(flags, kFlagBounds);
         continue;
@@ -279,7 +300,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (EPI_WARP0 + EW
     bool ok = true;
     bool issued = false;
     for (int j = 0; j < njobs && ok; ++j) {
-      const TileJob tj = Prob::job(p, cluster, nclusters, j);
+      const TileJob tj = Prob::job(p, plan, j);
       if (kChecks && !Prob::job_ok(p, tj)) continue;
       const uint32_t idesc = Prob::idesc(tj.kind);
       if (!mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, abort)) {
@@ -323,33 +344,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (EPI_WARP0 + EW
     // ---------------- epilogue (both CTAs) ----------------
     const int e = warp - EPI_WARP0;
     const int q = warp & 3;
-    const int half = e >> 2;
     EpiCtx ctx{staging + e * STAGE_TILE_BYTES, nullptr, lane, q * 32, flags};
-    int acc = 0;
-    uint32_t acc_phase = 0;
     typename Prob::State st;
     Prob::init(p, st);
-    for (int j = 0; j < njobs; ++j) {
-      if (kChecks && !Prob::job_ok(p, Prob::job(p, cluster, nclusters, j))) continue;
-      if (!warp_wait_cluster(&tfull[acc], acc_phase, abort, lane)) {
+    for (int j = 0, t = -1; j < njobs; ++j) {  // t: number of the tile among those that are worked on
+      if (kChecks && !Prob::job_ok(p, Prob::job(p, plan, j))) continue;
+      ++t;
+      if (EW > EPI_WARPS && (t & 1) != e / EPI_WARPS) continue;  // the other four warps' accumulator
+      const int acc = t & 1;
+      const TileJob tj = Prob::job(p, plan, j);
+      const int m0 = tj.mb * P_TILE_M + static_cast<int>(rank) * 128;
+      Prob::ahead(p, st, tj, m0 + ctx.row0 + lane);
+      if (!warp_wait_cluster(&tfull[acc], (t >> 1) & 1, abort, lane)) {
         if (lane == 0) report_timeout(abort, flags);
         break;
       }
       tc_fence_after_sync();
-      const TileJob tj = Prob::job(p, cluster, nclusters, j);
-      for (int h = half; h < 2; h += EW / 4) {  // the 128-column halves this warp owns
+      for (int h = 0; h < 2; ++h) {
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                static_cast<uint32_t>(acc * BN + h * EPI_COLS);
-        Prob::epilogue(p, st, tj, ctx, tj.mb * P_TILE_M + static_cast<int>(rank) * 128, tj.nb * BN + h * EPI_COLS,
-                       taddr);
+        Prob::epilogue(p, st, tj, ctx, m0, tj.nb * BN + h * EPI_COLS, taddr);
       }
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&tempty[acc]), 0));
-      if (++acc == 2) {
-        acc = 0;
-        acc_phase ^= 1u;
-      }
+      if (lane == 0) mbar_arrive_remote_relaxed(mapa_shared(smem_u32(&tempty[acc]), 0));
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();

@@ -148,11 +148,15 @@ inline int dh_parts_for(long long V) {
 }
 
 // Time of a dW tile in units of one of its k-blocks (w_k of them): short ones are bound by their epilogue and by writing
-// dW. Weighed as their k-blocks alone, short batches piled dW tiles onto the clusters that share no dH tile (policy steps
-// at V = 151936, d = 4096 with four dH parts, us before / after: 64 rows 2344 / 881, 256 rows 1180 / 953, 512 rows 1338 /
-// 1315; from 1024 rows on nothing changes).
-inline double dw_tile_cost(long long w_k) {
-  return w_k >= 14 ? static_cast<double>(w_k) : w_k >= 8 ? 14.0 : static_cast<double>(w_k + 6);
+// dW, in fp32 twice the bytes. Weighed as their k-blocks alone, short batches piled dW tiles onto the clusters that share no
+// dH tile (64 rows of V = 151936, d = 4096 with four dH parts: 2344 us and 881). Backward of V = 151936, d = 2048 in us with
+// a tile at: 128 rows (w_k 2) 4 280 to 302, 6 245, 8 275, 10 294; 256 rows 5 270, 6 256, 8 282, 10 301; 384 rows 7 371, 8
+// 348, 10 381; 512 rows 9 404, 10 398, 11 410, 14 430; 768 rows 12 585, 13 574, 14 553. fp32: 256 rows 6 363, 8 345 to 357,
+// 10 378; 512 rows 11 477, 14 463.
+inline double dw_tile_cost(long long w_k, bool bf16) {
+  if (w_k >= 14) return static_cast<double>(w_k);
+  if (!bf16) return w_k >= 8 ? 14.0 : static_cast<double>(w_k + 4);
+  return w_k > 12 ? 14.0 : w_k > 4 ? static_cast<double>(w_k + 2) : 6.0;
 }
 
 // dH parts where no such promise is made (the policy and preference losses). Each is stored as an fp32 tile of its own
@@ -166,7 +170,7 @@ inline int dh_parts_balanced(long long rows, long long V, long long d) {
   const long long kb = (V + 63) / 64, cols = (d + 255) / 256;
   const double k = static_cast<double>(kb);
   const double fair = (static_cast<double>((rows + 255) / 256 * cols) * k +
-                       static_cast<double>((V + 255) / 256 * cols) * dw_tile_cost((rows + 63) / 64)) / 76.0;
+                       static_cast<double>((V + 255) / 256 * cols) * dw_tile_cost((rows + 63) / 64, true)) / 76.0;
   const double bytes = 8.0 * static_cast<double>(rows) * static_cast<double>(d);  // of a part, written and read
   auto time = [&](int p) {
     const double longest = p == 1 ? k : k / p + kDhStore;

@@ -411,6 +411,21 @@ struct DwBfEpi {
   static __device__ __forceinline__ float add_scaled(float v, float f, float e) {
     return __fadd_rn(__fmul_rn(v, f), e);
   }
+  // 32 columns from c on, in bf16
+  static __device__ __forceinline__ void group(const float (&v)[32], const float* add, int c, int N, float f,
+                                               uint32_t (&pk)[16]) {
+    if (add == nullptr) {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) pk[q] = pack_bf16x2(add_scaled(v[2 * q], f, 0.f), add_scaled(v[2 * q + 1], f, 0.f));
+      return;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {  // d % 8 == 0: a group of four lies inside the row or outside it
+      const float4 e = c + 4 * q < N ? __ldcs(reinterpret_cast<const float4*>(add + c + 4 * q)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      pk[2 * q] = pack_bf16x2(add_scaled(v[4 * q], f, e.x), add_scaled(v[4 * q + 1], f, e.y));
+      pk[2 * q + 1] = pack_bf16x2(add_scaled(v[4 * q + 2], f, e.z), add_scaled(v[4 * q + 3], f, e.w));
+    }
+  }
 
   static __device__ __forceinline__ void tile(const Params& p, State& st, const EpiCtx& ctx, int m0, int col0,
                                               uint32_t taddr) {
@@ -418,32 +433,23 @@ struct DwBfEpi {
     if (m0 + ctx.row0 >= p.rows) return;  // all 32 rows of this warp are past the vocabulary
     const int r = m0 + ctx.row0 + ctx.lane;
     const float* add = p.add != nullptr && r < p.rows ? p.add + static_cast<long long>(r) * p.ld : nullptr;
+    float va[32], vb[32];
+    tmem_ld_issue_x32(taddr, va);
 #pragma unroll 1
-    for (int u = 0; u < EPI_COLS / 64; ++u) {
-      if (col0 + u * 64 >= p.N) break;
+    for (int c0 = 0; c0 < EPI_COLS; c0 += 64) {  // two groups of 32 columns in flight, a staged tile of 64
+      if (col0 + c0 >= p.N) break;
+      uint32_t pa[16], pb[16];
+      tmem_ld_wait(va);
+      tmem_ld_issue_x32(taddr + c0 + 32, vb);
+      group(va, add, col0 + c0, p.N, f, pa);
+      tmem_ld_wait(vb);
+      if (c0 + 64 < EPI_COLS) tmem_ld_issue_x32(taddr + c0 + 64, va);
+      group(vb, add, col0 + c0 + 32, p.N, f, pb);
       stage_acquire(ctx);
-#pragma unroll 1
-      for (int hh = 0; hh < 2; ++hh) {
-        const int c = col0 + u * 64 + hh * 32;
-        float4 e[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q)  // d % 8 == 0: a group of four lies inside the row or outside it
-          e[q] = add != nullptr && c + 4 * q < p.N ? __ldcs(reinterpret_cast<const float4*>(add + c + 4 * q))
-                                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-        float v[32];
-        tmem_ld_32x32b_x32(taddr + u * 64 + hh * 32, v);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint4 w;
-          w.x = pack_bf16x2(add_scaled(v[8 * q + 0], f, e[2 * q].x), add_scaled(v[8 * q + 1], f, e[2 * q].y));
-          w.y = pack_bf16x2(add_scaled(v[8 * q + 2], f, e[2 * q].z), add_scaled(v[8 * q + 3], f, e[2 * q].w));
-          w.z = pack_bf16x2(add_scaled(v[8 * q + 4], f, e[2 * q + 1].x), add_scaled(v[8 * q + 5], f, e[2 * q + 1].y));
-          w.w = pack_bf16x2(add_scaled(v[8 * q + 6], f, e[2 * q + 1].z), add_scaled(v[8 * q + 7], f, e[2 * q + 1].w));
-          *reinterpret_cast<uint4*>(ctx.stage + stage_off(ctx.lane, hh * 4 + q)) = w;
-        }
-      }
-      stage_release(ctx, col0 + u * 64, m0 + ctx.row0, false);
+      stage_bf16(ctx, pa, pb);
+      stage_release(ctx, col0 + c0, m0 + ctx.row0, false);
     }
+    tmem_ld_wait(va);  // a load that a break left under way
   }
 };
 
@@ -884,12 +890,13 @@ struct LogitsProb {
   static __device__ __forceinline__ bool skip(const Params& p) { return FwdEpi::skip(p.ep); }
   static __device__ __forceinline__ bool no_loads(const Params& p) { return p.no_loads != 0; }
   static __device__ __forceinline__ int* flags(const Params& p) { return p.flags; }
-  static __device__ __forceinline__ int num_jobs(const Params& p, int c, int P) {
-    const int tiles = p.m_tiles * p.n_tiles;
-    return c < tiles ? (tiles - 1 - c) / P + 1 : 0;
+  using Plan = RoundRobin;
+  static __device__ __forceinline__ Plan plan(const Params& p, int c, int P) {
+    return round_robin(p.m_tiles * p.n_tiles, c, P);
   }
-  static __device__ __forceinline__ TileJob job(const Params& p, int c, int P, int j) {
-    const int t = c + j * P;
+  static __device__ __forceinline__ int num_jobs(const Plan& s) { return s.jobs; }
+  static __device__ __forceinline__ TileJob job(const Params& p, const Plan& s, int j) {
+    const int t = s.c + j * s.P;
     return TileJob{KIND_LOGITS, t % p.m_tiles, t / p.m_tiles, p.k_blocks, 0, 0};
   }
   static __device__ __forceinline__ bool job_ok(const Params& p, const TileJob& tj) {
@@ -905,6 +912,7 @@ struct LogitsProb {
   static __device__ __forceinline__ uint64_t b_desc(int, uint32_t addr, int k) { return desc_k_major(addr, k); }
   static __device__ __forceinline__ uint32_t idesc(int) { return idesc_bf16_f32(P_TILE_M, BN, false, false); }
   static __device__ __forceinline__ void init(const Params& p, State& st) { FwdEpi::init(p.ep, st); }
+  static __device__ __forceinline__ void ahead(const Params&, State&, const TileJob&, int) {}
   static __device__ __forceinline__ void epilogue(const Params& p, State& st, const TileJob&, EpiCtx ctx, int m0,
                                                   int col0, uint32_t taddr) {
     ctx.out = &p.c;
@@ -946,8 +954,11 @@ struct BwdProbT {
     DhEpi::State h;
     typename Dw::State w;
   };
-  struct Sched {
-    int hcount, q1, li, nlight, count2;
+  struct Plan {
+    int k, P;                            // position in the dealing order, clusters
+    int hcount, q1, li, nlight, count2;  // dH tiles; dW tiles of phase 1; place among the clusters of phase 3, their number, dW tiles
+    int vb0, nmb;                        // the launch's dW tiles: first and number of vocabulary blocks
+    bool dh_first;                       // dH tiles, then the dW tiles of phase 1
   };
   // Position of cluster c in the dealing order. Normally c itself; when odd clusters take their
   // dH tiles first, the even clusters come first and then the odd ones, so that the tiles dealt
@@ -957,9 +968,11 @@ struct BwdProbT {
     if (!p.odd_dh_first) return c;
     return (c & 1) ? (P + 1) / 2 + c / 2 : c / 2;
   }
-  static __device__ __forceinline__ Sched sched(const Params& p, int c, int P) {
-    Sched s;
-    c = deal_rank(p, c, P);
+  static __device__ __forceinline__ Plan plan(const Params& p, int c, int P) {
+    Plan s;
+    s.dh_first = p.odd_dh_first && (c & 1);
+    s.k = c = deal_rank(p, c, P);
+    s.P = P;
     const int nH = p.h_m * p.h_n * p.h_parts / p.h_group, nW = p.w_tiles;  // dH units dealt
     s.hcount = (c < nH ? (nH - 1 - c) / P + 1 : 0) * p.h_group;
     const int r = nH % P;  // clusters c < r hold one dH unit more
@@ -968,45 +981,43 @@ struct BwdProbT {
     s.li = r == 0 ? c : c - r;
     const int rem = nW - p.w_phase1;
     s.count2 = (s.li >= 0 && s.li < rem) ? (rem - 1 - s.li) / s.nlight + 1 : 0;
+    s.vb0 = p.w_t0 / p.w_n;
+    s.nmb = p.w_tiles / p.w_n;
     return s;
   }
   static __device__ __forceinline__ bool skip(const Params&) { return false; }
   static __device__ __forceinline__ bool no_loads(const Params&) { return false; }
   static __device__ __forceinline__ int* flags(const Params& p) { return p.flags; }
-  static __device__ __forceinline__ int num_jobs(const Params& p, int c, int P) {
-    const Sched s = sched(p, c, P);
-    return s.hcount + s.q1 + s.count2;
-  }
+  static __device__ __forceinline__ int num_jobs(const Plan& s) { return s.hcount + s.q1 + s.count2; }
   // dW tile t of the launch's range [w_t0, w_t0 + w_tiles), in groups of up to kDwGroup column
   // blocks of d: a group runs through every vocabulary block of the range before the next group
   // starts, so the part of Ht that the running tiles read (kDwGroup x C x 256 bf16) stays small
   // enough for L2; each exp-tile column block is then read once per group. With d <= 2048 there
   // is one group and the order is vocabulary block, then column block of d.
   static constexpr int kDwGroup = 8;
-  static __device__ __forceinline__ TileJob dw_job(const Params& p, int t) {
-    const int vb0 = p.w_t0 / p.w_n, nmb = p.w_tiles / p.w_n;
-    const int G = p.w_n < kDwGroup ? p.w_n : kDwGroup;
-    const int tl = t - p.w_t0;
-    const int g = tl / (nmb * G);
-    const int gc = p.w_n - g * G < G ? p.w_n - g * G : G;
-    const int r = tl - g * nmb * G;
-    return TileJob{KIND_DW, vb0 + r / gc, g * G + r % gc, p.w_k, 0, 0};
-  }
-  static __device__ __forceinline__ TileJob job(const Params& p, int c, int P, int j) {
-    const Sched s = sched(p, c, P);
-    const int k = deal_rank(p, c, P);
-    if (p.odd_dh_first && (c & 1)) {  // this cluster: dH tiles, then its first-phase dW tiles
-      if (j < s.hcount) return dh_job(p, k, P, j);
-      j -= s.hcount;
-      if (j < s.q1) return dw_job(p, p.w_t0 + k + j * P);
-      j -= s.q1;
-      return dw_job(p, p.w_t0 + p.w_phase1 + s.li + j * s.nlight);
+  static __device__ __forceinline__ TileJob dw_job(const Params& p, const Plan& s, int t) {  // t: of the launch's tiles
+    int g = 0, gc = p.w_n, r = t;
+    if (p.w_n > kDwGroup) {
+      g = t / (s.nmb * kDwGroup);
+      gc = p.w_n - g * kDwGroup < kDwGroup ? p.w_n - g * kDwGroup : kDwGroup;
+      r = t - g * s.nmb * kDwGroup;
     }
-    if (j < s.q1) return dw_job(p, p.w_t0 + k + j * P);
-    j -= s.q1;
-    if (j < s.hcount) return dh_job(p, k, P, j);
-    j -= s.hcount;
-    return dw_job(p, p.w_t0 + p.w_phase1 + s.li + j * s.nlight);
+    const int mb = r / gc;
+    return TileJob{KIND_DW, s.vb0 + mb, g * kDwGroup + r - mb * gc, p.w_k, 0, 0};
+  }
+  static __device__ __forceinline__ TileJob job(const Params& p, const Plan& s, int j) {
+    if (s.dh_first) {
+      if (j < s.hcount) return dh_job(p, s.k, s.P, j);
+      j -= s.hcount;
+      if (j < s.q1) return dw_job(p, s, s.k + j * s.P);
+      j -= s.q1;
+    } else {
+      if (j < s.q1) return dw_job(p, s, s.k + j * s.P);
+      j -= s.q1;
+      if (j < s.hcount) return dh_job(p, s.k, s.P, j);
+      j -= s.hcount;
+    }
+    return dw_job(p, s, p.w_phase1 + s.li + j * s.nlight);
   }
   static __device__ __forceinline__ bool job_ok(const Params& p, const TileJob& tj) {
     if (tj.kind == KIND_DH)
@@ -1051,6 +1062,7 @@ struct BwdProbT {
     DhEpi::init(p.h, st.h);
     Dw::init(p.w, st.w);
   }
+  static __device__ __forceinline__ void ahead(const Params&, State&, const TileJob&, int) {}
   static __device__ __forceinline__ void epilogue(const Params& p, State& st, const TileJob& tj, EpiCtx ctx, int m0,
                                                   int col0, uint32_t taddr) {
     if (tj.kind == KIND_DH) {
@@ -1063,14 +1075,14 @@ struct BwdProbT {
   }
 };
 
-template <class Prob, int EW = EPI_WARPS>
+template <class Prob>
 static cudaError_t launch_pair(const typename Prob::Params& p, int clusters, cudaStream_t s) {
   if (clusters <= 0) return cudaSuccess;
-  auto kern = gemm_pair_kernel<Prob, EW>;
-  constexpr int bytes = PairSmemLayoutT<EW>::kDynamicBytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  auto kern = gemm_pair_kernel<Prob>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PairSmemLayout::kDynamicBytes);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, 2 * clusters, 32 * (EPI_WARP0 + EW), bytes, s, p);
+  return launch_k(kern, 2 * clusters, NUM_THREADS, PairSmemLayout::kDynamicBytes, s, p);
 }
 
 static int ceil_div_i(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
@@ -1095,7 +1107,7 @@ cudaError_t launch_logits(const CUtensorMap& a, const CUtensorMap& b, const CUte
 constexpr int kOddDhFirstMaxK = 16;  // k-blocks of a dW tile (chunks of up to 1024 rows)
 constexpr double kDhBlockMaxShare = 1.25;
 
-template <class Dw, bool PARTS = true, int EW = EPI_WARPS>
+template <class Dw, bool PARTS = true>
 static cudaError_t launch_backward_t(const CUtensorMap& ah, const CUtensorMap& bh, const CUtensorMap& ch,
                                      const CUtensorMap& aw, const CUtensorMap& bw, const CUtensorMap& cw,
                                      long long rows, long long V, long long d, const DhParams& h, const DwParams& w,
@@ -1147,7 +1159,7 @@ static cudaError_t launch_backward_t(const CUtensorMap& ah, const CUtensorMap& b
   // K-major, B N-major) runs in ~0.98 of a dW k-block's time (both N-major): 584 vs 594 SM cycles
   // per 64-deep k-block, measured on the Qwen3.5-2B-like head with cycle counters in the MMA issuer.
   constexpr double kDhKblockCost = 0.98;
-  const double w_cost = dw_tile_cost(p.w_k);
+  const double w_cost = dw_tile_cost(p.w_k, w.bf16_out != 0);
   // The parts of a dH block go to one cluster back to back when the whole block is no longer than
   // kDhBlockMaxShare of a cluster's fair share: the blocks then run side by side on some clusters,
   // each W and exp-tile block read by all the tiles that need it at once, while the other clusters
@@ -1178,30 +1190,19 @@ static cudaError_t launch_backward_t(const CUtensorMap& ah, const CUtensorMap& b
   for (long long q = q0 > 0 ? q0 - 1 : 0; q <= q0 + 1 && q <= nW / P; ++q)
     if (longest(q) < longest(q1)) q1 = q;
   p.w_phase1 = static_cast<int>(q1 * P);
-  return launch_pair<BwdProb, EW>(p, P, s);
+  return launch_pair<BwdProb>(p, P, s);
 }
-
-// Rows of a chunk up to which the backward's epilogue takes eight warps: a dW tile has as many k-blocks as the chunk has
-// rows, so a short chunk's launch is bound by its epilogue. V = 151936, d = 2048, bf16 dW, eight warps and four: 128 rows
-// 319-336 and 399 us, 256 rows 309 and 333, 512 rows 433 and 440, 768 rows 616 and 600, 1024 rows 803-832 and 770-780;
-// 256 rows of d = 4096 660-670 and 723-756.
-constexpr long long kShortRows = 512;
 
 cudaError_t launch_backward(const CUtensorMap& ah, const CUtensorMap& bh, const CUtensorMap& ch, const CUtensorMap& aw,
                             const CUtensorMap& bw, const CUtensorMap& cw, long long rows, long long V, long long d,
                             const DhParams& h, const DwParams& w, int* flags, int num_sms, cudaStream_t s,
                             long long v_begin, long long v_end, bool with_dh) {
   if (h.parts > 0) {  // parts that are not added in the epilogue (dh_parts_balanced)
-    const bool few = rows <= kShortRows;
     if (w.bf16_out)
-      return few ? launch_backward_t<DwBfEpi, false, EPI_WARPS_SHORT>(ah, bh, ch, aw, bw, cw, rows, V, d, h, w, flags, num_sms,
-                                                                      s, v_begin, v_end, with_dh)
-                 : launch_backward_t<DwBfEpi, false>(ah, bh, ch, aw, bw, cw, rows, V, d, h, w, flags, num_sms, s, v_begin,
-                                                     v_end, with_dh);
-    return few ? launch_backward_t<DwEpi, false, EPI_WARPS_SHORT>(ah, bh, ch, aw, bw, cw, rows, V, d, h, w, flags, num_sms, s,
-                                                                  v_begin, v_end, with_dh)
-               : launch_backward_t<DwEpi, false>(ah, bh, ch, aw, bw, cw, rows, V, d, h, w, flags, num_sms, s, v_begin, v_end,
-                                                 with_dh);
+      return launch_backward_t<DwBfEpi, false>(ah, bh, ch, aw, bw, cw, rows, V, d, h, w, flags, num_sms, s, v_begin, v_end,
+                                               with_dh);
+    return launch_backward_t<DwEpi, false>(ah, bh, ch, aw, bw, cw, rows, V, d, h, w, flags, num_sms, s, v_begin, v_end,
+                                           with_dh);
   }
   if (w.bf16_out)
     return launch_backward_t<DwBfEpi>(ah, bh, ch, aw, bw, cw, rows, V, d, h, w, flags, num_sms, s, v_begin, v_end,

@@ -127,7 +127,10 @@ __device__ __forceinline__ void reset_status(const TokParams& p) {
 template <int MODE>
 struct TokEpi {
   using Params = TokParams;
-  struct State {};
+  struct State {
+    long long y;  // TOK_EXP: the row's label and its logit
+    float z;
+  };
 
   // 32 columns c0.. of the half tile: their logits stored, the row's four numbers brought up to date.
   // The maximum and the sums run in four strands each: a warp has its sub-partition's issue slots to
@@ -225,18 +228,19 @@ struct TokEpi {
     }
   }
 
-  static __device__ __forceinline__ void exp_tile(const Params& p, const EpiCtx& ctx, int m0, int col0, uint32_t taddr) {
+  static __device__ __forceinline__ void exp_tile(const Params& p, const State& st, const EpiCtx& ctx, int m0, int col0,
+                                                  uint32_t taddr) {
     const int r = m0 + ctx.row0 + ctx.lane;
     const int vlim = p.V - col0, part = col0 / EPI_COLS;
     if (m0 + ctx.row0 >= p.rows) return;  // no row of this warp
     const bool live = r < p.rows;
-    const long long y = live ? static_cast<long long>(p.y[r]) : p.ignore_index;
+    const long long y = st.y;
     const bool given = live && y != p.ignore_index && y >= 0 && y < p.V;
     float sum = 0.f;
     if (vlim > 0) {
       const long long yc = y - col0;
       const int ycol = given && yc >= 0 && yc < EPI_COLS ? static_cast<int>(yc) : -1;
-      const float z = given ? p.ref[r] : 0.f, k = p.inv_t * kLog2e;
+      const float z = given ? st.z : 0.f, k = p.inv_t * kLog2e;
       const uint32_t keep = given ? ~0u : 0u;  // rows without a token are zero whatever they hold
       uint64_t s[2] = {0, 0};
       float va[32], vb[32];
@@ -251,15 +255,8 @@ struct TokEpi {
         tmem_ld_wait(vb);
         if (c0 + 64 < EPI_COLS) tmem_ld_issue_x32(taddr + c0 + 64, va);
         exp_group(vb, c0 + 32, vlim, ycol, z, k, keep, s, pb);
-        // The store before this one is read while the exponentials are computed.
-        stage_acquire(ctx);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          *reinterpret_cast<uint4*>(ctx.stage + stage_off(ctx.lane, q)) =
-              make_uint4(pa[4 * q], pa[4 * q + 1], pa[4 * q + 2], pa[4 * q + 3]);
-          *reinterpret_cast<uint4*>(ctx.stage + stage_off(ctx.lane, 4 + q)) =
-              make_uint4(pb[4 * q], pb[4 * q + 1], pb[4 * q + 2], pb[4 * q + 3]);
-        }
+        stage_acquire(ctx);  // the store before this one is read while the exponentials are computed
+        stage_bf16(ctx, pa, pb);
         stage_release(ctx, col0 + c0, m0 + ctx.row0, false);
       }
       tmem_ld_wait(va);  // a load that a break left under way
@@ -320,16 +317,17 @@ struct TokProb {
     int m_tiles, n_tiles, k_blocks;
     TokParams ep;
   };
-  struct State {};
+  using State = typename TokEpi<MODE>::State;
   static __device__ __forceinline__ bool skip(const Params& p) { return p.ep.only_if != nullptr && *p.ep.only_if == 0; }
   static __device__ __forceinline__ bool no_loads(const Params& p) { return p.ep.no_loads != 0; }
   static __device__ __forceinline__ int* flags(const Params& p) { return p.ep.flags; }
-  static __device__ __forceinline__ int num_jobs(const Params& p, int c, int P) {
-    const int tiles = p.m_tiles * p.n_tiles;
-    return c < tiles ? (tiles - 1 - c) / P + 1 : 0;
+  using Plan = RoundRobin;
+  static __device__ __forceinline__ Plan plan(const Params& p, int c, int P) {
+    return round_robin(p.m_tiles * p.n_tiles, c, P);
   }
-  static __device__ __forceinline__ TileJob job(const Params& p, int c, int P, int j) {
-    const int t = c + j * P;
+  static __device__ __forceinline__ int num_jobs(const Plan& s) { return s.jobs; }
+  static __device__ __forceinline__ TileJob job(const Params& p, const Plan& s, int j) {
+    const int t = s.c + j * s.P;
     return TileJob{0, t % p.m_tiles, t / p.m_tiles, p.k_blocks, 0, 0};
   }
   static __device__ __forceinline__ bool job_ok(const Params& p, const TileJob& tj) {
@@ -344,13 +342,18 @@ struct TokProb {
   static __device__ __forceinline__ uint64_t b_desc(int, uint32_t addr, int k) { return desc_k_major(addr, k); }
   static __device__ __forceinline__ uint32_t idesc(int) { return idesc_bf16_f32(P_TILE_M, BN, false, false); }
   static __device__ __forceinline__ void init(const Params& p, State&) { reset_status(p.ep); }
-  static __device__ __forceinline__ void epilogue(const Params& p, State&, const TileJob&, EpiCtx ctx, int m0,
+  static __device__ __forceinline__ void ahead(const Params& p, State& st, const TileJob&, int r) {
+    if (MODE != TOK_EXP) return;
+    st.y = r < p.ep.rows ? static_cast<long long>(p.ep.y[r]) : p.ep.ignore_index;
+    st.z = r < p.ep.rows ? p.ep.ref[r] : 0.f;
+  }
+  static __device__ __forceinline__ void epilogue(const Params& p, State& st, const TileJob&, EpiCtx ctx, int m0,
                                                   int col0, uint32_t taddr) {
     ctx.out = &p.c;
     if constexpr (MODE == TOK_GRAD)
       TokEpi<MODE>::grad_tile(p.ep, ctx, m0, col0, taddr);
     else if constexpr (MODE == TOK_EXP)
-      TokEpi<MODE>::exp_tile(p.ep, ctx, m0, col0, taddr);
+      TokEpi<MODE>::exp_tile(p.ep, st, ctx, m0, col0, taddr);
     else
       TokEpi<MODE>::stats_tile(p.ep, ctx, m0, col0, taddr);
   }
@@ -1184,10 +1187,9 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_distill_row(const DistillArg
 // ----------------------------------------------------------------------------
 // Launch wrappers
 // ----------------------------------------------------------------------------
-// Hidden size up to which the exp tile's epilogue takes eight warps: a tile of few k-blocks is bound by the latencies of
-// its epilogue, a tile of many by the MMA. 2048 rows of V = 151936, eight warps and four: d = 256 225 and 253 us, 512 270
-// and 278, 1024 level; at 2048 the difference is within the noise and four leave more issue slots.
-constexpr long long kExpShortK = 512;
+// Hidden size up to which the exp tile's epilogue takes eight warps: a tile of few k-blocks is bound by its epilogue, a tile
+// of many by the MMA. 2048 rows of V = 151936, eight warps and four: d = 64 128 and 182 us, 256 159 and 186, 512 217 and 215.
+constexpr long long kExpShortK = 256;
 
 cudaError_t launch_tok_logits(int mode, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, long long M,
                               long long N, long long K, const TokParams& ep, int num_sms, cudaStream_t s) {

@@ -1102,7 +1102,8 @@ def lce_policy_fwd_bwd(H, W, y, advantages, old_logp=None, ref_logp=None, grad_l
                        need_dW: bool = True, workspace=None, stream=None, **opt_kw):
     """lce_policy_forward and its gradients in one call: loss, logp, row_loss, dH
     (bf16 [N, d]), dW (fp32 [V, d], or bf16 with dW_dtype); a gradient that is
-    not wanted is None."""
+    not wanted is None. By default a large call holds 2 bytes a logit of up to
+    18432 rows; chunk_tokens bounds that."""
     import torch
     N, d, V, policy = _check_policy(H, W, y, advantages, old_logp, ref_logp, weights, kl, kl_coef, clip_low, clip_high,
                                     dual_clip)
@@ -1170,7 +1171,8 @@ def lce_preference_fwd_bwd(H, W, y, cu_seqlens, ref_logp=None, grad_loss=None, *
     """lce_preference_forward and its gradients in one call: loss, pair_loss,
     seq_logp, dH (bf16 [N, d]), dW (fp32 [V, d], or bf16 with dW_dtype); a
     gradient that is not wanted is None. Rows of more than one chunk
-    (chunk_tokens, by default 6143) have their logits computed twice."""
+    (chunk_tokens, by default 6143, or 18432 where exp tiles are kept: see
+    include/lce.h) have their logits computed twice."""
     import torch
     N, d, V, P, pref = _check_preference(H, W, y, cu_seqlens, ref_logp, kind, beta, label_smoothing, margin, average)
     _check_dev(grad_loss, "grad_loss", torch.float32, numel=1, device=H.device)
