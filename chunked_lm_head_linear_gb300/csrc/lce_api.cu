@@ -1509,8 +1509,15 @@ struct LossLayout {
 // bytes each, the exp tile's further launches some 4 us that the launches around them do not hide. Policy steps (replayed
 // from a graph) with kept logits / exp tiles, us: 256 x 8192 x 256 (rows, V, d) 31.3 / 32.3, 416 x 16818 x 2032 92.0 / 93.9,
 // 256 x 32000 x 256 47.2 / 43.1, 1024 x 8192 x 256 43.2 / 40.5, 512 x 16384 x 2048 96.8 / 93.0, 1024 x 32000 x 256 110 / 68,
-// 512 x 151936 x 256 330 / 140, 1024 x 151936 x 2048 1344 / 1142.
-constexpr int64_t kExpLogits = 8000000;
+// 512 x 151936 x 256 330 / 140, 1024 x 151936 x 2048 1344 / 1142. Few rows (up to 96) leave that pass, a block a row, to few
+// SMs: 32 x 32000 x 256 36.5 / 39.7, 64 x 65536 (4.2 million) level, 96 x 49152 x 256 53.4 / 49.0, 96 x 65536 x 2048 191 /
+// 182, 96 x 151936 x 256 122 / 83; with V from about 98304 on however few: 8 x 65536 x 256 50.3 / 53.8, 8 x 98304 x 256 67.1 /
+// 63.9 (x 2048 258 / 264), 4 x 151936 x 256 90.5 / 80.8 (x 2048 385 / 365).
+constexpr int64_t kExpLogits = 8000000, kExpLogitsFew = 4500000, kExpV = 98304;
+
+bool exp_tiles_pay(int64_t rows, int64_t V) {
+  return V >= kExpV || rows * V >= (rows <= lce::kFewRows ? kExpLogitsFew : kExpLogits);
+}
 
 // Most rows whose exp tiles are kept together by default (logits launches of at most 6143 rows each, so that a launch's
 // H stays in L2): 2 bytes a logit, as much as the kept logits and the gradient tile of one chunk of 6144 rows take. One
@@ -1524,7 +1531,7 @@ LossLayout loss_layout(int64_t N, int64_t d, int64_t V, int64_t pairs, bool with
   LossLayout L;
   lce_opts o = *opts;
   L.step = tok_chunk(N, &o);
-  const bool large = with_grad && L.step > lce::kFewRows && L.step * V >= kExpLogits;
+  const bool large = with_grad && N > 0 && exp_tiles_pay(L.step, V);
   if (large && o.chunk_tokens == 0 && N <= kExpRows) o.chunk_tokens = N;
   const bool one = N <= tok_chunk(N, &o);
   L.exp = large && (pairs < 0 || one);

@@ -411,10 +411,17 @@ int lce_scale_grads_bfloat(void* dH, void* dW, int64_t N, int64_t d, int64_t V, 
 /*
  * Losses on the log-probabilities of given tokens, with their gradients in one
  * call (6 N V d flops, as lce_fwd_bwd). z, z', p, logp, H, W, y, opts, grads, ws
- * and stream are those of the token operators; chunk_tokens = 0 cuts the rows as
- * they do. grad_loss: device fp32 [1] or NULL (1.0); either of dH, dW may be
- * NULL: not wanted, not computed. opts->reserved must be 0. All arrays of floats
- * are fp32, on the device.
+ * and stream are those of the token operators. grad_loss: device fp32 [1] or NULL
+ * (1.0); either of dH, dW may be NULL: not wanted, not computed. opts->reserved
+ * must be 0. All arrays of floats are fp32, on the device.
+ * Small calls keep the chunk's logits (4 bytes a logit, and 2 for the gradient
+ * tile); large ones (8 million logits or more in a chunk, 4.5 million in one of
+ * up to 96 rows, or a vocabulary of 98304 or more) keep the tile alone.
+ * chunk_tokens = 0 cuts the rows as the token operators do, but a large call with
+ * gradients keeps the tiles of up to 18432 rows together (2 bytes a logit), so
+ * that one launch writes dW; name a chunk to hold less. Results of other chunk
+ * sizes differ in the order of fp32 sums and, between the two ways, in the
+ * rounding of the gradient tile; a call repeats itself bit for bit.
  *
  * lce_policy_forward, lce_policy_fwd_bwd: the clipped policy loss. Per row with a
  * given token (y neither ignore_index nor out of range), A = advantages_i, w =
@@ -480,9 +487,11 @@ int lce_policy_fwd_bwd(const void* H, const void* W, const int64_t* y, int64_t N
  * label_smoothing must be 0 but for the first. beta > 0. Outputs: loss [1],
  * pair_loss [pairs], seq_logp [2 pairs] (S), dH, dW as above; rows in no sequence
  * have a zero gradient. S is summed in fp64. Bounds that fall, or leave [0, N],
- * set LCE_DEVICE_LABEL_RANGE; that pair then has no loss and no gradient. Where
- * the rows are one chunk their logits are kept for the gradient, else they are
- * computed twice (8 N V d flops). Workspace: lce_preference_workspace_size.
+ * set LCE_DEVICE_LABEL_RANGE; that pair then has no loss and no gradient (a row
+ * that bounds out of order give to several sequences has that of one of them).
+ * Where all rows' logits or tiles are held together (one chunk) they are used for
+ * the gradient, else the logits are computed twice (8 N V d flops); without pairs
+ * cu_seqlens is not read. Workspace: lce_preference_workspace_size.
  */
 #define LCE_PREFERENCE_SIGMOID 0
 #define LCE_PREFERENCE_HINGE 1

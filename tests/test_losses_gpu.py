@@ -67,7 +67,8 @@ def head(H, W, y, T):
 
 
 def uses_exp_tiles(N, V, chunk):
-    return min(N, chunk or N) > 96 and min(N, chunk or N) * V >= 8_000_000
+    rows = min(N, chunk or N)
+    return V >= 98304 or rows * V >= (4_500_000 if rows <= 96 else 8_000_000)
 
 
 def check_gradients(dH, dW, ref, slack, exp=False):
@@ -640,6 +641,26 @@ def test_exp_tiles_of_a_label_past_fp32(cuda_lib):
     others = torch.arange(6, device="cuda") != seq
     assert got[0].isnan().all() and (0 <= seq < 6) and got[2][seq].isnan() and torch.isfinite(got[2][others]).all()
     assert torch.isfinite(want_seq).all()
+
+
+@pytest.mark.parametrize("N,V", [(1, 100003), (5, 98304), (60, 80101), (96, 131072)])
+def test_exp_tiles_of_few_rows(cuda_lib, N, V):
+    """Few rows of a large vocabulary, and the same with a label out of the tile's range."""
+    rng, H, W, y = make(N, 64, V, seed=N)
+    y[-1] = V - 1
+    for far in (False, True):
+        if far:
+            W[:, 0] = 0.0
+            H[:, 0] = 0.0
+            W[y[-1], 0] = -1.0
+            H[-1, 0] = 100.0
+        Ht, Wt = heads(H, W)
+        inp = policy_inputs(rng, H, W, y, 1.0)
+        kw = dict(clip_low=0.2, clip_high=0.28, kl="k3", kl_coef=0.1)
+        check_policy(call_policy(cuda_lib, Ht, Wt, dev(y), inp, sync_check=True, **kw), H, W, y, inp, **kw)
+        cu = bounds(rng, N, 2)
+        check_preference(call_preference(cuda_lib, Ht, Wt, y, cu, None, average=True, sync_check=True), H, W, y, cu, None,
+                         average=True)
 
 
 @pytest.mark.parametrize("shift", [50.0, 70.0, 200.0])
