@@ -272,6 +272,10 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T, B) k_layernorm_fwd(const La
 // teams' shares are added in order and the block writes one partial row of each.
 // ONE: the launch is one cluster, whose blocks add their shares through each
 // other's shared memory, in order; there is nothing left for another launch.
+// Bound by HBM: x and dH read once, dx written once, 65536 rows of bf16 in 19 us
+// (d = 256), 37, 68, 134, 246 (4096) with the sum of the partial rows, 32768 of
+// fp32 in 107 (2048), 201 (4096); at the copy rate 15, 30, 59, 119, 237 and 99, 198.
+// (dx and dw in two kernels, each reading both, took 596 us at 65536 x 4096.)
 template <bool F32, int T, int K, int R, int D, int B, bool ONE>
 __global__ void __launch_bounds__(kLnThreads, B) k_layernorm_bwd(const LayerNormArgs p) {
   grid_dep_wait();

@@ -16,8 +16,13 @@
 // so E with -R in the label's place is the tile, the factor the row's scale, and
 // neither p_y near 1 (R keeps its relative precision) nor a far label loses
 // anything as long as the sums are finite. Where one is not (a label more than 60
-// nats below its row's maximum, at T = 1), a guard turns on three launches that
-// otherwise return at once: exact statistics, and the exact gradient tile.
+// nats below its row's maximum, at T = 1, or a logit that is not finite), a guard
+// turns on two launches that otherwise return at once: exact statistics, and the
+// exact gradient tile. A factor so small that a / (T (1 + R)) leaves fp32 is lost.
+//
+// The kernels here are short beside the GEMMs (1024 rows of d = 2048 and V =
+// 151936: label logits 7.3 us, rows 9.0, of 1130): one block a row, bound by the
+// latency of its few dependent reads; over kept logits by HBM (6 bytes a logit).
 #include "lce_rows.cuh"
 
 namespace lce {
