@@ -1187,17 +1187,21 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_distill_row(const DistillArg
 // ----------------------------------------------------------------------------
 // Launch wrappers
 // ----------------------------------------------------------------------------
-// Hidden size up to which the exp tile's epilogue takes eight warps: a tile of few k-blocks is bound by its epilogue, a tile
-// of many by the MMA. 2048 rows of V = 151936, eight warps and four: d = 64 128 and 182 us, 256 159 and 186, 512 217 and 215.
-constexpr long long kExpShortK = 256;
+// Hidden size up to which epilogues that store little (bf16 exp tiles, or nothing) take eight warps: a tile of few k-blocks
+// is bound by its epilogue, a tile of many by the MMA. 2048 rows of V = 151936, eight warps and four, us: exp tiles d = 64
+// 128 and 182, 256 159 and 186, 512 217 and 215; statistics alone d = 64 140 and 196, 256 174 and 200, 512 212 and 209; with
+// fp32 logits stored d = 256 272 and 253.
+constexpr long long kShortK = 256;
 
 cudaError_t launch_tok_logits(int mode, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, long long M,
                               long long N, long long K, const TokParams& ep, int num_sms, cudaStream_t s) {
   switch (mode) {
-    case TOK_STATS: return launch_tok_mode<TOK_STATS>(a, b, c, M, N, K, ep, num_sms, s);
+    case TOK_STATS:
+      return K <= kShortK ? launch_tok_mode<TOK_STATS, EPI_WARPS_SHORT>(a, b, c, M, N, K, ep, num_sms, s)
+                          : launch_tok_mode<TOK_STATS>(a, b, c, M, N, K, ep, num_sms, s);
     case TOK_STATS_Z: return launch_tok_mode<TOK_STATS_Z>(a, b, c, M, N, K, ep, num_sms, s);
     case TOK_EXP:
-      return K <= kExpShortK ? launch_tok_mode<TOK_EXP, EPI_WARPS_SHORT>(a, b, c, M, N, K, ep, num_sms, s)
+      return K <= kShortK ? launch_tok_mode<TOK_EXP, EPI_WARPS_SHORT>(a, b, c, M, N, K, ep, num_sms, s)
                              : launch_tok_mode<TOK_EXP>(a, b, c, M, N, K, ep, num_sms, s);
     default: return launch_tok_mode<TOK_GRAD>(a, b, c, M, N, K, ep, num_sms, s);
   }
