@@ -3,6 +3,8 @@
 // tcgen05 MMA with TMEM accumulators, and the shared-memory / instruction
 // descriptors those MMAs read. Every wait is bounded: a wait that runs out
 // returns false so the caller can record an error and leave cleanly.
+// Instructions with .aligned ask for a whole warp: their wrappers begin with
+// __syncwarp(), so that a caller may have branched by lane before.
 #pragma once
 
 #include <cuda.h>
@@ -134,16 +136,19 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 // tcgen05: TMEM allocation, MMA, commit, loads, fences (cta_group::1)
 // ----------------------------------------------------------------------------
 __device__ __forceinline__ void tmem_alloc(uint32_t* smem_holder, uint32_t ncols) {
+  __syncwarp();
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem_holder)),
                "r"(ncols)
                : "memory");
 }
 
 __device__ __forceinline__ void tmem_relinquish() {
+  __syncwarp();
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  __syncwarp();
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
@@ -176,6 +181,7 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
 // 32 lanes x 32 consecutive fp32 columns: thread t of the warp receives the
 // 32 columns of TMEM lane (lane base + t) starting at the address's column.
 __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, float (&v)[32]) {
+  __syncwarp();
   uint32_t r[32];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -195,6 +201,7 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, float (&v)[32
 // The same in two steps, so that the next load can be under way while a group
 // is worked on: issue, and a wait that every later use of v depends on.
 __device__ __forceinline__ void tmem_ld_issue_x32(uint32_t taddr, float (&v)[32]) {
+  __syncwarp();
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -208,6 +215,7 @@ __device__ __forceinline__ void tmem_ld_issue_x32(uint32_t taddr, float (&v)[32]
 }
 
 __device__ __forceinline__ void tmem_ld_wait(float (&v)[32]) {
+  __syncwarp();
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
                  "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
@@ -260,6 +268,7 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 
 // Every thread of every CTA of the cluster arrives, then waits for all.
 __device__ __forceinline__ void cluster_sync_all() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -323,16 +332,19 @@ __device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorM
 }
 
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* smem_holder, uint32_t ncols) {
+  __syncwarp();
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem_holder)),
                "r"(ncols)
                : "memory");
 }
 
 __device__ __forceinline__ void tmem_relinquish_pair() {
+  __syncwarp();
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  __syncwarp();
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
