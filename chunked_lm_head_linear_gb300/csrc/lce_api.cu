@@ -1632,7 +1632,10 @@ int exp_fallback(const Call& c, int64_t c0, int64_t rows, lce::TokParams p, cons
   return tok_logits(c, c0, rows, lce::TOK_GRAD, a.G, c.L.ldp, p);
 }
 
-void loss_row_exp(lce::LossRowArgs* a, const Call& c, const LossLayout& L, const int* guard, int64_t at) {
+// Rows [c0, ...) of the call, in the chunk's buffers from row `at` on.
+void loss_row_exp(lce::LossRowArgs* a, const Call& c, const LossLayout& L, const int* guard, int64_t c0, int64_t at) {
+  a->ref = reinterpret_cast<const float*>(c.ws + L.ref) + c0;
+  a->ztgt = reinterpret_cast<const float*>(c.ws + c.L.ztgt) + at;
   a->sums = reinterpret_cast<const float*>(c.ws + L.sums) + at * a->nparts;
   a->guard = guard;
   a->a = reinterpret_cast<float*>(c.ws + L.a) + at;
@@ -1707,7 +1710,7 @@ int policy_loss(const void* H, const void* W, const int64_t* y, int64_t N, int64
     a.row = loss_row(c, T, c0, p, Z, with_grad, dW != nullptr, at);
     a.row.logp = logp + c0;
     if (L.exp) {
-      loss_row_exp(&a.row, c, L, guard, at);
+      loss_row_exp(&a.row, c, L, guard, c0, at);
       a.row.stats = reinterpret_cast<float2*>(c.ws + T.stats) + at;
     }
     a.advantages = advantages + c0;
@@ -1819,7 +1822,7 @@ int preference_loss(const void* H, const void* W, const int64_t* y, int64_t N, i
       lce::LossRowArgs a = loss_row(c, T, c0, p, nullptr, true, false, c0);
       a.logp = logp + c0;
       a.stats = stats + c0;
-      loss_row_exp(&a, c, L, guard + k, c0);
+      loss_row_exp(&a, c, L, guard + k, c0, c0);
       LCE_TRY(timed(c.s, K_COMBINE, static_cast<double>(rows) * (8.0 * static_cast<double>(c.L.T) + 28.0),
                     [&] { return cuda_rc(lce::launch_logp_rows(a, q, pairs_here, static_cast<int>(rows), c.s)); }));
       continue;
@@ -1854,7 +1857,7 @@ int preference_loss(const void* H, const void* W, const int64_t* y, int64_t N, i
     a.cu32 = cu32;
     a.P = pairs;
     a.coef = coef;
-    if (L.exp) loss_row_exp(&a.row, c, L, guard + k, at);
+    if (L.exp) loss_row_exp(&a.row, c, L, guard + k, c0, at);
     LCE_TRY(timed(c.s, K_COMBINE, static_cast<double>(rows) * (4.0 * static_cast<double>(d) + (Z ? 6.0 * static_cast<double>(V) : 0.0)),
                   [&] { return cuda_rc(lce::launch_preference_row(a, static_cast<int>(rows), c.s)); }));
     if (L.exp) {  // the tiles of all rows are there: one backward launch behind the last of them

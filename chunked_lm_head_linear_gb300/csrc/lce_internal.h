@@ -304,7 +304,7 @@ struct TokParams {
   long long ignore_index;
   const int64_t* y;      // labels of this chunk (TOK_STATS, TOK_GRAD)
   float4* partials;      // [rows, nparts] (m, s, t, c), see lce_tokens.cu
-  float* ztgt;           // [rows] logit of the label (TOK_STATS)
+  float* ztgt;           // [rows] logit of the label (TOK_STATS, TOK_EXP)
   const float* lse;      // [rows] (TOK_GRAD; the next four too), used without stats
   const float2* stats;   // [rows] (max z, log sum exp((z - max)/T)), or null
   const float* entropy;  // [rows]
@@ -318,15 +318,19 @@ struct TokParams {
   int* cnt;
   int ncnt;
   int no_loads;          // timeout test only: no operand is loaded, so the waits run out
-  const float* ref;      // [rows] the labels' logits (TOK_EXP; the next two too)
+  const float* ref;      // [rows] the labels' logits from before the GEMM (TOK_EXP; the next two too)
   float* sums;           // [rows, nparts] sums of the exp tile, the label's column left out
-  int* guard;            // set to 1 where a sum of a row with a given token is not below kExpGuard
+  int* guard;            // set to 1 where a sum of a row with a given token is not below kExpGuard, or ref is further
+                         // than kExpShift T from ztgt
   const int* only_if;    // not null: the launch does nothing unless *only_if != 0 (TOK_STATS, TOK_GRAD)
 };
 
 // An exp tile is used while its half tiles' sums stay below this: entries and sums are then finite, and what
 // they are scaled by, 1 / (1 + their sum), is a normal number.
 constexpr float kExpGuard = 1.0e26f;
+// Nats by which the label's logit from before the GEMM may differ from the GEMM's own: the tile is against the one, the
+// row's results against the other (a factor of e^8 leaves the sums finite). Only the coldest temperatures come near.
+constexpr float kExpShift = 8.f;
 
 struct TokScoreArgs {
   int rows, V, nparts, K;
@@ -429,7 +433,7 @@ struct LossRowArgs {
   long long ignore_index;
   const int64_t* y;        // [rows] labels of this chunk
   const float4* partials;  // [rows, nparts]
-  const float* ztgt;       // Z null: the label logits
+  const float* ztgt;       // Z null: the label logits of the GEMM
   const float* Z;          // [rows, ldz] fp32 logits, or null: no gradient tile here
   __nv_bfloat16* G;        // [rows, ldg]
   const uint4* H;          // [rows, d] bf16
@@ -443,7 +447,8 @@ struct LossRowArgs {
   // from the exp tile (sums not null): used where *guard == 0, else the row comes from partials and ztgt
   const float* sums;       // [rows, nparts]
   const int* guard;
-  float* rest;             // [rows] sum of exp((z_v - z_y)/T) over v != y: out, then in (preference)
+  const float* ref;        // [rows] the label logits that the tile's entries are against
+  float* rest;             // [rows] sum of the row's entries but the label's: out, then in (preference)
 };
 
 struct PolicyArgs {

@@ -15,10 +15,15 @@
 //   logp = -log1p(R),  p_v = E_v / (1 + R),  G_v = -(a / T) / (1 + R) (E_v, at y: -R)
 // so E with -R in the label's place is the tile, the factor the row's scale, and
 // neither p_y near 1 (R keeps its relative precision) nor a far label loses
-// anything as long as the sums are finite. Where one is not (a label more than 60
-// nats below its row's maximum, at T = 1, or a logit that is not finite), a guard
-// turns on two launches that otherwise return at once: exact statistics, and the
-// exact gradient tile. A factor so small that a / (T (1 + R)) leaves fp32 is lost.
+// anything as long as the sums are finite. That z_y is a sum of its own, which
+// errs otherwise than the tensor core's sums of the row: by 2e-5 at d = 2048, 1e-4
+// at 7168, and all of E with it. The GEMM meets the label's column too; with its
+// value z_y' and f = exp((z_y - z_y')/T) the row's sum is f R, and the
+// log-probabilities are those of the other operators. Where a sum is not finite (a
+// label more than 60 nats below its row's maximum, at T = 1, or a logit that is not
+// finite), a guard turns on two launches that otherwise return at once: exact
+// statistics, and the exact gradient tile. A factor so small that a / (T (1 + R))
+// leaves fp32 is lost.
 //
 // The kernels here are short beside the GEMMs (1024 rows of d = 2048 and V =
 // 151936: label logits 7.3 us, rows 9.0, of 1130): one block a row, bound by the
@@ -58,13 +63,16 @@ __device__ __forceinline__ float exp_rest(const LossRowArgs& p, int r, float* re
   return block_sum(s, red);
 }
 
+// What the entries of row r, which has a label, and their sum are multiplied by to be against the GEMM's own z_y.
+__device__ __forceinline__ float exp_shift(const LossRowArgs& p, int r) { return expf((p.ref[r] - p.ztgt[r]) * p.inv_t); }
+
 // The row's scale, the label's entry of the exp tile and the row of dW's second operand. The entry is
 // rounded to bf16; the scale makes up for that, as the label's is as a rule the row's largest share.
-__device__ __forceinline__ void exp_gradient(const LossRowArgs& p, int r, int y, float a, float rest) {
+__device__ __forceinline__ void exp_gradient(const LossRowArgs& p, int r, int y, float a, float rest, float shift) {
   const int tid = threadIdx.x;
   const __nv_bfloat16 label = __float2bfloat16_rn(rest);
   const float held = __bfloat162float(label);
-  float scale = -a * p.inv_t / (1.f + rest);
+  float scale = -a * p.inv_t * shift / fmaf(rest, shift, 1.f);
   if (held >= 1.0e-30f) scale *= rest / held;
   if (tid == 0) {
     p.rowscale[r] = scale;
@@ -196,14 +204,15 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_policy_row(const PolicyArgs 
   const int r = blockIdx.x, tid = threadIdx.x;
   const LossRowArgs& q = p.row;
   const int y = given_label(q.y, r, q.ignore_index, q.V);
-  float logp = 0.f, a = 0.f, rest = 0.f;
+  float logp = 0.f, a = 0.f, rest = 0.f, shift = 1.f;
   double row = 0.0;  // thread 0's
   RowStats s{0.f, 0.f};
   const bool by_exp = EXP && *q.guard == 0;
   if (y >= 0) {
     if (by_exp) {
       rest = exp_rest(q, r, red);
-      logp = -log1pf(rest);
+      shift = exp_shift(q, r);
+      logp = -log1pf(rest * shift);
     } else {
       s = merge_row(q, r, red, s_sum);
       const float z = q.Z != nullptr ? q.Z[static_cast<long long>(r) * q.ldz + y] : q.ztgt[r];
@@ -225,7 +234,7 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_policy_row(const PolicyArgs 
   }
   if (GRAD) {
     if (by_exp)
-      exp_gradient(q, r, y, a, rest);
+      exp_gradient(q, r, y, a, rest, shift);
     else
       row_gradient<TILE>(q, r, y, a, logp, s);
   }
@@ -379,7 +388,7 @@ __global__ void __launch_bounds__(kRowThreads) k_logp_rows(const LossRowArgs p, 
   if (y >= 0) {
     if (EXP && *p.guard == 0) {
       rest = exp_rest(p, r, red);
-      logp = -log1pf(rest);
+      logp = -log1pf(rest * exp_shift(p, r));
     } else {
       s = merge_row(p, r, red, s_rows);
       const float z = p.Z != nullptr ? p.Z[static_cast<long long>(r) * p.ldz + y] : p.ztgt[r];
@@ -448,7 +457,7 @@ __global__ void __launch_bounds__(kRowThreads, 8) k_preference_row(const Prefere
     if (s >= 0 && s < 2 * p.P) a = p.coef[s];
   }
   if (EXP && *q.guard == 0) {
-    exp_gradient(q, r, y, a, q.rest[r]);
+    exp_gradient(q, r, y, a, q.rest[r], y >= 0 ? exp_shift(q, r) : 1.f);
     return;
   }
   const float2 st = q.stats[r];

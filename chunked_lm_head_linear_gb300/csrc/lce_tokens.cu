@@ -97,7 +97,9 @@ __device__ __forceinline__ void add_columns(Mst& a, float (&v)[32], float inv_t)
 //                before the GEMM, and the sums of E without the label's column: with
 //                R their sum logp = -log1p(R) and p_v = E_v / (1 + R), so that the
 //                tile is the gradient's up to a factor per row and nothing needs the
-//                logits again. A sum that is too large, or NaN, sets the guard.
+//                logits again. The label's logit as this GEMM has it goes out too, for
+//                the row kernels to refer R to. A sum that is too large, or NaN, or the
+//                two logits of a label far apart, set the guard.
 // ----------------------------------------------------------------------------
 __device__ __forceinline__ void clear_status(DevStatus* st, int* cnt, int ncnt, int thread, int threads) {
   for (int i = thread; i < ncnt; i += threads) cnt[i] = 0;
@@ -203,9 +205,9 @@ struct TokEpi {
     if (MODE == TOK_STATS && have_t) p.ztgt[r] = zt;
   }
 
-  // 32 columns c0.. of the exp tile in bf16; their sum is added to s.
+  // 32 columns c0.. of the exp tile in bf16; their sum is added to s. zt: the label's logit, if it is among them.
   static __device__ __forceinline__ void exp_group(float (&v)[32], int c0, int vlim, int ycol, float z, float k,
-                                                   uint32_t keep, uint64_t (&s)[2], uint32_t (&pk)[16]) {
+                                                   uint32_t keep, uint64_t (&s)[2], uint32_t (&pk)[16], float& zt) {
     if (vlim < c0 + 32) {
 #pragma unroll
       for (int c = 0; c < 32; ++c)
@@ -215,7 +217,10 @@ struct TokEpi {
     if (yo >= 0 && yo < 32) {  // the label's own column has no part in the sum; its entry is written later
 #pragma unroll
       for (int c = 0; c < 32; ++c)
-        if (c == yo) v[c] = kMasked;
+        if (c == yo) {
+          zt = v[c];
+          v[c] = kMasked;
+        }
     }
     const uint64_t z2 = pair_f32(-z, -z), k2 = pair_f32(k, k);
 #pragma unroll
@@ -236,11 +241,11 @@ struct TokEpi {
     const bool live = r < p.rows;
     const long long y = st.y;
     const bool given = live && y != p.ignore_index && y >= 0 && y < p.V;
-    float sum = 0.f;
+    const long long yc = y - col0;
+    const int ycol = given && yc >= 0 && yc < EPI_COLS ? static_cast<int>(yc) : -1;
+    const float z = given ? st.z : 0.f, k = p.inv_t * kLog2e;
+    float sum = 0.f, zt = z;
     if (vlim > 0) {
-      const long long yc = y - col0;
-      const int ycol = given && yc >= 0 && yc < EPI_COLS ? static_cast<int>(yc) : -1;
-      const float z = given ? st.z : 0.f, k = p.inv_t * kLog2e;
       const uint32_t keep = given ? ~0u : 0u;  // rows without a token are zero whatever they hold
       uint64_t s[2] = {0, 0};
       float va[32], vb[32];
@@ -251,10 +256,10 @@ struct TokEpi {
         uint32_t pa[16], pb[16];
         tmem_ld_wait(va);
         tmem_ld_issue_x32(taddr + c0 + 32, vb);
-        exp_group(va, c0, vlim, ycol, z, k, keep, s, pa);
+        exp_group(va, c0, vlim, ycol, z, k, keep, s, pa, zt);
         tmem_ld_wait(vb);
         if (c0 + 64 < EPI_COLS) tmem_ld_issue_x32(taddr + c0 + 64, va);
-        exp_group(vb, c0 + 32, vlim, ycol, z, k, keep, s, pb);
+        exp_group(vb, c0 + 32, vlim, ycol, z, k, keep, s, pb, zt);
         stage_acquire(ctx);  // the store before this one is read while the exponentials are computed
         stage_bf16(ctx, pa, pb);
         stage_release(ctx, col0 + c0, m0 + ctx.row0, false);
@@ -266,7 +271,8 @@ struct TokEpi {
     }
     if (!live || !in_bounds(part, p.nparts, p.flags)) return;
     p.sums[static_cast<long long>(r) * p.nparts + part] = sum;
-    if (given && !(sum <= kExpGuard)) *p.guard = 1;
+    if (ycol >= 0) p.ztgt[r] = zt;
+    if (given && !(sum <= kExpGuard && fabsf(z - zt) * p.inv_t <= kExpShift)) *p.guard = 1;
   }
 
   static __device__ __forceinline__ void grad_tile(const Params& p, const EpiCtx& ctx, int m0, int col0,

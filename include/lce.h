@@ -421,7 +421,9 @@ int lce_scale_grads_bfloat(void* dH, void* dW, int64_t N, int64_t d, int64_t V, 
  * gradients keeps the tiles of up to 18432 rows together (2 bytes a logit), so
  * that one launch writes dW; name a chunk to hold less. Results of other chunk
  * sizes differ in the order of fp32 sums and, between the two ways, in the
- * rounding of the gradient tile; a call repeats itself bit for bit.
+ * rounding of the gradient tile; a call repeats itself bit for bit. In all of them
+ * logp is lce_logprobs' but for the rounding of sums of exponentials (a few 1e-6):
+ * the ratio to a model's own log-probabilities is 1.
  *
  * lce_policy_forward, lce_policy_fwd_bwd: the clipped policy loss. Per row with a
  * given token (y neither ignore_index nor out of range), A = advantages_i, w =

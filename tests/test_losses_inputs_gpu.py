@@ -1,0 +1,85 @@
+"""The policy and preference losses on hidden states and weights as a model gives them (normally distributed bf16), whose
+logits no fp32 sum has exactly; against the other operators of the head, and against fp64 on the device.
+
+Tolerances, eps = 2^-24, u = 2^-8, x the largest |z_v - m| of the row over T:
+  between operators  both take the logits from the same GEMM. On either side a term exp(x) errs by the roundings of its
+                     argument, 3 eps x, and 2^-22 (ex2.approx); its sum runs through 32 terms, 4 groups and 40 merges of
+                     half tiles, and logp's own operations add 8 eps (|logp| + 2): (3 x + 4 + 76 + 8 (|logp| + 2)) eps a side
+  against fp64       the GEMM adds d / 16 partial products into an fp32 that may be cut instead of rounded: each step
+                     2^-23 of the sum so far, which is at most the row's sum of |h w| =: s; so a logit errs by
+                     tz = (d / 16) 2^-23 s at most, logp by 2 tz / T and the above
+  gradients          p errs by 2 tz relative; entries and scales as in test_losses_gpu.py (exp tiles)
+"""
+import numpy as np
+import pytest
+
+from test_losses_gpu import uses_exp_tiles
+from test_tokens_gpu import U
+
+pytestmark = pytest.mark.gpu
+
+EPS = 2.0 ** -24
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def model_inputs(N, d, V, peak=14.0, seed=0):
+    torch = _torch()
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    W = (torch.randn(V, d, generator=g, device="cuda") * 0.02).bfloat16()
+    y = torch.randint(0, V, (N,), generator=g, device="cuda")
+    lean = peak * torch.rand(N, 1, generator=g, device="cuda") / (0.0004 * d)
+    H = (torch.randn(N, d, generator=g, device="cuda") + W[y].float() * lean).bfloat16()
+    y[::9] = -100
+    return g, H, W, y
+
+
+@pytest.mark.parametrize("N,d,V,T", [(300, 2048, 40001, 1.0), (300, 7168, 40001, 1.0), (300, 7168, 40001, 0.5),
+                                     (100, 4096, 100003, 1.0), (200, 7168, 4099, 1.0)])
+def test_losses_of_a_models_hidden_states(cuda_lib, N, d, V, T):
+    torch = _torch()
+    g, H, W, y = model_inputs(N, d, V, seed=d)
+    told = y >= 0
+    at = torch.where(told, y, 0)[:, None]
+    A = torch.randn(N, generator=g, device="cuda")
+    cu = torch.tensor([0, N // 3, N // 2, N - 20, N - 1], device="cuda")
+    kw = dict(temperature=T, sync_check=True)
+    loss, logp, row, dH, dW = cuda_lib.lce_policy_fwd_bwd(H, W, y, A, dW_dtype=torch.bfloat16, **kw)
+    other = cuda_lib.lce_logprobs(H, W, y, temperature=T)[0]
+    forward = cuda_lib.lce_policy_forward(H, W, y, A, temperature=T)[1]
+    seq = cuda_lib.lce_preference_fwd_bwd(H, W, y, cu, **kw)[2]
+    z = H.double() @ W.double().t() / T
+    far = (z.amax(1) - z.amin(1)).clamp_min(1.0)
+    e = torch.exp(z - z.gather(1, at)).scatter_(1, at, 0.0)
+    rest = e.sum(1)
+    want = torch.where(told, -torch.log1p(rest), 0.0)
+    side = (3 * far + 80 + 8 * (want.abs() + 2)) * EPS
+    for got, name in ((logp, "policy step"), (forward, "policy loss")):
+        assert ((got - other).abs() <= 2 * side).all(), (name, ((got - other).abs() / side).max().item())
+    for s in range(4):
+        rows = slice(int(cu[s]), int(cu[s + 1]))
+        assert (seq[s].double() - other[rows].double().sum()).abs() <= 2 * side[rows].sum() + 2 * EPS * want[rows].abs().sum()
+    # a ratio to the same model's log-probabilities is 1
+    ratio = cuda_lib.lce_policy_fwd_bwd(H, W, y, torch.ones_like(A), other, clip_low=0.0, clip_high=0.0, **kw)[2]
+    assert ((ratio + told.float()).abs() <= 2 * side + 2 * EPS).all()
+    s = (H.double().abs() @ W.double().abs().t()).amax(1)
+    tz = (d / 16) * 2.0 ** -23 * s / T
+    assert ((logp - want).abs() <= 2 * tz + side).all(), ((logp - want).abs() / (2 * tz + side)).max().item()
+    # gradients, at columns of both ends
+    a = torch.where(told, -A.double(), 0.0)[:, None] / int(told.sum()) / T
+    p = e / (1 + rest)[:, None]
+    G = (-p).scatter_(1, at, (rest / (1 + rest))[:, None]) * a
+    size = G.abs()
+    exp = 1 if uses_exp_tiles(N, V, 0) else 0
+    slack = (2 * tz + 2.0 ** -10)[:, None]
+    want_dH, bulk = G @ W.double(), size @ W.double().abs()
+    assert ((dH - want_dH).abs() <= ((1 + U) ** (1 + exp) - 1 + slack) * bulk + U * want_dH.abs() + 1e-30).all()
+    cols = torch.tensor([0, 127, 128, 255, 256, V // 2, V - 130, V - 2, V - 1, *np.unique(y[told][:5].cpu())], device="cuda")
+    want_dW = G[:, cols].t() @ H.double()
+    bulk = ((1 + U) ** (2 + exp) - 1 + slack) * size[:, cols]
+    assert ((dW[cols] - want_dW).abs() <= bulk.t() @ H.double().abs() + U * want_dW.abs() + 1e-30).all()
+    for got, ref in ((dH, want_dH), (dW[cols], want_dW)):
+        assert (got - ref).norm() <= 5e-3 * ref.norm()
