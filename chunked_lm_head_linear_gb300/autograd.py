@@ -175,8 +175,9 @@ class _Distillation(torch.autograd.Function):
     def forward(ctx, H, W, idx, t, kw):
         need_dH, need_dW = ctx.needs_input_grad[:2]
         if not (need_dH or need_dW):
-            loss, _ = lce.lce_distill_forward(H, W, idx, t, **kw)
-            return loss.reshape(())
+            loss = lce.lce_distill_forward(H, W, idx, t, **kw)[0].reshape(())
+            ctx.mark_non_differentiable(loss)   # an input without a gradient here (t) may ask for one
+            return loss
         loss, _, dH, dW = lce.lce_distill_fwd_bwd(H, W, idx, t, dW_dtype=W.dtype, need_dH=need_dH, need_dW=need_dW,
                                                   **kw)
         ctx.grads = dH, dW
@@ -213,12 +214,14 @@ class _PolicyLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, H, W, y, advantages, old_logp, ref_logp, weights, kw):
         need_dH, need_dW = ctx.needs_input_grad[:2]
-        if need_dH or need_dW:
-            loss, logp, _, dH, dW = lce.lce_policy_fwd_bwd(H, W, y, advantages, old_logp, ref_logp, weights=weights,
-                                                           dW_dtype=W.dtype, need_dH=need_dH, need_dW=need_dW, **kw)
-            ctx.grads = dH, dW
-        else:
+        if not (need_dH or need_dW):
             loss, logp, _ = lce.lce_policy_forward(H, W, y, advantages, old_logp, ref_logp, weights=weights, **kw)
+            loss = loss.reshape(())
+            ctx.mark_non_differentiable(loss, logp)   # advantages, old_logp, ref_logp or weights may ask for a gradient
+            return loss, logp
+        loss, logp, _, dH, dW = lce.lce_policy_fwd_bwd(H, W, y, advantages, old_logp, ref_logp, weights=weights,
+                                                       dW_dtype=W.dtype, need_dH=need_dH, need_dW=need_dW, **kw)
+        ctx.grads = dH, dW
         ctx.mark_non_differentiable(logp)
         return loss.reshape(()), logp
 
@@ -255,12 +258,14 @@ class _PreferenceLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, H, W, y, cu_seqlens, ref_logp, kw):
         need_dH, need_dW = ctx.needs_input_grad[:2]
-        if need_dH or need_dW:
-            loss, _, seq_logp, dH, dW = lce.lce_preference_fwd_bwd(H, W, y, cu_seqlens, ref_logp, dW_dtype=W.dtype,
-                                                                   need_dH=need_dH, need_dW=need_dW, **kw)
-            ctx.grads = dH, dW
-        else:
+        if not (need_dH or need_dW):
             loss, _, seq_logp = lce.lce_preference_forward(H, W, y, cu_seqlens, ref_logp, **kw)
+            loss = loss.reshape(())
+            ctx.mark_non_differentiable(loss, seq_logp)   # ref_logp may ask for a gradient
+            return loss, seq_logp
+        loss, _, seq_logp, dH, dW = lce.lce_preference_fwd_bwd(H, W, y, cu_seqlens, ref_logp, dW_dtype=W.dtype,
+                                                               need_dH=need_dH, need_dW=need_dW, **kw)
+        ctx.grads = dH, dW
         ctx.mark_non_differentiable(seq_logp)
         return loss.reshape(()), seq_logp
 
