@@ -1978,6 +1978,8 @@ int lce_layernorm_forward(const void* x, const void* w, const void* b, int64_t N
 int lce_layernorm_backward(const void* x, const void* w, const float* mean, const float* rstd, const void* dH, int64_t N,
                            int64_t d, int32_t types, void* dx, float* dw, float* db, void* ws, size_t ws_bytes,
                            void* stream) {
+  const bool no_cluster = (types & LCE_TEST_NO_CLUSTER) != 0;
+  types &= ~LCE_TEST_NO_CLUSTER;
   LCE_TRY(layernorm_args(N, d, types));
   if ((!dx && !dw && !db) || (N > 0 && (!x || !mean || !rstd || !dH)) || ((dw || db) && !ws))
     return LCE_ERR_INVALID_ARG;
@@ -1997,6 +1999,7 @@ int lce_layernorm_backward(const void* x, const void* w, const float* mean, cons
   p.d = static_cast<int>(d);
   p.mean = const_cast<float*>(mean);
   p.rstd = const_cast<float*>(rstd);
+  p.no_cluster = no_cluster ? 1 : 0;
   p.dH = dH;
   p.dx = dx;
   p.dw = dw;

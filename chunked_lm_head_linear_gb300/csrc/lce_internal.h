@@ -261,6 +261,7 @@ struct LayerNormArgs {
   const void* w;           // [d] or null (ones)
   const void* b;           // [d] or null (zeros), forward only
   int x_f32, w_bf16;
+  int no_cluster;          // backward: as where no cluster of sixteen fits (tests)
   long long N;
   int d;
   float eps;

@@ -570,12 +570,11 @@ constexpr long long kLnOneLaunch = 1 << 19;
 
 bool one_launch(long long N, long long d) { return d <= kLnFusedD && N * (d > 256 ? d : 256) <= kLnOneLaunch; }
 
-template <bool F32, int T, int K, int R, int D, int B = 2>
-cudaError_t bwd_pass(const LayerNormArgs& p, int parts, cudaStream_t s) {
-  constexpr int bytes = Ring<F32, T, K, R, F32 ? 3 : 2>::bytes(D);
-  if (!one_launch(p.N, p.d)) return launch_ring(k_layernorm_bwd<F32, T, K, R, D, B, false>, parts, kLnThreads, bytes, p, s);
+// The pass as a launch of one cluster, where dw or db is wanted and such a cluster fits the SMs there are (not on a small
+// partition of them): *done. cudaSuccess without *done: it does not.
+template <bool F32, int T, int K, int R, int D, int B>
+cudaError_t bwd_cluster(const LayerNormArgs& p, int bytes, bool* done, cudaStream_t s) {
   auto kern = k_layernorm_bwd<F32, T, K, R, D, B, true>;
-  static_assert(bytes >= 2 * 4 * 8 * T * K, "a block's dw and db fit the ring");
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   const cudaError_t wide = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);  // above 8 blocks
@@ -593,7 +592,25 @@ cudaError_t bwd_pass(const LayerNormArgs& p, int parts, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  int fit = 0;
+  if (cudaOccupancyMaxActiveClusters(&fit, kern, &cfg) != cudaSuccess || fit < 1) {
+    (void)cudaGetLastError();
+    return cudaSuccess;
+  }
+  *done = true;
   return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+// *done: dw and db are written, else the blocks' partial rows are.
+template <bool F32, int T, int K, int R, int D, int B = 2>
+cudaError_t bwd_pass(const LayerNormArgs& p, int parts, bool* done, cudaStream_t s) {
+  constexpr int bytes = Ring<F32, T, K, R, F32 ? 3 : 2>::bytes(D);
+  static_assert(bytes >= 2 * 4 * 8 * T * K, "a block's dw and db fit the ring");
+  if ((p.dw != nullptr || p.db != nullptr) && !p.no_cluster && one_launch(p.N, p.d)) {
+    const cudaError_t e = bwd_cluster<F32, T, K, R, D, B>(p, bytes, done, s);
+    if (e != cudaSuccess || *done) return e;
+  }
+  return launch_ring(k_layernorm_bwd<F32, T, K, R, D, B, false>, parts, kLnThreads, bytes, p, s);
 }
 
 // Rows that a block of the one-pass backward takes at a time.
@@ -606,18 +623,19 @@ cudaError_t bwd(const LayerNormArgs& p, int num_sms, cudaStream_t s) {
   const bool sums = p.dw != nullptr || p.db != nullptr;
   const int parts = layernorm_parts(p.N, p.d);
   cudaError_t e = cudaSuccess;
+  bool done = !sums;
   if (p.d <= 256)
-    e = bwd_pass<F32, 32, 1, 2, F32 ? 3 : 4>(p, parts, s);
+    e = bwd_pass<F32, 32, 1, 2, F32 ? 3 : 4>(p, parts, &done, s);
   else if (p.d <= 512)
-    e = bwd_pass<F32, 32, 2, 1, F32 ? 3 : 4>(p, parts, s);
+    e = bwd_pass<F32, 32, 2, 1, F32 ? 3 : 4>(p, parts, &done, s);
   else if (p.d <= 1024)
-    e = bwd_pass<F32, 64, 2, 1, F32 ? 3 : 4>(p, parts, s);
+    e = bwd_pass<F32, 64, 2, 1, F32 ? 3 : 4>(p, parts, &done, s);
   else if (p.d <= 2048)
-    e = bwd_pass<F32, 256, 1, 2, 4>(p, parts, s);
+    e = bwd_pass<F32, 256, 1, 2, 4>(p, parts, &done, s);
   else if (p.d <= 4096)
-    e = bwd_pass<F32, 256, 2, 1, 4>(p, parts, s);
+    e = bwd_pass<F32, 256, 2, 1, 4>(p, parts, &done, s);
   else if (p.d <= kLnFusedD)
-    e = bwd_pass<F32, 256, 4, 1, 4, 1>(p, parts, s);
+    e = bwd_pass<F32, 256, 4, 1, 4, 1>(p, parts, &done, s);
   else {
     if (p.dx != nullptr && p.N > 0) {
       const long long need = (p.N + kLnWarps - 1) / kLnWarps, most = 8LL * num_sms;
@@ -625,7 +643,7 @@ cudaError_t bwd(const LayerNormArgs& p, int num_sms, cudaStream_t s) {
     }
     if (e == cudaSuccess && sums) e = launch_k(k_layernorm_dw<F32>, dim3((p.d + 255) / 256, parts), kLnThreads, 0, s, p);
   }
-  if (e != cudaSuccess || !sums || one_launch(p.N, p.d)) return e;
+  if (e != cudaSuccess || done) return e;
   return launch_k(k_layernorm_sum, dim3((p.d + 31) / 32, 2), 32 * kSumWarps, 0, s, p, parts);
 }
 
@@ -633,7 +651,6 @@ cudaError_t bwd(const LayerNormArgs& p, int num_sms, cudaStream_t s) {
 
 // Blocks of the backward, each with a partial row of dw and db.
 int layernorm_parts(long long N, long long d) {
-  if (one_launch(N, d)) return 1;
   const long long rows = d <= kLnFusedD ? bwd_rows(d) : kLnWarps;
   const long long need = (N + rows - 1) / rows, most = d <= 4096 ? 2 * kSms : d <= kLnFusedD ? kSms : 512 / ((d + 255) / 256) + 1;
   const long long parts = need < most ? need : most;

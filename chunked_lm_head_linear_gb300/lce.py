@@ -52,6 +52,7 @@ LCE_OP_FORWARD, LCE_OP_BACKWARD, LCE_OP_FWD_BWD, LCE_OP_VSHARD_COMBINE, LCE_OP_N
 LCE_OP_VSHARD_CHUNK = 5
 LCE_DEVICE_LABEL_RANGE, LCE_DEVICE_TIMEOUT, LCE_DEVICE_BOUNDS = 1, 2, 4
 LCE_TEST_FORCE_TIMEOUT = 0x7E57
+LCE_TEST_NO_CLUSTER = 0x4000
 LCE_MAX_TOP = 128
 LCE_TEACHER_BF16, LCE_TEACHER_LOGPROBS = 1, 2
 LCE_DW_BF16 = 1

@@ -104,6 +104,8 @@ typedef struct lce_opts {
  * lce_read_device_status). Outputs are meaningless. It exists to test the
  * timeout path without faulting or hanging the GPU; other calls reject it. */
 #define LCE_TEST_FORCE_TIMEOUT 0x7E57
+/* In lce_layernorm_backward's types (tests only): do as where the device has no room for a cluster of sixteen blocks. */
+#define LCE_TEST_NO_CLUSTER 0x4000
 
 /* Fill *opts with the defaults above. */
 void lce_opts_init(lce_opts* opts);
