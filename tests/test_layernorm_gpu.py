@@ -1,4 +1,5 @@
-"""Layer norm where no cluster is used, whole outputs against fp64 on the device. Tolerances: those of test_losses_gpu.py (g = (d / 32 + 16) eps and so on)."""
+"""Layer norm where its persistent blocks take many turns of their ring, for every class of row length, and where no cluster
+is used, whole outputs against fp64 on the device. Tolerances: those of test_losses_gpu.py (g = (d / 32 + 16) eps and so on)."""
 import ctypes
 
 import pytest
@@ -55,6 +56,26 @@ def check(x, w, b, dH, eps, H=None, mean=None, rstd=None, dx=None, dw=None, db=N
         within(dw, (G * xh).sum(0), (G.abs() * ex).sum(0) + (N * EPS + 2.0 ** -21) * (G * xh).abs().sum(0) + 1e-38, "dw")
     if db is not None:
         within(db, G.sum(0), (N * EPS + 2.0 ** -21) * G.abs().sum(0) + 1e-38, "db")
+
+
+# More rows than all blocks hold in all turns of their rings, and a last turn that is not full
+@pytest.mark.parametrize("N,d", [(60013, 8), (40001, 200), (31999, 256), (12001, 264), (11003, 512), (7001, 520), (6501, 1024),
+                                 (5003, 1032), (3001, 2048), (2707, 2056), (2501, 4096), (1603, 4104), (1201, 8192), (801, 8200),
+                                 (653, 16384), (455, 32768)])
+@pytest.mark.parametrize("f32_x", [False, True])
+def test_many_turns(cuda_lib, N, d, f32_x):
+    torch = _torch()
+    x, w, b, dH = inputs(N, d, f32_x, seed=d)
+    H, mean, rstd = cuda_lib.lce_layernorm_forward(x, w, b, 1e-5)
+    eps = torch.tensor(1e-5).item()
+    check(x, w, b, dH, eps, H, mean, rstd)
+    dx, dw, db = cuda_lib.lce_layernorm_backward(x, w, mean, rstd, dH)
+    check(x, w, b, dH, eps, dx=dx, dw=dw, db=db)
+    # dx alone (no sums), dw and db alone (no exchange in a row), db alone
+    assert torch.equal(cuda_lib.lce_layernorm_backward(x, w, mean, rstd, dH, need_dw=False, bias=False)[0], dx)
+    _, dw2, db2 = cuda_lib.lce_layernorm_backward(x, w, mean, rstd, dH, need_dx=False)
+    assert torch.equal(dw2, dw) and torch.equal(db2, db)
+    assert torch.equal(cuda_lib.lce_layernorm_backward(x, w, mean, rstd, dH, need_dx=False, need_dw=False)[2], db)
 
 
 @pytest.mark.parametrize("N,d", [(0, 64), (1, 8), (1, 8192), (3, 24), (65, 256), (300, 264), (1531, 264), (33, 520), (500, 1000),
