@@ -35,7 +35,6 @@ template <>
 struct Group<false> {
   uint4 v;
   __device__ __forceinline__ void load(const void* p, long long i) { v = static_cast<const uint4*>(p)[i]; }
-  __device__ __forceinline__ void clear() { v = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -52,7 +51,6 @@ struct Group<true> {
     a = static_cast<const float4*>(p)[2 * i];
     b = static_cast<const float4*>(p)[2 * i + 1];
   }
-  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
@@ -281,7 +279,6 @@ __global__ void __launch_bounds__(kLnThreads, B) k_layernorm_bwd(const LayerNorm
   grid_dep_wait();
   grid_dep_launch();
   constexpr int PX = F32 ? 2 : 1, PER = PX + 1;
-  using Rg = Ring<F32, T, K, R, PER>;
   constexpr int S = kLnThreads / T, W = T / 32;
   extern __shared__ uint4 ring[];
   __shared__ float red[2][S][W][2 * R];
