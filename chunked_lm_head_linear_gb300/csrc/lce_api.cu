@@ -75,19 +75,21 @@ struct Layout {
   size_t status = 0, loss_i = 0, lse = 0, ztgt = 0, partials = 0, P = 0;
   size_t ref = 0, alpha = 0, guard = 0, Ht = 0, total = 0;
   int dh_parts = 0;                // vocabulary parts of a dH tile; 0: dh_parts_for(V)
+  int dh_room = 0;                 // parts that the workspace has room for (dh_parts not 0)
   size_t dh_cnt = 0, dh_part = 0;  // dH part counters and part sums (backward calls)
   int dh_ncnt = 0;                 // number of dH part counters
 };
 
 // The dH part counters and part sums of one chunk's backward launch: a counter
 // per (dH tile, CTA, epilogue warp), and, when the vocabulary is cut into more
-// than one part, one fp32 [256 x 256] sum per dH tile and part.
+// than one part, one fp32 [256 x 256] sum per dH tile and part (or the parts
+// as whole matrices, dh_room of them).
 void take_dh_parts(Layout& L, int64_t d, int64_t V, const std::function<size_t(size_t)>& take) {
   const int64_t tiles = ceil_div(L.C, 256) * ceil_div(d, 256);
   L.dh_ncnt = static_cast<int>(tiles * 8);
   L.dh_cnt = take(sizeof(int) * static_cast<size_t>(L.dh_ncnt));
-  if (L.dh_parts > 1)  // stored as [parts, rows, d]
-    L.dh_part = take(sizeof(float) * static_cast<size_t>(L.dh_parts) * static_cast<size_t>(ceil_div(L.C, 256) * 256) *
+  if (L.dh_room > 1)  // stored as [parts, rows, d]
+    L.dh_part = take(sizeof(float) * static_cast<size_t>(L.dh_room) * static_cast<size_t>(ceil_div(L.C, 256) * 256) *
                      static_cast<size_t>(d));
   if (L.dh_parts > 0) return;
   const int parts = lce::dh_parts_for(V);
@@ -1029,12 +1031,18 @@ int64_t tok_chunk(int64_t N, const lce_opts* o) {
   return C < N ? C : N;
 }
 
+// balanced: dH parts by dh_parts_balanced, for a launch with dW (with_dW) or without; the workspace, whose size is asked for
+// before it is known which, has room for either.
 TokLayout tok_layout(int64_t N, int64_t d, int64_t V, bool with_z, bool with_grad, bool dW_bf16, bool with_scale,
-                     const lce_opts* o, bool balanced_parts = false) {
+                     const lce_opts* o, bool balanced = false, bool with_dW = true) {
   TokLayout T;
   Layout& L = T.base;
   L.C = tok_chunk(N, o);
-  if (balanced_parts) L.dh_parts = lce::dh_parts_balanced(L.C, V, d);
+  if (balanced) {
+    const int both = lce::dh_parts_balanced(L.C, V, d, true), alone = lce::dh_parts_balanced(L.C, V, d, false);
+    L.dh_parts = with_dW ? both : alone;
+    L.dh_room = both > alone ? both : alone;
+  }
   L.T = ceil_div(V, kVocabTile);
   L.ldp = L.T * kVocabTile;
   L.chunks = N > 0 ? ceil_div(N, L.C) : 0;
@@ -1526,8 +1534,9 @@ bool exp_tiles_pay(int64_t rows, int64_t V) {
 // computes the logits once (9000 rows: 9.0 ms, twice 12.1).
 constexpr int64_t kExpRows = 3 * 6144;
 
-// pairs < 0: the policy loss.
-LossLayout loss_layout(int64_t N, int64_t d, int64_t V, int64_t pairs, bool with_grad, bool dW_bf16, const lce_opts* opts) {
+// pairs < 0: the policy loss. with_dW: what the call computes (the size does not depend on it).
+LossLayout loss_layout(int64_t N, int64_t d, int64_t V, int64_t pairs, bool with_grad, bool dW_bf16, const lce_opts* opts,
+                       bool with_dW = true) {
   LossLayout L;
   lce_opts o = *opts;
   L.step = tok_chunk(N, &o);
@@ -1535,7 +1544,7 @@ LossLayout loss_layout(int64_t N, int64_t d, int64_t V, int64_t pairs, bool with
   if (large && o.chunk_tokens == 0 && N <= kExpRows) o.chunk_tokens = N;
   const bool one = N <= tok_chunk(N, &o);
   L.exp = large && (pairs < 0 || one);
-  L.tok = tok_layout(N, d, V, with_grad && (pairs < 0 || one) && !L.exp, with_grad, dW_bf16, with_grad, &o, true);
+  L.tok = tok_layout(N, d, V, with_grad && (pairs < 0 || one) && !L.exp, with_grad, dW_bf16, with_grad, &o, true, with_dW);
   size_t off = L.tok.total;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -1675,7 +1684,7 @@ int policy_loss(const void* H, const void* W, const int64_t* y, int64_t N, int64
       !aligned(logp, 4) || !aligned(row_loss, 4) || !aligned(advantages, 4) || !aligned(old_logp, 4) ||
       !aligned(ref_logp, 4) || !aligned(weights, 4) || !aligned(grad_loss, 4) || !aligned(dH, 16) || !aligned(dW, 16))
     return LCE_ERR_ALIGNMENT;
-  const LossLayout L = loss_layout(N, d, V, -1, with_grad, dW_bf16 && dW, &o);
+  const LossLayout L = loss_layout(N, d, V, -1, with_grad, dW_bf16 && dW, &o, dW != nullptr);
   if (ws_bytes < L.total) return LCE_ERR_WORKSPACE;
   const TokLayout& T = L.tok;
   Call c;
@@ -1770,7 +1779,7 @@ int preference_loss(const void* H, const void* W, const int64_t* y, int64_t N, i
       !aligned(ref_logp, 4) || !aligned(grad_loss, 4) || !aligned(loss, 4) || !aligned(pair_loss, 4) ||
       !aligned(seq_logp, 4) || !aligned(dH, 16) || !aligned(dW, 16))
     return LCE_ERR_ALIGNMENT;
-  const LossLayout L = loss_layout(N, d, V, pairs, with_grad, dW_bf16 && dW, &o);
+  const LossLayout L = loss_layout(N, d, V, pairs, with_grad, dW_bf16 && dW, &o, dW != nullptr);
   if (ws_bytes < L.total) return LCE_ERR_WORKSPACE;
   const TokLayout& T = L.tok;
   Call c;

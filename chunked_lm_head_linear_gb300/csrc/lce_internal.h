@@ -161,20 +161,28 @@ inline double dw_tile_cost(long long w_k, bool bf16) {
 
 // dH parts where no such promise is made (the policy and preference losses). Each is stored as an fp32 tile of its own
 // and a launch behind the GEMMs adds them. In k-blocks of time (0.31 us), a part takes its share of the kb there are and
-// kDhStore more, the sum kDhSum and what it reads and writes, and a cluster's fair share of the launch is `fair`: the fewest
-// parts that stay within a tenth of the best. Short batches have few dH tiles, and four parts of V = 151936 run 594 k-blocks each
-// on one cluster, 207 us whatever the rest takes; long ones do without parts.
+// kDhStore more, the sum kDhSum and what it reads and writes; the fewest parts that stay within a tenth of the best are
+// taken. With dW in the launch its tiles fill the clusters that have no part of dH, and the launch takes a cluster's fair
+// share, or a part, whichever is longer. Short batches have few dH tiles, and four parts of V = 151936 run 594 k-blocks
+// each on one cluster, 207 us whatever the rest takes; long ones do without parts. (Weighed with a bf16 dW; an fp32 one is
+// within 3% of its best with the same: 128 rows of d = 2048 475 us of 454 to 559, 512 rows 695 of 662 to 719.) Without dW
+// the clusters take the parts in rounds. Policy steps of a frozen W, V = 151936, us with the parts that a launch with dW
+// would have, and with these: 256 x 2048 302 -> 245, 512 x 2048 531 -> 394, 512 x 4096 1128 -> 775, 2560 x 2048 2257 ->
+// 1854, 2048 x 256 335 -> 309. clusters: two of the device's 152 SMs each (the workspace's size may not depend on it).
 constexpr int kMaxDhParts = 32;
 constexpr double kDhStore = 8.0, kDhSum = 10.0;
-inline int dh_parts_balanced(long long rows, long long V, long long d) {
-  const long long kb = (V + 63) / 64, cols = (d + 255) / 256;
+inline int dh_parts_balanced(long long rows, long long V, long long d, bool with_dw) {
+  constexpr long long clusters = 76;
+  const long long kb = (V + 63) / 64, cols = (d + 255) / 256, tiles = (rows + 255) / 256 * cols;
   const double k = static_cast<double>(kb);
-  const double fair = (static_cast<double>((rows + 255) / 256 * cols) * k +
-                       static_cast<double>((V + 255) / 256 * cols) * dw_tile_cost((rows + 63) / 64, true)) / 76.0;
+  const double fair = (static_cast<double>(tiles) * k +
+                       static_cast<double>((V + 255) / 256 * cols) * dw_tile_cost((rows + 63) / 64, true)) / clusters;
   const double bytes = 8.0 * static_cast<double>(rows) * static_cast<double>(d);  // of a part, written and read
   auto time = [&](int p) {
-    const double longest = p == 1 ? k : k / p + kDhStore;
-    return (longest > fair ? longest : fair) + (p == 1 ? 0.0 : kDhSum + p * bytes / (5.0e12 * 0.31e-6));
+    const double part = p == 1 ? k : k / p + kDhStore;
+    const double sum = p == 1 ? 0.0 : kDhSum + p * bytes / (5.0e12 * 0.31e-6);
+    if (!with_dw) return static_cast<double>((tiles * p + clusters - 1) / clusters) * part + sum;
+    return (part > fair ? part : fair) + sum;
   };
   double best = time(1);
   for (int p = 2; p <= kMaxDhParts; ++p) best = time(p) < best ? time(p) : best;

@@ -414,8 +414,9 @@ int lce_scale_grads_bfloat(void* dH, void* dW, int64_t N, int64_t d, int64_t V, 
  * Losses on the log-probabilities of given tokens, with their gradients in one
  * call (6 N V d flops, as lce_fwd_bwd). z, z', p, logp, H, W, y, opts, grads, ws
  * and stream are those of the token operators. grad_loss: device fp32 [1] or NULL
- * (1.0); either of dH, dW may be NULL: not wanted, not computed. opts->reserved
- * must be 0. All arrays of floats are fp32, on the device.
+ * (1.0); either of dH, dW may be NULL: not wanted, not computed (dH's sums over a
+ * large vocabulary run in another order then). opts->reserved must be 0. All
+ * arrays of floats are fp32, on the device.
  * Small calls keep the chunk's logits (4 bytes a logit, and 2 for the gradient
  * tile); large ones (8 million logits or more in a chunk, 4.5 million in one of
  * up to 96 rows, or a vocabulary of 98304 or more) keep the tile alone.

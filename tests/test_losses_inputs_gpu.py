@@ -83,3 +83,43 @@ def test_losses_of_a_models_hidden_states(cuda_lib, N, d, V, T):
     assert ((dW[cols] - want_dW).abs() <= bulk.t() @ H.double().abs() + U * want_dW.abs() + 1e-30).all()
     for got, ref in ((dH, want_dH), (dW[cols], want_dW)):
         assert (got - ref).norm() <= 5e-3 * ref.norm()
+
+
+@pytest.mark.parametrize("N,d,V,chunk", [(40, 256, 151936, 0), (300, 2048, 100003, 0), (600, 1032, 100003, 256), (200, 264, 4099, 0)])
+def test_a_frozen_head(cuda_lib, N, d, V, chunk):
+    """dH alone, whose launch cuts the vocabulary otherwise than one with dW does: against fp64, in a workspace of the size
+    asked for, and nothing behind it touched. The bound on dH as above; sums of up to 32 parts add 32 eps of the terms."""
+    torch = _torch()
+    g, H, W, y = model_inputs(N, d, V, seed=d)
+    told = y >= 0
+    at = torch.where(told, y, 0)[:, None]
+    A = torch.randn(N, generator=g, device="cuda")
+    cu = torch.tensor([0, N // 3, N - 1], device="cuda")
+    opts = cuda_lib.make_opts(chunk_tokens=chunk)
+    z = H.double() @ W.double().t()
+    e = torch.exp(z - z.gather(1, at)).scatter_(1, at, 0.0)
+    rest = e.sum(1)
+    unit = (-e / (1 + rest)[:, None]).scatter_(1, at, (rest / (1 + rest))[:, None])
+    tz = (d / 16) * 2.0 ** -23 * (H.double().abs() @ W.double().abs().t()).amax(1)
+    exp = 1 if uses_exp_tiles(N, V, chunk) else 0
+    for name, size, args in (("policy", cuda_lib.lce_policy_workspace_size(N, d, V, True, 0, opts), (A,)),
+                             ("preference", cuda_lib.lce_preference_workspace_size(N, d, V, 1, True, 0, opts), (cu,))):
+        ws = torch.full((size + 4096,), 9, dtype=torch.uint8, device="cuda")
+        call = getattr(cuda_lib, f"lce_{name}_fwd_bwd")
+        out = call(H, W, y, *args, need_dW=False, workspace=ws[:size], chunk_tokens=chunk, sync_check=True)
+        assert out[4] is None and bool((ws[size:] == 9).all())
+        again = call(H, W, y, *args, need_dW=False, chunk_tokens=chunk)
+        assert torch.equal(out[3], again[3])
+        if name == "policy":
+            a = torch.where(told, -A.double() / int(told.sum()), 0.0)
+        else:   # sigmoid, beta = 0.1, one pair: the slope from the sums that came out
+            slope = -0.1 * torch.sigmoid(-0.1 * (out[2][0] - out[2][1]).double())
+            a = torch.zeros(N, dtype=torch.float64, device="cuda")
+            a[:N // 3], a[N // 3:N - 1] = slope, -slope
+            a = torch.where(told, a, 0.0)
+        G = unit * a[:, None]
+        want, bulk = G @ W.double(), G.abs() @ W.double().abs()
+        slack = (2 * tz + 2.0 ** -10 + 32 * EPS)[:, None]
+        assert ((out[3] - want).abs() <= ((1 + U) ** (1 + exp) - 1 + slack) * bulk + U * want.abs() + 1e-30).all()
+        # a pair hundreds of nats apart has a slope below the least normal number of fp32 and bf16, 2^-126: such elements may be 0
+        assert (out[3] - want).norm() <= 5e-3 * want.norm() + 2.0 ** -126 * want.numel() ** 0.5
