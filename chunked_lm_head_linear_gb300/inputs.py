@@ -24,6 +24,9 @@ workloads, the page's 154,880 is context only.
 from __future__ import annotations
 
 import math
+import os
+from collections import deque
+from concurrent.futures import ThreadPoolExecutor
 from dataclasses import dataclass, field, replace
 
 import numpy as np
@@ -89,10 +92,12 @@ def f64_to_bf16_bits(x) -> np.ndarray:
 
     Returns the bf16 bit patterns as uint16. NaNs never occur in the draws.
     """
-    f = np.ascontiguousarray(np.asarray(x, dtype=np.float64).astype(np.float32))
-    u = f.view(np.uint32).astype(np.uint64)
-    u = (u + 0x7FFF + ((u >> 16) & 1)) >> 16
-    return u.astype(np.uint16)
+    u = np.ascontiguousarray(np.asarray(x, dtype=np.float64).astype(np.float32)).view(np.uint32)
+    up = (u >> np.uint32(16)) & np.uint32(1)
+    up += np.uint32(0x7FFF)
+    up += u   # below 2^32: the largest finite pattern is 0xFF7FFFFF
+    up >>= np.uint32(16)
+    return up.astype(np.uint16)
 
 
 def bf16_bits_to_f32(bits) -> np.ndarray:
@@ -102,20 +107,35 @@ def bf16_bits_to_f32(bits) -> np.ndarray:
 
 
 def _normal_bf16(rng: np.random.Generator, rows: int, cols: int, sigma: float,
-                 block_rows: int = 4096) -> np.ndarray:
+                 block_rows: int = 1024) -> np.ndarray:
     """rows x cols bf16 draws of N(0, sigma^2), generated in row blocks.
 
     Drawing in blocks consumes the generator in exactly the same order as one
     large call, so the result does not depend on ``block_rows``; it only bounds
-    the fp64 scratch to block_rows*cols*8 bytes.
+    the fp64 scratch to a few blocks of block_rows*cols*8 bytes. The draws are in
+    order, on this thread; blocks are scaled and rounded on others meanwhile.
     """
     out = np.empty((rows, cols), dtype=np.uint16)
-    for r0 in range(0, rows, block_rows):
-        r1 = min(rows, r0 + block_rows)
-        blk = rng.standard_normal((r1 - r0, cols))
+
+    def finish(r0, r1, blk):
         if sigma != 1.0:
             blk *= sigma
         out[r0:r1] = f64_to_bf16_bits(blk)
+
+    if rows <= block_rows:
+        finish(0, rows, rng.standard_normal((rows, cols)))
+        return out
+    workers = min(4, os.cpu_count() or 1)
+    with ThreadPoolExecutor(workers) as pool:
+        waiting = deque()
+        for r0 in range(0, rows, block_rows):
+            r1 = min(rows, r0 + block_rows)
+            blk = rng.standard_normal((r1 - r0, cols))
+            if len(waiting) >= 2 * workers:
+                waiting.popleft().result()
+            waiting.append(pool.submit(finish, r0, r1, blk))
+        for w in waiting:
+            w.result()
     return out
 
 
