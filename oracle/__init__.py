@@ -19,10 +19,11 @@ import numpy as np
 
 from .lce_oracle import (  # noqa: F401
     IGNORE_INDEX, MEAN, SUM, LabelRangeError, decode_bf16, dH_rows_f64,
-    dW_rows_f64, forward_rows_f64, grad_scale, lce_bf16, lce_chunked_online,
-    lce_f64, norm_lce_bf16, rmsnorm_backward_f64, rmsnorm_f64, round_bf16_bits,
+    dW_rows_f64, forward_rows_f64, grad_scale, lce_chunked_online, lce_f64,
+    norm_lce_bf16, rmsnorm_backward_f64, rmsnorm_f64, round_bf16_bits,
     vshard_backward_f64, vshard_merge_f64, vshard_stats_f64,
 )
+from .large import LARGE, lce_large_f64  # noqa: F401
 from .losses_oracle import (  # noqa: F401
     head_gradients_f64,
     layernorm_backward_f64,
@@ -41,6 +42,12 @@ _SRC = os.path.join(_HERE, "lce_oracle.c")
 _LIB = os.path.join(_HERE, "_build", "liblce_oracle.so")
 _lock = threading.Lock()
 _lib = None
+
+
+def lce_bf16(Hbits, Wbits, y, **kw):
+    """``lce_f64`` on bf16 bit-pattern inputs (the CUDA path's input format), on all cores for full-size heads."""
+    f = lce_large_f64 if len(Hbits) * len(Wbits) >= LARGE else lce_f64
+    return f(decode_bf16(Hbits), decode_bf16(Wbits), y, **kw)
 
 
 def build_c_oracle(force: bool = False) -> str:

@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import numpy as np
 
+from ._rows import by_rows
 from .lce_oracle import IGNORE_INDEX, MEAN
 from .tokens_oracle import _head
 
@@ -20,11 +21,16 @@ def head_gradients_f64(H, W, y, a, *, temperature=1.0, ignore_index=IGNORE_INDEX
     _, logq, _ = _head(H, W, temperature)
     told = _given(y, W.shape[0], ignore_index)
     a = np.where(told, a, 0.0)[:, None]
-    hot = np.zeros_like(logq)
-    hot[np.arange(len(y))[told], y[told]] = 1.0
-    p = np.exp(logq)
-    G = (hot - p) * a / temperature
-    size = (hot + p) * np.abs(a) / temperature
+    G, size = logq, np.empty_like(logq)
+
+    def rows(lo, hi):
+        p, given = np.exp(logq[lo:hi]), told[lo:hi]
+        hot = np.zeros_like(p)
+        hot[np.flatnonzero(given), y[lo:hi][given]] = 1.0
+        G[lo:hi] = (hot - p) * a[lo:hi] / temperature
+        size[lo:hi] = (hot + p) * np.abs(a[lo:hi]) / temperature
+
+    by_rows(rows, *logq.shape)
     return {"dH": G @ W, "dW": G.T @ H, "dH_bulk": size @ np.abs(W), "dW_bulk": size.T @ np.abs(H)}
 
 

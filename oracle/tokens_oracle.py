@@ -15,15 +15,23 @@ from __future__ import annotations
 
 import numpy as np
 
+from ._rows import by_rows
 from .lce_oracle import IGNORE_INDEX, MEAN
 
 
 def _head(H, W, temperature):
     z = H @ W.T
-    zt = z / temperature
-    m = zt.max(axis=1, keepdims=True)
-    lse = m + np.log(np.exp(zt - m).sum(axis=1, keepdims=True))
-    return z, zt - lse, lse[:, 0]
+    logq, lse = np.empty_like(z), np.empty(len(z))
+
+    def rows(a, b):
+        zt = z[a:b] / temperature
+        m = zt.max(axis=1, keepdims=True)
+        total = m + np.log(np.exp(zt - m).sum(axis=1, keepdims=True))
+        logq[a:b] = zt - total
+        lse[a:b] = total[:, 0]
+
+    by_rows(rows, *z.shape)
+    return z, logq, lse
 
 
 def _xlogx(p, logp):
