@@ -32,7 +32,20 @@ def pytest_terminal_summary(terminalreporter):
             terminalreporter.write_line(line)
 
 
+SLOW_SECONDS = 20.0
+_config = None
+
+
+def pytest_runtest_logreport(report):
+    """Tests that took long, named as they end: a run that is stopped shows where its time went."""
+    reporter = _config.pluginmanager.get_plugin("terminalreporter") if _config is not None else None
+    if reporter is not None and report.when == "call" and report.duration >= SLOW_SECONDS:
+        reporter.write_line(f" {report.duration:.0f} s {report.nodeid}")
+
+
 def pytest_configure(config):
+    global _config
+    _config = config
     config.addinivalue_line("markers", "gpu: needs a GB300 (sm_103a) GPU and the built CUDA library")
     config.addinivalue_line("markers", "slow: full-size workload (minutes)")
 
