@@ -1105,7 +1105,7 @@ cudaError_t launch_logits(const CUtensorMap& a, const CUtensorMap& b, const CUte
 }
 
 constexpr int kOddDhFirstMaxK = 16;  // k-blocks of a dW tile (chunks of up to 1024 rows)
-constexpr double kDhBlockMaxShare = 1.25;
+constexpr double kDhBlockMaxShare = 1.1;
 
 template <class Dw, bool PARTS = true>
 static cudaError_t launch_backward_t(const CUtensorMap& ah, const CUtensorMap& bh, const CUtensorMap& ch,
@@ -1163,9 +1163,11 @@ static cudaError_t launch_backward_t(const CUtensorMap& ah, const CUtensorMap& b
   // The parts of a dH block go to one cluster back to back when the whole block is no longer than
   // kDhBlockMaxShare of a cluster's fair share: the blocks then run side by side on some clusters,
   // each W and exp-tile block read by all the tiles that need it at once, while the other clusters
-  // stream the dW tiles (A/B on one box, Qwen3.5-2B-like head: 784K vs 755K tokens/s at 1024-token
-  // chunks, equal at 2048 and 4096). Otherwise the parts are dealt one by one, which balances the
-  // clusters when the blocks are fewer than them (540K vs 470K tokens/s at 512-token chunks).
+  // stream the dW tiles. Otherwise the parts are dealt one by one, which balances the clusters when
+  // the blocks are fewer than them. Cross-entropy steps, blocks together / parts one by one, us: 1024
+  // rows of d = 2048, V = 151936 (a block is 1.18 shares) 1167 / 1121, 2048 of 1024 (1.18) 1164 /
+  // 1106, 1024 of 2048, V = 32000 280 / 273; 3000 of 768, V = 50257 (1.02) 442 / 478, 1100 of 2048
+  // (0.99) 1289 / 1310, 2048 of 2048 (0.59) 2084 / 2100.
   const double fair = (static_cast<double>(nParts) * kDhKblockCost * p.h_kpart + static_cast<double>(nW) * w_cost) / P;
   p.h_group = (p.h_parts > 1 && h.split_rows == 0 && kDhKblockCost * p.h_k <= kDhBlockMaxShare * fair) ? p.h_parts : 1;
   p.h.block_major = p.h_group > 1 ? 1 : 0;
