@@ -1104,7 +1104,9 @@ def lce_policy_fwd_bwd(H, W, y, advantages, old_logp=None, ref_logp=None, grad_l
     """lce_policy_forward and its gradients in one call: loss, logp, row_loss, dH
     (bf16 [N, d]), dW (fp32 [V, d], or bf16 with dW_dtype); a gradient that is
     not wanted is None. By default a large call holds 2 bytes a logit of up to
-    18432 rows; chunk_tokens bounds that."""
+    18432 rows; chunk_tokens bounds that. A label some 60 nats below its row's
+    largest z / temperature makes a large call compute its rows' logits twice
+    more (include/lce.h)."""
     import torch
     N, d, V, policy = _check_policy(H, W, y, advantages, old_logp, ref_logp, weights, kl, kl_coef, clip_low, clip_high,
                                     dual_clip)

@@ -412,7 +412,7 @@ int lce_scale_grads_bfloat(void* dH, void* dW, int64_t N, int64_t d, int64_t V, 
 
 /*
  * Losses on the log-probabilities of given tokens, with their gradients in one
- * call (6 N V d flops, as lce_fwd_bwd). z, z', p, logp, H, W, y, opts, grads, ws
+ * call (6 N V d flops, as lce_fwd_bwd; see below for 10). z, z', p, logp, H, W, y, opts, grads, ws
  * and stream are those of the token operators. grad_loss: device fp32 [1] or NULL
  * (1.0); either of dH, dW may be NULL: not wanted, not computed (dH's sums over a
  * large vocabulary run in another order then). opts->reserved must be 0. All
@@ -427,6 +427,12 @@ int lce_scale_grads_bfloat(void* dH, void* dW, int64_t N, int64_t d, int64_t V, 
  * rounding of the gradient tile; a call repeats itself bit for bit. In all of them
  * logp is lce_logprobs' but for the rounding of sums of exponentials (a few 1e-6):
  * the ratio to a model's own log-probabilities is 1.
+ * Large calls write the tile against the label's logit, as long as no sum of
+ * exp(z'_v - z'_y) over 128 columns passes 1e26: with the label some 60 nats below
+ * the row's largest z' (6 in z at a temperature of 0.1), or logits that are not
+ * finite, in any row with a given token, also one with a weight of 0 or in no
+ * sequence, the rows of that launch (up to 6143) have their logits computed twice
+ * more, 10 N V d flops (1024 rows of d = 2048, V = 151936: 1.19 -> 1.81 ms).
  *
  * lce_policy_forward, lce_policy_fwd_bwd: the clipped policy loss. Per row with a
  * given token (y neither ignore_index nor out of range), A = advantages_i, w =
