@@ -123,3 +123,24 @@ def test_a_frozen_head(cuda_lib, N, d, V, chunk):
         assert ((out[3] - want).abs() <= ((1 + U) ** (1 + exp) - 1 + slack) * bulk + U * want.abs() + 1e-30).all()
         # a pair hundreds of nats apart has a slope below the least normal number of fp32 and bf16, 2^-126: such elements may be 0
         assert (out[3] - want).norm() <= 5e-3 * want.norm() + 2.0 ** -126 * want.numel() ** 0.5
+
+
+def test_coldest_temperature_with_two_sums_of_a_logit(cuda_lib):
+    """Logits of thousands at T = 1e-6: the label's two sums lie hundreds of nats apart, and the exact tiles take over. With the
+    label the row's largest logit it has all of the probability (log 1 = 0, no gradient), else it has none of it."""
+    torch = _torch()
+    N, d, V, T = 300, 2048, 40001, 1.0e-6
+    g, H, W, y = model_inputs(N, d, V, seed=3)
+    H = (H.float() * 60).bfloat16()
+    other = cuda_lib.lce_logprobs(H, W, torch.zeros_like(y), temperature=T, top_k=2)
+    gap = (other[3][:, 0] - other[3][:, 1])
+    y = torch.where(gap > 1.0e3, other[4][:, 0], -100)
+    assert int((y >= 0).sum()) > N // 2
+    y[0] = other[4][0, 1]
+    A = torch.randn(N, generator=g, device="cuda")
+    loss, logp, row, dH, dW = cuda_lib.lce_policy_fwd_bwd(H, W, y, A, temperature=T, dW_dtype=torch.bfloat16, sync_check=True)
+    want = cuda_lib.lce_logprobs(H, W, y, temperature=T)[0]
+    assert torch.equal(logp[1:], torch.zeros_like(logp[1:])) and not dH[1:].any()
+    assert logp[0] == want[0] < -1.0e3 and torch.isfinite(dH).all() and torch.isfinite(dW.float()).all()
+    told = y >= 0
+    assert ((row + torch.where(told, A, 0.0)).abs() <= 2 * EPS * A.abs()).all() and torch.isfinite(loss).all()
